@@ -14,6 +14,11 @@ Functions (same names as the C ABI):
   kda_prefill_host(q, k, v, log_alpha, beta (host), ..., segment_tokens)
   kda_decode_step_fused(q, k, v, z, A, beta, S_inout, ..., q_scale)
   kda_state_gather(states, S_in, accept, ...)
+  kda_decode_tree(q, k, v, log_alpha, beta, S_in, parent, ...)
+  kda_tree_attention(q, k, v, k_cache, v_cache, page_table, lengths, parent=None, ...)
+  kda_token_logprobs(logits, tokens, num_top=0, ...)
+  kda_cache_commit(k, v, path, count, k_cache, v_cache, page_table, lengths, ...)
+  kda_cache_append(k, v, cu_seqlens, k_cache, v_cache, page_table, lengths, ...)
   kda_prefill_workspace_bytes(num_seqs, H, d_k, d_v)
   kda_status_string(code)
 """
@@ -33,7 +38,9 @@ EXPORTS = ("kda_prefill_workspace_bytes", "kda_prefill", "kda_decode_step",
            "kda_status_string", "kda_prefill_noalloc", "kda_prefill_snapshots",
            "kda_decode_multi", "kda_state_gather", "kda_prefill_fused",
            "kda_decode_step_fused", "kda_prefill_host_staging_bytes", "kda_prefill_host",
-           "kda_prefill_segmented_workspace_bytes", "kda_prefill_segmented")
+           "kda_prefill_segmented_workspace_bytes", "kda_prefill_segmented",
+           "kda_decode_tree", "kda_tree_attention_workspace_bytes", "kda_tree_attention",
+           "kda_token_logprobs", "kda_cache_commit", "kda_cache_append")
 
 
 class KdaError(RuntimeError):
@@ -89,6 +96,25 @@ def _declare(lib):
     lib.kda_prefill_snapshots.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                           _i32, _i64, _i32, _i32, _i32, ctypes.c_int,
                                           _vp, _vp, _i32, _vp, _vp, _vp, _sz, _vp]
+    lib.kda_decode_tree.restype = ctypes.c_int
+    lib.kda_decode_tree.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
+                                    _i32, ctypes.c_int, _vp, _vp, _vp]
+    lib.kda_tree_attention_workspace_bytes.restype = _sz
+    lib.kda_tree_attention_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32, ctypes.c_int]
+    lib.kda_tree_attention.restype = ctypes.c_int
+    lib.kda_tree_attention.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
+                                       _i32, _i32, _i32, _i32, _i32, _i64, ctypes.c_int,
+                                       ctypes.c_float, _vp, _vp, _sz, _vp]
+    lib.kda_token_logprobs.restype = ctypes.c_int
+    lib.kda_token_logprobs.argtypes = [_vp, _i64, _vp, _i32, _i32, _i32, _i32, ctypes.c_int,
+                                       _vp, _vp, _vp, _vp, _vp]
+    lib.kda_cache_commit.restype = ctypes.c_int
+    lib.kda_cache_commit.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                     _i32, _i32, _i32, _i64, _i64, ctypes.c_int, _vp, _vp, _vp,
+                                     _vp]
+    lib.kda_cache_append.restype = ctypes.c_int
+    lib.kda_cache_append.argtypes = [_vp, _vp, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                     _i32, _i32, _i64, _i64, ctypes.c_int, _vp, _vp, _vp, _vp]
     return lib
 
 
@@ -434,6 +460,236 @@ def kda_state_gather(states, S_in, accept, *, S_out=None, stream=None):
     if rc != KDA_OK:
         raise KdaError(rc, "kda_state_gather")
     return S_out
+
+
+def _shape(name, t, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def kda_decode_tree(q, k, v, log_alpha, beta, S_in, parent=None, *, o=None, states=None,
+                    stream=None, o_dtype=None):
+    """The KDA step of every node of a tree of drafted tokens, each from the
+    state after its parent node (C ABI: kda_decode_tree).  Arguments as in
+    kda_decode_multi; parent: int32 [N, Ts], -1 for a node that follows the
+    context, -2 for an unused one (o = 0, its state not written), None for a
+    chain.  Returns (o [N, Ts, H, d_v], states [N, Ts, H, d_k, d_v])."""
+    torch = _torch()
+    N, Ts, H, dk = q.shape
+    dv = v.shape[3]
+    if o_dtype is None:
+        o_dtype = o.dtype if o is not None else q.dtype
+    dt = _dtype_code(q, o_dtype)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_cuda(name, t, q.dtype)
+    _check_cuda("log_alpha", log_alpha, torch.float32)
+    _check_cuda("beta", beta, torch.float32)
+    _check_cuda("S_in", S_in, torch.float32)
+    _check_cuda("parent", parent, torch.int32)
+    for name, t, shape in (("k", k, (N, Ts, H, dk)), ("v", v, (N, Ts, H, dv)),
+                           ("log_alpha", log_alpha, (N, Ts, H, dk)), ("beta", beta, (N, Ts, H)),
+                           ("S_in", S_in, (N, H, dk, dv))):
+        _shape(name, t, shape)
+    if parent is not None:
+        _shape("parent", parent, (N, Ts))
+    if o is None:
+        o = torch.empty((N, Ts, H, dv), dtype=o_dtype, device=q.device)
+    if states is None:
+        states = torch.empty((N, Ts, H, dk, dv), dtype=torch.float32, device=q.device)
+    _check_cuda("o", o, o_dtype)
+    _check_cuda("states", states, torch.float32)
+    _shape("o", o, (N, Ts, H, dv))
+    _shape("states", states, (N, Ts, H, dk, dv))
+    with torch.cuda.device(q.device):
+        rc = lib().kda_decode_tree(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(S_in), _ptr(parent),
+            N, Ts, H, dk, dv, dt, _ptr(o), _ptr(states), _stream_handle(stream, q.device))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_decode_tree")
+    return o, states
+
+
+def _check_pages(name, t, dtype, device):
+    """A pool of pages [..., num_pages, page_size, Hkv, d], dense in a page."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    _, h, d = t.shape[-3:]
+    if t.numel() and t.stride()[-3:] != (h * d, d, 1):
+        raise ValueError("%s must be dense within a page" % name)
+
+
+def kda_tree_attention_workspace_bytes(N: int, Ts: int, Hq: int, Hkv: int, d: int,
+                                       dtype: int) -> int:
+    return int(lib().kda_tree_attention_workspace_bytes(N, Ts, Hq, Hkv, d, dtype))
+
+
+def kda_tree_attention(q, k, v, k_cache, v_cache, page_table, lengths, parent=None, *,
+                       scale=None, o=None, workspace=None, stream=None, o_dtype=None):
+    """Attention of a tree of drafted tokens to a paged cache and to their
+    ancestors (C ABI: kda_tree_attention).
+
+    q: [N, Ts, Hq, d]; k, v: [N, Ts, Hkv, d], the drafted nodes' own;
+    k_cache, v_cache: [num_pages, page_size, Hkv, d], dense within a page, the
+    pages at any stride (both at the same); page_table: int32 [N, max_pages];
+    lengths: int32 [N]; parent: int32 [N, Ts] (-1: follows the context, -2:
+    unused) or None for a chain; scale: d ** -0.5 by default.  Returns o
+    [N, Ts, Hq, d]."""
+    torch = _torch()
+    N, Ts, Hq, d = q.shape
+    Hkv = k.shape[2]
+    dev = q.device
+    if o_dtype is None:
+        o_dtype = o.dtype if o is not None else q.dtype
+    dt = _dtype_code(q, o_dtype)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_cuda(name, t, q.dtype)
+    for name, t in (("page_table", page_table), ("lengths", lengths), ("parent", parent)):
+        _check_cuda(name, t, torch.int32)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check_pages(name, t, q.dtype, dev)
+        _shape(name, t, (k_cache.shape[0], k_cache.shape[1], Hkv, d))
+    _shape("k", k, (N, Ts, Hkv, d))
+    _shape("v", v, (N, Ts, Hkv, d))
+    _shape("page_table", page_table, (N, page_table.shape[1]))
+    _shape("lengths", lengths, (N,))
+    if parent is not None:
+        _shape("parent", parent, (N, Ts))
+    pages, page = k_cache.shape[:2]
+    if pages > 1 and k_cache.stride(0) != v_cache.stride(0):
+        raise ValueError("k_cache and v_cache must have the same page stride")
+    if o is None:
+        o = torch.empty((N, Ts, Hq, d), dtype=o_dtype, device=dev)
+    _check_cuda("o", o, o_dtype)
+    _shape("o", o, (N, Ts, Hq, d))
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = lib().kda_tree_attention_workspace_bytes(N, Ts, Hq, Hkv, d, dt)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        _check_cuda("workspace", workspace)
+        rc = lib().kda_tree_attention(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(parent), _ptr(k_cache), _ptr(v_cache),
+            _ptr(page_table), _ptr(lengths), N, Ts, Hq, Hkv, d, pages, page,
+            page_table.shape[1], k_cache.stride(0), dt, d ** -0.5 if scale is None else scale,
+            _ptr(o), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _stream_handle(stream, dev))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_tree_attention")
+    return o
+
+
+def kda_token_logprobs(logits, tokens=None, num_top=0, *, logprobs=None, entropy=None,
+                       top_ids=None, top_logprobs=None, stream=None):
+    """Log probabilities of given tokens, the entropy and the ``num_top`` most
+    probable tokens of each row of logits (C ABI: kda_token_logprobs).
+
+    logits: [T, V] bf16 or fp32, rows at any stride; tokens: int32 [T, J] or
+    None (J = 0).  Returns (logprobs [T, J], entropy [T], top_ids [T, num_top]
+    int32, top_logprobs [T, num_top]), all but the ids fp32."""
+    torch = _torch()
+    T, V = logits.shape
+    dev = logits.device
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if logits.stride(1) != 1 and V > 1:
+        raise ValueError("logits must be dense within a row")
+    dt = _dtype_code(logits, torch.float32)
+    _check_cuda("tokens", tokens, torch.int32)
+    J = 0 if tokens is None else tokens.shape[1]
+    K = int(num_top)
+    new = lambda *s, **kw: torch.empty(s, device=dev, **{"dtype": torch.float32, **kw})
+    if tokens is not None:
+        _shape("tokens", tokens, (T, J))
+    logprobs = new(T, J) if logprobs is None else logprobs
+    entropy = new(T) if entropy is None else entropy
+    top_ids = new(T, max(K, 0), dtype=torch.int32) if top_ids is None else top_ids
+    top_logprobs = new(T, max(K, 0)) if top_logprobs is None else top_logprobs
+    for name, t, shape in (("logprobs", logprobs, (T, J)), ("entropy", entropy, (T,)),
+                           ("top_ids", top_ids, (T, K)), ("top_logprobs", top_logprobs, (T, K))):
+        if K >= 0:
+            _shape(name, t, shape)
+        _check_cuda(name, t, torch.int32 if name == "top_ids" else torch.float32)
+    with torch.cuda.device(dev):
+        rc = lib().kda_token_logprobs(
+            _ptr(logits), max(logits.stride(0), V) if T == 1 else logits.stride(0), _ptr(tokens),
+            T, V, J, K, dt, _ptr(logprobs), _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs),
+            _stream_handle(stream, dev))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_token_logprobs")
+    return logprobs, entropy, top_ids, top_logprobs
+
+
+def _cache_rows(call, name, k, v, middle, k_cache, v_cache, page_table, lengths, new_lengths,
+                counts, stream):
+    """The part that kda_cache_commit and kda_cache_append share: checks, and
+    the call with ``middle`` between k, v and the page table."""
+    torch = _torch()
+    dev = k.device
+    dt = _dtype_code(k, torch.float32)
+    layers, Hkv, d = k.shape[0], k.shape[-2], k.shape[-1]
+    _check_cuda("k", k)
+    _check_cuda("v", v, k.dtype)
+    _shape("v", v, k.shape)
+    for what, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check_pages(what, t, k.dtype, dev)
+        _shape(what, t, (layers, k_cache.shape[1], k_cache.shape[2], Hkv, d))
+    for dim, size in ((0, layers), (1, k_cache.shape[1])):
+        if size > 1 and k_cache.stride(dim) != v_cache.stride(dim):
+            raise ValueError("k_cache and v_cache must have the same strides")
+    _check_cuda("page_table", page_table, torch.int32)
+    _check_cuda("lengths", lengths, torch.int32)
+    N = lengths.shape[0]
+    _shape("lengths", lengths, (N,))
+    _shape("page_table", page_table, (N, page_table.shape[1]))
+    if new_lengths is None:
+        new_lengths = torch.empty_like(lengths)
+    _check_cuda("new_lengths", new_lengths, torch.int32)
+    _shape("new_lengths", new_lengths, (N,))
+    with torch.cuda.device(dev):
+        rc = call(_ptr(k), _ptr(v), *middle, _ptr(page_table), _ptr(lengths), layers, N, *counts,
+                  Hkv, d, k_cache.shape[1], k_cache.shape[2], page_table.shape[1],
+                  k_cache.stride(1), k_cache.stride(0), dt, _ptr(k_cache), _ptr(v_cache),
+                  _ptr(new_lengths), _stream_handle(stream, dev))
+    if rc != KDA_OK:
+        raise KdaError(rc, name)
+    return new_lengths
+
+
+def kda_cache_commit(k, v, path, count, k_cache, v_cache, page_table, lengths, *,
+                     new_lengths=None, stream=None):
+    """Accepted drafted rows into the pages of a cache, all layers at once (C
+    ABI: kda_cache_commit): row path[n, i] of k and v goes to position
+    lengths[n] + i of sequence n for i < count[n].
+
+    k, v: [layers, N, Ts, Hkv, d]; path: int32 [N, Ts] or None (i itself);
+    count: int32 [N] or None (all Ts); k_cache, v_cache: [layers, num_pages,
+    page_size, Hkv, d], dense within a page; page_table: int32 [N, max_pages];
+    lengths: int32 [N] (not changed).  Returns new_lengths [N]."""
+    torch = _torch()
+    _, N, Ts, _, _ = k.shape
+    _check_cuda("path", path, torch.int32)
+    _check_cuda("count", count, torch.int32)
+    if path is not None:
+        _shape("path", path, (N, Ts))
+    if count is not None:
+        _shape("count", count, (N,))
+    _shape("lengths", lengths, (N,))
+    return _cache_rows(lib().kda_cache_commit, "kda_cache_commit", k, v, (_ptr(path), _ptr(count)),
+                       k_cache, v_cache, page_table, lengths, new_lengths, (Ts,), stream)
+
+
+def kda_cache_append(k, v, cu_seqlens, k_cache, v_cache, page_table, lengths, *,
+                     new_lengths=None, stream=None):
+    """A packed batch's rows into the pages of a cache (C ABI:
+    kda_cache_append).  k, v: [layers, T, Hkv, d]; cu_seqlens: int32 [N+1];
+    the rest as in kda_cache_commit.  Returns new_lengths [N]."""
+    torch = _torch()
+    _, T, _, _ = k.shape
+    _check_cuda("cu_seqlens", cu_seqlens, torch.int32)
+    _shape("lengths", lengths, (cu_seqlens.shape[0] - 1,))
+    return _cache_rows(lib().kda_cache_append, "kda_cache_append", k, v, (_ptr(cu_seqlens), T),
+                       k_cache, v_cache, page_table, lengths, new_lengths, (), stream)
 
 
 def kda_prefill_fused(q, k, v, z, A, beta, S0=None, cu_seqlens=None, *, q_scale, o=None,

@@ -1,0 +1,101 @@
+// kda_cache.cu -- rows of drafted or prompt tokens into the pages of a cache:
+// a gather of accepted rows (kda_cache_commit) or a packed batch
+// (kda_cache_append) to positions lengths[n] + i of each sequence, for every
+// layer and both of K and V in one launch.  Bound by the bytes it moves.
+//
+// A block moves kRowsPerBlock rows of one layer.  Its first threads work out
+// where each row goes (sequence, position, page); then groups of lanes copy
+// whole rows in 16-byte pieces.
+#include "kda_internal.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowsPerBlock = 32;
+
+__global__ void __launch_bounds__(kThreads)
+cache_rows_kernel(const CacheArgs a)
+{
+    __shared__ long long sh_dst[kRowsPerBlock];      // byte offset in a layer's cache; -1: not written
+    __shared__ long long sh_src[kRowsPerBlock];      // row of k and v
+    const int tid = threadIdx.x;
+    const long long first = (long long)blockIdx.x * kRowsPerBlock;
+    if (tid < kRowsPerBlock) {
+        const long long r = first + tid;
+        long long src = -1, dst = -1;
+        if (r < a.rows) {
+            int n, i;
+            bool there;
+            src = r;
+            if (a.cu_seqlens) {
+                int lo = 0, hi = a.N;                // the last n with cu[n] <= r
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (__ldg(a.cu_seqlens + mid) <= r) lo = mid;
+                    else hi = mid;
+                }
+                n = lo;
+                i = (int)(r - __ldg(a.cu_seqlens + n));
+                there = i >= 0 && r < __ldg(a.cu_seqlens + n + 1);
+            } else {
+                n = (int)(r / a.Ts);
+                i = (int)(r - (long long)n * a.Ts);
+                there = !a.count || i < __ldg(a.count + n);
+                if (there && a.path) {
+                    const int t = __ldg(a.path + r);
+                    there = t >= 0 && t < a.Ts;
+                    src = (long long)n * a.Ts + t;
+                }
+            }
+            const int len = __ldg(a.lengths + n);
+            const long long pos = (long long)len + i;
+            if (there && len >= 0 && pos < (long long)a.max_pages * a.page_size) {
+                const int p = (int)(pos / a.page_size);
+                const int page = __ldg(a.page_table + (long long)n * a.max_pages + p);
+                if (page >= 0 && page < a.num_pages)
+                    dst = page * a.page_bytes + (pos - (long long)p * a.page_size) * a.row_bytes;
+            }
+        }
+        sh_src[tid] = src;
+        sh_dst[tid] = dst;
+    }
+    if (a.new_lengths && blockIdx.y == 0) {
+        for (long long n = (long long)blockIdx.x * kThreads + tid; n < a.N;
+             n += (long long)gridDim.x * kThreads) {
+            int c;
+            if (a.cu_seqlens) {
+                c = a.cu_seqlens[n + 1] - a.cu_seqlens[n];
+            } else {
+                c = a.count ? a.count[n] : a.Ts;
+                c = c < 0 ? 0 : (c > a.Ts ? a.Ts : c);
+            }
+            a.new_lengths[n] = a.lengths[n] + c;
+        }
+    }
+    __syncthreads();
+    const int vecs = a.row_bytes / 16;
+    const long long src_layer = (long long)blockIdx.y * a.rows * a.row_bytes;
+    const long long dst_layer = (long long)blockIdx.y * a.layer_bytes;
+    for (int e = tid; e < kRowsPerBlock * vecs; e += kThreads) {
+        const int r = e / vecs, c = e - r * vecs;
+        const long long dst = sh_dst[r];
+        if (dst < 0) continue;
+        const long long s = src_layer + sh_src[r] * a.row_bytes + 16ll * c, d = dst_layer + dst + 16ll * c;
+        *reinterpret_cast<uint4*>(a.k_cache + d) = __ldcs(reinterpret_cast<const uint4*>(a.k + s));
+        *reinterpret_cast<uint4*>(a.v_cache + d) = __ldcs(reinterpret_cast<const uint4*>(a.v + s));
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_rows(const CacheArgs& args, cudaStream_t stream)
+{
+    long long blocks = (args.rows + kRowsPerBlock - 1) / kRowsPerBlock;
+    if (blocks < 1) blocks = 1;                      // no rows: new_lengths alone
+    if (blocks > 0x7fffffffLL || args.layers > 65535) return cudaErrorInvalidConfiguration;
+    cache_rows_kernel<<<dim3((unsigned)blocks, (unsigned)args.layers), kThreads, 0, stream>>>(args);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

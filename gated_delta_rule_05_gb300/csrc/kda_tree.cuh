@@ -1,0 +1,186 @@
+// kda_tree.cuh -- what the tree attention kernels share: the arguments, the
+// drafted tree's ancestor masks, and the split of the work over the CTAs.
+//
+// Work split.  An item is one (sequence, cache head, row tile): up to RT query
+// rows (node t, query head of the group) against the sequence's context and
+// drafted nodes.  Its keys come in tiles of KT: ceil(L / KT) tiles of the
+// context, then one tile that holds the drafted nodes.  Laid end to end in
+// (sequence, head, row tile, key tile) order, the tiles are cut into equal
+// ranges, one per CTA, whatever the lengths are; the lengths stay on the device
+// and every CTA finds its own range from them.  A range covers at most one
+// item that began in an earlier CTA and one that goes on in the next: those
+// pieces go to the CTA's two workspace slots as (unnormalised o, m, l), and a
+// second launch joins them.  Every other item is finished in its CTA.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+constexpr int kTreeMaxNodes = 64;     // one bit per node in a 64-bit mask
+
+struct TreeArgs {
+    const void *q, *k, *v;
+    const int32_t* parent;            // [N, Ts], or null for a chain
+    const void *k_cache, *v_cache;
+    const int32_t *page_table, *lengths;
+    int32_t N, Ts, Hq, Hkv, G, R;     // G = Hq / Hkv, R = Ts G rows per (sequence, cache head)
+    int32_t num_pages, page_size, max_pages;
+    long long page_stride;            // elements from one page to the next
+    float scale_log2;                 // scale * log2(e)
+    void* o;
+    int32_t* status;                  // workspace words (kWsTimeoutWord is used)
+    float* part;                      // 2 slots per CTA: [RT][d] o, [RT] m, [RT] l
+    int32_t ctas, row_tiles;
+};
+
+__device__ __forceinline__ int tree_context(const TreeArgs& a, int n)
+{
+    const long long most = (long long)a.max_pages * a.page_size;
+    const int len = __ldg(a.lengths + n);
+    return len < 0 ? 0 : (int)(len < most ? len : most);
+}
+
+// The row of the flattened cache [num_pages * page_size] that holds position
+// `pos` of sequence n as an element offset of (page, slot), or -1 when its
+// page table entry names no page.
+__device__ __forceinline__ long long tree_cache_row(const TreeArgs& a, const int32_t* table, int pos,
+                                                    int row_elems)
+{
+    const int p = pos / a.page_size;
+    const int page = __ldg(table + p);
+    if (page < 0 || page >= a.num_pages) return -1;
+    return (long long)page * a.page_stride + (long long)(pos - p * a.page_size) * row_elems;
+}
+
+// anc[t]: bit j set when node j is t or an ancestor of t; 0 when t is unused
+// (its chain of parents does not end at the context).  One warp, two nodes per
+// lane; six rounds of pointer doubling cover 64 nodes.
+__device__ __forceinline__ void tree_masks(const int32_t* parent, int Ts, int lane,
+                                           unsigned long long* anc, int32_t* up)
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = lane + 32 * i;
+        int p = -2;
+        if (t < Ts) {
+            p = parent ? __ldg(parent + t) : t - 1;
+            if (p < -1 || p >= t) p = -2;
+        }
+        anc[t] = 1ull << t;
+        up[t] = p;
+    }
+    __syncwarp();
+    for (int round = 0; round < 6; ++round) {
+        unsigned long long m[2];
+        int32_t u[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = lane + 32 * i, p = up[t];
+            m[i] = anc[t] | (p >= 0 ? anc[p] : 0ull);
+            u[i] = p >= 0 ? up[p] : p;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            anc[lane + 32 * i] = m[i];
+            up[lane + 32 * i] = u[i];
+        }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (up[lane + 32 * i] != -1) anc[lane + 32 * i] = 0ull;
+    __syncwarp();
+}
+
+// A position in the flattened tile order.
+struct TreeSpot {
+    long long total;        // tiles of the whole launch
+    long long start;        // first tile of sequence n
+    int n;
+};
+
+template <int KT>
+__device__ __forceinline__ long long tree_seq_tiles(const TreeArgs& a, int n)
+{
+    return ((long long)tree_context(a, n) + KT - 1) / KT + 1;
+}
+
+// First tile of CTA c's range.
+__device__ __forceinline__ long long tree_begin(long long total, int c, int ctas)
+{
+    return total * c / ctas;
+}
+
+// The sequence that holds the first tile of CTA c's range (c < ctas, range not
+// empty).  All THREADS threads of the block call it; `sh` is shared scratch of
+// THREADS / 32 + 2 words.
+template <int THREADS, int KT>
+__device__ TreeSpot tree_locate(const TreeArgs& a, int c, long long* sh)
+{
+    constexpr int W = THREADS / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long items = (long long)a.Hkv * a.row_tiles;
+    long long sum = 0;
+    for (int n = tid; n < a.N; n += THREADS) sum += tree_seq_tiles<KT>(a, n) * items;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    __syncthreads();
+    if (lane == 0) sh[warp] = sum;
+    __syncthreads();
+    TreeSpot r;
+    r.total = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) r.total += sh[i];
+    const long long at = tree_begin(r.total, c, a.ctas);
+    long long base = 0;
+    for (int n0 = 0; n0 < a.N; n0 += THREADS) {
+        const int n = n0 + tid;
+        const long long w = n < a.N ? tree_seq_tiles<KT>(a, n) * items : 0;
+        long long incl = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += x;
+        }
+        __syncthreads();
+        if (lane == 31) sh[warp] = incl;
+        __syncthreads();
+        long long before = base, chunk = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if (i < warp) before += sh[i];
+            chunk += sh[i];
+        }
+        if (at >= before + incl - w && at < before + incl) {
+            sh[W] = n;
+            sh[W + 1] = before + incl - w;
+        }
+        base += chunk;
+        if (at < base) break;                       // uniform: the block has found it
+    }
+    __syncthreads();
+    r.n = (int)sh[W];
+    r.start = sh[W + 1];
+    return r;
+}
+
+// Bytes of the partial slots of a launch of `ctas` CTAs, row tiles of `rt`.
+inline size_t tree_part_bytes(int ctas, int rt, int d)
+{
+    return (size_t)ctas * 2 * rt * (d + 2) * sizeof(float);
+}
+
+struct TreePlan {
+    int rt, ctas;               // rows per item, CTAs of the launch
+    bool tc;
+    size_t bytes;               // workspace
+};
+TreePlan tree_plan(int32_t N, int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype_t dtype,
+                   int sms);
+
+cudaError_t launch_tree_attention(TreeArgs args, const TreePlan& plan, int32_t d,
+                                  kda_dtype_t dtype, cudaStream_t stream);
+
+}  // namespace kda

@@ -389,6 +389,148 @@ kda_status_t kda_prefill_noalloc(const void *q, const void *k, const void *v,
                                  kda_dtype_t dtype, void *o, float *S_final,
                                  cudaStream_t stream);
 
+/* ---- Verifying a tree of drafted tokens --------------------------------
+ *
+ * The KDA layers of a model stand beside layers of softmax attention over a
+ * cache ("[논문 리뷰] Kimi K3 Technical Report", section 1: 69 of 93 layers are
+ * KDA), and a drafter may propose a tree instead of a chain.  One verification
+ * step is then: kda_decode_tree in the KDA layers, kda_tree_attention in the
+ * others, kda_token_logprobs on the logits; and after the caller has chosen
+ * the accepted path, kda_state_gather (with accept[n] = last accepted node + 1)
+ * and kda_cache_commit.
+ *
+ * A tree is given as parent[n][t] (device int32 [N, Ts], Ts <= 64, more is
+ * KDA_ERR_UNSUPPORTED): the node that node t follows, an earlier one (< t), or
+ * -1 when t follows the context directly.  A node with any other parent, or
+ * with an unused parent, is unused: it takes no part and its output is 0, so
+ * sequences with fewer nodes fill their rows with -2.  A NULL parent is the
+ * chain parent[t] = t - 1.
+ *
+ * A cache is a pool of num_pages pages of page_size rows of Hkv heads,
+ * [num_pages, page_size, Hkv, d], dense within a page, page p starting
+ * page_stride elements after page p - 1 (page_stride >= page_size * Hkv * d,
+ * a multiple of 16 bytes).  page_table [N, max_pages] (device int32) names the
+ * pages of each sequence in order: position i of sequence n is row i %
+ * page_size of page page_table[n][i / page_size].  Entries that no position
+ * needs are never read; one that names no page (outside [0, num_pages)) hides
+ * its positions from attention and drops rows written to it.  Any page_size
+ * >= 1 will do; max_pages * page_size must fit 31 bits. */
+
+/* Bytes of device workspace kda_tree_attention needs (partial results of
+ * sequences whose keys are spread over several CTAs; it depends on the SM
+ * count, not on N or the lengths).  0 for bad arguments. */
+size_t kda_tree_attention_workspace_bytes(int32_t N, int32_t Ts, int32_t Hq,
+                                          int32_t Hkv, int32_t d,
+                                          kda_dtype_t dtype);
+
+/* Softmax attention of drafted nodes: node t of sequence n, query head h sees
+ * the lengths[n] rows of its sequence in the cache and, among the drafted
+ * nodes, its ancestors and itself, all in cache head g = h / (Hq / Hkv):
+ *     o = sum_j softmax_j(scale q . k_j) v_j.
+ * Ts = 1 is the attention of ordinary decode; a NULL parent a causal block.
+ *
+ *   q, o          [N, Ts, Hq, d];  k, v: [N, Ts, Hkv, d], the drafted nodes'
+ *                 own keys and values (the cache is only read); Hkv divides Hq
+ *   parent        see above
+ *   k_cache, v_cache, page_table, num_pages, page_size, max_pages, page_stride
+ *                 see above; in q's dtype.  May be NULL when num_pages or
+ *                 max_pages is 0 (no context).  Rows past lengths[n] are never
+ *                 read, whatever they hold.
+ *   lengths       device int32 [N], context rows (values outside [0, max_pages
+ *                 * page_size] are clamped)
+ *   workspace     kda_tree_attention_workspace_bytes(...) bytes, 256-byte
+ *                 aligned, not shared with concurrent calls; contents on entry
+ *                 do not matter
+ * dtype is that of q, k, v and the cache, and of o.  An infinity or NaN in a
+ * node's k or v reaches the nodes that see it and no others.  The result does
+ * not depend on timing (no atomics on values); it may differ in rounding
+ * between GPUs with different SM counts. */
+kda_status_t kda_tree_attention(const void *q, const void *k, const void *v,
+                                const int32_t *parent, const void *k_cache,
+                                const void *v_cache, const int32_t *page_table,
+                                const int32_t *lengths, int32_t N, int32_t Ts,
+                                int32_t Hq, int32_t Hkv, int32_t d,
+                                int32_t num_pages, int32_t page_size,
+                                int32_t max_pages, int64_t page_stride,
+                                kda_dtype_t dtype, float scale, void *o,
+                                void *workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
+/* kda_decode_multi over a tree: node t is one decode step from the state after
+ * its parent node (parent -1: from S_in).  Arguments are those of
+ * kda_decode_multi, plus parent (see above; NULL is kda_decode_multi itself).
+ * states[n, t] of an unused node is not written; its o is 0. */
+kda_status_t kda_decode_tree(const void *q, const void *k, const void *v,
+                             const float *log_alpha, const float *beta,
+                             const float *S_in, const int32_t *parent, int32_t N,
+                             int32_t Ts, int32_t H, int32_t d_k, int32_t d_v,
+                             kda_dtype_t dtype, void *o, float *states,
+                             cudaStream_t stream);
+
+/* For each row of logits x, with lse = log sum_i e^{x_i}: the log
+ * probabilities x_i - lse of given tokens, the entropy -sum p log p, and the K
+ * most probable tokens.
+ *
+ *   logits        [T, V] in rows of row_stride elements (>= V, any), base
+ *                 16-byte aligned; bf16 (KDA_BF16_F32OUT) or fp32 (KDA_FP32)
+ *   tokens        device int32 [T, J], J >= 0 (none: NULL)
+ *   logprobs      [T, J] fp32 (written); -inf for a token outside [0, V)
+ *   entropy       [T] fp32 (written) or NULL
+ *   top_ids, top_logprobs   [T, K] int32 and fp32 (written), 0 <= K <= min(V,
+ *                 32) (more than 32 is KDA_ERR_UNSUPPORTED), most probable
+ *                 first, equal logits by the lower index; NULL when K is 0
+ * A logit of -inf is a masked token.  A row of nothing but -inf gives -inf log
+ * probabilities and entropy 0.  A NaN or +inf logit makes its row's
+ * logprobs and entropy NaN; in the order of top_ids NaN counts as -inf. */
+kda_status_t kda_token_logprobs(const void *logits, int64_t row_stride,
+                                const int32_t *tokens, int32_t T, int32_t V,
+                                int32_t J, int32_t K, kda_dtype_t dtype,
+                                float *logprobs, float *entropy,
+                                int32_t *top_ids, float *top_logprobs,
+                                cudaStream_t stream);
+
+/* The accepted nodes' rows into the cache, for all layers at once: row
+ * path[n][i] of k and v goes to position lengths[n] + i of sequence n, for
+ * i < count[n].
+ *
+ *   k, v          [layers, N, Ts, Hkv, d], any dtype code (o's part of it does
+ *                 not matter); Ts may be any size
+ *   path          device int32 [N, Ts] or NULL (path[i] = i); entries outside
+ *                 [0, Ts) are skipped (their position is not written)
+ *   count         device int32 [N] or NULL (all Ts), clamped to [0, Ts]
+ *   lengths       device int32 [N], rows already there
+ *   k_cache, v_cache, page_table, ...   see above; layer l starts layer_stride
+ *                 elements after layer l - 1 (>= page_size * Hkv * d, a multiple
+ *                 of 16 bytes; ignored for one layer).  Rows past the table or
+ *                 to entries that name no page are dropped.  Two sequences must
+ *                 not write one row.
+ *   new_lengths   [N] (written: lengths + count) or NULL; must not overlap
+ *                 lengths, which other CTAs still read
+ * k and v must not overlap the cache. */
+kda_status_t kda_cache_commit(const void *k, const void *v, const int32_t *path,
+                              const int32_t *count, const int32_t *page_table,
+                              const int32_t *lengths, int32_t layers, int32_t N,
+                              int32_t Ts, int32_t Hkv, int32_t d,
+                              int32_t num_pages, int32_t page_size,
+                              int32_t max_pages, int64_t page_stride,
+                              int64_t layer_stride, kda_dtype_t dtype,
+                              void *k_cache, void *v_cache, int32_t *new_lengths,
+                              cudaStream_t stream);
+
+/* The same for a packed batch (a prefill): k, v [layers, total_tokens, Hkv, d],
+ * sequence n owning rows cu_seqlens[n] .. cu_seqlens[n+1] - 1 (device int32
+ * [N+1], as in kda_prefill), which go to positions lengths[n], lengths[n] + 1,
+ * and so on.  Rows that cu_seqlens gives to no sequence are dropped. */
+kda_status_t kda_cache_append(const void *k, const void *v,
+                              const int32_t *cu_seqlens, int64_t total_tokens,
+                              const int32_t *page_table, const int32_t *lengths,
+                              int32_t layers, int32_t N, int32_t Hkv, int32_t d,
+                              int32_t num_pages, int32_t page_size,
+                              int32_t max_pages, int64_t page_stride,
+                              int64_t layer_stride, kda_dtype_t dtype,
+                              void *k_cache, void *v_cache, int32_t *new_lengths,
+                              cudaStream_t stream);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char *kda_status_string(kda_status_t status);
 
