@@ -1,16 +1,17 @@
 // kda_tree.cuh -- what the tree attention kernels share: the arguments, the
 // drafted tree's ancestor masks, and the split of the work over the CTAs.
 //
-// Work split.  An item is one (sequence, cache head, row tile): up to RT query
-// rows (node t, query head of the group) against the sequence's context and
-// drafted nodes.  Its keys come in tiles of KT: ceil(L / KT) tiles of the
-// context, then one tile that holds the drafted nodes.  Laid end to end in
-// (sequence, head, row tile, key tile) order, the tiles are cut into equal
-// ranges, one per CTA, whatever the lengths are; the lengths stay on the device
-// and every CTA finds its own range from them.  A range covers at most one
-// item that began in an earlier CTA and one that goes on in the next: those
-// pieces go to the CTA's two workspace slots as (unnormalised o, m, l), and a
-// second launch joins them.  Every other item is finished in its CTA.
+// Work split.  An item is one (sequence, cache head); its keys come in tiles of
+// KT: ceil(L / KT) tiles of the context, then one tile that holds the drafted
+// nodes.  Laid end to end in (sequence, head, tile) order, the tiles are cut
+// into equal ranges, one per group of CTAs, whatever the lengths are; the
+// lengths stay on the device and every CTA finds its own range from them.  The
+// CTAs of a group have one row tile (up to RT of the item's Ts G query rows)
+// each and walk the same keys side by side, so that all but one find them in
+// L2.  A range covers at most one item that began in an earlier group and one
+// that goes on in the next: those pieces go to the CTA's two workspace slots as
+// (unnormalised o, m, l), and a second launch joins them.  Every other item is
+// finished in its CTAs.
 #pragma once
 
 #include "kda_internal.cuh"
@@ -31,7 +32,7 @@ struct TreeArgs {
     void* o;
     int32_t* status;                  // workspace words (kWsTimeoutWord is used)
     float* part;                      // 2 slots per CTA: [RT][d] o, [RT] m, [RT] l
-    int32_t ctas, row_tiles;
+    int32_t groups, row_tiles;        // CTA b: group b / row_tiles, row tile b % row_tiles
 };
 
 __device__ __forceinline__ int tree_context(const TreeArgs& a, int n)
@@ -94,7 +95,7 @@ __device__ __forceinline__ void tree_masks(const int32_t* parent, int Ts, int la
     __syncwarp();
 }
 
-// A position in the flattened tile order.
+// Where a group's range begins in the flattened tile order.
 struct TreeSpot {
     long long total;        // tiles of the whole launch
     long long start;        // first tile of sequence n
@@ -107,21 +108,20 @@ __device__ __forceinline__ long long tree_seq_tiles(const TreeArgs& a, int n)
     return ((long long)tree_context(a, n) + KT - 1) / KT + 1;
 }
 
-// First tile of CTA c's range.
-__device__ __forceinline__ long long tree_begin(long long total, int c, int ctas)
+// First tile of group c's range.
+__device__ __forceinline__ long long tree_begin(long long total, int c, int groups)
 {
-    return total * c / ctas;
+    return total * c / groups;
 }
 
-// The sequence that holds the first tile of CTA c's range (c < ctas, range not
-// empty).  All THREADS threads of the block call it; `sh` is shared scratch of
+// The sequence that holds the first tile of group c's range (c < groups).  All THREADS threads of the block call it; `sh` is shared scratch of
 // THREADS / 32 + 2 words.
 template <int THREADS, int KT>
 __device__ TreeSpot tree_locate(const TreeArgs& a, int c, long long* sh)
 {
     constexpr int W = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long items = (long long)a.Hkv * a.row_tiles;
+    const long long items = a.Hkv;
     long long sum = 0;
     for (int n = tid; n < a.N; n += THREADS) sum += tree_seq_tiles<KT>(a, n) * items;
 #pragma unroll
@@ -133,7 +133,7 @@ __device__ TreeSpot tree_locate(const TreeArgs& a, int c, long long* sh)
     r.total = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) r.total += sh[i];
-    const long long at = tree_begin(r.total, c, a.ctas);
+    const long long at = tree_begin(r.total, c, a.groups);
     long long base = 0;
     for (int n0 = 0; n0 < a.N; n0 += THREADS) {
         const int n = n0 + tid;
@@ -166,21 +166,45 @@ __device__ TreeSpot tree_locate(const TreeArgs& a, int c, long long* sh)
     return r;
 }
 
-// Bytes of the partial slots of a launch of `ctas` CTAs, row tiles of `rt`.
-inline size_t tree_part_bytes(int ctas, int rt, int d)
+// A stretch of one item's tiles in a group's range.
+struct TreePiece {
+    int n, hk, ctx;
+    int tiles, t0, t1;      // the item's tiles, and those of this piece
+};
+
+// Takes the next piece of [pos, end) and moves pos and sp behind it.
+template <int KT>
+__device__ __forceinline__ TreePiece tree_next(const TreeArgs& a, TreeSpot& sp, long long& pos,
+                                               long long end)
 {
-    return (size_t)ctas * 2 * rt * (d + 2) * sizeof(float);
+    TreePiece w;
+    w.n = sp.n;
+    w.ctx = tree_context(a, w.n);
+    w.tiles = (w.ctx + KT - 1) / KT + 1;
+    const long long at = pos - sp.start;
+    w.hk = (int)(at / w.tiles);
+    w.t0 = (int)(at - (long long)w.hk * w.tiles);
+    const long long left = end - pos;
+    w.t1 = left < w.tiles - w.t0 ? w.t0 + (int)left : w.tiles;
+    pos += w.t1 - w.t0;
+    if (w.t1 == w.tiles && w.hk == a.Hkv - 1) {
+        sp.start += (long long)w.tiles * a.Hkv;
+        ++sp.n;
+    }
+    return w;
 }
 
 struct TreePlan {
-    int rt, ctas;               // rows per item, CTAs of the launch
+    int rt;                 // rows per row tile
+    int row_tiles, groups;
     bool tc;
-    size_t bytes;               // workspace
 };
-TreePlan tree_plan(int32_t N, int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype_t dtype,
-                   int sms);
+// Workspace of a call, enough for either kernel.
+size_t tree_workspace_bytes(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype_t dtype, int sms);
 
-cudaError_t launch_tree_attention(TreeArgs args, const TreePlan& plan, int32_t d,
-                                  kda_dtype_t dtype, cudaStream_t stream);
+cudaError_t launch_tree_attention(TreeArgs args, int32_t d, kda_dtype_t dtype, int sms,
+                                  cudaStream_t stream);
+cudaError_t launch_tree_attention_tc(const TreeArgs& args, const TreePlan& plan, int32_t d,
+                                     cudaStream_t stream);
 
 }  // namespace kda

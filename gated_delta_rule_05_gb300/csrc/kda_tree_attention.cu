@@ -60,21 +60,17 @@ tree_attention_simt_kernel(const TreeArgs a)
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const TI* q = static_cast<const TI*>(a.q);
 
-    TreeSpot sp = tree_locate<kSimtThreads, kSimtKeys>(a, blockIdx.x, sh_loc);
-    long long pos = tree_begin(sp.total, blockIdx.x, a.ctas);
-    const long long end = tree_begin(sp.total, blockIdx.x + 1, a.ctas);
-    if (pos >= end) return;
-    const int items = a.Hkv * a.row_tiles;
+    const int group = blockIdx.x / a.row_tiles, r0 = (blockIdx.x % a.row_tiles) * RT;
+    const int rows = a.R - r0 < RT ? a.R - r0 : RT;
+    TreeSpot sp = tree_locate<kSimtThreads, kSimtKeys>(a, group, sh_loc);
+    long long pos = tree_begin(sp.total, group, a.groups);
+    const long long end = tree_begin(sp.total, group + 1, a.groups);
     const int row_elems = a.Hkv * D;
     int have = -1;                                  // the sequence anc[] is of
 
     while (pos < end) {
-        const int n = sp.n, ctx = tree_context(a, n);
-        const int tiles = (int)tree_seq_tiles<kSimtKeys>(a, n);
-        const int item = (int)((pos - sp.start) / tiles), t0 = (int)((pos - sp.start) % tiles);
-        const int t1 = (int)(end - pos < tiles - t0 ? t0 + (end - pos) : tiles);
-        const int hk = item / a.row_tiles, r0 = (item % a.row_tiles) * RT;
-        const int rows = a.R - r0 < RT ? a.R - r0 : RT;
+        const TreePiece w = tree_next<kSimtKeys>(a, sp, pos, end);
+        const int n = w.n, ctx = w.ctx, tiles = w.tiles, t0 = w.t0, t1 = w.t1, hk = w.hk;
         const int32_t* table = a.page_table + (long long)n * a.max_pages;
         if (have != n) {
             __syncthreads();
@@ -227,7 +223,7 @@ tree_attention_simt_kernel(const TreeArgs a)
             if (whole) {
                 const int t = (r0 + r) / a.G, g = (r0 + r) % a.G;
                 TO* op = static_cast<TO*>(a.o) + (((long long)n * a.Ts + t) * a.Hq + hk * a.G + g) * D;
-                const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+                const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
                 for (int c = 0; c < CR; ++c) st_f(op + tx + 16 * c, mask[i] ? acc[i][c] * inv : 0.f);
             } else {
@@ -239,18 +235,13 @@ tree_attention_simt_kernel(const TreeArgs a)
                 }
             }
         }
-        pos += t1 - t0;
-        if (t1 == tiles && item == items - 1) {
-            sp.start += (long long)tiles * items;
-            ++sp.n;
-        }
     }
 }
 
-// Joins the pieces of the items that were cut between CTAs.  Block (c, y): the
-// item that the boundary before CTA c + 1 falls into, if that is the item's
-// first boundary; rows y 8 .. y 8 + 7 of it.  The pieces are read in the order
-// of the CTAs, so the result does not depend on timing.
+// Joins the pieces of the items that were cut between groups.  Block (c, y, z):
+// the item that the boundary before group c + 1 falls into, if that is the
+// item's first boundary; rows y 8 .. y 8 + 7 of row tile z.  The pieces are read
+// in the order of the groups, so the result does not depend on timing.
 constexpr int kJoinThreads = 128;
 constexpr int kJoinRows = 8;
 
@@ -261,15 +252,14 @@ tree_join_kernel(const TreeArgs a, int RT)
     __shared__ long long sh_loc[kJoinThreads / 32 + 2];
     const int c = blockIdx.x + 1, tid = threadIdx.x;
     const TreeSpot sp = tree_locate<kJoinThreads, KT>(a, c, sh_loc);
-    const long long at = tree_begin(sp.total, c, a.ctas);
-    if (at >= sp.total) return;
+    const long long at = tree_begin(sp.total, c, a.groups);
     const int tiles = (int)tree_seq_tiles<KT>(a, sp.n);
-    const int item = (int)((at - sp.start) / tiles);
-    const long long first = sp.start + (long long)item * tiles;
-    if (at == first || tree_begin(sp.total, c - 1, a.ctas) > first) return;
-    int last = c;                                   // the last CTA with tiles of this item
-    while (last + 1 < a.ctas && tree_begin(sp.total, last + 1, a.ctas) < first + tiles) ++last;
-    const int hk = item / a.row_tiles, r0 = (item % a.row_tiles) * RT;
+    const int hk = (int)((at - sp.start) / tiles);
+    const long long first = sp.start + (long long)hk * tiles;
+    if (at == first || tree_begin(sp.total, c - 1, a.groups) > first) return;
+    int last = c;                                   // the last group with tiles of this item
+    while (last + 1 < a.groups && tree_begin(sp.total, last + 1, a.groups) < first + tiles) ++last;
+    const int r0 = blockIdx.z * RT;
     const int rows = a.R - r0 < RT ? a.R - r0 : RT;
     const size_t slot = (size_t)RT * (D + 2);
     constexpr int LPR = D / 4;                      // lanes per row
@@ -279,10 +269,11 @@ tree_join_kernel(const TreeArgs a, int RT)
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int p = c - 1; p <= last; ++p) {
-            if (tree_begin(sp.total, p, a.ctas) == tree_begin(sp.total, p + 1, a.ctas)) continue;
-            const float* part = a.part + ((size_t)p * 2 + (p == c - 1 ? 1 : 0)) * slot;
+            if (tree_begin(sp.total, p, a.groups) == tree_begin(sp.total, p + 1, a.groups)) continue;
+            const float* part =
+                a.part + (((size_t)p * a.row_tiles + blockIdx.z) * 2 + (p == c - 1 ? 1 : 0)) * slot;
             const float pm = part[RT * D + r], pl = part[RT * D + RT + r];
-            const float4 x = *reinterpret_cast<const float4*>(part + r * D + c4);
+            const float4 x = *reinterpret_cast<const float4*>(part + (size_t)r * D + c4);
             const float top = fmaxf(m, pm);
             const float ref = top == -INFINITY ? 0.f : top;
             const float f = exp2f(m - ref), w = exp2f(pm - ref);
@@ -293,7 +284,7 @@ tree_join_kernel(const TreeArgs a, int RT)
             o.w = o.w * f + x.w * w;
             m = top;
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;   // l = 0: an unused node; a NaN stays
         const int t = (r0 + r) / a.G, g = (r0 + r) % a.G;
         TO* op = static_cast<TO*>(a.o) + (((long long)sp.n * a.Ts + t) * a.Hq + hk * a.G + g) * D + c4;
         st_f(op, o.x * inv);
@@ -303,6 +294,16 @@ tree_join_kernel(const TreeArgs a, int RT)
     }
 }
 
+template <typename TO, int D, int KT>
+cudaError_t launch_join(const TreeArgs& a, int rt, cudaStream_t stream)
+{
+    if (a.groups < 2) return cudaSuccess;
+    const int rows = a.R < rt ? a.R : rt;
+    const dim3 grid(a.groups - 1, (rows + kJoinRows - 1) / kJoinRows, a.row_tiles);
+    tree_join_kernel<TO, D, KT><<<grid, kJoinThreads, 0, stream>>>(a, rt);
+    return cudaGetLastError();
+}
+
 template <typename TI, typename TO, int D, int RT>
 cudaError_t launch_simt(const TreeArgs& a, cudaStream_t stream)
 {
@@ -310,7 +311,7 @@ cudaError_t launch_simt(const TreeArgs& a, cudaStream_t stream)
     const size_t bytes = SimtShape<D, RT>::kBytes;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    kern<<<a.ctas, kSimtThreads, bytes, stream>>>(a);
+    kern<<<a.groups * a.row_tiles, kSimtThreads, bytes, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -319,11 +320,8 @@ cudaError_t launch_d(const TreeArgs& a, const TreePlan& plan, cudaStream_t strea
 {
     cudaError_t e = plan.rt == 8 ? launch_simt<TI, TO, D, 8>(a, stream)
                                  : launch_simt<TI, TO, D, 32>(a, stream);
-    if (e != cudaSuccess || a.ctas < 2) return e;
-    const int rows = a.R < plan.rt ? a.R : plan.rt;
-    const dim3 grid(a.ctas - 1, (rows + kJoinRows - 1) / kJoinRows);
-    tree_join_kernel<TO, D, kSimtKeys><<<grid, kJoinThreads, 0, stream>>>(a, plan.rt);
-    return cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_join<TO, D, kSimtKeys>(a, plan.rt, stream);
 }
 
 template <typename TI, typename TO>
@@ -340,24 +338,51 @@ cudaError_t launch_typed(const TreeArgs& a, const TreePlan& plan, int d, cudaStr
 
 }  // namespace
 
-TreePlan tree_plan(int32_t N, int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype_t dtype,
-                   int sms)
+TreePlan tree_plan(int32_t Ts, int32_t Hq, int32_t Hkv, int sms, bool tc)
 {
-    (void)N;
-    (void)dtype;
+    const int R = Ts * (Hq / Hkv);
     TreePlan p;
-    p.tc = false;
-    p.rt = (long long)Ts * (Hq / Hkv) <= 8 ? 8 : 32;
-    p.ctas = (sms > 0 ? sms : 1) * 2;
-    p.bytes = kWsHeaderBytes + tree_part_bytes(p.ctas, p.rt, d);
+    p.tc = tc;
+    p.rt = tc ? (R <= 128 ? 128 : 256) : (R <= 8 ? 8 : 32);
+    p.row_tiles = (R + p.rt - 1) / p.rt;
+    const int ctas = (sms > 0 ? sms : 1) * (tc ? 1 : 2);
+    p.groups = ctas / p.row_tiles > 1 ? ctas / p.row_tiles : 1;
     return p;
 }
 
-cudaError_t launch_tree_attention(TreeArgs args, const TreePlan& plan, int32_t d,
-                                  kda_dtype_t dtype, cudaStream_t stream)
+// The tensor-core kernel takes bf16 with d = 64 or 128 and bf16 output (its
+// probabilities are rounded to bf16, which an fp32 output would show).
+bool tree_tc_supported(int32_t d, kda_dtype_t dtype)
 {
-    args.ctas = plan.ctas;
-    args.row_tiles = (args.R + plan.rt - 1) / plan.rt;
+    return dtype == KDA_BF16 && (d == 64 || d == 128);
+}
+
+size_t tree_workspace_bytes(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype_t dtype, int sms)
+{
+    size_t most = 0;
+    for (int tc = 0; tc <= (int)tree_tc_supported(d, dtype); ++tc) {
+        const TreePlan p = tree_plan(Ts, Hq, Hkv, sms, tc != 0);
+        const size_t b = (size_t)p.groups * p.row_tiles * 2 * p.rt * (d + 2) * sizeof(float);
+        if (b > most) most = b;
+    }
+    return kWsHeaderBytes + most;
+}
+
+// A negative (or NaN) scale takes the CUDA-core kernel: the tensor-core one
+// finds a row's maximum before it applies the scale.
+cudaError_t launch_tree_attention(TreeArgs args, int32_t d, kda_dtype_t dtype, int sms,
+                                  cudaStream_t stream)
+{
+    const bool tc = tree_tc_supported(d, dtype) && args.scale_log2 >= 0.f && getenv("KDA_FORCE_SIMT") == nullptr;
+    const TreePlan plan = tree_plan(args.Ts, args.Hq, args.Hkv, sms, tc);
+    args.groups = plan.groups;
+    args.row_tiles = plan.row_tiles;
+    if (plan.tc) {
+        const cudaError_t e = launch_tree_attention_tc(args, plan, d, stream);
+        if (e != cudaSuccess) return e;
+        return d == 64 ? launch_join<__nv_bfloat16, 64, 128>(args, plan.rt, stream)
+                       : launch_join<__nv_bfloat16, 128, 128>(args, plan.rt, stream);
+    }
     switch (dtype) {
         case KDA_BF16: return launch_typed<__nv_bfloat16, __nv_bfloat16>(args, plan, d, stream);
         case KDA_BF16_F32OUT: return launch_typed<__nv_bfloat16, float>(args, plan, d, stream);

@@ -1,0 +1,682 @@
+// kda_tree_attention_tc.cu -- the tensor-core form of the tree attention (bf16,
+// d = 64 or 128): one CTA per SM, tcgen05 products with TMEM accumulators.
+//
+// Per tile of 128 keys and 128 query rows (lane = row):
+//     S = Q K^T             (M = 128, N = 128, K = d; Q, K in shared memory)
+//     P = 2^(c S - m)       (registers; c = scale log2 e; bf16 back over S)
+//     O += P V              (M = 128, N = d, K = 128; P in TMEM, V MN-major)
+// with the running maximum m and sum l of each row in the registers of the
+// thread that owns the row.  m moves only when a tile exceeds it by more than
+// 8, i.e. P may reach 2^8: then O and l are scaled by 2^(m - m').  Any m gives
+// the same quotient O / l, and after the first tiles of a row O is left alone.
+// P is rounded to bf16, the type of V, as one product takes one type; l sums
+// the values before the rounding.
+//
+// Roles: a warpgroup per 128 query rows (softmax and output), one warp that
+// issues the products, four warps that copy keys and values.  With up to 128
+// rows (RT = 128) S is double-buffered, so that the next tile's scores are
+// computed during this tile's softmax; with more (RT = 256) two row tiles share
+// every K and V tile and alternate on the tensor core.
+//
+// Copies: 16-byte cp.async by 16 lanes per row (d = 128), which take any page
+// size and page stride, and fill rows past the length and rows of pages that do
+// not exist with zeros, so that nothing stored there can reach a product.  They
+// run ahead through a ring of tiles.  A row of drafted values is copied through
+// registers instead, and an infinity or NaN in it is replaced by 0: the
+// product's 0 * inf would reach rows that do not see the node.  The rows that
+// do see it add it to their output at the end.
+//
+// Every wait has a limit (mbar_wait); a wait that gives up sets the workspace's
+// timeout word, and the CTA runs to its end without waiting again.
+#include "kda_sm100.cuh"
+#include "kda_tree.cuh"
+
+namespace kda {
+namespace {
+
+using namespace sm100;
+
+constexpr int KT = 128;                    // keys per tile
+constexpr int kRingMeta = 16;              // tiles whose key masks are kept
+
+template <int D, int NT>
+struct TcShape {
+    static constexpr int kQBytes = NT * 128 * D * 2;
+    static constexpr int kSlotBytes = KT * D * 2;
+    static constexpr int kSlots = (D == 128) ? (NT == 1 ? 6 : 5) : 12;
+    static constexpr int kThreads = NT * 128 + 32 + 128;
+    static constexpr int kMmaWarp = NT * 4;
+    static constexpr int kCopyWarp = NT * 4 + 1;
+    static constexpr size_t kBytes = 1024 + kQBytes + (size_t)kSlots * kSlotBytes;
+    // TMEM columns
+    static constexpr int kS1 = 128, kO0 = 256, kO1 = 256 + D;
+};
+
+struct TcShared {
+    uint64_t kv_full[12], kv_empty[12], q_empty, done;
+    uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2];
+    uint32_t tmem;
+    int dead;
+    uint32_t keys[kRingMeta][4];           // valid keys of a context tile
+    uint32_t bad[kRingMeta][2];            // drafted nodes of a piece whose v is not finite
+    long long loc[16 + 2];
+};
+
+// Waits unless some wait of this CTA has already given up.
+__device__ __forceinline__ void wait(TcShared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
+{
+    if (mbar_try_wait(bar, parity)) return;
+    if (*reinterpret_cast<volatile int*>(&sh.dead)) return;
+    if (!mbar_wait(bar, parity)) {
+        *reinterpret_cast<volatile int*>(&sh.dead) = 1;
+        atomicOr(status + kWsTimeoutWord, 2);
+    }
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Waits until at most `left` of this thread's groups are in flight.
+__device__ __forceinline__ void cp_async_wait(int left)
+{
+    switch (left) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+        case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+        case 7: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+        case 8: asm volatile("cp.async.wait_group 8;" ::: "memory"); break;
+        case 9: asm volatile("cp.async.wait_group 9;" ::: "memory"); break;
+        case 10: asm volatile("cp.async.wait_group 10;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 11;" ::: "memory"); break;
+    }
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Which of eight bf16 (four words) are inf or NaN are set to 0; returns whether any was.
+__device__ __forceinline__ bool clear_nonfinite(uint4& x)
+{
+    uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0x7F80u) == 0x7F80u) { w[i] &= 0xFFFF0000u; any = true; }
+        if ((w[i] & 0x7F800000u) == 0x7F800000u) { w[i] &= 0x0000FFFFu; any = true; }
+    }
+    return any;
+}
+
+// anc[t] of one node (see tree_masks), by a whole warp: pointer doubling in
+// registers, two nodes per lane, then each lane picks its t.
+__device__ __forceinline__ unsigned long long tree_mask_of(const int32_t* parent, int Ts, int lane, int t)
+{
+    unsigned long long m[2];
+    int u[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int x = lane + 32 * i;
+        int p = -2;
+        if (x < Ts) {
+            p = parent ? __ldg(parent + x) : x - 1;
+            if (p < -1 || p >= x) p = -2;
+        }
+        m[i] = 1ull << x;
+        u[i] = p;
+    }
+#pragma unroll
+    for (int round = 0; round < 6; ++round) {
+        unsigned long long m2[2];
+        int u2[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int src = u[i] & 31;
+            const unsigned long long a = __shfl_sync(0xffffffffu, m[0], src);
+            const unsigned long long b = __shfl_sync(0xffffffffu, m[1], src);
+            const int ua = __shfl_sync(0xffffffffu, u[0], src), ub = __shfl_sync(0xffffffffu, u[1], src);
+            const bool up = u[i] >= 0, hi = u[i] >= 32;
+            m2[i] = m[i] | (up ? (hi ? b : a) : 0ull);
+            u2[i] = up ? (hi ? ub : ua) : u[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            m[i] = m2[i];
+            u[i] = u2[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (u[i] != -1) m[i] = 0ull;
+    const unsigned long long a = __shfl_sync(0xffffffffu, m[0], t & 31);
+    const unsigned long long b = __shfl_sync(0xffffffffu, m[1], t & 31);
+    return t >= 32 ? b : a;
+}
+
+// ---------------------------------------------------------------- the copies
+// Four warps.  A ring entry is one K or V tile; the entries of a piece are K_0,
+// then (RT = 128) K_1 V_0 K_2 V_1 ... V_last or (RT = 256) V_0 K_1 V_1 ..., the
+// order in which the products take them.  Q goes with the piece's first entry.
+template <int D, int NT>
+struct Copier {
+    using Sh = TcShape<D, NT>;
+    static constexpr int LPR = D / 8;              // lanes per row of 16-byte chunks
+    static constexpr int RPI = 32 / LPR;           // rows per instruction
+    TcShared& sh;
+    const TreeArgs& a;
+    uint32_t q_smem, slots;
+    int lane, warp;                                // warp 0 .. 3
+    int next = 0, landed = 0;                      // entries issued, entries handed over
+
+    __device__ uint32_t entry(int i) const { return slots + (uint32_t)(i % Sh::kSlots) * Sh::kSlotBytes; }
+
+    // Byte offset of chunk c of row r in a tile of `rows` rows: 128-byte rows
+    // with the 128-byte swizzle, one block of rows per 64 columns.
+    static __device__ uint32_t at(int r, int c, int rows)
+    {
+        return (uint32_t)(c >> 3) * (uint32_t)(rows * 128) + (uint32_t)r * 128 +
+               (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+    }
+
+    // Hands the oldest entry in flight over to the products.
+    __device__ void hand_over()
+    {
+        cp_async_wait(next - landed - 1);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.kv_full[landed % Sh::kSlots]);
+        ++landed;
+    }
+
+    // A wait during which landed entries are handed over.
+    __device__ void wait_for(uint64_t* bar, uint32_t parity)
+    {
+        while (landed < next) {
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
+            hand_over();
+        }
+        wait(sh, bar, parity, a.status);
+        __syncwarp();
+    }
+
+    __device__ void wait_slot()
+    {
+        const int use = next / Sh::kSlots;
+        if (use > 0) wait_for(&sh.kv_empty[next % Sh::kSlots], (uint32_t)(use - 1) & 1);
+    }
+
+    // 32 rows of this warp, row `lane`'s source at p (null: zeros) for lane's own row.
+    __device__ void rows32(uint32_t dst, int row0, int rows, const __nv_bfloat16* p)
+    {
+        const int c = lane % LPR;
+        const unsigned long long mine = reinterpret_cast<unsigned long long>(p);
+        const void* any = a.q;
+#pragma unroll 4
+        for (int i = 0; i < 32 / RPI; ++i) {
+            const int j = i * RPI + lane / LPR;
+            const unsigned long long src = __shfl_sync(0xffffffffu, mine, j);
+            const void* from = src ? reinterpret_cast<const void*>(src + 16ull * c) : any;
+            cp_async16(dst + at(row0 + j, c, rows), from, src ? 16u : 0u);
+        }
+    }
+
+    __device__ void finish_entry()
+    {
+        cp_async_commit();
+        ++next;
+    }
+
+    __device__ void load_q(const TreePiece& w, int r0)
+    {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int r = r0 + i * 128 + warp * 32 + lane;
+            const __nv_bfloat16* p = nullptr;
+            if (r < a.R) {
+                const int t = r / a.G, g = r - t * a.G;
+                p = static_cast<const __nv_bfloat16*>(a.q) +
+                    (((long long)w.n * a.Ts + t) * a.Hq + w.hk * a.G + g) * D;
+            }
+            rows32(q_smem + i * 128 * D * 2, warp * 32, 128, p);
+        }
+    }
+
+    // Element offset of this lane's row of tile t (-1: none), the same for K and V.
+    __device__ long long row_of(const TreePiece& w, int t) const
+    {
+        const int j = warp * 32 + lane, row_elems = a.Hkv * D;
+        if (t == w.tiles - 1)
+            return j < a.Ts ? ((long long)w.n * a.Ts + j) * row_elems + (long long)w.hk * D : -1;
+        const int pos = t * KT + j;
+        if (pos >= w.ctx) return -1;
+        const long long off = tree_cache_row(a, a.page_table + (long long)w.n * a.max_pages, pos, row_elems);
+        return off < 0 ? -1 : off + (long long)w.hk * D;
+    }
+
+    __device__ void load_k(const TreePiece& w, int t, long long off, int g)
+    {
+        const bool draft = t == w.tiles - 1;
+        const uint32_t there = __ballot_sync(0xffffffffu, off >= 0);
+        if (lane == 0) sh.keys[g % kRingMeta][warp] = there;
+        const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(draft ? a.k : a.k_cache);
+        rows32(entry(next), warp * 32, KT, off >= 0 ? k + off : nullptr);
+        finish_entry();
+    }
+
+    __device__ void load_v(const TreePiece& w, int t, long long off, int piece)
+    {
+        if (t < w.tiles - 1) {
+            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_cache);
+            rows32(entry(next), warp * 32, KT, off >= 0 ? v + off : nullptr);
+        } else {
+            const int c = lane % LPR;
+            uint32_t bad = 0;
+            for (int i = 0; i < 32 / RPI; ++i) {
+                const int j = i * RPI + lane / LPR;
+                const long long src = __shfl_sync(0xffffffffu, off, j);
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (src >= 0)
+                    x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + src + 8 * c));
+                if (clear_nonfinite(x)) bad |= 1u << j;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(entry(next) + at(warp * 32 + j, c, KT)),
+                             "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                             : "memory");
+            }
+            bad = __reduce_or_sync(0xffffffffu, bad);
+            if (lane == 0 && warp < 2) sh.bad[piece % kRingMeta][warp] = bad;
+        }
+        finish_entry();
+    }
+};
+
+template <int D, int NT>
+__device__ void copy_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint32_t slots, TreeSpot sp,
+                          long long pos, long long end, int r0, int warp, int lane)
+{
+    Copier<D, NT> c{sh, a, q_smem, slots, lane, warp};
+    int g = 0, piece = 0;                          // tiles and pieces so far
+    while (pos < end) {
+        const TreePiece w = tree_next<KT>(a, sp, pos, end);
+        long long off = c.row_of(w, w.t0), ahead = -1;
+        c.wait_slot();
+        if (piece > 0) c.wait_for(&sh.q_empty, (uint32_t)(piece - 1) & 1);
+        c.load_q(w, r0);
+        c.load_k(w, w.t0, off, g);
+        for (int t = w.t0; t < w.t1; ++t, ++g) {
+            const bool more = t + 1 < w.t1;
+            if (more) ahead = c.row_of(w, t + 1);
+            if (NT == 1 && more) {
+                c.wait_slot();
+                c.load_k(w, t + 1, ahead, g + 1);
+            }
+            c.wait_slot();
+            c.load_v(w, t, off, piece);
+            if (NT == 2 && more) {
+                c.wait_slot();
+                c.load_k(w, t + 1, ahead, g + 1);
+            }
+            off = ahead;
+        }
+        ++piece;
+    }
+    while (c.landed < c.next) c.hand_over();
+}
+
+// -------------------------------------------------------------- the products
+template <int D, int NT>
+__device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint32_t slots, TreeSpot sp,
+                         long long pos, long long end, int r0, uint32_t tmem)
+{
+    using Sh = TcShape<D, NT>;
+    constexpr uint32_t id_qk = make_idesc_bf16(128, KT, false, false);
+    constexpr uint32_t id_pv = make_idesc_bf16(128, D, false, true);
+    int entry = 0;                                 // next ring entry to take
+    int tile = 0, piece = 0;
+    int used[2] = {0, 0};                          // tiles of each row tile so far
+    int pieces[2] = {0, 0};                        // pieces of each row tile so far
+    const int nt = (NT == 2 && a.R - r0 > 128) ? 2 : 1;
+
+    auto take = [&](int e) { wait(sh, &sh.kv_full[e % Sh::kSlots], (uint32_t)(e / Sh::kSlots) & 1, a.status);
+                             __syncwarp(); tc_fence_after(); };
+    auto qk = [&](int i, int e, uint32_t d_tmem) {
+        const uint64_t da = make_sdesc(q_smem + i * 128 * D * 2, 16, 1024, kSwizzle128B);
+        const uint64_t db = make_sdesc(slots + (uint32_t)(e % Sh::kSlots) * Sh::kSlotBytes, 16, 1024, kSwizzle128B);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+            const uint64_t off = (uint64_t)((s >> 2) * 1024 + 2 * (s & 3));
+            mma_ss(d_tmem, da + off, db + off, id_qk, s > 0);
+        }
+    };
+    auto pv = [&](int e, uint32_t p_tmem, uint32_t d_tmem, bool first) {
+        const uint64_t db = make_sdesc(slots + (uint32_t)(e % Sh::kSlots) * Sh::kSlotBytes, KT * 128, 1024, kSwizzle128B);
+#pragma unroll
+        for (int s = 0; s < KT / 16; ++s)
+            mma_ts(d_tmem, p_tmem + s * 8, db + 128 * s, id_pv, !(first && s == 0));
+    };
+
+    while (pos < end) {
+        const TreePiece w = tree_next<KT>(a, sp, pos, end);
+        const int cnt = w.t1 - w.t0;
+        take(entry);
+        if constexpr (NT == 1) {
+            qk(0, entry, tmem + (tile & 1) * Sh::kS1);
+            mma_commit(&sh.s_full[tile & 1]);
+            mma_commit(&sh.kv_empty[entry % Sh::kSlots]);
+            ++entry;
+            if (cnt == 1) mma_commit(&sh.q_empty);
+            for (int j = 0; j < cnt; ++j, ++tile) {
+                if (j + 1 < cnt) {
+                    take(entry);
+                    qk(0, entry, tmem + ((tile + 1) & 1) * Sh::kS1);
+                    mma_commit(&sh.s_full[(tile + 1) & 1]);
+                    mma_commit(&sh.kv_empty[entry % Sh::kSlots]);
+                    ++entry;
+                    if (j + 2 == cnt) mma_commit(&sh.q_empty);
+                }
+                take(entry);
+                wait(sh, &sh.p_full[tile & 1], (uint32_t)(tile >> 1) & 1, a.status);
+                if (j == 0 && piece > 0) wait(sh, &sh.o_empty[0], (uint32_t)(piece - 1) & 1, a.status);
+                __syncwarp();
+                tc_fence_after();
+                pv(entry, tmem + (tile & 1) * Sh::kS1, tmem + Sh::kO0, j == 0);
+                mma_commit(&sh.pv_done[0]);
+                mma_commit(&sh.kv_empty[entry % Sh::kSlots]);
+                ++entry;
+            }
+        } else {
+            for (int i = 0; i < nt; ++i) {
+                qk(i, entry, tmem + i * Sh::kS1);
+                mma_commit(&sh.s_full[i]);
+            }
+            mma_commit(&sh.kv_empty[entry % Sh::kSlots]);
+            if (cnt == 1) mma_commit(&sh.q_empty);
+            ++entry;
+            for (int j = 0; j < cnt; ++j) {
+                const bool more = j + 1 < cnt;
+                take(entry);
+                for (int i = 0; i < nt; ++i) {
+                    wait(sh, &sh.p_full[i], (uint32_t)used[i] & 1, a.status);
+                    if (j == 0 && pieces[i] > 0) wait(sh, &sh.o_empty[i], (uint32_t)(pieces[i] - 1) & 1, a.status);
+                    __syncwarp();
+                    tc_fence_after();
+                    pv(entry, tmem + i * Sh::kS1, tmem + (i ? Sh::kO1 : Sh::kO0), j == 0);
+                    mma_commit(&sh.pv_done[i]);
+                    if (more) {
+                        if (i == 0) take(entry + 1);
+                        qk(i, entry + 1, tmem + i * Sh::kS1);
+                        mma_commit(&sh.s_full[i]);
+                    }
+                    ++used[i];
+                }
+                mma_commit(&sh.kv_empty[entry % Sh::kSlots]);
+                if (more) mma_commit(&sh.kv_empty[(entry + 1) % Sh::kSlots]);
+                if (j + 2 == cnt) mma_commit(&sh.q_empty);
+                entry += more ? 2 : 1;
+            }
+            for (int i = 0; i < nt; ++i) ++pieces[i];
+        }
+        ++piece;
+    }
+    // the last arrivals on the ring's barriers come before the block ends
+    mma_commit(&sh.done);
+    wait(sh, &sh.done, 0, a.status);
+    __syncwarp();
+}
+
+// --------------------------------------------------- the softmax and the output
+template <int D, int NT>
+__device__ void softmax_role(TcShared& sh, const TreeArgs& a, TreeSpot sp, long long pos, long long end,
+                             int r0, int warp, int lane, uint32_t tmem)
+{
+    using Sh = TcShape<D, NT>;
+    constexpr int RT = NT * 128;
+    constexpr float kSlack = 8.f;
+    const int wg = warp >> 2;
+    const int local = warp * 32 + lane;            // row within the CTA's row tile
+    const int r = r0 + local;
+    const int rows = a.R - r0 < RT ? a.R - r0 : RT;
+    if (NT == 2 && wg * 128 >= rows) return;       // nothing in this row tile
+    const bool live = warp * 32 < rows;            // some row of this warp exists
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t to = lanes + (wg ? Sh::kO1 : Sh::kO0);
+    const int node = (r < a.R ? r : a.R - 1) / a.G;
+    int tile = 0, piece = 0, have = -1;
+    unsigned long long seen = 0;
+    while (pos < end) {
+        const TreePiece w = tree_next<KT>(a, sp, pos, end);
+        if (have != w.n) {
+            seen = tree_mask_of(a.parent ? a.parent + (long long)w.n * a.Ts : nullptr, a.Ts, lane, node);
+            have = w.n;
+        }
+        float m = -INFINITY, l = 0.f;
+        for (int t = w.t0; t < w.t1; ++t, ++tile) {
+            const int b = NT == 1 ? tile & 1 : wg;
+            const uint32_t phase = (uint32_t)(NT == 1 ? tile >> 1 : tile) & 1;
+            const uint32_t ts = lanes + b * Sh::kS1;
+            // Every phase of pv_done is waited for in turn: with RT = 128 the
+            // scores of this tile may be there before the last tile's product.
+            if (tile > 0) wait(sh, &sh.pv_done[NT == 1 ? 0 : wg], (uint32_t)(tile - 1) & 1, a.status);
+            wait(sh, &sh.s_full[b], phase, a.status);
+            __syncwarp();
+            tc_fence_after();
+            if (live) {
+                uint32_t keep[4];
+                if (t == w.tiles - 1) {
+                    keep[0] = (uint32_t)seen;
+                    keep[1] = (uint32_t)(seen >> 32);
+                    keep[2] = keep[3] = 0;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) keep[c] = sh.keys[tile % kRingMeta][c];
+                }
+                const bool all = (keep[0] & keep[1] & keep[2] & keep[3]) == 0xffffffffu;
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32];
+                    tmem_ld32(ts + 32 * c, x);
+                    tmem_ld_wait();
+                    if (all) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(x[j]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if ((keep[c] >> j) & 1) top = fmaxf(top, __uint_as_float(x[j]));
+                    }
+                }
+                top *= a.scale_log2;               // scale >= 0 on this path
+                if (!(top >= -INFINITY)) top = -INFINITY;   // 0 * -inf
+                const bool grow = top > m + kSlack || (m == -INFINITY && top > m);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float m2 = grow ? top : m;
+                    const float f = m2 == -INFINITY ? 1.f : ex2(m - m2);
+                    m = m2;
+                    l *= f;
+                    if (t > w.t0) {
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t x[32];
+                            tmem_ld32(to + 32 * c, x);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
+                            tmem_st32(to + 32 * c, x);
+                        }
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32], p[16];
+                    tmem_ld32(ts + 32 * c, x);
+                    tmem_ld_wait();
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float e = ex2(fmaf(__uint_as_float(x[j]), a.scale_log2, -ref));
+                        if (!all && !((keep[c] >> j) & 1)) e = 0.f;
+                        sum += e;
+                        x[j] = __float_as_uint(e);
+                    }
+                    l += sum;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        p[j] = pack_bf16x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+                    tmem_st16(ts + 16 * c, p);     // over columns already read
+                }
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[b]);
+        }
+        // the output of the piece
+        wait(sh, &sh.pv_done[NT == 1 ? 0 : wg], (uint32_t)(tile - 1) & 1, a.status);
+        __syncwarp();
+        tc_fence_after();
+        const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+        if (live) {
+            const bool mine = r < a.R;
+            unsigned long long add = 0;            // seen nodes with inf or NaN values
+            if (w.t1 == w.tiles)
+                add = seen & (((unsigned long long)sh.bad[piece % kRingMeta][1] << 32) | sh.bad[piece % kRingMeta][0]);
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int g = r - node * a.G;
+            __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.o) +
+                                (((long long)w.n * a.Ts + node) * a.Hq + w.hk * a.G + g) * D;
+            float* part = a.part + ((size_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * RT * (D + 2);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t x[32];
+                tmem_ld32(to + 32 * c, x);
+                tmem_ld_wait();
+                if (add) {
+                    for (unsigned long long rest = add; rest; rest &= rest - 1) {
+                        const int j = __ffsll((long long)rest) - 1;
+                        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) +
+                            (((long long)w.n * a.Ts + j) * a.Hkv + w.hk) * D + 32 * c;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float y = __bfloat162float(v[i]);
+                            if (!(fabsf(y) < INFINITY)) x[i] = __float_as_uint(__uint_as_float(x[i]) + y);
+                        }
+                    }
+                }
+                if (mine && whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            y[j] = pack_bf16x2(__uint_as_float(x[i + 2 * j]) * inv,
+                                               __uint_as_float(x[i + 2 * j + 1]) * inv);
+                        *reinterpret_cast<uint4*>(op + 32 * c + i) =
+                            seen == 0 ? make_uint4(0, 0, 0, 0) : make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                } else if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4*>(part + (size_t)local * D + 32 * c + i) =
+                            seen == 0 ? make_uint4(0, 0, 0, 0)
+                                      : make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                }
+                __syncwarp();                      // before the next collective load
+            }
+            if (mine && !whole) {
+                part[RT * D + local] = seen == 0 ? -INFINITY : m;
+                part[RT * D + RT + local] = seen == 0 ? 0.f : l;
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.o_empty[NT == 1 ? 0 : wg]);
+        ++piece;
+    }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
+tree_attention_tc_kernel(const __grid_constant__ TreeArgs a)
+{
+    using Sh = TcShape<D, NT>;
+    extern __shared__ uint8_t raw[];
+    __shared__ TcShared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t q_smem = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t slots = q_smem + Sh::kQBytes;
+    if (tid == 0) {
+        for (int i = 0; i < Sh::kSlots; ++i) {
+            mbar_init(&sh.kv_full[i], 4);
+            mbar_init(&sh.kv_empty[i], 1);
+        }
+        mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.pv_done[i], 1);
+            mbar_init(&sh.o_empty[i], 4);
+        }
+        sh.dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == Sh::kMmaWarp) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    const int group = blockIdx.x / a.row_tiles, r0 = (blockIdx.x % a.row_tiles) * (NT * 128);
+    const TreeSpot sp = tree_locate<Sh::kThreads, KT>(a, group, sh.loc);   // has block barriers
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
+    const long long pos = tree_begin(sp.total, group, a.groups);
+    const long long end = tree_begin(sp.total, group + 1, a.groups);
+    if (warp < Sh::kMmaWarp)
+        softmax_role<D, NT>(sh, a, sp, pos, end, r0, warp, lane, tmem);
+    else if (warp == Sh::kMmaWarp)
+        mma_role<D, NT>(sh, a, q_smem, slots, sp, pos, end, r0, tmem);
+    else
+        copy_role<D, NT>(sh, a, q_smem, slots, sp, pos, end, r0, warp - Sh::kCopyWarp, lane);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == Sh::kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, int NT>
+cudaError_t launch_tc(const TreeArgs& a, cudaStream_t stream)
+{
+    auto kern = tree_attention_tc_kernel<D, NT>;
+    const size_t bytes = TcShape<D, NT>::kBytes;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    kern<<<a.groups * a.row_tiles, TcShape<D, NT>::kThreads, bytes, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tree_attention_tc(const TreeArgs& args, const TreePlan& plan, int32_t d,
+                                     cudaStream_t stream)
+{
+    if (d == 64)
+        return plan.rt == 128 ? launch_tc<64, 1>(args, stream) : launch_tc<64, 2>(args, stream);
+    return plan.rt == 128 ? launch_tc<128, 1>(args, stream) : launch_tc<128, 2>(args, stream);
+}
+
+}  // namespace kda

@@ -44,7 +44,7 @@ size_t kda_tree_attention_workspace_bytes(int32_t N, int32_t Ts, int32_t Hq, int
     if (N < 1 || Ts < 1 || Ts > kda::kTreeMaxNodes || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 ||
         !supported_d(d) || !valid_dtype(dtype))
         return 0;
-    return kda::tree_plan(N, Ts, Hq, Hkv, d, dtype, kda::device_sm_count()).bytes;
+    return kda::tree_workspace_bytes(Ts, Hq, Hkv, d, dtype, kda::device_sm_count());
 }
 
 kda_status_t kda_tree_attention(const void* q, const void* k, const void* v, const int32_t* parent,
@@ -59,8 +59,8 @@ kda_status_t kda_tree_attention(const void* q, const void* k, const void* v, con
     if (Ts > kda::kTreeMaxNodes) return KDA_ERR_UNSUPPORTED;
     if (N < 1 || Ts < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0) return KDA_ERR_INVALID_ARG;
     if (num_pages < 0 || page_size < 1 || max_pages < 0) return KDA_ERR_INVALID_ARG;
-    // Positions and rows are 32-bit.
-    if ((int64_t)max_pages * page_size > INT32_MAX || (int64_t)Ts * Hq > INT32_MAX ||
+    // Positions are 32-bit; a row tile is a block index.
+    if ((int64_t)max_pages * page_size > INT32_MAX || (int64_t)Ts * Hq > (1 << 20) ||
         (int64_t)Hkv * d > INT32_MAX)
         return KDA_ERR_INVALID_ARG;
     if (!q || !k || !v || !lengths || !o) return KDA_ERR_INVALID_ARG;
@@ -83,8 +83,9 @@ kda_status_t kda_tree_attention(const void* q, const void* k, const void* v, con
         return KDA_ERR_INVALID_ARG;
     if (cached && (overlaps(o, o_bytes, k_cache, cache_bytes) || overlaps(o, o_bytes, v_cache, cache_bytes)))
         return KDA_ERR_INVALID_ARG;
-    const kda::TreePlan plan = kda::tree_plan(N, Ts, Hq, Hkv, d, dtype, kda::device_sm_count());
-    if (!workspace || workspace_bytes < plan.bytes || !aligned(workspace, 256)) return KDA_ERR_WORKSPACE;
+    const int sms = kda::device_sm_count();
+    if (!workspace || workspace_bytes < kda::tree_workspace_bytes(Ts, Hq, Hkv, d, dtype, sms) ||
+        !aligned(workspace, 256)) return KDA_ERR_WORKSPACE;
 
     kda::TreeArgs a = {};
     a.q = q;
@@ -109,7 +110,7 @@ kda_status_t kda_tree_attention(const void* q, const void* k, const void* v, con
     a.o = o;
     a.status = static_cast<int32_t*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kda::kWsHeaderBytes);
-    const cudaError_t err = kda::launch_tree_attention(a, plan, d, dtype, stream);
+    const cudaError_t err = kda::launch_tree_attention(a, d, dtype, sms, stream);
     return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

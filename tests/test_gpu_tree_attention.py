@@ -125,6 +125,21 @@ def test_page_stride_and_pages_that_do_not_exist(kda, dtype):
     check(run(kda, inp), *attention_reference(inp), exact_p=dtype == F32)
 
 
+@pytest.mark.parametrize("dtype,scale", [(BF16, -0.11), (BF16, 0.0), (F32, -0.11)])
+def test_other_scales(kda, dtype, scale):
+    inp = AttentionInputs(2, 5, 4, 2, 64, 16, [200, 31], dtype, seed=16)
+    inp.scale = scale
+    check(run(kda, inp), *attention_reference(inp), exact_p=dtype == F32)
+
+
+@pytest.mark.parametrize("Ts,G", [(1, 128), (43, 3), (64, 3), (64, 4), (50, 7), (64, 9)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_row_tiles_of_the_tensor_core_kernel(kda, Ts, G, d):
+    # 128, 129, 192, 256, 350 and 576 query rows per cache head
+    inp = AttentionInputs(2, Ts, 2 * G, 2, d, 32, [391, 12], BF16, seed=Ts + G)
+    check(run(kda, inp), *attention_reference(inp), exact_p=False)
+
+
 def test_lengths_are_clamped(kda):
     inp = AttentionInputs(2, 2, 2, 1, 64, 16, [48, 0], BF16, seed=10)
     args = inp.on("cuda")
@@ -149,6 +164,19 @@ def test_many_sequences(kda, dtype):
     lengths[[5, 300, 699]] = [3000, 2000, 1000]
     inp = AttentionInputs(700, 2, 2, 1, 64, 16, lengths, dtype, seed=12)
     check(run(kda, inp), *attention_reference(inp), exact_p=dtype == F32)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Ts,G", [(3, 2), (33, 4), (33, 9)])
+def test_many_tiles_in_a_range(kda, Ts, G, d):
+    # more tiles than CTAs: ranges of several tiles, items and sequences, also
+    # where every item is finished in its own CTA
+    rng = np.random.default_rng(17)
+    for N, lengths in ((2, [22000, 9000]), (160, rng.integers(0, 300, 160))):
+        inp = AttentionInputs(N, Ts, 2 * G, 2, d, 64, lengths, BF16, seed=N + G)
+        # the reference of a few nodes is enough
+        inp.parent[:, 4:] = np.where(np.arange(4, Ts) % 8 == 0, inp.parent[:, 4:], -2)
+        check(run(kda, inp), *attention_reference(inp), exact_p=False)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
