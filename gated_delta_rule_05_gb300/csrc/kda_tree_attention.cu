@@ -368,12 +368,12 @@ size_t tree_workspace_bytes(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, kda_
     return kWsHeaderBytes + most;
 }
 
-// A negative (or NaN) scale takes the CUDA-core kernel: the tensor-core one
+// A scale that is not positive takes the CUDA-core kernel: the tensor-core one
 // finds a row's maximum before it applies the scale.
 cudaError_t launch_tree_attention(TreeArgs args, int32_t d, kda_dtype_t dtype, int sms,
                                   cudaStream_t stream)
 {
-    const bool tc = tree_tc_supported(d, dtype) && args.scale_log2 >= 0.f && getenv("KDA_FORCE_SIMT") == nullptr;
+    const bool tc = tree_tc_supported(d, dtype) && args.scale_log2 > 0.f && getenv("KDA_FORCE_SIMT") == nullptr;
     const TreePlan plan = tree_plan(args.Ts, args.Hq, args.Hkv, sms, tc);
     args.groups = plan.groups;
     args.row_tiles = plan.row_tiles;

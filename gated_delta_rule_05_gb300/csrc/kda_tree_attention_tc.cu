@@ -44,9 +44,15 @@ struct TcShape {
     static constexpr int kQBytes = NT * 128 * D * 2;
     static constexpr int kSlotBytes = KT * D * 2;
     static constexpr int kSlots = (D == 128) ? (NT == 1 ? 6 : 5) : 12;
-    static constexpr int kThreads = NT * 128 + 32 + 128;
-    static constexpr int kMmaWarp = NT * 4;
-    static constexpr int kCopyWarp = NT * 4 + 1;
+    // Warps: softmax, copies, one that issues products, filled up to whole
+    // warpgroups so that registers can be moved from the latter two to the
+    // softmax: 384 x 168 >= 128 x 232 + 256 x 128, 512 x 128 = 256 x 192 + 256 x 64.
+    // block is filled to whole warpgroups, so that registers can be moved from
+    // the copies and the products to the softmax (512 x 128 = 256 x 192 + 256 x 64)
+    static constexpr int kThreads = NT == 1 ? 384 : 512;
+    static constexpr int kCopyWarp = NT * 4;
+    static constexpr int kMmaWarp = NT * 4 + 4;
+    static constexpr int kMore = NT == 1 ? 232 : 192, kFewer = NT == 1 ? 128 : 64;
     static constexpr size_t kBytes = 1024 + kQBytes + (size_t)kSlots * kSlotBytes;
     // TMEM columns
     static constexpr int kS1 = 128, kO0 = 256, kO1 = 256 + D;
@@ -61,6 +67,20 @@ struct TcShared {
     uint32_t bad[kRingMeta][2];            // drafted nodes of a piece whose v is not finite
     long long loc[16 + 2];
 };
+
+// Whether the phase has completed, without the suspension of a try_wait.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 
 // Waits unless some wait of this CTA has already given up.
 __device__ __forceinline__ void wait(TcShared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
@@ -104,6 +124,45 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Pairs of fp32 for the two-wide FMA and add.
+__device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    return pack2u(__float_as_uint(a), __float_as_uint(b));
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Which of eight bf16 (four words) are inf or NaN are set to 0; returns whether any was.
@@ -203,7 +262,7 @@ struct Copier {
     __device__ void wait_for(uint64_t* bar, uint32_t parity)
     {
         while (landed < next) {
-            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
+            if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return;
             hand_over();
         }
         wait(sh, bar, parity, a.status);
@@ -252,16 +311,30 @@ struct Copier {
         }
     }
 
-    // Element offset of this lane's row of tile t (-1: none), the same for K and V.
-    __device__ long long row_of(const TreePiece& w, int t) const
+    // What this lane has to know of its row of tile t: the page's number, loaded
+    // a tile ahead of its use, and the slot in it; drafted rows need no page.
+    struct Row {
+        int page, slot;                            // page -1: no row
+    };
+    __device__ Row look_up(const TreePiece& w, int t) const
     {
-        const int j = warp * 32 + lane, row_elems = a.Hkv * D;
-        if (t == w.tiles - 1)
-            return j < a.Ts ? ((long long)w.n * a.Ts + j) * row_elems + (long long)w.hk * D : -1;
+        const int j = warp * 32 + lane;
+        if (t >= w.t1) return {-1, 0};
+        if (t == w.tiles - 1) return {j < a.Ts ? 0 : -1, j};
         const int pos = t * KT + j;
-        if (pos >= w.ctx) return -1;
-        const long long off = tree_cache_row(a, a.page_table + (long long)w.n * a.max_pages, pos, row_elems);
-        return off < 0 ? -1 : off + (long long)w.hk * D;
+        if (pos >= w.ctx) return {-1, 0};
+        const int p = pos / a.page_size;
+        return {__ldg(a.page_table + (long long)w.n * a.max_pages + p), pos - p * a.page_size};
+    }
+
+    // Element offset of the row in K and V (-1: none).
+    __device__ long long row_of(const TreePiece& w, int t, const Row& r) const
+    {
+        const int row_elems = a.Hkv * D;
+        if (t == w.tiles - 1)
+            return r.page < 0 ? -1 : ((long long)w.n * a.Ts + r.slot) * row_elems + (long long)w.hk * D;
+        if (r.page < 0 || r.page >= a.num_pages) return -1;
+        return (long long)r.page * a.page_stride + (long long)r.slot * row_elems + (long long)w.hk * D;
     }
 
     __device__ void load_k(const TreePiece& w, int t, long long off, int g)
@@ -308,14 +381,17 @@ __device__ void copy_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint
     int g = 0, piece = 0;                          // tiles and pieces so far
     while (pos < end) {
         const TreePiece w = tree_next<KT>(a, sp, pos, end);
-        long long off = c.row_of(w, w.t0), ahead = -1;
+        auto row = c.look_up(w, w.t0);
+        auto row1 = c.look_up(w, w.t0 + 1);
+        long long off = c.row_of(w, w.t0, row), ahead = -1;
         c.wait_slot();
         if (piece > 0) c.wait_for(&sh.q_empty, (uint32_t)(piece - 1) & 1);
         c.load_q(w, r0);
         c.load_k(w, w.t0, off, g);
         for (int t = w.t0; t < w.t1; ++t, ++g) {
             const bool more = t + 1 < w.t1;
-            if (more) ahead = c.row_of(w, t + 1);
+            if (more) ahead = c.row_of(w, t + 1, row1);
+            row1 = c.look_up(w, t + 2);
             if (NT == 1 && more) {
                 c.wait_slot();
                 c.load_k(w, t + 1, ahead, g + 1);
@@ -464,13 +540,24 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, TreeSpot sp, long 
             const int b = NT == 1 ? tile & 1 : wg;
             const uint32_t phase = (uint32_t)(NT == 1 ? tile >> 1 : tile) & 1;
             const uint32_t ts = lanes + b * Sh::kS1;
-            // Every phase of pv_done is waited for in turn: with RT = 128 the
-            // scores of this tile may be there before the last tile's product.
-            if (tile > 0) wait(sh, &sh.pv_done[NT == 1 ? 0 : wg], (uint32_t)(tile - 1) & 1, a.status);
+            // Every phase of pv_done is waited for in turn (wait_last): with RT =
+            // 128 the scores of this tile may be there before the last tile's
+            // product, and a parity names only the phase before the current one.
             wait(sh, &sh.s_full[b], phase, a.status);
             __syncwarp();
             tc_fence_after();
+            bool waited = tile == 0;
+            auto wait_last = [&]() {
+                if (waited) return;
+                waited = true;
+                wait(sh, &sh.pv_done[NT == 1 ? 0 : wg], (uint32_t)(tile - 1) & 1, a.status);
+                __syncwarp();
+                tc_fence_after();
+            };
             if (live) {
+                uint32_t x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, x[c]);
                 uint32_t keep[4];
                 if (t == w.tiles - 1) {
                     keep[0] = (uint32_t)seen;
@@ -481,23 +568,25 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, TreeSpot sp, long 
                     for (int c = 0; c < 4; ++c) keep[c] = sh.keys[tile % kRingMeta][c];
                 }
                 const bool all = (keep[0] & keep[1] & keep[2] & keep[3]) == 0xffffffffu;
-                float top = -INFINITY;
+                tmem_ld_wait();
+                if (!all) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32];
-                    tmem_ld32(ts + 32 * c, x);
-                    tmem_ld_wait();
-                    if (all) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(x[j]));
-                    } else {
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if ((keep[c] >> j) & 1) top = fmaxf(top, __uint_as_float(x[j]));
-                    }
+                            if (!((keep[c] >> j) & 1)) x[c][j] = 0xff800000u;      // -inf
                 }
-                top *= a.scale_log2;               // scale >= 0 on this path
-                if (!(top >= -INFINITY)) top = -INFINITY;   // 0 * -inf
+                float tops[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tops[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+                    for (int j = 1; j < 31; j += 2)
+                        tops[c] = fmaxf(tops[c], fmaxf(__uint_as_float(x[c][j]), __uint_as_float(x[c][j + 1])));
+                    tops[c] = fmaxf(tops[c], __uint_as_float(x[c][31]));
+                }
+                float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                top *= a.scale_log2;               // the scale is positive on this path
                 const bool grow = top > m + kSlack || (m == -INFINITY && top > m);
                 if (__any_sync(0xffffffffu, grow)) {
                     const float m2 = grow ? top : m;
@@ -505,39 +594,43 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, TreeSpot sp, long 
                     m = m2;
                     l *= f;
                     if (t > w.t0) {
+                        wait_last();
 #pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t x[32];
-                            tmem_ld32(to + 32 * c, x);
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t y[16];
+                            tmem_ld16(to + 16 * c, y);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
-                            tmem_st32(to + 32 * c, x);
+                            for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                            tmem_st16(to + 16 * c, y);
                         }
                     }
                 }
-                const float ref = m == -INFINITY ? 0.f : m;
+                // masked scores stay -inf (their e is 0) unless nothing was seen so far
+                const uint64_t ref2 = pack2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
+                const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
+                uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32], p[16];
-                    tmem_ld32(ts + 32 * c, x);
-                    tmem_ld_wait();
-                    float sum = 0.f;
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        float e = ex2(fmaf(__uint_as_float(x[j]), a.scale_log2, -ref));
-                        if (!all && !((keep[c] >> j) & 1)) e = 0.f;
-                        sum += e;
-                        x[j] = __float_as_uint(e);
+                        const int c = 2 * h + (j >> 4), k = 2 * (j & 15);
+                        float e0, e1;
+                        unpack2(fma2(pack2u(x[c][k], x[c][k + 1]), scale2, ref2), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        sum[j & 3] = add2(sum[j & 3], pack2(e0, e1));
+                        p[j] = pack_bf16x2(e0, e1);
                     }
-                    l += sum;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        p[j] = pack_bf16x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
-                    tmem_st16(ts + 16 * c, p);     // over columns already read
+                    tmem_st32(ts + 32 * h, p);     // over scores, all of them in registers
                 }
+                float s0, s1;
+                unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+                l += s0 + s1;
                 tmem_st_wait();
             }
+            wait_last();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_full[b]);
@@ -644,12 +737,16 @@ tree_attention_tc_kernel(const __grid_constant__ TreeArgs a)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
     const long long pos = tree_begin(sp.total, group, a.groups);
     const long long end = tree_begin(sp.total, group + 1, a.groups);
-    if (warp < Sh::kMmaWarp)
+    if (warp < Sh::kCopyWarp) {
+        more_registers<Sh::kMore>();
         softmax_role<D, NT>(sh, a, sp, pos, end, r0, warp, lane, tmem);
-    else if (warp == Sh::kMmaWarp)
-        mma_role<D, NT>(sh, a, q_smem, slots, sp, pos, end, r0, tmem);
-    else
+    } else if (warp < Sh::kMmaWarp) {
+        fewer_registers<Sh::kFewer>();
         copy_role<D, NT>(sh, a, q_smem, slots, sp, pos, end, r0, warp - Sh::kCopyWarp, lane);
+    } else {
+        fewer_registers<Sh::kFewer>();
+        if (warp == Sh::kMmaWarp) mma_role<D, NT>(sh, a, q_smem, slots, sp, pos, end, r0, tmem);
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == Sh::kMmaWarp) {
