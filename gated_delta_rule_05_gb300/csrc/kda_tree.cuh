@@ -32,6 +32,8 @@ struct TreeArgs {
     void* o;
     int32_t* status;                  // workspace words (kWsTimeoutWord is used)
     float* part;                      // 2 slots per CTA: [RT][d] o, [RT] m, [RT] l
+    int32_t box, tile_pages, tile_rows;   // tensor-core kernel: rows per TMA box (0: none), and
+                                      // a tile's keys as whole pages and rows
     int32_t groups, row_tiles;        // CTA b: group b / row_tiles, row tile b % row_tiles
 };
 
@@ -98,6 +100,7 @@ __device__ __forceinline__ void tree_masks(const int32_t* parent, int Ts, int la
 // Where a group's range begins in the flattened tile order.
 struct TreeSpot {
     long long total;        // tiles of the whole launch
+    long long per, more;    // each group has `per` tiles, the first `more` one more
     long long start;        // first tile of sequence n
     int n;
 };
@@ -109,42 +112,44 @@ __device__ __forceinline__ long long tree_seq_tiles(const TreeArgs& a, int n)
 }
 
 // First tile of group c's range.
-__device__ __forceinline__ long long tree_begin(long long total, int c, int groups)
+__device__ __forceinline__ long long tree_begin(const TreeSpot& sp, int c)
 {
-    return total * c / groups;
+    return sp.per * c + (c < sp.more ? c : sp.more);
 }
 
-// The sequence that holds the first tile of group c's range (c < groups).  All THREADS threads of the block call it; `sh` is shared scratch of
-// THREADS / 32 + 2 words.
+// The sequence that holds the first tile of group c's range (c < groups).  All
+// THREADS threads of the block call it; `sh` is shared scratch of THREADS / 32 +
+// 2 words.  With up to THREADS sequences the lengths are read once.
 template <int THREADS, int KT>
 __device__ TreeSpot tree_locate(const TreeArgs& a, int c, long long* sh)
 {
     constexpr int W = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long items = a.Hkv;
-    long long sum = 0;
-    for (int n = tid; n < a.N; n += THREADS) sum += tree_seq_tiles<KT>(a, n) * items;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    __syncthreads();
-    if (lane == 0) sh[warp] = sum;
-    __syncthreads();
     TreeSpot r;
-    r.total = 0;
+    long long mine = 0;                             // the first THREADS sequences' tiles
+    if (tid < a.N) mine = tree_seq_tiles<KT>(a, tid) * a.Hkv;
+    long long rest = 0;
+    for (int n = tid + THREADS; n < a.N; n += THREADS) rest += tree_seq_tiles<KT>(a, n) * a.Hkv;
+    if (a.N > THREADS) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) r.total += sh[i];
-    const long long at = tree_begin(r.total, c, a.groups);
-    long long base = 0;
+        for (int off = 16; off > 0; off >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, off);
+        if (lane == 0) sh[warp] = rest;
+        __syncthreads();
+        rest = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) rest += sh[i];
+        __syncthreads();
+    }
+    long long base = 0, at = 0;
     for (int n0 = 0; n0 < a.N; n0 += THREADS) {
         const int n = n0 + tid;
-        const long long w = n < a.N ? tree_seq_tiles<KT>(a, n) * items : 0;
+        const long long w = n0 == 0 ? mine : (n < a.N ? tree_seq_tiles<KT>(a, n) * a.Hkv : 0);
         long long incl = w;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const long long x = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += x;
         }
-        __syncthreads();
         if (lane == 31) sh[warp] = incl;
         __syncthreads();
         long long before = base, chunk = 0;
@@ -153,14 +158,20 @@ __device__ TreeSpot tree_locate(const TreeArgs& a, int c, long long* sh)
             if (i < warp) before += sh[i];
             chunk += sh[i];
         }
+        if (n0 == 0) {
+            r.total = chunk + rest;
+            r.per = r.total / a.groups;
+            r.more = r.total - r.per * a.groups;
+            at = tree_begin(r, c);
+        }
         if (at >= before + incl - w && at < before + incl) {
             sh[W] = n;
             sh[W + 1] = before + incl - w;
         }
         base += chunk;
+        __syncthreads();
         if (at < base) break;                       // uniform: the block has found it
     }
-    __syncthreads();
     r.n = (int)sh[W];
     r.start = sh[W + 1];
     return r;
@@ -204,7 +215,7 @@ size_t tree_workspace_bytes(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, kda_
 
 cudaError_t launch_tree_attention(TreeArgs args, int32_t d, kda_dtype_t dtype, int sms,
                                   cudaStream_t stream);
-cudaError_t launch_tree_attention_tc(const TreeArgs& args, const TreePlan& plan, int32_t d,
+cudaError_t launch_tree_attention_tc(TreeArgs args, const TreePlan& plan, int32_t d,
                                      cudaStream_t stream);
 
 }  // namespace kda

@@ -63,8 +63,9 @@ tree_attention_simt_kernel(const TreeArgs a)
     const int group = blockIdx.x / a.row_tiles, r0 = (blockIdx.x % a.row_tiles) * RT;
     const int rows = a.R - r0 < RT ? a.R - r0 : RT;
     TreeSpot sp = tree_locate<kSimtThreads, kSimtKeys>(a, group, sh_loc);
-    long long pos = tree_begin(sp.total, group, a.groups);
-    const long long end = tree_begin(sp.total, group + 1, a.groups);
+    long long pos = tree_begin(sp, group);
+    const long long end = tree_begin(sp, group + 1);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int row_elems = a.Hkv * D;
     int have = -1;                                  // the sequence anc[] is of
 
@@ -241,8 +242,10 @@ tree_attention_simt_kernel(const TreeArgs a)
 // Joins the pieces of the items that were cut between groups.  Block (c, y, z):
 // the item that the boundary before group c + 1 falls into, if that is the
 // item's first boundary; rows y 8 .. y 8 + 7 of row tile z.  The pieces are read
-// in the order of the groups, so the result does not depend on timing.
-constexpr int kJoinThreads = 128;
+// in the order of the groups, so the result does not depend on timing.  The
+// launch may start before the attention kernel has ended (its blocks fill the
+// SMs that have finished) and waits for it before the first partial result.
+constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 8;
 
 template <typename TO, int D, int KT>
@@ -250,48 +253,50 @@ __global__ void __launch_bounds__(kJoinThreads)
 tree_join_kernel(const TreeArgs a, int RT)
 {
     __shared__ long long sh_loc[kJoinThreads / 32 + 2];
-    const int c = blockIdx.x + 1, tid = threadIdx.x;
+    const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const TreeSpot sp = tree_locate<kJoinThreads, KT>(a, c, sh_loc);
-    const long long at = tree_begin(sp.total, c, a.groups);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long at = tree_begin(sp, c);
+    if (at >= sp.total) return;                     // an empty range at the end
     const int tiles = (int)tree_seq_tiles<KT>(a, sp.n);
     const int hk = (int)((at - sp.start) / tiles);
     const long long first = sp.start + (long long)hk * tiles;
-    if (at == first || tree_begin(sp.total, c - 1, a.groups) > first) return;
+    if (at == first || tree_begin(sp, c - 1) > first) return;
     int last = c;                                   // the last group with tiles of this item
-    while (last + 1 < a.groups && tree_begin(sp.total, last + 1, a.groups) < first + tiles) ++last;
+    while (last + 1 < a.groups && tree_begin(sp, last + 1) < first + tiles) ++last;
     const int r0 = blockIdx.z * RT;
     const int rows = a.R - r0 < RT ? a.R - r0 : RT;
+    const int r = blockIdx.y * kJoinRows + warp;    // a warp per row
+    if (r >= rows) return;
     const size_t slot = (size_t)RT * (D + 2);
-    constexpr int LPR = D / 4;                      // lanes per row
-    for (int r = blockIdx.y * kJoinRows + tid / LPR; r < rows && r < (blockIdx.y + 1) * kJoinRows;
-         r += kJoinThreads / LPR) {
-        const int c4 = (tid % LPR) * 4;
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = c - 1; p <= last; ++p) {
-            if (tree_begin(sp.total, p, a.groups) == tree_begin(sp.total, p + 1, a.groups)) continue;
-            const float* part =
-                a.part + (((size_t)p * a.row_tiles + blockIdx.z) * 2 + (p == c - 1 ? 1 : 0)) * slot;
-            const float pm = part[RT * D + r], pl = part[RT * D + RT + r];
-            const float4 x = *reinterpret_cast<const float4*>(part + (size_t)r * D + c4);
-            const float top = fmaxf(m, pm);
-            const float ref = top == -INFINITY ? 0.f : top;
-            const float f = exp2f(m - ref), w = exp2f(pm - ref);
-            l = l * f + pl * w;
-            o.x = o.x * f + x.x * w;
-            o.y = o.y * f + x.y * w;
-            o.z = o.z * f + x.z * w;
-            o.w = o.w * f + x.w * w;
-            m = top;
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;   // l = 0: an unused node; a NaN stays
-        const int t = (r0 + r) / a.G, g = (r0 + r) % a.G;
-        TO* op = static_cast<TO*>(a.o) + (((long long)sp.n * a.Ts + t) * a.Hq + hk * a.G + g) * D + c4;
-        st_f(op, o.x * inv);
-        st_f(op + 1, o.y * inv);
-        st_f(op + 2, o.z * inv);
-        st_f(op + 3, o.w * inv);
+    // piece p of the item: group p's first slot, but the second of group c - 1
+    auto piece = [&](int p) {
+        return a.part + (((size_t)p * a.row_tiles + blockIdx.z) * 2 + (p == c - 1 ? 1 : 0)) * slot;
+    };
+    constexpr int E = D / 32 > 0 ? D / 32 : 1;      // elements per lane
+    float m = -INFINITY;
+    for (int p = c - 1 + lane; p <= last; p += 32) m = fmaxf(m, piece(p)[RT * D + r]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int p = c - 1; p <= last; ++p) {
+        const float* x = piece(p);
+        const float w = exp2f(x[RT * D + r] - ref);
+        l = fmaf(x[RT * D + RT + r], w, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (D >= 32 || lane < D) o[e] = fmaf(x[(size_t)r * D + lane + 32 * e], w, o[e]);
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;     // l = 0: an unused node; a NaN stays
+    const int t = (r0 + r) / a.G, g = (r0 + r) % a.G;
+    TO* op = static_cast<TO*>(a.o) + (((long long)sp.n * a.Ts + t) * a.Hq + hk * a.G + g) * D;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (D >= 32 || lane < D) st_f(op + lane + 32 * e, o[e] * inv);
 }
 
 template <typename TO, int D, int KT>
@@ -299,9 +304,16 @@ cudaError_t launch_join(const TreeArgs& a, int rt, cudaStream_t stream)
 {
     if (a.groups < 2) return cudaSuccess;
     const int rows = a.R < rt ? a.R : rt;
-    const dim3 grid(a.groups - 1, (rows + kJoinRows - 1) / kJoinRows, a.row_tiles);
-    tree_join_kernel<TO, D, KT><<<grid, kJoinThreads, 0, stream>>>(a, rt);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.groups - 1, (rows + kJoinRows - 1) / kJoinRows, a.row_tiles);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<TO, D, KT>, a, rt);
 }
 
 template <typename TI, typename TO, int D, int RT>

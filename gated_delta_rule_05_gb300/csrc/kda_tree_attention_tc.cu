@@ -18,26 +18,34 @@
 // computed during this tile's softmax; with more (RT = 256) two row tiles share
 // every K and V tile and alternate on the tensor core.
 //
-// Copies: 16-byte cp.async by 16 lanes per row (d = 128), which take any page
-// size and page stride, and fill rows past the length and rows of pages that do
-// not exist with zeros, so that nothing stored there can reach a product.  They
-// run ahead through a ring of tiles.  A row of drafted values is copied through
-// registers instead, and an infinity or NaN in it is replaced by 0: the
-// product's 0 * inf would reach rows that do not see the node.  The rows that
-// do see it add it to their output at the end.
+// Copies run ahead through a ring of K and V tiles: TMA boxes where 32 rows in
+// a row are there and the page size allows, 16-byte cp.async elsewhere, which
+// takes any page size and fills rows past the length and rows of pages that do
+// not exist with zeros, so that nothing stored there can reach a product.  A row
+// of drafted values is copied through registers, and an infinity or NaN in it
+// is replaced by 0: the product's 0 * inf would reach rows that do not see the
+// node.  The rows that do see it add it to their output at the end.
 //
 // Every wait has a limit (mbar_wait); a wait that gives up sets the workspace's
 // timeout word, and the CTA runs to its end without waiting again.
+#include <cudaTypedefs.h>
+#include <stdio.h>
+
 #include "kda_sm100.cuh"
 #include "kda_tree.cuh"
 
 namespace kda {
+
+// The driver's tensor-map encoder (kda_prefill_tc.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn();
+
 namespace {
 
 using namespace sm100;
 
 constexpr int KT = 128;                    // keys per tile
 constexpr int kRingMeta = 16;              // tiles whose key masks are kept
+constexpr int kQWarps = 2;                 // warps that copy q
 
 template <int D, int NT>
 struct TcShape {
@@ -59,7 +67,7 @@ struct TcShape {
 };
 
 struct TcShared {
-    uint64_t kv_full[12], kv_empty[12], q_empty, done;
+    uint64_t kv_full[12], kv_empty[12], q_full, q_empty, done;
     uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2];
     uint32_t tmem;
     int dead;
@@ -93,10 +101,26 @@ __device__ __forceinline__ void wait(TcShared& sh, uint64_t* bar, uint32_t parit
     }
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
+// 16 bytes to shared memory, asynchronously; zeros when src is null.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, const void* any)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.eq.u64 p, %1, 0;\n\t"
+        "cp.async.cg.shared.global [%0], [%2], 16, p;\n\t}" ::"r"(dst),
+        "l"(src), "l"(src ? src : any)
+        : "memory");
+}
+
+// One box of a page pool [num_pages][page_size][Hkv][d]: rows of one page, 64
+// columns of one head.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t h,
+                                            int32_t row, int32_t page, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(row), "r"(page), "r"(smem_u32(bar))
+        : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
@@ -224,9 +248,40 @@ __device__ __forceinline__ unsigned long long tree_mask_of(const int32_t* parent
 }
 
 // ---------------------------------------------------------------- the copies
-// Four warps.  A ring entry is one K or V tile; the entries of a piece are K_0,
-// then (RT = 128) K_1 V_0 K_2 V_1 ... V_last or (RT = 256) V_0 K_1 V_1 ..., the
-// order in which the products take them.  Q goes with the piece's first entry.
+// Byte offset of 16-byte chunk c of row r in a tile of 128 rows: 128-byte rows
+// with the 128-byte swizzle, one block of rows per 64 columns.
+__device__ __forceinline__ uint32_t tile_at(int r, int c)
+{
+    return (uint32_t)(c >> 3) * (128 * 128) + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+}
+
+// Copies 32 rows of D bf16 to rows row0 .. row0 + 31 of a tile; lane's argument
+// p is the source of row row0 + lane (null: zeros).  A warp, whole rows at a time.
+template <int D>
+__device__ __forceinline__ void copy_rows32(uint32_t dst, int row0, const __nv_bfloat16* p,
+                                            const void* any, int lane)
+{
+    constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes per row, rows per instruction
+    const int c = lane % LPR;
+    const unsigned long long mine = reinterpret_cast<unsigned long long>(p);
+#pragma unroll 4
+    for (int i = 0; i < 32 / RPI; ++i) {
+        const int j = i * RPI + lane / LPR;
+        const unsigned long long src = __shfl_sync(0xffffffffu, mine, j);
+        cp_async16(dst + tile_at(row0 + j, c), src ? reinterpret_cast<const void*>(src + 16ull * c) : nullptr, any);
+    }
+}
+
+// Four warps, 32 rows of every tile each.  A ring entry is one K or V tile; the
+// entries of a piece are K_0, then (RT = 128) K_1 V_0 K_2 V_1 ... V_last or (RT =
+// 256) V_0 K_1 V_1 ..., the order in which the products take them.  Two other
+// warps copy each piece's q when the products of the piece before have read
+// theirs, so that the ring does not drain between pieces.
+//
+// Where all 32 rows are context rows of pages that exist, and the page size
+// allows (a.box), the rows come as TMA boxes that complete on the entry's
+// barrier.  Elsewhere (the end of a context, drafted rows, other page sizes) the
+// lanes copy them, and hand the entry over when it has landed.
 template <int D, int NT>
 struct Copier {
     using Sh = TcShape<D, NT>;
@@ -234,21 +289,22 @@ struct Copier {
     static constexpr int RPI = 32 / LPR;           // rows per instruction
     TcShared& sh;
     const TreeArgs& a;
-    uint32_t q_smem, slots;
+    const CUtensorMap *map_k, *map_v;
+    uint32_t slots;
     int lane, warp;                                // warp 0 .. 3
     int next = 0, landed = 0;                      // entries issued, entries handed over
+    uint32_t boxes = 0;                            // bit e % 32: entry e came as boxes
 
     __device__ uint32_t entry(int i) const { return slots + (uint32_t)(i % Sh::kSlots) * Sh::kSlotBytes; }
 
-    // Byte offset of chunk c of row r in a tile of `rows` rows: 128-byte rows
-    // with the 128-byte swizzle, one block of rows per 64 columns.
-    static __device__ uint32_t at(int r, int c, int rows)
+    // Entry `landed` is the oldest that the lanes copied and have not handed over
+    // yet; it holds the products up, so that next - landed <= kSlots.
+    __device__ void skip_boxes()
     {
-        return (uint32_t)(c >> 3) * (uint32_t)(rows * 128) + (uint32_t)r * 128 +
-               (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+        while (landed < next && ((boxes >> (landed & 31)) & 1)) ++landed;
     }
 
-    // Hands the oldest entry in flight over to the products.
+    // Hands it over to the products.
     __device__ void hand_over()
     {
         cp_async_wait(next - landed - 1);
@@ -256,11 +312,16 @@ struct Copier {
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.kv_full[landed % Sh::kSlots]);
         ++landed;
+        skip_boxes();
     }
 
-    // A wait during which landed entries are handed over.
-    __device__ void wait_for(uint64_t* bar, uint32_t parity)
+    // Waits until the next entry's slot is free, handing over what has landed.
+    __device__ void wait_slot()
     {
+        const int use = next / Sh::kSlots;
+        if (use == 0) return;
+        uint64_t* bar = &sh.kv_empty[next % Sh::kSlots];
+        const uint32_t parity = (uint32_t)(use - 1) & 1;
         while (landed < next) {
             if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return;
             hand_over();
@@ -269,92 +330,109 @@ struct Copier {
         __syncwarp();
     }
 
-    __device__ void wait_slot()
+    __device__ void finish_entry(bool box)
     {
-        const int use = next / Sh::kSlots;
-        if (use > 0) wait_for(&sh.kv_empty[next % Sh::kSlots], (uint32_t)(use - 1) & 1);
-    }
-
-    // 32 rows of this warp, row `lane`'s source at p (null: zeros) for lane's own row.
-    __device__ void rows32(uint32_t dst, int row0, int rows, const __nv_bfloat16* p)
-    {
-        const int c = lane % LPR;
-        const unsigned long long mine = reinterpret_cast<unsigned long long>(p);
-        const void* any = a.q;
-#pragma unroll 4
-        for (int i = 0; i < 32 / RPI; ++i) {
-            const int j = i * RPI + lane / LPR;
-            const unsigned long long src = __shfl_sync(0xffffffffu, mine, j);
-            const void* from = src ? reinterpret_cast<const void*>(src + 16ull * c) : any;
-            cp_async16(dst + at(row0 + j, c, rows), from, src ? 16u : 0u);
-        }
-    }
-
-    __device__ void finish_entry()
-    {
-        cp_async_commit();
+        cp_async_commit();                         // a group per entry, empty for boxes
+        boxes = (boxes & ~(1u << (next & 31))) | ((uint32_t)box << (next & 31));
         ++next;
+        skip_boxes();
     }
 
-    __device__ void load_q(const TreePiece& w, int r0)
-    {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int r = r0 + i * 128 + warp * 32 + lane;
-            const __nv_bfloat16* p = nullptr;
-            if (r < a.R) {
-                const int t = r / a.G, g = r - t * a.G;
-                p = static_cast<const __nv_bfloat16*>(a.q) +
-                    (((long long)w.n * a.Ts + t) * a.Hq + w.hk * a.G + g) * D;
-            }
-            rows32(q_smem + i * 128 * D * 2, warp * 32, 128, p);
-        }
-    }
-
-    // What this lane has to know of its row of tile t: the page's number, loaded
-    // a tile ahead of its use, and the slot in it; drafted rows need no page.
+    // This lane's row of a tile: its page (-1: no such row) and its place there;
+    // of drafted rows the place alone.
     struct Row {
-        int page, slot;                            // page -1: no row
+        int page, slot;
     };
-    __device__ Row look_up(const TreePiece& w, int t) const
+    // Walks this lane's rows tile by tile; the page number is loaded when the
+    // row is looked up, a tile before it is used.
+    struct Walk {
+        int pos, p, slot;
+    };
+    __device__ Walk walk_from(const TreePiece& w, int t) const
     {
-        const int j = warp * 32 + lane;
-        if (t >= w.t1) return {-1, 0};
-        if (t == w.tiles - 1) return {j < a.Ts ? 0 : -1, j};
-        const int pos = t * KT + j;
-        if (pos >= w.ctx) return {-1, 0};
+        const int pos = t * KT + warp * 32 + lane;
         const int p = pos / a.page_size;
-        return {__ldg(a.page_table + (long long)w.n * a.max_pages + p), pos - p * a.page_size};
+        return {pos, p, pos - p * a.page_size};
+    }
+    __device__ Row look_up(const TreePiece& w, int t, Walk& k) const
+    {
+        Row r = {-1, k.slot};
+        if (t >= w.t1) return r;
+        if (t == w.tiles - 1) {
+            const int j = warp * 32 + lane;
+            return {j < a.Ts ? 0 : -1, j};
+        }
+        if (k.pos < w.ctx) r.page = __ldg(a.page_table + (long long)w.n * a.max_pages + k.p);
+        k.pos += KT;
+        k.p += a.tile_pages;
+        k.slot += a.tile_rows;
+        if (k.slot >= a.page_size) {
+            k.slot -= a.page_size;
+            ++k.p;
+        }
+        return r;
+    }
+
+    __device__ bool exists(const Row& r, bool draft) const
+    {
+        return r.page >= 0 && (draft || r.page < a.num_pages);
     }
 
     // Element offset of the row in K and V (-1: none).
-    __device__ long long row_of(const TreePiece& w, int t, const Row& r) const
+    __device__ long long offset(const TreePiece& w, const Row& r, bool draft) const
     {
         const int row_elems = a.Hkv * D;
-        if (t == w.tiles - 1)
-            return r.page < 0 ? -1 : ((long long)w.n * a.Ts + r.slot) * row_elems + (long long)w.hk * D;
-        if (r.page < 0 || r.page >= a.num_pages) return -1;
-        return (long long)r.page * a.page_stride + (long long)r.slot * row_elems + (long long)w.hk * D;
+        if (!exists(r, draft)) return -1;
+        return (draft ? (long long)w.n * a.Ts * row_elems : (long long)r.page * a.page_stride) +
+               (long long)r.slot * row_elems + (long long)w.hk * D;
     }
 
-    __device__ void load_k(const TreePiece& w, int t, long long off, int g)
+    // The warp's 32 rows as boxes of a.box rows and 64 columns, a lane each.
+    __device__ void load_boxes(const CUtensorMap* map, const TreePiece& w, const Row& r)
+    {
+        uint64_t* bar = &sh.kv_full[next % Sh::kSlots];
+        if (lane == 0) mbar_arrive_expect_tx(bar, 32 * D * 2);
+        __syncwarp();
+        const int nb = 32 / a.box;
+        const int b = lane % nb, half = lane / nb;
+        const int page = __shfl_sync(0xffffffffu, r.page, b * a.box);
+        const int slot = __shfl_sync(0xffffffffu, r.slot, b * a.box);
+        if (half < D / 64)
+            tma_load_4d(entry(next) + half * (128 * 128) + (warp * 32 + b * a.box) * 128, map, half * 64,
+                        w.hk, slot, page, bar);
+        __syncwarp();
+    }
+
+    __device__ void load_k(const TreePiece& w, int t, const Row& r, int g)
     {
         const bool draft = t == w.tiles - 1;
-        const uint32_t there = __ballot_sync(0xffffffffu, off >= 0);
+        const uint32_t there = __ballot_sync(0xffffffffu, exists(r, draft));
         if (lane == 0) sh.keys[g % kRingMeta][warp] = there;
-        const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(draft ? a.k : a.k_cache);
-        rows32(entry(next), warp * 32, KT, off >= 0 ? k + off : nullptr);
-        finish_entry();
+        const bool box = a.box > 0 && !draft && there == 0xffffffffu;
+        if (box) {
+            load_boxes(map_k, w, r);
+        } else {
+            const long long off = offset(w, r, draft);
+            const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(draft ? a.k : a.k_cache);
+            copy_rows32<D>(entry(next), warp * 32, off >= 0 ? k + off : nullptr, a.q, lane);
+        }
+        finish_entry(box);
     }
 
-    __device__ void load_v(const TreePiece& w, int t, long long off, int piece)
+    __device__ void load_v(const TreePiece& w, int t, const Row& r, int piece)
     {
-        if (t < w.tiles - 1) {
+        const bool draft = t == w.tiles - 1;
+        const bool box = a.box > 0 && !draft && __all_sync(0xffffffffu, exists(r, draft));
+        const long long off = offset(w, r, draft);
+        if (box) {
+            load_boxes(map_v, w, r);
+        } else if (!draft) {
             const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_cache);
-            rows32(entry(next), warp * 32, KT, off >= 0 ? v + off : nullptr);
+            copy_rows32<D>(entry(next), warp * 32, off >= 0 ? v + off : nullptr, a.q, lane);
         } else {
             const int c = lane % LPR;
             uint32_t bad = 0;
+#pragma unroll 4
             for (int i = 0; i < 32 / RPI; ++i) {
                 const int j = i * RPI + lane / LPR;
                 const long long src = __shfl_sync(0xffffffffu, off, j);
@@ -362,51 +440,81 @@ struct Copier {
                 if (src >= 0)
                     x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + src + 8 * c));
                 if (clear_nonfinite(x)) bad |= 1u << j;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(entry(next) + at(warp * 32 + j, c, KT)),
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(entry(next) + tile_at(warp * 32 + j, c)),
                              "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
                              : "memory");
             }
             bad = __reduce_or_sync(0xffffffffu, bad);
             if (lane == 0 && warp < 2) sh.bad[piece % kRingMeta][warp] = bad;
         }
-        finish_entry();
+        finish_entry(box);
     }
 };
 
 template <int D, int NT>
-__device__ void copy_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint32_t slots, TreeSpot sp,
-                          long long pos, long long end, int r0, int warp, int lane)
+__device__ void copy_role(TcShared& sh, const TreeArgs& a, const CUtensorMap* map_k, const CUtensorMap* map_v,
+                          uint32_t slots, TreeSpot sp, long long pos, long long end, int warp, int lane)
 {
-    Copier<D, NT> c{sh, a, q_smem, slots, lane, warp};
+    using Sh = TcShape<D, NT>;
+    Copier<D, NT> c{sh, a, map_k, map_v, slots, lane, warp};
     int g = 0, piece = 0;                          // tiles and pieces so far
     while (pos < end) {
         const TreePiece w = tree_next<KT>(a, sp, pos, end);
-        auto row = c.look_up(w, w.t0);
-        auto row1 = c.look_up(w, w.t0 + 1);
-        long long off = c.row_of(w, w.t0, row), ahead = -1;
+        auto walk = c.walk_from(w, w.t0);
+        auto row = c.look_up(w, w.t0, walk), row1 = c.look_up(w, w.t0 + 1, walk);
         c.wait_slot();
-        if (piece > 0) c.wait_for(&sh.q_empty, (uint32_t)(piece - 1) & 1);
-        c.load_q(w, r0);
-        c.load_k(w, w.t0, off, g);
+        c.load_k(w, w.t0, row, g);
         for (int t = w.t0; t < w.t1; ++t, ++g) {
             const bool more = t + 1 < w.t1;
-            if (more) ahead = c.row_of(w, t + 1, row1);
-            row1 = c.look_up(w, t + 2);
+            const auto row2 = c.look_up(w, t + 2, walk);
             if (NT == 1 && more) {
                 c.wait_slot();
-                c.load_k(w, t + 1, ahead, g + 1);
+                c.load_k(w, t + 1, row1, g + 1);
             }
             c.wait_slot();
-            c.load_v(w, t, off, piece);
+            c.load_v(w, t, row, piece);
             if (NT == 2 && more) {
                 c.wait_slot();
-                c.load_k(w, t + 1, ahead, g + 1);
+                c.load_k(w, t + 1, row1, g + 1);
             }
-            off = ahead;
+            row = row1;
+            row1 = row2;
         }
         ++piece;
     }
     while (c.landed < c.next) c.hand_over();
+    // After a wait that gave up nothing else has waited for the boxes in flight.
+    if (*reinterpret_cast<volatile int*>(&sh.dead))
+        for (int e = c.next > Sh::kSlots ? c.next - Sh::kSlots : 0; e < c.next; ++e)
+            mbar_wait(&sh.kv_full[e % Sh::kSlots], (uint32_t)(e / Sh::kSlots) & 1, 1ll << 24);
+}
+
+template <int D, int NT>
+__device__ void q_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, TreeSpot sp, long long pos,
+                       long long end, int r0, int warp, int lane)
+{
+    int piece = 0;
+    while (pos < end) {
+        const TreePiece w = tree_next<KT>(a, sp, pos, end);
+        if (piece > 0) wait(sh, &sh.q_empty, (uint32_t)(piece - 1) & 1, a.status);
+        __syncwarp();
+        for (int b = warp; b < NT * 4; b += kQWarps) {
+            const int r = r0 + b * 32 + lane;
+            const __nv_bfloat16* p = nullptr;
+            if (r < a.R) {
+                const int t = r / a.G, g = r - t * a.G;
+                p = static_cast<const __nv_bfloat16*>(a.q) +
+                    (((long long)w.n * a.Ts + t) * a.Hq + w.hk * a.G + g) * D;
+            }
+            copy_rows32<D>(q_smem + (b >> 2) * 128 * D * 2, (b & 3) * 32, p, a.q, lane);
+        }
+        cp_async_commit();
+        cp_async_wait(0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full);
+        ++piece;
+    }
 }
 
 // -------------------------------------------------------------- the products
@@ -444,6 +552,7 @@ __device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint3
     while (pos < end) {
         const TreePiece w = tree_next<KT>(a, sp, pos, end);
         const int cnt = w.t1 - w.t0;
+        wait(sh, &sh.q_full, (uint32_t)piece & 1, a.status);
         take(entry);
         if constexpr (NT == 1) {
             qk(0, entry, tmem + (tile & 1) * Sh::kS1);
@@ -701,7 +810,8 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, TreeSpot sp, long 
 
 template <int D, int NT>
 __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
-tree_attention_tc_kernel(const __grid_constant__ TreeArgs a)
+tree_attention_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ CUtensorMap map_v)
 {
     using Sh = TcShape<D, NT>;
     extern __shared__ uint8_t raw[];
@@ -714,6 +824,7 @@ tree_attention_tc_kernel(const __grid_constant__ TreeArgs a)
             mbar_init(&sh.kv_full[i], 4);
             mbar_init(&sh.kv_empty[i], 1);
         }
+        mbar_init(&sh.q_full, kQWarps);
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.done, 1);
         for (int i = 0; i < 2; ++i) {
@@ -735,17 +846,21 @@ tree_attention_tc_kernel(const __grid_constant__ TreeArgs a)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
-    const long long pos = tree_begin(sp.total, group, a.groups);
-    const long long end = tree_begin(sp.total, group + 1, a.groups);
+    const long long pos = tree_begin(sp, group);
+    const long long end = tree_begin(sp, group + 1);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp < Sh::kCopyWarp) {
         more_registers<Sh::kMore>();
         softmax_role<D, NT>(sh, a, sp, pos, end, r0, warp, lane, tmem);
     } else if (warp < Sh::kMmaWarp) {
         fewer_registers<Sh::kFewer>();
-        copy_role<D, NT>(sh, a, q_smem, slots, sp, pos, end, r0, warp - Sh::kCopyWarp, lane);
+        copy_role<D, NT>(sh, a, &map_k, &map_v, slots, sp, pos, end, warp - Sh::kCopyWarp, lane);
     } else {
         fewer_registers<Sh::kFewer>();
-        if (warp == Sh::kMmaWarp) mma_role<D, NT>(sh, a, q_smem, slots, sp, pos, end, r0, tmem);
+        if (warp == Sh::kMmaWarp)
+            mma_role<D, NT>(sh, a, q_smem, slots, sp, pos, end, r0, tmem);
+        else if (warp <= Sh::kMmaWarp + kQWarps)
+            q_role<D, NT>(sh, a, q_smem, sp, pos, end, r0, warp - Sh::kMmaWarp - 1, lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -756,24 +871,56 @@ tree_attention_tc_kernel(const __grid_constant__ TreeArgs a)
 }
 
 template <int D, int NT>
-cudaError_t launch_tc(const TreeArgs& a, cudaStream_t stream)
+cudaError_t launch_tc(const TreeArgs& a, const CUtensorMap& map_k, const CUtensorMap& map_v, cudaStream_t stream)
 {
     auto kern = tree_attention_tc_kernel<D, NT>;
     const size_t bytes = TcShape<D, NT>::kBytes;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    kern<<<a.groups * a.row_tiles, TcShape<D, NT>::kThreads, bytes, stream>>>(a);
+    kern<<<a.groups * a.row_tiles, TcShape<D, NT>::kThreads, bytes, stream>>>(a, map_k, map_v);
     return cudaGetLastError();
+}
+
+// The pool as [num_pages][page_size][Hkv][d], boxes of `box` rows of one page
+// and 64 columns of one head in the 128-byte swizzle.
+bool make_pool_map(CUtensorMap* m, const void* base, const TreeArgs& a, int d, int box)
+{
+    const auto fn = tc_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)a.Hkv, (cuuint64_t)a.page_size, (cuuint64_t)a.num_pages};
+    const cuuint64_t row = (cuuint64_t)a.Hkv * d * 2;
+    const cuuint64_t page = a.num_pages > 1 ? (cuuint64_t)a.page_stride * 2 : row * a.page_size;
+    const cuuint64_t strides[3] = {(cuuint64_t)d * 2, row, page};
+    const cuuint32_t boxes[4] = {64, 1, (cuuint32_t)box, 1};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, boxes, steps,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS && debug_enabled())
+        fprintf(stderr, "kda: cuTensorMapEncodeTiled failed (CUresult %d, page pool)\n", (int)r);
+    return r == CUDA_SUCCESS;
 }
 
 }  // namespace
 
-cudaError_t launch_tree_attention_tc(const TreeArgs& args, const TreePlan& plan, int32_t d,
-                                     cudaStream_t stream)
+cudaError_t launch_tree_attention_tc(TreeArgs args, const TreePlan& plan, int32_t d, cudaStream_t stream)
 {
+    // Boxes of up to 32 rows that a page holds whole, and no fewer than the 8
+    // rows of a swizzle group; other page sizes are copied by the lanes.
+    int box = 32;
+    while (box >= 8 && args.page_size % box != 0) box /= 2;
+    CUtensorMap map_k = {}, map_v = {};
+    if (box < 8 || args.num_pages == 0 || !make_pool_map(&map_k, args.k_cache, args, d, box) ||
+        !make_pool_map(&map_v, args.v_cache, args, d, box))
+        box = 0;
+    args.box = box;
+    args.tile_pages = KT / args.page_size;
+    args.tile_rows = KT % args.page_size;
     if (d == 64)
-        return plan.rt == 128 ? launch_tc<64, 1>(args, stream) : launch_tc<64, 2>(args, stream);
-    return plan.rt == 128 ? launch_tc<128, 1>(args, stream) : launch_tc<128, 2>(args, stream);
+        return plan.rt == 128 ? launch_tc<64, 1>(args, map_k, map_v, stream)
+                              : launch_tc<64, 2>(args, map_k, map_v, stream);
+    return plan.rt == 128 ? launch_tc<128, 1>(args, map_k, map_v, stream)
+                          : launch_tc<128, 2>(args, map_k, map_v, stream);
 }
 
 }  // namespace kda
