@@ -1,9 +1,9 @@
 // kda_tree.cuh -- what the tree attention kernels share: the arguments, the
 // drafted tree's ancestor masks, and the split of the work over the CTAs.
 //
-// Work split.  An item is one (sequence, cache head); its keys come in tiles of
-// KT: ceil(L / KT) tiles of the context, then one tile that holds the drafted
-// nodes.  Laid end to end in (sequence, head, tile) order, the tiles are cut
+// Work split.  An item is one (sequence, cache head); its keys, the L rows of the
+// context and after them the Ts drafted nodes, come in ceil((L + Ts) / KT) tiles
+// of KT.  Laid end to end in (sequence, head, tile) order, the tiles are cut
 // into equal ranges, one per group of CTAs, whatever the lengths are; the
 // lengths stay on the device and every CTA finds its own range from them.  The
 // CTAs of a group have one row tile (up to RT of the item's Ts G query rows)
@@ -108,7 +108,7 @@ struct TreeSpot {
 template <int KT>
 __device__ __forceinline__ long long tree_seq_tiles(const TreeArgs& a, int n)
 {
-    return ((long long)tree_context(a, n) + KT - 1) / KT + 1;
+    return (tree_context(a, n) + a.Ts + KT - 1) / KT;
 }
 
 // First tile of group c's range.
@@ -191,7 +191,7 @@ __device__ __forceinline__ TreePiece tree_next(const TreeArgs& a, TreeSpot& sp, 
     TreePiece w;
     w.n = sp.n;
     w.ctx = tree_context(a, w.n);
-    w.tiles = (w.ctx + KT - 1) / KT + 1;
+    w.tiles = (w.ctx + a.Ts + KT - 1) / KT;
     const long long at = pos - sp.start;
     w.hk = (int)(at / w.tiles);
     w.t0 = (int)(at - (long long)w.hk * w.tiles);

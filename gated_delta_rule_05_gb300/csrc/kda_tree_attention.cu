@@ -103,9 +103,10 @@ tree_attention_simt_kernel(const TreeArgs a)
             for (int c = 0; c < CR; ++c) acc[i][c] = 0.f;
         }
         for (int t = t0; t < t1; ++t) {
-            const bool draft = t == tiles - 1;
             const int k0 = t * kSimtKeys;
-            const int nk = draft ? a.Ts : (ctx - k0 < kSimtKeys ? ctx - k0 : kSimtKeys);
+            const int nc = ctx - k0;                // key j is drafted node j - nc from j = nc on
+            const int nk = nc + a.Ts < kSimtKeys ? nc + a.Ts : kSimtKeys;
+            const bool draft = nc < kSimtKeys;      // some are
             __syncthreads();                        // the previous tile has been read
             for (int e = tid; e < kSimtKeys * V4; e += kSimtThreads) {
                 const int j = e / V4, c = e % V4;
@@ -113,8 +114,8 @@ tree_attention_simt_kernel(const TreeArgs a)
                 if (j < nk) {
                     long long off;
                     const TI *kp = static_cast<const TI*>(a.k_cache), *vp = static_cast<const TI*>(a.v_cache);
-                    if (draft) {
-                        off = ((long long)n * a.Ts + j) * row_elems;
+                    if (j >= nc) {
+                        off = ((long long)n * a.Ts + j - nc) * row_elems;
                         kp = static_cast<const TI*>(a.k);
                         vp = static_cast<const TI*>(a.v);
                     } else {
@@ -152,23 +153,20 @@ tree_attention_simt_kernel(const TreeArgs a)
                     }
                 }
             }
-            unsigned long long there = ~0ull;       // context keys whose page exists
-            if (!draft) {
-                unsigned bits = 0;
+            unsigned there = 0;                     // context keys whose page exists
 #pragma unroll
-                for (int j = 0; j < KR; ++j) {
-                    const int kk = tx + 16 * j;
-                    if (kk < nk && tree_cache_row(a, table, k0 + kk, row_elems) >= 0) bits |= 1u << j;
-                }
-                there = bits;
+            for (int j = 0; j < KR; ++j) {
+                const int kk = tx + 16 * j;
+                if (kk < nc && tree_cache_row(a, table, k0 + kk, row_elems) >= 0) there |= 1u << j;
             }
 #pragma unroll
             for (int i = 0; i < RR; ++i) {
                 float top = m[i];
 #pragma unroll
                 for (int j = 0; j < KR; ++j) {
-                    const bool see = draft ? (mask[i] >> (tx + 16 * j)) & 1ull
-                                           : mask[i] != 0ull && ((there >> j) & 1ull);
+                    const int node = tx + 16 * j - nc;
+                    const bool see = node < 0 ? mask[i] != 0ull && ((there >> j) & 1)
+                                              : node < a.Ts && ((mask[i] >> node) & 1ull);
                     if (!see) s[i][j] = -INFINITY;
                     top = fmaxf(top, s[i][j]);
                 }
@@ -207,7 +205,8 @@ tree_attention_simt_kernel(const TreeArgs a)
                     for (int i = 0; i < RR; ++i) {
                         const float pp = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
                         // a node that this row does not see may hold inf or NaN: 0 * v would keep it
-                        if (draft && !((mask[i] >> (j + jj)) & 1ull)) continue;
+                        if (draft && j + jj >= nc && (j + jj >= nk || !((mask[i] >> (j + jj - nc)) & 1ull)))
+                            continue;
 #pragma unroll
                         for (int c = 0; c < CR; ++c) acc[i][c] = fmaf(pp, v[c], acc[i][c]);
                     }

@@ -71,24 +71,10 @@ struct TcShared {
     uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2];
     uint32_t tmem;
     int dead;
-    uint32_t keys[kRingMeta][4];           // valid keys of a context tile
-    uint32_t bad[kRingMeta][2];            // drafted nodes of a piece whose v is not finite
+    uint32_t keys[kRingMeta][4];           // a tile's keys that are context rows of pages that exist
+    uint32_t bad[kRingMeta][4];            // a tile's keys that are drafted nodes with inf or NaN in v
     long long loc[16 + 2];
 };
-
-// Whether the phase has completed, without the suspension of a try_wait.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 
 // Waits unless some wait of this CTA has already given up.
 __device__ __forceinline__ void wait(TcShared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
@@ -124,23 +110,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// Waits until at most `left` of this thread's groups are in flight.
-__device__ __forceinline__ void cp_async_wait(int left)
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// The barrier's current phase stays open until this thread's copies have landed.
+__device__ __forceinline__ void cp_async_hold(uint64_t* bar)
 {
-    switch (left) {
-        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-        case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-        case 7: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-        case 8: asm volatile("cp.async.wait_group 8;" ::: "memory"); break;
-        case 9: asm volatile("cp.async.wait_group 9;" ::: "memory"); break;
-        case 10: asm volatile("cp.async.wait_group 10;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 11;" ::: "memory"); break;
-    }
+    asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -280,66 +255,34 @@ __device__ __forceinline__ void copy_rows32(uint32_t dst, int row0, const __nv_b
 //
 // Where all 32 rows are context rows of pages that exist, and the page size
 // allows (a.box), the rows come as TMA boxes that complete on the entry's
-// barrier.  Elsewhere (the end of a context, drafted rows, other page sizes) the
-// lanes copy them, and hand the entry over when it has landed.
+// barrier.  Elsewhere (the end of a context, other page sizes) the lanes copy
+// them with cp.async; drafted values go through registers.
 template <int D, int NT>
 struct Copier {
     using Sh = TcShape<D, NT>;
     static constexpr int LPR = D / 8;              // lanes per row of 16-byte chunks
     static constexpr int RPI = 32 / LPR;           // rows per instruction
+    static constexpr int kDrafted = -2;
     TcShared& sh;
     const TreeArgs& a;
     const CUtensorMap *map_k, *map_v;
     uint32_t slots;
     int lane, warp;                                // warp 0 .. 3
-    int next = 0, landed = 0;                      // entries issued, entries handed over
-    uint32_t boxes = 0;                            // bit e % 32: entry e came as boxes
+    int next = 0;                                  // ring entries issued
 
-    __device__ uint32_t entry(int i) const { return slots + (uint32_t)(i % Sh::kSlots) * Sh::kSlotBytes; }
+    __device__ uint32_t entry() const { return slots + (uint32_t)(next % Sh::kSlots) * Sh::kSlotBytes; }
+    __device__ uint64_t* full() const { return &sh.kv_full[next % Sh::kSlots]; }
 
-    // Entry `landed` is the oldest that the lanes copied and have not handed over
-    // yet; it holds the products up, so that next - landed <= kSlots.
-    __device__ void skip_boxes()
-    {
-        while (landed < next && ((boxes >> (landed & 31)) & 1)) ++landed;
-    }
-
-    // Hands it over to the products.
-    __device__ void hand_over()
-    {
-        cp_async_wait(next - landed - 1);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.kv_full[landed % Sh::kSlots]);
-        ++landed;
-        skip_boxes();
-    }
-
-    // Waits until the next entry's slot is free, handing over what has landed.
+    // Waits until the next entry's slot is free.
     __device__ void wait_slot()
     {
         const int use = next / Sh::kSlots;
-        if (use == 0) return;
-        uint64_t* bar = &sh.kv_empty[next % Sh::kSlots];
-        const uint32_t parity = (uint32_t)(use - 1) & 1;
-        while (landed < next) {
-            if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return;
-            hand_over();
-        }
-        wait(sh, bar, parity, a.status);
+        if (use > 0) wait(sh, &sh.kv_empty[next % Sh::kSlots], (uint32_t)(use - 1) & 1, a.status);
         __syncwarp();
     }
 
-    __device__ void finish_entry(bool box)
-    {
-        cp_async_commit();                         // a group per entry, empty for boxes
-        boxes = (boxes & ~(1u << (next & 31))) | ((uint32_t)box << (next & 31));
-        ++next;
-        skip_boxes();
-    }
-
-    // This lane's row of a tile: its page (-1: no such row) and its place there;
-    // of drafted rows the place alone.
+    // This lane's row of a tile: its page and its place there, or kDrafted and
+    // the node; page -1: no row.
     struct Row {
         int page, slot;
     };
@@ -348,7 +291,7 @@ struct Copier {
     struct Walk {
         int pos, p, slot;
     };
-    __device__ Walk walk_from(const TreePiece& w, int t) const
+    __device__ Walk walk_from(int t) const
     {
         const int pos = t * KT + warp * 32 + lane;
         const int p = pos / a.page_size;
@@ -358,11 +301,8 @@ struct Copier {
     {
         Row r = {-1, k.slot};
         if (t >= w.t1) return r;
-        if (t == w.tiles - 1) {
-            const int j = warp * 32 + lane;
-            return {j < a.Ts ? 0 : -1, j};
-        }
         if (k.pos < w.ctx) r.page = __ldg(a.page_table + (long long)w.n * a.max_pages + k.p);
+        else if (k.pos - w.ctx < a.Ts) r = {kDrafted, k.pos - w.ctx};
         k.pos += KT;
         k.p += a.tile_pages;
         k.slot += a.tile_rows;
@@ -373,81 +313,86 @@ struct Copier {
         return r;
     }
 
-    __device__ bool exists(const Row& r, bool draft) const
-    {
-        return r.page >= 0 && (draft || r.page < a.num_pages);
-    }
+    __device__ bool cached(const Row& r) const { return r.page >= 0 && r.page < a.num_pages; }
 
-    // Element offset of the row in K and V (-1: none).
-    __device__ long long offset(const TreePiece& w, const Row& r, bool draft) const
+    // The row's source in the cache or among the drafted rows (null: none).
+    __device__ const __nv_bfloat16* source(const TreePiece& w, const Row& r, const void* cache,
+                                           const void* drafted) const
     {
         const int row_elems = a.Hkv * D;
-        if (!exists(r, draft)) return -1;
-        return (draft ? (long long)w.n * a.Ts * row_elems : (long long)r.page * a.page_stride) +
-               (long long)r.slot * row_elems + (long long)w.hk * D;
+        if (cached(r))
+            return static_cast<const __nv_bfloat16*>(cache) + (long long)r.page * a.page_stride +
+                   (long long)r.slot * row_elems + (long long)w.hk * D;
+        if (r.page == kDrafted)
+            return static_cast<const __nv_bfloat16*>(drafted) +
+                   ((long long)w.n * a.Ts + r.slot) * row_elems + (long long)w.hk * D;
+        return nullptr;
     }
 
     // The warp's 32 rows as boxes of a.box rows and 64 columns, a lane each.
     __device__ void load_boxes(const CUtensorMap* map, const TreePiece& w, const Row& r)
     {
-        uint64_t* bar = &sh.kv_full[next % Sh::kSlots];
-        if (lane == 0) mbar_arrive_expect_tx(bar, 32 * D * 2);
+        if (lane == 0) mbar_arrive_expect_tx(full(), 32 * D * 2);
         __syncwarp();
         const int nb = 32 / a.box;
         const int b = lane % nb, half = lane / nb;
         const int page = __shfl_sync(0xffffffffu, r.page, b * a.box);
         const int slot = __shfl_sync(0xffffffffu, r.slot, b * a.box);
         if (half < D / 64)
-            tma_load_4d(entry(next) + half * (128 * 128) + (warp * 32 + b * a.box) * 128, map, half * 64,
-                        w.hk, slot, page, bar);
+            tma_load_4d(entry() + half * (128 * 128) + (warp * 32 + b * a.box) * 128, map, half * 64,
+                        w.hk, slot, page, full());
         __syncwarp();
     }
 
-    __device__ void load_k(const TreePiece& w, int t, const Row& r, int g)
+    __device__ void load_lanes(const __nv_bfloat16* p)
     {
-        const bool draft = t == w.tiles - 1;
-        const uint32_t there = __ballot_sync(0xffffffffu, exists(r, draft));
-        if (lane == 0) sh.keys[g % kRingMeta][warp] = there;
-        const bool box = a.box > 0 && !draft && there == 0xffffffffu;
-        if (box) {
-            load_boxes(map_k, w, r);
-        } else {
-            const long long off = offset(w, r, draft);
-            const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(draft ? a.k : a.k_cache);
-            copy_rows32<D>(entry(next), warp * 32, off >= 0 ? k + off : nullptr, a.q, lane);
-        }
-        finish_entry(box);
+        copy_rows32<D>(entry(), warp * 32, p, a.q, lane);
+        cp_async_hold(full());
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full());
     }
 
-    __device__ void load_v(const TreePiece& w, int t, const Row& r, int piece)
+    __device__ void load_k(const TreePiece& w, const Row& r, int g)
     {
-        const bool draft = t == w.tiles - 1;
-        const bool box = a.box > 0 && !draft && __all_sync(0xffffffffu, exists(r, draft));
-        const long long off = offset(w, r, draft);
-        if (box) {
-            load_boxes(map_v, w, r);
-        } else if (!draft) {
-            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_cache);
-            copy_rows32<D>(entry(next), warp * 32, off >= 0 ? v + off : nullptr, a.q, lane);
-        } else {
+        const uint32_t there = __ballot_sync(0xffffffffu, cached(r));
+        if (lane == 0) sh.keys[g % kRingMeta][warp] = there;
+        if (a.box > 0 && there == 0xffffffffu) load_boxes(map_k, w, r);
+        else load_lanes(source(w, r, a.k_cache, a.k));
+        ++next;
+    }
+
+    __device__ void load_v(const TreePiece& w, const Row& r, int g)
+    {
+        const uint32_t there = __ballot_sync(0xffffffffu, cached(r));
+        const uint32_t drafted = __ballot_sync(0xffffffffu, r.page == kDrafted);
+        uint32_t bad = 0;
+        const unsigned long long p = reinterpret_cast<unsigned long long>(source(w, r, a.v_cache, a.v));
+        if (drafted) {
             const int c = lane % LPR;
-            uint32_t bad = 0;
 #pragma unroll 4
             for (int i = 0; i < 32 / RPI; ++i) {
                 const int j = i * RPI + lane / LPR;
-                const long long src = __shfl_sync(0xffffffffu, off, j);
+                const unsigned long long src = __shfl_sync(0xffffffffu, p, j);
                 uint4 x = make_uint4(0, 0, 0, 0);
-                if (src >= 0)
-                    x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + src + 8 * c));
-                if (clear_nonfinite(x)) bad |= 1u << j;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(entry(next) + tile_at(warp * 32 + j, c)),
+                if (src) x = __ldg(reinterpret_cast<const uint4*>(src + 16ull * c));
+                if (((drafted >> j) & 1) && clear_nonfinite(x)) bad |= 1u << j;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(entry() + tile_at(warp * 32 + j, c)),
                              "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
                              : "memory");
             }
             bad = __reduce_or_sync(0xffffffffu, bad);
-            if (lane == 0 && warp < 2) sh.bad[piece % kRingMeta][warp] = bad;
         }
-        finish_entry(box);
+        if (lane == 0) sh.bad[g % kRingMeta][warp] = bad;
+        if (drafted) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full());
+        } else if (a.box > 0 && there == 0xffffffffu) {
+            load_boxes(map_v, w, r);
+        } else {
+            load_lanes(reinterpret_cast<const __nv_bfloat16*>(p));
+        }
+        ++next;
     }
 };
 
@@ -457,33 +402,31 @@ __device__ void copy_role(TcShared& sh, const TreeArgs& a, const CUtensorMap* ma
 {
     using Sh = TcShape<D, NT>;
     Copier<D, NT> c{sh, a, map_k, map_v, slots, lane, warp};
-    int g = 0, piece = 0;                          // tiles and pieces so far
+    int g = 0;                                     // tiles so far
     while (pos < end) {
         const TreePiece w = tree_next<KT>(a, sp, pos, end);
-        auto walk = c.walk_from(w, w.t0);
+        auto walk = c.walk_from(w.t0);
         auto row = c.look_up(w, w.t0, walk), row1 = c.look_up(w, w.t0 + 1, walk);
         c.wait_slot();
-        c.load_k(w, w.t0, row, g);
+        c.load_k(w, row, g);
         for (int t = w.t0; t < w.t1; ++t, ++g) {
             const bool more = t + 1 < w.t1;
             const auto row2 = c.look_up(w, t + 2, walk);
             if (NT == 1 && more) {
                 c.wait_slot();
-                c.load_k(w, t + 1, row1, g + 1);
+                c.load_k(w, row1, g + 1);
             }
             c.wait_slot();
-            c.load_v(w, t, row, piece);
+            c.load_v(w, row, g);
             if (NT == 2 && more) {
                 c.wait_slot();
-                c.load_k(w, t + 1, row1, g + 1);
+                c.load_k(w, row1, g + 1);
             }
             row = row1;
             row1 = row2;
         }
-        ++piece;
     }
-    while (c.landed < c.next) c.hand_over();
-    // After a wait that gave up nothing else has waited for the boxes in flight.
+    // After a wait that gave up nothing else has waited for the copies in flight.
     if (*reinterpret_cast<volatile int*>(&sh.dead))
         for (int e = c.next > Sh::kSlots ? c.next - Sh::kSlots : 0; e < c.next; ++e)
             mbar_wait(&sh.kv_full[e % Sh::kSlots], (uint32_t)(e / Sh::kSlots) & 1, 1ll << 24);
@@ -509,7 +452,7 @@ __device__ void q_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, TreeSpo
             copy_rows32<D>(q_smem + (b >> 2) * 128 * D * 2, (b & 3) * 32, p, a.q, lane);
         }
         cp_async_commit();
-        cp_async_wait(0);
+        cp_async_wait_all();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full);
@@ -532,7 +475,9 @@ __device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint3
     const int nt = (NT == 2 && a.R - r0 > 128) ? 2 : 1;
 
     auto take = [&](int e) { wait(sh, &sh.kv_full[e % Sh::kSlots], (uint32_t)(e / Sh::kSlots) & 1, a.status);
-                             __syncwarp(); tc_fence_after(); };
+                             fence_proxy_async_smem();   // rows that the lanes copied with cp.async
+                             __syncwarp();
+                             tc_fence_after(); };
     auto qk = [&](int i, int e, uint32_t d_tmem) {
         const uint64_t da = make_sdesc(q_smem + i * 128 * D * 2, 16, 1024, kSwizzle128B);
         const uint64_t db = make_sdesc(slots + (uint32_t)(e % Sh::kSlots) * Sh::kSlotBytes, 16, 1024, kSwizzle128B);
@@ -668,13 +613,16 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, TreeSpot sp, long 
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, x[c]);
                 uint32_t keep[4];
-                if (t == w.tiles - 1) {
-                    keep[0] = (uint32_t)seen;
-                    keep[1] = (uint32_t)(seen >> 32);
-                    keep[2] = keep[3] = 0;
-                } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) keep[c] = sh.keys[tile % kRingMeta][c];
+                for (int c = 0; c < 4; ++c) keep[c] = sh.keys[tile % kRingMeta][c];
+                const int nc = w.ctx - t * KT;     // key j is drafted node j - nc from j = nc on
+                if (nc < KT) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int i = 32 * c - nc; // the node at bit 0 of this word
+                        if (i >= 0) keep[c] |= i < 64 ? (uint32_t)(seen >> i) : 0u;
+                        else if (i > -32) keep[c] |= (uint32_t)(seen << -i);
+                    }
                 }
                 const bool all = (keep[0] & keep[1] & keep[2] & keep[3]) == 0xffffffffu;
                 tmem_ld_wait();
@@ -752,8 +700,15 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, TreeSpot sp, long 
         if (live) {
             const bool mine = r < a.R;
             unsigned long long add = 0;            // seen nodes with inf or NaN values
-            if (w.t1 == w.tiles)
-                add = seen & (((unsigned long long)sh.bad[piece % kRingMeta][1] << 32) | sh.bad[piece % kRingMeta][0]);
+            for (int t = w.t1 - 1, k = 1; t >= w.t0 && (t + 1) * KT > w.ctx; --t, ++k) {
+                for (int c = 0; c < 4; ++c) {
+                    const unsigned long long bits = sh.bad[(tile - k) % kRingMeta][c];
+                    const int i = 32 * c - (w.ctx - t * KT);
+                    if (i >= 0) add |= i < 64 ? bits << i : 0ull;
+                    else if (i > -32) add |= bits >> -i;
+                }
+            }
+            add &= seen;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const int g = r - node * a.G;
             __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.o) +

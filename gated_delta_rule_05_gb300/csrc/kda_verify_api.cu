@@ -59,8 +59,8 @@ kda_status_t kda_tree_attention(const void* q, const void* k, const void* v, con
     if (Ts > kda::kTreeMaxNodes) return KDA_ERR_UNSUPPORTED;
     if (N < 1 || Ts < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0) return KDA_ERR_INVALID_ARG;
     if (num_pages < 0 || page_size < 1 || max_pages < 0) return KDA_ERR_INVALID_ARG;
-    // Positions are 32-bit; a row tile is a block index.
-    if ((int64_t)max_pages * page_size > INT32_MAX || (int64_t)Ts * Hq > (1 << 20) ||
+    // Positions (of the drafted rows too) are 32-bit; a row tile is a block index.
+    if ((int64_t)max_pages * page_size > INT32_MAX - 1024 || (int64_t)Ts * Hq > (1 << 20) ||
         (int64_t)Hkv * d > INT32_MAX)
         return KDA_ERR_INVALID_ARG;
     if (!q || !k || !v || !lengths || !o) return KDA_ERR_INVALID_ARG;
