@@ -76,14 +76,22 @@ struct TcShared {
     long long loc[16 + 2];
 };
 
-// Waits unless some wait of this CTA has already given up.
+// Waits for a phase of a barrier, for about two seconds at most (see mbar_wait),
+// and not at all once some wait of this CTA has given up.  Written short: the
+// roles run side by side and have to share the SM's instruction cache (with
+// mbar_wait's loops at every wait and all loops below unrolled they took 242 KB,
+// and a piece's start and end cost 20 us).
 __device__ __forceinline__ void wait(TcShared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
 {
     if (mbar_try_wait(bar, parity)) return;
-    if (*reinterpret_cast<volatile int*>(&sh.dead)) return;
-    if (!mbar_wait(bar, parity)) {
-        *reinterpret_cast<volatile int*>(&sh.dead) = 1;
-        atomicOr(status + kWsTimeoutWord, 2);
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (*reinterpret_cast<volatile int*>(&sh.dead)) return;
+        if (clock64() - t0 > (1ll << 32)) {
+            *reinterpret_cast<volatile int*>(&sh.dead) = 1;
+            atomicOr(status + kWsTimeoutWord, 2);
+        }
     }
 }
 
@@ -194,7 +202,7 @@ __device__ __forceinline__ unsigned long long tree_mask_of(const int32_t* parent
         m[i] = 1ull << x;
         u[i] = p;
     }
-#pragma unroll
+#pragma unroll 1
     for (int round = 0; round < 6; ++round) {
         unsigned long long m2[2];
         int u2[2];
@@ -344,55 +352,64 @@ struct Copier {
         __syncwarp();
     }
 
-    __device__ void load_lanes(const __nv_bfloat16* p)
+    // The next ring entry: the K or V rows of a piece's tile, the g-th tile of
+    // the CTA.
+    __device__ void load(bool is_k, const TreePiece& w, const Row& r, int g)
     {
-        copy_rows32<D>(entry(), warp * 32, p, a.q, lane);
-        cp_async_hold(full());
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full());
-    }
-
-    __device__ void load_k(const TreePiece& w, const Row& r, int g)
-    {
-        const uint32_t there = __ballot_sync(0xffffffffu, cached(r));
-        if (lane == 0) sh.keys[g % kRingMeta][warp] = there;
-        if (a.box > 0 && there == 0xffffffffu) load_boxes(map_k, w, r);
-        else load_lanes(source(w, r, a.k_cache, a.k));
-        ++next;
-    }
-
-    __device__ void load_v(const TreePiece& w, const Row& r, int g)
-    {
+        wait_slot();
         const uint32_t there = __ballot_sync(0xffffffffu, cached(r));
         const uint32_t drafted = __ballot_sync(0xffffffffu, r.page == kDrafted);
-        uint32_t bad = 0;
-        const unsigned long long p = reinterpret_cast<unsigned long long>(source(w, r, a.v_cache, a.v));
-        if (drafted) {
-            const int c = lane % LPR;
-#pragma unroll 4
-            for (int i = 0; i < 32 / RPI; ++i) {
-                const int j = i * RPI + lane / LPR;
-                const unsigned long long src = __shfl_sync(0xffffffffu, p, j);
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (src) x = __ldg(reinterpret_cast<const uint4*>(src + 16ull * c));
-                if (((drafted >> j) & 1) && clear_nonfinite(x)) bad |= 1u << j;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(entry() + tile_at(warp * 32 + j, c)),
-                             "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
-                             : "memory");
+        if (a.box > 0 && there == 0xffffffffu) {
+            if (lane == 0) {
+                if (is_k) sh.keys[g % kRingMeta][warp] = there;
+                else sh.bad[g % kRingMeta][warp] = 0;
             }
-            bad = __reduce_or_sync(0xffffffffu, bad);
-        }
-        if (lane == 0) sh.bad[g % kRingMeta][warp] = bad;
-        if (drafted) {
-            fence_proxy_async_smem();
+            load_boxes(is_k ? map_k : map_v, w, r);
+        } else {
+            const __nv_bfloat16* p = is_k ? source(w, r, a.k_cache, a.k) : source(w, r, a.v_cache, a.v);
+            if (is_k || !drafted) {
+                if (lane == 0) {
+                    if (is_k) sh.keys[g % kRingMeta][warp] = there;
+                    else sh.bad[g % kRingMeta][warp] = 0;
+                }
+                copy_rows32<D>(entry(), warp * 32, p, a.q, lane);
+                cp_async_hold(full());
+            } else {
+                load_drafted(p, drafted, g);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(full());
-        } else if (a.box > 0 && there == 0xffffffffu) {
-            load_boxes(map_v, w, r);
-        } else {
-            load_lanes(reinterpret_cast<const __nv_bfloat16*>(p));
         }
         ++next;
+    }
+
+    // V rows with drafted ones among them, through registers.
+    __device__ void load_drafted(const __nv_bfloat16* p, uint32_t drafted, int g)
+    {
+        const unsigned long long mine = reinterpret_cast<unsigned long long>(p);
+        const int c = lane % LPR;
+        uint32_t bad = 0;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32 / RPI; i0 += 4) {
+            uint4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const unsigned long long src = __shfl_sync(0xffffffffu, mine, (i0 + k) * RPI + lane / LPR);
+                x[k] = make_uint4(0, 0, 0, 0);
+                if (src) x[k] = __ldg(reinterpret_cast<const uint4*>(src + 16ull * c));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = (i0 + k) * RPI + lane / LPR;
+                if (((drafted >> j) & 1) && clear_nonfinite(x[k])) bad |= 1u << j;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(entry() + tile_at(warp * 32 + j, c)),
+                             "r"(x[k].x), "r"(x[k].y), "r"(x[k].z), "r"(x[k].w)
+                             : "memory");
+            }
+        }
+        bad = __reduce_or_sync(0xffffffffu, bad);
+        if (lane == 0) sh.bad[g % kRingMeta][warp] = bad;
+        fence_proxy_async_smem();
     }
 };
 
@@ -402,29 +419,30 @@ __device__ void copy_role(TcShared& sh, const TreeArgs& a, const CUtensorMap* ma
 {
     using Sh = TcShape<D, NT>;
     Copier<D, NT> c{sh, a, map_k, map_v, slots, lane, warp};
-    int g = 0;                                     // tiles so far
+    int g = 0;                                     // tiles of the pieces before
     while (pos < end) {
         const TreePiece w = tree_next<KT>(a, sp, pos, end);
+        const int cnt = w.t1 - w.t0;
         auto walk = c.walk_from(w.t0);
+        // the rows of the tile whose V comes next, of the one after it, and of
+        // the next to look up
         auto row = c.look_up(w, w.t0, walk), row1 = c.look_up(w, w.t0 + 1, walk);
-        c.wait_slot();
-        c.load_k(w, row, g);
-        for (int t = w.t0; t < w.t1; ++t, ++g) {
-            const bool more = t + 1 < w.t1;
-            const auto row2 = c.look_up(w, t + 2, walk);
-            if (NT == 1 && more) {
-                c.wait_slot();
-                c.load_k(w, row1, g + 1);
+        auto row2 = c.look_up(w, w.t0 + 2, walk);
+        int jk = 0, jv = 0;                        // tiles whose K, V are on their way
+#pragma unroll 1
+        while (jv < cnt) {
+            const bool is_k = jk < cnt && jk < jv + (NT == 1 ? 2 : 1);
+            c.load(is_k, w, is_k && jk > jv ? row1 : row, g + (is_k ? jk : jv));
+            if (is_k) {
+                ++jk;
+            } else {
+                ++jv;
+                row = row1;
+                row1 = row2;
+                row2 = c.look_up(w, w.t0 + jv + 2, walk);
             }
-            c.wait_slot();
-            c.load_v(w, row, g);
-            if (NT == 2 && more) {
-                c.wait_slot();
-                c.load_k(w, row1, g + 1);
-            }
-            row = row1;
-            row1 = row2;
         }
+        g += cnt;
     }
     // After a wait that gave up nothing else has waited for the copies in flight.
     if (*reinterpret_cast<volatile int*>(&sh.dead))
@@ -652,7 +670,7 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, TreeSpot sp, long 
                     l *= f;
                     if (t > w.t0) {
                         wait_last();
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
                             uint32_t y[16];
                             tmem_ld16(to + 16 * c, y);
@@ -700,7 +718,9 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, TreeSpot sp, long 
         if (live) {
             const bool mine = r < a.R;
             unsigned long long add = 0;            // seen nodes with inf or NaN values
+#pragma unroll 1
             for (int t = w.t1 - 1, k = 1; t >= w.t0 && (t + 1) * KT > w.ctx; --t, ++k) {
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     const unsigned long long bits = sh.bad[(tile - k) % kRingMeta][c];
                     const int i = 32 * c - (w.ctx - t * KT);
@@ -709,45 +729,42 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, TreeSpot sp, long 
                 }
             }
             add &= seen;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float scale_o = seen == 0 || l == 0.f ? 0.f : 1.f / l;
             const int g = r - node * a.G;
             __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.o) +
                                 (((long long)w.n * a.Ts + node) * a.Hq + w.hk * a.G + g) * D;
             float* part = a.part + ((size_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * RT * (D + 2);
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t x[32];
-                tmem_ld32(to + 32 * c, x);
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t x[16];
+                tmem_ld16(to + 16 * c, x);
                 tmem_ld_wait();
-                if (add) {
-                    for (unsigned long long rest = add; rest; rest &= rest - 1) {
-                        const int j = __ffsll((long long)rest) - 1;
-                        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) +
-                            (((long long)w.n * a.Ts + j) * a.Hkv + w.hk) * D + 32 * c;
+                for (unsigned long long left = add; left; left &= left - 1) {
+                    const int j = __ffsll((long long)left) - 1;
+                    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) +
+                        (((long long)w.n * a.Ts + j) * a.Hkv + w.hk) * D + 16 * c;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float y = __bfloat162float(v[i]);
-                            if (!(fabsf(y) < INFINITY)) x[i] = __float_as_uint(__uint_as_float(x[i]) + y);
-                        }
+                    for (int i = 0; i < 16; ++i) {
+                        const float y = __bfloat162float(v[i]);
+                        if (!(fabsf(y) < INFINITY)) x[i] = __float_as_uint(__uint_as_float(x[i]) + y);
                     }
                 }
+                if (seen == 0) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = 0;
+                }
                 if (mine && whole) {
+                    uint32_t y[8];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            y[j] = pack_bf16x2(__uint_as_float(x[i + 2 * j]) * inv,
-                                               __uint_as_float(x[i + 2 * j + 1]) * inv);
-                        *reinterpret_cast<uint4*>(op + 32 * c + i) =
-                            seen == 0 ? make_uint4(0, 0, 0, 0) : make_uint4(y[0], y[1], y[2], y[3]);
-                    }
+                    for (int j = 0; j < 8; ++j)
+                        y[j] = pack_bf16x2(__uint_as_float(x[2 * j]) * scale_o, __uint_as_float(x[2 * j + 1]) * scale_o);
+                    *reinterpret_cast<uint4*>(op + 16 * c) = make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4*>(op + 16 * c + 8) = make_uint4(y[4], y[5], y[6], y[7]);
                 } else if (mine) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<uint4*>(part + (size_t)local * D + 32 * c + i) =
-                            seen == 0 ? make_uint4(0, 0, 0, 0)
-                                      : make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<uint4*>(part + (size_t)local * D + 16 * c + i) =
+                            make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                 }
                 __syncwarp();                      // before the next collective load
             }
