@@ -177,33 +177,48 @@ __device__ TreeSpot tree_locate(const TreeArgs& a, int c, long long* sh)
     return r;
 }
 
-// A stretch of one item's tiles in a group's range.
-struct TreePiece {
+// A stretch of one item's tiles in a group's range, and the walk over them:
+// start() takes the first, next() moves on (only the first needs a division).
+template <int KT>
+struct TreePieces {
     int n, hk, ctx;
     int tiles, t0, t1;      // the item's tiles, and those of this piece
-};
+    long long left;         // tiles of the range from t0 on
 
-// Takes the next piece of [pos, end) and moves pos and sp behind it.
-template <int KT>
-__device__ __forceinline__ TreePiece tree_next(const TreeArgs& a, TreeSpot& sp, long long& pos,
-                                               long long end)
-{
-    TreePiece w;
-    w.n = sp.n;
-    w.ctx = tree_context(a, w.n);
-    w.tiles = (w.ctx + a.Ts + KT - 1) / KT;
-    const long long at = pos - sp.start;
-    w.hk = (int)(at / w.tiles);
-    w.t0 = (int)(at - (long long)w.hk * w.tiles);
-    const long long left = end - pos;
-    w.t1 = left < w.tiles - w.t0 ? w.t0 + (int)left : w.tiles;
-    pos += w.t1 - w.t0;
-    if (w.t1 == w.tiles && w.hk == a.Hkv - 1) {
-        sp.start += (long long)w.tiles * a.Hkv;
-        ++sp.n;
+    __device__ __forceinline__ void enter(const TreeArgs& a)
+    {
+        ctx = tree_context(a, n);
+        tiles = (ctx + a.Ts + KT - 1) / KT;
     }
-    return w;
-}
+    __device__ __forceinline__ void cut() { t1 = left < tiles - t0 ? t0 + (int)left : tiles; }
+
+    // False when the range is empty.
+    __device__ __forceinline__ bool start(const TreeArgs& a, const TreeSpot& sp, int group)
+    {
+        const long long begin = tree_begin(sp, group);
+        left = tree_begin(sp, group + 1) - begin;
+        if (left <= 0) return false;
+        n = sp.n;
+        enter(a);
+        hk = (int)((begin - sp.start) / tiles);
+        t0 = (int)(begin - sp.start - (long long)hk * tiles);
+        cut();
+        return true;
+    }
+    __device__ __forceinline__ bool next(const TreeArgs& a)
+    {
+        left -= t1 - t0;
+        if (left <= 0) return false;
+        if (++hk == a.Hkv) {
+            hk = 0;
+            ++n;
+            enter(a);
+        }
+        t0 = 0;
+        cut();
+        return true;
+    }
+};
 
 struct TreePlan {
     int rt;                 // rows per row tile

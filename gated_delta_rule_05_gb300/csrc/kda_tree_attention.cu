@@ -62,15 +62,13 @@ tree_attention_simt_kernel(const TreeArgs a)
 
     const int group = blockIdx.x / a.row_tiles, r0 = (blockIdx.x % a.row_tiles) * RT;
     const int rows = a.R - r0 < RT ? a.R - r0 : RT;
-    TreeSpot sp = tree_locate<kSimtThreads, kSimtKeys>(a, group, sh_loc);
-    long long pos = tree_begin(sp, group);
-    const long long end = tree_begin(sp, group + 1);
+    const TreeSpot sp = tree_locate<kSimtThreads, kSimtKeys>(a, group, sh_loc);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int row_elems = a.Hkv * D;
     int have = -1;                                  // the sequence anc[] is of
 
-    while (pos < end) {
-        const TreePiece w = tree_next<kSimtKeys>(a, sp, pos, end);
+    TreePieces<kSimtKeys> w;
+    for (bool more = w.start(a, sp, group); more; more = w.next(a)) {
         const int n = w.n, ctx = w.ctx, tiles = w.tiles, t0 = w.t0, t1 = w.t1, hk = w.hk;
         const int32_t* table = a.page_table + (long long)n * a.max_pages;
         if (have != n) {

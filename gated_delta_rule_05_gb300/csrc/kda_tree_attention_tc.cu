@@ -44,6 +44,7 @@ namespace {
 using namespace sm100;
 
 constexpr int KT = 128;                    // keys per tile
+using Piece = TreePieces<KT>;
 constexpr int kRingMeta = 16;              // tiles whose key masks are kept
 constexpr int kQWarps = 2;                 // warps that copy q
 
@@ -305,7 +306,7 @@ struct Copier {
         const int p = pos / a.page_size;
         return {pos, p, pos - p * a.page_size};
     }
-    __device__ Row look_up(const TreePiece& w, int t, Walk& k) const
+    __device__ Row look_up(const Piece& w, int t, Walk& k) const
     {
         Row r = {-1, k.slot};
         if (t >= w.t1) return r;
@@ -324,7 +325,7 @@ struct Copier {
     __device__ bool cached(const Row& r) const { return r.page >= 0 && r.page < a.num_pages; }
 
     // The row's source in the cache or among the drafted rows (null: none).
-    __device__ const __nv_bfloat16* source(const TreePiece& w, const Row& r, const void* cache,
+    __device__ const __nv_bfloat16* source(const Piece& w, const Row& r, const void* cache,
                                            const void* drafted) const
     {
         const int row_elems = a.Hkv * D;
@@ -337,24 +338,25 @@ struct Copier {
         return nullptr;
     }
 
-    // The warp's 32 rows as boxes of a.box rows and 64 columns, a lane each.
-    __device__ void load_boxes(const CUtensorMap* map, const TreePiece& w, const Row& r)
+    // The warp's 32 rows as boxes of a.box rows and 64 columns.
+    __device__ void load_boxes(const CUtensorMap* map, const Piece& w, const Row& r)
     {
         if (lane == 0) mbar_arrive_expect_tx(full(), 32 * D * 2);
-        __syncwarp();
-        const int nb = 32 / a.box;
-        const int b = lane % nb, half = lane / nb;
-        const int page = __shfl_sync(0xffffffffu, r.page, b * a.box);
-        const int slot = __shfl_sync(0xffffffffu, r.slot, b * a.box);
-        if (half < D / 64)
-            tma_load_4d(entry() + half * (128 * 128) + (warp * 32 + b * a.box) * 128, map, half * 64,
-                        w.hk, slot, page, full());
-        __syncwarp();
+#pragma unroll 1
+        for (int j = 0; j < 32; j += a.box) {
+            const int page = __shfl_sync(0xffffffffu, r.page, j), slot = __shfl_sync(0xffffffffu, r.slot, j);
+            if (lane == 0) {
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h)
+                    tma_load_4d(entry() + h * (128 * 128) + (warp * 32 + j) * 128, map, h * 64, w.hk, slot, page, full());
+            }
+            __syncwarp();
+        }
     }
 
     // The next ring entry: the K or V rows of a piece's tile, the g-th tile of
     // the CTA.
-    __device__ void load(bool is_k, const TreePiece& w, const Row& r, int g)
+    __device__ void load(bool is_k, const Piece& w, const Row& r, int g)
     {
         wait_slot();
         const uint32_t there = __ballot_sync(0xffffffffu, cached(r));
@@ -415,13 +417,12 @@ struct Copier {
 
 template <int D, int NT>
 __device__ void copy_role(TcShared& sh, const TreeArgs& a, const CUtensorMap* map_k, const CUtensorMap* map_v,
-                          uint32_t slots, TreeSpot sp, long long pos, long long end, int warp, int lane)
+                          uint32_t slots, Piece w, bool go, int warp, int lane)
 {
     using Sh = TcShape<D, NT>;
     Copier<D, NT> c{sh, a, map_k, map_v, slots, lane, warp};
     int g = 0;                                     // tiles of the pieces before
-    while (pos < end) {
-        const TreePiece w = tree_next<KT>(a, sp, pos, end);
+    for (; go; go = w.next(a)) {
         const int cnt = w.t1 - w.t0;
         auto walk = c.walk_from(w.t0);
         // the rows of the tile whose V comes next, of the one after it, and of
@@ -451,14 +452,14 @@ __device__ void copy_role(TcShared& sh, const TreeArgs& a, const CUtensorMap* ma
 }
 
 template <int D, int NT>
-__device__ void q_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, TreeSpot sp, long long pos,
-                       long long end, int r0, int warp, int lane)
+__device__ void q_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, Piece w, bool go, int r0,
+                       int warp, int lane)
 {
     int piece = 0;
-    while (pos < end) {
-        const TreePiece w = tree_next<KT>(a, sp, pos, end);
+    for (; go; go = w.next(a)) {
         if (piece > 0) wait(sh, &sh.q_empty, (uint32_t)(piece - 1) & 1, a.status);
         __syncwarp();
+#pragma unroll 1
         for (int b = warp; b < NT * 4; b += kQWarps) {
             const int r = r0 + b * 32 + lane;
             const __nv_bfloat16* p = nullptr;
@@ -479,101 +480,134 @@ __device__ void q_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, TreeSpo
 }
 
 // -------------------------------------------------------------- the products
+// D = Q K^T: K-major operands, d / 16 steps of 32 bytes within 64-column blocks
+// 16 KB apart.  One elected lane issues all steps.
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t q_desc, uint64_t k_desc, uint32_t idesc)
+{
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) {
+        asm volatile(
+            "{\n\t.reg .pred e, t, f;\n\t.reg .b64 x, y;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+            "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+            "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+            "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d_tmem),
+            "l"(q_desc + 1024 * b), "l"(k_desc + 1024 * b), "r"(idesc), "r"(b)
+            : "memory");
+    }
+}
+
+// D (+)= P V: P in TMEM (8 columns of bf16 pairs per step), V MN-major (16 keys of
+// 128 bytes per step).
+__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_t v_desc, uint32_t idesc,
+                                         uint32_t accumulate)
+{
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        asm volatile(
+            "{\n\t.reg .pred e, t, f;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+            "add.s32 x, %1, 8;\n\tadd.s64 y, %2, 128;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+            "add.s32 x, %1, 16;\n\tadd.s64 y, %2, 256;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+            "add.s32 x, %1, 24;\n\tadd.s64 y, %2, 384;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t}" ::"r"(d_tmem),
+            "r"(p_tmem + 32 * b), "l"(v_desc + 512 * b), "r"(idesc), "r"(b ? 1u : accumulate)
+            : "memory");
+    }
+}
+
+// Takes the ring's entries in their order.  RT = 128: the scores of tile j + 1
+// before the output of tile j.  RT = 256: for both row tiles in turn, the output
+// of tile j and the scores of tile j + 1 (which go where tile j's P was: the
+// tensor core runs one thread's products in order).
 template <int D, int NT>
-__device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint32_t slots, TreeSpot sp,
-                         long long pos, long long end, int r0, uint32_t tmem)
+__device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint32_t slots, Piece w, bool go,
+                         int r0, uint32_t tmem)
 {
     using Sh = TcShape<D, NT>;
     constexpr uint32_t id_qk = make_idesc_bf16(128, KT, false, false);
     constexpr uint32_t id_pv = make_idesc_bf16(128, D, false, true);
     int entry = 0;                                 // next ring entry to take
-    int tile = 0, piece = 0;
-    int used[2] = {0, 0};                          // tiles of each row tile so far
-    int pieces[2] = {0, 0};                        // pieces of each row tile so far
+    int first = 0, piece = 0;                      // tiles of the pieces before, pieces
     const int nt = (NT == 2 && a.R - r0 > 128) ? 2 : 1;
+    const uint64_t q_desc = make_sdesc(q_smem, 16, 1024, kSwizzle128B);
 
-    auto take = [&](int e) { wait(sh, &sh.kv_full[e % Sh::kSlots], (uint32_t)(e / Sh::kSlots) & 1, a.status);
-                             fence_proxy_async_smem();   // rows that the lanes copied with cp.async
-                             __syncwarp();
-                             tc_fence_after(); };
+    auto take = [&](int e) {
+        wait(sh, &sh.kv_full[e % Sh::kSlots], (uint32_t)(e / Sh::kSlots) & 1, a.status);
+        fence_proxy_async_smem();                  // rows that the lanes copied with cp.async
+        __syncwarp();
+        tc_fence_after();
+    };
     auto qk = [&](int i, int e, uint32_t d_tmem) {
-        const uint64_t da = make_sdesc(q_smem + i * 128 * D * 2, 16, 1024, kSwizzle128B);
-        const uint64_t db = make_sdesc(slots + (uint32_t)(e % Sh::kSlots) * Sh::kSlotBytes, 16, 1024, kSwizzle128B);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-            const uint64_t off = (uint64_t)((s >> 2) * 1024 + 2 * (s & 3));
-            mma_ss(d_tmem, da + off, db + off, id_qk, s > 0);
-        }
+        const uint32_t k = slots + (uint32_t)(e % Sh::kSlots) * Sh::kSlotBytes;
+        issue_qk<D>(d_tmem, q_desc + (uint64_t)(i * 128 * D * 2 / 16), make_sdesc(k, 16, 1024, kSwizzle128B), id_qk);
     };
-    auto pv = [&](int e, uint32_t p_tmem, uint32_t d_tmem, bool first) {
-        const uint64_t db = make_sdesc(slots + (uint32_t)(e % Sh::kSlots) * Sh::kSlotBytes, KT * 128, 1024, kSwizzle128B);
-#pragma unroll
-        for (int s = 0; s < KT / 16; ++s)
-            mma_ts(d_tmem, p_tmem + s * 8, db + 128 * s, id_pv, !(first && s == 0));
+    // the output of tile `tile`, the j-th of the piece, of row tile i
+    auto pv = [&](int i, int e, int j, int tile, int buf, uint32_t phase) {
+        wait(sh, &sh.p_full[buf], phase, a.status);
+        if (j == 0 && piece > 0) wait(sh, &sh.o_empty[i], (uint32_t)(piece - 1) & 1, a.status);
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t v = slots + (uint32_t)(e % Sh::kSlots) * Sh::kSlotBytes;
+        issue_pv(tmem + (i ? Sh::kO1 : Sh::kO0), tmem + buf * Sh::kS1, make_sdesc(v, KT * 128, 1024, kSwizzle128B),
+                 id_pv, j > 0);
+        mma_commit(&sh.pv_done[i]);
     };
 
-    while (pos < end) {
-        const TreePiece w = tree_next<KT>(a, sp, pos, end);
+    for (; go; go = w.next(a)) {
         const int cnt = w.t1 - w.t0;
         wait(sh, &sh.q_full, (uint32_t)piece & 1, a.status);
-        take(entry);
         if constexpr (NT == 1) {
-            qk(0, entry, tmem + (tile & 1) * Sh::kS1);
-            mma_commit(&sh.s_full[tile & 1]);
-            mma_commit(&sh.kv_empty[entry % Sh::kSlots]);
-            ++entry;
-            if (cnt == 1) mma_commit(&sh.q_empty);
-            for (int j = 0; j < cnt; ++j, ++tile) {
-                if (j + 1 < cnt) {
-                    take(entry);
-                    qk(0, entry, tmem + ((tile + 1) & 1) * Sh::kS1);
-                    mma_commit(&sh.s_full[(tile + 1) & 1]);
-                    mma_commit(&sh.kv_empty[entry % Sh::kSlots]);
-                    ++entry;
-                    if (j + 2 == cnt) mma_commit(&sh.q_empty);
-                }
+            int jk = 0, jv = 0;
+#pragma unroll 1
+            while (jv < cnt) {
                 take(entry);
-                wait(sh, &sh.p_full[tile & 1], (uint32_t)(tile >> 1) & 1, a.status);
-                if (j == 0 && piece > 0) wait(sh, &sh.o_empty[0], (uint32_t)(piece - 1) & 1, a.status);
-                __syncwarp();
-                tc_fence_after();
-                pv(entry, tmem + (tile & 1) * Sh::kS1, tmem + Sh::kO0, j == 0);
-                mma_commit(&sh.pv_done[0]);
+                if (jk < cnt && jk < jv + 2) {
+                    const int t = first + jk;
+                    qk(0, entry, tmem + (t & 1) * Sh::kS1);
+                    mma_commit(&sh.s_full[t & 1]);
+                    if (++jk == cnt) mma_commit(&sh.q_empty);
+                } else {
+                    const int t = first + jv;
+                    pv(0, entry, jv, t, t & 1, (uint32_t)(t >> 1) & 1);
+                    ++jv;
+                }
                 mma_commit(&sh.kv_empty[entry % Sh::kSlots]);
                 ++entry;
             }
         } else {
-            for (int i = 0; i < nt; ++i) {
-                qk(i, entry, tmem + i * Sh::kS1);
-                mma_commit(&sh.s_full[i]);
-            }
-            mma_commit(&sh.kv_empty[entry % Sh::kSlots]);
-            if (cnt == 1) mma_commit(&sh.q_empty);
-            ++entry;
-            for (int j = 0; j < cnt; ++j) {
+#pragma unroll 1
+            for (int j = -1; j < cnt; ++j) {
+                // V of tile j, then K of tile j + 1
+                const int ev = entry, ek = entry + (j >= 0 ? 1 : 0);
                 const bool more = j + 1 < cnt;
-                take(entry);
+                if (j >= 0) take(ev);
+#pragma unroll 1
                 for (int i = 0; i < nt; ++i) {
-                    wait(sh, &sh.p_full[i], (uint32_t)used[i] & 1, a.status);
-                    if (j == 0 && pieces[i] > 0) wait(sh, &sh.o_empty[i], (uint32_t)(pieces[i] - 1) & 1, a.status);
-                    __syncwarp();
-                    tc_fence_after();
-                    pv(entry, tmem + i * Sh::kS1, tmem + (i ? Sh::kO1 : Sh::kO0), j == 0);
-                    mma_commit(&sh.pv_done[i]);
+                    if (j >= 0) pv(i, ev, j, first + j, i, (uint32_t)(first + j) & 1);
                     if (more) {
-                        if (i == 0) take(entry + 1);
-                        qk(i, entry + 1, tmem + i * Sh::kS1);
+                        if (i == 0) take(ek);
+                        qk(i, ek, tmem + i * Sh::kS1);
                         mma_commit(&sh.s_full[i]);
                     }
-                    ++used[i];
                 }
-                mma_commit(&sh.kv_empty[entry % Sh::kSlots]);
-                if (more) mma_commit(&sh.kv_empty[(entry + 1) % Sh::kSlots]);
+                if (j >= 0) mma_commit(&sh.kv_empty[ev % Sh::kSlots]);
+                if (more) mma_commit(&sh.kv_empty[ek % Sh::kSlots]);
                 if (j + 2 == cnt) mma_commit(&sh.q_empty);
-                entry += more ? 2 : 1;
+                entry += (j >= 0 ? 1 : 0) + (more ? 1 : 0);
             }
-            for (int i = 0; i < nt; ++i) ++pieces[i];
         }
+        first += cnt;
         ++piece;
     }
     // the last arrivals on the ring's barriers come before the block ends
@@ -584,8 +618,8 @@ __device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint3
 
 // --------------------------------------------------- the softmax and the output
 template <int D, int NT>
-__device__ void softmax_role(TcShared& sh, const TreeArgs& a, TreeSpot sp, long long pos, long long end,
-                             int r0, int warp, int lane, uint32_t tmem)
+__device__ void softmax_role(TcShared& sh, const TreeArgs& a, Piece w, bool go, int r0, int warp, int lane,
+                             uint32_t tmem)
 {
     using Sh = TcShape<D, NT>;
     constexpr int RT = NT * 128;
@@ -599,10 +633,9 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, TreeSpot sp, long 
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t to = lanes + (wg ? Sh::kO1 : Sh::kO0);
     const int node = (r < a.R ? r : a.R - 1) / a.G;
-    int tile = 0, piece = 0, have = -1;
+    int tile = 0, have = -1;
     unsigned long long seen = 0;
-    while (pos < end) {
-        const TreePiece w = tree_next<KT>(a, sp, pos, end);
+    for (; go; go = w.next(a)) {
         if (have != w.n) {
             seen = tree_mask_of(a.parent ? a.parent + (long long)w.n * a.Ts : nullptr, a.Ts, lane, node);
             have = w.n;
@@ -776,7 +809,6 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, TreeSpot sp, long 
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.o_empty[NT == 1 ? 0 : wg]);
-        ++piece;
     }
 }
 
@@ -818,21 +850,21 @@ tree_attention_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
-    const long long pos = tree_begin(sp, group);
-    const long long end = tree_begin(sp, group + 1);
+    Piece first;
+    const bool go = first.start(a, sp, group);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp < Sh::kCopyWarp) {
         more_registers<Sh::kMore>();
-        softmax_role<D, NT>(sh, a, sp, pos, end, r0, warp, lane, tmem);
+        softmax_role<D, NT>(sh, a, first, go, r0, warp, lane, tmem);
     } else if (warp < Sh::kMmaWarp) {
         fewer_registers<Sh::kFewer>();
-        copy_role<D, NT>(sh, a, &map_k, &map_v, slots, sp, pos, end, warp - Sh::kCopyWarp, lane);
+        copy_role<D, NT>(sh, a, &map_k, &map_v, slots, first, go, warp - Sh::kCopyWarp, lane);
     } else {
         fewer_registers<Sh::kFewer>();
         if (warp == Sh::kMmaWarp)
-            mma_role<D, NT>(sh, a, q_smem, slots, sp, pos, end, r0, tmem);
+            mma_role<D, NT>(sh, a, q_smem, slots, first, go, r0, tmem);
         else if (warp <= Sh::kMmaWarp + kQWarps)
-            q_role<D, NT>(sh, a, q_smem, sp, pos, end, r0, warp - Sh::kMmaWarp - 1, lane);
+            q_role<D, NT>(sh, a, q_smem, first, go, r0, warp - Sh::kMmaWarp - 1, lane);
     }
     tc_fence_before();
     __syncthreads();
