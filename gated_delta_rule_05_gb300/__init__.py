@@ -463,8 +463,30 @@ def kda_state_gather(states, S_in, accept, *, S_out=None, stream=None):
 
 
 def _shape(name, t, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+# The calls below are made once per layer and step, with a few tokens at a time:
+# what they spend on the host counts, so that they pass plain integers and switch
+# the device only where it is another one.
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, device, stream, *args):
+    """lib().<name>(*args, stream) on ``device``; raises KdaError."""
+    torch = _torch()
+    f = getattr(_lib if _lib is not None else lib(), name)
+    raw = stream.cuda_stream if stream is not None else \
+        torch._C._cuda_getCurrentRawStream(device.index)
+    if torch.cuda.current_device() == device.index:
+        rc = f(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, raw)
+    if rc != KDA_OK:
+        raise KdaError(rc, name)
 
 
 def kda_decode_tree(q, k, v, log_alpha, beta, S_in, parent=None, *, o=None, states=None,
@@ -500,12 +522,9 @@ def kda_decode_tree(q, k, v, log_alpha, beta, S_in, parent=None, *, o=None, stat
     _check_cuda("states", states, torch.float32)
     _shape("o", o, (N, Ts, H, dv))
     _shape("states", states, (N, Ts, H, dk, dv))
-    with torch.cuda.device(q.device):
-        rc = lib().kda_decode_tree(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(S_in), _ptr(parent),
-            N, Ts, H, dk, dv, dt, _ptr(o), _ptr(states), _stream_handle(stream, q.device))
-    if rc != KDA_OK:
-        raise KdaError(rc, "kda_decode_tree")
+    _call("kda_decode_tree", q.device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_alpha.data_ptr(), beta.data_ptr(), S_in.data_ptr(), _address(parent), N, Ts, H, dk,
+          dv, dt, o.data_ptr(), states.data_ptr())
     return o, states
 
 
@@ -563,19 +582,19 @@ def kda_tree_attention(q, k, v, k_cache, v_cache, page_table, lengths, parent=No
         o = torch.empty((N, Ts, Hq, d), dtype=o_dtype, device=dev)
     _check_cuda("o", o, o_dtype)
     _shape("o", o, (N, Ts, Hq, d))
-    with torch.cuda.device(dev):
-        if workspace is None:
+    if workspace is None:
+        if torch.cuda.current_device() == dev.index:
             need = lib().kda_tree_attention_workspace_bytes(N, Ts, Hq, Hkv, d, dt)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        _check_cuda("workspace", workspace)
-        rc = lib().kda_tree_attention(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(parent), _ptr(k_cache), _ptr(v_cache),
-            _ptr(page_table), _ptr(lengths), N, Ts, Hq, Hkv, d, pages, page,
-            page_table.shape[1], k_cache.stride(0), dt, d ** -0.5 if scale is None else scale,
-            _ptr(o), _ptr(workspace), workspace.numel() * workspace.element_size(),
-            _stream_handle(stream, dev))
-    if rc != KDA_OK:
-        raise KdaError(rc, "kda_tree_attention")
+        else:
+            with torch.cuda.device(dev):
+                need = lib().kda_tree_attention_workspace_bytes(N, Ts, Hq, Hkv, d, dt)
+        workspace = torch.empty(need or 256, dtype=torch.uint8, device=dev)
+    _check_cuda("workspace", workspace)
+    _call("kda_tree_attention", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          _address(parent), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+          lengths.data_ptr(), N, Ts, Hq, Hkv, d, pages, page, page_table.shape[1],
+          k_cache.stride(0), dt, d ** -0.5 if scale is None else scale, o.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return o
 
 
@@ -610,17 +629,14 @@ def kda_token_logprobs(logits, tokens=None, num_top=0, *, logprobs=None, entropy
         if K >= 0:
             _shape(name, t, shape)
         _check_cuda(name, t, torch.int32 if name == "top_ids" else torch.float32)
-    with torch.cuda.device(dev):
-        rc = lib().kda_token_logprobs(
-            _ptr(logits), max(logits.stride(0), V) if T == 1 else logits.stride(0), _ptr(tokens),
-            T, V, J, K, dt, _ptr(logprobs), _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs),
-            _stream_handle(stream, dev))
-    if rc != KDA_OK:
-        raise KdaError(rc, "kda_token_logprobs")
+    _call("kda_token_logprobs", dev, stream, logits.data_ptr(),
+          max(logits.stride(0), V) if T == 1 else logits.stride(0), _address(tokens), T, V, J, K,
+          dt, logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(),
+          top_logprobs.data_ptr())
     return logprobs, entropy, top_ids, top_logprobs
 
 
-def _cache_rows(call, name, k, v, middle, k_cache, v_cache, page_table, lengths, new_lengths,
+def _cache_rows(name, k, v, middle, k_cache, v_cache, page_table, lengths, new_lengths,
                 counts, stream):
     """The part that kda_cache_commit and kda_cache_append share: checks, and
     the call with ``middle`` between k, v and the page table."""
@@ -646,13 +662,10 @@ def _cache_rows(call, name, k, v, middle, k_cache, v_cache, page_table, lengths,
         new_lengths = torch.empty_like(lengths)
     _check_cuda("new_lengths", new_lengths, torch.int32)
     _shape("new_lengths", new_lengths, (N,))
-    with torch.cuda.device(dev):
-        rc = call(_ptr(k), _ptr(v), *middle, _ptr(page_table), _ptr(lengths), layers, N, *counts,
-                  Hkv, d, k_cache.shape[1], k_cache.shape[2], page_table.shape[1],
-                  k_cache.stride(1), k_cache.stride(0), dt, _ptr(k_cache), _ptr(v_cache),
-                  _ptr(new_lengths), _stream_handle(stream, dev))
-    if rc != KDA_OK:
-        raise KdaError(rc, name)
+    _call(name, dev, stream, k.data_ptr(), v.data_ptr(), *middle, page_table.data_ptr(),
+          lengths.data_ptr(), layers, N, *counts, Hkv, d, k_cache.shape[1], k_cache.shape[2],
+          page_table.shape[1], k_cache.stride(1), k_cache.stride(0), dt, k_cache.data_ptr(),
+          v_cache.data_ptr(), new_lengths.data_ptr())
     return new_lengths
 
 
@@ -675,8 +688,8 @@ def kda_cache_commit(k, v, path, count, k_cache, v_cache, page_table, lengths, *
     if count is not None:
         _shape("count", count, (N,))
     _shape("lengths", lengths, (N,))
-    return _cache_rows(lib().kda_cache_commit, "kda_cache_commit", k, v, (_ptr(path), _ptr(count)),
-                       k_cache, v_cache, page_table, lengths, new_lengths, (Ts,), stream)
+    return _cache_rows("kda_cache_commit", k, v, (_address(path), _address(count)), k_cache,
+                        v_cache, page_table, lengths, new_lengths, (Ts,), stream)
 
 
 def kda_cache_append(k, v, cu_seqlens, k_cache, v_cache, page_table, lengths, *,
@@ -688,8 +701,8 @@ def kda_cache_append(k, v, cu_seqlens, k_cache, v_cache, page_table, lengths, *,
     _, T, _, _ = k.shape
     _check_cuda("cu_seqlens", cu_seqlens, torch.int32)
     _shape("lengths", lengths, (cu_seqlens.shape[0] - 1,))
-    return _cache_rows(lib().kda_cache_append, "kda_cache_append", k, v, (_ptr(cu_seqlens), T),
-                       k_cache, v_cache, page_table, lengths, new_lengths, (), stream)
+    return _cache_rows("kda_cache_append", k, v, (cu_seqlens.data_ptr(), T), k_cache,
+                        v_cache, page_table, lengths, new_lengths, (), stream)
 
 
 def kda_prefill_fused(q, k, v, z, A, beta, S0=None, cu_seqlens=None, *, q_scale, o=None,
