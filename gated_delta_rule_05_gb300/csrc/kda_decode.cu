@@ -21,12 +21,6 @@
 // state once, applies Ts steps to it in registers and writes each step's state
 // to its own slot; the one-token decode is the case Ts = 1 written in place.
 //
-// A tree of drafted tokens: node t continues from the state after its parent
-// node instead of from token t - 1 (parent -1: from S_in).  The state stays in
-// registers along a chain; where a node's parent is not the node before it,
-// each thread reads back the elements that it wrote itself (or S_in's).  A node
-// whose chain of parents does not end at S_in is unused: o = 0, no state.
-//
 // With the gate prologue (A not null; "[논문 리뷰] Kimi K3 Technical Report",
 // section 3.5) the log_alpha input is the gate pre-activation z,
 // g = -5 sigmoid(e^A z), and q, k are L2-normalised in the kernel: the sums
@@ -61,13 +55,13 @@ struct DecodeShape {
 // after token t of (n, h) goes to S_out + ((n Ts + t) H + h) d_k d_v (for
 // Ts = 1 this is S_in's own layout, so the one-token decode passes
 // S_out = S_in).
-template <typename TI, typename TO, int DK, int DVS, int THREADS, bool TREE>
+template <typename TI, typename TO, int DK, int DVS, int THREADS>
 __global__ void __launch_bounds__(THREADS)
 decode_kernel(const TI* __restrict__ q, const TI* __restrict__ k,
               const TI* __restrict__ v, const float* __restrict__ log_alpha,
               const float* __restrict__ beta, const float* S_in, float* S_out,
               TO* __restrict__ o, int dv, int Ts, int H, const float* __restrict__ gateA,
-              float q_scale, const int32_t* __restrict__ parent)
+              float q_scale)
 {
     using Sh = DecodeShape<DK, DVS, THREADS>;
     constexpr int LPR = Sh::kLanesPerRow;
@@ -102,26 +96,9 @@ decode_kernel(const TI* __restrict__ q, const TI* __restrict__ k,
     const bool fused = gateA != nullptr;
     const float eA = (fused && tid < DK) ? expf(gateA[h * DK + tid]) : 0.f;
 
-    unsigned long long used = 0;              // TREE: nodes whose chain ends at S_in
-    int at = -1;                              // TREE: the node whose state s[] holds
     for (int t = 0; t < Ts; ++t) {
         const long long tok = (n * Ts + t) * H + h;       // token row of this (n, t, h)
         float* Sq = S_out + tok * (long long)DK * dv;
-        if constexpr (TREE) {
-            const int p = parent[n * Ts + t];             // the same for the whole block
-            if (p != -1 && (p < 0 || p >= t || !((used >> p) & 1ull))) {
-                if (tid < DVS) st_f(o + tok * dv + slab * DVS + tid, 0.f);
-                continue;
-            }
-            used |= 1ull << t;
-            if (p != at) {
-                const float* Sr = p < 0 ? Sp : S_out + ((n * Ts + p) * H + h) * (long long)DK * dv;
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    s[r] = *reinterpret_cast<const float4*>(Sr + (long long)(rg + r * RPP) * dv + col);
-            }
-            at = t;
-        }
         if (t > 0) __syncthreads();                        // the previous token's reads are done
 
         // 2. Token inputs: alpha, k, alpha.*k, alpha.*q and the partial k.q.
@@ -256,7 +233,7 @@ template <typename TI, typename TO, int D>
 cudaError_t launch_typed(const void* q, const void* k, const void* v,
                          const float* g, const float* beta, const float* S_in, float* S_out,
                          int32_t N, int32_t Ts, int32_t H, void* o, const GateArgs& gate,
-                         const int32_t* parent, cudaStream_t stream)
+                         cudaStream_t stream)
 {
     // Slab widths and thread counts: 32 KiB of state per CTA at d = 128
     // (8 float4 per thread), one warp-row pattern per smaller head size.
@@ -265,11 +242,9 @@ cudaError_t launch_typed(const void* q, const void* k, const void* v,
     const long long blocks = (long long)N * H * (D / DVS);
     if (blocks <= 0) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    auto kern = parent ? decode_kernel<TI, TO, D, DVS, THREADS, true>
-                       : decode_kernel<TI, TO, D, DVS, THREADS, false>;
-    kern<<<(unsigned)blocks, THREADS, 0, stream>>>(
+    decode_kernel<TI, TO, D, DVS, THREADS><<<(unsigned)blocks, THREADS, 0, stream>>>(
         static_cast<const TI*>(q), static_cast<const TI*>(k), static_cast<const TI*>(v),
-        g, beta, S_in, S_out, static_cast<TO*>(o), D, Ts, H, gate.A, gate.q_scale, parent);
+        g, beta, S_in, S_out, static_cast<TO*>(o), D, Ts, H, gate.A, gate.q_scale);
     return cudaGetLastError();
 }
 
@@ -277,13 +252,13 @@ template <typename TI, typename TO>
 cudaError_t launch_d(int32_t d, const void* q, const void* k, const void* v,
                      const float* g, const float* beta, const float* S_in, float* S_out,
                      int32_t N, int32_t Ts, int32_t H, void* o, const GateArgs& gate,
-                     const int32_t* parent, cudaStream_t stream)
+                     cudaStream_t stream)
 {
     switch (d) {
-        case 16: return launch_typed<TI, TO, 16>(q, k, v, g, beta, S_in, S_out, N, Ts, H, o, gate, parent, stream);
-        case 32: return launch_typed<TI, TO, 32>(q, k, v, g, beta, S_in, S_out, N, Ts, H, o, gate, parent, stream);
-        case 64: return launch_typed<TI, TO, 64>(q, k, v, g, beta, S_in, S_out, N, Ts, H, o, gate, parent, stream);
-        case 128: return launch_typed<TI, TO, 128>(q, k, v, g, beta, S_in, S_out, N, Ts, H, o, gate, parent, stream);
+        case 16: return launch_typed<TI, TO, 16>(q, k, v, g, beta, S_in, S_out, N, Ts, H, o, gate, stream);
+        case 32: return launch_typed<TI, TO, 32>(q, k, v, g, beta, S_in, S_out, N, Ts, H, o, gate, stream);
+        case 64: return launch_typed<TI, TO, 64>(q, k, v, g, beta, S_in, S_out, N, Ts, H, o, gate, stream);
+        case 128: return launch_typed<TI, TO, 128>(q, k, v, g, beta, S_in, S_out, N, Ts, H, o, gate, stream);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -291,18 +266,18 @@ cudaError_t launch_d(int32_t d, const void* q, const void* k, const void* v,
 cudaError_t launch_multi(const void* q, const void* k, const void* v, const float* log_alpha,
                          const float* beta, const float* S_in, float* S_out, int32_t N,
                          int32_t Ts, int32_t H, int32_t d, kda_dtype_t dtype, void* o,
-                         const GateArgs& gate, const int32_t* parent, cudaStream_t stream)
+                         const GateArgs& gate, cudaStream_t stream)
 {
     switch (dtype) {
         case KDA_BF16:
             return launch_d<__nv_bfloat16, __nv_bfloat16>(d, q, k, v, log_alpha, beta, S_in, S_out,
-                                                          N, Ts, H, o, gate, parent, stream);
+                                                          N, Ts, H, o, gate, stream);
         case KDA_BF16_F32OUT:
             return launch_d<__nv_bfloat16, float>(d, q, k, v, log_alpha, beta, S_in, S_out, N, Ts,
-                                                  H, o, gate, parent, stream);
+                                                  H, o, gate, stream);
         default:
             return launch_d<float, float>(d, q, k, v, log_alpha, beta, S_in, S_out, N, Ts, H, o,
-                                          gate, parent, stream);
+                                          gate, stream);
     }
 }
 
@@ -313,7 +288,7 @@ cudaError_t launch_decode(const void* q, const void* k, const void* v,
                           int32_t N, int32_t H, int32_t d, kda_dtype_t dtype,
                           void* o, const GateArgs& gate, cudaStream_t stream)
 {
-    return launch_multi(q, k, v, log_alpha, beta, S, S, N, 1, H, d, dtype, o, gate, nullptr, stream);
+    return launch_multi(q, k, v, log_alpha, beta, S, S, N, 1, H, d, dtype, o, gate, stream);
 }
 
 cudaError_t launch_decode_multi(const void* q, const void* k, const void* v,
@@ -323,17 +298,7 @@ cudaError_t launch_decode_multi(const void* q, const void* k, const void* v,
                                 cudaStream_t stream)
 {
     return launch_multi(q, k, v, log_alpha, beta, S_in, states, N, Ts, H, d, dtype, o, gate,
-                        nullptr, stream);
-}
-
-cudaError_t launch_decode_tree(const void* q, const void* k, const void* v,
-                               const float* log_alpha, const float* beta, const float* S_in,
-                               const int32_t* parent, float* states, int32_t N, int32_t Ts,
-                               int32_t H, int32_t d, kda_dtype_t dtype, void* o,
-                               cudaStream_t stream)
-{
-    return launch_multi(q, k, v, log_alpha, beta, S_in, states, N, Ts, H, d, dtype, o,
-                        GateArgs{nullptr, 1.f}, parent, stream);
+                        stream);
 }
 
 cudaError_t launch_state_gather(const float* states, const float* S_in, const int32_t* accept,
