@@ -3,8 +3,9 @@
 //
 // Work split.  An item is one (sequence, cache head); its keys, the L rows of the
 // context and after them the Ts drafted nodes, come in ceil((L + Ts) / KT) tiles
-// of KT.  Laid end to end in (sequence, head, tile) order, the tiles are cut
-// into equal ranges, one per group of CTAs, whatever the lengths are; the
+// of KT.  An item costs its tiles and LEAD more, for what its start and end take.
+// Laid end to end in (sequence, head, tile) order, the costs are cut into equal
+// ranges, one per group of CTAs, whatever the lengths are; the
 // lengths stay on the device and every CTA finds its own range from them.  The
 // CTAs of a group have one row tile (up to RT of the item's Ts G query rows)
 // each and walk the same keys side by side, so that all but one find them in
@@ -19,6 +20,8 @@
 namespace kda {
 
 constexpr int kTreeMaxNodes = 64;     // one bit per node in a 64-bit mask
+constexpr int kTcKeys = 128;          // the tensor-core kernel's KT and LEAD
+constexpr int kTcLead = 8;
 
 struct TreeArgs {
     const void *q, *k, *v;
@@ -42,18 +45,6 @@ __device__ __forceinline__ int tree_context(const TreeArgs& a, int n)
     const long long most = (long long)a.max_pages * a.page_size;
     const int len = __ldg(a.lengths + n);
     return len < 0 ? 0 : (int)(len < most ? len : most);
-}
-
-// The row of the flattened cache [num_pages * page_size] that holds position
-// `pos` of sequence n as an element offset of (page, slot), or -1 when its
-// page table entry names no page.
-__device__ __forceinline__ long long tree_cache_row(const TreeArgs& a, const int32_t* table, int pos,
-                                                    int row_elems)
-{
-    const int p = pos / a.page_size;
-    const int page = __ldg(table + p);
-    if (page < 0 || page >= a.num_pages) return -1;
-    return (long long)page * a.page_stride + (long long)(pos - p * a.page_size) * row_elems;
 }
 
 // anc[t]: bit j set when node j is t or an ancestor of t; 0 when t is unused
@@ -97,39 +88,45 @@ __device__ __forceinline__ void tree_masks(const int32_t* parent, int Ts, int la
     __syncwarp();
 }
 
-// Where a group's range begins in the flattened tile order.
+// Where a group's range begins in the flattened order, in units of a tile's cost.
 struct TreeSpot {
-    long long total;        // tiles of the whole launch
-    long long per, more;    // each group has `per` tiles, the first `more` one more
-    long long start;        // first tile of sequence n
+    long long total;        // of the whole launch
+    long long per, more;    // each group has `per` units, the first `more` one more
+    long long start;        // where sequence n begins
     int n;
 };
 
 template <int KT>
-__device__ __forceinline__ long long tree_seq_tiles(const TreeArgs& a, int n)
+__device__ __forceinline__ int tree_tiles(const TreeArgs& a, int n)
 {
     return (tree_context(a, n) + a.Ts + KT - 1) / KT;
 }
 
-// First tile of group c's range.
+template <int KT, int LEAD>
+__device__ __forceinline__ long long tree_cost(const TreeArgs& a, int n)
+{
+    return (long long)(tree_tiles<KT>(a, n) + LEAD) * a.Hkv;
+}
+
+// Where group c's range begins.
 __device__ __forceinline__ long long tree_begin(const TreeSpot& sp, int c)
 {
     return sp.per * c + (c < sp.more ? c : sp.more);
 }
 
-// The sequence that holds the first tile of group c's range (c < groups).  All
+// The sequence that group c's range begins in (c < groups).  All
 // THREADS threads of the block call it; `sh` is shared scratch of THREADS / 32 +
 // 2 words.  With up to THREADS sequences the lengths are read once.
-template <int THREADS, int KT>
+template <int THREADS, int KT, int LEAD>
 __device__ TreeSpot tree_locate(const TreeArgs& a, int c, long long* sh)
 {
     constexpr int W = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     TreeSpot r;
-    long long mine = 0;                             // the first THREADS sequences' tiles
-    if (tid < a.N) mine = tree_seq_tiles<KT>(a, tid) * a.Hkv;
+    long long mine = 0;                             // the first THREADS sequences' costs
+    if (tid < a.N) mine = tree_cost<KT, LEAD>(a, tid);
     long long rest = 0;
-    for (int n = tid + THREADS; n < a.N; n += THREADS) rest += tree_seq_tiles<KT>(a, n) * a.Hkv;
+    for (int n = tid + THREADS; n < a.N; n += THREADS) rest += tree_cost<KT, LEAD>(a, n);
     if (a.N > THREADS) {
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, off);
@@ -143,7 +140,7 @@ __device__ TreeSpot tree_locate(const TreeArgs& a, int c, long long* sh)
     long long base = 0, at = 0;
     for (int n0 = 0; n0 < a.N; n0 += THREADS) {
         const int n = n0 + tid;
-        const long long w = n0 == 0 ? mine : (n < a.N ? tree_seq_tiles<KT>(a, n) * a.Hkv : 0);
+        const long long w = n0 == 0 ? mine : (n < a.N ? tree_cost<KT, LEAD>(a, n) : 0);
         long long incl = w;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -179,20 +176,28 @@ __device__ TreeSpot tree_locate(const TreeArgs& a, int c, long long* sh)
 
 // A stretch of one item's tiles in a group's range, and the walk over them:
 // start() takes the first, next() moves on (only the first needs a division).
-template <int KT>
+template <int KT, int LEAD>
 struct TreePieces {
     int n, hk, ctx;
     int tiles, t0, t1;      // the item's tiles, and those of this piece
-    long long left;         // tiles of the range from t0 on
+    long long left;         // of the range, from the item's part of it on
 
     __device__ __forceinline__ void enter(const TreeArgs& a)
     {
         ctx = tree_context(a, n);
         tiles = (ctx + a.Ts + KT - 1) / KT;
     }
-    __device__ __forceinline__ void cut() { t1 = left < tiles - t0 ? t0 + (int)left : tiles; }
+    // The piece of an item of which the first `skip` units lie before the range.
+    __device__ __forceinline__ bool cut(long long skip)
+    {
+        t0 = skip > LEAD ? (int)(skip - LEAD) : 0;
+        const long long end = skip + left - LEAD;
+        t1 = end < tiles ? (int)end : tiles;
+        left -= tiles + LEAD - skip;
+        return t1 > t0;
+    }
 
-    // False when the range is empty.
+    // False when the range has no tile.
     __device__ __forceinline__ bool start(const TreeArgs& a, const TreeSpot& sp, int group)
     {
         const long long begin = tree_begin(sp, group);
@@ -200,23 +205,19 @@ struct TreePieces {
         if (left <= 0) return false;
         n = sp.n;
         enter(a);
-        hk = (int)((begin - sp.start) / tiles);
-        t0 = (int)(begin - sp.start - (long long)hk * tiles);
-        cut();
-        return true;
+        hk = (int)((begin - sp.start) / (tiles + LEAD));
+        // a range that begins in an item's lead and ends there has no tile
+        return cut(begin - sp.start - (long long)hk * (tiles + LEAD));
     }
     __device__ __forceinline__ bool next(const TreeArgs& a)
     {
-        left -= t1 - t0;
         if (left <= 0) return false;
         if (++hk == a.Hkv) {
             hk = 0;
             ++n;
             enter(a);
         }
-        t0 = 0;
-        cut();
-        return true;
+        return cut(0);
     }
 };
 

@@ -13,15 +13,391 @@
 namespace kda {
 namespace {
 
-constexpr int kSimtThreads = 128;
-constexpr int kSimtKeys = 64;        // keys per tile (a drafted tree fits one)
+// The CUDA-core kernels: fp32, bf16 with small heads or fp32 output, scales that
+// are not positive.
 
-template <int D, int RT>
-struct SimtShape {
-    static constexpr int kLdk = D + 4;
-    static constexpr int kLdp = kSimtKeys + 4;
+// Pairs of fp32 for the two-wide FMA.
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Eight consecutive values (16-byte pieces x, the next one `next` pieces on) as
+// four pairs of fp32.
+__device__ __forceinline__ void pairs8(const float*, const uint4* p, int next, uint64_t (&x)[4])
+{
+    const uint4 a = p[0], b = p[next];
+    x[0] = (uint64_t)a.y << 32 | a.x;
+    x[1] = (uint64_t)a.w << 32 | a.z;
+    x[2] = (uint64_t)b.y << 32 | b.x;
+    x[3] = (uint64_t)b.w << 32 | b.z;
+}
+__device__ __forceinline__ void pairs8(const __nv_bfloat16*, const uint4* p, int, uint64_t (&x)[4])
+{
+    const uint4 a = p[0];
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = (uint64_t)(w[i] & 0xFFFF0000u) << 32 | (w[i] << 16);
+}
+
+// 16 bytes to shared memory, asynchronously; zeros when src is null.
+__device__ __forceinline__ void copy16(void* dst, const void* src, const void* any)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.eq.u64 p, %1, 0;\n\t"
+        "cp.async.cg.shared.global [%0], [%2], 16, p;\n\t}" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+        "l"(src), "l"(src ? src : any)
+        : "memory");
+}
+
+// Up to 8 query rows per cache head: a stream.  D / 8 lanes share a key, eight
+// channels each, and the groups of a CTA take keys in turn: a lane has its eight
+// channels of q and of the output for all eight rows in registers.  Its pieces
+// of K and V come by cp.async through kAhead stages of shared memory that no
+// other lane touches, page numbers two steps earlier still.  The scores of a key
+// are added up across its lanes so that each lane ends with the rows it owns
+// (halving the rows at every step of the butterfly), takes their exponentials,
+// and the probabilities go back to all lanes.  Every group has its own running
+// maximum and sum per owned row (a maximum moves when a score exceeds it by more
+// than 8, in base 2); they meet at the end of a piece.  Nothing in the loop
+// waits for another warp.
+constexpr int kAhead = 4;            // stages of two keys
+constexpr int kStreamRows = 8;
+constexpr int kStreamThreads = 128;
+constexpr int kStreamKeys = 64;      // keys per tile of the work split
+constexpr int kStreamLead = 2;
+constexpr int kStreamCtas = 2;       // per SM: registers
+
+template <typename TI, typename TO, int D>
+__global__ void __launch_bounds__(kStreamThreads, kStreamCtas)
+tree_attention_stream_kernel(const TreeArgs a)
+{
+    constexpr int RT = kStreamRows, LK = D / 8, GW = 32 / LK;     // lanes per key, groups per warp
+    constexpr int kWarps = kStreamThreads / 32, kStep = kWarps * GW;
+    constexpr int RO = RT / LK > 0 ? RT / LK : 1;               // rows a lane owns
+    constexpr float kSlack = 8.f;
+    __shared__ long long sh_loc[kWarps + 2];
+    __shared__ unsigned long long anc[kTreeMaxNodes];
+    __shared__ int32_t up[kTreeMaxNodes];
+    __shared__ float sh_m[kWarps][RT], sh_l[kWarps][RT];
+    __shared__ __align__(16) float sh_o[kWarps][RT][D];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane % LK, sub = lane / LK;                   // lane of the group, group of the warp
+    // the first row this lane owns; lanes g and g ^ 1 share it when LK > RT
+    const int own = LK >= RT ? g / (LK / RT) : g * RO;
+    const TI* q = static_cast<const TI*>(a.q);
+    constexpr int PC = sizeof(TI) / 2, VR = 16 / (int)sizeof(TI);   // 16-byte pieces of eight values, values of one
+    extern __shared__ __align__(16) uint4 ring[];               // [kAhead][2 keys][K, V][PC][threads]
+
+    const int group = blockIdx.x / a.row_tiles, r0 = (blockIdx.x % a.row_tiles) * RT;
+    const int rows = a.R - r0 < RT ? a.R - r0 : RT;
+    const TreeSpot sp = tree_locate<kStreamThreads, kStreamKeys, kStreamLead>(a, group, sh_loc);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int row_elems = a.Hkv * D;
+    const int step_pages = kStep / a.page_size, step_rows = kStep % a.page_size;
+    int have = -1;                                  // the sequence anc[] is of
+
+    TreePieces<kStreamKeys, kStreamLead> w;
+    for (bool more = w.start(a, sp, group); more; more = w.next(a)) {
+        const int n = w.n, ctx = w.ctx, hk = w.hk;
+        const int keys_end = w.t1 == w.tiles ? ctx + a.Ts : w.t1 * kStreamKeys;
+        const int32_t* table = a.page_table + (long long)n * a.max_pages;
+        __syncthreads();                            // the last piece's shared arrays have been read
+        if (have != n) {
+            if (tid < 32)
+                tree_masks(a.parent ? a.parent + (long long)n * a.Ts : nullptr, a.Ts, tid, anc, up);
+            have = n;
+        }
+        // q, scaled, eight channels of every row
+        uint64_t qr[RT][4], acc[RT][4];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qr[r][i] = acc[r][i] = 0;
+            if (r < rows) {
+                const int t = (r0 + r) / a.G, h = (r0 + r) % a.G;
+                const TI* from = q + (((long long)n * a.Ts + t) * a.Hq + hk * a.G + h) * D + 8 * g;
+                pairs8(q, reinterpret_cast<const uint4*>(from), 1, qr[r]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qr[r][i] = mul2(qr[r][i], pack2(a.scale_log2, a.scale_log2));
+            }
+        }
+        __syncthreads();
+        unsigned long long seen[RO];
+        float m[RO], l[RO];
+#pragma unroll
+        for (int i = 0; i < RO; ++i) {
+            seen[i] = own + i < rows ? anc[(r0 + own + i) / a.G] : 0ull;
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+        }
+        // This group's keys: pos, pos + kStep, ..., two at a time; at, in: the next
+        // position to fetch and the next to look up.
+        int pos = w.t0 * kStreamKeys + warp * GW + sub, at = pos;
+        int in = pos, in_p = pos / a.page_size, in_slot = pos - in_p * a.page_size;
+        int page[2], slot[2];
+        auto look = [&]() {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                page[i] = -1;
+                slot[i] = in_slot;
+                if (in < ctx && in < keys_end) page[i] = __ldg(table + in_p);
+                in += kStep;
+                in_p += step_pages;
+                in_slot += step_rows;
+                if (in_slot >= a.page_size) {
+                    in_slot -= a.page_size;
+                    ++in_p;
+                }
+            }
+        };
+        unsigned there = 0;                         // bit 2 s + i: key i of stage s exists
+        auto fetch = [&](int stage) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const TI *kp = nullptr, *vp = nullptr;
+                long long off = (long long)hk * D + 8 * g;
+                if (page[i] >= 0 && page[i] < a.num_pages) {
+                    off += (long long)page[i] * a.page_stride + (long long)slot[i] * row_elems;
+                    kp = static_cast<const TI*>(a.k_cache) + off;
+                    vp = static_cast<const TI*>(a.v_cache) + off;
+                } else if (at >= ctx && at < keys_end) {
+                    off += ((long long)n * a.Ts + at - ctx) * row_elems;
+                    kp = static_cast<const TI*>(a.k) + off;
+                    vp = static_cast<const TI*>(a.v) + off;
+                }
+                const int bit = 2 * stage + i;
+                there = (there & ~(1u << bit)) | ((unsigned)(kp != nullptr) << bit);
+                uint4* to = ring + (bit * 2 * PC) * kStreamThreads + tid;
+#pragma unroll
+                for (int c = 0; c < PC; ++c) {
+                    copy16(to + c * kStreamThreads, kp ? kp + c * VR : nullptr, q);
+                    copy16(to + (PC + c) * kStreamThreads, vp ? vp + c * VR : nullptr, q);
+                }
+                at += kStep;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        look();
+#pragma unroll 1
+        for (int i = 0; i < kAhead - 1; ++i) {
+            fetch(i);
+            look();
+        }
+        const int steps = (keys_end - w.t0 * kStreamKeys + 2 * kStep - 1) / (2 * kStep);
+        int stage = 0;
+#pragma unroll 1
+        for (int step = 0; step < steps; ++step) {
+            // the stage used in the step before takes the next keys
+            fetch(stage ? stage - 1 : kAhead - 1);
+            look();
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            const uint4* mine = ring + (stage * 4 * PC) * kStreamThreads + tid;
+            // the scores of this group's keys: partial sums of all rows
+            float s[2][RT];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint64_t x[4];
+                pairs8(q, mine + u * 2 * PC * kStreamThreads, kStreamThreads, x);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    uint64_t t = mul2(qr[r][0], x[0]);
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) t = fma2(qr[r][i], x[i], t);
+                    const float2 y = unpack2(t);
+                    s[u][r] = y.x + y.y;
+                }
+            }
+            // across the group's lanes, each keeping half of the rows
+            int cnt = RT;
+#pragma unroll
+            for (int off = LK / 2; off > 0; off /= 2) {
+                if (cnt > 1) {
+                    cnt /= 2;
+                    const bool up_half = g & off;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int r = 0; r < cnt; ++r) {
+                            const float give = up_half ? s[u][r] : s[u][r + cnt];
+                            const float keep = up_half ? s[u][r + cnt] : s[u][r];
+                            s[u][r] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+                        }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) s[u][0] += __shfl_xor_sync(0xffffffffu, s[u][0], off);
+                }
+            }
+            const int node = pos - ctx;             // of the first key; the second's is kStep on
+            bool grow = false;
+            float top[RO];
+#pragma unroll
+            for (int i = 0; i < RO; ++i) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int nd = node + u * kStep;
+                    const bool see = ((there >> (2 * stage + u)) & 1) &&
+                                     (nd < 0 ? seen[i] != 0ull : ((seen[i] >> (nd & 63)) & 1ull));
+                    if (!see) s[u][i] = -INFINITY;
+                }
+                top[i] = fmaxf(s[0][i], s[1][i]);
+                grow = grow || top[i] > m[i] + kSlack || (m[i] == -INFINITY && top[i] > m[i]);
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+                float f[RO];
+#pragma unroll
+                for (int i = 0; i < RO; ++i) {
+                    const bool up_m = top[i] > m[i] + kSlack || (m[i] == -INFINITY && top[i] > m[i]);
+                    f[i] = up_m ? exp2f(m[i] - top[i]) : 1.f;
+                    if (up_m) m[i] = top[i];
+                    l[i] *= f[i];
+                }
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const int from = LK >= RT ? r * (LK / RT) : r / RO;
+                    const float fr = __shfl_sync(0xffffffffu, f[r % RO], (lane & ~(LK - 1)) + from);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[r][i] = mul2(acc[r][i], pack2(fr, fr));
+                }
+            }
+            float p[2][RO];
+#pragma unroll
+            for (int i = 0; i < RO; ++i)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    p[u][i] = exp2f(s[u][i] - (m[i] == -INFINITY ? 0.f : m[i]));
+                    l[i] += p[u][i];
+                }
+            const bool tail = __any_sync(0xffffffffu, node + kStep >= 0);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint64_t x[4];
+                pairs8(q, mine + (u * 2 + 1) * PC * kStreamThreads, kStreamThreads, x);
+                const int nd = node + u * kStep;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const int from = LK >= RT ? r * (LK / RT) : r / RO;
+                    const float pr = __shfl_sync(0xffffffffu, p[u][r % RO], (lane & ~(LK - 1)) + from);
+                    // a node that row r does not see may hold inf or NaN: 0 * v would keep it
+                    if (tail && nd >= 0 && !(r < rows && nd < a.Ts && ((anc[(r0 + r) / a.G] >> nd) & 1ull)))
+                        continue;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[r][i] = fma2(pack2(pr, pr), x[i], acc[r][i]);
+                }
+            }
+            pos += 2 * kStep;
+            if (++stage == kAhead) stage = 0;
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");   // the stages are free
+        // The groups' maxima, sums and outputs meet: in the warp, then in the CTA.
+        float top[RO], sum[RO];
+#pragma unroll
+        for (int i = 0; i < RO; ++i) {
+            top[i] = m[i];
+#pragma unroll
+            for (int off = LK; off < 32; off <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], off));
+            if (sub == 0) sh_m[warp][own + i] = top[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < RO; ++i) {
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) top[i] = fmaxf(top[i], sh_m[k][own + i]);
+            const float f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - top[i]);
+            sum[i] = l[i] * f;
+            m[i] = f;                               // this group's factor
+#pragma unroll
+            for (int off = LK; off < 32; off <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], off);
+            if (sub == 0) sh_l[warp][own + i] = sum[i];
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const int from = LK >= RT ? r * (LK / RT) : r / RO;
+            const float fr = __shfl_sync(0xffffffffu, m[r % RO], (lane & ~(LK - 1)) + from);
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 z = unpack2(acc[r][i]);
+                // a group that has seen nothing of a row has an output of 0
+                y[2 * i] = fr == 0.f ? 0.f : z.x * fr;
+                y[2 * i + 1] = fr == 0.f ? 0.f : z.y * fr;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int off = LK; off < 32; off <<= 1) y[i] += __shfl_xor_sync(0xffffffffu, y[i], off);
+            if (sub == 0) {
+                *reinterpret_cast<float4*>(&sh_o[warp][r][8 * g]) = make_float4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<float4*>(&sh_o[warp][r][8 * g + 4]) = make_float4(y[4], y[5], y[6], y[7]);
+            }
+        }
+        __syncthreads();
+        // Finished here, or one of the CTA's two pieces.
+        const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+        float* part = a.part + ((size_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * RT * (D + 2);
+        for (int e = tid; e < rows * D; e += kStreamThreads) {
+            const int r = e / D, c = e % D;
+            float o = 0.f, sl = 0.f, sm = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                o += sh_o[k][r][c];
+                sl += sh_l[k][r];
+                sm = fmaxf(sm, sh_m[k][r]);
+            }
+            const int t = (r0 + r) / a.G, h = (r0 + r) % a.G;
+            if (whole) {
+                st_f(static_cast<TO*>(a.o) + (((long long)n * a.Ts + t) * a.Hq + hk * a.G + h) * D + c,
+                     sl == 0.f ? 0.f : o / sl);     // nothing seen: an unused node
+            } else {
+                part[e] = o;
+                if (c == 0) {
+                    part[RT * D + r] = sm;
+                    part[RT * D + RT + r] = sl;
+                }
+            }
+        }
+    }
+}
+
+// More rows: tiles.  128 threads as 8 row groups x 16 columns for 32 query rows:
+// thread (ty, tx) owns rows 4 ty .. 4 ty + 3 throughout, their scores for keys tx
+// and tx + 16 and D / 16 of their output columns, so that m, l and the rescaling
+// stay in registers.  K and V come by cp.async in two stages, one tile ahead;
+// page numbers are loaded two tiles before that.  Bound by shared-memory reads.
+constexpr int kTileThreads = 128;
+constexpr int kTileKeys = 32;
+constexpr int kTileRows = 32;
+constexpr int kTileLead = 2;
+__host__ __device__ constexpr int tile_ctas(int D) { return D == 128 ? 2 : (D == 64 ? 4 : 5); }   // per SM
+
+template <typename TI, int D>
+struct TileShape {
+    static constexpr int kLdq = D + 4;
+    static constexpr int kLdk = D + 16 / (int)sizeof(TI);      // rows stay 16-byte aligned
+    static constexpr int kLdp = kTileKeys + 4;
+    static constexpr int kStage = kTileKeys * (kLdk + D);       // elements: K, then V
     static constexpr size_t kBytes =
-        sizeof(float) * (RT * kLdk + kSimtKeys * kLdk + kSimtKeys * D + RT * kLdp);
+        sizeof(float) * (kTileRows * kLdq + kTileRows * kLdp) + 2 * sizeof(TI) * kStage;
 };
 
 template <typename T>
@@ -39,56 +415,103 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p)
                        __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
 }
 
-// 128 threads as 8 row groups x 16 columns.  Thread (ty, tx) owns rows
-// ty RR .. ty RR + RR - 1 throughout: their scores for keys tx + 16 j, and D /
-// 16 of their output columns, so m, l and the rescaling stay in registers.
-template <typename TI, typename TO, int D, int RT>
-__global__ void __launch_bounds__(kSimtThreads)
-tree_attention_simt_kernel(const TreeArgs a)
+template <typename TI, typename TO, int D>
+__global__ void __launch_bounds__(kTileThreads, tile_ctas(D))
+tree_attention_tile_kernel(const TreeArgs a)
 {
-    using Sh = SimtShape<D, RT>;
-    constexpr int RR = RT / 8, KR = kSimtKeys / 16, CR = D / 16;
-    constexpr int V4 = D / 4;
+    using Sh = TileShape<TI, D>;
+    constexpr int RT = kTileRows, RR = RT / 8, KR = kTileKeys / 16, CR = D / 16;
+    constexpr int V4 = D / 4, VR = 16 / (int)sizeof(TI);        // elements per 16 bytes
+    constexpr int kVecs = D / VR;                               // 16-byte pieces of a row
     extern __shared__ __align__(16) float smem[];
-    float* sQ = smem;                               // [RT][kLdk]
-    float* sK = sQ + RT * Sh::kLdk;                 // [keys][kLdk]
-    float* sV = sK + kSimtKeys * Sh::kLdk;          // [keys][D]
-    float* sP = sV + kSimtKeys * D;                 // [RT][kLdp]
-    __shared__ long long sh_loc[kSimtThreads / 32 + 2];
+    float* sQ = smem;                               // [RT][kLdq]
+    float* sP = sQ + RT * Sh::kLdq;                 // [RT][kLdp]
+    TI* stages = reinterpret_cast<TI*>(sP + RT * Sh::kLdp);
+    __shared__ long long sh_loc[kTileThreads / 32 + 2];
     __shared__ unsigned long long anc[kTreeMaxNodes];
     __shared__ int32_t up[kTreeMaxNodes];
+    __shared__ long long sh_off[4][kTileKeys];      // a key's row in the cache (-1: none), by tile % 4
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const TI* q = static_cast<const TI*>(a.q);
 
     const int group = blockIdx.x / a.row_tiles, r0 = (blockIdx.x % a.row_tiles) * RT;
     const int rows = a.R - r0 < RT ? a.R - r0 : RT;
-    const TreeSpot sp = tree_locate<kSimtThreads, kSimtKeys>(a, group, sh_loc);
+    const TreeSpot sp = tree_locate<kTileThreads, kTileKeys, kTileLead>(a, group, sh_loc);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int row_elems = a.Hkv * D;
     int have = -1;                                  // the sequence anc[] is of
 
-    TreePieces<kSimtKeys> w;
+    TreePieces<kTileKeys, kTileLead> w;
     for (bool more = w.start(a, sp, group); more; more = w.next(a)) {
         const int n = w.n, ctx = w.ctx, tiles = w.tiles, t0 = w.t0, t1 = w.t1, hk = w.hk;
         const int32_t* table = a.page_table + (long long)n * a.max_pages;
+        __syncthreads();                            // the last piece's tiles and masks have been read
         if (have != n) {
-            __syncthreads();
             if (tid < 32)
                 tree_masks(a.parent ? a.parent + (long long)n * a.Ts : nullptr, a.Ts, tid, anc, up);
             have = n;
         }
-        __syncthreads();
-        for (int e = tid; e < RT * V4; e += kSimtThreads) {
+        // The rows of a tile, by one warp: ask() loads their page numbers, put()
+        // a tile later turns them into offsets.
+        int page = -1, slot = 0;
+        auto ask = [&](int t) {
+            if (tid < kTileKeys && t < t1) {
+                const int pos = t * kTileKeys + tid;
+                page = -1;
+                if (pos < ctx) {
+                    const int p = pos / a.page_size;
+                    page = __ldg(table + p);
+                    slot = pos - p * a.page_size;
+                }
+            }
+        };
+        auto put = [&](int t) {
+            if (tid < kTileKeys && t < t1) {
+                const int node = t * kTileKeys + tid - ctx;
+                long long off = -1;
+                if (page >= 0 && page < a.num_pages) off = (long long)page * a.page_stride + (long long)slot * row_elems;
+                else if (node >= 0 && node < a.Ts) off = ((long long)n * a.Ts + node) * row_elems;
+                sh_off[t & 3][tid] = off;
+            }
+        };
+        auto fetch = [&](int t) {
+            if (t < t1) {
+                const int nc = ctx - t * kTileKeys;
+                TI* sk = stages + (t & 1) * Sh::kStage;
+                TI* sv = sk + kTileKeys * Sh::kLdk;
+#pragma unroll 4
+                for (int e = tid; e < kTileKeys * kVecs; e += kTileThreads) {
+                    const int j = e / kVecs, c = (e % kVecs) * VR;
+                    const long long off = sh_off[t & 3][j];
+                    const TI *kp = nullptr, *vp = nullptr;
+                    if (off >= 0) {
+                        kp = static_cast<const TI*>(j >= nc ? a.k : a.k_cache) + off + hk * D + c;
+                        vp = static_cast<const TI*>(j >= nc ? a.v : a.v_cache) + off + hk * D + c;
+                    }
+                    copy16(sk + j * Sh::kLdk + c, kp, q);
+                    copy16(sv + j * D + c, vp, q);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        ask(t0);
+        put(t0);
+        ask(t0 + 1);
+        put(t0 + 1);
+        ask(t0 + 2);
+        for (int e = tid; e < RT * V4; e += kTileThreads) {
             const int r = e / V4, c = e % V4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
                 const int t = (r0 + r) / a.G, g = (r0 + r) % a.G;
                 x = load4(q + (((long long)n * a.Ts + t) * a.Hq + hk * a.G + g) * D + 4 * c);
             }
-            *reinterpret_cast<float4*>(sQ + r * Sh::kLdk + 4 * c) =
+            *reinterpret_cast<float4*>(sQ + r * Sh::kLdq + 4 * c) =
                 make_float4(x.x * a.scale_log2, x.y * a.scale_log2, x.z * a.scale_log2,
                             x.w * a.scale_log2);
         }
+        __syncthreads();
+        fetch(t0);
         unsigned long long mask[RR];
         float m[RR], l[RR], acc[RR][CR];
 #pragma unroll
@@ -101,33 +524,17 @@ tree_attention_simt_kernel(const TreeArgs a)
             for (int c = 0; c < CR; ++c) acc[i][c] = 0.f;
         }
         for (int t = t0; t < t1; ++t) {
-            const int k0 = t * kSimtKeys;
+            const int k0 = t * kTileKeys;
             const int nc = ctx - k0;                // key j is drafted node j - nc from j = nc on
-            const int nk = nc + a.Ts < kSimtKeys ? nc + a.Ts : kSimtKeys;
-            const bool draft = nc < kSimtKeys;      // some are
-            __syncthreads();                        // the previous tile has been read
-            for (int e = tid; e < kSimtKeys * V4; e += kSimtThreads) {
-                const int j = e / V4, c = e % V4;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-                if (j < nk) {
-                    long long off;
-                    const TI *kp = static_cast<const TI*>(a.k_cache), *vp = static_cast<const TI*>(a.v_cache);
-                    if (j >= nc) {
-                        off = ((long long)n * a.Ts + j - nc) * row_elems;
-                        kp = static_cast<const TI*>(a.k);
-                        vp = static_cast<const TI*>(a.v);
-                    } else {
-                        off = tree_cache_row(a, table, k0 + j, row_elems);
-                    }
-                    if (off >= 0) {
-                        x = load4(kp + off + hk * D + 4 * c);
-                        y = load4(vp + off + hk * D + 4 * c);
-                    }
-                }
-                *reinterpret_cast<float4*>(sK + j * Sh::kLdk + 4 * c) = x;
-                *reinterpret_cast<float4*>(sV + j * D + 4 * c) = y;
-            }
-            __syncthreads();
+            const int nk = nc + a.Ts < kTileKeys ? nc + a.Ts : kTileKeys;
+            const bool draft = nc < kTileKeys;      // some are
+            fetch(t + 1);
+            put(t + 2);
+            ask(t + 3);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncthreads();                        // tile t, and the rows of tile t + 2
+            const TI* sK = stages + (t & 1) * Sh::kStage;
+            const TI* sV = sK + kTileKeys * Sh::kLdk;
             float s[RR][KR];
 #pragma unroll
             for (int i = 0; i < RR; ++i)
@@ -137,11 +544,10 @@ tree_attention_simt_kernel(const TreeArgs a)
             for (int c = 0; c < V4; ++c) {
                 float4 kv[KR];
 #pragma unroll
-                for (int j = 0; j < KR; ++j)
-                    kv[j] = *reinterpret_cast<const float4*>(sK + (tx + 16 * j) * Sh::kLdk + 4 * c);
+                for (int j = 0; j < KR; ++j) kv[j] = load4(sK + (tx + 16 * j) * Sh::kLdk + 4 * c);
 #pragma unroll
                 for (int i = 0; i < RR; ++i) {
-                    const float4 x = *reinterpret_cast<const float4*>(sQ + (ty * RR + i) * Sh::kLdk + 4 * c);
+                    const float4 x = *reinterpret_cast<const float4*>(sQ + (ty * RR + i) * Sh::kLdq + 4 * c);
 #pragma unroll
                     for (int j = 0; j < KR; ++j) {
                         s[i][j] = fmaf(x.x, kv[j].x, s[i][j]);
@@ -151,19 +557,16 @@ tree_attention_simt_kernel(const TreeArgs a)
                     }
                 }
             }
-            unsigned there = 0;                     // context keys whose page exists
+            bool there[KR];                         // context keys whose page exists
 #pragma unroll
-            for (int j = 0; j < KR; ++j) {
-                const int kk = tx + 16 * j;
-                if (kk < nc && tree_cache_row(a, table, k0 + kk, row_elems) >= 0) there |= 1u << j;
-            }
+            for (int j = 0; j < KR; ++j) there[j] = tx + 16 * j < nc && sh_off[t & 3][tx + 16 * j] >= 0;
 #pragma unroll
             for (int i = 0; i < RR; ++i) {
                 float top = m[i];
 #pragma unroll
                 for (int j = 0; j < KR; ++j) {
                     const int node = tx + 16 * j - nc;
-                    const bool see = node < 0 ? mask[i] != 0ull && ((there >> j) & 1)
+                    const bool see = node < 0 ? mask[i] != 0ull && there[j]
                                               : node < a.Ts && ((mask[i] >> node) & 1ull);
                     if (!see) s[i][j] = -INFINITY;
                     top = fmaxf(top, s[i][j]);
@@ -188,28 +591,45 @@ tree_attention_simt_kernel(const TreeArgs a)
                 for (int c = 0; c < CR; ++c) acc[i][c] *= shrink;
             }
             __syncwarp();                           // a row's P is written and read by one warp
-#pragma unroll 2
-            for (int j = 0; j < kSimtKeys; j += 4) {
-                float4 p[RR];
+            // column c of this thread: its 4-column groups are 64 apart (d >= 64)
+            auto add = [&](int j, const float (&p)[RR]) {
+                float v[CR];
+                if constexpr (CR % 4 == 0) {
 #pragma unroll
-                for (int i = 0; i < RR; ++i)
-                    p[i] = *reinterpret_cast<const float4*>(sP + (ty * RR + i) * Sh::kLdp + j);
-#pragma unroll
-                for (int jj = 0; jj < 4; ++jj) {
-                    float v[CR];
-#pragma unroll
-                    for (int c = 0; c < CR; ++c) v[c] = sV[(j + jj) * D + tx + 16 * c];
-#pragma unroll
-                    for (int i = 0; i < RR; ++i) {
-                        const float pp = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
-                        // a node that this row does not see may hold inf or NaN: 0 * v would keep it
-                        if (draft && j + jj >= nc && (j + jj >= nk || !((mask[i] >> (j + jj - nc)) & 1ull)))
-                            continue;
-#pragma unroll
-                        for (int c = 0; c < CR; ++c) acc[i][c] = fmaf(pp, v[c], acc[i][c]);
+                    for (int c = 0; c < CR; c += 4) {
+                        const float4 x = load4(sV + j * D + c * 16 + tx * 4);
+                        v[c] = x.x;
+                        v[c + 1] = x.y;
+                        v[c + 2] = x.z;
+                        v[c + 3] = x.w;
                     }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < CR; ++c) v[c] = ld_f(sV + j * D + tx + 16 * c);
                 }
+#pragma unroll
+                for (int i = 0; i < RR; ++i) {
+                    // a node that this row does not see may hold inf or NaN: 0 * v would keep it
+                    if (draft && j >= nc && (j >= nk || !((mask[i] >> (j - nc)) & 1ull))) continue;
+#pragma unroll
+                    for (int c = 0; c < CR; ++c) acc[i][c] = fmaf(p[i], v[c], acc[i][c]);
+                }
+            };
+#pragma unroll 2
+            for (int j = 0; j < kTileKeys; j += 4) {
+                float p[4][RR];
+#pragma unroll
+                for (int i = 0; i < RR; ++i) {
+                    const float4 x = *reinterpret_cast<const float4*>(sP + (ty * RR + i) * Sh::kLdp + j);
+                    p[0][i] = x.x;
+                    p[1][i] = x.y;
+                    p[2][i] = x.z;
+                    p[3][i] = x.w;
+                }
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) add(j + jj, p[jj]);
             }
+            __syncthreads();                        // tile t has been read: its stage is free
         }
         // Finished here, or one of the CTA's two pieces.
         const bool whole = t0 == 0 && t1 == tiles;
@@ -218,19 +638,18 @@ tree_attention_simt_kernel(const TreeArgs a)
         for (int i = 0; i < RR; ++i) {
             const int r = ty * RR + i;
             if (r >= rows) continue;
-            if (whole) {
-                const int t = (r0 + r) / a.G, g = (r0 + r) % a.G;
-                TO* op = static_cast<TO*>(a.o) + (((long long)n * a.Ts + t) * a.Hq + hk * a.G + g) * D;
-                const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+            const int t = (r0 + r) / a.G, g = (r0 + r) % a.G;
+            TO* op = static_cast<TO*>(a.o) + (((long long)n * a.Ts + t) * a.Hq + hk * a.G + g) * D;
+            const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
-                for (int c = 0; c < CR; ++c) st_f(op + tx + 16 * c, mask[i] ? acc[i][c] * inv : 0.f);
-            } else {
-#pragma unroll
-                for (int c = 0; c < CR; ++c) part[r * D + tx + 16 * c] = acc[i][c];
-                if (tx == 0) {
-                    part[RT * D + r] = m[i];
-                    part[RT * D + RT + r] = l[i];
-                }
+            for (int c = 0; c < CR; ++c) {
+                const int col = CR % 4 == 0 ? (c / 4) * 64 + tx * 4 + c % 4 : tx + 16 * c;
+                if (whole) st_f(op + col, mask[i] ? acc[i][c] * inv : 0.f);
+                else part[r * D + col] = acc[i][c];
+            }
+            if (!whole && tx == 0) {
+                part[RT * D + r] = m[i];
+                part[RT * D + RT + r] = l[i];
             }
         }
     }
@@ -245,20 +664,21 @@ tree_attention_simt_kernel(const TreeArgs a)
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 8;
 
-template <typename TO, int D, int KT>
+template <typename TO, int D, int KT, int LEAD>
 __global__ void __launch_bounds__(kJoinThreads)
 tree_join_kernel(const TreeArgs a, int RT)
 {
     __shared__ long long sh_loc[kJoinThreads / 32 + 2];
     const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const TreeSpot sp = tree_locate<kJoinThreads, KT>(a, c, sh_loc);
+    const TreeSpot sp = tree_locate<kJoinThreads, KT, LEAD>(a, c, sh_loc);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long at = tree_begin(sp, c);
     if (at >= sp.total) return;                     // an empty range at the end
-    const int tiles = (int)tree_seq_tiles<KT>(a, sp.n);
-    const int hk = (int)((at - sp.start) / tiles);
-    const long long first = sp.start + (long long)hk * tiles;
-    if (at == first || tree_begin(sp, c - 1) > first) return;
+    const int tiles = tree_tiles<KT>(a, sp.n);
+    const int hk = (int)((at - sp.start) / (tiles + LEAD));
+    // where the item's tiles begin; a boundary up to there cuts nothing
+    const long long first = sp.start + (long long)hk * (tiles + LEAD) + LEAD;
+    if (at <= first || tree_begin(sp, c - 1) > first) return;
     int last = c;                                   // the last group with tiles of this item
     while (last + 1 < a.groups && tree_begin(sp, last + 1) < first + tiles) ++last;
     const int r0 = blockIdx.z * RT;
@@ -296,7 +716,7 @@ tree_join_kernel(const TreeArgs a, int RT)
         if (D >= 32 || lane < D) st_f(op + lane + 32 * e, o[e] * inv);
 }
 
-template <typename TO, int D, int KT>
+template <typename TO, int D, int KT, int LEAD>
 cudaError_t launch_join(const TreeArgs& a, int rt, cudaStream_t stream)
 {
     if (a.groups < 2) return cudaSuccess;
@@ -310,51 +730,47 @@ cudaError_t launch_join(const TreeArgs& a, int rt, cudaStream_t stream)
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_join_kernel<TO, D, KT>, a, rt);
-}
-
-template <typename TI, typename TO, int D, int RT>
-cudaError_t launch_simt(const TreeArgs& a, cudaStream_t stream)
-{
-    auto kern = tree_attention_simt_kernel<TI, TO, D, RT>;
-    const size_t bytes = SimtShape<D, RT>::kBytes;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
-    kern<<<a.groups * a.row_tiles, kSimtThreads, bytes, stream>>>(a);
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<TO, D, KT, LEAD>, a, rt);
 }
 
 template <typename TI, typename TO, int D>
-cudaError_t launch_d(const TreeArgs& a, const TreePlan& plan, cudaStream_t stream)
+cudaError_t launch_d(const TreeArgs& a, int rt, cudaStream_t stream)
 {
-    cudaError_t e = plan.rt == 8 ? launch_simt<TI, TO, D, 8>(a, stream)
-                                 : launch_simt<TI, TO, D, 32>(a, stream);
+    const bool stream_kernel = rt == kStreamRows;
+    auto kern = stream_kernel ? tree_attention_stream_kernel<TI, TO, D> : tree_attention_tile_kernel<TI, TO, D>;
+    const size_t bytes = stream_kernel ? (size_t)kAhead * 4 * (sizeof(TI) / 2) * kStreamThreads * 16
+                                       : TileShape<TI, D>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    return launch_join<TO, D, kSimtKeys>(a, plan.rt, stream);
+    kern<<<a.groups * a.row_tiles, stream_kernel ? kStreamThreads : kTileThreads, bytes, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return stream_kernel ? launch_join<TO, D, kStreamKeys, kStreamLead>(a, rt, stream)
+                         : launch_join<TO, D, kTileKeys, kTileLead>(a, rt, stream);
 }
 
 template <typename TI, typename TO>
-cudaError_t launch_typed(const TreeArgs& a, const TreePlan& plan, int d, cudaStream_t stream)
+cudaError_t launch_typed(const TreeArgs& a, int rt, int d, cudaStream_t stream)
 {
     switch (d) {
-        case 16: return launch_d<TI, TO, 16>(a, plan, stream);
-        case 32: return launch_d<TI, TO, 32>(a, plan, stream);
-        case 64: return launch_d<TI, TO, 64>(a, plan, stream);
-        case 128: return launch_d<TI, TO, 128>(a, plan, stream);
+        case 16: return launch_d<TI, TO, 16>(a, rt, stream);
+        case 32: return launch_d<TI, TO, 32>(a, rt, stream);
+        case 64: return launch_d<TI, TO, 64>(a, rt, stream);
+        case 128: return launch_d<TI, TO, 128>(a, rt, stream);
         default: return cudaErrorInvalidValue;
     }
 }
 
 }  // namespace
 
-TreePlan tree_plan(int32_t Ts, int32_t Hq, int32_t Hkv, int sms, bool tc)
+TreePlan tree_plan(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, int sms, bool tc)
 {
     const int R = Ts * (Hq / Hkv);
     TreePlan p;
     p.tc = tc;
-    p.rt = tc ? (R <= 128 ? 128 : 256) : (R <= 8 ? 8 : 32);
+    p.rt = tc ? (R <= 128 ? 128 : 256) : (R <= kStreamRows ? kStreamRows : kTileRows);
     p.row_tiles = (R + p.rt - 1) / p.rt;
-    const int ctas = (sms > 0 ? sms : 1) * (tc ? 1 : 2);
+    const int ctas = (sms > 0 ? sms : 1) * (tc ? 1 : p.rt == kStreamRows ? kStreamCtas : tile_ctas(d));
     p.groups = ctas / p.row_tiles > 1 ? ctas / p.row_tiles : 1;
     return p;
 }
@@ -370,7 +786,7 @@ size_t tree_workspace_bytes(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, kda_
 {
     size_t most = 0;
     for (int tc = 0; tc <= (int)tree_tc_supported(d, dtype); ++tc) {
-        const TreePlan p = tree_plan(Ts, Hq, Hkv, sms, tc != 0);
+        const TreePlan p = tree_plan(Ts, Hq, Hkv, d, sms, tc != 0);
         const size_t b = (size_t)p.groups * p.row_tiles * 2 * p.rt * (d + 2) * sizeof(float);
         if (b > most) most = b;
     }
@@ -383,19 +799,19 @@ cudaError_t launch_tree_attention(TreeArgs args, int32_t d, kda_dtype_t dtype, i
                                   cudaStream_t stream)
 {
     const bool tc = tree_tc_supported(d, dtype) && args.scale_log2 > 0.f && getenv("KDA_FORCE_SIMT") == nullptr;
-    const TreePlan plan = tree_plan(args.Ts, args.Hq, args.Hkv, sms, tc);
+    const TreePlan plan = tree_plan(args.Ts, args.Hq, args.Hkv, d, sms, tc);
     args.groups = plan.groups;
     args.row_tiles = plan.row_tiles;
     if (plan.tc) {
         const cudaError_t e = launch_tree_attention_tc(args, plan, d, stream);
         if (e != cudaSuccess) return e;
-        return d == 64 ? launch_join<__nv_bfloat16, 64, 128>(args, plan.rt, stream)
-                       : launch_join<__nv_bfloat16, 128, 128>(args, plan.rt, stream);
+        return d == 64 ? launch_join<__nv_bfloat16, 64, kTcKeys, kTcLead>(args, plan.rt, stream)
+                       : launch_join<__nv_bfloat16, 128, kTcKeys, kTcLead>(args, plan.rt, stream);
     }
     switch (dtype) {
-        case KDA_BF16: return launch_typed<__nv_bfloat16, __nv_bfloat16>(args, plan, d, stream);
-        case KDA_BF16_F32OUT: return launch_typed<__nv_bfloat16, float>(args, plan, d, stream);
-        default: return launch_typed<float, float>(args, plan, d, stream);
+        case KDA_BF16: return launch_typed<__nv_bfloat16, __nv_bfloat16>(args, plan.rt, d, stream);
+        case KDA_BF16_F32OUT: return launch_typed<__nv_bfloat16, float>(args, plan.rt, d, stream);
+        default: return launch_typed<float, float>(args, plan.rt, d, stream);
     }
 }
 

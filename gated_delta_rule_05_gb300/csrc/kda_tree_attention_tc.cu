@@ -43,8 +43,8 @@ namespace {
 
 using namespace sm100;
 
-constexpr int KT = 128;                    // keys per tile
-using Piece = TreePieces<KT>;
+constexpr int KT = kTcKeys;                // keys per tile
+using Piece = TreePieces<KT, kTcLead>;
 constexpr int kRingMeta = 16;              // tiles whose key masks are kept
 constexpr int kQWarps = 2;                 // warps that copy q
 
@@ -767,39 +767,54 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, Piece w, bool go, 
             __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.o) +
                                 (((long long)w.n * a.Ts + node) * a.Hq + w.hk * a.G + g) * D;
             float* part = a.part + ((size_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * RT * (D + 2);
+            if (__any_sync(0xffffffffu, add != 0)) {
+                // O is corrected in place
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-                uint32_t x[16];
-                tmem_ld16(to + 16 * c, x);
-                tmem_ld_wait();
-                for (unsigned long long left = add; left; left &= left - 1) {
-                    const int j = __ffsll((long long)left) - 1;
-                    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) +
-                        (((long long)w.n * a.Ts + j) * a.Hkv + w.hk) * D + 16 * c;
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t x[16];
+                    tmem_ld16(to + 16 * c, x);
+                    tmem_ld_wait();
+#pragma unroll 1
+                    for (unsigned long long left = add; left; left &= left - 1) {
+                        const int j = __ffsll((long long)left) - 1;
+                        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) +
+                            (((long long)w.n * a.Ts + j) * a.Hkv + w.hk) * D + 16 * c;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float y = __bfloat162float(v[i]);
-                        if (!(fabsf(y) < INFINITY)) x[i] = __float_as_uint(__uint_as_float(x[i]) + y);
+                        for (int i = 0; i < 16; ++i) {
+                            const float y = __bfloat162float(v[i]);
+                            if (!(fabsf(y) < INFINITY)) x[i] = __float_as_uint(__uint_as_float(x[i]) + y);
+                        }
                     }
+                    __syncwarp();
+                    tmem_st16(to + 16 * c, x);
                 }
-                if (seen == 0) {
+                tmem_st_wait();
+            }
+            uint32_t x[D / 32][32];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = 0;
-                }
-                if (mine && whole) {
-                    uint32_t y[8];
+            for (int c = 0; c < D / 32; ++c) tmem_ld32(to + 32 * c, x[c]);
+            tmem_ld_wait();
+            if (mine && whole) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        y[j] = pack_bf16x2(__uint_as_float(x[2 * j]) * scale_o, __uint_as_float(x[2 * j + 1]) * scale_o);
-                    *reinterpret_cast<uint4*>(op + 16 * c) = make_uint4(y[0], y[1], y[2], y[3]);
-                    *reinterpret_cast<uint4*>(op + 16 * c + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-                } else if (mine) {
+                for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        *reinterpret_cast<uint4*>(part + (size_t)local * D + 16 * c + i) =
-                            make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                }
-                __syncwarp();                      // before the next collective load
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            y[j] = pack_bf16x2(__uint_as_float(x[c][i + 2 * j]) * scale_o,
+                                               __uint_as_float(x[c][i + 2 * j + 1]) * scale_o);
+                        *reinterpret_cast<uint4*>(op + 32 * c + i) =
+                            seen == 0 ? make_uint4(0, 0, 0, 0) : make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+            } else if (mine) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4*>(part + (size_t)local * D + 32 * c + i) =
+                            seen == 0 ? make_uint4(0, 0, 0, 0)
+                                      : make_uint4(x[c][i], x[c][i + 1], x[c][i + 2], x[c][i + 3]);
             }
             if (mine && !whole) {
                 part[RT * D + local] = seen == 0 ? -INFINITY : m;
@@ -846,7 +861,7 @@ tree_attention_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_consta
     }
     tc_fence_before();
     const int group = blockIdx.x / a.row_tiles, r0 = (blockIdx.x % a.row_tiles) * (NT * 128);
-    const TreeSpot sp = tree_locate<Sh::kThreads, KT>(a, group, sh.loc);   // has block barriers
+    const TreeSpot sp = tree_locate<Sh::kThreads, KT, kTcLead>(a, group, sh.loc);   // has block barriers
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
