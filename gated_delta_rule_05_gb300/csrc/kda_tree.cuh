@@ -21,7 +21,7 @@ namespace kda {
 
 constexpr int kTreeMaxNodes = 64;     // one bit per node in a 64-bit mask
 constexpr int kTcKeys = 128;          // the tensor-core kernel's KT and LEAD
-constexpr int kTcLead = 8;
+constexpr int kTcLead = 12;
 
 struct TreeArgs {
     const void *q, *k, *v;
@@ -133,7 +133,7 @@ __device__ TreeSpot tree_locate(const TreeArgs& a, int c, long long* sh)
         if (lane == 0) sh[warp] = rest;
         __syncthreads();
         rest = 0;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < W; ++i) rest += sh[i];
         __syncthreads();
     }
@@ -149,12 +149,16 @@ __device__ TreeSpot tree_locate(const TreeArgs& a, int c, long long* sh)
         }
         if (lane == 31) sh[warp] = incl;
         __syncthreads();
-        long long before = base, chunk = 0;
+        // the warps' sums, a lane each (W <= 32), added up the same way
+        long long upto = lane < W ? sh[lane] : 0;
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            if (i < warp) before += sh[i];
-            chunk += sh[i];
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += x;
         }
+        const long long chunk = __shfl_sync(0xffffffffu, upto, 31);
+        const long long below = __shfl_sync(0xffffffffu, upto, warp ? warp - 1 : 0);
+        const long long before = base + (warp ? below : 0);
         if (n0 == 0) {
             r.total = chunk + rest;
             r.per = r.total / a.groups;

@@ -706,7 +706,8 @@ tree_join_kernel(const TreeArgs a, int RT)
         l = fmaf(x[RT * D + RT + r], w, l);
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            if (D >= 32 || lane < D) o[e] = fmaf(x[(size_t)r * D + lane + 32 * e], w, o[e]);
+            if ((D >= 32 || lane < D) && w != 0.f)   // w = 0: o may be anything (an unused node)
+                o[e] = fmaf(x[(size_t)r * D + lane + 32 * e], w, o[e]);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;     // l = 0: an unused node; a NaN stays
     const int t = (r0 + r) / a.G, g = (r0 + r) % a.G;

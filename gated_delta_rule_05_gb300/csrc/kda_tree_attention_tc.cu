@@ -19,12 +19,12 @@
 // every K and V tile and alternate on the tensor core.
 //
 // Copies run ahead through a ring of K and V tiles: TMA boxes where 32 rows in
-// a row are there and the page size allows, 16-byte cp.async elsewhere, which
-// takes any page size and fills rows past the length and rows of pages that do
-// not exist with zeros, so that nothing stored there can reach a product.  A row
-// of drafted values is copied through registers, and an infinity or NaN in it
-// is replaced by 0: the product's 0 * inf would reach rows that do not see the
-// node.  The rows that do see it add it to their output at the end.
+// a row are there and the page size allows, loads by the lanes elsewhere, which
+// take any page size and fill rows past the length and rows of pages that do not
+// exist with zeros, so that nothing stored there can reach a product.  In drafted
+// values an infinity or NaN is replaced by 0: the product's 0 * inf would reach
+// rows that do not see the node.  The rows that do see it add it to their output
+// at the end.
 //
 // Every wait has a limit (mbar_wait); a wait that gives up sets the workspace's
 // timeout word, and the CTA runs to its end without waiting again.
@@ -55,13 +55,13 @@ struct TcShape {
     static constexpr int kSlots = (D == 128) ? (NT == 1 ? 6 : 5) : 12;
     // Warps: softmax, copies, one that issues products, filled up to whole
     // warpgroups so that registers can be moved from the latter two to the
-    // softmax: 384 x 168 >= 128 x 232 + 256 x 128, 512 x 128 = 256 x 192 + 256 x 64.
+    // softmax: 384 x 168 >= 128 x 232 + 256 x 128, 512 x 128 = 256 x 184 + 256 x 72.
     // block is filled to whole warpgroups, so that registers can be moved from
     // the copies and the products to the softmax (512 x 128 = 256 x 192 + 256 x 64)
     static constexpr int kThreads = NT == 1 ? 384 : 512;
     static constexpr int kCopyWarp = NT * 4;
     static constexpr int kMmaWarp = NT * 4 + 4;
-    static constexpr int kMore = NT == 1 ? 232 : 192, kFewer = NT == 1 ? 128 : 64;
+    static constexpr int kMore = NT == 1 ? 232 : 184, kFewer = NT == 1 ? 128 : 72;
     static constexpr size_t kBytes = 1024 + kQBytes + (size_t)kSlots * kSlotBytes;
     // TMEM columns
     static constexpr int kS1 = 128, kO0 = 256, kO1 = 256 + D;
@@ -72,7 +72,7 @@ struct TcShared {
     uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2];
     uint32_t tmem;
     int dead;
-    uint32_t keys[kRingMeta][4];           // a tile's keys that are context rows of pages that exist
+    alignas(16) uint32_t keys[kRingMeta][4];           // a tile's keys that are context rows of pages that exist
     uint32_t bad[kRingMeta][4];            // a tile's keys that are drafted nodes with inf or NaN in v
     long long loc[16 + 2];
 };
@@ -96,16 +96,6 @@ __device__ __forceinline__ void wait(TcShared& sh, uint64_t* bar, uint32_t parit
     }
 }
 
-// 16 bytes to shared memory, asynchronously; zeros when src is null.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, const void* any)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.eq.u64 p, %1, 0;\n\t"
-        "cp.async.cg.shared.global [%0], [%2], 16, p;\n\t}" ::"r"(dst),
-        "l"(src), "l"(src ? src : any)
-        : "memory");
-}
-
 // One box of a page pool [num_pages][page_size][Hkv][d]: rows of one page, 64
 // columns of one head.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t h,
@@ -117,21 +107,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(row), "r"(page), "r"(smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-
-// The barrier's current phase stays open until this thread's copies have landed.
-__device__ __forceinline__ void cp_async_hold(uint64_t* bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return r;
 }
 
 // Pairs of fp32 for the two-wide FMA and add.
@@ -240,20 +227,44 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c)
 }
 
 // Copies 32 rows of D bf16 to rows row0 .. row0 + 31 of a tile; lane's argument
-// p is the source of row row0 + lane (null: zeros).  A warp, whole rows at a time.
-template <int D>
-__device__ __forceinline__ void copy_rows32(uint32_t dst, int row0, const __nv_bfloat16* p,
-                                            const void* any, int lane)
+// p is the source of row row0 + lane (null: zeros).  A warp, whole rows at a time,
+// BATCH loads under way.  In rows whose bit of `clear` is set infinities and NaN
+// become 0; returns the bits of those that had any.  The copy is ordered before
+// the asynchronous reads of whoever the caller then tells.  (The same by cp.async
+// took five times as long: 650 cycles an instruction, one after the other.)
+template <int D, int BATCH>
+__device__ __forceinline__ uint32_t copy_rows32(uint32_t dst, int row0, const __nv_bfloat16* p, uint32_t clear,
+                                                int lane)
 {
     constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes per row, rows per instruction
-    const int c = lane % LPR;
+    constexpr int B = BATCH < 32 / RPI ? BATCH : 32 / RPI;
+    const int c = lane % LPR, j0 = lane / LPR;
     const unsigned long long mine = reinterpret_cast<unsigned long long>(p);
-#pragma unroll 4
-    for (int i = 0; i < 32 / RPI; ++i) {
-        const int j = i * RPI + lane / LPR;
-        const unsigned long long src = __shfl_sync(0xffffffffu, mine, j);
-        cp_async16(dst + tile_at(row0 + j, c), src ? reinterpret_cast<const void*>(src + 16ull * c) : nullptr, any);
+    uint32_t bad = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32 / RPI; i0 += B) {
+        uint4 x[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const unsigned long long src = __shfl_sync(0xffffffffu, mine, (i0 + k) * RPI + j0);
+            x[k] = make_uint4(0, 0, 0, 0);
+            if (src) x[k] = __ldg(reinterpret_cast<const uint4*>(src + 16ull * c));
+        }
+        if (clear) {
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                const int j = (i0 + k) * RPI + j0;
+                if (((clear >> j) & 1) && clear_nonfinite(x[k])) bad |= 1u << j;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + tile_at(row0 + (i0 + k) * RPI + j0, c)),
+                         "r"(x[k].x), "r"(x[k].y), "r"(x[k].z), "r"(x[k].w)
+                         : "memory");
     }
+    fence_proxy_async_smem();
+    return clear ? __reduce_or_sync(0xffffffffu, bad) : 0u;
 }
 
 // Four warps, 32 rows of every tile each.  A ring entry is one K or V tile; the
@@ -265,28 +276,25 @@ __device__ __forceinline__ void copy_rows32(uint32_t dst, int row0, const __nv_b
 // Where all 32 rows are context rows of pages that exist, and the page size
 // allows (a.box), the rows come as TMA boxes that complete on the entry's
 // barrier.  Elsewhere (the end of a context, other page sizes) the lanes copy
-// them with cp.async; drafted values go through registers.
+// them through registers.
 template <int D, int NT>
 struct Copier {
     using Sh = TcShape<D, NT>;
-    static constexpr int LPR = D / 8;              // lanes per row of 16-byte chunks
-    static constexpr int RPI = 32 / LPR;           // rows per instruction
     static constexpr int kDrafted = -2;
     TcShared& sh;
     const TreeArgs& a;
     const CUtensorMap *map_k, *map_v;
     uint32_t slots;
     int lane, warp;                                // warp 0 .. 3
-    int next = 0;                                  // ring entries issued
+    int slot = 0, round = 0;                       // of the next ring entry
 
-    __device__ uint32_t entry() const { return slots + (uint32_t)(next % Sh::kSlots) * Sh::kSlotBytes; }
-    __device__ uint64_t* full() const { return &sh.kv_full[next % Sh::kSlots]; }
+    __device__ uint32_t entry() const { return slots + (uint32_t)slot * Sh::kSlotBytes; }
+    __device__ uint64_t* full() const { return &sh.kv_full[slot]; }
 
     // Waits until the next entry's slot is free.
     __device__ void wait_slot()
     {
-        const int use = next / Sh::kSlots;
-        if (use > 0) wait(sh, &sh.kv_empty[next % Sh::kSlots], (uint32_t)(use - 1) & 1, a.status);
+        if (round > 0) wait(sh, &sh.kv_empty[slot], (uint32_t)(round - 1) & 1, a.status);
         __syncwarp();
     }
 
@@ -360,7 +368,6 @@ struct Copier {
     {
         wait_slot();
         const uint32_t there = __ballot_sync(0xffffffffu, cached(r));
-        const uint32_t drafted = __ballot_sync(0xffffffffu, r.page == kDrafted);
         if (a.box > 0 && there == 0xffffffffu) {
             if (lane == 0) {
                 if (is_k) sh.keys[g % kRingMeta][warp] = there;
@@ -368,50 +375,20 @@ struct Copier {
             }
             load_boxes(is_k ? map_k : map_v, w, r);
         } else {
-            const __nv_bfloat16* p = is_k ? source(w, r, a.k_cache, a.k) : source(w, r, a.v_cache, a.v);
-            if (is_k || !drafted) {
-                if (lane == 0) {
-                    if (is_k) sh.keys[g % kRingMeta][warp] = there;
-                    else sh.bad[g % kRingMeta][warp] = 0;
-                }
-                copy_rows32<D>(entry(), warp * 32, p, a.q, lane);
-                cp_async_hold(full());
-            } else {
-                load_drafted(p, drafted, g);
+            const uint32_t drafted = is_k ? 0u : __ballot_sync(0xffffffffu, r.page == kDrafted);
+            const uint32_t bad = copy_rows32<D, NT == 1 ? 8 : 4>(
+                entry(), warp * 32, is_k ? source(w, r, a.k_cache, a.k) : source(w, r, a.v_cache, a.v), drafted, lane);
+            if (lane == 0) {
+                if (is_k) sh.keys[g % kRingMeta][warp] = there;
+                else sh.bad[g % kRingMeta][warp] = bad;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(full());
         }
-        ++next;
-    }
-
-    // V rows with drafted ones among them, through registers.
-    __device__ void load_drafted(const __nv_bfloat16* p, uint32_t drafted, int g)
-    {
-        const unsigned long long mine = reinterpret_cast<unsigned long long>(p);
-        const int c = lane % LPR;
-        uint32_t bad = 0;
-#pragma unroll 1
-        for (int i0 = 0; i0 < 32 / RPI; i0 += 4) {
-            uint4 x[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const unsigned long long src = __shfl_sync(0xffffffffu, mine, (i0 + k) * RPI + lane / LPR);
-                x[k] = make_uint4(0, 0, 0, 0);
-                if (src) x[k] = __ldg(reinterpret_cast<const uint4*>(src + 16ull * c));
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int j = (i0 + k) * RPI + lane / LPR;
-                if (((drafted >> j) & 1) && clear_nonfinite(x[k])) bad |= 1u << j;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(entry() + tile_at(warp * 32 + j, c)),
-                             "r"(x[k].x), "r"(x[k].y), "r"(x[k].z), "r"(x[k].w)
-                             : "memory");
-            }
+        if (++slot == Sh::kSlots) {
+            slot = 0;
+            ++round;
         }
-        bad = __reduce_or_sync(0xffffffffu, bad);
-        if (lane == 0) sh.bad[g % kRingMeta][warp] = bad;
-        fence_proxy_async_smem();
     }
 };
 
@@ -425,15 +402,14 @@ __device__ void copy_role(TcShared& sh, const TreeArgs& a, const CUtensorMap* ma
     for (; go; go = w.next(a)) {
         const int cnt = w.t1 - w.t0;
         auto walk = c.walk_from(w.t0);
-        // the rows of the tile whose V comes next, of the one after it, and of
-        // the next to look up
-        auto row = c.look_up(w, w.t0, walk), row1 = c.look_up(w, w.t0 + 1, walk);
-        auto row2 = c.look_up(w, w.t0 + 2, walk);
-        int jk = 0, jv = 0;                        // tiles whose K, V are on their way
+        // the rows of the tile whose V comes next, of the one after it, and of the
+        // one after that, whose page numbers are on their way
+        typename Copier<D, NT>::Row row = {-1, 0}, row1 = row, row2 = row;
+        int jk = 0, jv = -3;                       // tiles whose K, V are on their way
 #pragma unroll 1
         while (jv < cnt) {
-            const bool is_k = jk < cnt && jk < jv + (NT == 1 ? 2 : 1);
-            c.load(is_k, w, is_k && jk > jv ? row1 : row, g + (is_k ? jk : jv));
+            const bool is_k = jv >= 0 && jk < cnt && jk < jv + (NT == 1 ? 2 : 1);
+            if (jv >= 0) c.load(is_k, w, is_k && jk > jv ? row1 : row, g + (is_k ? jk : jv));
             if (is_k) {
                 ++jk;
             } else {
@@ -447,8 +423,10 @@ __device__ void copy_role(TcShared& sh, const TreeArgs& a, const CUtensorMap* ma
     }
     // After a wait that gave up nothing else has waited for the copies in flight.
     if (*reinterpret_cast<volatile int*>(&sh.dead))
-        for (int e = c.next > Sh::kSlots ? c.next - Sh::kSlots : 0; e < c.next; ++e)
-            mbar_wait(&sh.kv_full[e % Sh::kSlots], (uint32_t)(e / Sh::kSlots) & 1, 1ll << 24);
+        for (int i = 0; i < Sh::kSlots; ++i) {
+            const int r = i < c.slot ? c.round : c.round - 1;
+            if (r >= 0) mbar_wait(&sh.kv_full[i], (uint32_t)r & 1, 1ll << 24);
+        }
 }
 
 template <int D, int NT>
@@ -468,11 +446,8 @@ __device__ void q_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, Piece w
                 p = static_cast<const __nv_bfloat16*>(a.q) +
                     (((long long)w.n * a.Ts + t) * a.Hq + w.hk * a.G + g) * D;
             }
-            copy_rows32<D>(q_smem + (b >> 2) * 128 * D * 2, (b & 3) * 32, p, a.q, lane);
+            copy_rows32<D, NT == 1 ? 8 : 4>(q_smem + (b >> 2) * 128 * D * 2, (b & 3) * 32, p, 0, lane);
         }
-        cp_async_commit();
-        cp_async_wait_all();
-        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full);
         ++piece;
@@ -503,27 +478,24 @@ __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t q_desc, uint6
     }
 }
 
-// D (+)= P V: P in TMEM (8 columns of bf16 pairs per step), V MN-major (16 keys of
-// 128 bytes per step).
+// D (+)= P V for 64 keys: P in TMEM (8 columns of bf16 pairs per step), V MN-major
+// (16 keys of 128 bytes per step).
 __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_t v_desc, uint32_t idesc,
                                          uint32_t accumulate)
 {
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        asm volatile(
-            "{\n\t.reg .pred e, t, f;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\t"
-            "elect.sync _|e, 0xffffffff;\n\t"
-            "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
-            "add.s32 x, %1, 8;\n\tadd.s64 y, %2, 128;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
-            "add.s32 x, %1, 16;\n\tadd.s64 y, %2, 256;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
-            "add.s32 x, %1, 24;\n\tadd.s64 y, %2, 384;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t}" ::"r"(d_tmem),
-            "r"(p_tmem + 32 * b), "l"(v_desc + 512 * b), "r"(idesc), "r"(b ? 1u : accumulate)
-            : "memory");
-    }
+    asm volatile(
+        "{\n\t.reg .pred e, t, f;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+        "add.s32 x, %1, 8;\n\tadd.s64 y, %2, 128;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+        "add.s32 x, %1, 16;\n\tadd.s64 y, %2, 256;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+        "add.s32 x, %1, 24;\n\tadd.s64 y, %2, 384;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t}" ::"r"(d_tmem),
+        "r"(p_tmem), "l"(v_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // Takes the ring's entries in their order.  RT = 128: the scores of tile j + 1
@@ -537,30 +509,39 @@ __device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint3
     using Sh = TcShape<D, NT>;
     constexpr uint32_t id_qk = make_idesc_bf16(128, KT, false, false);
     constexpr uint32_t id_pv = make_idesc_bf16(128, D, false, true);
-    int entry = 0;                                 // next ring entry to take
+    int slot = 0;                                  // of the next ring entry to take
+    uint32_t turn = 0;                             // parity of its use
     int first = 0, piece = 0;                      // tiles of the pieces before, pieces
     const int nt = (NT == 2 && a.R - r0 > 128) ? 2 : 1;
     const uint64_t q_desc = make_sdesc(q_smem, 16, 1024, kSwizzle128B);
 
-    auto take = [&](int e) {
-        wait(sh, &sh.kv_full[e % Sh::kSlots], (uint32_t)(e / Sh::kSlots) & 1, a.status);
-        fence_proxy_async_smem();                  // rows that the lanes copied with cp.async
+    // Waits for the next ring entry; returns its slot.
+    auto take = [&]() {
+        const int mine = slot;
+        wait(sh, &sh.kv_full[mine], turn, a.status);
         __syncwarp();
         tc_fence_after();
+        if (++slot == Sh::kSlots) {
+            slot = 0;
+            turn ^= 1;
+        }
+        return mine;
     };
     auto qk = [&](int i, int e, uint32_t d_tmem) {
-        const uint32_t k = slots + (uint32_t)(e % Sh::kSlots) * Sh::kSlotBytes;
+        const uint32_t k = slots + (uint32_t)e * Sh::kSlotBytes;
         issue_qk<D>(d_tmem, q_desc + (uint64_t)(i * 128 * D * 2 / 16), make_sdesc(k, 16, 1024, kSwizzle128B), id_qk);
     };
     // the output of tile `tile`, the j-th of the piece, of row tile i
     auto pv = [&](int i, int e, int j, int tile, int buf, uint32_t phase) {
+        const uint32_t v = slots + (uint32_t)e * Sh::kSlotBytes;
+        const uint64_t v_desc = make_sdesc(v, KT * 128, 1024, kSwizzle128B);
+        const uint32_t d_tmem = tmem + (i ? Sh::kO1 : Sh::kO0);
         wait(sh, &sh.p_full[buf], phase, a.status);
         if (j == 0 && piece > 0) wait(sh, &sh.o_empty[i], (uint32_t)(piece - 1) & 1, a.status);
         __syncwarp();
         tc_fence_after();
-        const uint32_t v = slots + (uint32_t)(e % Sh::kSlots) * Sh::kSlotBytes;
-        issue_pv(tmem + (i ? Sh::kO1 : Sh::kO0), tmem + buf * Sh::kS1, make_sdesc(v, KT * 128, 1024, kSwizzle128B),
-                 id_pv, j > 0);
+        issue_pv(d_tmem, tmem + buf * Sh::kS1, v_desc, id_pv, j > 0);
+        issue_pv(d_tmem, tmem + buf * Sh::kS1 + 32, v_desc + 512, id_pv, 1);
         mma_commit(&sh.pv_done[i]);
     };
 
@@ -571,7 +552,7 @@ __device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint3
             int jk = 0, jv = 0;
 #pragma unroll 1
             while (jv < cnt) {
-                take(entry);
+                const int entry = take();
                 if (jk < cnt && jk < jv + 2) {
                     const int t = first + jk;
                     qk(0, entry, tmem + (t & 1) * Sh::kS1);
@@ -582,29 +563,27 @@ __device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint3
                     pv(0, entry, jv, t, t & 1, (uint32_t)(t >> 1) & 1);
                     ++jv;
                 }
-                mma_commit(&sh.kv_empty[entry % Sh::kSlots]);
-                ++entry;
+                mma_commit(&sh.kv_empty[entry]);
             }
         } else {
 #pragma unroll 1
             for (int j = -1; j < cnt; ++j) {
                 // V of tile j, then K of tile j + 1
-                const int ev = entry, ek = entry + (j >= 0 ? 1 : 0);
                 const bool more = j + 1 < cnt;
-                if (j >= 0) take(ev);
+                const int ev = j >= 0 ? take() : 0;
+                int ek = 0;
 #pragma unroll 1
                 for (int i = 0; i < nt; ++i) {
                     if (j >= 0) pv(i, ev, j, first + j, i, (uint32_t)(first + j) & 1);
                     if (more) {
-                        if (i == 0) take(ek);
+                        if (i == 0) ek = take();
                         qk(i, ek, tmem + i * Sh::kS1);
                         mma_commit(&sh.s_full[i]);
                     }
                 }
-                if (j >= 0) mma_commit(&sh.kv_empty[ev % Sh::kSlots]);
-                if (more) mma_commit(&sh.kv_empty[ek % Sh::kSlots]);
+                if (j >= 0) mma_commit(&sh.kv_empty[ev]);
+                if (more) mma_commit(&sh.kv_empty[ek]);
                 if (j + 2 == cnt) mma_commit(&sh.q_empty);
-                entry += (j >= 0 ? 1 : 0) + (more ? 1 : 0);
             }
         }
         first += cnt;
@@ -651,47 +630,39 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, Piece w, bool go, 
             wait(sh, &sh.s_full[b], phase, a.status);
             __syncwarp();
             tc_fence_after();
-            bool waited = tile == 0;
             auto wait_last = [&]() {
-                if (waited) return;
-                waited = true;
-                wait(sh, &sh.pv_done[NT == 1 ? 0 : wg], (uint32_t)(tile - 1) & 1, a.status);
-                __syncwarp();
-                tc_fence_after();
+                if (tile > 0) wait(sh, &sh.pv_done[NT == 1 ? 0 : wg], (uint32_t)(tile - 1) & 1, a.status);
             };
             if (live) {
+                const uint4 there = *reinterpret_cast<const uint4*>(sh.keys[tile % kRingMeta]);
+                if ((there.x & there.y & there.z & there.w) != 0xffffffffu) {
+                    // masked scores become -inf in place, 32 keys at a time
+                    const int nc = w.ctx - t * KT; // key j is drafted node j - nc from j = nc on
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t keep = sh.keys[tile % kRingMeta][c], y[32];
+                        const int i = 32 * c - nc; // the node at bit 0 of this word
+                        if (i >= 0) keep |= i < 64 ? (uint32_t)(seen >> i) : 0u;
+                        else if (i > -32) keep |= (uint32_t)(seen << -i);
+                        tmem_ld32(ts + 32 * c, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!((keep >> j) & 1)) y[j] = 0xff800000u;
+                        tmem_st32(ts + 32 * c, y);
+                    }
+                    tmem_st_wait();
+                }
                 uint32_t x[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, x[c]);
-                uint32_t keep[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) keep[c] = sh.keys[tile % kRingMeta][c];
-                const int nc = w.ctx - t * KT;     // key j is drafted node j - nc from j = nc on
-                if (nc < KT) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int i = 32 * c - nc; // the node at bit 0 of this word
-                        if (i >= 0) keep[c] |= i < 64 ? (uint32_t)(seen >> i) : 0u;
-                        else if (i > -32) keep[c] |= (uint32_t)(seen << -i);
-                    }
-                }
-                const bool all = (keep[0] & keep[1] & keep[2] & keep[3]) == 0xffffffffu;
                 tmem_ld_wait();
-                if (!all) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!((keep[c] >> j) & 1)) x[c][j] = 0xff800000u;      // -inf
-                }
                 float tops[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    tops[c] = __uint_as_float(x[c][0]);
+                    tops[c] = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
 #pragma unroll
-                    for (int j = 1; j < 31; j += 2)
-                        tops[c] = fmaxf(tops[c], fmaxf(__uint_as_float(x[c][j]), __uint_as_float(x[c][j + 1])));
-                    tops[c] = fmaxf(tops[c], __uint_as_float(x[c][31]));
+                    for (int j = 2; j < 32; j += 2) tops[c] = max3(tops[c], x[c][j], x[c][j + 1]);
                 }
                 float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 top *= a.scale_log2;               // the scale is positive on this path
@@ -703,6 +674,8 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, Piece w, bool go, 
                     l *= f;
                     if (t > w.t0) {
                         wait_last();
+                        __syncwarp();
+                        tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
                             uint32_t y[16];
@@ -790,31 +763,30 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, Piece w, bool go, 
                 }
                 tmem_st_wait();
             }
-            uint32_t x[D / 32][32];
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) tmem_ld32(to + 32 * c, x[c]);
-            tmem_ld_wait();
-            if (mine && whole) {
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c)
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t x[32];
+                tmem_ld32(to + 32 * c, x);
+                tmem_ld_wait();
+                if (mine && whole) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
                         uint32_t y[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            y[j] = pack_bf16x2(__uint_as_float(x[c][i + 2 * j]) * scale_o,
-                                               __uint_as_float(x[c][i + 2 * j + 1]) * scale_o);
+                            y[j] = pack_bf16x2(__uint_as_float(x[i + 2 * j]) * scale_o,
+                                               __uint_as_float(x[i + 2 * j + 1]) * scale_o);
                         *reinterpret_cast<uint4*>(op + 32 * c + i) =
                             seen == 0 ? make_uint4(0, 0, 0, 0) : make_uint4(y[0], y[1], y[2], y[3]);
                     }
-            } else if (mine) {
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c)
+                } else if (mine) {
+                    // of an unused node whatever is there: its weight is 0
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
                         *reinterpret_cast<uint4*>(part + (size_t)local * D + 32 * c + i) =
-                            seen == 0 ? make_uint4(0, 0, 0, 0)
-                                      : make_uint4(x[c][i], x[c][i + 1], x[c][i + 2], x[c][i + 3]);
+                            make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                }
+                __syncwarp();                      // before the next collective load
             }
             if (mine && !whole) {
                 part[RT * D + local] = seen == 0 ? -INFINITY : m;
