@@ -42,19 +42,14 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
     return r;
 }
 
-// Eight consecutive values (16-byte pieces x, the next one `next` pieces on) as
-// four pairs of fp32.
-__device__ __forceinline__ void pairs8(const float*, const uint4* p, int next, uint64_t (&x)[4])
+// 16 bytes of values as pairs of fp32.
+__device__ __forceinline__ void pairs(const float*, const uint4& a, uint64_t (&x)[2])
 {
-    const uint4 a = p[0], b = p[next];
     x[0] = (uint64_t)a.y << 32 | a.x;
     x[1] = (uint64_t)a.w << 32 | a.z;
-    x[2] = (uint64_t)b.y << 32 | b.x;
-    x[3] = (uint64_t)b.w << 32 | b.z;
 }
-__device__ __forceinline__ void pairs8(const __nv_bfloat16*, const uint4* p, int, uint64_t (&x)[4])
+__device__ __forceinline__ void pairs(const __nv_bfloat16*, const uint4& a, uint64_t (&x)[4])
 {
-    const uint4 a = p[0];
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = (uint64_t)(w[i] & 0xFFFF0000u) << 32 | (w[i] << 16);
@@ -70,9 +65,9 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, const void* a
         : "memory");
 }
 
-// Up to 8 query rows per cache head: a stream.  D / 8 lanes share a key, eight
-// channels each, and the groups of a CTA take keys in turn: a lane has its eight
-// channels of q and of the output for all eight rows in registers.  Its pieces
+// Up to 8 query rows per cache head: a stream.  A group of lanes shares a key, 16
+// bytes each, and the groups of a CTA take keys in turn: a lane has its channels
+// of q and of the output for all eight rows in registers.  Its pieces
 // of K and V come by cp.async through kAhead stages of shared memory that no
 // other lane touches, page numbers two steps earlier still.  The scores of a key
 // are added up across its lanes so that each lane ends with the rows it owns
@@ -81,18 +76,26 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, const void* a
 // maximum and sum per owned row (a maximum moves when a score exceeds it by more
 // than 8, in base 2); they meet at the end of a piece.  Nothing in the loop
 // waits for another warp.
-constexpr int kAhead = 4;            // stages of two keys
+// Bound by instructions between the loads (eight rows of FMAs and one butterfly
+// a key), not by HBM: fp32, 16 heads, 5 nodes, 8 contexts of 10 to 5000 rows, d =
+// 64: 60 us (2.3 TB/s); d = 128, 8 nodes, 8 x 4096 rows: 185 us (2.9 TB/s).  With
+// 8 bytes per lane, whose groups are twice as wide, the first took 72 us.
+constexpr int kAhead = 4;            // stages of two keys; 6 leave room for fewer CTAs: 95 us
 constexpr int kStreamRows = 8;
 constexpr int kStreamThreads = 128;
 constexpr int kStreamKeys = 64;      // keys per tile of the work split
 constexpr int kStreamLead = 2;
-constexpr int kStreamCtas = 2;       // per SM: registers
+// Per SM, by the registers that eight rows of q and of the output take.  fp32
+// (4 channels a lane): 3, 4, 5 and 6 took 67, 60, 83 and 126 us.  bf16 (8
+// channels, fp32 output, d = 128, 8 x 4096 rows): 2, 3 and 4 took 158, 139 and 237.
+__host__ __device__ constexpr int stream_ctas(bool fp32) { return fp32 ? 4 : 3; }
 
 template <typename TI, typename TO, int D>
-__global__ void __launch_bounds__(kStreamThreads, kStreamCtas)
+__global__ void __launch_bounds__(kStreamThreads, stream_ctas(sizeof(TI) == 4))
 tree_attention_stream_kernel(const TreeArgs a)
 {
-    constexpr int RT = kStreamRows, LK = D / 8, GW = 32 / LK;     // lanes per key, groups per warp
+    constexpr int RT = kStreamRows, CH = 16 / (int)sizeof(TI);  // rows, channels per lane
+    constexpr int CP = CH / 2, LK = D / CH, GW = 32 / LK;       // pairs, lanes per key, groups per warp
     constexpr int kWarps = kStreamThreads / 32, kStep = kWarps * GW;
     constexpr int RO = RT / LK > 0 ? RT / LK : 1;               // rows a lane owns
     constexpr float kSlack = 8.f;
@@ -103,11 +106,10 @@ tree_attention_stream_kernel(const TreeArgs a)
     __shared__ __align__(16) float sh_o[kWarps][RT][D];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane % LK, sub = lane / LK;                   // lane of the group, group of the warp
-    // the first row this lane owns; lanes g and g ^ 1 share it when LK > RT
+    // the first row this lane owns; LK / RT lanes share it when LK > RT
     const int own = LK >= RT ? g / (LK / RT) : g * RO;
     const TI* q = static_cast<const TI*>(a.q);
-    constexpr int PC = sizeof(TI) / 2, VR = 16 / (int)sizeof(TI);   // 16-byte pieces of eight values, values of one
-    extern __shared__ __align__(16) uint4 ring[];               // [kAhead][2 keys][K, V][PC][threads]
+    extern __shared__ __align__(16) uint4 ring[];               // [kAhead][2 keys][K, V][threads]
 
     const int group = blockIdx.x / a.row_tiles, r0 = (blockIdx.x % a.row_tiles) * RT;
     const int rows = a.R - r0 < RT ? a.R - r0 : RT;
@@ -128,18 +130,18 @@ tree_attention_stream_kernel(const TreeArgs a)
                 tree_masks(a.parent ? a.parent + (long long)n * a.Ts : nullptr, a.Ts, tid, anc, up);
             have = n;
         }
-        // q, scaled, eight channels of every row
-        uint64_t qr[RT][4], acc[RT][4];
+        // q, scaled, this lane's channels of every row
+        uint64_t qr[RT][CP], acc[RT][CP];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) qr[r][i] = acc[r][i] = 0;
+            for (int i = 0; i < CP; ++i) qr[r][i] = acc[r][i] = 0;
             if (r < rows) {
                 const int t = (r0 + r) / a.G, h = (r0 + r) % a.G;
-                const TI* from = q + (((long long)n * a.Ts + t) * a.Hq + hk * a.G + h) * D + 8 * g;
-                pairs8(q, reinterpret_cast<const uint4*>(from), 1, qr[r]);
+                const TI* from = q + (((long long)n * a.Ts + t) * a.Hq + hk * a.G + h) * D + CH * g;
+                pairs(q, *reinterpret_cast<const uint4*>(from), qr[r]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) qr[r][i] = mul2(qr[r][i], pack2(a.scale_log2, a.scale_log2));
+                for (int i = 0; i < CP; ++i) qr[r][i] = mul2(qr[r][i], pack2(a.scale_log2, a.scale_log2));
             }
         }
         __syncthreads();
@@ -176,7 +178,7 @@ tree_attention_stream_kernel(const TreeArgs a)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const TI *kp = nullptr, *vp = nullptr;
-                long long off = (long long)hk * D + 8 * g;
+                long long off = (long long)hk * D + CH * g;
                 if (page[i] >= 0 && page[i] < a.num_pages) {
                     off += (long long)page[i] * a.page_stride + (long long)slot[i] * row_elems;
                     kp = static_cast<const TI*>(a.k_cache) + off;
@@ -188,12 +190,9 @@ tree_attention_stream_kernel(const TreeArgs a)
                 }
                 const int bit = 2 * stage + i;
                 there = (there & ~(1u << bit)) | ((unsigned)(kp != nullptr) << bit);
-                uint4* to = ring + (bit * 2 * PC) * kStreamThreads + tid;
-#pragma unroll
-                for (int c = 0; c < PC; ++c) {
-                    copy16(to + c * kStreamThreads, kp ? kp + c * VR : nullptr, q);
-                    copy16(to + (PC + c) * kStreamThreads, vp ? vp + c * VR : nullptr, q);
-                }
+                uint4* to = ring + bit * 2 * kStreamThreads + tid;
+                copy16(to, kp, q);
+                copy16(to + kStreamThreads, vp, q);
                 at += kStep;
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -212,18 +211,18 @@ tree_attention_stream_kernel(const TreeArgs a)
             fetch(stage ? stage - 1 : kAhead - 1);
             look();
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-            const uint4* mine = ring + (stage * 4 * PC) * kStreamThreads + tid;
+            const uint4* mine = ring + stage * 4 * kStreamThreads + tid;
             // the scores of this group's keys: partial sums of all rows
             float s[2][RT];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                uint64_t x[4];
-                pairs8(q, mine + u * 2 * PC * kStreamThreads, kStreamThreads, x);
+                uint64_t x[CP];
+                pairs(q, mine[u * 2 * kStreamThreads], x);
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     uint64_t t = mul2(qr[r][0], x[0]);
 #pragma unroll
-                    for (int i = 1; i < 4; ++i) t = fma2(qr[r][i], x[i], t);
+                    for (int i = 1; i < CP; ++i) t = fma2(qr[r][i], x[i], t);
                     const float2 y = unpack2(t);
                     s[u][r] = y.x + y.y;
                 }
@@ -277,7 +276,7 @@ tree_attention_stream_kernel(const TreeArgs a)
                     const int from = LK >= RT ? r * (LK / RT) : r / RO;
                     const float fr = __shfl_sync(0xffffffffu, f[r % RO], (lane & ~(LK - 1)) + from);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[r][i] = mul2(acc[r][i], pack2(fr, fr));
+                    for (int i = 0; i < CP; ++i) acc[r][i] = mul2(acc[r][i], pack2(fr, fr));
                 }
             }
             float p[2][RO];
@@ -291,8 +290,8 @@ tree_attention_stream_kernel(const TreeArgs a)
             const bool tail = __any_sync(0xffffffffu, node + kStep >= 0);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                uint64_t x[4];
-                pairs8(q, mine + (u * 2 + 1) * PC * kStreamThreads, kStreamThreads, x);
+                uint64_t x[CP];
+                pairs(q, mine[(u * 2 + 1) * kStreamThreads], x);
                 const int nd = node + u * kStep;
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
@@ -302,7 +301,7 @@ tree_attention_stream_kernel(const TreeArgs a)
                     if (tail && nd >= 0 && !(r < rows && nd < a.Ts && ((anc[(r0 + r) / a.G] >> nd) & 1ull)))
                         continue;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[r][i] = fma2(pack2(pr, pr), x[i], acc[r][i]);
+                    for (int i = 0; i < CP; ++i) acc[r][i] = fma2(pack2(pr, pr), x[i], acc[r][i]);
                 }
             }
             pos += 2 * kStep;
@@ -334,21 +333,22 @@ tree_attention_stream_kernel(const TreeArgs a)
         for (int r = 0; r < RT; ++r) {
             const int from = LK >= RT ? r * (LK / RT) : r / RO;
             const float fr = __shfl_sync(0xffffffffu, m[r % RO], (lane & ~(LK - 1)) + from);
-            float y[8];
+            float y[CH];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < CP; ++i) {
                 const float2 z = unpack2(acc[r][i]);
                 // a group that has seen nothing of a row has an output of 0
                 y[2 * i] = fr == 0.f ? 0.f : z.x * fr;
                 y[2 * i + 1] = fr == 0.f ? 0.f : z.y * fr;
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < CH; ++i)
 #pragma unroll
                 for (int off = LK; off < 32; off <<= 1) y[i] += __shfl_xor_sync(0xffffffffu, y[i], off);
             if (sub == 0) {
-                *reinterpret_cast<float4*>(&sh_o[warp][r][8 * g]) = make_float4(y[0], y[1], y[2], y[3]);
-                *reinterpret_cast<float4*>(&sh_o[warp][r][8 * g + 4]) = make_float4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+                for (int i = 0; i < CH; i += 4)
+                    *reinterpret_cast<float4*>(&sh_o[warp][r][CH * g + i]) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
             }
         }
         __syncthreads();
@@ -739,7 +739,7 @@ cudaError_t launch_d(const TreeArgs& a, int rt, cudaStream_t stream)
 {
     const bool stream_kernel = rt == kStreamRows;
     auto kern = stream_kernel ? tree_attention_stream_kernel<TI, TO, D> : tree_attention_tile_kernel<TI, TO, D>;
-    const size_t bytes = stream_kernel ? (size_t)kAhead * 4 * (sizeof(TI) / 2) * kStreamThreads * 16
+    const size_t bytes = stream_kernel ? (size_t)kAhead * 4 * kStreamThreads * 16
                                        : TileShape<TI, D>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
@@ -764,14 +764,14 @@ cudaError_t launch_typed(const TreeArgs& a, int rt, int d, cudaStream_t stream)
 
 }  // namespace
 
-TreePlan tree_plan(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, int sms, bool tc)
+TreePlan tree_plan(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, bool fp32, int sms, bool tc)
 {
     const int R = Ts * (Hq / Hkv);
     TreePlan p;
     p.tc = tc;
     p.rt = tc ? (R <= 128 ? 128 : 256) : (R <= kStreamRows ? kStreamRows : kTileRows);
     p.row_tiles = (R + p.rt - 1) / p.rt;
-    const int ctas = (sms > 0 ? sms : 1) * (tc ? 1 : p.rt == kStreamRows ? kStreamCtas : tile_ctas(d));
+    const int ctas = (sms > 0 ? sms : 1) * (tc ? 1 : p.rt == kStreamRows ? stream_ctas(fp32) : tile_ctas(d));
     p.groups = ctas / p.row_tiles > 1 ? ctas / p.row_tiles : 1;
     return p;
 }
@@ -787,7 +787,7 @@ size_t tree_workspace_bytes(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, kda_
 {
     size_t most = 0;
     for (int tc = 0; tc <= (int)tree_tc_supported(d, dtype); ++tc) {
-        const TreePlan p = tree_plan(Ts, Hq, Hkv, d, sms, tc != 0);
+        const TreePlan p = tree_plan(Ts, Hq, Hkv, d, dtype == KDA_FP32, sms, tc != 0);
         const size_t b = (size_t)p.groups * p.row_tiles * 2 * p.rt * (d + 2) * sizeof(float);
         if (b > most) most = b;
     }
@@ -800,7 +800,7 @@ cudaError_t launch_tree_attention(TreeArgs args, int32_t d, kda_dtype_t dtype, i
                                   cudaStream_t stream)
 {
     const bool tc = tree_tc_supported(d, dtype) && args.scale_log2 > 0.f && getenv("KDA_FORCE_SIMT") == nullptr;
-    const TreePlan plan = tree_plan(args.Ts, args.Hq, args.Hkv, d, sms, tc);
+    const TreePlan plan = tree_plan(args.Ts, args.Hq, args.Hkv, d, dtype == KDA_FP32, sms, tc);
     args.groups = plan.groups;
     args.row_tiles = plan.row_tiles;
     if (plan.tc) {
