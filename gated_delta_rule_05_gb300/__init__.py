@@ -474,6 +474,17 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
+def _new(shape, dtype, device, stream):
+    """An output or workspace the caller did not pass.  It belongs to the stream
+    that uses it: memory freed on the current stream, or reused there after the
+    call, may still be in use by the other one."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _call(name, device, stream, *args):
     """lib().<name>(*args, stream) on ``device``; raises KdaError."""
     torch = _torch()
@@ -515,9 +526,9 @@ def kda_decode_tree(q, k, v, log_alpha, beta, S_in, parent=None, *, o=None, stat
     if parent is not None:
         _shape("parent", parent, (N, Ts))
     if o is None:
-        o = torch.empty((N, Ts, H, dv), dtype=o_dtype, device=q.device)
+        o = _new((N, Ts, H, dv), o_dtype, q.device, stream)
     if states is None:
-        states = torch.empty((N, Ts, H, dk, dv), dtype=torch.float32, device=q.device)
+        states = _new((N, Ts, H, dk, dv), torch.float32, q.device, stream)
     _check_cuda("o", o, o_dtype)
     _check_cuda("states", states, torch.float32)
     _shape("o", o, (N, Ts, H, dv))
@@ -579,7 +590,7 @@ def kda_tree_attention(q, k, v, k_cache, v_cache, page_table, lengths, parent=No
     if pages > 1 and k_cache.stride(0) != v_cache.stride(0):
         raise ValueError("k_cache and v_cache must have the same page stride")
     if o is None:
-        o = torch.empty((N, Ts, Hq, d), dtype=o_dtype, device=dev)
+        o = _new((N, Ts, Hq, d), o_dtype, dev, stream)
     _check_cuda("o", o, o_dtype)
     _shape("o", o, (N, Ts, Hq, d))
     if workspace is None:
@@ -588,7 +599,7 @@ def kda_tree_attention(q, k, v, k_cache, v_cache, page_table, lengths, parent=No
         else:
             with torch.cuda.device(dev):
                 need = lib().kda_tree_attention_workspace_bytes(N, Ts, Hq, Hkv, d, dt)
-        workspace = torch.empty(need or 256, dtype=torch.uint8, device=dev)
+        workspace = _new((need or 256,), torch.uint8, dev, stream)
     _check_cuda("workspace", workspace)
     _call("kda_tree_attention", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           _address(parent), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
@@ -617,7 +628,7 @@ def kda_token_logprobs(logits, tokens=None, num_top=0, *, logprobs=None, entropy
     _check_cuda("tokens", tokens, torch.int32)
     J = 0 if tokens is None else tokens.shape[1]
     K = int(num_top)
-    new = lambda *s, **kw: torch.empty(s, device=dev, **{"dtype": torch.float32, **kw})
+    new = lambda *s, dtype=torch.float32: _new(s, dtype, dev, stream)
     if tokens is not None:
         _shape("tokens", tokens, (T, J))
     logprobs = new(T, J) if logprobs is None else logprobs
@@ -659,7 +670,7 @@ def _cache_rows(name, k, v, middle, k_cache, v_cache, page_table, lengths, new_l
     _shape("lengths", lengths, (N,))
     _shape("page_table", page_table, (N, page_table.shape[1]))
     if new_lengths is None:
-        new_lengths = torch.empty_like(lengths)
+        new_lengths = _new((N,), torch.int32, dev, stream)
     _check_cuda("new_lengths", new_lengths, torch.int32)
     _shape("new_lengths", new_lengths, (N,))
     _call(name, dev, stream, k.data_ptr(), v.data_ptr(), *middle, page_table.data_ptr(),
