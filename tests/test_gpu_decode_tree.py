@@ -120,3 +120,47 @@ def test_gather_of_an_accepted_node(kda):
     S = x[5].cuda()
     out = kda.kda_state_gather(st, S, node + 1)
     assert torch.equal(out[0], st[0, 4]) and torch.equal(out[1], S[1]) and torch.equal(out[2], st[2, 2])
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_many_sequences(kda, d, dtype):
+    # more (sequence, head) pairs than SMs
+    N, Ts, H = 170, 9, 2
+    _, *x = multi_inputs(N, Ts, H, d, dtype, 1000 + d)
+    parent = random_trees(N, Ts, np.random.default_rng(d))
+    o, st = run(kda, x, parent)
+    few = [0, 1, 76, 151, 152, 169]
+    o_ref, st_ref = reference(*(y[few] for y in x), parent[few])
+    compare_out(o[few], o_ref, TOL[dtype], "o")
+    used = np.array([[lineage(p, t) is not None for t in range(Ts)] for p in parent])
+    assert_close(to64(st[few])[used[few]], st_ref[used[few]], TOL[dtype], "states")
+    assert torch.all(st[~torch.from_numpy(used).cuda()] == 7.0), "an unused node's state was written"
+    assert torch.all(o[~torch.from_numpy(used).cuda()] == 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_chains_are_decode_multi_bit_for_bit(kda, d):
+    N, Ts, H = 90, 6, 2
+    _, *x = multi_inputs(N, Ts, H, d, "bf16", 1010)
+    q, k, v, g, b, S = (t.cuda() for t in x)
+    o, st = kda.kda_decode_multi(q, k, v, g, b, S)
+    o2, st2 = kda.kda_decode_tree(q, k, v, g, b, S)
+    assert torch.equal(o, o2) and torch.equal(st, st2)
+
+
+@pytest.mark.parametrize("N,H", [(1, 2), (80, 2)])
+@pytest.mark.parametrize("kind", ["comb", "binary", "star of stars"])
+def test_many_states_with_children_to_come(kda, kind, N, H):
+    # more open states than the kernel holds on chip at once
+    Ts, d = 63, 128
+    t = np.arange(Ts)
+    parent = {"comb": np.where(t < 32, t - 1, t - 32), "binary": (t + 1) // 2 - 1,
+              "star of stars": np.where(t < 8, -1, (t - 8) % 8)}[kind].astype(np.int32)
+    parent = np.tile(parent, (N, 1))
+    _, *x = multi_inputs(N, Ts, H, d, "bf16", 1020)
+    o, st = run(kda, x, parent)
+    few = [0, N - 1]
+    o_ref, st_ref = reference(*(y[few] for y in x), parent[few])
+    compare_out(o[few], o_ref, TOL["bf16"], "o")
+    assert_close(to64(st[few]), st_ref, TOL["bf16"], "states")

@@ -36,7 +36,7 @@ def reference(x, tokens, K):
     return logp, H, order, np.take_along_axis(x, order, -1) - lse
 
 
-def check(kda, x, J=3, K=8, seed=0):
+def check(kda, x, J=3, K=8, seed=0, threads=256):
     T, V = x.shape
     K = min(K, V)
     tokens = np.random.default_rng(seed).integers(0, V, (T, J)).astype(np.int32)
@@ -46,7 +46,7 @@ def check(kda, x, J=3, K=8, seed=0):
     assert np.array_equal(ids.cpu().numpy(), rids)
     big = np.abs(x.double().cpu().numpy())
     big = float(big[np.isfinite(big)].max())
-    tol = (V / 256 + 64) * 2.0 ** -23 + 2.0 ** -22 * big
+    tol = (V / threads + 64) * 2.0 ** -23 + 2.0 ** -22 * big
     for got, want in ((logp, rl), (top, rtop)):
         got = got.double().cpu().numpy()
         assert np.array_equal(np.isneginf(got), np.isneginf(want))
@@ -152,3 +152,23 @@ def test_another_stream(kda):
     s.synchronize()
     for y, z in zip(a, b):
         assert torch.equal(y, z)
+
+
+# Many rows, whose blocks have 128 threads.
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [1, 130, 5003, 20000])
+@pytest.mark.parametrize("K", [1, 32])
+def test_many_rows(kda, dtype, V, K):
+    check(kda, logits(900, V, dtype, V + K), K=K, threads=128)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind", ["equal", "rising", "falling", "two values"])
+def test_many_rows_of_ties_and_sorted_values(kda, dtype, kind):
+    V = 7001
+    i = torch.arange(V, device="cuda", dtype=torch.float32)
+    row = {"equal": i * 0 + 1.5, "rising": i / V * 8 - 4, "falling": 4 - i / V * 8,
+           "two values": (i % 5 == 3).float()}[kind]
+    x = row.to(dtype).expand(700, V).contiguous()
+    x[1::7, ::2] = float("-inf")
+    check(kda, x, K=32, threads=128)

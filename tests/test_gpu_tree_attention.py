@@ -179,6 +179,35 @@ def test_many_tiles_in_a_range(kda, Ts, G, d):
         check(run(kda, inp), *attention_reference(inp), exact_p=False)
 
 
+@pytest.mark.parametrize("dtype,d", [(F32, 16), (F32, 32), (F32, 64), (F32, 128), (BF16, 16), (BF16, 128)])
+@pytest.mark.parametrize("Ts,G", [(1, 1), (4, 2), (5, 4), (33, 3)])
+def test_many_tiles_in_a_range_of_the_fp32_kernels(kda, Ts, G, dtype, d):
+    # 1, 8, 20 and 99 query rows per cache head: the stream and the tiles
+    rng = np.random.default_rng(18)
+    for N, lengths in ((2, [9000, 5001]), (160, rng.integers(0, 300, 160))):
+        inp = AttentionInputs(N, Ts, 2 * G, 2, d, 48, lengths, dtype, seed=N + G)
+        inp.parent[:, 5:] = np.where(np.arange(5, Ts) % 8 == 0, inp.parent[:, 5:], -2)
+        check(run(kda, inp, o_dtype=F32), *attention_reference(inp), exact_p=True)
+
+
+@pytest.mark.parametrize("page", [1, 7, 24, 40, 96, 1000])
+@pytest.mark.parametrize("Ts,G", [(5, 4), (40, 4)])
+def test_page_sizes_over_full_tiles(kda, page, Ts, G):
+    # pages that end inside a tile, and inside the boxes of a bulk copy
+    inp = AttentionInputs(3, Ts, 2 * G, 2, 128, page, [1500, 129, 1024], BF16, seed=page)
+    inp.parent[:, 6:] = -2
+    check(run(kda, inp), *attention_reference(inp), exact_p=False)
+
+
+def test_the_cuda_core_kernels_agree(kda, monkeypatch):
+    inp = AttentionInputs(3, 12, 8, 2, 128, 64, [1500, 0, 77], BF16, seed=19)
+    ref = attention_reference(inp)
+    monkeypatch.setenv("KDA_FORCE_SIMT", "1")
+    check(run(kda, inp), *ref, exact_p=False)
+    monkeypatch.delenv("KDA_FORCE_SIMT")
+    check(run(kda, inp), *ref, exact_p=False)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_same_bits_every_time_and_on_another_stream(kda, dtype):
     inp = AttentionInputs(3, 16, 8, 2, 128, 64, [4000, 17, 900], dtype, seed=13)
@@ -191,6 +220,23 @@ def test_same_bits_every_time_and_on_another_stream(kda, dtype):
             again = kda.kda_tree_attention(**args)
         s.synchronize()
         assert torch.equal(first, again)
+
+
+def test_a_workspace_of_the_given_stream(kda):
+    # what the call allocates stays its own while the given stream still runs
+    inp = AttentionInputs(1, 4, 8, 2, 128, 64, [4000], BF16, seed=20)
+    args = inp.on("cuda")
+    want = kda.kda_tree_attention(**args)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)               # some 10 ms
+    o = kda.kda_tree_attention(**args, stream=s)
+    need = kda.kda_tree_attention_workspace_bytes(1, 4, 8, 2, 128, kda.KDA_BF16)
+    for _ in range(4):
+        torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
 
 
 def test_offsets_beyond_32_bits(kda):
