@@ -8,6 +8,8 @@
 // ancestors.  One pass over the keys with the running maximum m and sum l: a
 // new tile with maximum m' scales o and l by e^{m - m'}.  Exponentials are
 // taken in base 2 with log2(e) folded into q.
+#include <type_traits>
+
 #include "kda_tree.cuh"
 
 namespace kda {
@@ -55,14 +57,19 @@ __device__ __forceinline__ void pairs(const __nv_bfloat16*, const uint4& a, uint
     for (int i = 0; i < 4; ++i) x[i] = (uint64_t)(w[i] & 0xFFFF0000u) << 32 | (w[i] << 16);
 }
 
-// 16 bytes to shared memory, asynchronously; zeros when src is null.
-__device__ __forceinline__ void copy16(void* dst, const void* src, const void* any)
+__device__ __forceinline__ float ex2(float x)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.eq.u64 p, %1, 0;\n\t"
-        "cp.async.cg.shared.global [%0], [%2], 16, p;\n\t}" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
-        "l"(src), "l"(src ? src : any)
-        : "memory");
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16 bytes to shared memory, asynchronously; zeros, and no read, unless there.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+                 "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
 }
 
 // Up to 8 query rows per cache head: a stream.  A group of lanes shares a key, 16
@@ -76,19 +83,23 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, const void* a
 // maximum and sum per owned row (a maximum moves when a score exceeds it by more
 // than 8, in base 2); they meet at the end of a piece.  Nothing in the loop
 // waits for another warp.
-// Bound by instructions between the loads (eight rows of FMAs and one butterfly
-// a key), not by HBM: fp32, 16 heads, 5 nodes, 8 contexts of 10 to 5000 rows, d =
-// 64: 60 us (2.3 TB/s); d = 128, 8 nodes, 8 x 4096 rows: 185 us (2.9 TB/s).  With
-// 8 bytes per lane, whose groups are twice as wide, the first took 72 us.
-constexpr int kAhead = 4;            // stages of two keys; 6 leave room for fewer CTAs: 95 us
+// The context's keys have a loop of their own, without the tests that drafted
+// nodes need.  Bound by instructions between the loads (eight rows of FMAs and one
+// butterfly a key; 60 % of the issue slots), not by HBM: fp32, 16 heads, 5 nodes, 8
+// contexts of 10 to 4000 rows, d = 64: 46 us (3.0 TB/s), 60 with one loop for all
+// keys and with selects in the butterfly instead of q's permuted places; d = 128, 8
+// nodes, 8 x 4096 rows: 132 us (4.1 TB/s).  K and V straight to registers, one or
+// two steps ahead: 1.8 times as long; 4 keys a step 1.2 times.
+constexpr int kAhead = 4;            // stages of two keys; 3 cost 5 % with one row
 constexpr int kStreamRows = 8;
 constexpr int kStreamThreads = 128;
 constexpr int kStreamKeys = 64;      // keys per tile of the work split
 constexpr int kStreamLead = 2;
 // Per SM, by the registers that eight rows of q and of the output take.  fp32
-// (4 channels a lane): 3, 4, 5 and 6 took 67, 60, 83 and 126 us.  bf16 (8
-// channels, fp32 output, d = 128, 8 x 4096 rows): 2, 3 and 4 took 158, 139 and 237.
-__host__ __device__ constexpr int stream_ctas(bool fp32) { return fp32 ? 4 : 3; }
+// (4 channels a lane): 3, 4 and 5 took 50, 50 and 83 us at 8 x 2100 rows; at 5 they
+// spill.  bf16 (8 channels, fp32 output, d = 128, 8 x 4096 rows): 2 and 3 took 100
+// and 127.
+__host__ __device__ constexpr int stream_ctas(bool fp32) { return fp32 ? 4 : 2; }
 
 template <typename TI, typename TO, int D>
 __global__ void __launch_bounds__(kStreamThreads, stream_ctas(sizeof(TI) == 4))
@@ -130,14 +141,16 @@ tree_attention_stream_kernel(const TreeArgs a)
                 tree_masks(a.parent ? a.parent + (long long)n * a.Ts : nullptr, a.Ts, tid, anc, up);
             have = n;
         }
-        // q, scaled, this lane's channels of every row
+        // q, scaled, this lane's channels of every row; place r has row r ^ own, so
+        // that the places that a step of the butterfly keeps are the same in all lanes
         uint64_t qr[RT][CP], acc[RT][CP];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
 #pragma unroll
             for (int i = 0; i < CP; ++i) qr[r][i] = acc[r][i] = 0;
-            if (r < rows) {
-                const int t = (r0 + r) / a.G, h = (r0 + r) % a.G;
+            const int row = r0 + (r ^ own);
+            if (row < a.R) {
+                const int t = row / a.G, h = row % a.G;
                 const TI* from = q + (((long long)n * a.Ts + t) * a.Hq + hk * a.G + h) * D + CH * g;
                 pairs(q, *reinterpret_cast<const uint4*>(from), qr[r]);
 #pragma unroll
@@ -157,13 +170,14 @@ tree_attention_stream_kernel(const TreeArgs a)
         // position to fetch and the next to look up.
         int pos = w.t0 * kStreamKeys + warp * GW + sub, at = pos;
         int in = pos, in_p = pos / a.page_size, in_slot = pos - in_p * a.page_size;
+        const int cached_end = ctx < keys_end ? ctx : keys_end;
         int page[2], slot[2];
         auto look = [&]() {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 page[i] = -1;
                 slot[i] = in_slot;
-                if (in < ctx && in < keys_end) page[i] = __ldg(table + in_p);
+                if (in < cached_end) page[i] = __ldg(table + in_p);
                 in += kStep;
                 in_p += step_pages;
                 in_slot += step_rows;
@@ -173,26 +187,27 @@ tree_attention_stream_kernel(const TreeArgs a)
                 }
             }
         };
+        // (a cache without pages is never read, but an address is formed)
+        const TI* kc = a.num_pages > 0 ? static_cast<const TI*>(a.k_cache) + (long long)hk * D + CH * g : q;
+        const TI* vc = a.num_pages > 0 ? static_cast<const TI*>(a.v_cache) + (long long)hk * D + CH * g : q;
         unsigned there = 0;                         // bit 2 s + i: key i of stage s exists
         auto fetch = [&](int stage) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const TI *kp = nullptr, *vp = nullptr;
-                long long off = (long long)hk * D + CH * g;
-                if (page[i] >= 0 && page[i] < a.num_pages) {
-                    off += (long long)page[i] * a.page_stride + (long long)slot[i] * row_elems;
-                    kp = static_cast<const TI*>(a.k_cache) + off;
-                    vp = static_cast<const TI*>(a.v_cache) + off;
-                } else if (at >= ctx && at < keys_end) {
-                    off += ((long long)n * a.Ts + at - ctx) * row_elems;
-                    kp = static_cast<const TI*>(a.k) + off;
-                    vp = static_cast<const TI*>(a.v) + off;
+                bool row = (unsigned)page[i] < (unsigned)a.num_pages;
+                const long long off = row ? page[i] * a.page_stride + (long long)slot[i] * row_elems : 0;
+                const TI *kp = kc + off, *vp = vc + off;
+                if (at >= ctx) {
+                    row = at < keys_end;
+                    const long long own_off = row ? (long long)hk * D + CH * g + ((long long)n * a.Ts + at - ctx) * row_elems : 0;
+                    kp = static_cast<const TI*>(a.k) + own_off;
+                    vp = static_cast<const TI*>(a.v) + own_off;
                 }
                 const int bit = 2 * stage + i;
-                there = (there & ~(1u << bit)) | ((unsigned)(kp != nullptr) << bit);
+                there = (there & ~(1u << bit)) | ((unsigned)row << bit);
                 uint4* to = ring + bit * 2 * kStreamThreads + tid;
-                copy16(to, kp, q);
-                copy16(to + kStreamThreads, vp, q);
+                copy16(to, kp, row);
+                copy16(to + kStreamThreads, vp, row);
                 at += kStep;
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -205,8 +220,8 @@ tree_attention_stream_kernel(const TreeArgs a)
         }
         const int steps = (keys_end - w.t0 * kStreamKeys + 2 * kStep - 1) / (2 * kStep);
         int stage = 0;
-#pragma unroll 1
-        for (int step = 0; step < steps; ++step) {
+        auto keys = [&](auto drafted) {             // whether drafted nodes may be among the keys
+            constexpr bool kTail = decltype(drafted)::value;
             // the stage used in the step before takes the next keys
             fetch(stage ? stage - 1 : kAhead - 1);
             look();
@@ -233,15 +248,11 @@ tree_attention_stream_kernel(const TreeArgs a)
             for (int off = LK / 2; off > 0; off /= 2) {
                 if (cnt > 1) {
                     cnt /= 2;
-                    const bool up_half = g & off;
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int r = 0; r < cnt; ++r) {
-                            const float give = up_half ? s[u][r] : s[u][r + cnt];
-                            const float keep = up_half ? s[u][r + cnt] : s[u][r];
-                            s[u][r] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-                        }
+                        for (int r = 0; r < cnt; ++r)
+                            s[u][r] += __shfl_xor_sync(0xffffffffu, s[u][r + cnt], off);
                 } else {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) s[u][0] += __shfl_xor_sync(0xffffffffu, s[u][0], off);
@@ -255,8 +266,8 @@ tree_attention_stream_kernel(const TreeArgs a)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int nd = node + u * kStep;
-                    const bool see = ((there >> (2 * stage + u)) & 1) &&
-                                     (nd < 0 ? seen[i] != 0ull : ((seen[i] >> (nd & 63)) & 1ull));
+                    bool see = (there >> (2 * stage + u)) & 1;
+                    if (kTail) see = see && (nd < 0 || ((seen[i] >> (nd & 63)) & 1ull));
                     if (!see) s[u][i] = -INFINITY;
                 }
                 top[i] = fmaxf(s[0][i], s[1][i]);
@@ -284,10 +295,9 @@ tree_attention_stream_kernel(const TreeArgs a)
             for (int i = 0; i < RO; ++i)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    p[u][i] = exp2f(s[u][i] - (m[i] == -INFINITY ? 0.f : m[i]));
+                    p[u][i] = ex2(s[u][i] - (m[i] == -INFINITY ? 0.f : m[i]));
                     l[i] += p[u][i];
                 }
-            const bool tail = __any_sync(0xffffffffu, node + kStep >= 0);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 uint64_t x[CP];
@@ -298,7 +308,7 @@ tree_attention_stream_kernel(const TreeArgs a)
                     const int from = LK >= RT ? r * (LK / RT) : r / RO;
                     const float pr = __shfl_sync(0xffffffffu, p[u][r % RO], (lane & ~(LK - 1)) + from);
                     // a node that row r does not see may hold inf or NaN: 0 * v would keep it
-                    if (tail && nd >= 0 && !(r < rows && nd < a.Ts && ((anc[(r0 + r) / a.G] >> nd) & 1ull)))
+                    if (kTail && nd >= 0 && !(r < rows && nd < a.Ts && ((anc[(r0 + r) / a.G] >> nd) & 1ull)))
                         continue;
 #pragma unroll
                     for (int i = 0; i < CP; ++i) acc[r][i] = fma2(pack2(pr, pr), x[i], acc[r][i]);
@@ -306,12 +316,22 @@ tree_attention_stream_kernel(const TreeArgs a)
             }
             pos += 2 * kStep;
             if (++stage == kAhead) stage = 0;
-        }
+        };
+        const int context = (cached_end - w.t0 * kStreamKeys) / (2 * kStep);
+        int step = 0;
+#pragma unroll 1
+        for (; step < context; ++step) keys(std::false_type());
+#pragma unroll 1
+        for (; step < steps; ++step) keys(std::true_type());
         asm volatile("cp.async.wait_group 0;" ::: "memory");   // the stages are free
         // The groups' maxima, sums and outputs meet: in the warp, then in the CTA.
         float top[RO], sum[RO];
 #pragma unroll
         for (int i = 0; i < RO; ++i) {
+            if (seen[i] == 0ull) {                  // an unused node
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+            }
             top[i] = m[i];
 #pragma unroll
             for (int off = LK; off < 32; off <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], off));
@@ -483,13 +503,13 @@ tree_attention_tile_kernel(const TreeArgs a)
                 for (int e = tid; e < kTileKeys * kVecs; e += kTileThreads) {
                     const int j = e / kVecs, c = (e % kVecs) * VR;
                     const long long off = sh_off[t & 3][j];
-                    const TI *kp = nullptr, *vp = nullptr;
+                    const TI *kp = q, *vp = q;           // not read
                     if (off >= 0) {
                         kp = static_cast<const TI*>(j >= nc ? a.k : a.k_cache) + off + hk * D + c;
                         vp = static_cast<const TI*>(j >= nc ? a.v : a.v_cache) + off + hk * D + c;
                     }
-                    copy16(sk + j * Sh::kLdk + c, kp, q);
-                    copy16(sv + j * D + c, vp, q);
+                    copy16(sk + j * Sh::kLdk + c, kp, off >= 0);
+                    copy16(sv + j * D + c, vp, off >= 0);
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -575,11 +595,11 @@ tree_attention_tile_kernel(const TreeArgs a)
                 for (int off = 1; off < 16; off <<= 1)
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                 const float ref = top == -INFINITY ? 0.f : top;
-                const float shrink = exp2f(m[i] - ref);
+                const float shrink = ex2(m[i] - ref);
                 float sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < KR; ++j) {
-                    const float p = exp2f(s[i][j] - ref);
+                    const float p = ex2(s[i][j] - ref);
                     sP[(ty * RR + i) * Sh::kLdp + tx + 16 * j] = p;
                     sum += p;
                 }
