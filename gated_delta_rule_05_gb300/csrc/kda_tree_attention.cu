@@ -403,12 +403,18 @@ tree_attention_stream_kernel(const TreeArgs a)
 // thread (ty, tx) owns rows 4 ty .. 4 ty + 3 throughout, their scores for keys tx
 // and tx + 16 and D / 16 of their output columns, so that m, l and the rescaling
 // stay in registers.  K and V come by cp.async in two stages, one tile ahead;
-// page numbers are loaded two tiles before that.  Bound by shared-memory reads.
+// page numbers are loaded two tiles before that.  Bound by shared-memory reads
+// (6 words of K and q for 8 FMAs) and by the few warps that its registers leave:
+// fp32, 8 x 16 nodes, 32 heads on 8, 8 x 4096 rows: d = 128 313 us (27 TFLOP/s),
+// d = 64 160 us; 352 and 210 with scalar FMAs and one loop for all keys.
 constexpr int kTileThreads = 128;
 constexpr int kTileKeys = 32;
 constexpr int kTileRows = 32;
 constexpr int kTileLead = 2;
-__host__ __device__ constexpr int tile_ctas(int D) { return D == 128 ? 2 : (D == 64 ? 4 : 5); }   // per SM
+// Per SM.  At d = 128 two and three took 313 and 365 us in fp32 (298 and 271 from
+// bf16), at d = 64 three, four and five 172, 160 and 224; below that four to six are
+// within 2 %.
+__host__ __device__ constexpr int tile_ctas(int D) { return D == 128 ? 2 : (D == 64 ? 4 : 5); }
 
 template <typename TI, int D>
 struct TileShape {
@@ -555,28 +561,36 @@ tree_attention_tile_kernel(const TreeArgs a)
             __syncthreads();                        // tile t, and the rows of tile t + 2
             const TI* sK = stages + (t & 1) * Sh::kStage;
             const TI* sV = sK + kTileKeys * Sh::kLdk;
-            float s[RR][KR];
+            uint64_t s2[RR][KR];                    // sums of even and odd channels
 #pragma unroll
             for (int i = 0; i < RR; ++i)
 #pragma unroll
-                for (int j = 0; j < KR; ++j) s[i][j] = 0.f;
+                for (int j = 0; j < KR; ++j) s2[i][j] = 0;
 #pragma unroll 4
             for (int c = 0; c < V4; ++c) {
-                float4 kv[KR];
+                uint64_t kv[KR][2];
 #pragma unroll
-                for (int j = 0; j < KR; ++j) kv[j] = load4(sK + (tx + 16 * j) * Sh::kLdk + 4 * c);
+                for (int j = 0; j < KR; ++j) {
+                    const float4 x = load4(sK + (tx + 16 * j) * Sh::kLdk + 4 * c);
+                    kv[j][0] = pack2(x.x, x.y);
+                    kv[j][1] = pack2(x.z, x.w);
+                }
 #pragma unroll
                 for (int i = 0; i < RR; ++i) {
                     const float4 x = *reinterpret_cast<const float4*>(sQ + (ty * RR + i) * Sh::kLdq + 4 * c);
 #pragma unroll
-                    for (int j = 0; j < KR; ++j) {
-                        s[i][j] = fmaf(x.x, kv[j].x, s[i][j]);
-                        s[i][j] = fmaf(x.y, kv[j].y, s[i][j]);
-                        s[i][j] = fmaf(x.z, kv[j].z, s[i][j]);
-                        s[i][j] = fmaf(x.w, kv[j].w, s[i][j]);
-                    }
+                    for (int j = 0; j < KR; ++j)
+                        s2[i][j] = fma2(pack2(x.z, x.w), kv[j][1], fma2(pack2(x.x, x.y), kv[j][0], s2[i][j]));
                 }
             }
+            float s[RR][KR];
+#pragma unroll
+            for (int i = 0; i < RR; ++i)
+#pragma unroll
+                for (int j = 0; j < KR; ++j) {
+                    const float2 y = unpack2(s2[i][j]);
+                    s[i][j] = y.x + y.y;
+                }
             bool there[KR];                         // context keys whose page exists
 #pragma unroll
             for (int j = 0; j < KR; ++j) there[j] = tx + 16 * j < nc && sh_off[t & 3][tx + 16 * j] >= 0;
@@ -612,7 +626,7 @@ tree_attention_tile_kernel(const TreeArgs a)
             }
             __syncwarp();                           // a row's P is written and read by one warp
             // column c of this thread: its 4-column groups are 64 apart (d >= 64)
-            auto add = [&](int j, const float (&p)[RR]) {
+            auto add = [&](int j, const float (&p)[RR], auto drafted) {
                 float v[CR];
                 if constexpr (CR % 4 == 0) {
 #pragma unroll
@@ -630,25 +644,39 @@ tree_attention_tile_kernel(const TreeArgs a)
 #pragma unroll
                 for (int i = 0; i < RR; ++i) {
                     // a node that this row does not see may hold inf or NaN: 0 * v would keep it
-                    if (draft && j >= nc && (j >= nk || !((mask[i] >> (j - nc)) & 1ull))) continue;
+                    if (decltype(drafted)::value && j >= nc && (j >= nk || !((mask[i] >> (j - nc)) & 1ull))) continue;
+                    if constexpr (CR % 2 == 0) {
 #pragma unroll
-                    for (int c = 0; c < CR; ++c) acc[i][c] = fmaf(p[i], v[c], acc[i][c]);
+                        for (int c = 0; c < CR; c += 2) {
+                            const float2 y = unpack2(fma2(pack2(p[i], p[i]), pack2(v[c], v[c + 1]),
+                                                          pack2(acc[i][c], acc[i][c + 1])));
+                            acc[i][c] = y.x;
+                            acc[i][c + 1] = y.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < CR; ++c) acc[i][c] = fmaf(p[i], v[c], acc[i][c]);
+                    }
                 }
             };
+            auto products = [&](auto drafted) {
 #pragma unroll 2
-            for (int j = 0; j < kTileKeys; j += 4) {
-                float p[4][RR];
+                for (int j = 0; j < kTileKeys; j += 4) {
+                    float p[4][RR];
 #pragma unroll
-                for (int i = 0; i < RR; ++i) {
-                    const float4 x = *reinterpret_cast<const float4*>(sP + (ty * RR + i) * Sh::kLdp + j);
-                    p[0][i] = x.x;
-                    p[1][i] = x.y;
-                    p[2][i] = x.z;
-                    p[3][i] = x.w;
+                    for (int i = 0; i < RR; ++i) {
+                        const float4 x = *reinterpret_cast<const float4*>(sP + (ty * RR + i) * Sh::kLdp + j);
+                        p[0][i] = x.x;
+                        p[1][i] = x.y;
+                        p[2][i] = x.z;
+                        p[3][i] = x.w;
+                    }
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj) add(j + jj, p[jj], drafted);
                 }
-#pragma unroll
-                for (int jj = 0; jj < 4; ++jj) add(j + jj, p[jj]);
-            }
+            };
+            if (draft) products(std::true_type());
+            else products(std::false_type());
             __syncthreads();                        // tile t has been read: its stage is free
         }
         // Finished here, or one of the CTA's two pieces.

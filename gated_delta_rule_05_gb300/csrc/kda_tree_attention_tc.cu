@@ -56,8 +56,6 @@ struct TcShape {
     // Warps: softmax, copies, one that issues products, filled up to whole
     // warpgroups so that registers can be moved from the latter two to the
     // softmax: 384 x 168 >= 128 x 232 + 256 x 128, 512 x 128 = 256 x 184 + 256 x 72.
-    // block is filled to whole warpgroups, so that registers can be moved from
-    // the copies and the products to the softmax (512 x 128 = 256 x 192 + 256 x 64)
     static constexpr int kThreads = NT == 1 ? 384 : 512;
     static constexpr int kCopyWarp = NT * 4;
     static constexpr int kMmaWarp = NT * 4 + 4;
