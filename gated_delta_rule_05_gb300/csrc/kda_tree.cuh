@@ -20,7 +20,11 @@
 namespace kda {
 
 constexpr int kTreeMaxNodes = 64;     // one bit per node in a 64-bit mask
-constexpr int kTcKeys = 128;          // the tensor-core kernel's KT and LEAD
+// The tensor-core kernel's KT and LEAD.  LEAD 0, 4, 8, 12 and 20, us: 32 ragged
+// contexts of 0 to 16,384 rows, 16 nodes, 351, 245, 206, 192 and 193 (cut without
+// it, a range of short sequences is the last to end); 4 x 32,768 rows 113, 111,
+// 106, 103 and 104; 64 x 4,096 rows, one token, 179, 177, 178, 179 and 183.
+constexpr int kTcKeys = 128;
 constexpr int kTcLead = 12;
 
 struct TreeArgs {

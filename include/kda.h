@@ -441,7 +441,12 @@ size_t kda_tree_attention_workspace_bytes(int32_t N, int32_t Ts, int32_t Hq,
  *   workspace     kda_tree_attention_workspace_bytes(...) bytes, 256-byte
  *                 aligned, not shared with concurrent calls; contents on entry
  *                 do not matter
- * dtype is that of q, k, v and the cache, and of o.  An infinity or NaN in a
+ * dtype is that of q, k, v and the cache, and of o.  KDA_BF16 with d = 64 or 128
+ * and scale > 0 runs on the tensor cores, with probabilities rounded to bf16 for
+ * the second product; everything else, and everything when the environment
+ * variable KDA_FORCE_SIMT is set, on the CUDA cores in fp32.  The waits of the
+ * tensor-core kernel are bounded: one that gives up sets the int32 at byte 8 of
+ * the workspace, which no call clears.  An infinity or NaN in a
  * node's k or v reaches the nodes that see it and no others.  The result does
  * not depend on timing (no atomics on values); it may differ in rounding
  * between GPUs with different SM counts. */
