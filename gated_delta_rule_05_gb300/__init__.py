@@ -25,6 +25,7 @@ Functions (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -485,13 +486,22 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _out(name, t, shape, dtype, device, stream):
+    """The output the caller passed, checked, or a new one."""
+    if t is None:
+        return _new(shape, dtype, device, stream)
+    _check_cuda(name, t, dtype)
+    _shape(name, t, shape)
+    return t
+
+
 def _call(name, device, stream, *args):
     """lib().<name>(*args, stream) on ``device``; raises KdaError."""
     torch = _torch()
     f = getattr(_lib if _lib is not None else lib(), name)
     raw = stream.cuda_stream if stream is not None else \
         torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         rc = f(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -525,14 +535,8 @@ def kda_decode_tree(q, k, v, log_alpha, beta, S_in, parent=None, *, o=None, stat
         _shape(name, t, shape)
     if parent is not None:
         _shape("parent", parent, (N, Ts))
-    if o is None:
-        o = _new((N, Ts, H, dv), o_dtype, q.device, stream)
-    if states is None:
-        states = _new((N, Ts, H, dk, dv), torch.float32, q.device, stream)
-    _check_cuda("o", o, o_dtype)
-    _check_cuda("states", states, torch.float32)
-    _shape("o", o, (N, Ts, H, dv))
-    _shape("states", states, (N, Ts, H, dk, dv))
+    o = _out("o", o, (N, Ts, H, dv), o_dtype, q.device, stream)
+    states = _out("states", states, (N, Ts, H, dk, dv), torch.float32, q.device, stream)
     _call("kda_decode_tree", q.device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           log_alpha.data_ptr(), beta.data_ptr(), S_in.data_ptr(), _address(parent), N, Ts, H, dk,
           dv, dt, o.data_ptr(), states.data_ptr())
@@ -553,6 +557,13 @@ def _check_pages(name, t, dtype, device):
 def kda_tree_attention_workspace_bytes(N: int, Ts: int, Hq: int, Hkv: int, d: int,
                                        dtype: int) -> int:
     return int(lib().kda_tree_attention_workspace_bytes(N, Ts, Hq, Hkv, d, dtype))
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_bytes(device, *sizes):
+    """kda_tree_attention_workspace_bytes on ``device``, at least 256."""
+    with _torch().cuda.device(device):
+        return max(kda_tree_attention_workspace_bytes(*sizes), 256)
 
 
 def kda_tree_attention(q, k, v, k_cache, v_cache, page_table, lengths, parent=None, *,
@@ -589,18 +600,11 @@ def kda_tree_attention(q, k, v, k_cache, v_cache, page_table, lengths, parent=No
     pages, page = k_cache.shape[:2]
     if pages > 1 and k_cache.stride(0) != v_cache.stride(0):
         raise ValueError("k_cache and v_cache must have the same page stride")
-    if o is None:
-        o = _new((N, Ts, Hq, d), o_dtype, dev, stream)
-    _check_cuda("o", o, o_dtype)
-    _shape("o", o, (N, Ts, Hq, d))
+    o = _out("o", o, (N, Ts, Hq, d), o_dtype, dev, stream)
     if workspace is None:
-        if torch.cuda.current_device() == dev.index:
-            need = lib().kda_tree_attention_workspace_bytes(N, Ts, Hq, Hkv, d, dt)
-        else:
-            with torch.cuda.device(dev):
-                need = lib().kda_tree_attention_workspace_bytes(N, Ts, Hq, Hkv, d, dt)
-        workspace = _new((need or 256,), torch.uint8, dev, stream)
-    _check_cuda("workspace", workspace)
+        workspace = _new((_attention_bytes(dev, N, Ts, Hq, Hkv, d, dt),), torch.uint8, dev, stream)
+    else:
+        _check_cuda("workspace", workspace)
     _call("kda_tree_attention", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           _address(parent), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
           lengths.data_ptr(), N, Ts, Hq, Hkv, d, pages, page, page_table.shape[1],
@@ -628,18 +632,13 @@ def kda_token_logprobs(logits, tokens=None, num_top=0, *, logprobs=None, entropy
     _check_cuda("tokens", tokens, torch.int32)
     J = 0 if tokens is None else tokens.shape[1]
     K = int(num_top)
-    new = lambda *s, dtype=torch.float32: _new(s, dtype, dev, stream)
     if tokens is not None:
         _shape("tokens", tokens, (T, J))
-    logprobs = new(T, J) if logprobs is None else logprobs
-    entropy = new(T) if entropy is None else entropy
-    top_ids = new(T, max(K, 0), dtype=torch.int32) if top_ids is None else top_ids
-    top_logprobs = new(T, max(K, 0)) if top_logprobs is None else top_logprobs
-    for name, t, shape in (("logprobs", logprobs, (T, J)), ("entropy", entropy, (T,)),
-                           ("top_ids", top_ids, (T, K)), ("top_logprobs", top_logprobs, (T, K))):
-        if K >= 0:
-            _shape(name, t, shape)
-        _check_cuda(name, t, torch.int32 if name == "top_ids" else torch.float32)
+    f32, top = torch.float32, (T, max(K, 0))
+    logprobs = _out("logprobs", logprobs, (T, J), f32, dev, stream)
+    entropy = _out("entropy", entropy, (T,), f32, dev, stream)
+    top_ids = _out("top_ids", top_ids, top, torch.int32, dev, stream)
+    top_logprobs = _out("top_logprobs", top_logprobs, top, f32, dev, stream)
     _call("kda_token_logprobs", dev, stream, logits.data_ptr(),
           max(logits.stride(0), V) if T == 1 else logits.stride(0), _address(tokens), T, V, J, K,
           dt, logprobs.data_ptr(), entropy.data_ptr(), top_ids.data_ptr(),
@@ -669,10 +668,7 @@ def _cache_rows(name, k, v, middle, k_cache, v_cache, page_table, lengths, new_l
     N = lengths.shape[0]
     _shape("lengths", lengths, (N,))
     _shape("page_table", page_table, (N, page_table.shape[1]))
-    if new_lengths is None:
-        new_lengths = _new((N,), torch.int32, dev, stream)
-    _check_cuda("new_lengths", new_lengths, torch.int32)
-    _shape("new_lengths", new_lengths, (N,))
+    new_lengths = _out("new_lengths", new_lengths, (N,), torch.int32, dev, stream)
     _call(name, dev, stream, k.data_ptr(), v.data_ptr(), *middle, page_table.data_ptr(),
           lengths.data_ptr(), layers, N, *counts, Hkv, d, k_cache.shape[1], k_cache.shape[2],
           page_table.shape[1], k_cache.stride(1), k_cache.stride(0), dt, k_cache.data_ptr(),
