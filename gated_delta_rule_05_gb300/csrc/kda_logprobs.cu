@@ -25,9 +25,8 @@
 // on their way during this one's arithmetic.
 //
 // Bound by HBM for long batches (4,096 x 50,257 fp32, K = 20: 151 us, 5.5 TB/s, 82 %
-// of a copy); 512 x 131,072 bf16 (37 us, 3.6 TB/s) by instructions, the exponential
-// above all (16 a clock and SM: 14 us), and by 512 rows on 152 SMs: three rows on
-// some, four on others.
+// of a copy); 512 x 131,072 bf16 (37 us, 3.6 TB/s) by instructions (61 % of the
+// issue slots) and by 512 rows on 152 SMs: three rows on some, four on others.
 //
 // One cluster of CTAs per row splits a row into slices when there are few rows;
 // the first CTA joins the slices through distributed shared memory.
@@ -537,7 +536,8 @@ cudaError_t launch(const void* logits, long long row_stride, const int32_t* toke
 // per row as long as they are not more than two per SM.  Measured on one GB300
 // (128 and 256 threads): 4,096 x 50,257 fp32, K = 20, 151 and 165 us; 2,048 x
 // 131,072 bf16, K = 8, 107 and 114 us; 512 x 131,072 39 and 35 us; 1 x 131,072,
-// K = 20, 17 and 13 us.  Two parts a row at 512 rows: 35 and, at four, 45 us.
+// K = 20, 17 and 13 us.  Two and four parts a row at 512 rows: 44 and 61 us, with
+// 128 threads 36 and 48; at 200 rows 21 and 29 against 21.
 cudaError_t launch_token_logprobs(const void* logits, long long row_stride, const int32_t* tokens,
                                   int32_t T, int32_t V, int32_t J, int32_t K, bool bf16,
                                   float* logprobs, float* entropy, int32_t* top_ids,

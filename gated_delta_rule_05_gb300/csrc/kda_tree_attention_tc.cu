@@ -30,9 +30,11 @@
 // 16,384 rows, 64 rows per cache head, 189 us, 5.7 TB/s (85 % of a copy), 64 x
 // 4,096 rows, one token, 6.0 TB/s.  For many rows by the softmax beside the
 // products: 4 x 64 nodes over 32K to 64K rows, 512 rows per cache head, 349 us, 1.18
-// PFLOP/s (63 % of a library product), tensor pipe 53 % busy.  The
-// exponentials of a tile, 16 a clock and SM, take 1,024 clocks, its products 1,300.  Pages
-// of 16 rows cost 3 % against pages of 128.
+// PFLOP/s (63 % of a library product), tensor pipe 53 % busy.  TMEM has room for one
+// S per row tile then, so that a row tile's softmax and products take turns; a
+// polynomial on the FMA pipe for every eighth exponential makes it 6 % slower, so it
+// is instructions, not the exponential unit.  Pages of 16 rows cost 3 % against
+// pages of 128.
 //
 // Every wait has a limit (mbar_wait); a wait that gives up sets the workspace's
 // timeout word, and the CTA runs to its end without waiting again.
