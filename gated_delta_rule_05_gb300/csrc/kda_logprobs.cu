@@ -537,7 +537,7 @@ cudaError_t launch(const void* logits, long long row_stride, const int32_t* toke
 // (128 and 256 threads): 4,096 x 50,257 fp32, K = 20, 151 and 165 us; 2,048 x
 // 131,072 bf16, K = 8, 107 and 114 us; 512 x 131,072 39 and 35 us; 1 x 131,072,
 // K = 20, 17 and 13 us.  Two and four parts a row at 512 rows: 44 and 61 us, with
-// 128 threads 36 and 48; at 200 rows 21 and 29 against 21.
+// 128 threads 36 and 48; at 200 rows, where two are taken, 21 and 29.
 cudaError_t launch_token_logprobs(const void* logits, long long row_stride, const int32_t* tokens,
                                   int32_t T, int32_t V, int32_t J, int32_t K, bool bf16,
                                   float* logprobs, float* entropy, int32_t* top_ids,
