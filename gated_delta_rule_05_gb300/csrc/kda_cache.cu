@@ -9,7 +9,7 @@
 // than 32 rows of 2 KB in four passes, took the commit of 32 x 16 rows of 8 layers
 // from 6.4 to 5.3 us (in a graph) and the append of 16 prompts from 172 to 165 us,
 // 100 % of the measured copy bandwidth; depths 1 and 2 took 167 and 170.
-#include "kda_internal.cuh"
+#include "kda_verify.cuh"
 
 namespace kda {
 namespace {

@@ -25,8 +25,8 @@
 // 12 us instead of 18.  The inputs of the next nodes are loaded and combined
 // (alpha k, alpha q, k . q) ahead of their steps, which then touch shared memory
 // alone until the state is written.  Arithmetic is two-wide.
-#include "kda_internal.cuh"
 #include "kda_tree.cuh"
+#include "kda_verify.cuh"
 
 namespace kda {
 namespace {

@@ -32,7 +32,7 @@
 // the first CTA joins the slices through distributed shared memory.
 #include <cooperative_groups.h>
 
-#include "kda_internal.cuh"
+#include "kda_verify.cuh"
 
 namespace kda {
 namespace {

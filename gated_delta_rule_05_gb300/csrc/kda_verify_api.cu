@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "kda_tree.cuh"
+#include "kda_verify.cuh"
 
 namespace {
 
