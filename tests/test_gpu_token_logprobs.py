@@ -172,3 +172,74 @@ def test_many_rows_of_ties_and_sorted_values(kda, dtype, kind):
     x = row.to(dtype).expand(700, V).contiguous()
     x[1::7, ::2] = float("-inf")
     check(kda, x, K=32, threads=128)
+
+
+# Finite values as masks.  The bound of an unmasked token's log probability and of
+# the entropy goes by the unmasked logits alone: a masked token's probability is 0.
+# A masked token's own log probability, and all of a row of nothing but masks, are
+# off by what fp32 holds of a number of the mask's size, 2^-23 of it.
+FILLS = [-1e4, -1e9, -1e10, -1e12, -1e15, -1e20, -1e30, -1e32, -1e34, -1e36, "lowest"]
+
+
+def check_finite(kda, x, K, size, threads):
+    """Like check, row by row, with ``size`` the magnitude of each row's largest logits.
+    Rows repeat from len(size) on and, where they start at the same place in 16 bytes,
+    have to give the same bits again."""
+    T, V = x.shape
+    rows = len(size)
+    tokens = np.random.default_rng(V).integers(0, V, (rows, 5)).astype(np.int32)
+    tokens[:, 3], tokens[:, 4] = 0, V - 1
+    got = kda.kda_token_logprobs(x, torch.from_numpy(tokens).cuda().repeat(T // rows, 1), K)
+    for y in got:
+        if x.stride(0) % 8 == 0:
+            assert torch.equal(y, y[:rows].repeat((T // rows,) + (1,) * (y.dim() - 1)))
+    logp, H, ids, top = (y[:rows].double().cpu().numpy() for y in got)
+    # relative to the maximum, as float64 would cancel: all four are the same
+    top_of = x[:rows].double().amax(-1, keepdim=True)
+    rl, rH, rids, rtop = reference(x[:rows].double() - top_of, tokens, K)
+    assert np.array_equal(ids, rids)
+    size = np.asarray(size, float)[:, None]
+    sums = (V / threads + 64) * 2.0 ** -23
+    tol = sums + 2.0 ** -22 * size
+    for y, want in ((logp, rl), (top, rtop)):
+        assert np.all(np.abs(y - want) <= tol + 2.0 ** -23 * np.abs(want)), (y - want, want)
+    bound = np.where(size > 1e3, sums, tol)[:, 0]   # differences alone
+    assert np.all(np.abs(H - rH) <= bound * (1 + rH)), (H, rH)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("fill", FILLS)
+@pytest.mark.parametrize("repeat,V", [(1, 50), (1, 1000), (1, 131072), (100, 1000), (100, 5003)])
+def test_finite_masks(kda, dtype, fill, repeat, V):
+    fill = torch.finfo(dtype).min if fill == "lowest" else fill
+    x = logits(7, V, dtype, 11)
+    i = torch.arange(V, device="cuda")
+    masked = torch.stack([i < 0, i != V // 2, (i // 64) % 2 == 0, i >= V // 2, i < V // 2, i < V - 3, i >= 0])
+    x[masked] = fill
+    nothing = masked.all(-1, keepdim=True)          # nothing but masks
+    size = torch.where(masked & ~nothing, 0, x.float().abs()).amax(-1).tolist()
+    rows = torch.zeros((7 * repeat, -(-V // 8) * 8), dtype=dtype, device="cuda")[:, :V]
+    rows.copy_(x.repeat(repeat, 1))
+    check_finite(kda, rows, 8, size, 128 if repeat > 1 else 256)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("offset", [1e3, 1e6, 1e8, 1e10, 1e20, 1e30, 1e36, 1e37, 1e38])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("V", [1, 6, 1000, 50001])
+def test_large_logits(kda, dtype, offset, sign, V):
+    # two values 2^-6 of their size apart
+    i = torch.arange(V, device="cuda")
+    big = torch.tensor(sign * offset, device="cuda").to(dtype).float()
+    x = torch.stack([torch.where((i + r) % 7 == 0, big, big * (1 - 2.0 ** -6)) for r in range(3)])
+    x = x.to(dtype)
+    check_finite(kda, x, min(V, 8), x.float().abs().amax(-1).tolist(), 256)
+
+
+@pytest.mark.parametrize("centre", [-(1 << 20), -(1 << 18), 1 << 16, 1 << 20, 1 << 21])
+@pytest.mark.parametrize("V", [5, 1000, 50001])
+def test_large_logits_close_to_each_other(kda, centre, V):
+    # threads' maxima on either side of a power of two, all of them weighty
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = centre + 0.5 * torch.randint(-8, 9, (4, V), generator=g, device="cuda").float()
+    check_finite(kda, x, 5, [abs(centre) + 4] * 4, 256)
