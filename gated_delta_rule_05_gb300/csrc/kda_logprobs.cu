@@ -365,9 +365,11 @@ token_logprobs_kernel(const T* __restrict__ logits, long long row_stride,
     };
     fetch(v0);
     float given = -INFINITY;                         // the logit of given token tid
+    bool outside = true;                             // whether there is none
     if (part == 0 && tid < J) {
         const int t = tokens[row * J + tid];
-        if (t >= 0 && t < V) given = ld_f(x + t);
+        outside = t < 0 || t >= V;
+        if (!outside) given = ld_f(x + t);
     }
     if (tid == 0) {
         sh.count = sh.kept = part == 0 ? V - nv * Vx::kN : 0;
@@ -537,7 +539,7 @@ token_logprobs_kernel(const T* __restrict__ logits, long long row_stride,
                 top_logprobs[row * K + tid] = lse == -INFINITY ? -INFINITY : key_value(k) - lse;
             }
         }
-        if (tid < J) logprobs[row * J + tid] = lse == -INFINITY ? -INFINITY : given - lse;
+        if (tid < J) logprobs[row * J + tid] = outside || lse == -INFINITY ? -INFINITY : given - lse;
         for (int j = tid + kThreads; j < J; j += kThreads) {
             const int t = tokens[row * J + j];
             logprobs[row * J + j] = (t < 0 || t >= V || lse == -INFINITY) ? -INFINITY : ld_f(x + t) - lse;

@@ -479,14 +479,15 @@ kda_status_t kda_decode_tree(const void *q, const void *k, const void *v,
  *   logits        [T, V] in rows of row_stride elements (>= V, any), base
  *                 16-byte aligned; bf16 (KDA_BF16_F32OUT) or fp32 (KDA_FP32)
  *   tokens        device int32 [T, J], J >= 0 (none: NULL)
- *   logprobs      [T, J] fp32 (written); -inf for a token outside [0, V)
+ *   logprobs      [T, J] fp32 (written); -inf for a token outside [0, V), in
+ *                 any row
  *   entropy       [T] fp32 (written) or NULL
  *   top_ids, top_logprobs   [T, K] int32 and fp32 (written), 0 <= K <= min(V,
  *                 32) (more than 32 is KDA_ERR_UNSUPPORTED), most probable
  *                 first, equal logits by the lower index; NULL when K is 0
  * A logit of -inf is a masked token.  A row of nothing but -inf gives -inf log
- * probabilities and entropy 0.  A NaN or +inf logit makes its row's
- * logprobs and entropy NaN; in the order of top_ids NaN counts as -inf. */
+ * probabilities and entropy 0.  A NaN or +inf logit makes the log
+ * probabilities of its row's tokens and its entropy NaN; in the order of top_ids NaN counts as -inf. */
 kda_status_t kda_token_logprobs(const void *logits, int64_t row_stride,
                                 const int32_t *tokens, int32_t T, int32_t V,
                                 int32_t J, int32_t K, kda_dtype_t dtype,

@@ -243,3 +243,25 @@ def test_large_logits_close_to_each_other(kda, centre, V):
     g = torch.Generator(device="cuda").manual_seed(V)
     x = centre + 0.5 * torch.randint(-8, 9, (4, V), generator=g, device="cuda").float()
     check_finite(kda, x, 5, [abs(centre) + 4] * 4, 256)
+
+
+@pytest.mark.parametrize("T", [1, 700])
+def test_tokens_outside_the_vocabulary_in_any_column_of_any_row(kda, T):
+    # more columns than a block has threads; a NaN row and one of nothing
+    V, J = 500, 600
+    x = logits(T, V, F32, 12)
+    tok = torch.randint(-V // 2, V + V // 2, (T, J), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    outside = ((tok < 0) | (tok >= V)).cuda()
+    for fill in (None, float("nan"), float("inf"), float("-inf")):
+        if fill is not None:
+            x[-1, 7 if fill == fill and fill > 0 else slice(None)] = fill
+        logp, *_ = kda.kda_token_logprobs(x, tok.cuda())
+        assert torch.isneginf(logp[outside]).all()
+        inside = logp[-1][~outside[-1]]
+        if fill is None:
+            assert torch.isfinite(inside).all()
+        elif fill == float("-inf"):
+            assert torch.isneginf(inside).all()
+        else:
+            assert torch.isnan(inside).all()
+        x[-1] = logits(1, V, F32, 13)[0]
