@@ -23,6 +23,20 @@ __host__ __device__ int rows_per_block(long long row_bytes)
     return rows < 1 ? 1 : rows > kThreads ? kThreads : (int)rows;
 }
 
+// The packed rows of sequence n: from cu_seqlens[n] to cu_seqlens[n + 1], as far as
+// they exist.
+__device__ __forceinline__ int first_row(const CacheArgs& a, int n)
+{
+    const int r = __ldg(a.cu_seqlens + n);
+    return r > 0 ? r : 0;
+}
+__device__ __forceinline__ int row_count(const CacheArgs& a, int n)
+{
+    const long long end = __ldg(a.cu_seqlens + n + 1), most = end < a.rows ? end : a.rows;
+    const long long c = most - first_row(a, n);
+    return c > 0 ? (int)c : 0;
+}
+
 __global__ void __launch_bounds__(kThreads)
 cache_rows_kernel(const CacheArgs a)
 {
@@ -46,8 +60,8 @@ cache_rows_kernel(const CacheArgs a)
                     else hi = mid;
                 }
                 n = lo;
-                i = (int)(r - __ldg(a.cu_seqlens + n));
-                there = i >= 0 && r < __ldg(a.cu_seqlens + n + 1);
+                i = (int)(r - first_row(a, n));
+                there = i >= 0 && i < row_count(a, n);
             } else {
                 n = (int)(r / a.Ts);
                 i = (int)(r - (long long)n * a.Ts);
@@ -75,7 +89,7 @@ cache_rows_kernel(const CacheArgs a)
              n += (long long)gridDim.x * kThreads) {
             int c;
             if (a.cu_seqlens) {
-                c = a.cu_seqlens[n + 1] - a.cu_seqlens[n];
+                c = row_count(a, n);
             } else {
                 c = a.count ? a.count[n] : a.Ts;
                 c = c < 0 ? 0 : (c > a.Ts ? a.Ts : c);

@@ -526,7 +526,10 @@ kda_status_t kda_cache_commit(const void *k, const void *v, const int32_t *path,
 /* The same for a packed batch (a prefill): k, v [layers, total_tokens, Hkv, d],
  * sequence n owning rows cu_seqlens[n] .. cu_seqlens[n+1] - 1 (device int32
  * [N+1], as in kda_prefill), which go to positions lengths[n], lengths[n] + 1,
- * and so on.  Rows that cu_seqlens gives to no sequence are dropped. */
+ * and so on.  Rows that cu_seqlens gives to no sequence are dropped; rows before 0
+ * or from total_tokens on do not exist and a sequence that ends before it begins
+ * has none, in new_lengths too.  (Of sequences that claim the same row one gets
+ * it, which is not defined.) */
 kda_status_t kda_cache_append(const void *k, const void *v,
                               const int32_t *cu_seqlens, int64_t total_tokens,
                               const int32_t *page_table, const int32_t *lengths,

@@ -163,3 +163,25 @@ def test_offsets_beyond_32_bits(kda):
         tail = pool[0, -2:].reshape(-1, Hkv, d)
         assert torch.equal(tail[62:65], x[0, 0])
         assert torch.all(tail[:62] == fill) and torch.all(tail[65:] == fill)
+
+
+@pytest.mark.parametrize("cu", [[0, 3, 5], [2, 3, 8], [0, 6, 4], [0, 9, 12], [5, 2, 8], [-2, 3, 8], [9, 9, 9]])
+def test_append_of_any_cu_seqlens_counts_the_rows_that_it_wrote(kda, cu):
+    # rows before 0 and from T on do not exist, a sequence that ends before it
+    # begins has none
+    T, page = 8, 4
+    k, v = (torch.randn((2, T, 1, 16), device="cuda") for _ in range(2))
+    table = np.arange(6, dtype=np.int32).reshape(2, 3)
+    lengths = np.array([3, 1], np.int32)
+    kc, vc = pools(2, 6, page, 1, 16, F32)
+    want, count = [kc.clone(), vc.clone()], []
+    for n in range(2):
+        own = range(max(cu[n], 0), min(cu[n + 1], T))
+        count.append(len(own))
+        for i, r in enumerate(own):
+            for pool, x in zip(want, (k, v)):
+                put(pool, x[:, r], table[n], int(lengths[n]) + i, page)
+    c = lambda x: torch.from_numpy(np.asarray(x, np.int32)).cuda()
+    new = kda.kda_cache_append(k, v, c(cu), kc, vc, c(table), c(lengths))
+    assert torch.equal(kc, want[0]) and torch.equal(vc, want[1])
+    assert new.tolist() == (lengths + count).tolist()
