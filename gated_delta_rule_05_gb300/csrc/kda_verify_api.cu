@@ -201,8 +201,14 @@ kda_status_t cache_rows(const void* k, const void* v, const int32_t* path, const
     for (const void* x : ins)
         for (const void* y : outs)
             if (rows > 0 && overlaps(x, in, y, cache_bytes)) return KDA_ERR_INVALID_ARG;
-    if (new_lengths && overlaps(new_lengths, 4 * (size_t)N, lengths, 4 * (size_t)N))
-        return KDA_ERR_INVALID_ARG;
+    // Written by some CTAs while others still read theirs.
+    if (new_lengths) {
+        const struct { const void* p; size_t n; } reads[] = {
+            {lengths, (size_t)N}, {count, (size_t)N}, {path, (size_t)rows}, {cu_seqlens, (size_t)N + 1},
+            {page_table, (size_t)N * max_pages}};
+        for (const auto& r : reads)
+            if (r.p && overlaps(new_lengths, 4 * (size_t)N, r.p, 4 * r.n)) return KDA_ERR_INVALID_ARG;
+    }
 
     kda::CacheArgs a = {};
     a.k = static_cast<const uint8_t*>(k);

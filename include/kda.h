@@ -511,7 +511,8 @@ kda_status_t kda_token_logprobs(const void *logits, int64_t row_stride,
  *                 to entries that name no page are dropped.  Two sequences must
  *                 not write one row.
  *   new_lengths   [N] (written: lengths + count) or NULL; must not overlap
- *                 lengths, which other CTAs still read
+ *                 lengths, count, path, cu_seqlens (kda_cache_append) or
+ *                 page_table, which other CTAs still read
  * k and v must not overlap the cache. */
 kda_status_t kda_cache_commit(const void *k, const void *v, const int32_t *path,
                               const int32_t *count, const int32_t *page_table,

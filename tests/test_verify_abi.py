@@ -119,3 +119,13 @@ def test_cache_calls_reject_their_own(lib):
     assert append(lib, cu=NULL) == BAD
     assert append(lib, T=-1) == BAD
     assert append(lib, T=1 << 31) == BAD
+
+
+@pytest.mark.parametrize("at", [A * 7, A * 7 + 4, A * 7 - 4])
+def test_cache_calls_reject_new_lengths_over_what_they_read(lib, at):
+    # N = 2: new_lengths is 8 bytes, and so is count
+    assert commit(lib, count=A * 7, new=at) == BAD
+    assert commit(lib, path=A * 7, new=at) == BAD
+    assert commit(lib, table=A * 7, new=at) == BAD
+    assert append(lib, cu=A * 7, new=at) == BAD
+    assert append(lib, table=A * 7, new=at) == BAD
