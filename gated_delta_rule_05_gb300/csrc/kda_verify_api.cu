@@ -120,11 +120,8 @@ kda_status_t kda_decode_tree(const void* q, const void* k, const void* v, const 
                              int32_t Ts, int32_t H, int32_t d_k, int32_t d_v, kda_dtype_t dtype,
                              void* o, float* states, cudaStream_t stream)
 {
-    if (!parent)
-        return kda_decode_multi(q, k, v, log_alpha, beta, S_in, N, Ts, H, d_k, d_v, dtype, o, states,
-                                stream);
     if (!valid_dtype(dtype)) return KDA_ERR_UNSUPPORTED;
-    if (d_k != d_v || !supported_d(d_k) || Ts > kda::kTreeMaxNodes) return KDA_ERR_UNSUPPORTED;
+    if (d_k != d_v || !supported_d(d_k) || (parent && Ts > kda::kTreeMaxNodes)) return KDA_ERR_UNSUPPORTED;
     if (N < 1 || Ts < 1 || H < 1) return KDA_ERR_INVALID_ARG;
     if (!q || !k || !v || !log_alpha || !beta || !S_in || !o || !states) return KDA_ERR_INVALID_ARG;
     const void* ptrs16[] = {q, k, v, log_alpha, o, S_in, states};
@@ -133,10 +130,19 @@ kda_status_t kda_decode_tree(const void* q, const void* k, const void* v, const 
     if (!aligned(beta, 4) || !aligned(parent, 4)) return KDA_ERR_INVALID_ARG;
     const size_t state_bytes = (size_t)N * H * d_k * d_v * sizeof(float);
     const size_t states_bytes = state_bytes * Ts;
-    const size_t o_bytes = (size_t)N * Ts * H * d_v * out_bytes(dtype);
-    if (overlaps(states, states_bytes, S_in, state_bytes) || overlaps(states, states_bytes, o, o_bytes) ||
-        overlaps(o, o_bytes, S_in, state_bytes))
-        return KDA_ERR_INVALID_ARG;
+    const size_t tokens = (size_t)N * Ts * H;
+    const size_t o_bytes = tokens * d_v * out_bytes(dtype), qkv_bytes = tokens * d_k * in_bytes(dtype);
+    if (overlaps(states, states_bytes, o, o_bytes)) return KDA_ERR_INVALID_ARG;
+    // Read by the CTAs of other value columns, and ahead, while one writes its results.
+    const struct { const void* p; size_t n; } reads[] = {
+        {S_in, state_bytes}, {q, qkv_bytes}, {k, qkv_bytes}, {v, qkv_bytes}, {log_alpha, tokens * d_k * 4},
+        {beta, tokens * 4}, {parent, (size_t)N * Ts * 4}};
+    for (const auto& r : reads)
+        if (r.p && (overlaps(o, o_bytes, r.p, r.n) || overlaps(states, states_bytes, r.p, r.n)))
+            return KDA_ERR_INVALID_ARG;
+    if (!parent)
+        return kda_decode_multi(q, k, v, log_alpha, beta, S_in, N, Ts, H, d_k, d_v, dtype, o, states,
+                                stream);
     const cudaError_t err = kda::launch_decode_tree(q, k, v, log_alpha, beta, S_in, parent, states, N,
                                                     Ts, H, d_k, dtype, o, stream);
     return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

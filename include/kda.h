@@ -464,7 +464,8 @@ kda_status_t kda_tree_attention(const void *q, const void *k, const void *v,
 /* kda_decode_multi over a tree: node t is one decode step from the state after
  * its parent node (parent -1: from S_in).  Arguments are those of
  * kda_decode_multi, plus parent (see above; NULL is kda_decode_multi itself).
- * states[n, t] of an unused node is not written; its o is 0. */
+ * states[n, t] of an unused node is not written; its o is 0.  o and states must
+ * overlap neither each other nor any input, with a NULL parent too. */
 kda_status_t kda_decode_tree(const void *q, const void *k, const void *v,
                              const float *log_alpha, const float *beta,
                              const float *S_in, const int32_t *parent, int32_t N,

@@ -129,3 +129,14 @@ def test_cache_calls_reject_new_lengths_over_what_they_read(lib, at):
     assert commit(lib, table=A * 7, new=at) == BAD
     assert append(lib, cu=A * 7, new=at) == BAD
     assert append(lib, table=A * 7, new=at) == BAD
+
+
+@pytest.mark.parametrize("out", ["o", "states"])
+@pytest.mark.parametrize("over,size", [("q", 1536), ("k", 1536), ("v", 1536), ("g", 3072), ("b", 48), ("parent", 24)])
+def test_decode_tree_rejects_results_over_what_it_reads(lib, out, over, size):
+    # N = 2, Ts = 3, H = 2, d = 64, bf16; the last 16-byte piece that lies in the input
+    for parent in (A * 9, NULL):
+        apart = dict(q=A, k=A * 3, v=A * 4, g=A * 5, b=A * 6, parent=parent)
+        if apart[over] is not None:
+            for at in (apart[over], apart[over] + (size - 1) // 16 * 16):
+                assert tree(lib, **{**apart, out: at}) == BAD
