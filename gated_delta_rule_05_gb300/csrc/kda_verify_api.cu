@@ -23,6 +23,13 @@ bool valid_dtype(kda_dtype_t t) { return t == KDA_BF16 || t == KDA_FP32 || t == 
 size_t in_bytes(kda_dtype_t t) { return t == KDA_FP32 ? 4 : 2; }
 size_t out_bytes(kda_dtype_t t) { return t == KDA_BF16 ? 2 : 4; }
 
+// The sizes that the attention and its workspace take: a row tile is a block index.
+bool attention_sizes(int32_t N, int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d)
+{
+    return N >= 1 && Ts >= 1 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && (int64_t)Ts * Hq <= (1 << 20) &&
+           (int64_t)Hkv * d <= INT32_MAX;
+}
+
 // Bytes from the first to the last element of a layer's pages, and whether the
 // strides are ones that the kernels take.
 bool cache_shape(int32_t num_pages, int32_t page_size, int32_t Hkv, int32_t d, int64_t page_stride,
@@ -42,8 +49,8 @@ extern "C" {
 size_t kda_tree_attention_workspace_bytes(int32_t N, int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d,
                                           kda_dtype_t dtype)
 {
-    if (N < 1 || Ts < 1 || Ts > kda::kTreeMaxNodes || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 ||
-        !supported_d(d) || !valid_dtype(dtype))
+    if (!valid_dtype(dtype) || !supported_d(d) || Ts > kda::kTreeMaxNodes ||
+        !attention_sizes(N, Ts, Hq, Hkv, d))
         return 0;
     return kda::tree_workspace_bytes(Ts, Hq, Hkv, d, dtype, kda::device_sm_count());
 }
@@ -58,12 +65,10 @@ kda_status_t kda_tree_attention(const void* q, const void* k, const void* v, con
 {
     if (!valid_dtype(dtype) || !supported_d(d)) return KDA_ERR_UNSUPPORTED;
     if (Ts > kda::kTreeMaxNodes) return KDA_ERR_UNSUPPORTED;
-    if (N < 1 || Ts < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0) return KDA_ERR_INVALID_ARG;
+    if (!attention_sizes(N, Ts, Hq, Hkv, d)) return KDA_ERR_INVALID_ARG;
     if (num_pages < 0 || page_size < 1 || max_pages < 0) return KDA_ERR_INVALID_ARG;
-    // Positions (of the drafted rows too) are 32-bit; a row tile is a block index.
-    if ((int64_t)max_pages * page_size > INT32_MAX - 1024 || (int64_t)Ts * Hq > (1 << 20) ||
-        (int64_t)Hkv * d > INT32_MAX)
-        return KDA_ERR_INVALID_ARG;
+    // Positions (of the drafted rows too) are 32-bit.
+    if ((int64_t)max_pages * page_size > INT32_MAX - 1024) return KDA_ERR_INVALID_ARG;
     if (!q || !k || !v || !lengths || !o) return KDA_ERR_INVALID_ARG;
     const bool cached = num_pages > 0 && max_pages > 0;
     if (cached && (!k_cache || !v_cache || !page_table)) return KDA_ERR_INVALID_ARG;

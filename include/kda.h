@@ -418,7 +418,8 @@ kda_status_t kda_prefill_noalloc(const void *q, const void *k, const void *v,
 
 /* Bytes of device workspace kda_tree_attention needs (partial results of
  * sequences whose keys are spread over several CTAs; it depends on the SM
- * count, not on N or the lengths).  0 for bad arguments. */
+ * count, not on N or the lengths).  0 for arguments that kda_tree_attention
+ * refuses; Ts * Hq is at most 2^20. */
 size_t kda_tree_attention_workspace_bytes(int32_t N, int32_t Ts, int32_t Hq,
                                           int32_t Hkv, int32_t d,
                                           kda_dtype_t dtype);

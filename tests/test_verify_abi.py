@@ -1,9 +1,14 @@
 """Argument checks of the calls that verify a tree of drafted tokens: each bad
 call returns its status before anything is launched (no GPU needed)."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 import gated_delta_rule_05_gb300 as kda
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 A = 0x10000            # a fake, aligned address: never dereferenced
 NULL = None
 BAD, UNSUPPORTED, WORKSPACE = kda.KDA_ERR_INVALID_ARG, kda.KDA_ERR_UNSUPPORTED, kda.KDA_ERR_WORKSPACE
@@ -140,3 +145,18 @@ def test_decode_tree_rejects_results_over_what_it_reads(lib, out, over, size):
         if apart[over] is not None:
             for at in (apart[over], apart[over] + (size - 1) // 16 * 16):
                 assert tree(lib, **{**apart, out: at}) == BAD
+
+
+@pytest.mark.parametrize("args", [(1, 64, 1 << 30, 1, 128, 0), (1, 64, 1 << 25, 1, 64, 2), (1, 64, (1 << 14) + 1, 1, 128, 1),
+                                  (1, 1, (1 << 20) + 1, 1, 128, 0), (1, 1, 1 << 24, 1 << 24, 128, 0)])
+def test_attention_workspace_of_sizes_that_the_call_refuses(args):
+    # in a process of its own: an arithmetic exception would end this one
+    code = "import gated_delta_rule_05_gb300 as k; print(k.kda_tree_attention_workspace_bytes(*%r))" % (args,)
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert out.returncode == 0 and out.stdout.strip() == "0", out
+    N, Ts, Hq, Hkv, d, dt = args
+    assert attention(kda.lib(), N=N, Ts=Ts, Hq=Hq, Hkv=Hkv, d=d, dt=dt) == BAD
+
+
+def test_attention_workspace_of_the_widest_call(lib):
+    assert kda.kda_tree_attention_workspace_bytes(1, 64, 1 << 14, 1, 128, kda.KDA_BF16) > 256
