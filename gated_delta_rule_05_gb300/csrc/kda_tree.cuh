@@ -41,6 +41,7 @@ struct TreeArgs {
     float* part;                      // 2 slots per CTA: [RT][d] o, [RT] m, [RT] l
     int32_t box, tile_pages, tile_rows;   // tensor-core kernel: rows per TMA box (0: none), and
                                       // a tile's keys as whole pages and rows
+    bool starve;                      // test of the waits that give up (tensor-core kernel)
     int32_t groups, row_tiles;        // CTA b: group b / row_tiles, row tile b % row_tiles
 };
 

@@ -36,8 +36,13 @@
 // is instructions, not the exponential unit.  Pages of 16 rows cost 3 % against
 // pages of 128.
 //
-// Every wait has a limit (mbar_wait); a wait that gives up sets the workspace's
-// timeout word, and the CTA runs to its end without waiting again.
+// Every wait has a limit; one that gives up sets the workspace's timeout word and
+// stops its CTA: the warps that start copies and products end at their next wait and
+// wait for what they have started (again with a limit), and the softmax runs on
+// without waiting, over whatever is there, and gives its rows a sum of NaN.  (The
+// softmax warps may then arrive early at each other's barriers; nothing that follows
+// from it is used.)  The environment variable KDA_TEST_STARVE_CONSUMERS, for the test
+// of that path only, has the copying warps exit at once.
 #include <cudaTypedefs.h>
 #include <stdio.h>
 
@@ -85,23 +90,31 @@ struct TcShared {
     long long loc[16 + 2];
 };
 
-// Waits for a phase of a barrier, for about two seconds at most (see mbar_wait),
-// and not at all once some wait of this CTA has given up.  Written short: the
+// Waits for a phase of a barrier, for about two seconds at most and no longer than
+// until some wait of this CTA has given up; false then.  Written short: the
 // roles run side by side and have to share the SM's instruction cache (with
 // mbar_wait's loops at every wait and all loops below unrolled they took 242 KB,
 // and a piece's start and end cost 20 us).
-__device__ __forceinline__ void wait(TcShared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
+__device__ __forceinline__ bool wait_lane(TcShared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
 {
-    if (mbar_try_wait(bar, parity)) return;
+    if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
 #pragma unroll 1
     while (!mbar_try_wait(bar, parity)) {
-        if (*reinterpret_cast<volatile int*>(&sh.dead)) return;
+        if (*reinterpret_cast<volatile int*>(&sh.dead)) return false;
         if (clock64() - t0 > (1ll << 32)) {
             *reinterpret_cast<volatile int*>(&sh.dead) = 1;
             atomicOr(status + kWsTimeoutWord, 2);
+            return false;
         }
     }
+    return true;
+}
+
+// The same for a warp, which goes on as one or stops as one.
+__device__ __forceinline__ bool wait(TcShared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
+{
+    return __all_sync(0xffffffffu, wait_lane(sh, bar, parity, status));
 }
 
 // One box of a page pool [num_pages][page_size][Hkv][d]: rows of one page, 64
@@ -300,10 +313,9 @@ struct Copier {
     __device__ uint64_t* full() const { return &sh.kv_full[slot]; }
 
     // Waits until the next entry's slot is free.
-    __device__ void wait_slot()
+    __device__ bool wait_slot()
     {
-        if (round > 0) wait(sh, &sh.kv_empty[slot], (uint32_t)(round - 1) & 1, a.status);
-        __syncwarp();
+        return round == 0 || wait(sh, &sh.kv_empty[slot], (uint32_t)(round - 1) & 1, a.status);
     }
 
     // This lane's row of a tile: its page and its place there, or kDrafted and
@@ -371,10 +383,10 @@ struct Copier {
     }
 
     // The next ring entry: the K or V rows of a piece's tile, the g-th tile of
-    // the CTA.
-    __device__ void load(bool is_k, const Piece& w, const Row& r, int g)
+    // the CTA.  False when the CTA has stopped.
+    __device__ bool load(bool is_k, const Piece& w, const Row& r, int g)
     {
-        wait_slot();
+        if (!wait_slot()) return false;
         const uint32_t there = __ballot_sync(0xffffffffu, cached(r));
         if (a.box > 0 && there == 0xffffffffu) {
             if (lane == 0) {
@@ -397,17 +409,20 @@ struct Copier {
             slot = 0;
             ++round;
         }
+        return true;
     }
 };
 
+// Returns how many ring entries it has filled.
 template <int D, int NT>
-__device__ void copy_role(TcShared& sh, const TreeArgs& a, const CUtensorMap* map_k, const CUtensorMap* map_v,
+__device__ int copy_role(TcShared& sh, const TreeArgs& a, const CUtensorMap* map_k, const CUtensorMap* map_v,
                           uint32_t slots, Piece w, bool go, int warp, int lane)
 {
     using Sh = TcShape<D, NT>;
     Copier<D, NT> c{sh, a, map_k, map_v, slots, lane, warp};
     int g = 0;                                     // tiles of the pieces before
-    for (; go; go = w.next(a)) {
+    bool ok = !a.starve;
+    for (; ok && go; go = w.next(a)) {
         const int cnt = w.t1 - w.t0;
         auto walk = c.walk_from(w.t0);
         // the rows of the tile whose V comes next, of the one after it, and of the
@@ -417,7 +432,7 @@ __device__ void copy_role(TcShared& sh, const TreeArgs& a, const CUtensorMap* ma
 #pragma unroll 1
         while (jv < cnt) {
             const bool is_k = jv >= 0 && jk < cnt && jk < jv + (NT == 1 ? 2 : 1);
-            if (jv >= 0) c.load(is_k, w, is_k && jk > jv ? row1 : row, g + (is_k ? jk : jv));
+            if (jv >= 0 && !(ok = c.load(is_k, w, is_k && jk > jv ? row1 : row, g + (is_k ? jk : jv)))) break;
             if (is_k) {
                 ++jk;
             } else {
@@ -429,12 +444,7 @@ __device__ void copy_role(TcShared& sh, const TreeArgs& a, const CUtensorMap* ma
         }
         g += cnt;
     }
-    // After a wait that gave up nothing else has waited for the copies in flight.
-    if (*reinterpret_cast<volatile int*>(&sh.dead))
-        for (int i = 0; i < Sh::kSlots; ++i) {
-            const int r = i < c.slot ? c.round : c.round - 1;
-            if (r >= 0) mbar_wait(&sh.kv_full[i], (uint32_t)r & 1, 1ll << 24);
-        }
+    return c.round * Sh::kSlots + c.slot;
 }
 
 template <int D, int NT>
@@ -443,8 +453,7 @@ __device__ void q_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, Piece w
 {
     int piece = 0;
     for (; go; go = w.next(a)) {
-        if (piece > 0) wait(sh, &sh.q_empty, (uint32_t)(piece - 1) & 1, a.status);
-        __syncwarp();
+        if (piece > 0 && !wait(sh, &sh.q_empty, (uint32_t)(piece - 1) & 1, a.status)) return;
 #pragma unroll 1
         for (int b = warp; b < NT * 4; b += kQWarps) {
             const int r = r0 + b * 32 + lane;
@@ -464,15 +473,16 @@ __device__ void q_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, Piece w
 
 // -------------------------------------------------------------- the products
 // D = Q K^T: K-major operands, d / 16 steps of 32 bytes within 64-column blocks
-// 16 KB apart.  One elected lane issues all steps.
+// 16 KB apart.  One elected lane issues all steps, if its ok is true.
 template <int D>
-__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t q_desc, uint64_t k_desc, uint32_t idesc)
+__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t q_desc, uint64_t k_desc, uint32_t idesc, bool ok)
 {
 #pragma unroll
     for (int b = 0; b < D / 64; ++b) {
         asm volatile(
             "{\n\t.reg .pred e, t, f;\n\t.reg .b64 x, y;\n\t"
             "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.and.b32 e, %5, 0, e;\n\t"
             "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
             "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
             "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
@@ -481,7 +491,7 @@ __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t q_desc, uint6
             "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
             "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
             "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d_tmem),
-            "l"(q_desc + 1024 * b), "l"(k_desc + 1024 * b), "r"(idesc), "r"(b)
+            "l"(q_desc + 1024 * b), "l"(k_desc + 1024 * b), "r"(idesc), "r"(b), "r"((int)ok)
             : "memory");
     }
 }
@@ -489,11 +499,12 @@ __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t q_desc, uint6
 // D (+)= P V for 64 keys: P in TMEM (8 columns of bf16 pairs per step), V MN-major
 // (16 keys of 128 bytes per step).
 __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_t v_desc, uint32_t idesc,
-                                         uint32_t accumulate)
+                                         uint32_t accumulate, bool ok)
 {
     asm volatile(
         "{\n\t.reg .pred e, t, f;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.and.b32 e, %5, 0, e;\n\t"
         "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
         "add.s32 x, %1, 8;\n\tadd.s64 y, %2, 128;\n\t"
@@ -502,14 +513,27 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint6
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
         "add.s32 x, %1, 24;\n\tadd.s64 y, %2, 384;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t}" ::"r"(d_tmem),
-        "r"(p_tmem), "l"(v_desc), "r"(idesc), "r"(accumulate)
+        "r"(p_tmem), "l"(v_desc), "r"(idesc), "r"(accumulate), "r"((int)ok)
+        : "memory");
+}
+
+// mma_commit (kda_sm100.cuh), if the elected lane's ok is true.
+__device__ __forceinline__ void commit_if(uint64_t* bar, bool ok)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.and.b32 e, %1, 0, e;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"((int)ok)
         : "memory");
 }
 
 // Takes the ring's entries in their order.  RT = 128: the scores of tile j + 1
 // before the output of tile j.  RT = 256: for both row tiles in turn, the output
 // of tile j and the scores of tile j + 1 (which go where tile j's P was: the
-// tensor core runs one thread's products in order).
+// tensor core runs one thread's products in order).  Once a wait has given up no
+// product is issued and nothing signalled any more; that is a predicate, as branches
+// out of these loops cost 5 % with 512 query rows.
 template <int D, int NT>
 __device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint32_t slots, Piece w, bool go,
                          int r0, uint32_t tmem)
@@ -521,12 +545,13 @@ __device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint3
     uint32_t turn = 0;                             // parity of its use
     int first = 0, piece = 0;                      // tiles of the pieces before, pieces
     const int nt = (NT == 2 && a.R - r0 > 128) ? 2 : 1;
+    bool ok = true;                                // no wait of this lane has given up
     const uint64_t q_desc = make_sdesc(q_smem, 16, 1024, kSwizzle128B);
 
     // Waits for the next ring entry; returns its slot.
     auto take = [&]() {
         const int mine = slot;
-        wait(sh, &sh.kv_full[mine], turn, a.status);
+        ok &= wait_lane(sh, &sh.kv_full[mine], turn, a.status);
         __syncwarp();
         tc_fence_after();
         if (++slot == Sh::kSlots) {
@@ -537,25 +562,25 @@ __device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint3
     };
     auto qk = [&](int i, int e, uint32_t d_tmem) {
         const uint32_t k = slots + (uint32_t)e * Sh::kSlotBytes;
-        issue_qk<D>(d_tmem, q_desc + (uint64_t)(i * 128 * D * 2 / 16), make_sdesc(k, 16, 1024, kSwizzle128B), id_qk);
+        issue_qk<D>(d_tmem, q_desc + (uint64_t)(i * 128 * D * 2 / 16), make_sdesc(k, 16, 1024, kSwizzle128B), id_qk, ok);
     };
     // the output of tile `tile`, the j-th of the piece, of row tile i
     auto pv = [&](int i, int e, int j, int tile, int buf, uint32_t phase) {
         const uint32_t v = slots + (uint32_t)e * Sh::kSlotBytes;
         const uint64_t v_desc = make_sdesc(v, KT * 128, 1024, kSwizzle128B);
         const uint32_t d_tmem = tmem + (i ? Sh::kO1 : Sh::kO0);
-        wait(sh, &sh.p_full[buf], phase, a.status);
-        if (j == 0 && piece > 0) wait(sh, &sh.o_empty[i], (uint32_t)(piece - 1) & 1, a.status);
+        ok &= wait_lane(sh, &sh.p_full[buf], phase, a.status);
+        if (j == 0 && piece > 0) ok &= wait_lane(sh, &sh.o_empty[i], (uint32_t)(piece - 1) & 1, a.status);
         __syncwarp();
         tc_fence_after();
-        issue_pv(d_tmem, tmem + buf * Sh::kS1, v_desc, id_pv, j > 0);
-        issue_pv(d_tmem, tmem + buf * Sh::kS1 + 32, v_desc + 512, id_pv, 1);
-        mma_commit(&sh.pv_done[i]);
+        issue_pv(d_tmem, tmem + buf * Sh::kS1, v_desc, id_pv, j > 0, ok);
+        issue_pv(d_tmem, tmem + buf * Sh::kS1 + 32, v_desc + 512, id_pv, 1, ok);
+        commit_if(&sh.pv_done[i], ok);
     };
 
     for (; go; go = w.next(a)) {
         const int cnt = w.t1 - w.t0;
-        wait(sh, &sh.q_full, (uint32_t)piece & 1, a.status);
+        ok &= wait_lane(sh, &sh.q_full, (uint32_t)piece & 1, a.status);
         if constexpr (NT == 1) {
             int jk = 0, jv = 0;
 #pragma unroll 1
@@ -564,14 +589,14 @@ __device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint3
                 if (jk < cnt && jk < jv + 2) {
                     const int t = first + jk;
                     qk(0, entry, tmem + (t & 1) * Sh::kS1);
-                    mma_commit(&sh.s_full[t & 1]);
-                    if (++jk == cnt) mma_commit(&sh.q_empty);
+                    commit_if(&sh.s_full[t & 1], ok);
+                    if (++jk == cnt) commit_if(&sh.q_empty, ok);
                 } else {
                     const int t = first + jv;
                     pv(0, entry, jv, t, t & 1, (uint32_t)(t >> 1) & 1);
                     ++jv;
                 }
-                mma_commit(&sh.kv_empty[entry]);
+                commit_if(&sh.kv_empty[entry], ok);
             }
         } else {
 #pragma unroll 1
@@ -586,20 +611,20 @@ __device__ void mma_role(TcShared& sh, const TreeArgs& a, uint32_t q_smem, uint3
                     if (more) {
                         if (i == 0) ek = take();
                         qk(i, ek, tmem + i * Sh::kS1);
-                        mma_commit(&sh.s_full[i]);
+                        commit_if(&sh.s_full[i], ok);
                     }
                 }
-                if (j >= 0) mma_commit(&sh.kv_empty[ev]);
-                if (more) mma_commit(&sh.kv_empty[ek]);
-                if (j + 2 == cnt) mma_commit(&sh.q_empty);
+                if (j >= 0) commit_if(&sh.kv_empty[ev], ok);
+                if (more) commit_if(&sh.kv_empty[ek], ok);
+                if (j + 2 == cnt) commit_if(&sh.q_empty, ok);
             }
         }
         first += cnt;
         ++piece;
     }
-    // the last arrivals on the ring's barriers come before the block ends
+    // the last products and their arrivals on the ring's barriers come before the block ends
     mma_commit(&sh.done);
-    wait(sh, &sh.done, 0, a.status);
+    mbar_wait(&sh.done, 0);
     __syncwarp();
 }
 
@@ -635,11 +660,11 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, Piece w, bool go, 
             // Every phase of pv_done is waited for in turn (wait_last): with RT =
             // 128 the scores of this tile may be there before the last tile's
             // product, and a parity names only the phase before the current one.
-            wait(sh, &sh.s_full[b], phase, a.status);
+            wait_lane(sh, &sh.s_full[b], phase, a.status);
             __syncwarp();
             tc_fence_after();
             auto wait_last = [&]() {
-                if (tile > 0) wait(sh, &sh.pv_done[NT == 1 ? 0 : wg], (uint32_t)(tile - 1) & 1, a.status);
+                if (tile > 0) wait_lane(sh, &sh.pv_done[NT == 1 ? 0 : wg], (uint32_t)(tile - 1) & 1, a.status);
             };
             if (live) {
                 const uint4 there = *reinterpret_cast<const uint4*>(sh.keys[tile % kRingMeta]);
@@ -725,9 +750,11 @@ __device__ void softmax_role(TcShared& sh, const TreeArgs& a, Piece w, bool go, 
             if (lane == 0) mbar_arrive(&sh.p_full[b]);
         }
         // the output of the piece
-        wait(sh, &sh.pv_done[NT == 1 ? 0 : wg], (uint32_t)(tile - 1) & 1, a.status);
+        wait_lane(sh, &sh.pv_done[NT == 1 ? 0 : wg], (uint32_t)(tile - 1) & 1, a.status);
         __syncwarp();
         tc_fence_after();
+        // when some wait has given up, this piece and those after it are not known
+        if (*reinterpret_cast<volatile int*>(&sh.dead)) l = __int_as_float(0x7fffffff);
         const bool whole = w.t0 == 0 && w.t1 == w.tiles;
         if (live) {
             const bool mine = r < a.R;
@@ -848,12 +875,13 @@ tree_attention_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_consta
     Piece first;
     const bool go = first.start(a, sp, group);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int filled = 0;
     if (warp < Sh::kCopyWarp) {
         more_registers<Sh::kMore>();
         softmax_role<D, NT>(sh, a, first, go, r0, warp, lane, tmem);
     } else if (warp < Sh::kMmaWarp) {
         fewer_registers<Sh::kFewer>();
-        copy_role<D, NT>(sh, a, &map_k, &map_v, slots, first, go, warp - Sh::kCopyWarp, lane);
+        filled = copy_role<D, NT>(sh, a, &map_k, &map_v, slots, first, go, warp - Sh::kCopyWarp, lane);
     } else {
         fewer_registers<Sh::kFewer>();
         if (warp == Sh::kMmaWarp)
@@ -863,6 +891,12 @@ tree_attention_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
+    // After a wait that gave up nobody has waited for the last copies in flight.
+    if (sh.dead) {
+#pragma unroll 1
+        for (int e = filled > Sh::kSlots ? filled - Sh::kSlots : 0; e < filled; ++e)
+            mbar_wait(&sh.kv_full[e % Sh::kSlots], (uint32_t)(e / Sh::kSlots) & 1, 1ll << 24);
+    }
     if (warp == Sh::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -915,6 +949,7 @@ cudaError_t launch_tree_attention_tc(TreeArgs args, const TreePlan& plan, int32_
     args.box = box;
     args.tile_pages = KT / args.page_size;
     args.tile_rows = KT % args.page_size;
+    args.starve = getenv("KDA_TEST_STARVE_CONSUMERS") != nullptr;
     if (d == 64)
         return plan.rt == 128 ? launch_tc<64, 1>(args, map_k, map_v, stream)
                               : launch_tc<64, 2>(args, map_k, map_v, stream);

@@ -446,8 +446,9 @@ size_t kda_tree_attention_workspace_bytes(int32_t N, int32_t Ts, int32_t Hq,
  * and scale > 0 runs on the tensor cores, with probabilities rounded to bf16 for
  * the second product; everything else, and everything when the environment
  * variable KDA_FORCE_SIMT is set, on the CUDA cores in fp32.  The waits of the
- * tensor-core kernel are bounded: one that gives up sets the int32 at byte 8 of
- * the workspace, which no call clears.  An infinity or NaN in a
+ * tensor-core kernel are bounded: one that gives up (after some two seconds) sets
+ * the int32 at byte 8 of the workspace, which no call clears, and the rows of o
+ * that depended on it are NaN.  An infinity or NaN in a
  * node's k or v reaches the nodes that see it and no others.  The result does
  * not depend on timing (no atomics on values); it may differ in rounding
  * between GPUs with different SM counts. */

@@ -13,7 +13,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests._tree import AttentionInputs, attention_reference
+from tests._tree import AttentionInputs, attention_reference, lineage
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -271,3 +271,29 @@ def test_in_a_cuda_graph(kda):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("d,Ts,G", [(128, 4, 2), (64, 33, 9)])
+def test_waits_that_give_up(kda, monkeypatch, d, Ts, G):
+    # Through the library's test hook: the copying warps exit at once, and the other
+    # warps' waits run out after their usual limit (about two seconds).  The call
+    # returns, the timeout word is set and every row that had anything to see is NaN,
+    # of items in one block and of items cut between several; the next call on the
+    # same workspace is right.  Nothing here traps or waits without a bound.
+    inp = AttentionInputs(3, Ts, 2 * G, 2, d, 64, [4000, 17, 900], BF16, seed=21)
+    inp.parent[1, Ts - 1] = -2
+    args = inp.on("cuda")
+    need = kda.kda_tree_attention_workspace_bytes(3, Ts, 2 * G, 2, d, kda.KDA_BF16)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    o = torch.full_like(args["q"], 5.0)
+    monkeypatch.setenv("KDA_TEST_STARVE_CONSUMERS", "1")
+    kda.kda_tree_attention(**args, o=o, workspace=ws)
+    torch.cuda.synchronize()
+    monkeypatch.delenv("KDA_TEST_STARVE_CONSUMERS")
+    assert ws[8:12].view(torch.int32).item() & 2, "the timeout bit must be set"
+    used = torch.tensor([[lineage(p, t) is not None for t in range(Ts)] for p in inp.parent], device="cuda")
+    assert not used.all() and torch.isnan(o[used]).all() and torch.all(o[~used] == 0)
+    ws[8:12].zero_()
+    kda.kda_tree_attention(**args, o=o, workspace=ws)
+    check(o, *attention_reference(inp), exact_p=False)
+    assert ws[8:12].view(torch.int32).item() == 0
