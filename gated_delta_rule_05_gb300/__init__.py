@@ -549,9 +549,12 @@ def _check_pages(name, t, dtype, device):
         raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    _, h, d = t.shape[-3:]
-    if t.numel() and t.stride()[-3:] != (h * d, d, 1):
-        raise ValueError("%s must be dense within a page" % name)
+    _, h, d = size = t.shape[-3:]
+    dense = (h * d, d, 1)
+    if t.numel() and t.stride()[-3:] != dense:
+        # the stride of a dimension of one is never used
+        if any(n > 1 and x != y for n, x, y in zip(size, t.stride()[-3:], dense)):
+            raise ValueError("%s must be dense within a page" % name)
 
 
 def kda_tree_attention_workspace_bytes(N: int, Ts: int, Hq: int, Hkv: int, d: int,

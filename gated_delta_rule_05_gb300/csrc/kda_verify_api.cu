@@ -36,8 +36,7 @@ bool cache_shape(int32_t num_pages, int32_t page_size, int32_t Hkv, int32_t d, i
                  size_t elem, size_t* bytes)
 {
     const int64_t page_elems = (int64_t)page_size * Hkv * d;
-    if (num_pages > 1 && page_stride < page_elems) return false;
-    if ((page_stride * (int64_t)elem) % 16 != 0) return false;
+    if (num_pages > 1 && (page_stride < page_elems || (page_stride * (int64_t)elem) % 16 != 0)) return false;
     *bytes = ((size_t)(num_pages - 1) * (size_t)(num_pages > 1 ? page_stride : 0) + (size_t)page_elems) * elem;
     return true;
 }

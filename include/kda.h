@@ -409,7 +409,7 @@ kda_status_t kda_prefill_noalloc(const void *q, const void *k, const void *v,
  * A cache is a pool of num_pages pages of page_size rows of Hkv heads,
  * [num_pages, page_size, Hkv, d], dense within a page, page p starting
  * page_stride elements after page p - 1 (page_stride >= page_size * Hkv * d,
- * a multiple of 16 bytes).  page_table [N, max_pages] (device int32) names the
+ * a multiple of 16 bytes; ignored for one page).  page_table [N, max_pages] (device int32) names the
  * pages of each sequence in order: position i of sequence n is row i %
  * page_size of page page_table[n][i / page_size].  Entries that no position
  * needs are never read; one that names no page (outside [0, num_pages)) hides

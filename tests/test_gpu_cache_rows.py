@@ -185,3 +185,19 @@ def test_append_of_any_cu_seqlens_counts_the_rows_that_it_wrote(kda, cu):
     new = kda.kda_cache_append(k, v, c(cu), kc, vc, c(table), c(lengths))
     assert torch.equal(kc, want[0]) and torch.equal(vc, want[1])
     assert new.tolist() == (lengths + count).tolist()
+
+
+@pytest.mark.parametrize("layers,P,page,Hkv,odd", [(2, 1, 8, 2, 1), (1, 3, 8, 2, 0), (2, 3, 1, 2, 2), (2, 3, 8, 1, 3)])
+def test_strides_of_dimensions_of_one_do_not_matter(kda, layers, P, page, Hkv, odd):
+    kc, vc = pools(layers, P, page, Hkv, 16, F32)
+    k, v = (torch.randn((layers, 1, 2, Hkv, 16), device="cuda") for _ in range(2))
+    table = torch.arange(P, dtype=torch.int32, device="cuda")[None]
+    stride = list(kc.stride())
+    stride[odd] = 12345
+    kda.kda_cache_commit(k, v, None, None, kc.as_strided(kc.shape, stride), vc.as_strided(vc.shape, stride), table,
+                         torch.tensor([1], dtype=torch.int32, device="cuda"))
+    for pool, x in ((kc, k), (vc, v)):
+        rows = pool.reshape(layers, P * page, Hkv, 16)
+        places = [i for i in (1, 2) if i < P * page]
+        assert torch.equal(rows[:, places], x[:, 0, :len(places)])
+        assert torch.all(rows[:, [i for i in range(P * page) if i not in places]] == (9 if x is k else 10))

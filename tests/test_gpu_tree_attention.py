@@ -297,3 +297,19 @@ def test_waits_that_give_up(kda, monkeypatch, d, Ts, G):
     kda.kda_tree_attention(**args, o=o, workspace=ws)
     check(o, *attention_reference(inp), exact_p=False)
     assert ws[8:12].view(torch.int32).item() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("page,Hkv,pages,odd", [(64, 2, 1, 0), (64, 1, 5, 2), (1, 2, 40, 1), (1, 1, 1, 0)])
+def test_strides_of_dimensions_of_one_do_not_matter(kda, dtype, page, Hkv, pages, odd):
+    lengths = [min(page * pages - 1, 37), 0]
+    inp = AttentionInputs(2, 3, 2 * Hkv, Hkv, 64, page, lengths, dtype, seed=22)
+    args = inp.on("cuda")
+    for name in ("k_cache", "v_cache"):
+        t = args[name][inp.table[0, :pages].tolist()].contiguous()
+        stride = list(t.stride())
+        stride[odd] = 12345
+        args[name] = t.as_strided(t.shape, stride)
+    table = torch.arange(args["k_cache"].shape[0], dtype=torch.int32)
+    args["page_table"] = torch.stack([table, table]).cuda()
+    check(kda.kda_tree_attention(**args), *attention_reference(inp), exact_p=dtype == F32)
