@@ -475,6 +475,16 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
+def _forward_only(name, *tensors):
+    """The calls below have no backward pass; a result without one, where one is
+    wanted, would pass for a constant."""
+    if _torch().is_grad_enabled():
+        for t in tensors:
+            if t.requires_grad:
+                raise RuntimeError("%s has no backward pass: call it under torch.no_grad() or on "
+                                   "detached tensors" % name)
+
+
 def _new(shape, dtype, device, stream):
     """An output or workspace the caller did not pass.  It belongs to the stream
     that uses it: memory freed on the current stream, or reused there after the
@@ -518,6 +528,7 @@ def kda_decode_tree(q, k, v, log_alpha, beta, S_in, parent=None, *, o=None, stat
     context, -2 for an unused one (o = 0, its state not written), None for a
     chain.  Returns (o [N, Ts, H, d_v], states [N, Ts, H, d_k, d_v])."""
     torch = _torch()
+    _forward_only("kda_decode_tree", q, k, v, log_alpha, beta, S_in)
     N, Ts, H, dk = q.shape
     dv = v.shape[3]
     if o_dtype is None:
@@ -581,6 +592,7 @@ def kda_tree_attention(q, k, v, k_cache, v_cache, page_table, lengths, parent=No
     unused) or None for a chain; scale: d ** -0.5 by default.  Returns o
     [N, Ts, Hq, d]."""
     torch = _torch()
+    _forward_only("kda_tree_attention", q, k, v, k_cache, v_cache)
     N, Ts, Hq, d = q.shape
     Hkv = k.shape[2]
     dev = q.device
@@ -625,6 +637,7 @@ def kda_token_logprobs(logits, tokens=None, num_top=0, *, logprobs=None, entropy
     None (J = 0).  Returns (logprobs [T, J], entropy [T], top_ids [T, num_top]
     int32, top_logprobs [T, num_top]), all but the ids fp32."""
     torch = _torch()
+    _forward_only("kda_token_logprobs", logits)
     T, V = logits.shape
     dev = logits.device
     if not logits.is_cuda:
@@ -691,6 +704,7 @@ def kda_cache_commit(k, v, path, count, k_cache, v_cache, page_table, lengths, *
     lengths: int32 [N] (not changed).  Returns new_lengths [N]."""
     torch = _torch()
     _, N, Ts, _, _ = k.shape
+    _forward_only("kda_cache_commit", k, v, k_cache, v_cache)
     _check_cuda("path", path, torch.int32)
     _check_cuda("count", count, torch.int32)
     if path is not None:
@@ -709,6 +723,7 @@ def kda_cache_append(k, v, cu_seqlens, k_cache, v_cache, page_table, lengths, *,
     the rest as in kda_cache_commit.  Returns new_lengths [N]."""
     torch = _torch()
     _, T, _, _ = k.shape
+    _forward_only("kda_cache_append", k, v, k_cache, v_cache)
     _check_cuda("cu_seqlens", cu_seqlens, torch.int32)
     _shape("lengths", lengths, (cu_seqlens.shape[0] - 1,))
     return _cache_rows("kda_cache_append", k, v, (cu_seqlens.data_ptr(), T), k_cache,

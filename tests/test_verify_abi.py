@@ -5,6 +5,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 import gated_delta_rule_05_gb300 as kda
 
@@ -160,3 +161,28 @@ def test_attention_workspace_of_sizes_that_the_call_refuses(args):
 
 def test_attention_workspace_of_the_widest_call(lib):
     assert kda.kda_tree_attention_workspace_bytes(1, 64, 1 << 14, 1, 128, kda.KDA_BF16) > 256
+
+
+def _calls():
+    """Each wrapper with the tensors whose gradients it would drop (on the CPU, where
+    they are refused too, for being there)."""
+    f, i = torch.zeros, lambda *s: torch.zeros(s, dtype=torch.int32)
+    x, c = f(1, 2, 1, 16), f(3, 4, 1, 16)
+    pool = [f(1, 3, 4, 1, 16), f(1, 3, 4, 1, 16)]
+    return {
+        "kda_decode_tree": ([x, x, x, x, f(1, 2, 1), f(1, 1, 16, 16)], [i(1, 2)]),
+        "kda_tree_attention": ([x, x, x, c, c], [i(1, 3), i(1), i(1, 2)]),
+        "kda_token_logprobs": ([f(2, 8)], [i(2, 1)]),
+        "kda_cache_commit": ([x[None], x[None]], [i(1, 2), i(1)] + pool + [i(1, 3), i(1)]),
+        "kda_cache_append": ([x, x], [i(2)] + pool + [i(1, 3), i(1)]),
+    }
+
+
+@pytest.mark.parametrize("name,at", [(n, k) for n, (x, _) in _calls().items() for k in range(len(x))])
+def test_gradients_are_refused_not_dropped(name, at):
+    call, (floats, rest) = getattr(kda, name), _calls()[name]
+    floats = [t.clone().requires_grad_(k == at) for k, t in enumerate(floats)]
+    with pytest.raises(RuntimeError, match=name + " has no backward pass"):
+        call(*floats, *rest)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensor"):
+        call(*floats, *rest)
