@@ -590,7 +590,8 @@ def kda_tree_attention(q, k, v, k_cache, v_cache, page_table, lengths, parent=No
     pages at any stride (both at the same); page_table: int32 [N, max_pages];
     lengths: int32 [N]; parent: int32 [N, Ts] (-1: follows the context, -2:
     unused) or None for a chain; scale: d ** -0.5 by default.  Returns o
-    [N, Ts, Hq, d]."""
+    [N, Ts, Hq, d].  NaN in o where the inputs have none means that a wait in the
+    kernel gave up."""
     torch = _torch()
     _forward_only("kda_tree_attention", q, k, v, k_cache, v_cache)
     N, Ts, Hq, d = q.shape
@@ -633,7 +634,8 @@ def kda_token_logprobs(logits, tokens=None, num_top=0, *, logprobs=None, entropy
     """Log probabilities of given tokens, the entropy and the ``num_top`` most
     probable tokens of each row of logits (C ABI: kda_token_logprobs).
 
-    logits: [T, V] bf16 or fp32, rows at any stride; tokens: int32 [T, J] or
+    logits: [T, V] bf16 or fp32, rows at any stride, the first at a multiple of 16
+    bytes (clone() a slice that is not); tokens: int32 [T, J] or
     None (J = 0).  Returns (logprobs [T, J], entropy [T], top_ids [T, num_top]
     int32, top_logprobs [T, num_top]), all but the ids fp32."""
     torch = _torch()

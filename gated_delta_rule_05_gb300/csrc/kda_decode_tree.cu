@@ -20,7 +20,9 @@
 // slabs of 32 write 128 bytes here and there, 375 us instead of 340 for 64
 // sequences of 16 nodes (12.25 used on average) of 32 heads, d = 128, i.e. 5,060
 // GB/s of states; the whole width needs 64 registers a thread and spills, 349
-// us.  A chain of the same size takes 390 us, 5,970 GB/s.  Few (sequence, head)
+// us.  A chain of the same size takes 390 us, 5,970 GB/s.  All 16 nodes used: d = 128
+// 427 us, d = 64 129, d = 32 53, d = 16 23 (80, 66, 41 and 23 % of a copy: the steps
+// stay as many).  Few (sequence, head)
 // units (fewer than SMs) take slabs of 32, for the CTAs: one sequence of 8 nodes
 // 12 us instead of 18.  The inputs of the next nodes are loaded and combined
 // (alpha k, alpha q, k . q) ahead of their steps, which then touch shared memory

@@ -29,8 +29,8 @@
 // the last are taken singly; all others come in 16-byte loads, the next round's
 // on their way during this one's arithmetic.
 //
-// Bound by HBM for long batches (4,096 x 50,257 fp32, K = 20: 151 us, 5.5 TB/s, 82 %
-// of a copy); 512 x 131,072 bf16 (37 us, 3.6 TB/s) by instructions (61 % of the
+// Bound by HBM for long batches (4,096 x 50,257 fp32, K = 20: 148 us, 5.6 TB/s, 83 %
+// of a copy); 512 x 131,072 bf16 (37 us, 3.6 TB/s) by instructions (60 % of the
 // issue slots) and by 512 rows on 152 SMs: three rows on some, four on others.
 //
 // One cluster of CTAs per row splits a row into slices when there are few rows;
@@ -571,11 +571,11 @@ cudaError_t launch(const void* logits, long long row_stride, const int32_t* toke
 
 // Many rows: a CTA of 128 threads per row, eight on an SM, whose reductions
 // hide behind one another's loads.  Few rows: 256 threads, and up to eight CTAs
-// per row as long as they are not more than two per SM.  Measured on one GB300
-// (128 and 256 threads): 4,096 x 50,257 fp32, K = 20, 151 and 165 us; 2,048 x
-// 131,072 bf16, K = 8, 107 and 114 us; 512 x 131,072 39 and 35 us; 1 x 131,072,
-// K = 20, 17 and 13 us.  Two and four parts a row at 512 rows: 44 and 61 us, with
-// 128 threads 36 and 48; at 200 rows, where two are taken, 21 and 29.
+// per row as long as they are not more than two per SM.  Measured on one GB300 in a
+// graph (128 and 256 threads): 4,096 x 50,257 fp32, K = 20, 147 and 160 us; 2,048 x
+// 131,072 bf16, K = 8, 102 and 108 us; 512 x 131,072 38 and 34 us; 1 x 131,072,
+// K = 20, eight CTAs, 16 and 12 us.  Two and four parts a row at 512 rows: 41 and 56
+// us, with 128 threads 35 and 46; at 200 rows one part 23, two (taken) 20, four 28.
 cudaError_t launch_token_logprobs(const void* logits, long long row_stride, const int32_t* tokens,
                                   int32_t T, int32_t V, int32_t J, int32_t K, bool bf16,
                                   float* logprobs, float* entropy, int32_t* top_ids,

@@ -88,7 +88,8 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool there)
 // butterfly a key; 60 % of the issue slots), not by HBM: fp32, 16 heads, 5 nodes, 8
 // contexts of 10 to 4000 rows, d = 64: 46 us (3.0 TB/s), 60 with one loop for all
 // keys and with selects in the butterfly instead of q's permuted places; d = 128, 8
-// nodes, 8 x 4096 rows: 132 us (4.1 TB/s).  K and V straight to registers, one or
+// nodes, 8 x 4096 rows: 132 us (4.1 TB/s); bf16, 16 heads, 5 nodes, 8 x 4096 rows:
+// d = 32 38 us, d = 16 34 us (1.8 and 1.0 TB/s: as many steps of less).  K and V straight to registers, one or
 // two steps ahead: 1.8 times as long; 4 keys a step 1.2 times.
 constexpr int kAhead = 4;            // stages of two keys; 3 cost 5 % with one row
 constexpr int kStreamRows = 8;
@@ -406,7 +407,8 @@ tree_attention_stream_kernel(const TreeArgs a)
 // page numbers are loaded two tiles before that.  Bound by shared-memory reads
 // (6 words of K and q for 8 FMAs) and by the few warps that its registers leave:
 // fp32, 8 x 16 nodes, 32 heads on 8, 8 x 4096 rows: d = 128 313 us (27 TFLOP/s),
-// d = 64 160 us; 352 and 210 with scalar FMAs and one loop for all keys.
+// d = 64 160 us; 352 and 210 with scalar FMAs and one loop for all keys.  bf16, 16
+// heads on 4, 8 x 16 nodes, 8 x 4096 rows: d = 32 64 us, d = 16 48 us.
 constexpr int kTileThreads = 128;
 constexpr int kTileKeys = 32;
 constexpr int kTileRows = 32;

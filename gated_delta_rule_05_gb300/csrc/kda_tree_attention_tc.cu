@@ -27,10 +27,10 @@
 // at the end.
 //
 // Bound, for few rows per cache head, by HBM: 32 x 16 nodes over contexts of 0 to
-// 16,384 rows, 64 rows per cache head, 189 us, 5.7 TB/s (85 % of a copy), 64 x
+// 16,384 rows, 64 rows per cache head, 187 us, 5.8 TB/s (86 % of a copy), 64 x
 // 4,096 rows, one token, 6.0 TB/s.  For many rows by the softmax beside the
-// products: 4 x 64 nodes over 32K to 64K rows, 512 rows per cache head, 349 us, 1.18
-// PFLOP/s (63 % of a library product), tensor pipe 53 % busy.  TMEM has room for one
+// products: 4 x 64 nodes over 32K to 64K rows, 512 rows per cache head, 352 us, 1.17
+// PFLOP/s (63 % of a library product), tensor pipe 54 % busy.  TMEM has room for one
 // S per row tile then, so that a row tile's softmax and products take turns; a
 // polynomial on the FMA pipe for every eighth exponential makes it 6 % slower, so it
 // is instructions, not the exponential unit.  Pages of 16 rows cost 3 % against

@@ -393,7 +393,10 @@ kda_status_t kda_prefill_noalloc(const void *q, const void *k, const void *v,
  *
  * The KDA layers of a model stand beside layers of softmax attention over a
  * cache ("[논문 리뷰] Kimi K3 Technical Report", section 1: 69 of 93 layers are
- * KDA), and a drafter may propose a tree instead of a chain.  One verification
+ * KDA), and a drafter may propose a tree instead of a chain.  (The other layers of
+ * that model are MLA, whose cache is one latent row for all heads: these calls do
+ * not read it.  They serve models whose softmax layers keep keys and values per
+ * cache head, of 16 to 128 channels.)  One verification
  * step is then: kda_decode_tree in the KDA layers, kda_tree_attention in the
  * others, kda_token_logprobs on the logits; and after the caller has chosen
  * the accepted path, kda_state_gather (with accept[n] = last accepted node + 1)
