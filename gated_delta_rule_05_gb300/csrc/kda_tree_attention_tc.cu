@@ -416,7 +416,7 @@ struct Copier {
 // Returns how many ring entries it has filled.
 template <int D, int NT>
 __device__ int copy_role(TcShared& sh, const TreeArgs& a, const CUtensorMap* map_k, const CUtensorMap* map_v,
-                          uint32_t slots, Piece w, bool go, int warp, int lane)
+                         uint32_t slots, Piece w, bool go, int warp, int lane)
 {
     using Sh = TcShape<D, NT>;
     Copier<D, NT> c{sh, a, map_k, map_v, slots, lane, warp};
