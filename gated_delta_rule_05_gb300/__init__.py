@@ -19,6 +19,9 @@ Functions (same names as the C ABI):
   kda_token_logprobs(logits, tokens, num_top=0, ...)
   kda_cache_commit(k, v, path, count, k_cache, v_cache, page_table, lengths, ...)
   kda_cache_append(k, v, cu_seqlens, k_cache, v_cache, page_table, lengths, ...)
+  kda_prompt_attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, ...)
+  kda_cache_append_rotary(q, k, v, cu_seqlens, inv_freq, k_cache, v_cache, page_table, lengths, ...)
+  kda_cache_attention_e4m3(q, k_cache, v_cache, k_scales, v_scales, page_table, lengths, ...)
   kda_prefill_workspace_bytes(num_seqs, H, d_k, d_v)
   kda_status_string(code)
 """
@@ -41,7 +44,9 @@ EXPORTS = ("kda_prefill_workspace_bytes", "kda_prefill", "kda_decode_step",
            "kda_decode_step_fused", "kda_prefill_host_staging_bytes", "kda_prefill_host",
            "kda_prefill_segmented_workspace_bytes", "kda_prefill_segmented",
            "kda_decode_tree", "kda_tree_attention_workspace_bytes", "kda_tree_attention",
-           "kda_token_logprobs", "kda_cache_commit", "kda_cache_append")
+           "kda_token_logprobs", "kda_cache_commit", "kda_cache_append",
+           "kda_prompt_attention", "kda_cache_append_rotary",
+           "kda_cache_attention_e4m3_workspace_bytes", "kda_cache_attention_e4m3")
 
 
 class KdaError(RuntimeError):
@@ -116,6 +121,22 @@ def _declare(lib):
     lib.kda_cache_append.restype = ctypes.c_int
     lib.kda_cache_append.argtypes = [_vp, _vp, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
                                      _i32, _i32, _i64, _i64, ctypes.c_int, _vp, _vp, _vp, _vp]
+    lib.kda_prompt_attention.restype = ctypes.c_int
+    lib.kda_prompt_attention.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _i64,
+                                         _i64, _i32, _i32, _i32, ctypes.c_int, ctypes.c_float,
+                                         _vp, _vp, _vp]
+    lib.kda_cache_append_rotary.restype = ctypes.c_int
+    lib.kda_cache_append_rotary.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i32,
+                                            _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                            _i32, _i64, _i32, ctypes.c_int, _vp, _i64, _vp, _i64,
+                                            _vp, _vp, _vp, _vp, _vp, _vp]
+    lib.kda_cache_attention_e4m3_workspace_bytes.restype = _sz
+    lib.kda_cache_attention_e4m3_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32,
+                                                             ctypes.c_int]
+    lib.kda_cache_attention_e4m3.restype = ctypes.c_int
+    lib.kda_cache_attention_e4m3.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
+                                             _i32, _i32, _i32, _i32, _i32, _i64, _i32,
+                                             ctypes.c_int, ctypes.c_float, _vp, _vp, _sz, _vp]
     return lib
 
 
@@ -730,6 +751,200 @@ def kda_cache_append(k, v, cu_seqlens, k_cache, v_cache, page_table, lengths, *,
     _shape("lengths", lengths, (cu_seqlens.shape[0] - 1,))
     return _cache_rows("kda_cache_append", k, v, (cu_seqlens.data_ptr(), T), k_cache,
                         v_cache, page_table, lengths, new_lengths, (), stream)
+
+
+def _check_rows(name, t, dtype, device):
+    """Tokens [T, h, d] at any stride, dense within a token; the stride."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    T, h, d = t.shape
+    row, head, one = t.stride()
+    if t.numel() and ((one != 1 and d > 1) or (head != d and h > 1)):
+        raise ValueError("%s must be dense within a token" % name)
+    return row if T > 1 else h * d
+
+
+def kda_prompt_attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=None, o=None,
+                         status=None, stream=None, o_dtype=None):
+    """Causal softmax attention over packed sequences (C ABI:
+    kda_prompt_attention).
+
+    q: [T, Hq, d]; k, v: [Tk, Hkv, d], dense within a token, the tokens at any
+    stride (views of one projection's output); cu_seqlens: int32 [N+1] or None for
+    one sequence; cu_seqlens_k: the same for k and v, None when it is cu_seqlens.  The
+    queries of a sequence are its last: query i sees keys 0 .. i + Lk - Lq.  scale:
+    d ** -0.5 by default.  status: int32 [1] or None, bit 1 set when a wait in the
+    kernel gave up (o has NaN then).  Returns o [T, Hq, d]; rows of an ``o`` that
+    cu_seqlens gives to no sequence keep what they hold."""
+    torch = _torch()
+    _forward_only("kda_prompt_attention", q, k, v)
+    T, Hq, d = q.shape
+    Tk, Hkv, _ = k.shape
+    dev = q.device
+    if o_dtype is None:
+        o_dtype = o.dtype if o is not None else q.dtype
+    dt = _dtype_code(q, o_dtype)
+    strides = [_check_rows(name, t, q.dtype, dev) for name, t in (("q", q), ("k", k), ("v", v))]
+    _check_cuda("cu_seqlens", cu_seqlens, torch.int32)
+    _check_cuda("cu_seqlens_k", cu_seqlens_k, torch.int32)
+    _check_cuda("status", status, torch.int32)
+    _shape("k", k, (Tk, Hkv, d))
+    _shape("v", v, (Tk, Hkv, d))
+    N = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    if cu_seqlens_k is not None:
+        if cu_seqlens is None:
+            raise ValueError("cu_seqlens_k needs cu_seqlens")
+        _shape("cu_seqlens_k", cu_seqlens_k, cu_seqlens.shape)
+    elif Tk != T:
+        raise ValueError("k must have q's tokens, or cu_seqlens_k be given")
+    o = _out("o", o, (T, Hq, d), o_dtype, dev, stream)
+    _call("kda_prompt_attention", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
+          _address(cu_seqlens), _address(cu_seqlens_k), N, T, Tk, Hq, Hkv, d, dt,
+          d ** -0.5 if scale is None else scale, o.data_ptr(), _address(status))
+    return o
+
+
+def _check_scales(name, t, pages, page, Hkv, device):
+    """The scales of a cache of 8 bits; the rows of a block."""
+    torch = _torch()
+    if t is None or t.device != device:
+        raise ValueError("%s must be given, on %s" % (name, device))
+    _check_cuda(name, t, torch.float32)
+    _shape(name, t, (pages, t.shape[1], Hkv))
+    if t.shape[1] < 1 or page % t.shape[1] != 0:
+        raise ValueError("%s: %d blocks do not divide a page of %d rows" % (name, t.shape[1], page))
+    return page // t.shape[1]
+
+
+def kda_cache_append_rotary(q, k, v, cu_seqlens, inv_freq, k_cache, v_cache, page_table, lengths,
+                            *, k_scales=None, v_scales=None, interleaved=False, q_out=None,
+                            k_out=None, want_k=False, new_lengths=None, stream=None):
+    """Queries and keys turned to their positions lengths[n] + i, keys and values
+    into the pages of a cache (C ABI: kda_cache_append_rotary).
+
+    q: [T, Hq, d] or None; k, v: [T, Hkv, d], dense within a token, the tokens at
+    any stride; cu_seqlens: int32 [N+1]; inv_freq: fp32 [r / 2], the first r channels
+    are turned, as pairs (j, j + r / 2) or, interleaved, (2 j, 2 j + 1); k_cache,
+    v_cache: [num_pages, page_size, Hkv, d], dense within a page, in k's dtype or
+    float8_e4m3fn, then with k_scales, v_scales: fp32 [num_pages, blocks, Hkv];
+    page_table: int32 [N, max_pages]; lengths: int32 [N] (not changed).
+    q_out, k_out may be q and k themselves.  Returns (q_out, k_out, new_lengths);
+    k_out is None when it was neither given nor wanted."""
+    torch = _torch()
+    _forward_only("kda_cache_append_rotary", k, v, inv_freq, *(() if q is None else (q,)))
+    T, Hkv, d = k.shape
+    dev = k.device
+    if k.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("unsupported dtype %s" % k.dtype)
+    dt = KDA_BF16 if k.dtype == torch.bfloat16 else KDA_FP32
+    k_stride, v_stride = _check_rows("k", k, k.dtype, dev), _check_rows("v", v, k.dtype, dev)
+    _shape("v", v, (T, Hkv, d))
+    for name, t in (("cu_seqlens", cu_seqlens), ("page_table", page_table), ("lengths", lengths)):
+        _check_cuda(name, t, torch.int32)
+    _check_cuda("inv_freq", inv_freq, torch.float32)
+    _shape("inv_freq", inv_freq, (inv_freq.shape[0],))
+    N = lengths.shape[0]
+    _shape("lengths", lengths, (N,))
+    _shape("cu_seqlens", cu_seqlens, (N + 1,))
+    _shape("page_table", page_table, (N, page_table.shape[1]))
+    eight = k_cache.dtype == torch.float8_e4m3fn
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check_pages(name, t, torch.float8_e4m3fn if eight else k.dtype, dev)
+        _shape(name, t, (k_cache.shape[0], k_cache.shape[1], Hkv, d))
+    pages, page = k_cache.shape[:2]
+    if pages > 1 and k_cache.stride(0) != v_cache.stride(0):
+        raise ValueError("k_cache and v_cache must have the same page stride")
+    block = 0
+    if eight:
+        block = _check_scales("k_scales", k_scales, pages, page, Hkv, dev)
+        if _check_scales("v_scales", v_scales, pages, page, Hkv, dev) != block:
+            raise ValueError("k_scales and v_scales must have the same blocks")
+    elif k_scales is not None or v_scales is not None:
+        raise ValueError("k_scales and v_scales belong to a cache of float8_e4m3fn")
+    Hq = q_stride = q_out_stride = k_out_stride = 0
+    if q is not None:
+        Hq = q.shape[1]
+        q_stride = _check_rows("q", q, k.dtype, dev)
+        _shape("q", q, (T, Hq, d))
+        if q_out is None:
+            q_out = _new((T, Hq, d), k.dtype, dev, stream)
+        q_out_stride = _check_rows("q_out", q_out, k.dtype, dev)
+        _shape("q_out", q_out, (T, Hq, d))
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if k_out is None and want_k:
+        k_out = _new((T, Hkv, d), k.dtype, dev, stream)
+    if k_out is not None:
+        k_out_stride = _check_rows("k_out", k_out, k.dtype, dev)
+        _shape("k_out", k_out, (T, Hkv, d))
+    new_lengths = _out("new_lengths", new_lengths, (N,), torch.int32, dev, stream)
+    _call("kda_cache_append_rotary", dev, stream, _address(q), k.data_ptr(), v.data_ptr(),
+          q_stride, k_stride, v_stride, cu_seqlens.data_ptr(), T, inv_freq.data_ptr(),
+          2 * inv_freq.shape[0], int(bool(interleaved)), page_table.data_ptr(),
+          lengths.data_ptr(), N, Hq, Hkv, d, pages, page, page_table.shape[1], k_cache.stride(0),
+          block, dt, _address(q_out), q_out_stride, _address(k_out), k_out_stride,
+          k_cache.data_ptr(), v_cache.data_ptr(), _address(k_scales), _address(v_scales),
+          new_lengths.data_ptr())
+    return q_out, k_out, new_lengths
+
+
+def kda_cache_attention_e4m3_workspace_bytes(N: int, Ts: int, Hq: int, Hkv: int, d: int,
+                                             dtype: int) -> int:
+    return int(lib().kda_cache_attention_e4m3_workspace_bytes(N, Ts, Hq, Hkv, d, dtype))
+
+
+@functools.lru_cache(maxsize=1024)
+def _e4m3_bytes(device, *sizes):
+    """kda_cache_attention_e4m3_workspace_bytes on ``device``, at least 256."""
+    with _torch().cuda.device(device):
+        return max(kda_cache_attention_e4m3_workspace_bytes(*sizes), 256)
+
+
+def kda_cache_attention_e4m3(q, k_cache, v_cache, k_scales, v_scales, page_table, lengths, *,
+                             scale=None, o=None, workspace=None, stream=None, o_dtype=None):
+    """Attention of each sequence's Ts newest tokens to a cache of 8 bits that
+    holds them already (C ABI: kda_cache_attention_e4m3).
+
+    q: [N, Ts, Hq, d]; k_cache, v_cache: float8_e4m3fn [num_pages, page_size, Hkv,
+    d], dense within a page (both at the same page stride); k_scales, v_scales: fp32
+    [num_pages, blocks, Hkv]; page_table: int32 [N, max_pages]; lengths: int32 [N],
+    the Ts tokens counted (new_lengths of kda_cache_append_rotary): token t sees
+    rows 0 .. lengths[n] - Ts + t.  scale: d ** -0.5 by default.  Returns o [N, Ts,
+    Hq, d]."""
+    torch = _torch()
+    _forward_only("kda_cache_attention_e4m3", q, k_scales, v_scales)
+    N, Ts, Hq, d = q.shape
+    dev = q.device
+    if o_dtype is None:
+        o_dtype = o.dtype if o is not None else q.dtype
+    dt = _dtype_code(q, o_dtype)
+    _check_cuda("q", q)
+    for name, t in (("page_table", page_table), ("lengths", lengths)):
+        _check_cuda(name, t, torch.int32)
+    pages, page, Hkv, _ = k_cache.shape
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check_pages(name, t, torch.float8_e4m3fn, dev)
+        _shape(name, t, (pages, page, Hkv, d))
+    if pages > 1 and k_cache.stride(0) != v_cache.stride(0):
+        raise ValueError("k_cache and v_cache must have the same page stride")
+    block = _check_scales("k_scales", k_scales, pages, page, Hkv, dev)
+    if _check_scales("v_scales", v_scales, pages, page, Hkv, dev) != block:
+        raise ValueError("k_scales and v_scales must have the same blocks")
+    _shape("page_table", page_table, (N, page_table.shape[1]))
+    _shape("lengths", lengths, (N,))
+    o = _out("o", o, (N, Ts, Hq, d), o_dtype, dev, stream)
+    if workspace is None:
+        workspace = _new((_e4m3_bytes(dev, N, Ts, Hq, Hkv, d, dt),), torch.uint8, dev, stream)
+    else:
+        _check_cuda("workspace", workspace)
+    _call("kda_cache_attention_e4m3", dev, stream, q.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), page_table.data_ptr(),
+          lengths.data_ptr(), N, Ts, Hq, Hkv, d, pages, page, page_table.shape[1],
+          k_cache.stride(0), block, dt, d ** -0.5 if scale is None else scale, o.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return o
 
 
 def kda_prefill_fused(q, k, v, z, A, beta, S0=None, cu_seqlens=None, *, q_scale, o=None,

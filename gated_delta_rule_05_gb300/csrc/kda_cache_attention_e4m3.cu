@@ -1,0 +1,621 @@
+// kda_cache_attention_e4m3.cu -- attention of a sequence's newest tokens to a paged
+// cache of 8-bit keys and values with a scale per block of rows and head.
+//
+// Per 16 keys and 16 query rows (the Ts G rows that share a cache head), one warp:
+//     S = Q K^T, s = c ks S (c = scale log2 e, ks the key's scale)
+//     P = 2^(s - m), w = P vs 2^(m - n) (vs the value's scale), O += w V
+// on mma.sync m16n8k16 with K and V widened to fp16 in registers, which holds e4m3
+// exactly.  m and n are references near the running maxima of s and of s + log2 vs
+// of each row: P and w stay below 2^8, in fp16's range whatever the scales are; O
+// is in units of 2^n, the sum l of P in units of 2^m.  They move only when a score
+// exceeds them by more than 8, so that a step without that has no reduction over lanes.
+// q is brought into fp16's range by a power of two per row, which is exact.  With
+// fp32 queries or output, q and w are a sum of two fp16 each (22 bits).
+//
+// The tensor-core instruction of one thread and TMEM is not used: with 4 to 16 rows
+// most of its 128 would be empty, and 8-bit products would need q and w in 8 bits.
+//
+// A warp has every 8th group of 16 keys of its thread block's range and a ring of
+// its own, filled by cp.async a few groups ahead: no barrier until the end of an
+// item's part, where the warps' (O, m, n, l) are joined in shared memory.  The rows
+// lie in the ring so that the 16-byte reads below find all banks.
+//
+// The work is cut into equal ranges as for the tree attention (kda_tree.cuh).
+#include <cuda_fp16.h>
+
+#include "kda_prompt.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kKeys = 16;                          // of a warp's step
+constexpr int KT = kWarps * kKeys;                 // of a tile
+constexpr int kLead = 4;
+constexpr int kRows = 16;
+constexpr float kSlack = 8.f;
+using Piece = TreePieces<KT, kLead>;
+
+template <int D>
+struct Shape {
+    static constexpr int kStageBytes = 2 * kKeys * D + 2 * kKeys * 4 + 16;
+    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kRing = kWarps * kStages * kStageBytes;
+    static constexpr int OP = D + 4;               // row pitch of a warp's O
+    static constexpr int kJoin = kWarps * (kRows * OP + 3 * kRows) * 4;
+    static constexpr size_t kBytes = kRing + kJoin;
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 (the lower or the upper half of a word) as fp16, which holds them exactly.
+__device__ __forceinline__ uint32_t widen_lo(uint32_t w)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t w)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t two_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// What two_f16 leaves of the pair, as fp16.
+__device__ __forceinline__ uint32_t two_f16_rest(float lo, float hi, uint32_t taken)
+{
+    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&taken));
+    return two_f16(lo - t.x, hi - t.y);
+}
+__device__ __forceinline__ float quad_max(float x)
+{
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+template <int BYTES>
+struct Words {
+    uint32_t w[(BYTES + 3) / 4];
+};
+template <int BYTES>
+__device__ __forceinline__ Words<BYTES> read_words(uint32_t at)
+{
+    Words<BYTES> r;
+    if constexpr (BYTES == 16)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "r"(at));
+    else if constexpr (BYTES == 8)
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "r"(at));
+    else if constexpr (BYTES == 4)
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r.w[0]) : "r"(at));
+    else
+        asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tmov.b32 %0, {h, 0};\n\t}" : "=r"(r.w[0]) : "r"(at));
+    return r;
+}
+__device__ __forceinline__ float read_float(uint32_t at)
+{
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at));
+    return x;
+}
+
+// Byte offset of 16-byte piece c of row `key` of a step's 16 rows.
+template <int D>
+__device__ __forceinline__ int row_at(int key, int c)
+{
+    if constexpr (D == 128) return key * 128 + ((c ^ (key & 7)) << 4);
+    else if constexpr (D == 64) return key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
+    else return key * D + (c << 4);
+}
+// The key of a step that is column n of the first product's 8-key half, and the
+// first of the channels that are column n of the second product's D / 8 blocks.
+// Column pairs (2 i, 2 i + 1) are keys i and i + 4.
+__device__ __forceinline__ int key_of(int n) { return ((n & 1) << 2) | (n >> 1); }
+template <int D>
+__device__ __forceinline__ int channel_of(int n) { return key_of(n) * (D / 8); }
+
+// The walk of a warp's copies over its range: a step (16 keys) at a time, this
+// lane's key (lane % 16) in it; the page number is loaded when the step is entered, one
+// before it is used.
+struct Walk {
+    Piece w;
+    bool go;
+    int t, pos, p, slot, page;
+
+    __device__ __forceinline__ void look_up(const E4m3Args& a)
+    {
+        page = -1;
+        if (go && pos < w.ctx) page = __ldg(a.split.page_table + (long long)w.n * a.split.max_pages + p);
+    }
+    __device__ __forceinline__ void enter(const E4m3Args& a, int warp, int lane)
+    {
+        if (go) {
+            t = w.t0;
+            pos = t * KT + warp * kKeys + (lane & 15);
+            p = pos / a.split.page_size;
+            slot = pos - p * a.split.page_size;
+        }
+        look_up(a);
+    }
+    __device__ __forceinline__ void step(const E4m3Args& a, int warp, int lane)
+    {
+        if (!go) return;
+        if (++t == w.t1) {
+            go = w.next(a.split);
+            enter(a, warp, lane);
+            return;
+        }
+        pos += KT;
+        p += a.tile_pages;
+        slot += a.tile_rows;
+        if (slot >= a.split.page_size) {
+            slot -= a.split.page_size;
+            ++p;
+        }
+        look_up(a);
+    }
+};
+
+// Starts the copies of the walk's step into a stage.
+template <int D>
+__device__ __forceinline__ void start_copies(const E4m3Args& a, const Walk& k, uint32_t stage, int lane)
+{
+    constexpr int CPR = D / 16;                    // 16-byte pieces of a row
+    if (k.go) {
+        const bool there = k.page >= 0 && k.page < a.num_pages;
+        const uint32_t mask = __ballot_sync(0xffffffffu, there) & 0xFFFFu;
+        long long row = 0;
+        const float* scale = lane < 16 ? a.k_scales : a.v_scales;
+        if (there) {
+            row = k.page * a.page_stride + (long long)k.slot * (a.split.Hkv * D) + k.w.hk * D;
+            const int b = a.block == 1 ? k.slot : (int)__umulhi((uint32_t)k.slot, a.block_magic);
+            scale += ((long long)k.page * a.blocks + b) * a.split.Hkv + k.w.hk;
+        }
+        copy4(stage + 2 * kKeys * D + lane * 4, scale, there);
+        if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + 2 * kKeys * D + 128), "r"(mask) : "memory");
+        constexpr int N = kKeys * CPR;
+#pragma unroll
+        for (int e0 = 0; e0 < N; e0 += 32) {
+            const int e = e0 + lane, key = e / CPR, c = e % CPR;
+            const long long src = __shfl_sync(0xffffffffu, row, key & 15);
+            const bool ok = (mask >> (key & 15)) & 1;
+            if (N >= 32 || e < N) {
+                copy16(stage + row_at<D>(key, c), a.k_cache + src + c * 16, ok);
+                copy16(stage + kKeys * D + row_at<D>(key, c), a.v_cache + src + c * 16, ok);
+            }
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// The channel of word s (4 channels) that lane i of a row's four holds.
+template <int D>
+__device__ __forceinline__ int q_channel(int s, int i)
+{
+    return D == 128 ? 64 * (s >> 2) + 16 * i + 4 * (s & 3) : D / 4 * i + 4 * s;
+}
+
+template <class T, class O, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+cache_attention_kernel(const __grid_constant__ E4m3Args a)
+{
+    using Sh = Shape<D>;
+    constexpr bool QLO = sizeof(T) == 4, PLO = sizeof(O) == 4;
+    constexpr int KS = D / 16;                     // steps of 16 channels of the first product
+    constexpr int NT = D / 8;                      // blocks of 8 channels of the second
+    extern __shared__ __align__(128) uint8_t dyn[];
+    __shared__ long long sh_loc[kWarps + 2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, i4 = lane & 3;
+    const int group = blockIdx.x / a.split.row_tiles, r0 = (blockIdx.x % a.split.row_tiles) * kRows;
+    const TreeSpot sp = tree_locate<kThreads, KT, kLead>(a.split, group, sh_loc);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Walk ahead;
+    ahead.go = ahead.w.start(a.split, sp, group);
+    Piece w = ahead.w;
+    bool go = ahead.go;
+    ahead.enter(a, warp, lane);
+    const uint32_t ring = smem_at(dyn) + warp * Sh::kStages * Sh::kStageBytes;
+    float* join = reinterpret_cast<float*>(dyn + Sh::kRing);
+    int in = 0, out = 0;                           // stages
+#pragma unroll 1
+    for (int i = 0; i < Sh::kStages - 1; ++i) {
+        start_copies<D>(a, ahead, ring + in * Sh::kStageBytes, lane);
+        ahead.step(a, warp, lane);
+        in = in + 1 == Sh::kStages ? 0 : in + 1;
+    }
+    for (; go; go = w.next(a.split)) {
+        // the rows' queries, in fp16 times a power of two
+        uint32_t qh[KS][4], ql[QLO ? KS : 1][4];
+        float rs[2];
+        int lim[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = r0 + g + 8 * h, t = r / a.G;
+            const bool mine = r < a.R;
+            lim[h] = mine ? w.ctx - a.Ts + t + 1 : 0;
+            const T* qp = static_cast<const T*>(a.q) +
+                          (((long long)w.n * a.Ts + (mine ? t : 0)) * a.Hq + w.hk * a.G + (mine ? r - t * a.G : 0)) * D;
+            float x[KS][4];
+            uint32_t top = 0;
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[s][j] = mine ? to_float(qp[q_channel<D>(s, i4) + j]) : 0.f;
+                    top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
+                }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            int e = 14 + 127 - (int)(top >> 23);   // the largest magnitude becomes 2^14 or a little more
+            e = top == 0 ? 0 : min(max(e, -100), 100);
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            rs[h] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float u = x[s][2 * j] * up, v = x[s][2 * j + 1] * up;
+                    qh[s][2 * j + h] = two_f16(u, v);
+                    if constexpr (QLO) ql[s][2 * j + h] = two_f16_rest(u, v, qh[s][2 * j + h]);
+                }
+        }
+        const int all = w.ctx - a.Ts + r0 / a.G + 1;           // keys that every row sees
+        float o[NT][4], m[2], n[2], l[2], fac[2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            m[h] = n[h] = -INFINITY;
+            l[h] = fac[h] = 0.f;
+        }
+#pragma unroll 1
+        for (int t = w.t0; t < w.t1; ++t) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(Sh::kStages - 2) : "memory");
+            __syncwarp();                          // of all lanes; and the stage before has been read
+            start_copies<D>(a, ahead, ring + in * Sh::kStageBytes, lane);
+            ahead.step(a, warp, lane);
+            in = in + 1 == Sh::kStages ? 0 : in + 1;
+            const uint32_t st = ring + out * Sh::kStageBytes, sc = st + 2 * kKeys * D;
+            out = out + 1 == Sh::kStages ? 0 : out + 1;
+
+            float c[2][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) c[b][j] = 0.f;
+            {
+                constexpr int KB = D / 4 < 16 ? D / 4 : 16;    // bytes per read of a row of K
+                Words<KB> kw[2][D / 4 / KB];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int h = 0; h < D / 4 / KB; ++h) {
+                        const int at = KB * i4 + 64 * h;
+                        kw[b][h] = read_words<KB>(st + row_at<D>(8 * b + key_of(g), at >> 4) + (at & 15));
+                    }
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const uint32_t x = kw[b][s / (KB / 4)].w[s % (KB / 4)];
+                        const uint32_t b0 = widen_lo(x), b1 = widen_hi(x);
+                        mma(c[b], qh[s], b0, b1);
+                        if constexpr (QLO) mma(c[b], ql[s], b0, b1);
+                    }
+            }
+            float ks[2][2], vs[2][2];              // of keys 8 b + i4 + 4 j
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    ks[b][j] = read_float(sc + (8 * b + i4 + 4 * j) * 4);
+                    vs[b][j] = read_float(sc + (16 + 8 * b + i4 + 4 * j) * 4);
+                }
+            uint32_t mask;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(mask) : "r"(sc + 128));
+            const int pos = t * KT + warp * kKeys;
+            const bool masked = mask != 0xFFFFu || pos + kKeys > all;      // (the same for the warp)
+            bool grow = false;
+            float top[2], vtop[2], lv[2][2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) lv[b][j] = lg2(vs[b][j]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                top[h] = vtop[h] = -INFINITY;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float& x = c[b][2 * h + j];
+                        x = x * ks[b][j] * rs[h];
+                        const int key = 8 * b + i4 + 4 * j;
+                        if (masked && (!((mask >> key) & 1) || pos + key >= lim[h])) x = -INFINITY;
+                        top[h] = fmaxf(top[h], x);
+                        vtop[h] = fmaxf(vtop[h], x + lv[b][j]);
+                    }
+                grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + kSlack;
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float m2 = fmaxf(m[h], quad_max(top[h]));
+                    // n is kept near m, so that 2^(m - n) is finite
+                    const float n2 = fmaxf(fmaxf(n[h], quad_max(vtop[h])), m2 - 120.f);
+                    const float fl = m2 == -INFINITY ? 1.f : ex2(m[h] - m2), fo = n2 == -INFINITY ? 1.f : ex2(n[h] - n2);
+                    m[h] = m2;
+                    n[h] = n2;
+                    l[h] *= fl;
+                    fac[h] = m2 == -INFINITY ? 0.f : ex2(m2 - n2);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        o[j][2 * h] *= fo;
+                        o[j][2 * h + 1] *= fo;
+                    }
+                }
+            }
+            uint32_t ph[4], pl[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float ref = m[h] == -INFINITY ? 0.f : m[h];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    float y[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float x = c[b][2 * h + j];
+                        const float p = ex2(x - ref);
+                        l[h] += p;
+                        y[j] = p * (vs[b][j] * fac[h]);
+                        if (masked && x == -INFINITY) y[j] = 0.f;
+                    }
+                    ph[2 * b + h] = two_f16(y[0], y[1]);
+                    if constexpr (PLO) pl[2 * b + h] = two_f16_rest(y[0], y[1], ph[2 * b + h]);
+                }
+            }
+            {
+                // this lane's D / 8 channels of keys i4, i4 + 4, 8 + i4, 12 + i4
+                Words<NT> vw[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int at = channel_of<D>(g);
+                    vw[j] = read_words<NT>(st + kKeys * D + row_at<D>(i4 + 4 * j, at >> 4) + (at & 15));
+                }
+#pragma unroll
+                for (int x = 0; x < (NT + 3) / 4; ++x) {
+                    const uint32_t lo0 = __byte_perm(vw[0].w[x], vw[1].w[x], 0x5140), hi0 = __byte_perm(vw[0].w[x], vw[1].w[x], 0x7362);
+                    const uint32_t lo1 = __byte_perm(vw[2].w[x], vw[3].w[x], 0x5140), hi1 = __byte_perm(vw[2].w[x], vw[3].w[x], 0x7362);
+                    const uint32_t b0[4] = {widen_lo(lo0), widen_hi(lo0), widen_lo(hi0), widen_hi(hi0)};
+                    const uint32_t b1[4] = {widen_lo(lo1), widen_hi(lo1), widen_lo(hi1), widen_hi(hi1)};
+#pragma unroll
+                    for (int j = 0; j < (NT < 4 ? NT : 4); ++j) {
+                        mma(o[4 * x + j], ph, b0[j], b1[j]);
+                        if constexpr (PLO) mma(o[4 * x + j], pl, b0[j], b1[j]);
+                    }
+                }
+            }
+        }
+        // the warps' results of the piece
+        __syncthreads();                           // those of the piece before have been read
+        float* wj = join + warp * (kRows * Sh::OP + 3 * kRows);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+            const int r = g + 8 * h;
+            if (i4 == 0) {
+                wj[kRows * Sh::OP + r] = m[h];
+                wj[kRows * Sh::OP + kRows + r] = n[h];
+                wj[kRows * Sh::OP + 2 * kRows + r] = l[h];
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) wj[r * Sh::OP + channel_of<D>(2 * i4 + e) + j] = o[j][2 * h + e];
+        }
+        __syncthreads();
+        const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+        {
+            constexpr int E = D / 16;              // channels per thread
+            const int r = tid >> 4, c0 = (tid & 15) * E;
+            float mm = -INFINITY, nn = -INFINITY, ll = 0.f, oo[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) oo[e] = 0.f;
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) {
+                const float* y = join + x * (kRows * Sh::OP + 3 * kRows) + kRows * Sh::OP;
+                mm = fmaxf(mm, y[r]);
+                nn = fmaxf(nn, y[kRows + r]);
+            }
+            const float mr = mm == -INFINITY ? 0.f : mm, nr = nn == -INFINITY ? 0.f : nn;
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) {
+                const float* y = join + x * (kRows * Sh::OP + 3 * kRows);
+                ll += y[kRows * Sh::OP + 2 * kRows + r] * ex2(y[kRows * Sh::OP + r] - mr);
+                const float f = ex2(y[kRows * Sh::OP + kRows + r] - nr);
+#pragma unroll
+                for (int e = 0; e < E; ++e) oo[e] += y[r * Sh::OP + c0 + e] * f;
+            }
+            const int row = r0 + r;
+            if (row < a.R) {
+                if (whole) {
+                    const int t = row / a.G;
+                    const float f = ll == 0.f ? 0.f : ex2(nr - mr) / ll;
+                    O* op = static_cast<O*>(a.o) + (((long long)w.n * a.Ts + t) * a.Hq + w.hk * a.G + row - t * a.G) * D + c0;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) op[e] = O(oo[e] * f);
+                } else {
+                    float* part = a.part + ((size_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * kRows * (D + 3);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) part[r * D + c0 + e] = oo[e];
+                    if ((tid & 15) == 0) {
+                        part[kRows * D + r] = mm;
+                        part[kRows * D + kRows + r] = nn;
+                        part[kRows * D + 2 * kRows + r] = ll;
+                    }
+                }
+            }
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Joins the pieces of the items that were cut between groups.  Block (c, y, z): the
+// item that the boundary before group c + 1 falls into, if that is the item's first
+// boundary; rows y 8 .. y 8 + 7 of row tile z, a warp each.  The pieces are read
+// in the order of the groups, so the result does not depend on timing.
+constexpr int kJoinThreads = 256;
+
+template <class O, int D>
+__global__ void __launch_bounds__(kJoinThreads)
+cache_join_kernel(const __grid_constant__ E4m3Args a)
+{
+    __shared__ long long sh_loc[kJoinThreads / 32 + 2];
+    const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const TreeArgs& s = a.split;
+    const TreeSpot sp = tree_locate<kJoinThreads, KT, kLead>(s, c, sh_loc);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long at = tree_begin(sp, c);
+    if (at >= sp.total) return;                     // an empty range at the end
+    const int tiles = tree_tiles<KT>(s, sp.n);
+    const int hk = (int)((at - sp.start) / (tiles + kLead));
+    // where the item's tiles begin; a boundary up to there cuts nothing
+    const long long first = sp.start + (long long)hk * (tiles + kLead) + kLead;
+    if (at <= first || tree_begin(sp, c - 1) > first) return;
+    int last = c;                                   // the last group with tiles of this item
+    while (last + 1 < s.groups && tree_begin(sp, last + 1) < first + tiles) ++last;
+    const int r = blockIdx.y * (kJoinThreads / 32) + warp, row = blockIdx.z * kRows + r;
+    if (r >= kRows || row >= a.R) return;
+    // piece p of the item: group p's first slot, but the second of group c - 1
+    auto piece = [&](int p) {
+        return a.part + (((size_t)p * s.row_tiles + blockIdx.z) * 2 + (p == c - 1 ? 1 : 0)) * kRows * (D + 3);
+    };
+    constexpr int E = D / 32 > 0 ? D / 32 : 1;
+    float m = -INFINITY, n = -INFINITY;
+    for (int p = c - 1 + lane; p <= last; p += 32) {
+        m = fmaxf(m, piece(p)[kRows * D + r]);
+        n = fmaxf(n, piece(p)[kRows * D + kRows + r]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, off));
+    }
+    const float mr = m == -INFINITY ? 0.f : m, nr = n == -INFINITY ? 0.f : n;
+    float l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int p = c - 1; p <= last; ++p) {
+        const float* x = piece(p);
+        l += x[kRows * D + 2 * kRows + r] * ex2(x[kRows * D + r] - mr);
+        const float f = ex2(x[kRows * D + kRows + r] - nr);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (D >= 32 || lane < D) o[e] += x[r * D + lane + 32 * e] * f;
+    }
+    const float f = l == 0.f ? 0.f : ex2(nr - mr) / l;
+    const int t = row / a.G;
+    O* op = static_cast<O*>(a.o) + (((long long)sp.n * a.Ts + t) * a.Hq + hk * a.G + row - t * a.G) * D;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (D >= 32 || lane < D) op[lane + 32 * e] = O(o[e] * f);
+}
+
+template <class T, class O, int D>
+cudaError_t launch(const E4m3Args& a, cudaStream_t stream)
+{
+    auto kern = cache_attention_kernel<T, O, D>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    kern<<<a.split.groups * a.split.row_tiles, kThreads, Shape<D>::kBytes, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.split.groups < 2) return e;
+    cudaLaunchConfig_t cfg = {};
+    const int rows = a.R < kRows ? a.R : kRows;
+    cfg.gridDim = dim3(a.split.groups - 1, (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), a.split.row_tiles);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache_join_kernel<O, D>, a);
+}
+
+template <class T, class O>
+cudaError_t launch_d(const E4m3Args& a, int32_t d, cudaStream_t stream)
+{
+    switch (d) {
+    case 16: return launch<T, O, 16>(a, stream);
+    case 32: return launch<T, O, 32>(a, stream);
+    case 64: return launch<T, O, 64>(a, stream);
+    default: return launch<T, O, 128>(a, stream);
+    }
+}
+
+void plan(int32_t R, int sms, int32_t& groups, int32_t& row_tiles)
+{
+    row_tiles = (R + kRows - 1) / kRows;
+    groups = sms / row_tiles > 1 ? sms / row_tiles : 1;
+}
+
+}  // namespace
+
+size_t e4m3_workspace_bytes(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, int sms)
+{
+    int32_t groups, row_tiles;
+    plan(Ts * (Hq / Hkv), sms > 0 ? sms : 1, groups, row_tiles);
+    return (size_t)groups * row_tiles * 2 * kRows * (d + 3) * sizeof(float);
+}
+
+cudaError_t launch_cache_attention_e4m3(E4m3Args a, int32_t d, kda_dtype_t dtype, int sms, cudaStream_t stream)
+{
+    plan(a.R, sms > 0 ? sms : 1, a.split.groups, a.split.row_tiles);
+    a.tile_pages = KT / a.split.page_size;
+    a.tile_rows = KT % a.split.page_size;
+    if (dtype == KDA_BF16) return launch_d<__nv_bfloat16, __nv_bfloat16>(a, d, stream);
+    if (dtype == KDA_BF16_F32OUT) return launch_d<__nv_bfloat16, float>(a, d, stream);
+    return launch_d<float, float>(a, d, stream);
+}
+
+}  // namespace kda

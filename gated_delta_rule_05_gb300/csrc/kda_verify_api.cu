@@ -3,42 +3,19 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include "kda_args.cuh"
 #include "kda_tree.cuh"
 #include "kda_verify.cuh"
 
+using namespace kda::args;
+
 namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool supported_d(int32_t d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb)
-{
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
-bool valid_dtype(kda_dtype_t t) { return t == KDA_BF16 || t == KDA_FP32 || t == KDA_BF16_F32OUT; }
-
-size_t in_bytes(kda_dtype_t t) { return t == KDA_FP32 ? 4 : 2; }
-size_t out_bytes(kda_dtype_t t) { return t == KDA_BF16 ? 2 : 4; }
 
 // The sizes that the attention and its workspace take: a row tile is a block index.
 bool attention_sizes(int32_t N, int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d)
 {
     return N >= 1 && Ts >= 1 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && (int64_t)Ts * Hq <= (1 << 20) &&
            (int64_t)Hkv * d <= INT32_MAX;
-}
-
-// Bytes from the first to the last element of a layer's pages, and whether the
-// strides are ones that the kernels take.
-bool cache_shape(int32_t num_pages, int32_t page_size, int32_t Hkv, int32_t d, int64_t page_stride,
-                 size_t elem, size_t* bytes)
-{
-    const int64_t page_elems = (int64_t)page_size * Hkv * d;
-    if (num_pages > 1 && (page_stride < page_elems || (page_stride * (int64_t)elem) % 16 != 0)) return false;
-    *bytes = ((size_t)(num_pages - 1) * (size_t)(num_pages > 1 ? page_stride : 0) + (size_t)page_elems) * elem;
-    return true;
 }
 
 }  // namespace

@@ -547,6 +547,133 @@ kda_status_t kda_cache_append(const void *k, const void *v,
                               void *k_cache, void *v_cache, int32_t *new_lengths,
                               cudaStream_t stream);
 
+/* ---- A prompt and its answer in the softmax layers ------------------------
+ *
+ * What the softmax layers of such a hybrid do beside kda_prefill and
+ * kda_decode_step: kda_cache_append_rotary turns a batch's queries and keys to
+ * their positions and puts keys and values into the cache's pages, in the model's
+ * type or in 8 bits; kda_prompt_attention is the attention of the prompt itself;
+ * kda_cache_attention_e4m3 that of later tokens to a cache of 8 bits
+ * (kda_tree_attention reads one in the model's type).
+ *
+ * A token of q has Hq heads of d channels, dense, one of k and v Hkv; from token to
+ * token they lie q_stride, k_stride, v_stride elements apart (at least a token's
+ * own, a multiple of 16 bytes; ignored for one token), so that they may be views of
+ * one projection's output.  d is 16, 32, 64 or 128 and Hkv divides Hq: query head h
+ * goes with key head h / (Hq / Hkv).
+ *
+ * A cache of 8 bits is a pool as above of e4m3 values, with fp32 scales
+ * [num_pages, page_size / block, Hkv] for keys and for values: the value is scale *
+ * e4m3.  A block of `block` rows (of one page, position i of a sequence being row i
+ * % page_size) and head has the scale 2^e with the smallest e >= -126 for which 448
+ * * 2^e reaches its largest magnitude, 0 when it has only zeros, NaN (and bytes 0)
+ * when it has an infinity or NaN.  page_stride counts bytes here. */
+
+/* Causal softmax attention over packed sequences: with Lq and Lk rows of queries
+ * and keys in a sequence, query i sees its keys 0 .. i + Lk - Lq, so that the
+ * queries are the sequence's last (Lk = Lq: a whole prompt; Lk > Lq: its rest
+ * behind a prefix).  One that sees no key (Lk < Lq) gives 0.
+ *
+ *   q, o          [total_tokens, Hq, d] (o dense);  k, v [total_keys, Hkv, d]
+ *   cu_seqlens    device int32 [num_seqs + 1], as in kda_prefill, or NULL for one
+ *                 sequence of all rows
+ *   cu_seqlens_k  the same for k and v; NULL: cu_seqlens is used for them too, and
+ *                 total_keys is total_tokens
+ *   o             (written) rows that cu_seqlens gives to no sequence keep what they
+ *                 hold; must not overlap the inputs.  Rows before 0 or past the last
+ *                 do not exist; of sequences that claim the same row one gets it.
+ *   status        device int32 or NULL: bit 1 is set when a wait of the tensor-core
+ *                 kernel has given up (after some two seconds; never cleared).  The
+ *                 rows of o that depended on it are NaN.
+ * dtype is that of q, k, v, and of o.  KDA_BF16 with d = 64 or 128, scale > 0 and
+ * Hq / Hkv <= 128 runs on the tensor cores, with probabilities rounded to bf16 for
+ * the second product; everything else, and everything when the environment variable
+ * KDA_FORCE_SIMT is set, on the CUDA cores in fp32.  An infinity or NaN in a
+ * row of k or v reaches the queries that see it and no others.  No atomics: the
+ * result does not depend on timing. */
+kda_status_t kda_prompt_attention(const void *q, const void *k, const void *v,
+                                  int64_t q_stride, int64_t k_stride,
+                                  int64_t v_stride, const int32_t *cu_seqlens,
+                                  const int32_t *cu_seqlens_k, int32_t num_seqs,
+                                  int64_t total_tokens, int64_t total_keys,
+                                  int32_t Hq, int32_t Hkv, int32_t d,
+                                  kda_dtype_t dtype, float scale, void *o,
+                                  int32_t *status, cudaStream_t stream);
+
+/* Rows of a packed batch (a prefill, or one token per sequence) turned to their
+ * positions and into a cache: row i of sequence n has position p = lengths[n] + i.
+ * Each pair (x, y) of the first rot_dim channels of q and k becomes
+ *     (x cos a - y sin a, x sin a + y cos a),  a = p * inv_freq[j],
+ * the j-th pair being channels j and j + rot_dim / 2, or 2 j and 2 j + 1
+ * (interleaved != 0); the other channels, and v, stay.  The angle is exact to 2^-32
+ * of a turn at every position.
+ *
+ *   q, q_out      [total_tokens, Hq, d]; Hq = 0 and NULL: k and v only
+ *   k, v          [total_tokens, Hkv, d]
+ *   k_out         [total_tokens, Hkv, d] (the turned keys) or NULL
+ *   q_out, k_out  in dtype, q_out_stride, k_out_stride elements from token to token;
+ *                 may be q and k themselves (same stride), must overlap nothing else
+ *   cu_seqlens, lengths, page_table, k_cache, v_cache, new_lengths   as in
+ *                 kda_cache_append, for one layer (k_cache [num_pages, page_size,
+ *                 Hkv, d]).  Rows without a place in the cache are dropped there,
+ *                 but turned; those of no sequence, or of one with a negative
+ *                 length, are left as they were.
+ *   inv_freq      device fp32 [rot_dim / 2]; rot_dim is a multiple of 16, 16 .. d
+ *   block         0: the cache is in k's dtype, page_stride in elements, and
+ *                 the scales are not used.  Else the cache has 8 bits, a scale for
+ *                 each `block` rows (1 .. 128, more is KDA_ERR_UNSUPPORTED; it divides page_size): see above.
+ *                 A block that the sequence has already begun keeps its rows: when
+ *                 the new ones need a larger scale they are rounded to it.  Scales of
+ *                 such blocks must be those that this call wrote (or other powers
+ *                 of two).  Two sequences must not write one block.
+ *   new_lengths   [N] (written) or NULL; must overlap no input
+ * dtype is that of q, k, v, q_out and k_out (KDA_BF16_F32OUT is KDA_BF16 here); all arithmetic is fp32. */
+kda_status_t kda_cache_append_rotary(
+    const void *q, const void *k, const void *v, int64_t q_stride,
+    int64_t k_stride, int64_t v_stride, const int32_t *cu_seqlens,
+    int64_t total_tokens, const float *inv_freq, int32_t rot_dim,
+    int32_t interleaved, const int32_t *page_table, const int32_t *lengths,
+    int32_t N, int32_t Hq, int32_t Hkv, int32_t d, int32_t num_pages,
+    int32_t page_size, int32_t max_pages, int64_t page_stride, int32_t block,
+    kda_dtype_t dtype, void *q_out, int64_t q_out_stride, void *k_out,
+    int64_t k_out_stride, void *k_cache, void *v_cache, float *k_scales,
+    float *v_scales, int32_t *new_lengths, cudaStream_t stream);
+
+/* Bytes of device workspace kda_cache_attention_e4m3 needs; 0 for arguments that
+ * it refuses.  It depends on the SM count, not on N or the lengths. */
+size_t kda_cache_attention_e4m3_workspace_bytes(int32_t N, int32_t Ts,
+                                                int32_t Hq, int32_t Hkv,
+                                                int32_t d, kda_dtype_t dtype);
+
+/* Softmax attention of the Ts newest tokens of each sequence (one, or a chain of
+ * drafted ones) to a cache of 8 bits that holds them already: token t of sequence
+ * n sees rows 0 .. lengths[n] - Ts + t.  One before the first row gives 0, so that
+ * a sequence with fewer tokens has them in its last rows.
+ *
+ *   q, o          [N, Ts, Hq, d], dense; o must not overlap the inputs
+ *   k_cache, v_cache, k_scales, v_scales, page_table, num_pages, page_size,
+ *   max_pages, page_stride, block   see above; page_size at most 65536 (more is
+ *                 KDA_ERR_UNSUPPORTED).  Positions whose table entry names no page are
+ *                 hidden.  Rows past lengths[n] are never read.
+ *   lengths       device int32 [N], rows with those of the Ts tokens (values outside
+ *                 [0, max_pages * page_size] are clamped)
+ *   workspace     kda_cache_attention_e4m3_workspace_bytes(...) bytes, 256-byte
+ *                 aligned, not shared with concurrent calls; contents on entry do
+ *                 not matter
+ * dtype is that of q and of o.  Products are of fp16 pairs (q exactly, probabilities
+ * to 11 bits), with fp32 queries or output of sums of two (22 bits); sums are fp32.
+ * A scale of NaN makes the tokens that see a row of its block NaN and no others;
+ * an e4m3 code of NaN, which kda_cache_append_rotary never writes, may reach all
+ * tokens of its sequence; an infinity or NaN in q makes that head's output NaN.  No atomics: the result does not depend on
+ * timing; it may differ in rounding between GPUs with different SM counts. */
+kda_status_t kda_cache_attention_e4m3(
+    const void *q, const void *k_cache, const void *v_cache,
+    const float *k_scales, const float *v_scales, const int32_t *page_table,
+    const int32_t *lengths, int32_t N, int32_t Ts, int32_t Hq, int32_t Hkv,
+    int32_t d, int32_t num_pages, int32_t page_size, int32_t max_pages,
+    int64_t page_stride, int32_t block, kda_dtype_t dtype, float scale, void *o,
+    void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char *kda_status_string(kda_status_t status);
 

@@ -1,0 +1,229 @@
+"""kda_prompt_attention against a float64 reference.
+
+Bounds, per element, with A = sum_j p_j |v_j|:
+  fp32   |err| <= 1e-4 A: a score is a sum of d <= 128 products, off by at most
+         d 2^-24 sum |q k| scale (about 128 * 6e-8 * 12 = 9e-5 at these inputs'
+         scores), which is p's relative error; the rest is far below.
+  bf16   |err| <= 2^-8 |o| + 2^-8 A + 1e-4 A: the rounding of o, and p rounded to
+         bf16 for the second product (half a step, 2^-8, in the sum; the normaliser
+         sums the unrounded).  fp32 output from bf16 inputs is held to the fp32
+         bound (its probabilities are not rounded).
+"""
+import numpy as np
+import pytest
+import torch
+
+from tests._prompt import prompt_reference
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def kda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import gated_delta_rule_05_gb300 as m
+    m.build()
+    m.lib()
+    return m
+
+
+def inputs(T, Tk, Hq, Hkv, d, dtype, seed=0, fused=False):
+    g = torch.Generator().manual_seed(seed)
+    if fused:
+        x = torch.randn((T, Hq + 2 * Hkv, d), generator=g).to(dtype)
+        return [x[:, a:b] for a, b in ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, Hq + 2 * Hkv))], x
+    f = lambda t, h: torch.randn((t, h, d), generator=g).to(dtype)
+    return [1.5 * f(T, Hq), f(Tk, Hkv), f(Tk, Hkv)], None
+
+
+def on_gpu(parts, whole):
+    if whole is None:
+        return [x.cuda() for x in parts]
+    y, out, at = whole.cuda(), [], 0
+    for x in parts:
+        out.append(y[:, at:at + x.shape[1]])
+        at += x.shape[1]
+    return out
+
+
+def i32(x):
+    return None if x is None else torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def check(o, ref, mag, exact_p):
+    o64 = o.double().cpu().numpy()
+    bound = 1e-4 * mag + (0 if exact_p else 2.0 ** -8 * mag)
+    if o.dtype == BF16:
+        bound = bound + 2.0 ** -8 * np.abs(ref)
+    bad = ~(np.abs(o64 - ref) <= bound)
+    assert not bad.any(), "%d of %d elements off, worst %.3g of the bound, first at %s" % (
+        bad.sum(), bad.size, np.nanmax(np.abs(o64 - ref) / np.maximum(bound, 1e-30)), np.argwhere(bad)[0])
+
+
+def run(kda, parts, whole, cu, cu_k, **kw):
+    o = kda.kda_prompt_attention(*on_gpu(parts, whole), i32(cu), i32(cu_k), **kw)
+    torch.cuda.synchronize()
+    return o
+
+
+def starts(lens):
+    return [0] + np.cumsum(lens).tolist()
+
+
+CASES = [
+    # lengths, key lengths (None: the same), Hq, Hkv, d
+    ([1], None, 1, 1, 16),
+    ([1], None, 8, 2, 128),
+    ([127], None, 4, 4, 128),
+    ([128], None, 4, 1, 64),
+    ([129, 1, 0, 64], None, 6, 2, 128),
+    ([300, 5, 257], None, 8, 8, 64),
+    ([511], None, 16, 2, 128),
+    ([640, 130], None, 5, 1, 128),
+    ([70, 33], None, 14, 2, 32),
+    ([1000], None, 7, 7, 64),
+    ([33, 0, 200], [200, 17, 200], 4, 2, 128),
+    ([1, 1, 1], [1, 300, 128], 8, 1, 128),
+    ([65, 140], [400, 139], 3, 1, 64),
+    ([50, 20, 9], [3, 0, 9], 4, 2, 128),        # queries before the first key
+    ([200], None, 48, 2, 64),
+    ([400], None, 12, 3, 16),
+    ([2100], None, 2, 1, 128),
+    ([40], None, 130, 1, 128),                  # more heads than rows of a tile
+]
+
+
+@pytest.mark.parametrize("lens,keys,Hq,Hkv,d", CASES, ids=lambda c: str(c).replace(" ", ""))
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (BF16, F32), (F32, F32)])
+def test_matches_reference(kda, lens, keys, Hq, Hkv, d, dtype, out):
+    cu, cu_k = starts(lens), None if keys is None else starts(keys)
+    parts, whole = inputs(cu[-1], (cu_k or cu)[-1], Hq, Hkv, d, dtype, seed=sum(lens) + d)
+    o = run(kda, parts, whole, cu, cu_k, o_dtype=out)
+    assert o.dtype == out
+    check(o, *prompt_reference(*parts, cu, cu_k), exact_p=out == F32)
+
+
+@pytest.mark.parametrize("dtype,d,Hq,Hkv", [(BF16, 128, 4, 2), (BF16, 64, 3, 1), (F32, 64, 4, 4), (BF16, 32, 2, 1)])
+def test_views_of_one_projection(kda, dtype, d, Hq, Hkv):
+    cu = starts([100, 190])
+    parts, whole = inputs(290, 290, Hq, Hkv, d, dtype, seed=3, fused=True)
+    check(run(kda, parts, whole, cu, None), *prompt_reference(*parts, cu), exact_p=dtype == F32)
+    # one sequence without offsets is the same as with them
+    a, b = run(kda, parts, whole, None, None), run(kda, parts, whole, [0, 290], None)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,d,G", [(BF16, 128, 2), (BF16, 64, 5), (F32, 32, 1)])
+def test_inf_and_nan_reach_only_the_queries_that_see_them(kda, dtype, d, G):
+    # in the same tile, in the next sequence, in the rows behind the last one
+    lens = [150, 60, 40]
+    cu = starts(lens)
+    parts, _ = inputs(260, 260, 2 * G, 2, d, dtype, seed=7)
+    q, k, v = parts
+    v[100, 0, 1], v[101, 1, 0], k[120, 0] = float("inf"), float("nan"), float("nan")
+    v[150, 1, 2] = float("-inf")
+    v[209, 0, 3], v[250:], k[250:] = float("nan"), float("nan"), float("inf")
+    q[20, 0] = float("nan")
+    keep = torch.full(q.shape, 7.0, dtype=dtype, device="cuda")
+    o = run(kda, parts, None, cu, None, o=keep)
+    ref, mag = prompt_reference(*parts, cu, o=torch.full(q.shape, 7.0))
+    assert torch.all(o[250:] == 7)
+    o64 = o.double().cpu().numpy()
+    fine = np.isfinite(ref)
+    assert np.array_equal(fine, np.isfinite(o64)), np.argwhere(fine != np.isfinite(o64))[:4]
+    # (NaN where p underflows beside an infinity is the reference's 0 * inf)
+    assert np.isposinf(o64[100, :G, 1]).all() and np.isnan(o64[120, :G]).all() and np.isneginf(o64[150, G:, 2]).all()
+    bound = (2.0 ** -7 + 1e-4) * mag
+    assert (np.abs(o64 - ref)[fine] <= bound[fine]).all()
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
+def test_rising_scores(kda, dtype, d):
+    # maxima that grow along the keys by more than any slack, over many tiles
+    T = 700
+    q, k, v = inputs(T, T, 2, 1, d, dtype, seed=9)[0]
+    k = (torch.linspace(-1, 1, T)[:, None, None] * torch.ones_like(k) * 4).to(dtype)
+    q = torch.ones_like(q) * 4
+    # scores of 16 d^0.5 * (-1 .. 1): 181 and 128 in the exponent, fp32's rounding of them
+    # 2^-24 * 181 * d^0.5 is below the bound of 1e-4
+    o = run(kda, [q, k, v], None, None, None)
+    ref, mag = prompt_reference(q, k, v)
+    check(o, ref, mag * 2, exact_p=dtype == F32)
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-3, 2.0])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scales(kda, scale, dtype):
+    parts, _ = inputs(200, 200, 4, 2, 64, dtype, seed=11)
+    o = run(kda, parts, None, None, None, scale=scale)
+    ref, mag = prompt_reference(*parts, scale=scale)
+    # the bound's score error grows with the scale: at 2.0 16 times the default's
+    check(o, ref, mag * max(1.0, 8 * abs(scale)), exact_p=dtype == F32)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_of_no_sequence_keep_what_they_hold(kda, dtype):
+    for cu, cu_k in (([0, 30, 50], None), ([10, 30, 64], None), ([-5, 20, 90], None), ([0, 40, 20], None),
+                     ([64, 64, 70], None), ([0, 30, 50], [-3, 40, 200])):
+        parts, _ = inputs(64, 64, 4, 2, 64, dtype, seed=12)
+        keep = torch.full((64, 4, 64), 3.0, dtype=dtype, device="cuda")
+        o = run(kda, parts, None, cu, cu_k, o=keep)
+        ref, mag = prompt_reference(*parts, cu, cu_k, o=torch.full((64, 4, 64), 3.0))
+        check(o, ref, mag, exact_p=dtype == F32)
+
+
+def test_many_short_sequences(kda):
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 9, 1500).tolist()
+    cu = starts(lens)
+    parts, _ = inputs(cu[-1], cu[-1], 4, 2, 64, BF16, seed=13)
+    check(run(kda, parts, None, cu, None), *prompt_reference(*parts, cu), exact_p=False)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_other_streams_and_graphs(kda, dtype):
+    cu = starts([300, 77])
+    (q, k, v), _ = inputs(377, 377, 8, 2, 128, dtype, seed=14)
+    a = [x.cuda() for x in (q, k, v)]
+    b = [x.flip(0).contiguous() for x in a]
+    c = i32(cu)
+    want = [kda.kda_prompt_attention(*x, c) for x in (a, b)]
+    torch.cuda.synchronize()
+    # two at once, each on a stream of its own
+    s = [torch.cuda.Stream() for _ in range(2)]
+    got = [kda.kda_prompt_attention(*x, c, stream=t) for x, t in zip((a, b), s)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    # captured, replayed on other inputs
+    hold = [x.clone() for x in a]
+    o = torch.empty_like(hold[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kda.kda_prompt_attention(*hold, c, o=o)
+    for x, w in zip((a, b, a), want + want[:1]):
+        for y, z in zip(hold, x):
+            y.copy_(z)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, w)
+
+
+def test_no_rows(kda):
+    q, kv = torch.empty((0, 4, 64), dtype=BF16, device="cuda"), torch.empty((0, 2, 64), dtype=BF16, device="cuda")
+    assert kda.kda_prompt_attention(q, kv, kv, i32([0, 0])).shape == (0, 4, 64)
+    (q, _, _), _ = inputs(5, 5, 4, 2, 64, BF16)
+    o = kda.kda_prompt_attention(q.cuda(), kv, kv, i32([0, 5]), i32([0, 0]))
+    assert torch.all(o == 0)
+
+
+def test_kernels_agree(kda, monkeypatch):
+    cu = starts([900, 333])
+    parts, _ = inputs(1233, 1233, 8, 2, 128, BF16, seed=15)
+    tc = run(kda, parts, None, cu, None)
+    monkeypatch.setenv("KDA_FORCE_SIMT", "1")
+    simt = run(kda, parts, None, cu, None)
+    ref, mag = prompt_reference(*parts, cu)
+    check(tc, ref, mag, exact_p=False)
+    check(simt, ref, mag, exact_p=False)
