@@ -45,6 +45,11 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs& a, int n)
 // The CUDA-core kernel: every type, head size and scale.
 cudaError_t launch_prompt_attention(const PromptArgs& args, int32_t d, kda_dtype_t dtype, cudaStream_t stream);
 
+// The tensor-core kernel: bf16 in and out, d = 64 or 128, a positive scale (it finds a
+// row's maximum before it applies the scale), at most 128 heads to a key head.
+bool prompt_tc_supported(const PromptArgs& args, int32_t d, kda_dtype_t dtype);
+cudaError_t launch_prompt_attention_tc(PromptArgs args, int32_t d, int sms, cudaStream_t stream);
+
 // --------------------------------------------------- rotated rows into a cache
 struct RotaryArgs {
     const uint8_t *q, *k, *v;         // q may be null

@@ -114,7 +114,10 @@ kda_status_t kda_prompt_attention(const void* q, const void* k, const void* v, i
     a.scale_log2 = scale * 1.4426950408889634f;
     a.o = o;
     a.status = status;
-    const cudaError_t err = kda::launch_prompt_attention(a, d, dtype, stream);
+    const int sms = kda::device_sm_count();
+    const cudaError_t err = kda::prompt_tc_supported(a, d, dtype)
+                                ? kda::launch_prompt_attention_tc(a, d, sms > 0 ? sms : 1, stream)
+                                : kda::launch_prompt_attention(a, d, dtype, stream);
     return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

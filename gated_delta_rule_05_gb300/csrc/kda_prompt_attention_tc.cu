@@ -1,0 +1,883 @@
+// kda_prompt_attention_tc.cu -- causal attention over packed prompts on the tensor
+// cores (bf16, d = 64 or 128): a persistent CTA per SM, tcgen05 products with TMEM
+// accumulators.
+//
+// An item is two row tiles of 128 query rows of a (sequence, cache head); the rows
+// of the G heads that share it lie token by token, row r of a tile being head r % G
+// of its token r / G (128 / G tokens to a tile), so that a tile spans few positions.
+// Per tile of 128 keys and row tile
+//     S = Q K^T             (M = 128, N = 128, K = d; Q, K in shared memory)
+//     P = 2^(c S - m)       (registers; c = scale log2 e; bf16 back over S)
+//     O += P V              (M = 128, N = d, K = 128; P in TMEM, V MN-major)
+// with a reference m near the running maximum of each row that moves only when a tile
+// exceeds it by more than 8: P may reach 2^8, O and l are scaled by 2^(m - m') when m
+// moves, and after the first tiles of a row O is left alone.  P is rounded to
+// bf16, the type of V, as one product takes one type; l sums the values before
+// the rounding.
+//
+// Roles: four warpgroups of softmax and output, two per row tile with 64 of a
+// tile's 128 keys each (their threads of one row exchange its maximum and, at the end, its sum
+// through shared memory); a warp that issues products, one that copies keys and
+// values, one that copies queries, one that looks through values (below).  The row
+// tiles share K and V and alternate on the tensor core: one's softmax runs under the
+// other's products.
+//
+// Values that a row of the item does not see must not reach it through 0 * inf: in the
+// tiles on the diagonal and at the end of a sequence the fourth warp replaces
+// infinities and NaN by 0 before the product and notes their keys; the rows that do
+// see such a key add its value to their output at the end.
+//
+// Items are dealt to the CTAs in a fixed order, long ones first, to and fro, so that no
+// counter is shared between CTAs or calls.
+//
+// Every wait has a limit; one that gives up sets the caller's status word and stops
+// its CTA: the warps that start copies and products end at their next wait and wait for
+// what they have started (again with a limit), and the softmax runs on without
+// waiting, over whatever is there, and gives its rows a sum of NaN.  The environment
+// variable KDA_TEST_STARVE_CONSUMERS, for the test of that path only, has the copying
+// warps exit at once.
+#include <cudaTypedefs.h>
+#include <stdio.h>
+
+#include "kda_prompt.cuh"
+#include "kda_sm100.cuh"
+
+namespace kda {
+
+// The driver's tensor-map encoder (kda_prefill_tc.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn();
+
+namespace {
+
+using namespace sm100;
+
+constexpr int KT = 128;                    // keys per tile
+constexpr int kThreads = 640;              // 16 softmax warps, 4 others
+constexpr int kMmaWarp = 16, kKvWarp = 17, kQWarp = 18, kScanWarp = 19;
+// 640 threads are launched with 96 registers: 512 x 104 + 128 x 64 = 640 x 96
+constexpr int kMore = 104, kFewer = 64;
+constexpr int kMaxTable = 1024;            // sequences whose sizes are held in shared memory
+constexpr int kMaxSorted = 256;
+constexpr int kRingMeta = 16;              // tiles whose notes of infinities and NaN are kept
+
+template <int D>
+struct Shape {
+    static constexpr int kQBytes = 2 * 128 * D * 2;
+    static constexpr int kSlotBytes = KT * D * 2;
+    static constexpr int kSlots = D == 128 ? 4 : 8;
+    static constexpr size_t kBytes = 1024 + kQBytes + (size_t)kSlots * kSlotBytes;
+    static constexpr int kO = 256;         // TMEM column of the outputs; the scores are at 0 and 128
+};
+
+struct Seq {
+    int q0, lq, k0, lk;
+};
+
+struct Shared {
+    uint64_t kv_full[8], kv_land[8], kv_empty[8], q_full, q_empty, done;
+    uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2];
+    uint32_t tmem;
+    int dead;
+    int total;                             // row tile pairs of all sequences, for one cache head
+    int per;                               // sequences of a table entry
+    float top[2][2][128], sum[2][2][128];
+    alignas(16) uint32_t bad[kRingMeta][4];    // a tile's keys with inf or NaN in v
+    int sums[kThreads / 32];
+    int before[kMaxTable + 1];             // row tile pairs before a table entry
+    alignas(16) Seq seq[kMaxTable];        // (only where an entry is one sequence)
+};
+
+// Waits for a phase of a barrier, for about two seconds at most and no longer than
+// until some wait of this CTA has given up; false then.
+__device__ __forceinline__ bool wait_lane(Shared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (*reinterpret_cast<volatile int*>(&sh.dead)) return false;
+        if (clock64() - t0 > (1ll << 32)) {
+            *reinterpret_cast<volatile int*>(&sh.dead) = 1;
+            if (status) atomicOr(status, 2);
+            return false;
+        }
+    }
+    return true;
+}
+// The same for a warp, which goes on as one or stops as one.
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
+{
+    return __all_sync(0xffffffffu, wait_lane(sh, bar, parity, status));
+}
+
+// One box of rows [token][head][d]: 64 columns.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t h, int32_t row,
+                                            uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(row), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return r;
+}
+// Pairs of fp32 for the two-wide FMA and add.
+__device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) { return pack2u(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ------------------------------------------------------------------ the items
+struct Plan {
+    int tok;                               // tokens of a row tile
+    int rows;                              // rows of a row tile that are used
+};
+
+__device__ __forceinline__ int pairs_of(int lq, const Plan& p) { return (lq + 2 * p.tok - 1) / (2 * p.tok); }
+
+struct Item {
+    int q0, lq, k0, lk, hk;
+    int t0;                                // the first row tile's first token
+    int cnt[2];                            // key tiles of the row tiles
+    int all;                               // keys that every row of the item sees
+    __device__ __forceinline__ int tiles() const { return max(cnt[0], cnt[1]); }
+    // Whether some row of the item does not see all of key tile j.
+    __device__ __forceinline__ bool edge(int j) const { return (j + 1) * KT > all; }
+};
+
+// The x-th item.  A whole warp calls it.
+__device__ __forceinline__ Item item_at(const Shared& sh, const PromptArgs& a, const Plan& p, long long x)
+{
+    const int lane = threadIdx.x & 31;
+    Item it;
+    int y = (int)(x / a.Hkv);
+    it.hk = (int)(x - (long long)y * a.Hkv);
+    const int entries = (a.N + sh.per - 1) / sh.per;
+    int lo = 0, hi = entries;              // the last entry with before <= y
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (sh.before[mid] <= y) lo = mid;
+        else hi = mid;
+    }
+    y -= sh.before[lo];
+    Seq s;
+    if (sh.per == 1) {
+        s = sh.seq[lo];
+    } else {
+        // through the entry's sequences, 32 at a time
+        s = {0, 0, 0, 0};
+        for (int n0 = lo * sh.per;; n0 += 32) {
+            const int n = n0 + lane;
+            PromptSeq ps = {0, 0, 0, 0};
+            if (n < a.N) ps = prompt_seq(a, n);
+            const int w = pairs_of(ps.lq, p);
+            int incl = w;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int z = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += z;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, y < incl);
+            if (past || n0 + 32 >= a.N) {
+                const int src = past ? __ffs(past) - 1 : 31;
+                y -= __shfl_sync(0xffffffffu, incl - w, src);
+                s.q0 = __shfl_sync(0xffffffffu, ps.q0, src);
+                s.lq = __shfl_sync(0xffffffffu, ps.lq, src);
+                s.k0 = __shfl_sync(0xffffffffu, ps.k0, src);
+                s.lk = __shfl_sync(0xffffffffu, ps.lk, src);
+                break;
+            }
+            y -= __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    // (offsets that give rows twice may add up to anything)
+    if (y < 0 || y >= pairs_of(s.lq, p)) {
+        s = {0, 0, 0, 0};
+        y = -1;
+    }
+    it.q0 = s.q0;
+    it.lq = s.lq;
+    it.k0 = s.k0;
+    it.lk = s.lk;
+    it.t0 = (pairs_of(s.lq, p) - 1 - y) * 2 * p.tok;       // a sequence's last rows, the longest work, first
+    const int off = s.lk - s.lq;
+    it.all = min(max(it.t0 + off + 1, 0), s.lk);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int end = min(it.t0 + (i + 1) * p.tok, s.lq);        // one past the row tile's last token
+        const int most = it.t0 + i * p.tok < s.lq ? min(max(end + off, 0), s.lk) : 0;
+        it.cnt[i] = (most + KT - 1) / KT;
+    }
+    return it;
+}
+
+// This CTA's items, dealt to and fro.
+struct Deal {
+    long long x;
+    int round;
+    __device__ __forceinline__ void start() { round = 0; x = blockIdx.x; }
+    __device__ __forceinline__ void next()
+    {
+        ++round;
+        x = (long long)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    }
+};
+
+// Sizes of the sequences in shared memory, longest first; all threads call it.
+__device__ void build_table(Shared& sh, const PromptArgs& a, const Plan& p)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.N + kMaxTable - 1) / kMaxTable, entries = (a.N + per - 1) / per;
+    if (per == 1) {
+        for (int n = tid; n < a.N; n += kThreads) {
+            const PromptSeq s = prompt_seq(a, n);
+            sh.seq[n] = {s.q0, s.lq, s.k0, s.lk};
+        }
+        __syncthreads();
+        if (a.N > 1 && a.N <= kMaxSorted) {
+            Seq mine = {0, 0, 0, 0};
+            int rank = 0;
+            if (tid < a.N) {
+                mine = sh.seq[tid];
+                for (int m = 0; m < a.N; ++m) {
+                    const int lk = sh.seq[m].lk;
+                    rank += lk > mine.lk || (lk == mine.lk && m < tid);
+                }
+            }
+            __syncthreads();
+            if (tid < a.N) sh.seq[rank] = mine;
+            __syncthreads();
+        }
+    }
+    int base = 0;
+    for (int e0 = 0; e0 < entries; e0 += kThreads) {
+        const int e = e0 + tid;
+        int w = 0;
+        if (e < entries) {
+            if (per == 1) {
+                w = pairs_of(sh.seq[e].lq, p);
+            } else {
+                for (int n = e * per; n < min((e + 1) * per, a.N); ++n) {
+                    int first, count;
+                    prompt_rows(a.cu_q, n, a.T, first, count);
+                    w += pairs_of(count, p);
+                }
+            }
+        }
+        int incl = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += z;
+        }
+        if (lane == 31) sh.sums[warp] = incl;
+        __syncthreads();
+        int all = 0, below = 0;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) below += sh.sums[i];
+            all += sh.sums[i];
+        }
+        if (e < entries) sh.before[e] = base + below + incl - w;
+        base += all;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        sh.total = base;
+        sh.per = per;
+    }
+}
+
+// ---------------------------------------------------------------- the copies
+// The entries of an item are K_0 V_0 K_1 V_1 ...  A tile of values on an item's
+// edge goes to the scanning warp first.
+template <int D>
+__device__ void kv_role(Shared& sh, const PromptArgs& a, const Plan& p, const CUtensorMap* map_k, const CUtensorMap* map_v,
+                        uint32_t slots, int lane)
+{
+    using Sh = Shape<D>;
+    int slot = 0;
+    uint32_t turn = 0, land_turn = 0, landed = 0, used = 0;        // bits by slot
+    bool ok = !a.starve;
+    Deal deal;
+    for (deal.start(); ok && deal.x < (long long)sh.total * a.Hkv; deal.next()) {
+        const Item it = item_at(sh, a, p, deal.x);
+        const int entries = 2 * it.tiles();
+#pragma unroll 1
+        for (int e = 0; e < entries; ++e) {
+            if (((used >> slot) & 1) && !wait(sh, &sh.kv_empty[slot], (turn ^ 1) & 1, a.status)) {
+                ok = false;
+                break;
+            }
+            const int j = e >> 1;
+            const bool scan = (e & 1) && it.edge(j);
+            uint64_t* bar = scan ? &sh.kv_land[slot] : &sh.kv_full[slot];
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, Sh::kSlotBytes);
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h)
+                    tma_load_3d(slots + (uint32_t)slot * Sh::kSlotBytes + h * (KT * 128), (e & 1) ? map_v : map_k, h * 64,
+                                it.hk, it.k0 + j * KT, bar);
+            }
+            __syncwarp();
+            used |= 1u << slot;
+            landed = (landed & ~(1u << slot)) | ((uint32_t)scan << slot);
+            if (scan) land_turn ^= 1u << slot;
+            if (++slot == Sh::kSlots) {
+                slot = 0;
+                turn ^= 1;
+            }
+        }
+    }
+    // After a wait that gave up nobody has waited for the last copies in flight.
+    if (*reinterpret_cast<volatile int*>(&sh.dead)) {
+#pragma unroll 1
+        for (int s = 0; s < Sh::kSlots; ++s) {
+            if (!((used >> s) & 1)) continue;
+            // the phase of the slot's last copy
+            if ((landed >> s) & 1) mbar_wait(&sh.kv_land[s], ((land_turn >> s) & 1) ^ 1, 1ll << 24);
+            else mbar_wait(&sh.kv_full[s], s < slot ? turn & 1 : (turn ^ 1) & 1, 1ll << 24);
+        }
+    }
+}
+
+template <int D>
+__device__ void q_role(Shared& sh, const PromptArgs& a, const Plan& p, const CUtensorMap* map_q, uint32_t q_smem, int lane)
+{
+    int count = 0;
+    bool ok = !a.starve;
+    Deal deal;
+    for (deal.start(); ok && deal.x < (long long)sh.total * a.Hkv; deal.next()) {
+        const Item it = item_at(sh, a, p, deal.x);
+        if (it.tiles() == 0) continue;
+        if (count > 0 && !wait(sh, &sh.q_empty, (uint32_t)(count - 1) & 1, a.status)) break;
+        if (lane == 0) {
+            const int nt = it.cnt[1] > 0 ? 2 : 1;
+            mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(nt * p.rows * D * 2));
+            for (int i = 0; i < nt; ++i)
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h)
+                    tma_load_3d(q_smem + (uint32_t)(i * 128 * D * 2 + h * (128 * 128)), map_q, h * 64, it.hk * a.G,
+                                it.q0 + it.t0 + i * p.tok, &sh.q_full);
+        }
+        __syncwarp();
+        ++count;
+    }
+    if (count > 0 && *reinterpret_cast<volatile int*>(&sh.dead)) mbar_wait(&sh.q_full, (uint32_t)(count - 1) & 1, 1ll << 24);
+}
+
+// Looks through the tiles of values on the items' edges.  A lane has every 32nd row of
+// a tile: x * 0 added up is NaN where some x is an infinity or NaN.
+template <int D>
+__device__ void scan_role(Shared& sh, const PromptArgs& a, const Plan& p, uint32_t slots, int lane)
+{
+    using Sh = Shape<D>;
+    int entry = 0;                                 // ring entries before this item
+    int tile = 0;                                  // key tiles before this item
+    uint32_t turn = 0;                             // of the landing barriers, bits by slot
+    Deal deal;
+    for (deal.start(); deal.x < (long long)sh.total * a.Hkv; deal.next()) {
+        const Item it = item_at(sh, a, p, deal.x);
+        const int cnt = it.tiles();
+#pragma unroll 1
+        for (int j = it.all / KT; j < cnt; ++j) {
+            const int slot = (entry + 2 * j + 1) % Sh::kSlots;
+            if (!wait(sh, &sh.kv_land[slot], (turn >> slot) & 1, a.status)) return;
+            turn ^= 1u << slot;
+            const uint32_t base = slots + (uint32_t)slot * Sh::kSlotBytes;
+            bool wrote = false;
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                const int r = b * 32 + lane;
+                uint32_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint32_t at = base + (c >> 3) * (KT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                    uint32_t x[4];
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[k]) : "r"(x[k]), "r"(0));
+                }
+                bool nan = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) nan |= (acc[k] & 0x7FFFu) > 0x7F80u || (acc[k] & 0x7FFF0000u) > 0x7F800000u;
+                if (nan) {
+                    wrote = true;
+#pragma unroll 1
+                    for (int c = 0; c < D / 2; ++c) {
+                        const uint32_t at = base + (c >> 5) * (KT * 128) + r * 128 + ((((c >> 2) & 7) ^ (r & 7)) << 4) + (c & 3) * 4;
+                        uint32_t x;
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at));
+                        if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+                        if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+                    }
+                }
+                const uint32_t bits = __ballot_sync(0xffffffffu, nan);
+                if (lane == 0) sh.bad[(tile + j) % kRingMeta][b] = bits;
+            }
+            if (wrote) fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.kv_full[slot]);
+        }
+        entry = (entry + 2 * cnt) % Sh::kSlots;
+        tile += cnt;
+    }
+}
+
+// -------------------------------------------------------------- the products
+// D = Q K^T: K-major operands, d / 16 steps of 32 bytes within 64-column blocks
+// 16 KB apart.  One elected lane issues all steps, if its ok is true.
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t q_desc, uint64_t k_desc, uint32_t idesc, bool ok)
+{
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) {
+        asm volatile(
+            "{\n\t.reg .pred e, t, f;\n\t.reg .b64 x, y;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.and.b32 e, %5, 0, e;\n\t"
+            "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+            "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+            "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+            "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d_tmem),
+            "l"(q_desc + 1024 * b), "l"(k_desc + 1024 * b), "r"(idesc), "r"(b), "r"((int)ok)
+            : "memory");
+    }
+}
+
+// D (+)= P V for 64 keys: P in TMEM (8 columns of bf16 pairs per step), V MN-major
+// (16 keys of 128 bytes per step).
+__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_t v_desc, uint32_t idesc,
+                                         uint32_t accumulate, bool ok)
+{
+    asm volatile(
+        "{\n\t.reg .pred e, t, f;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.and.b32 e, %5, 0, e;\n\t"
+        "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+        "add.s32 x, %1, 8;\n\tadd.s64 y, %2, 128;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+        "add.s32 x, %1, 16;\n\tadd.s64 y, %2, 256;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+        "add.s32 x, %1, 24;\n\tadd.s64 y, %2, 384;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t}" ::"r"(d_tmem),
+        "r"(p_tmem), "l"(v_desc), "r"(idesc), "r"(accumulate), "r"((int)ok)
+        : "memory");
+}
+
+// mma_commit (kda_sm100.cuh), if the elected lane's ok is true.
+__device__ __forceinline__ void commit_if(uint64_t* bar, bool ok)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.and.b32 e, %1, 0, e;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"((int)ok)
+        : "memory");
+}
+
+// For both row tiles in turn, the output of tile j and the scores of tile j + 1, which
+// go where tile j's scores and P were (the tensor core runs one thread's products in
+// order).  Once a wait has given up no product is issued and nothing signalled any
+// more; that is a predicate, so that the loops have one way out.
+template <int D>
+__device__ void mma_role(Shared& sh, const PromptArgs& a, const Plan& p, uint32_t q_smem, uint32_t slots, uint32_t tmem)
+{
+    using Sh = Shape<D>;
+    constexpr uint32_t id_qk = make_idesc_bf16(128, KT, false, false);
+    constexpr uint32_t id_pv = make_idesc_bf16(128, D, false, true);
+    int slot = 0;                                  // of the next ring entry to take
+    uint32_t turn = 0;                             // parity of its use
+    int done[2] = {0, 0};                          // tiles of the items before, by row tile
+    int pieces[2] = {0, 0}, items = 0;             // items before with work, by row tile and in all
+    bool ok = true;                                // no wait of this lane has given up
+    const uint64_t q_desc = make_sdesc(q_smem, 16, 1024, kSwizzle128B);
+    auto take = [&]() {
+        const int mine = slot;
+        ok &= wait_lane(sh, &sh.kv_full[mine], turn, a.status);
+        __syncwarp();
+        tc_fence_after();
+        if (++slot == Sh::kSlots) {
+            slot = 0;
+            turn ^= 1;
+        }
+        return mine;
+    };
+    Deal deal;
+    for (deal.start(); deal.x < (long long)sh.total * a.Hkv; deal.next()) {
+        const Item it = item_at(sh, a, p, deal.x);
+        const int cnt = it.tiles();
+        if (cnt == 0) continue;
+        ok &= wait_lane(sh, &sh.q_full, (uint32_t)items & 1, a.status);
+#pragma unroll 1
+        for (int j = -1; j < cnt; ++j) {
+            // V of tile j, then K of tile j + 1
+            const bool more = j + 1 < cnt;
+            const int ev = j >= 0 ? take() : 0;
+            int ek = -1;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (j >= 0 && j < it.cnt[i]) {
+                    const uint32_t v = slots + (uint32_t)ev * Sh::kSlotBytes;
+                    const uint64_t v_desc = make_sdesc(v, KT * 128, 1024, kSwizzle128B);
+                    const uint32_t o = tmem + Sh::kO + i * D, s = tmem + i * 128;
+                    ok &= wait_lane(sh, &sh.p_full[i], (uint32_t)(done[i] + j) & 1, a.status);
+                    if (j == 0 && pieces[i] > 0) ok &= wait_lane(sh, &sh.o_empty[i], (uint32_t)(pieces[i] - 1) & 1, a.status);
+                    __syncwarp();
+                    tc_fence_after();
+                    issue_pv(o, s, v_desc, id_pv, j > 0, ok);
+                    issue_pv(o, s + 64, v_desc + 512, id_pv, 1, ok);
+                    commit_if(&sh.pv_done[i], ok);
+                }
+                if (j + 1 < it.cnt[i]) {
+                    if (ek < 0) ek = take();
+                    const uint32_t k = slots + (uint32_t)ek * Sh::kSlotBytes;
+                    issue_qk<D>(tmem + i * 128, q_desc + (uint64_t)(i * 128 * D * 2 / 16), make_sdesc(k, 16, 1024, kSwizzle128B),
+                                id_qk, ok);
+                    commit_if(&sh.s_full[i], ok);
+                }
+            }
+            if (j >= 0) commit_if(&sh.kv_empty[ev], ok);
+            if (more) commit_if(&sh.kv_empty[ek], ok);
+            if (j + 2 == cnt) commit_if(&sh.q_empty, ok);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            done[i] += it.cnt[i];
+            pieces[i] += it.cnt[i] > 0;
+        }
+        ++items;
+    }
+    // the last products and their arrivals on the ring's barriers come before the block ends
+    mma_commit(&sh.done);
+    mbar_wait(&sh.done, 0);
+    __syncwarp();
+}
+
+// --------------------------------------------------- the softmax and the output
+template <int D>
+__device__ void softmax_role(Shared& sh, const PromptArgs& a, const Plan& p, int warp, int lane, uint32_t tmem)
+{
+    using Sh = Shape<D>;
+    constexpr float kSlack = 8.f;
+    constexpr int H = D / 2;                       // channels of the output of one half
+    const int i = warp >> 3, half = (warp >> 2) & 1;       // row tile; which 64 keys, which half of O
+    const int r = (warp & 3) * 32 + lane;          // row of the row tile
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = lanes + i * 128 + half * 64, to = lanes + Sh::kO + i * D + half * H;
+    const uint32_t bar = 1 + i * 4 + (warp & 3);   // named barrier of the two warps of these rows
+    const int tok = r / a.G, g = r - tok * a.G;
+    const bool row = r < p.rows;
+    const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
+    int done = 0;                                  // tiles before, of this row tile
+    int tile = 0;                                  // key tiles before
+    Deal deal;
+    for (deal.start(); deal.x < (long long)sh.total * a.Hkv; deal.next()) {
+        const Item it = item_at(sh, a, p, deal.x);
+        const int cnt = i ? it.cnt[1] : it.cnt[0];
+        const int t = it.t0 + i * p.tok + tok;     // this row's token
+        const bool mine = row && t < it.lq;
+        const int lim = mine ? min(max(t + it.lk - it.lq + 1, 0), it.lk) : 0;
+        // the keys that every row of the tile sees
+        const int all = min(max(it.t0 + i * p.tok + it.lk - it.lq + 1, 0), it.lk);
+        float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+        for (int j = 0; j < cnt; ++j) {
+            wait_lane(sh, &sh.s_full[i], (uint32_t)(done + j) & 1, a.status);
+            __syncwarp();
+            tc_fence_after();
+            uint32_t x[2][32];
+            tmem_ld32(ts, x[0]);
+            tmem_ld32(ts + 32, x[1]);
+            tmem_ld_wait();
+            if ((j + 1) * KT > all) {
+                const int left = lim - j * KT - half * 64;         // this thread's keys from here on are hidden
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if (c >= left) x[c >> 5][c & 31] = 0xff800000u;
+            }
+            float tops[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int at = (c & 1) * 16;
+                tops[c] = fmaxf(__uint_as_float(x[c >> 1][at]), __uint_as_float(x[c >> 1][at + 1]));
+#pragma unroll
+                for (int e = 2; e < 16; e += 2) tops[c] = max3(tops[c], x[c >> 1][at + e], x[c >> 1][at + e + 1]);
+            }
+            float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+            sh.top[i][half][r] = top;
+            named_bar_sync(bar, 64);
+            top = fmaxf(top, sh.top[i][half ^ 1][r]) * a.scale_log2;   // the scale is positive on this path
+            const bool grow = top > m + kSlack || (m == -INFINITY && top > m);
+            if (__any_sync(0xffffffffu, grow)) {
+                const float m2 = grow ? top : m;
+                const float f = m2 == -INFINITY ? 1.f : ex2(m - m2);
+                m = m2;
+                l *= f;
+                if (j > 0) {
+                    wait_lane(sh, &sh.pv_done[i], (uint32_t)(done + j - 1) & 1, a.status);
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < H / 16; ++c) {
+                        uint32_t y[16];
+                        tmem_ld16(to + 16 * c, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+                        tmem_st16(to + 16 * c, y);
+                    }
+                }
+            }
+            // masked scores stay -inf (their e is 0) unless nothing was seen so far
+            const uint64_t ref2 = pack2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
+            uint64_t sum[2] = {0, 0};
+            uint32_t e2[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const int c = e >> 4, k = 2 * (e & 15);
+                float e0, e1;
+                unpack2(fma2(pack2u(x[c][k], x[c][k + 1]), scale2, ref2), e0, e1);
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+                sum[e & 1] = add2(sum[e & 1], pack2(e0, e1));
+                e2[e] = pack_bf16x2(e0, e1);
+            }
+            tmem_st32(ts, e2);                     // over this half's scores, all of them in registers
+            float s0, s1;
+            unpack2(add2(sum[0], sum[1]), s0, s1);
+            l += s0 + s1;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[i]);
+        }
+        // the output
+        __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.o) +
+                            ((long long)(it.q0 + (mine ? t : 0)) * a.Hq + (long long)it.hk * a.G + g) * D + half * H;
+        if (cnt == 0) {
+            if (mine) {
+#pragma unroll
+                for (int c = 0; c < H / 8; ++c) *(reinterpret_cast<uint4*>(op) + c) = make_uint4(0, 0, 0, 0);
+            }
+        } else {
+            sh.sum[i][half][r] = l;
+            wait_lane(sh, &sh.pv_done[i], (uint32_t)(done + cnt - 1) & 1, a.status);
+            named_bar_sync(bar, 64);
+            tc_fence_after();
+            l += sh.sum[i][half ^ 1][r];
+            // when some wait has given up, this item and those after it are not known
+            if (*reinterpret_cast<volatile int*>(&sh.dead)) l = __int_as_float(0x7fffffff);
+            const float scale_o = lim == 0 ? 0.f : 1.f / l;
+            // keys with an infinity or NaN that this row sees
+            bool any = false;
+#pragma unroll 1
+            for (int j = it.all / KT; j < cnt; ++j) {
+                const uint32_t* bad = sh.bad[(tile + j) % kRingMeta];
+                any |= (bad[0] | bad[1] | bad[2] | bad[3]) != 0;
+            }
+            if (any) {
+#pragma unroll 1
+                for (int c = 0; c < H / 16; ++c) {
+                    uint32_t y[16];
+                    tmem_ld16(to + 16 * c, y);
+                    tmem_ld_wait();
+#pragma unroll 1
+                    for (int k = it.all / KT * KT; k < min(lim, cnt * KT); ++k) {
+                        if (!((sh.bad[(tile + k / KT) % kRingMeta][(k >> 5) & 3] >> (k & 31)) & 1)) continue;
+                        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) +
+                            (long long)(it.k0 + k) * a.v_stride + it.hk * D + half * H + 16 * c;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float z = __bfloat162float(v[e]);
+                            if (!(fabsf(z) < INFINITY)) y[e] = __float_as_uint(__uint_as_float(y[e]) + z);
+                        }
+                    }
+                    __syncwarp();
+                    tmem_st16(to + 16 * c, y);
+                }
+                tmem_st_wait();
+            }
+#pragma unroll 1
+            for (int c = 0; c < H / 32; ++c) {
+                uint32_t y[32];
+                tmem_ld32(to + 32 * c, y);
+                tmem_ld_wait();
+                if (c + 1 == H / 32) {             // the last columns are in registers
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.o_empty[i]);
+                }
+                if (mine) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t z[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            z[k] = pack_bf16x2(__uint_as_float(y[e + 2 * k]) * scale_o, __uint_as_float(y[e + 2 * k + 1]) * scale_o);
+                        *reinterpret_cast<uint4*>(op + 32 * c + e) = lim == 0 ? make_uint4(0, 0, 0, 0) : make_uint4(z[0], z[1], z[2], z[3]);
+                    }
+                }
+                __syncwarp();                      // before the next collective load
+            }
+        }
+        done += cnt;
+        tile += it.tiles();
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_attention_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ Plan p,
+                           const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                           const __grid_constant__ CUtensorMap map_v)
+{
+    using Sh = Shape<D>;
+    extern __shared__ uint8_t raw[];
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t q_smem = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t slots = q_smem + Sh::kQBytes;
+    if (tid == 0) {
+        for (int i = 0; i < Sh::kSlots; ++i) {
+            mbar_init(&sh.kv_full[i], 1);
+            mbar_init(&sh.kv_land[i], 1);
+            mbar_init(&sh.kv_empty[i], 1);
+        }
+        mbar_init(&sh.q_full, 1);
+        mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], 8);
+            mbar_init(&sh.pv_done[i], 1);
+            mbar_init(&sh.o_empty[i], 8);
+        }
+        sh.dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    build_table(sh, a, p);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
+    if (warp < kMmaWarp) {
+        more_registers<kMore>();
+        softmax_role<D>(sh, a, p, warp, lane, tmem);
+    } else {
+        fewer_registers<kFewer>();
+        if (warp == kMmaWarp) mma_role<D>(sh, a, p, q_smem, slots, tmem);
+        else if (warp == kKvWarp) kv_role<D>(sh, a, p, &map_k, &map_v, slots, lane);
+        else if (warp == kQWarp) q_role<D>(sh, a, p, &map_q, q_smem, lane);
+        else scan_role<D>(sh, a, p, slots, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Rows [rows][heads][d], boxes of `tokens` rows, `group` heads and 64 columns in the
+// 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, int d, int heads, long long rows, long long stride, int group, int tokens)
+{
+    const auto fn = tc_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t boxes[3] = {64, (cuuint32_t)group, (cuuint32_t)tokens};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, boxes, steps,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS && debug_enabled())
+        fprintf(stderr, "kda: cuTensorMapEncodeTiled failed (CUresult %d, prompt)\n", (int)r);
+    return r == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const PromptArgs& a, int sms, cudaStream_t stream)
+{
+    Plan p;
+    p.tok = 128 / a.G;
+    p.rows = p.tok * a.G;
+    CUtensorMap map_q, map_k, map_v;
+    if (!make_map(&map_q, a.q, D, a.Hq, a.T, a.q_stride, a.G, p.tok) || !make_map(&map_k, a.k, D, a.Hkv, a.Tk, a.k_stride, 1, KT) ||
+        !make_map(&map_v, a.v, D, a.Hkv, a.Tk, a.v_stride, 1, KT))
+        return cudaErrorInvalidValue;
+    auto kern = prompt_attention_tc_kernel<D>;
+    const size_t bytes = Shape<D>::kBytes;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    // every sequence has at most one pair of row tiles that is not full
+    const long long items = ((long long)a.T / (2 * p.tok) + a.N) * a.Hkv;
+    kern<<<(unsigned)(items < sms ? items : sms), kThreads, bytes, stream>>>(a, p, map_q, map_k, map_v);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool prompt_tc_supported(const PromptArgs& a, int32_t d, kda_dtype_t dtype)
+{
+    return dtype == KDA_BF16 && (d == 64 || d == 128) && a.scale_log2 > 0.f && a.G <= 128 && a.Tk > 0 &&
+           getenv("KDA_FORCE_SIMT") == nullptr;
+}
+
+cudaError_t launch_prompt_attention_tc(PromptArgs a, int32_t d, int sms, cudaStream_t stream)
+{
+    a.starve = getenv("KDA_TEST_STARVE_CONSUMERS") != nullptr;
+    return d == 64 ? launch<64>(a, sms, stream) : launch<128>(a, sms, stream);
+}
+
+}  // namespace kda
