@@ -45,7 +45,8 @@ EXPORTS = ("kda_prefill_workspace_bytes", "kda_prefill", "kda_decode_step",
            "kda_prefill_segmented_workspace_bytes", "kda_prefill_segmented",
            "kda_decode_tree", "kda_tree_attention_workspace_bytes", "kda_tree_attention",
            "kda_token_logprobs", "kda_cache_commit", "kda_cache_append",
-           "kda_prompt_attention", "kda_cache_append_rotary",
+           "kda_prompt_attention_workspace_bytes", "kda_prompt_attention",
+           "kda_cache_append_rotary",
            "kda_cache_attention_e4m3_workspace_bytes", "kda_cache_attention_e4m3")
 
 
@@ -124,7 +125,9 @@ def _declare(lib):
     lib.kda_prompt_attention.restype = ctypes.c_int
     lib.kda_prompt_attention.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _i64,
                                          _i64, _i32, _i32, _i32, ctypes.c_int, ctypes.c_float,
-                                         _vp, _vp, _vp]
+                                         _vp, _vp, _sz, _vp]
+    lib.kda_prompt_attention_workspace_bytes.restype = _sz
+    lib.kda_prompt_attention_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, ctypes.c_int]
     lib.kda_cache_append_rotary.restype = ctypes.c_int
     lib.kda_cache_append_rotary.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i32,
                                             _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
@@ -766,8 +769,19 @@ def _check_rows(name, t, dtype, device):
     return row if T > 1 else h * d
 
 
+def kda_prompt_attention_workspace_bytes(num_seqs: int, Hq: int, Hkv: int, d: int,
+                                         dtype: int) -> int:
+    return int(lib().kda_prompt_attention_workspace_bytes(num_seqs, Hq, Hkv, d, dtype))
+
+
+@functools.lru_cache(maxsize=1024)
+def _prompt_bytes(*sizes):
+    """kda_prompt_attention_workspace_bytes, at least 256."""
+    return max(kda_prompt_attention_workspace_bytes(*sizes), 256)
+
+
 def kda_prompt_attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=None, o=None,
-                         status=None, stream=None, o_dtype=None):
+                         workspace=None, stream=None, o_dtype=None):
     """Causal softmax attention over packed sequences (C ABI:
     kda_prompt_attention).
 
@@ -775,9 +789,9 @@ def kda_prompt_attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=N
     stride (views of one projection's output); cu_seqlens: int32 [N+1] or None for
     one sequence; cu_seqlens_k: the same for k and v, None when it is cu_seqlens.  The
     queries of a sequence are its last: query i sees keys 0 .. i + Lk - Lq.  scale:
-    d ** -0.5 by default.  status: int32 [1] or None, bit 1 set when a wait in the
-    kernel gave up (o has NaN then).  Returns o [T, Hq, d]; rows of an ``o`` that
-    cu_seqlens gives to no sequence keep what they hold."""
+    d ** -0.5 by default.  Returns o [T, Hq, d]; rows of an ``o`` that cu_seqlens gives
+    to no sequence keep what they hold.  NaN in o where the inputs have none means
+    that a wait in the kernel gave up."""
     torch = _torch()
     _forward_only("kda_prompt_attention", q, k, v)
     T, Hq, d = q.shape
@@ -789,7 +803,6 @@ def kda_prompt_attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=N
     strides = [_check_rows(name, t, q.dtype, dev) for name, t in (("q", q), ("k", k), ("v", v))]
     _check_cuda("cu_seqlens", cu_seqlens, torch.int32)
     _check_cuda("cu_seqlens_k", cu_seqlens_k, torch.int32)
-    _check_cuda("status", status, torch.int32)
     _shape("k", k, (Tk, Hkv, d))
     _shape("v", v, (Tk, Hkv, d))
     N = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
@@ -800,9 +813,14 @@ def kda_prompt_attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=N
     elif Tk != T:
         raise ValueError("k must have q's tokens, or cu_seqlens_k be given")
     o = _out("o", o, (T, Hq, d), o_dtype, dev, stream)
+    if workspace is None:
+        workspace = _new((_prompt_bytes(N, Hq, Hkv, d, dt),), torch.uint8, dev, stream)
+    else:
+        _check_cuda("workspace", workspace)
     _call("kda_prompt_attention", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
           _address(cu_seqlens), _address(cu_seqlens_k), N, T, Tk, Hq, Hkv, d, dt,
-          d ** -0.5 if scale is None else scale, o.data_ptr(), _address(status))
+          d ** -0.5 if scale is None else scale, o.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return o
 
 

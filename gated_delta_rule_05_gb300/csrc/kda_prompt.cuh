@@ -15,7 +15,8 @@ struct PromptArgs {
     int32_t Hq, Hkv, G;               // G = Hq / Hkv
     float scale_log2;                 // scale * log2(e)
     void* o;                          // [T, Hq, d]
-    int32_t* status;                  // tensor-core kernel: the workspace's words
+    int32_t* status;                  // tensor-core kernel: words of the workspace
+    uint32_t* counter;
     bool starve;                      // test of the waits that give up
 };
 

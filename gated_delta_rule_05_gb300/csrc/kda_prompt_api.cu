@@ -51,6 +51,11 @@ bool head_sizes(int32_t Hq, int32_t Hkv, int32_t d)
     return Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq <= (1 << 20) && (int64_t)Hq * d * 4 <= INT32_MAX;
 }
 
+bool prompt_sizes(int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t d)
+{
+    return num_seqs >= 1 && head_sizes(Hq, Hkv, d) && Hkv <= 65535;
+}
+
 bool newest_sizes(int32_t N, int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d)
 {
     return N >= 1 && Ts >= 1 && head_sizes(Hq, Hkv, d) && (int64_t)Ts * Hq <= (1 << 20);
@@ -60,14 +65,19 @@ bool newest_sizes(int32_t N, int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d)
 
 extern "C" {
 
+size_t kda_prompt_attention_workspace_bytes(int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t d, kda_dtype_t dtype)
+{
+    return valid_dtype(dtype) && supported_d(d) && prompt_sizes(num_seqs, Hq, Hkv, d) ? kda::kWsHeaderBytes : 0;
+}
+
 kda_status_t kda_prompt_attention(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
                                   int64_t v_stride, const int32_t* cu_seqlens, const int32_t* cu_seqlens_k,
                                   int32_t num_seqs, int64_t total_tokens, int64_t total_keys, int32_t Hq, int32_t Hkv,
-                                  int32_t d, kda_dtype_t dtype, float scale, void* o, int32_t* status,
-                                  cudaStream_t stream)
+                                  int32_t d, kda_dtype_t dtype, float scale, void* o, void* workspace,
+                                  size_t workspace_bytes, cudaStream_t stream)
 {
     if (!valid_dtype(dtype) || !supported_d(d)) return KDA_ERR_UNSUPPORTED;
-    if (num_seqs < 1 || !head_sizes(Hq, Hkv, d) || Hkv > 65535) return KDA_ERR_INVALID_ARG;
+    if (!prompt_sizes(num_seqs, Hq, Hkv, d)) return KDA_ERR_INVALID_ARG;
     if (total_tokens < 0 || total_keys < 0 || total_tokens > INT32_MAX - 65536 || total_keys > INT32_MAX - 65536)
         return KDA_ERR_INVALID_ARG;
     if (num_seqs > 1 && !cu_seqlens) return KDA_ERR_INVALID_ARG;
@@ -77,7 +87,7 @@ kda_status_t kda_prompt_attention(const void* q, const void* k, const void* v, i
     const void* ptrs16[] = {q, k, v, o};
     for (const void* p : ptrs16)
         if (p && !aligned(p, 16)) return KDA_ERR_INVALID_ARG;
-    const void* ptrs4[] = {cu_seqlens, cu_seqlens_k, status};
+    const void* ptrs4[] = {cu_seqlens, cu_seqlens_k};
     for (const void* p : ptrs4)
         if (p && !aligned(p, 4)) return KDA_ERR_INVALID_ARG;
     const int64_t qw = (int64_t)Hq * d, kw = (int64_t)Hkv * d;
@@ -94,6 +104,12 @@ kda_status_t kda_prompt_attention(const void* q, const void* k, const void* v, i
         meets(row_span(v, v_stride, kw, total_keys, elem), o, o_bytes) ||
         (cu_seqlens && overlaps(cu_seqlens, cu_bytes, o, o_bytes)) ||
         (cu_seqlens_k && overlaps(cu_seqlens_k, cu_bytes, o, o_bytes)))
+        return KDA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kda::kWsHeaderBytes || !aligned(workspace, 256)) return KDA_ERR_WORKSPACE;
+    if (overlaps(workspace, kda::kWsHeaderBytes, o, o_bytes) ||
+        meets(row_span(q, q_stride, qw, total_tokens, elem), workspace, kda::kWsHeaderBytes) ||
+        meets(row_span(k, k_stride, kw, total_keys, elem), workspace, kda::kWsHeaderBytes) ||
+        meets(row_span(v, v_stride, kw, total_keys, elem), workspace, kda::kWsHeaderBytes))
         return KDA_ERR_INVALID_ARG;
 
     kda::PromptArgs a = {};
@@ -113,7 +129,8 @@ kda_status_t kda_prompt_attention(const void* q, const void* k, const void* v, i
     a.G = Hq / Hkv;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.o = o;
-    a.status = status;
+    a.status = static_cast<int32_t*>(workspace) + kda::kWsTimeoutWord;
+    a.counter = static_cast<uint32_t*>(workspace) + kda::kWsCounterWord;
     const int sms = kda::device_sm_count();
     const cudaError_t err = kda::prompt_tc_supported(a, d, dtype)
                                 ? kda::launch_prompt_attention_tc(a, d, sms > 0 ? sms : 1, stream)

@@ -15,22 +15,26 @@
 // bf16, the type of V, as one product takes one type; l sums the values before
 // the rounding.
 //
-// Roles: four warpgroups of softmax and output, two per row tile with 64 of a
-// tile's 128 keys each (their threads of one row exchange its maximum and, at the end, its sum
-// through shared memory); a warp that issues products, one that copies keys and
-// values, one that copies queries, one that looks through values (below).  The row
-// tiles share K and V and alternate on the tensor core: one's softmax runs under the
-// other's products.
+// Roles: four warpgroups of softmax and output, two per row tile with 64 of a tile's
+// 128 keys each (their threads of one row exchange its maximum and its sum through
+// shared memory); a warp that issues products, one that copies keys and values, one that
+// finds the items and copies their queries, one that looks through values (below).
+// The row tiles share K and V and alternate on the tensor core: one's softmax runs under
+// the other's products.
 //
 // Values that a row of the item does not see must not reach it through 0 * inf: in the
 // tiles on the diagonal and at the end of a sequence the fourth warp replaces
 // infinities and NaN by 0 before the product and notes their keys; the rows that do
 // see such a key add its value to their output at the end.
 //
-// Items are dealt to the CTAs in a fixed order, long ones first, to and fro, so that no
-// counter is shared between CTAs or calls.
+// Items go to the CTAs in order, the sequences with most keys first and of each its
+// last rows, one at a time from a counter in the caller's workspace: 12 prompts of 512
+// to 12,288 tokens, the longest CTA has 1.001 times the mean's tiles, dealt to and fro 1.07.
+// (Taken over all sequences by their length, dealt to and fro, 1.002, but the keys of
+// all of them pass through the L2 again and again: 4.05 ms against 3.85.)  Where there are few
+// items for a CTA they are dealt to and fro, which saves the clearing of the counter.
 //
-// Every wait has a limit; one that gives up sets the caller's status word and stops
+// Every wait has a limit; one that gives up sets the workspace's timeout word and stops
 // its CTA: the warps that start copies and products end at their next wait and wait for
 // what they have started (again with a limit), and the softmax runs on without
 // waiting, over whatever is there, and gives its rows a sum of NaN.  The environment
@@ -53,19 +57,21 @@ using namespace sm100;
 
 constexpr int KT = 128;                    // keys per tile
 constexpr int kThreads = 640;              // 16 softmax warps, 4 others
-constexpr int kMmaWarp = 16, kKvWarp = 17, kQWarp = 18, kScanWarp = 19;
+constexpr int kMmaWarp = 16, kKvWarp = 17, kQWarp = 18;
 // 640 threads are launched with 96 registers: 512 x 104 + 128 x 64 = 640 x 96
 constexpr int kMore = 104, kFewer = 64;
-constexpr int kMaxTable = 1024;            // sequences whose sizes are held in shared memory
-constexpr int kMaxSorted = 256;
+constexpr int kMaxTable = 256;             // sequences whose sizes are held in shared memory
 constexpr int kRingMeta = 16;              // tiles whose notes of infinities and NaN are kept
+constexpr int kItems = 4;                  // items that are known ahead
+constexpr int kItemReaders = 16 + 3;       // warps
 
 template <int D>
 struct Shape {
     static constexpr int kQBytes = 2 * 128 * D * 2;
     static constexpr int kSlotBytes = KT * D * 2;
     static constexpr int kSlots = D == 128 ? 4 : 8;
-    static constexpr size_t kBytes = 1024 + kQBytes + (size_t)kSlots * kSlotBytes;
+    static constexpr int kStageBytes = 1024;       // of a warp, for its rows on their way out
+    static constexpr size_t kBytes = 1024 + kQBytes + (size_t)kSlots * kSlotBytes + 16 * kStageBytes;
     static constexpr int kO = 256;         // TMEM column of the outputs; the scores are at 0 and 128
 };
 
@@ -73,41 +79,76 @@ struct Seq {
     int q0, lq, k0, lk;
 };
 
+// An item: its sequence, cache head and row tiles.
+struct alignas(16) Item {
+    int q0, lq, k0, lk;
+    int hk;                                // -1: there are no more
+    int t0;                                // the first row tile's first token
+    int cnt[2];                            // key tiles of the row tiles
+    int all;                               // keys that every row of the item sees
+    int pad[3];
+    __device__ __forceinline__ int tiles() const { return max(cnt[0], cnt[1]); }
+    // Whether some row of the item does not see all of key tile j.
+    __device__ __forceinline__ bool edge(int j) const { return (j + 1) * KT > all; }
+};
+
 struct Shared {
-    uint64_t kv_full[8], kv_land[8], kv_empty[8], q_full, q_empty, done;
-    uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2];
+    uint64_t kv_full[8], kv_land[8], kv_empty[8], q_full, q_empty, kv_started, done;
+    uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2], item_full[kItems], item_empty[kItems];
+    Item item[kItems];
     uint32_t tmem;
     int dead;
     int total;                             // row tile pairs of all sequences, for one cache head
     int per;                               // sequences of a table entry
-    float top[2][2][128], sum[2][2][128];
+    float top[2][2][128];                  // of a row tile and half of a tile's keys, by row
+    float sum[2][2][128];
+    int bad_tile;                          // one past the last tile with a note
     alignas(16) uint32_t bad[kRingMeta][4];    // a tile's keys with inf or NaN in v
     int sums[kThreads / 32];
-    int before[kMaxTable + 1];             // row tile pairs before a table entry
-    alignas(16) Seq seq[kMaxTable];        // (only where an entry is one sequence)
+    int before[kMaxTable];                 // row tile pairs before a table entry
+    int pairs[kMaxTable];                  // (these only where an entry is one sequence)
+    alignas(16) Seq seq[kMaxTable];
 };
 
-// Waits for a phase of a barrier, for about two seconds at most and no longer than
-// until some wait of this CTA has given up; false then.
-__device__ __forceinline__ bool wait_lane(Shared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
+// Waits for a phase of a barrier, for about two seconds at most and (STOP) no longer
+// than until some wait of this CTA has given up; false then.  Written short: the roles
+// run side by side and have to share the SM's instruction cache.
+template <bool STOP>
+__device__ __forceinline__ bool wait_for(Shared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
 {
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
 #pragma unroll 1
     while (!mbar_try_wait(bar, parity)) {
-        if (*reinterpret_cast<volatile int*>(&sh.dead)) return false;
+        if (STOP && *reinterpret_cast<volatile int*>(&sh.dead)) return false;
         if (clock64() - t0 > (1ll << 32)) {
             *reinterpret_cast<volatile int*>(&sh.dead) = 1;
-            if (status) atomicOr(status, 2);
+            atomicOr(status, 2);
             return false;
         }
     }
     return true;
 }
+__device__ __forceinline__ bool wait_lane(Shared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
+{
+    return wait_for<true>(sh, bar, parity, status);
+}
 // The same for a warp, which goes on as one or stops as one.
 __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
 {
-    return __all_sync(0xffffffffu, wait_lane(sh, bar, parity, status));
+    return __all_sync(0xffffffffu, wait_for<true>(sh, bar, parity, status));
+}
+// The same, of a barrier of the items, which are handed on when a wait has given up too.
+__device__ __forceinline__ bool wait_item(Shared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
+{
+    return __all_sync(0xffffffffu, wait_for<false>(sh, bar, parity, status));
+}
+// Waits for a copy in flight after some wait has given up.
+__device__ __noinline__ void settle(uint64_t* bar, uint32_t parity)
+{
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity) && clock64() - t0 < (1ll << 24)) {}
 }
 
 // One box of rows [token][head][d]: 64 columns.
@@ -175,38 +216,31 @@ struct Plan {
 
 __device__ __forceinline__ int pairs_of(int lq, const Plan& p) { return (lq + 2 * p.tok - 1) / (2 * p.tok); }
 
-struct Item {
-    int q0, lq, k0, lk, hk;
-    int t0;                                // the first row tile's first token
-    int cnt[2];                            // key tiles of the row tiles
-    int all;                               // keys that every row of the item sees
-    __device__ __forceinline__ int tiles() const { return max(cnt[0], cnt[1]); }
-    // Whether some row of the item does not see all of key tile j.
-    __device__ __forceinline__ bool edge(int j) const { return (j + 1) * KT > all; }
-};
-
-// The x-th item.  A whole warp calls it.
-__device__ __forceinline__ Item item_at(const Shared& sh, const PromptArgs& a, const Plan& p, long long x)
+// The x-th item: sequence by sequence, of a sequence its last rows, the longest work,
+// first, and of those every head; but head by head where the sequence's keys and values
+// would take much of the L2.  A whole warp calls it.
+template <int D>
+__device__ __noinline__ Item item_at(const Shared& sh, const PromptArgs& a, const Plan& p, long long x)
 {
     const int lane = threadIdx.x & 31;
-    Item it;
+    Item it = {};
     int y = (int)(x / a.Hkv);
-    it.hk = (int)(x - (long long)y * a.Hkv);
-    const int entries = (a.N + sh.per - 1) / sh.per;
+    const int per = sh.per, entries = (a.N + per - 1) / per;
     int lo = 0, hi = entries;              // the last entry with before <= y
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         if (sh.before[mid] <= y) lo = mid;
         else hi = mid;
     }
-    y -= sh.before[lo];
-    Seq s;
-    if (sh.per == 1) {
+    x -= (long long)sh.before[lo] * a.Hkv; // from the entry's first item
+    Seq s = {0, 0, 0, 0};
+    int pairs = 0;
+    if (per == 1) {
         s = sh.seq[lo];
+        pairs = sh.pairs[lo];
     } else {
         // through the entry's sequences, 32 at a time
-        s = {0, 0, 0, 0};
-        for (int n0 = lo * sh.per;; n0 += 32) {
+        for (int n0 = lo * per;; n0 += 32) {
             const int n = n0 + lane;
             PromptSeq ps = {0, 0, 0, 0};
             if (n < a.N) ps = prompt_seq(a, n);
@@ -217,29 +251,34 @@ __device__ __forceinline__ Item item_at(const Shared& sh, const PromptArgs& a, c
                 const int z = __shfl_up_sync(0xffffffffu, incl, off);
                 if (lane >= off) incl += z;
             }
-            const uint32_t past = __ballot_sync(0xffffffffu, y < incl);
+            const uint32_t past = __ballot_sync(0xffffffffu, x < (long long)incl * a.Hkv);
             if (past || n0 + 32 >= a.N) {
                 const int src = past ? __ffs(past) - 1 : 31;
-                y -= __shfl_sync(0xffffffffu, incl - w, src);
+                x -= (long long)__shfl_sync(0xffffffffu, incl - w, src) * a.Hkv;
                 s.q0 = __shfl_sync(0xffffffffu, ps.q0, src);
                 s.lq = __shfl_sync(0xffffffffu, ps.lq, src);
                 s.k0 = __shfl_sync(0xffffffffu, ps.k0, src);
                 s.lk = __shfl_sync(0xffffffffu, ps.lk, src);
                 break;
             }
-            y -= __shfl_sync(0xffffffffu, incl, 31);
+            x -= (long long)__shfl_sync(0xffffffffu, incl, 31) * a.Hkv;
         }
+        pairs = pairs_of(s.lq, p);
     }
     // (offsets that give rows twice may add up to anything)
-    if (y < 0 || y >= pairs_of(s.lq, p)) {
-        s = {0, 0, 0, 0};
-        y = -1;
+    if (x < 0 || x >= (long long)pairs * a.Hkv) return it;
+    if ((long long)s.lk * a.Hkv * D * 4 > (64 << 20)) {
+        it.hk = (int)(x / pairs);
+        y = (int)(x - (long long)it.hk * pairs);
+    } else {
+        y = (int)(x / a.Hkv);
+        it.hk = (int)(x - (long long)y * a.Hkv);
     }
     it.q0 = s.q0;
     it.lq = s.lq;
     it.k0 = s.k0;
     it.lk = s.lk;
-    it.t0 = (pairs_of(s.lq, p) - 1 - y) * 2 * p.tok;       // a sequence's last rows, the longest work, first
+    it.t0 = (pairs - 1 - y) * 2 * p.tok;
     const int off = s.lk - s.lq;
     it.all = min(max(it.t0 + off + 1, 0), s.lk);
 #pragma unroll
@@ -251,52 +290,70 @@ __device__ __forceinline__ Item item_at(const Shared& sh, const PromptArgs& a, c
     return it;
 }
 
-// This CTA's items, dealt to and fro.
-struct Deal {
-    long long x;
-    int round;
-    __device__ __forceinline__ void start() { round = 0; x = blockIdx.x; }
-    __device__ __forceinline__ void next()
+// A warp's way through this CTA's items, which the query warp finds out ahead of the
+// others.
+struct Items {
+    int n = 0;
+    // The next one; null: there is none.
+    __device__ __forceinline__ const Item* next(Shared& sh, int32_t* status)
     {
-        ++round;
-        x = (long long)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const Item* it = &sh.item[n % kItems];
+        if (!wait_item(sh, &sh.item_full[n % kItems], (uint32_t)(n / kItems) & 1, status)) return nullptr;
+        return it->hk < 0 ? nullptr : it;
+    }
+    // Has been read.
+    __device__ __forceinline__ void release(Shared& sh, int lane)
+    {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.item_empty[n % kItems]);
+        ++n;
     }
 };
 
-// Sizes of the sequences in shared memory, longest first; all threads call it.
+// Sizes of the sequences in shared memory, those with most keys first (up to
+// kMaxTable); all threads call it.
 __device__ void build_table(Shared& sh, const PromptArgs& a, const Plan& p)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.N + kMaxTable - 1) / kMaxTable, entries = (a.N + per - 1) / per;
     if (per == 1) {
+#pragma unroll 1
         for (int n = tid; n < a.N; n += kThreads) {
             const PromptSeq s = prompt_seq(a, n);
             sh.seq[n] = {s.q0, s.lq, s.k0, s.lk};
+            sh.pairs[n] = pairs_of(s.lq, p);
         }
         __syncthreads();
-        if (a.N > 1 && a.N <= kMaxSorted) {
+        if (a.N > 1) {
             Seq mine = {0, 0, 0, 0};
-            int rank = 0;
+            int rank = 0, pairs = 0;
             if (tid < a.N) {
                 mine = sh.seq[tid];
+                pairs = sh.pairs[tid];
+#pragma unroll 1
                 for (int m = 0; m < a.N; ++m) {
                     const int lk = sh.seq[m].lk;
                     rank += lk > mine.lk || (lk == mine.lk && m < tid);
                 }
             }
             __syncthreads();
-            if (tid < a.N) sh.seq[rank] = mine;
+            if (tid < a.N) {
+                sh.seq[rank] = mine;
+                sh.pairs[rank] = pairs;
+            }
             __syncthreads();
         }
     }
     int base = 0;
+#pragma unroll 1
     for (int e0 = 0; e0 < entries; e0 += kThreads) {
         const int e = e0 + tid;
         int w = 0;
         if (e < entries) {
             if (per == 1) {
-                w = pairs_of(sh.seq[e].lq, p);
+                w = sh.pairs[e];
             } else {
+#pragma unroll 1
                 for (int n = e * per; n < min((e + 1) * per, a.N); ++n) {
                     int first, count;
                     prompt_rows(a.cu_q, n, a.T, first, count);
@@ -313,11 +370,13 @@ __device__ void build_table(Shared& sh, const PromptArgs& a, const Plan& p)
         if (lane == 31) sh.sums[warp] = incl;
         __syncthreads();
         int all = 0, below = 0;
+#pragma unroll 1
         for (int i = 0; i < kThreads / 32; ++i) {
             if (i < warp) below += sh.sums[i];
             all += sh.sums[i];
         }
-        if (e < entries) sh.before[e] = base + below + incl - w;
+        incl += base + below;
+        if (e < entries) sh.before[e] = incl - w;
         base += all;
         __syncthreads();
     }
@@ -331,17 +390,17 @@ __device__ void build_table(Shared& sh, const PromptArgs& a, const Plan& p)
 // The entries of an item are K_0 V_0 K_1 V_1 ...  A tile of values on an item's
 // edge goes to the scanning warp first.
 template <int D>
-__device__ void kv_role(Shared& sh, const PromptArgs& a, const Plan& p, const CUtensorMap* map_k, const CUtensorMap* map_v,
-                        uint32_t slots, int lane)
+__device__ void kv_role(Shared& sh, const PromptArgs& a, const CUtensorMap* map_k, const CUtensorMap* map_v, uint32_t slots,
+                        int lane)
 {
     using Sh = Shape<D>;
     int slot = 0;
     uint32_t turn = 0, land_turn = 0, landed = 0, used = 0;        // bits by slot
     bool ok = !a.starve;
-    Deal deal;
-    for (deal.start(); ok && deal.x < (long long)sh.total * a.Hkv; deal.next()) {
-        const Item it = item_at(sh, a, p, deal.x);
-        const int entries = 2 * it.tiles();
+    Items items;
+    for (const Item* at; (at = items.next(sh, a.status)); items.release(sh, lane)) {
+        const Item it = *at;
+        const int entries = ok ? 2 * it.tiles() : 0;
 #pragma unroll 1
         for (int e = 0; e < entries; ++e) {
             if (((used >> slot) & 1) && !wait(sh, &sh.kv_empty[slot], (turn ^ 1) & 1, a.status)) {
@@ -367,6 +426,7 @@ __device__ void kv_role(Shared& sh, const PromptArgs& a, const Plan& p, const CU
                 turn ^= 1;
             }
         }
+        if (lane == 0) mbar_arrive(&sh.kv_started);
     }
     // After a wait that gave up nobody has waited for the last copies in flight.
     if (*reinterpret_cast<volatile int*>(&sh.dead)) {
@@ -374,54 +434,78 @@ __device__ void kv_role(Shared& sh, const PromptArgs& a, const Plan& p, const CU
         for (int s = 0; s < Sh::kSlots; ++s) {
             if (!((used >> s) & 1)) continue;
             // the phase of the slot's last copy
-            if ((landed >> s) & 1) mbar_wait(&sh.kv_land[s], ((land_turn >> s) & 1) ^ 1, 1ll << 24);
-            else mbar_wait(&sh.kv_full[s], s < slot ? turn & 1 : (turn ^ 1) & 1, 1ll << 24);
+            if ((landed >> s) & 1) settle(&sh.kv_land[s], ((land_turn >> s) & 1) ^ 1);
+            else settle(&sh.kv_full[s], s < slot ? turn & 1 : (turn ^ 1) & 1);
         }
     }
 }
 
+// Finds this CTA's items and copies their queries.  An item is claimed when the copies of
+// the keys and values of the one before have been started: early enough for its own to
+// follow those, and no earlier, so that the CTAs end together.
 template <int D>
 __device__ void q_role(Shared& sh, const PromptArgs& a, const Plan& p, const CUtensorMap* map_q, uint32_t q_smem, int lane)
 {
-    int count = 0;
+    int count = 0;                                 // items with queries
     bool ok = !a.starve;
-    Deal deal;
-    for (deal.start(); ok && deal.x < (long long)sh.total * a.Hkv; deal.next()) {
-        const Item it = item_at(sh, a, p, deal.x);
-        if (it.tiles() == 0) continue;
-        if (count > 0 && !wait(sh, &sh.q_empty, (uint32_t)(count - 1) & 1, a.status)) break;
+    const long long total = (long long)sh.total * a.Hkv;
+    long long x = blockIdx.x;
+#pragma unroll 1
+    for (int n = 0;; ++n) {
+        const int at = n % kItems;
+        Item it = {};
+        if (x < total) it = item_at<D>(sh, a, p, x);
+        else it.hk = -1;
+        if (n >= kItems && !wait_item(sh, &sh.item_empty[at], (uint32_t)(n / kItems - 1) & 1, a.status)) break;
         if (lane == 0) {
-            const int nt = it.cnt[1] > 0 ? 2 : 1;
-            mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(nt * p.rows * D * 2));
-            for (int i = 0; i < nt; ++i)
-#pragma unroll
-                for (int h = 0; h < D / 64; ++h)
-                    tma_load_3d(q_smem + (uint32_t)(i * 128 * D * 2 + h * (128 * 128)), map_q, h * 64, it.hk * a.G,
-                                it.q0 + it.t0 + i * p.tok, &sh.q_full);
+            sh.item[at] = it;
+            mbar_arrive(&sh.item_full[at]);
         }
         __syncwarp();
-        ++count;
+        if (it.hk < 0) break;
+        if (it.tiles() > 0 && ok && (count == 0 || (ok = wait(sh, &sh.q_empty, (uint32_t)(count - 1) & 1, a.status)))) {
+            if (lane == 0) {
+                const int nt = it.cnt[1] > 0 ? 2 : 1;
+                mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(nt * p.rows * D * 2));
+                for (int i = 0; i < nt; ++i)
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h)
+                        tma_load_3d(q_smem + (uint32_t)(i * 128 * D * 2 + h * (128 * 128)), map_q, h * 64, it.hk * a.G,
+                                    it.q0 + it.t0 + i * p.tok, &sh.q_full);
+            }
+            __syncwarp();
+            ++count;
+        }
+        if (a.counter) {
+            wait_item(sh, &sh.kv_started, (uint32_t)n & 1, a.status);
+            uint32_t c = 0;
+            if (lane == 0) c = atomicAdd(a.counter, 1u);
+            x = (long long)gridDim.x + __shfl_sync(0xffffffffu, c, 0);
+        } else {
+            x = (n + 1ll) * gridDim.x + ((n & 1) ? blockIdx.x : gridDim.x - 1 - blockIdx.x);       // to and fro
+        }
     }
-    if (count > 0 && *reinterpret_cast<volatile int*>(&sh.dead)) mbar_wait(&sh.q_full, (uint32_t)(count - 1) & 1, 1ll << 24);
+    if (count > 0 && *reinterpret_cast<volatile int*>(&sh.dead)) settle(&sh.q_full, (uint32_t)(count - 1) & 1);
 }
 
 // Looks through the tiles of values on the items' edges.  A lane has every 32nd row of
 // a tile: x * 0 added up is NaN where some x is an infinity or NaN.
 template <int D>
-__device__ void scan_role(Shared& sh, const PromptArgs& a, const Plan& p, uint32_t slots, int lane)
+__device__ void scan_role(Shared& sh, const PromptArgs& a, uint32_t slots, int lane)
 {
     using Sh = Shape<D>;
     int entry = 0;                                 // ring entries before this item
     int tile = 0;                                  // key tiles before this item
     uint32_t turn = 0;                             // of the landing barriers, bits by slot
-    Deal deal;
-    for (deal.start(); deal.x < (long long)sh.total * a.Hkv; deal.next()) {
-        const Item it = item_at(sh, a, p, deal.x);
+    bool ok = true;
+    Items items;
+    for (const Item* at; (at = items.next(sh, a.status)); items.release(sh, lane)) {
+        const Item it = *at;
         const int cnt = it.tiles();
 #pragma unroll 1
-        for (int j = it.all / KT; j < cnt; ++j) {
+        for (int j = it.all / KT; ok && j < cnt; ++j) {
             const int slot = (entry + 2 * j + 1) % Sh::kSlots;
-            if (!wait(sh, &sh.kv_land[slot], (turn >> slot) & 1, a.status)) return;
+            if (!(ok = wait(sh, &sh.kv_land[slot], (turn >> slot) & 1, a.status))) break;
             turn ^= 1u << slot;
             const uint32_t base = slots + (uint32_t)slot * Sh::kSlotBytes;
             bool wrote = false;
@@ -454,6 +538,7 @@ __device__ void scan_role(Shared& sh, const PromptArgs& a, const Plan& p, uint32
                 }
                 const uint32_t bits = __ballot_sync(0xffffffffu, nan);
                 if (lane == 0) sh.bad[(tile + j) % kRingMeta][b] = bits;
+                if (lane == 0 && bits) sh.bad_tile = tile + j + 1;
             }
             if (wrote) fence_proxy_async_smem();
             __syncwarp();
@@ -526,15 +611,15 @@ __device__ __forceinline__ void commit_if(uint64_t* bar, bool ok)
 // order).  Once a wait has given up no product is issued and nothing signalled any
 // more; that is a predicate, so that the loops have one way out.
 template <int D>
-__device__ void mma_role(Shared& sh, const PromptArgs& a, const Plan& p, uint32_t q_smem, uint32_t slots, uint32_t tmem)
+__device__ void mma_role(Shared& sh, const PromptArgs& a, uint32_t q_smem, uint32_t slots, uint32_t tmem, int lane)
 {
     using Sh = Shape<D>;
     constexpr uint32_t id_qk = make_idesc_bf16(128, KT, false, false);
     constexpr uint32_t id_pv = make_idesc_bf16(128, D, false, true);
     int slot = 0;                                  // of the next ring entry to take
     uint32_t turn = 0;                             // parity of its use
-    int done[2] = {0, 0};                          // tiles of the items before, by row tile
-    int pieces[2] = {0, 0}, items = 0;             // items before with work, by row tile and in all
+    int done0 = 0, done1 = 0;                      // tiles of the items before, by row tile
+    int pieces0 = 0, pieces1 = 0, some = 0;        // items before with work, by row tile and in all
     bool ok = true;                                // no wait of this lane has given up
     const uint64_t q_desc = make_sdesc(q_smem, 16, 1024, kSwizzle128B);
     auto take = [&]() {
@@ -548,12 +633,12 @@ __device__ void mma_role(Shared& sh, const PromptArgs& a, const Plan& p, uint32_
         }
         return mine;
     };
-    Deal deal;
-    for (deal.start(); deal.x < (long long)sh.total * a.Hkv; deal.next()) {
-        const Item it = item_at(sh, a, p, deal.x);
+    Items items;
+    for (const Item* at; (at = items.next(sh, a.status)); items.release(sh, lane)) {
+        const Item it = *at;
         const int cnt = it.tiles();
         if (cnt == 0) continue;
-        ok &= wait_lane(sh, &sh.q_full, (uint32_t)items & 1, a.status);
+        ok &= wait_lane(sh, &sh.q_full, (uint32_t)some & 1, a.status);
 #pragma unroll 1
         for (int j = -1; j < cnt; ++j) {
             // V of tile j, then K of tile j + 1
@@ -562,23 +647,25 @@ __device__ void mma_role(Shared& sh, const PromptArgs& a, const Plan& p, uint32_
             int ek = -1;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (j >= 0 && j < it.cnt[i]) {
+                const int tiles = i ? it.cnt[1] : it.cnt[0];
+                const uint32_t sc = tmem + i * 128;
+                if (j >= 0 && j < tiles) {
                     const uint32_t v = slots + (uint32_t)ev * Sh::kSlotBytes;
                     const uint64_t v_desc = make_sdesc(v, KT * 128, 1024, kSwizzle128B);
-                    const uint32_t o = tmem + Sh::kO + i * D, s = tmem + i * 128;
-                    ok &= wait_lane(sh, &sh.p_full[i], (uint32_t)(done[i] + j) & 1, a.status);
-                    if (j == 0 && pieces[i] > 0) ok &= wait_lane(sh, &sh.o_empty[i], (uint32_t)(pieces[i] - 1) & 1, a.status);
+                    const uint32_t o = tmem + Sh::kO + i * D;
+                    ok &= wait_lane(sh, &sh.p_full[i], (uint32_t)((i ? done1 : done0) + j) & 1, a.status);
+                    const int before = i ? pieces1 : pieces0;
+                    if (j == 0 && before > 0) ok &= wait_lane(sh, &sh.o_empty[i], (uint32_t)(before - 1) & 1, a.status);
                     __syncwarp();
                     tc_fence_after();
-                    issue_pv(o, s, v_desc, id_pv, j > 0, ok);
-                    issue_pv(o, s + 64, v_desc + 512, id_pv, 1, ok);
+                    issue_pv(o, sc, v_desc, id_pv, j > 0, ok);
+                    issue_pv(o, sc + 64, v_desc + 512, id_pv, 1, ok);
                     commit_if(&sh.pv_done[i], ok);
                 }
-                if (j + 1 < it.cnt[i]) {
+                if (j + 1 < tiles) {
                     if (ek < 0) ek = take();
                     const uint32_t k = slots + (uint32_t)ek * Sh::kSlotBytes;
-                    issue_qk<D>(tmem + i * 128, q_desc + (uint64_t)(i * 128 * D * 2 / 16), make_sdesc(k, 16, 1024, kSwizzle128B),
-                                id_qk, ok);
+                    issue_qk<D>(sc, q_desc + (uint64_t)(i * 128 * D * 2 / 16), make_sdesc(k, 16, 1024, kSwizzle128B), id_qk, ok);
                     commit_if(&sh.s_full[i], ok);
                 }
             }
@@ -586,22 +673,81 @@ __device__ void mma_role(Shared& sh, const PromptArgs& a, const Plan& p, uint32_
             if (more) commit_if(&sh.kv_empty[ek], ok);
             if (j + 2 == cnt) commit_if(&sh.q_empty, ok);
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            done[i] += it.cnt[i];
-            pieces[i] += it.cnt[i] > 0;
-        }
-        ++items;
+        done0 += it.cnt[0];
+        done1 += it.cnt[1];
+        pieces0 += it.cnt[0] > 0;
+        pieces1 += it.cnt[1] > 0;
+        ++some;
     }
     // the last products and their arrivals on the ring's barriers come before the block ends
     mma_commit(&sh.done);
-    mbar_wait(&sh.done, 0);
+    wait_for<false>(sh, &sh.done, 0, a.status);
     __syncwarp();
 }
 
 // --------------------------------------------------- the softmax and the output
+// Adds to O the infinities and NaN of the keys before `lim` that the scanning warp has
+// taken out.
 template <int D>
-__device__ void softmax_role(Shared& sh, const PromptArgs& a, const Plan& p, int warp, int lane, uint32_t tmem)
+__device__ __forceinline__ void add_nonfinite(Shared& sh, const PromptArgs& a, const Item& it, int tile, int lim, int half, uint32_t to)
+{
+    constexpr int H = D / 2;
+#pragma unroll 1
+    for (int c = 0; c < H / 16; ++c) {
+        uint32_t y[16];
+        tmem_ld16(to + 16 * c, y);
+        tmem_ld_wait();
+#pragma unroll 1
+        for (int k = it.all / KT * KT; k < lim; ++k) {
+            if (!((sh.bad[(tile + k / KT) % kRingMeta][(k >> 5) & 3] >> (k & 31)) & 1)) continue;
+            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + (long long)(it.k0 + k) * a.v_stride + it.hk * D +
+                                     half * H + 16 * c;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float z = __bfloat162float(v[e]);
+                if (!(fabsf(z) < INFINITY)) y[e] = __float_as_uint(__uint_as_float(y[e]) + z);
+            }
+        }
+        __syncwarp();
+        tmem_st16(to + 16 * c, y);
+    }
+    tmem_st_wait();
+}
+
+// A warp's 32 rows of H channels, a lane's row packed in z, to memory: through 1 KB
+// of shared memory, so that a store covers whole rows.  (Stored by each lane as
+// they are, 16 bytes to each of 32 lines at a time, an item's rows held up every
+// access to shared memory of the CTA for some 4,000 clocks.)
+template <int H>
+__device__ __forceinline__ void store_rows(const uint32_t (&z)[H / 2], int place, uint4* base, uint32_t stage, int lane)
+{
+    constexpr int L = H / 8;                       // 16-byte pieces, and lanes, of a row
+    constexpr int R = 1024 / (H * 2);              // rows at a time
+    const auto at = [&](int row, int c) { return stage + row * (H * 2) + ((c ^ (H == 64 ? row & 7 : (row >> 1) & 3)) << 4); };
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += R) {
+        __syncwarp();
+        if (lane >= r0 && lane < r0 + R) {
+#pragma unroll
+            for (int c = 0; c < L; ++c)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(lane - r0, c)), "r"(z[4 * c]), "r"(z[4 * c + 1]),
+                             "r"(z[4 * c + 2]), "r"(z[4 * c + 3])
+                             : "memory");
+        }
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < R * L / 32; ++q) {
+            const int row = q * (32 / L) + lane / L;
+            const int to = __shfl_sync(0xffffffffu, place, r0 + row);
+            uint4 w;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at(row, lane % L)));
+            if (to >= 0) base[to + lane % L] = w;
+        }
+    }
+}
+
+template <int D>
+__device__ void softmax_role(Shared& sh, const PromptArgs& a, const Plan& p, uint32_t stage, int warp, int lane, uint32_t tmem)
 {
     using Sh = Shape<D>;
     constexpr float kSlack = 8.f;
@@ -611,20 +757,17 @@ __device__ void softmax_role(Shared& sh, const PromptArgs& a, const Plan& p, int
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = lanes + i * 128 + half * 64, to = lanes + Sh::kO + i * D + half * H;
     const uint32_t bar = 1 + i * 4 + (warp & 3);   // named barrier of the two warps of these rows
-    const int tok = r / a.G, g = r - tok * a.G;
-    const bool row = r < p.rows;
+    const int tok = r < p.rows ? r / a.G : 1 << 29, g = r < p.rows ? r - tok * a.G : 0;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     int done = 0;                                  // tiles before, of this row tile
     int tile = 0;                                  // key tiles before
-    Deal deal;
-    for (deal.start(); deal.x < (long long)sh.total * a.Hkv; deal.next()) {
-        const Item it = item_at(sh, a, p, deal.x);
-        const int cnt = i ? it.cnt[1] : it.cnt[0];
-        const int t = it.t0 + i * p.tok + tok;     // this row's token
-        const bool mine = row && t < it.lq;
-        const int lim = mine ? min(max(t + it.lk - it.lq + 1, 0), it.lk) : 0;
-        // the keys that every row of the tile sees
-        const int all = min(max(it.t0 + i * p.tok + it.lk - it.lq + 1, 0), it.lk);
+    Items items;
+    for (const Item* at; (at = items.next(sh, a.status)); items.release(sh, lane)) {
+        const Item& it = *at;                      // (in shared memory)
+        const int cnt = it.cnt[i];
+        const int first = it.t0 + i * p.tok, off = it.lk - it.lq + 1;
+        const int lim = first + tok < it.lq ? min(max(first + tok + off, 0), it.lk) : 0;   // keys that this row sees
+        const int all = min(max(first + off, 0), it.lk);   // and those that every row of the tile sees
         float m = -INFINITY, l = 0.f;
 #pragma unroll 1
         for (int j = 0; j < cnt; ++j) {
@@ -692,84 +835,50 @@ __device__ void softmax_role(Shared& sh, const PromptArgs& a, const Plan& p, int
             float s0, s1;
             unpack2(add2(sum[0], sum[1]), s0, s1);
             l += s0 + s1;
+            if (j + 1 == cnt) sh.sum[i][half][r] = l;
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_full[i]);
         }
         // the output
-        __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.o) +
-                            ((long long)(it.q0 + (mine ? t : 0)) * a.Hq + (long long)it.hk * a.G + g) * D + half * H;
-        if (cnt == 0) {
-            if (mine) {
-#pragma unroll
-                for (int c = 0; c < H / 8; ++c) *(reinterpret_cast<uint4*>(op) + c) = make_uint4(0, 0, 0, 0);
-            }
-        } else {
-            sh.sum[i][half][r] = l;
+        float scale_o = 0.f;
+        if (cnt > 0) {
             wait_lane(sh, &sh.pv_done[i], (uint32_t)(done + cnt - 1) & 1, a.status);
-            named_bar_sync(bar, 64);
+            __syncwarp();
             tc_fence_after();
-            l += sh.sum[i][half ^ 1][r];
+            l += sh.sum[i][half ^ 1][r];           // (written before the last product began)
             // when some wait has given up, this item and those after it are not known
             if (*reinterpret_cast<volatile int*>(&sh.dead)) l = __int_as_float(0x7fffffff);
-            const float scale_o = lim == 0 ? 0.f : 1.f / l;
-            // keys with an infinity or NaN that this row sees
-            bool any = false;
-#pragma unroll 1
-            for (int j = it.all / KT; j < cnt; ++j) {
-                const uint32_t* bad = sh.bad[(tile + j) % kRingMeta];
-                any |= (bad[0] | bad[1] | bad[2] | bad[3]) != 0;
-            }
-            if (any) {
-#pragma unroll 1
-                for (int c = 0; c < H / 16; ++c) {
-                    uint32_t y[16];
-                    tmem_ld16(to + 16 * c, y);
-                    tmem_ld_wait();
-#pragma unroll 1
-                    for (int k = it.all / KT * KT; k < min(lim, cnt * KT); ++k) {
-                        if (!((sh.bad[(tile + k / KT) % kRingMeta][(k >> 5) & 3] >> (k & 31)) & 1)) continue;
-                        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) +
-                            (long long)(it.k0 + k) * a.v_stride + it.hk * D + half * H + 16 * c;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float z = __bfloat162float(v[e]);
-                            if (!(fabsf(z) < INFINITY)) y[e] = __float_as_uint(__uint_as_float(y[e]) + z);
-                        }
-                    }
-                    __syncwarp();
-                    tmem_st16(to + 16 * c, y);
-                }
-                tmem_st_wait();
-            }
-#pragma unroll 1
-            for (int c = 0; c < H / 32; ++c) {
-                uint32_t y[32];
-                tmem_ld32(to + 32 * c, y);
-                tmem_ld_wait();
-                if (c + 1 == H / 32) {             // the last columns are in registers
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.o_empty[i]);
-                }
-                if (mine) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t z[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            z[k] = pack_bf16x2(__uint_as_float(y[e + 2 * k]) * scale_o, __uint_as_float(y[e + 2 * k + 1]) * scale_o);
-                        *reinterpret_cast<uint4*>(op + 32 * c + e) = lim == 0 ? make_uint4(0, 0, 0, 0) : make_uint4(z[0], z[1], z[2], z[3]);
-                    }
-                }
-                __syncwarp();                      // before the next collective load
-            }
+            scale_o = lim == 0 ? 0.f : __fdividef(1.f, l);
+            if (*reinterpret_cast<volatile int*>(&sh.bad_tile) > tile)
+                add_nonfinite<D>(sh, a, it, tile, min(lim, cnt * KT), half, to);
         }
+        // this row's place, in 16-byte pieces from the item's first row; negative: none
+        const int place = first + tok < it.lq ? ((i * p.tok + tok) * a.Hq + g) * (D / 8) + half * (H / 8) : -1;
+        uint4* base = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) +
+                                               ((long long)(it.q0 + it.t0) * a.Hq + (long long)it.hk * a.G) * D);
         done += cnt;
         tile += it.tiles();
+        uint32_t z[H / 2];
+#pragma unroll
+        for (int c = 0; c < H / 32; ++c) {
+            uint32_t y[32];
+            tmem_ld32(to + 32 * c, y);             // (of no keys: whatever is there; all rows are 0 then)
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                z[16 * c + e] = lim == 0 ? 0u : pack_bf16x2(__uint_as_float(y[2 * e]) * scale_o, __uint_as_float(y[2 * e + 1]) * scale_o);
+        }
+        if (cnt > 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.o_empty[i]);
+        }
+        store_rows<H>(z, place, base, stage, lane);
     }
 }
+
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -792,6 +901,11 @@ prompt_attention_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_co
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.done, 1);
+        mbar_init(&sh.kv_started, 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&sh.item_full[i], 1);
+            mbar_init(&sh.item_empty[i], kItemReaders);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_full[i], 8);
@@ -799,6 +913,7 @@ prompt_attention_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_co
             mbar_init(&sh.o_empty[i], 8);
         }
         sh.dead = 0;
+        sh.bad_tile = 0;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -812,13 +927,13 @@ prompt_attention_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_co
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
     if (warp < kMmaWarp) {
         more_registers<kMore>();
-        softmax_role<D>(sh, a, p, warp, lane, tmem);
+        softmax_role<D>(sh, a, p, slots + Sh::kSlots * Sh::kSlotBytes + warp * Sh::kStageBytes, warp, lane, tmem);
     } else {
         fewer_registers<kFewer>();
-        if (warp == kMmaWarp) mma_role<D>(sh, a, p, q_smem, slots, tmem);
-        else if (warp == kKvWarp) kv_role<D>(sh, a, p, &map_k, &map_v, slots, lane);
+        if (warp == kMmaWarp) mma_role<D>(sh, a, q_smem, slots, tmem, lane);
+        else if (warp == kKvWarp) kv_role<D>(sh, a, &map_k, &map_v, slots, lane);
         else if (warp == kQWarp) q_role<D>(sh, a, p, &map_q, q_smem, lane);
-        else scan_role<D>(sh, a, p, slots, lane);
+        else scan_role<D>(sh, a, slots, lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -847,7 +962,7 @@ bool make_map(CUtensorMap* m, const void* base, int d, int heads, long long rows
 }
 
 template <int D>
-cudaError_t launch(const PromptArgs& a, int sms, cudaStream_t stream)
+cudaError_t launch(PromptArgs a, int sms, cudaStream_t stream)
 {
     Plan p;
     p.tok = 128 / a.G;
@@ -862,6 +977,12 @@ cudaError_t launch(const PromptArgs& a, int sms, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     // every sequence has at most one pair of row tiles that is not full
     const long long items = ((long long)a.T / (2 * p.tok) + a.N) * a.Hkv;
+    if (items > 2ll * sms) {
+        const cudaError_t z = cudaMemsetAsync(a.counter, 0, sizeof(uint32_t), stream);
+        if (z != cudaSuccess) return z;
+    } else {
+        a.counter = nullptr;
+    }
     kern<<<(unsigned)(items < sms ? items : sms), kThreads, bytes, stream>>>(a, p, map_q, map_k, map_v);
     return cudaGetLastError();
 }
@@ -870,7 +991,9 @@ cudaError_t launch(const PromptArgs& a, int sms, cudaStream_t stream)
 
 bool prompt_tc_supported(const PromptArgs& a, int32_t d, kda_dtype_t dtype)
 {
-    return dtype == KDA_BF16 && (d == 64 || d == 128) && a.scale_log2 > 0.f && a.G <= 128 && a.Tk > 0 &&
+    // (an item takes a microsecond per 128 keys, and no wait more than two seconds)
+    return dtype == KDA_BF16 && (d == 64 || d == 128) && a.scale_log2 > 0.f && a.G <= 128 && a.Tk > 0 && a.Tk <= (1 << 27) &&
+           a.T <= (1 << 27) &&
            getenv("KDA_FORCE_SIMT") == nullptr;
 }
 

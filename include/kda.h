@@ -569,6 +569,12 @@ kda_status_t kda_cache_append(const void *k, const void *v,
  * * 2^e reaches its largest magnitude, 0 when it has only zeros, NaN (and bytes 0)
  * when it has an infinity or NaN.  page_stride counts bytes here. */
 
+/* Bytes of device workspace kda_prompt_attention needs; 0 for arguments that it
+ * refuses. */
+size_t kda_prompt_attention_workspace_bytes(int32_t num_seqs, int32_t Hq,
+                                            int32_t Hkv, int32_t d,
+                                            kda_dtype_t dtype);
+
 /* Causal softmax attention over packed sequences: with Lq and Lk rows of queries
  * and keys in a sequence, query i sees its keys 0 .. i + Lk - Lq, so that the
  * queries are the sequence's last (Lk = Lq: a whole prompt; Lk > Lq: its rest
@@ -582,15 +588,17 @@ kda_status_t kda_cache_append(const void *k, const void *v,
  *   o             (written) rows that cu_seqlens gives to no sequence keep what they
  *                 hold; must not overlap the inputs.  Rows before 0 or past the last
  *                 do not exist; of sequences that claim the same row one gets it.
- *   status        device int32 or NULL: bit 1 is set when a wait of the tensor-core
- *                 kernel has given up (after some two seconds; never cleared).  The
- *                 rows of o that depended on it are NaN.
+ *   workspace     kda_prompt_attention_workspace_bytes(...) bytes, 256-byte aligned,
+ *                 not shared with concurrent calls; contents on entry do not matter.
+ *                 Bit 1 of the int32 at byte 8 is set when a wait of the tensor-core
+ *                 kernel has given up (after some two seconds), which no call
+ *                 clears; the rows of o that depended on it are NaN.
  * dtype is that of q, k, v, and of o.  KDA_BF16 with d = 64 or 128, scale > 0 and
  * Hq / Hkv <= 128 runs on the tensor cores, with probabilities rounded to bf16 for
  * the second product; everything else, and everything when the environment variable
  * KDA_FORCE_SIMT is set, on the CUDA cores in fp32.  An infinity or NaN in a
- * row of k or v reaches the queries that see it and no others.  No atomics: the
- * result does not depend on timing. */
+ * row of k or v reaches the queries that see it and no others.  The result does not
+ * depend on timing. */
 kda_status_t kda_prompt_attention(const void *q, const void *k, const void *v,
                                   int64_t q_stride, int64_t k_stride,
                                   int64_t v_stride, const int32_t *cu_seqlens,
@@ -598,7 +606,8 @@ kda_status_t kda_prompt_attention(const void *q, const void *k, const void *v,
                                   int64_t total_tokens, int64_t total_keys,
                                   int32_t Hq, int32_t Hkv, int32_t d,
                                   kda_dtype_t dtype, float scale, void *o,
-                                  int32_t *status, cudaStream_t stream);
+                                  void *workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
 
 /* Rows of a packed batch (a prefill, or one token per sequence) turned to their
  * positions and into a cache: row i of sequence n has position p = lengths[n] + i.

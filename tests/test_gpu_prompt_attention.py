@@ -227,3 +227,25 @@ def test_kernels_agree(kda, monkeypatch):
     ref, mag = prompt_reference(*parts, cu)
     check(tc, ref, mag, exact_p=False)
     check(simt, ref, mag, exact_p=False)
+
+
+def test_waits_that_give_up(kda, monkeypatch):
+    # the copying warps exit at once: the kernel's waits run out (about 2 s), it returns, sets
+    # the workspace's word and marks its rows, and the next call is right
+    cu = starts([700, 0, 90, 20])
+    parts, _ = inputs(815, 815, 8, 2, 128, BF16, seed=16)
+    a, c = on_gpu(parts, None), i32(cu)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    status = ws[8:12].view(torch.int32)
+    o = torch.full(a[0].shape, 5.0, dtype=BF16, device="cuda")
+    monkeypatch.setenv("KDA_TEST_STARVE_CONSUMERS", "1")
+    kda.kda_prompt_attention(*a, c, o=o, workspace=ws)
+    torch.cuda.synchronize()
+    monkeypatch.delenv("KDA_TEST_STARVE_CONSUMERS")
+    assert status.item() & 2
+    assert torch.isnan(o[:810]).all() and torch.all(o[810:] == 5)
+    status.zero_()
+    kda.kda_prompt_attention(*a, c, o=o, workspace=ws)
+    ref, mag = prompt_reference(*parts, cu, o=torch.full(a[0].shape, 5.0))
+    check(o, ref, mag, exact_p=False)
+    assert status.item() == 0

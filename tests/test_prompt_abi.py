@@ -20,7 +20,7 @@ def lib():
 
 def prompt(lib, **kw):
     args = dict(q=A, k=A * 16, v=A * 32, qs=512, ks=128, vs=128, cu=A * 64, cuk=NULL, N=2, T=10, Tk=10, Hq=8, Hkv=2,
-                d=64, dt=BF16, scale=0.1, o=A * 65, status=NULL, stream=NULL)
+                d=64, dt=BF16, scale=0.1, o=A * 65, ws=A * 256, wsb=256, stream=NULL)
     args.update(kw)
     return lib.kda_prompt_attention(*args.values())
 
@@ -30,13 +30,22 @@ def prompt(lib, **kw):
     (dict(Hq=1), BAD), (dict(Hq=0), BAD), (dict(T=-1), BAD), (dict(Tk=-1), BAD), (dict(T=1 << 31, Tk=1 << 31), BAD),
     (dict(Tk=11), BAD), (dict(cu=NULL), BAD), (dict(cu=NULL, cuk=A, N=1), BAD), (dict(q=NULL), BAD),
     (dict(k=NULL), BAD), (dict(v=NULL), BAD), (dict(o=NULL), BAD), (dict(q=A + 8), BAD), (dict(v=A * 32 + 2), BAD),
-    (dict(o=A * 65 + 8), BAD), (dict(cu=A * 64 + 2), BAD), (dict(status=A + 1), BAD), (dict(qs=511), BAD),
+    (dict(o=A * 65 + 8), BAD), (dict(cu=A * 64 + 2), BAD), (dict(qs=511), BAD),
     (dict(qs=516), BAD), (dict(ks=120), BAD), (dict(vs=-128), BAD), (dict(qs=1 << 60), BAD), (dict(o=A), BAD), (dict(o=A * 16 + 1024), BAD),
     (dict(o=A * 64 - 16), BAD), (dict(Hkv=1 << 17, Hq=1 << 17, ks=1 << 23, vs=1 << 23, qs=1 << 23), BAD),
     (dict(Hq=1 << 20, Hkv=1, qs=1 << 26), BAD),
+    (dict(ws=NULL), WORKSPACE), (dict(wsb=255), WORKSPACE), (dict(ws=A * 256 + 128), WORKSPACE),
+    (dict(ws=A * 65), BAD), (dict(ws=A * 32), BAD), (dict(ws=A + 256), BAD),
 ])
 def test_prompt_attention_rejects(lib, kw, code):
     assert prompt(lib, **kw) == code
+
+
+def test_prompt_attention_workspace(lib):
+    size = kda.kda_prompt_attention_workspace_bytes
+    for bad in ((0, 8, 2, 64, BF16), (2, 7, 2, 64, BF16), (2, 8, 2, 48, BF16), (2, 8, 2, 64, 5), (1, 1 << 17, 1 << 17, 16, BF16)):
+        assert size(*bad) == 0
+    assert size(1, 8, 2, 64, BF16) == 256
 
 
 def test_prompt_attention_of_no_rows_is_nothing_to_do(lib):
