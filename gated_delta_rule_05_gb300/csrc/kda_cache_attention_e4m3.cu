@@ -21,12 +21,26 @@
 // lie in the ring so that the 16-byte reads below find all banks.
 //
 // The work is cut into equal ranges as for the tree attention (kda_tree.cuh).
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
+#include <stdio.h>
 
 #include "kda_prompt.cuh"
+#include "kda_sm100.cuh"
 
 namespace kda {
+
+// The driver's tensor-map encoder (kda_prefill_tc.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn();
+
 namespace {
+
+using sm100::fence_mbar_init;
+using sm100::fence_proxy_async_smem;
+using sm100::mbar_arrive;
+using sm100::mbar_arrive_expect_tx;
+using sm100::mbar_init;
+using sm100::mbar_try_wait;
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kKeys = 16;                          // of a warp's step
@@ -219,8 +233,17 @@ __device__ __forceinline__ void start_copies(const E4m3Args& a, const Walk& k, u
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void load4(const float* p, float (&x)[4])
+{
+    const float4 w = __ldg(reinterpret_cast<const float4*>(p));
+    x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4])
+{
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+    x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
 
 // The channel of word s (4 channels) that lane i of a row's four holds.
 template <int D>
@@ -273,12 +296,14 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
             float x[KS][4];
             uint32_t top = 0;
 #pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                x[s][0] = x[s][1] = x[s][2] = x[s][3] = 0.f;
+                if (mine) load4(qp + q_channel<D>(s, i4), x[s]);
+            }
+#pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[s][j] = mine ? to_float(qp[q_channel<D>(s, i4) + j]) : 0.f;
-                    top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
-                }
+                for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             int e = 14 + 127 - (int)(top >> 23);   // the largest magnitude becomes 2^14 or a little more
@@ -498,13 +523,509 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// ------------------------------------------- whole groups of 16 rows, one scale each
+// The same where 16 rows from a multiple of 16 on lie in one page and one block of
+// scales: a warp's step is two such groups (32 keys), each of whose keys and values come
+// as one TMA box, with one scale, so that s = (c ks) S is one factor per row and
+// group and the step has half the instructions per key.  The pages' boxes come in the
+// swizzle of their row size, which is that of row_at above.
+constexpr int kStepGroups = 2;
+constexpr int kGroupKT = kWarps * kStepGroups * kKeys;
+constexpr int kGroupLead = 2;
+constexpr int kSlots = 6;                          // groups of a warp's ring
+using GroupPiece = TreePieces<kGroupKT, kGroupLead>;
+
+template <int D>
+struct GroupShape {
+    static constexpr int kSlotBytes = 2 * kKeys * D;
+    static constexpr int kRing = kWarps * kSlots * kSlotBytes;
+    static constexpr int kFrag = 32 * (D / 2);     // floats of a warp's O
+    static constexpr int kJoin = kWarps / 2 * (kFrag + 3 * kRows) * 4;
+    static constexpr size_t kBytes = 1024 + kRing + kJoin;
+};
+
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int h, int row, int page, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(h), "r"(row), "r"(page), "r"(smem_at(bar))
+        : "memory");
+}
+
+// The walk of a warp's copies, a step at a time; the page numbers of a step are loaded
+// when it is entered, one before they are used.
+struct GroupWalk {
+    GroupPiece w;
+    bool go;
+    int t, pos, p, slot;
+    int page[kStepGroups];
+
+    __device__ __forceinline__ void look_up(const E4m3Args& a)
+    {
+#pragma unroll
+        for (int i = 0; i < kStepGroups; ++i) {
+            page[i] = -1;
+            const bool over = slot + i * kKeys >= a.split.page_size;
+            if (go && pos + i * kKeys < w.ctx)
+                page[i] = __ldg(a.split.page_table + (long long)w.n * a.split.max_pages + p + (over ? 1 : 0));
+        }
+    }
+    __device__ __forceinline__ void enter(const E4m3Args& a, int warp)
+    {
+        if (go) {
+            t = w.t0;
+            pos = t * kGroupKT + warp * (kStepGroups * kKeys);
+            p = pos / a.split.page_size;
+            slot = pos - p * a.split.page_size;
+        }
+        look_up(a);
+    }
+    __device__ __forceinline__ void step(const E4m3Args& a, int warp)
+    {
+        if (!go) return;
+        if (++t == w.t1) {
+            go = w.next(a.split);
+            enter(a, warp);
+            return;
+        }
+        pos += kGroupKT;
+        p += a.tile_pages;
+        slot += a.tile_rows;
+        if (slot >= a.split.page_size) {
+            slot -= a.split.page_size;
+            ++p;
+        }
+        look_up(a);
+    }
+};
+
+struct GroupShared {
+    uint64_t full[kWarps][kSlots];
+    int scale[kWarps][kSlots];                     // of a group: the place of its scales; -1: no rows
+    long long loc[kWarps + 2];
+    int dead;
+};
+
+// Starts the copies of the walk's step into two slots.  What no row fills is zeros.
+template <int D>
+__device__ __forceinline__ void start_groups(GroupShared& sh, const E4m3Args& a, const CUtensorMap* map_k,
+                                             const CUtensorMap* map_v, const GroupWalk& k, uint32_t ring, int first, int warp,
+                                             int lane)
+{
+    if (!k.go) return;
+#pragma unroll
+    for (int i = 0; i < kStepGroups; ++i) {
+        const int at = first + i;
+        const uint32_t dst = ring + at * GroupShape<D>::kSlotBytes;
+        int row = k.slot + i * kKeys;
+        if (row >= a.split.page_size) row -= a.split.page_size;
+        if (k.page[i] >= 0 && k.page[i] < a.num_pages) {
+            if (lane == 0) {
+                const int b = a.block == 1 ? row : (int)__umulhi((uint32_t)row, a.block_magic);
+                sh.scale[warp][at] = (k.page[i] * a.blocks + b) * a.split.Hkv + k.w.hk;
+                mbar_arrive_expect_tx(&sh.full[warp][at], 2 * kKeys * D);
+                load_box(dst, map_k, k.w.hk, row, k.page[i], &sh.full[warp][at]);
+                load_box(dst + kKeys * D, map_v, k.w.hk, row, k.page[i], &sh.full[warp][at]);
+            }
+        } else {
+#pragma unroll 1
+            for (int e = lane; e < 2 * kKeys * D / 16; e += 32)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + e * 16), "r"(0) : "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                sh.scale[warp][at] = -1;
+                mbar_arrive(&sh.full[warp][at]);
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// Waits for a group's copies, for about two seconds at most; when a wait has given up
+// the CTA goes on with what is there and marks its rows.
+__device__ __forceinline__ void wait_group(GroupShared& sh, uint64_t* bar, uint32_t parity)
+{
+    if (mbar_try_wait(bar, parity)) return;
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (clock64() - t0 > (1ll << 32) || *reinterpret_cast<volatile int*>(&sh.dead)) {
+            *reinterpret_cast<volatile int*>(&sh.dead) = 1;
+            return;
+        }
+    }
+}
+
+// N neighbouring values, N of one row's channels to a lane.
+template <int N>
+__device__ __forceinline__ void store_run(float* p, const float (&y)[N])
+{
+    if constexpr (N >= 4) {
+#pragma unroll
+        for (int j = 0; j < N; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+    } else {
+        *reinterpret_cast<float2*>(p) = make_float2(y[0], y[1]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_run(__nv_bfloat16* p, const float (&y)[N])
+{
+    uint32_t z[N / 2];
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) z[j] = sm100::pack_bf16x2(y[2 * j], y[2 * j + 1]);
+    if constexpr (N >= 8) {
+#pragma unroll
+        for (int j = 0; j < N / 2; j += 4) *reinterpret_cast<uint4*>(p + 2 * j) = make_uint4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+    } else if constexpr (N == 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(z[0], z[1]);
+    } else {
+        *reinterpret_cast<uint32_t*>(p) = z[0];
+    }
+}
+
+template <class T, class O, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_constant__ CUtensorMap map_k,
+                             const __grid_constant__ CUtensorMap map_v)
+{
+    using Sh = GroupShape<D>;
+    constexpr bool QLO = sizeof(T) == 4, PLO = sizeof(O) == 4;
+    constexpr int KS = D / 16, NT = D / 8;
+    constexpr int KB = D / 4 < 16 ? D / 4 : 16;    // bytes per read of a row of K
+    extern __shared__ __align__(128) uint8_t dyn[];
+    __shared__ GroupShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, i4 = lane & 3;
+    const int group = blockIdx.x / a.split.row_tiles, r0 = (blockIdx.x % a.split.row_tiles) * kRows;
+    if (lane == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&sh.full[warp][i], 1);
+            sh.scale[warp][i] = -1;
+        }
+        if (warp == 0) sh.dead = 0;
+        fence_mbar_init();
+    }
+    const TreeSpot sp = tree_locate<kThreads, kGroupKT, kGroupLead>(a.split, group, sh.loc);   // has block barriers
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    GroupWalk ahead;
+    ahead.go = ahead.w.start(a.split, sp, group);
+    GroupPiece w = ahead.w;
+    bool go = ahead.go;
+    ahead.enter(a, warp);
+    const uint32_t base = (smem_at(dyn) + 1023u) & ~1023u;
+    const uint32_t ring = base + warp * kSlots * Sh::kSlotBytes;
+    float* join = reinterpret_cast<float*>(dyn + (base - smem_at(dyn)) + Sh::kRing);
+    int out = 0;                                   // slot of the next step
+    uint32_t turn = 0;
+#pragma unroll 1
+    for (int i = 0; i < kSlots; i += kStepGroups) {
+        start_groups<D>(sh, a, &map_k, &map_v, ahead, ring, i, warp, lane);
+        ahead.step(a, warp);
+    }
+    // the next step's scales
+    float ks[kStepGroups], vs[kStepGroups];
+    auto load_scales = [&](int first) {
+#pragma unroll
+        for (int i = 0; i < kStepGroups; ++i) {
+            const int at = sh.scale[warp][first + i];
+            ks[i] = at >= 0 ? __ldg(a.k_scales + at) : -1.f;       // (-1: no rows)
+            vs[i] = at >= 0 ? __ldg(a.v_scales + at) : 0.f;
+        }
+    };
+    if (go) load_scales(0);
+    for (; go; go = w.next(a.split)) {
+        // the rows' queries, in fp16 times a power of two (and -1 for a negative scale; 0 for 0)
+        uint32_t qh[KS][4], ql[QLO ? KS : 1][4];
+        float rs[2];
+        int lim[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = r0 + g + 8 * h, t = r / a.G;
+            const bool mine = r < a.R;
+            lim[h] = mine ? w.ctx - a.Ts + t + 1 : 0;
+            const T* qp = static_cast<const T*>(a.q) +
+                          (((long long)w.n * a.Ts + (mine ? t : 0)) * a.Hq + w.hk * a.G + (mine ? r - t * a.G : 0)) * D;
+            float x[KS][4];
+            uint32_t top = 0;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                x[s][0] = x[s][1] = x[s][2] = x[s][3] = 0.f;
+                if (mine) load4(qp + q_channel<D>(s, i4), x[s]);
+            }
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            int e = 14 + 127 - (int)(top >> 23);   // the largest magnitude becomes 2^14 or a little more
+            e = top == 0 ? 0 : min(max(e, -100), 100);
+            float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            rs[h] = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - e) << 23);
+            if (a.scale_log2 < 0.f) up = -up;
+            if (a.scale_log2 == 0.f) up = 0.f, rs[h] = 1.f;
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float u = x[s][2 * j] * up, v = x[s][2 * j + 1] * up;
+                    qh[s][2 * j + h] = two_f16(u, v);
+                    if constexpr (QLO) ql[s][2 * j + h] = two_f16_rest(u, v, qh[s][2 * j + h]);
+                }
+        }
+        const int all = w.ctx - a.Ts + r0 / a.G + 1;           // keys that every row sees
+        float o[NT][4], m[2], n[2], l[2], fac[2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            m[h] = n[h] = -INFINITY;
+            l[h] = fac[h] = 0.f;
+        }
+#pragma unroll 1
+        for (int t = w.t0; t < w.t1; ++t) {
+#pragma unroll
+            for (int i = 0; i < kStepGroups; ++i) wait_group(sh, &sh.full[warp][out + i], turn);
+            __syncwarp();
+            const uint32_t st = ring + out * Sh::kSlotBytes;
+            const float ksn[kStepGroups] = {ks[0], ks[1]}, vsn[kStepGroups] = {vs[0], vs[1]};
+            const int next = out + kStepGroups == kSlots ? 0 : out + kStepGroups;
+            load_scales(next);                     // (of the last step: whatever is there)
+            const int pos = t * kGroupKT + warp * (kStepGroups * kKeys);
+            const bool masked = pos + kStepGroups * kKeys > all || ksn[0] < 0.f || ksn[1] < 0.f;   // (the same for the warp)
+            if (masked && pos + kStepGroups * kKeys > w.ctx) {
+                // values past the last row, whatever the page holds there
+#pragma unroll
+                for (int i = 0; i < kStepGroups; ++i)
+#pragma unroll 1
+                    for (int e = lane; e < kKeys * D / 16; e += 32)
+                        if (pos + i * kKeys + e / (D / 16) >= w.ctx)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(st + i * Sh::kSlotBytes + kKeys * D + e * 16), "r"(0)
+                                         : "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            float c[kStepGroups][2][4];
+#pragma unroll
+            for (int i = 0; i < kStepGroups; ++i)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) c[i][b][j] = 0.f;
+            {
+                Words<KB> kw[kStepGroups][2][D / 4 / KB];
+#pragma unroll
+                for (int h = 0; h < D / 4 / KB; ++h)
+#pragma unroll
+                    for (int i = 0; i < kStepGroups; ++i)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const int at = KB * i4 + 64 * h;
+                            kw[i][b][h] = read_words<KB>(st + i * Sh::kSlotBytes + row_at<D>(8 * b + key_of(g), at >> 4) + (at & 15));
+                        }
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int i = 0; i < kStepGroups; ++i)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const uint32_t x = kw[i][b][s / (KB / 4)].w[s % (KB / 4)];
+                            const uint32_t b0 = widen_lo(x), b1 = widen_hi(x);
+                            mma(c[i][b], qh[s], b0, b1);
+                            if constexpr (QLO) mma(c[i][b], ql[s], b0, b1);
+                        }
+            }
+            float k1[kStepGroups][2], top[2], vtop[2];
+            bool grow = false;
+#pragma unroll
+            for (int i = 0; i < kStepGroups; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) k1[i][h] = ksn[i] * rs[h];
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < kStepGroups; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                float& x = c[i][b][2 * h + j];
+                                x *= k1[i][h];
+                                if (ksn[i] < 0.f || pos + i * kKeys + 8 * b + i4 + 4 * j >= lim[h]) x = -INFINITY;
+                            }
+                        k1[i][h] = 1.f;
+                    }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float tops[kStepGroups];
+#pragma unroll
+                for (int i = 0; i < kStepGroups; ++i)
+                    tops[i] = fmaxf(fmaxf(c[i][0][2 * h], c[i][0][2 * h + 1]), fmaxf(c[i][1][2 * h], c[i][1][2 * h + 1])) * k1[i][h];
+                top[h] = fmaxf(tops[0], tops[1]);
+                vtop[h] = fmaxf(tops[0] + lg2(vsn[0]), tops[1] + lg2(vsn[1]));
+                grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + kSlack;
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float m2 = fmaxf(m[h], quad_max(top[h]));
+                    // n is kept near m, so that 2^(m - n) is finite
+                    const float n2 = fmaxf(fmaxf(n[h], quad_max(vtop[h])), m2 - 120.f);
+                    const float fl = m2 == -INFINITY ? 1.f : ex2(m[h] - m2), fo = n2 == -INFINITY ? 1.f : ex2(n[h] - n2);
+                    m[h] = m2;
+                    n[h] = n2;
+                    l[h] *= fl;
+                    fac[h] = m2 == -INFINITY ? 0.f : ex2(m2 - n2);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        o[j][2 * h] *= fo;
+                        o[j][2 * h + 1] *= fo;
+                    }
+                }
+            }
+            uint32_t ph[kStepGroups][4], pl[kStepGroups][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float ref = m[h] == -INFINITY ? 0.f : m[h];
+#pragma unroll
+                for (int i = 0; i < kStepGroups; ++i) {
+                    const float w1 = vsn[i] * fac[h];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        float y[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float x = c[i][b][2 * h + j];
+                            const float p = ex2(fmaf(x, k1[i][h], -ref));
+                            l[h] += p;
+                            y[j] = p * w1;
+                            if (masked && x == -INFINITY) y[j] = 0.f;
+                        }
+                        ph[i][2 * b + h] = two_f16(y[0], y[1]);
+                        if constexpr (PLO) pl[i][2 * b + h] = two_f16_rest(y[0], y[1], ph[i][2 * b + h]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kStepGroups; ++i) {
+                // this lane's D / 8 channels of keys i4, i4 + 4, 8 + i4, 12 + i4
+                Words<NT> vw[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int at = channel_of<D>(g);
+                    vw[j] = read_words<NT>(st + i * Sh::kSlotBytes + kKeys * D + row_at<D>(i4 + 4 * j, at >> 4) + (at & 15));
+                }
+#pragma unroll
+                for (int x = 0; x < (NT + 3) / 4; ++x) {
+                    const uint32_t lo0 = __byte_perm(vw[0].w[x], vw[1].w[x], 0x5140), hi0 = __byte_perm(vw[0].w[x], vw[1].w[x], 0x7362);
+                    const uint32_t lo1 = __byte_perm(vw[2].w[x], vw[3].w[x], 0x5140), hi1 = __byte_perm(vw[2].w[x], vw[3].w[x], 0x7362);
+                    const uint32_t b0[4] = {widen_lo(lo0), widen_hi(lo0), widen_lo(hi0), widen_hi(hi0)};
+                    const uint32_t b1[4] = {widen_lo(lo1), widen_hi(lo1), widen_lo(hi1), widen_hi(hi1)};
+#pragma unroll
+                    for (int j = 0; j < (NT < 4 ? NT : 4); ++j) {
+                        mma(o[4 * x + j], ph[i], b0[j], b1[j]);
+                        if constexpr (PLO) mma(o[4 * x + j], pl[i], b0[j], b1[j]);
+                    }
+                }
+            }
+            __syncwarp();                          // the slots have been read
+            start_groups<D>(sh, a, &map_k, &map_v, ahead, ring, out, warp, lane);
+            ahead.step(a, warp);
+            out = next;
+            turn ^= next == 0;
+        }
+        // The warps' results of the piece, halved until one warp has them all: the upper
+        // half writes (O, m, n, l), the lower half adds them to its own.
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        }
+#pragma unroll 1
+        for (int half = kWarps / 2; half > 0; half >>= 1) {
+            __syncthreads();                       // what was there has been read
+            if (warp >= half && warp < 2 * half) {
+                float* y = join + (warp - half) * (Sh::kFrag + 3 * kRows);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    *reinterpret_cast<float4*>(y + j * 128 + lane * 4) = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+                if (i4 == 0) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        y[Sh::kFrag + g + 8 * h] = m[h];
+                        y[Sh::kFrag + kRows + g + 8 * h] = n[h];
+                        y[Sh::kFrag + 2 * kRows + g + 8 * h] = l[h];
+                    }
+                }
+            }
+            __syncthreads();
+            if (warp < half) {
+                const float* y = join + warp * (Sh::kFrag + 3 * kRows);
+                float f0[2], f1[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float ym = y[Sh::kFrag + g + 8 * h], yn = y[Sh::kFrag + kRows + g + 8 * h];
+                    const float m2 = fmaxf(m[h], ym), n2 = fmaxf(n[h], yn);
+                    const float mr = m2 == -INFINITY ? 0.f : m2, nr = n2 == -INFINITY ? 0.f : n2;
+                    l[h] = l[h] * ex2(m[h] - mr) + y[Sh::kFrag + 2 * kRows + g + 8 * h] * ex2(ym - mr);
+                    f0[h] = ex2(n[h] - nr);
+                    f1[h] = ex2(yn - nr);
+                    m[h] = m2;
+                    n[h] = n2;
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const float4 z = *reinterpret_cast<const float4*>(y + j * 128 + lane * 4);
+                    o[j][0] = o[j][0] * f0[0] + z.x * f1[0];
+                    o[j][1] = o[j][1] * f0[0] + z.y * f1[0];
+                    o[j][2] = o[j][2] * f0[1] + z.z * f1[1];
+                    o[j][3] = o[j][3] * f0[1] + z.w * f1[1];
+                }
+            }
+        }
+        if (warp == 0) {
+            const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+            float* part = a.part + ((size_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * kRows * (D + 3);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = g + 8 * h, row = r0 + r;
+                if (*reinterpret_cast<volatile int*>(&sh.dead)) l[h] = __int_as_float(0x7fffffff);
+                if (row >= a.R) continue;
+                const int t = row / a.G;
+                const float f = l[h] == 0.f ? 0.f : ex2(n[h] - m[h]) / l[h];
+                O* op = static_cast<O*>(a.o) + (((long long)w.n * a.Ts + t) * a.Hq + w.hk * a.G + row - t * a.G) * D;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int ch = channel_of<D>(2 * i4 + e);
+                    float y[NT];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) y[j] = o[j][2 * h + e] * (whole ? f : 1.f);
+                    if (whole) store_run<NT>(op + ch, y);
+                    else store_run<NT>(part + r * D + ch, y);
+                }
+                if (!whole && i4 == 0) {
+                    part[kRows * D + r] = m[h];
+                    part[kRows * D + kRows + r] = n[h];
+                    part[kRows * D + 2 * kRows + r] = l[h];
+                }
+            }
+        }
+    }
+}
+
 // Joins the pieces of the items that were cut between groups.  Block (c, y, z): the
 // item that the boundary before group c + 1 falls into, if that is the item's first
 // boundary; rows y 8 .. y 8 + 7 of row tile z, a warp each.  The pieces are read
 // in the order of the groups, so the result does not depend on timing.
 constexpr int kJoinThreads = 256;
 
-template <class O, int D>
+template <class O, int D, int KT, int kLead>
 __global__ void __launch_bounds__(kJoinThreads)
 cache_join_kernel(const __grid_constant__ E4m3Args a)
 {
@@ -560,15 +1081,10 @@ cache_join_kernel(const __grid_constant__ E4m3Args a)
         if (D >= 32 || lane < D) op[lane + 32 * e] = O(o[e] * f);
 }
 
-template <class T, class O, int D>
-cudaError_t launch(const E4m3Args& a, cudaStream_t stream)
+template <class O, int D, int KT, int LEAD>
+cudaError_t launch_join(const E4m3Args& a, cudaStream_t stream)
 {
-    auto kern = cache_attention_kernel<T, O, D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kBytes);
-    if (e != cudaSuccess) return e;
-    kern<<<a.split.groups * a.split.row_tiles, kThreads, Shape<D>::kBytes, stream>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || a.split.groups < 2) return e;
+    if (a.split.groups < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     const int rows = a.R < kRows ? a.R : kRows;
     cfg.gridDim = dim3(a.split.groups - 1, (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), a.split.row_tiles);
@@ -579,7 +1095,54 @@ cudaError_t launch(const E4m3Args& a, cudaStream_t stream)
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_join_kernel<O, D>, a);
+    return cudaLaunchKernelEx(&cfg, cache_join_kernel<O, D, KT, LEAD>, a);
+}
+
+// The pool as [num_pages][page_size][Hkv][d] bytes, boxes of 16 rows of one head.
+bool make_pool_map(CUtensorMap* m, const uint8_t* base, const E4m3Args& a, int d)
+{
+    const auto fn = tc_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t row = (cuuint64_t)a.split.Hkv * d, size = a.split.page_size;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)a.split.Hkv, size, (cuuint64_t)a.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)d, row, a.num_pages > 1 ? (cuuint64_t)a.page_stride : row * size};
+    const cuuint32_t boxes[4] = {(cuuint32_t)d, 1, kKeys, 1}, steps[4] = {1, 1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, boxes, steps,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                          // (256 bytes would fetch the next head's rows with these: 64 x 1 token 532 us)
+                          d == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS && debug_enabled())
+        fprintf(stderr, "kda: cuTensorMapEncodeTiled failed (CUresult %d, 8-bit pages)\n", (int)r);
+    return r == CUDA_SUCCESS;
+}
+
+template <class T, class O, int D>
+cudaError_t launch(E4m3Args a, cudaStream_t stream)
+{
+    const int blocks = a.split.groups * a.split.row_tiles;
+    // 16 rows from a multiple of 16 on in one page and one block of scales
+    CUtensorMap map_k, map_v;
+    if (a.split.page_size % kKeys == 0 && a.block % kKeys == 0 && (long long)a.num_pages * a.blocks * a.split.Hkv <= INT32_MAX &&
+        make_pool_map(&map_k, a.k_cache, a, D) && make_pool_map(&map_v, a.v_cache, a, D)) {
+        auto kern = cache_attention_group_kernel<T, O, D>;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GroupShape<D>::kBytes);
+        if (e != cudaSuccess) return e;
+        a.tile_pages = kGroupKT / a.split.page_size;
+        a.tile_rows = kGroupKT % a.split.page_size;
+        kern<<<blocks, kThreads, GroupShape<D>::kBytes, stream>>>(a, map_k, map_v);
+        const cudaError_t e2 = cudaGetLastError();
+        return e2 != cudaSuccess ? e2 : launch_join<O, D, kGroupKT, kGroupLead>(a, stream);
+    }
+    auto kern = cache_attention_kernel<T, O, D>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    a.tile_pages = KT / a.split.page_size;
+    a.tile_rows = KT % a.split.page_size;
+    kern<<<blocks, kThreads, Shape<D>::kBytes, stream>>>(a);
+    const cudaError_t e2 = cudaGetLastError();
+    return e2 != cudaSuccess ? e2 : launch_join<O, D, KT, kLead>(a, stream);
 }
 
 template <class T, class O>
@@ -611,8 +1174,6 @@ size_t e4m3_workspace_bytes(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, int 
 cudaError_t launch_cache_attention_e4m3(E4m3Args a, int32_t d, kda_dtype_t dtype, int sms, cudaStream_t stream)
 {
     plan(a.R, sms > 0 ? sms : 1, a.split.groups, a.split.row_tiles);
-    a.tile_pages = KT / a.split.page_size;
-    a.tile_rows = KT % a.split.page_size;
     if (dtype == KDA_BF16) return launch_d<__nv_bfloat16, __nv_bfloat16>(a, d, stream);
     if (dtype == KDA_BF16_F32OUT) return launch_d<__nv_bfloat16, float>(a, d, stream);
     return launch_d<float, float>(a, d, stream);
