@@ -7,22 +7,24 @@
 // p is, where fp32 would lose what matters (at position 10^6 an angle is off by
 // 0.03).  Its upper 32 bits go to sincospif.
 //
-// A unit is the part of one block of rows (of one scale, or 16 rows of a cache in
-// the model's type) that one sequence adds to; the thread block that owns the unit's
-// first row tabulates the sines and cosines of the unit's rows once and its warps
-// share out the heads.  A lane holds 16 channels of a row, two vectors of eight
-// that belong together: the halves of eight pairs, or eight neighbouring pairs.
+// Rows that are only turned and copied (queries; in a cache of the model's type keys and
+// values too): a lane holds 16 channels of a row, two vectors of eight that belong
+// together, namely the halves of eight pairs or eight neighbouring pairs.  It works out its row's
+// place and its eight sines and cosines once and goes through the heads with them, four
+// heads under way, no shared memory and no barrier.
 //
-// 8 bits: a warp has a unit of one head of k or v and reads it twice, first for the
-// largest magnitude (as bits, so that infinities and NaN win), then to store x / s
-// (from L1 or L2 then).  s is a power of two: e4m3 is a floating type, so a finer scale
-// would gain nothing, and the division, a later change of the scale and the product in
-// the attention are exact but for e4m3's own rounding.  A scale of NaN marks a block
-// with an infinity or NaN; its bytes are 0, so that no product of a weight of 0
-// with it is NaN.
+// 8 bits: a unit is the part of one block of rows that one sequence adds to.  The thread
+// block that owns its first row tabulates the sines and cosines of its rows; a team of as
+// many warps as hold the block in registers has a head of k or v: it reads the rows
+// once, finds the largest magnitude (as bits, so that infinities and NaN win) and stores
+// x / s.  s is a power of two: e4m3 is a floating type, so a finer scale would gain
+// nothing, and the division, a later change of the scale and the product in the attention
+// are exact but for e4m3's own rounding.  A scale of NaN marks a block with an infinity or
+// NaN; its bytes are 0, so that no product of a weight of 0 with it is NaN.
 //
 // Bound by the bytes moved.
 #include "kda_prompt.cuh"
+#include "kda_sm100.cuh"
 
 namespace kda {
 namespace {
@@ -153,28 +155,79 @@ __device__ __forceinline__ int table_at(int row, int j, int rot)
     return row * (rot / 2) + ((j & 7) >> 1) * (rot / 8) + (j >> 3) * 2 + (j & 1);
 }
 
-__device__ __forceinline__ void turn(const float2* table, int row, const Pair& p, int rot, bool interleaved,
-                                     float (&x)[8], float (&y)[8])
+template <class T>
+struct Pieces {
+    typename RawOf<T>::type a, b;
+};
+template <class T>
+__device__ __forceinline__ void widen(const Pieces<T>& r, float (&x)[8], float (&y)[8])
 {
-    const float4* t = reinterpret_cast<const float4*>(table + row * (rot / 2)) + p.c;
+    widen(r.a, x);
+    widen(r.b, y);
+}
+template <class T>
+__device__ __forceinline__ Pieces<T> load_pieces(const uint8_t* row, const Pair& p)
+{
+    return {load_raw<T>(row + p.a * (int)sizeof(T)), load_raw<T>(row + p.b * (int)sizeof(T))};
+}
+template <class T>
+__device__ __forceinline__ void store_pieces(uint8_t* row, const Pair& p, const float (&x)[8], const float (&y)[8])
+{
+    store8(reinterpret_cast<T*>(row + p.a * (int)sizeof(T)), x);
+    store8(reinterpret_cast<T*>(row + p.b * (int)sizeof(T)), y);
+}
+
+// (cos, sin) of pair j of a row at position pos.
+__device__ __forceinline__ float2 angle(unsigned long long turns, long long pos)
+{
+    float s, c;
+    // the upper 32 bits as a signed fraction of a turn, in half turns: times 2^-31
+    sincospif((float)(int32_t)(((unsigned long long)pos * turns) >> 32) * 4.656612873077393e-10f, &s, &c);
+    return make_float2(c, s);
+}
+// Turns per position of a pair, times 2^64.  In fp64: 53 bits of a fraction that a
+// position (31 bits) multiplies.
+__device__ __forceinline__ unsigned long long turns_of(float inv_freq)
+{
+    double f = (double)inv_freq * 0.15915494309189533577;
+    f -= floor(f);
+    return __double2ull_rn(f * 18446744073709551616.0);
+}
+
+// Turns a lane's 16 channels by its eight angles.
+__device__ __forceinline__ void turn(const float2 (&w)[8], bool interleaved, float (&x)[8], float (&y)[8])
+{
+    if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 w = t[i * (rot / 16)];        // (cos, sin) of pairs 2 i and 2 i + 1
-        if (interleaved) {
-            float* z = i < 2 ? x + 4 * i : y + 4 * (i - 2);
-            const float z0 = z[0], z2 = z[2];
-            z[0] = z0 * w.x - z[1] * w.y;
-            z[1] = z0 * w.y + z[1] * w.x;
-            z[2] = z2 * w.z - z[3] * w.w;
-            z[3] = z2 * w.w + z[3] * w.z;
-        } else {
-            const float x0 = x[2 * i], x1 = x[2 * i + 1];
-            x[2 * i] = x0 * w.x - y[2 * i] * w.y;
-            y[2 * i] = x0 * w.y + y[2 * i] * w.x;
-            x[2 * i + 1] = x1 * w.z - y[2 * i + 1] * w.w;
-            y[2 * i + 1] = x1 * w.w + y[2 * i + 1] * w.z;
+        for (int i = 0; i < 4; ++i) {
+            const float x0 = x[2 * i], y0 = y[2 * i];
+            x[2 * i] = x0 * w[i].x - x[2 * i + 1] * w[i].y;
+            x[2 * i + 1] = x0 * w[i].y + x[2 * i + 1] * w[i].x;
+            y[2 * i] = y0 * w[4 + i].x - y[2 * i + 1] * w[4 + i].y;
+            y[2 * i + 1] = y0 * w[4 + i].y + y[2 * i + 1] * w[4 + i].x;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x0 = x[i];
+            x[i] = x0 * w[i].x - y[i] * w[i].y;
+            y[i] = x0 * w[i].y + y[i] * w[i].x;
         }
     }
+}
+
+// The same from the table of a unit's rows.
+__device__ __forceinline__ void turn(const float2* table, int row, const Pair& p, int rot, bool interleaved, float (&x)[8], float (&y)[8])
+{
+    const float4* t = reinterpret_cast<const float4*>(table + row * (rot / 2)) + p.c;
+    float2 w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 z = t[i * (rot / 16)];        // (cos, sin) of pairs 2 i and 2 i + 1
+        w[2 * i] = make_float2(z.x, z.y);
+        w[2 * i + 1] = make_float2(z.z, z.w);
+    }
+    turn(w, interleaved, x, y);
 }
 
 __device__ __forceinline__ uint32_t top_bits(uint32_t top, const float (&x)[8])
@@ -184,104 +237,135 @@ __device__ __forceinline__ uint32_t top_bits(uint32_t top, const float (&x)[8])
     return top;
 }
 
-template <class T, int D>
-struct Rows {
-    static constexpr int kLanes = D / 16;          // lanes per row
-    static constexpr int kPass = 32 / kLanes;      // rows per pass of a warp
-    static constexpr int kDepth = sizeof(T) == 2 ? 4 : 2;
-};
-
-// One head of a unit's rows: src to dst (null: dropped) and to the rows of a cache
-// in the same type (place[row] < 0: dropped).
-template <class T, int D, bool TURN>
-__device__ void plain_head(const RotaryArgs& a, const Unit& u, const float2* table, const uint8_t* src,
-                           long long src_row, uint8_t* dst, long long dst_row, uint8_t* cache,
-                           const long long* place, int lane)
+// Where position pos of sequence n lies: page and row in it; false: nowhere.
+__device__ __forceinline__ bool place_of(const RotaryArgs& a, int n, long long pos, int& page, int& slot)
 {
-    using R = Rows<T, D>;
-    const Pair p = pair_of(lane % R::kLanes, TURN ? a.rot : 0, a.interleaved);
-    const int r0 = lane / R::kLanes;
-    const int ea = p.a * (int)sizeof(T), eb = p.b * (int)sizeof(T);
+    if (pos >= (long long)a.max_pages * a.page_size) return false;
+    const int at = (int)(pos / a.page_size);
+    page = __ldg(a.page_table + (long long)n * a.max_pages + at);
+    slot = (int)(pos - (long long)at * a.page_size);
+    return page >= 0 && page < a.num_pages;
+}
+
+constexpr int kAhead = 4;              // heads under way in the rows that are only turned
+
+// Heads h0 .. h1 - 1 of a row's tensor, `step` bytes from head to head; from src to dst and
+// to cache (either may be null).
+template <class T, int D, bool TURN>
+__device__ __forceinline__ void row_heads(const uint8_t* src, uint8_t* dst, uint8_t* cache, int heads, const Pair& p,
+                                          const float2 (&w)[8], bool interleaved)
+{
+    constexpr int kHead = D * (int)sizeof(T);
 #pragma unroll 1
-    for (int base = r0; base < u.count; base += R::kPass * R::kDepth) {
-        typename RawOf<T>::type ra[R::kDepth], rb[R::kDepth];
+    for (int h = 0; h < heads; h += kAhead) {
+        Pieces<T> r[kAhead];
 #pragma unroll
-        for (int i = 0; i < R::kDepth; ++i) {
-            const int r = base + i * R::kPass;
-            if (r < u.count) {
-                const uint8_t* s = src + (u.first + r) * src_row;
-                ra[i] = load_raw<T>(s + ea);
-                rb[i] = load_raw<T>(s + eb);
-            }
-        }
+        for (int i = 0; i < kAhead; ++i)
+            if (h + i < heads) r[i] = load_pieces<T>(src + (h + i) * kHead, p);
 #pragma unroll
-        for (int i = 0; i < R::kDepth; ++i) {
-            const int r = base + i * R::kPass;
-            if (r >= u.count) break;
+        for (int i = 0; i < kAhead; ++i) {
+            if (h + i >= heads) break;
             float x[8], y[8];
-            widen(ra[i], x);
-            widen(rb[i], y);
-            if (TURN && p.turned) turn(table, r, p, a.rot, a.interleaved, x, y);
-            if (dst) {
-                uint8_t* d = dst + (u.first + r) * dst_row;
-                store8(reinterpret_cast<T*>(d + ea), x);
-                store8(reinterpret_cast<T*>(d + eb), y);
-            }
-            if (cache && place[r] >= 0) {
-                store8(reinterpret_cast<T*>(cache + place[r] + ea), x);
-                store8(reinterpret_cast<T*>(cache + place[r] + eb), y);
-            }
+            widen(r[i], x, y);
+            if (TURN && p.turned) turn(w, interleaved, x, y);
+            if (dst) store_pieces<T>(dst + (h + i) * kHead, p, x, y);
+            if (cache) store_pieces<T>(cache + (h + i) * kHead, p, x, y);
         }
     }
 }
 
-// One head of a unit's rows as e4m3 into its block of the cache: `block0` the
-// block's first row there (null: the rows have no place), `off` the rows that it
-// already has, `scale` its scale.
-template <class T, int D, bool TURN>
-__device__ void e4m3_head(const RotaryArgs& a, const Unit& u, const float2* table, const uint8_t* src,
-                          long long src_row, uint8_t* dst, long long dst_row, uint8_t* block0, int off,
-                          float* scale, int lane)
+// Rows that are only turned and copied: a warp has 32 / (D / 16) rows and some of
+// their heads.
+template <class T, int D, bool EIGHT>
+__device__ __forceinline__ void rows_part(const RotaryArgs& a, const int32_t* cu, const unsigned long long* turns, int block, int warp, int lane)
 {
-    using R = Rows<T, D>;
-    const Pair p = pair_of(lane % R::kLanes, TURN ? a.rot : 0, a.interleaved);
-    const int r0 = lane / R::kLanes;
-    const int ea = p.a * (int)sizeof(T), eb = p.b * (int)sizeof(T);
+    constexpr int L = D / 16, R = 32 / L;
+    const long long id = (long long)block * kWarps + warp;
+    const int chunk = (int)(id % a.chunks), h0 = chunk * a.chunk_heads;
+    const long long first = id / a.chunks * R;
+    const int r = (int)(first + lane / L);
+    if (first >= a.T || r >= a.T) return;
+    int n, start, end;
+    if (!row_owner(a, cu, r, n, start, end)) return;
+    const int len = __ldg(a.lengths + n);
+    if (len < 0) return;
+    const long long pos = (long long)len + (r - start);
+    const int c = lane % L;
+    const Pair p = pair_of(c, a.rot, a.interleaved);
+    float2 w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = p.turned ? angle(turns[8 * c + i], pos) : make_float2(1.f, 0.f);
+    const int h1 = h0 + a.chunk_heads;             // of the queries, then keys, then values
+    constexpr int kHead = D * (int)sizeof(T);
+    if (h0 < a.Hq) {
+        const int n_q = min(h1, a.Hq) - h0;
+        row_heads<T, D, true>(a.q + r * a.q_row + h0 * kHead, a.q_out + r * a.q_out_row + h0 * kHead, nullptr, n_q, p, w, a.interleaved);
+    }
+    if constexpr (!EIGHT) {
+        if (h1 <= a.Hq) return;
+        int page, slot;
+        const bool there = place_of(a, n, pos, page, slot);
+        const long long at = there ? page * a.page_bytes + (long long)slot * a.Hkv * kHead : 0;
+        const int k0 = max(h0 - a.Hq, 0), k1 = min(h1 - a.Hq, a.Hkv);
+        if (k0 < k1)
+            row_heads<T, D, true>(a.k + r * a.k_row + k0 * kHead, a.k_out ? a.k_out + r * a.k_out_row + k0 * kHead : nullptr,
+                                  there ? a.k_cache + at + k0 * kHead : nullptr, k1 - k0, p, w, a.interleaved);
+        const int v0 = max(h0 - a.Hq - a.Hkv, 0), v1 = min(h1 - a.Hq - a.Hkv, a.Hkv);
+        if (v0 < v1 && there)
+            row_heads<T, D, false>(a.v + r * a.v_row + v0 * kHead, nullptr, a.v_cache + at + v0 * kHead, v1 - v0, p, w, a.interleaved);
+    }
+}
+
+// One head of a unit's rows as e4m3 into its block of the cache, by a team of `team`
+// warps: `block0` the block's first row there (null: the rows have no place), `off`
+// the rows that it already has, `scale` its scale.
+constexpr int kHeld = 4;               // rows of a lane
+template <class T, int D, bool TURN>
+__device__ __forceinline__ void e4m3_head(const RotaryArgs& a, const Unit& u, const float2* table, const uint8_t* src, long long src_row,
+                                          uint8_t* dst, long long dst_row, uint8_t* block0, int off, float* scale, uint32_t* tops, int team,
+                                          int warp, int lane)
+{
+    constexpr int L = D / 16;
+    const int tl = (warp % team) * 32 + lane;      // lane of the team
+    const Pair p = pair_of(tl % L, TURN ? a.rot : 0, a.interleaved);
+    const int r0 = tl / L, pass = team * 32 / L;
     const int row_bytes = a.Hkv * D;
+    Pieces<T> raw[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int r = r0 + i * pass;
+        if (r < u.count) raw[i] = load_pieces<T>(src + (u.first + r) * src_row, p);
+    }
+    uint32_t old = 0;
+    if (block0 && off > 0) old = __float_as_uint(*reinterpret_cast<volatile float*>(scale)) & 0x7FFFFFFFu;
     uint32_t top = 0;
-    if (block0) {
-#pragma unroll 1
-        for (int base = r0; base < u.count; base += R::kPass * R::kDepth) {
-            typename RawOf<T>::type ra[R::kDepth], rb[R::kDepth];
 #pragma unroll
-            for (int i = 0; i < R::kDepth; ++i) {
-                const int r = base + i * R::kPass;
-                if (r < u.count) {
-                    const uint8_t* s = src + (u.first + r) * src_row;
-                    ra[i] = load_raw<T>(s + ea);
-                    rb[i] = load_raw<T>(s + eb);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < R::kDepth; ++i) {
-                const int r = base + i * R::kPass;
-                if (r >= u.count) break;
-                float x[8], y[8];
-                widen(ra[i], x);
-                widen(rb[i], y);
-                if (TURN && p.turned) turn(table, r, p, a.rot, a.interleaved, x, y);
-                top = top_bits(top_bits(top, x), y);
-            }
+    for (int i = 0; i < kHeld; ++i) {
+        const int r = r0 + i * pass;
+        if (r < u.count) {
+            float x[8], y[8];
+            widen(raw[i], x, y);
+            if (TURN && p.turned) turn(table, r, p, a.rot, a.interleaved, x, y);
+            top = top_bits(top_bits(top, x), y);
         }
     }
     top = __reduce_max_sync(0xffffffffu, top);
+    if (team > 1) {
+        const int first = warp / team * team;
+        if (lane == 0) tops[warp] = top;
+        sm100::named_bar_sync(1 + first, team * 32);
+        for (int i = 0; i < team; ++i) top = max(top, tops[first + i]);
+        // (all have read before the next head's are written)
+        sm100::named_bar_sync(1 + first, team * 32);
+    } else {
+        __syncwarp();                              // every lane has read the old scale
+    }
     uint32_t sb = scale_bits(top);
-    if (block0 && off > 0) {
-        const uint32_t old = __float_as_uint(*scale) & 0x7FFFFFFFu;
+    if (block0) {
         if (sb > old && old > 0 && sb < 0x7F800000u) {
             // the rows that are there, in the new scale
             const float ratio = __uint_as_float(old) * __uint_as_float(0x7F000000u - sb);
-            for (int e = lane; e < off * (D / 8); e += 32) {
+            for (int e = tl; e < off * (D / 8); e += team * 32) {
                 uint2* w = reinterpret_cast<uint2*>(block0 + (long long)(e / (D / 8)) * row_bytes + e % (D / 8) * 8);
                 const uint2 b = *w;
                 const float2 b0 = from_e4m3(b.x), b1 = from_e4m3(b.x >> 16), b2 = from_e4m3(b.y), b3 = from_e4m3(b.y >> 16);
@@ -290,185 +374,141 @@ __device__ void e4m3_head(const RotaryArgs& a, const Unit& u, const float2* tabl
             }
         }
         sb = max(sb, old);
+        if (tl == 0) *scale = __uint_as_float(sb);
     }
-    __syncwarp();                                  // every lane has read the old scale
-    if (block0 && lane == 0) *scale = __uint_as_float(sb);
     const bool store = sb > 0 && sb < 0x7F800000u;
     const float inv = store ? __uint_as_float(0x7F000000u - sb) : 0.f;
-    if (!block0 && !dst) return;
-#pragma unroll 1
-    for (int base = r0; base < u.count; base += R::kPass * R::kDepth) {
-        typename RawOf<T>::type ra[R::kDepth], rb[R::kDepth];
 #pragma unroll
-        for (int i = 0; i < R::kDepth; ++i) {
-            const int r = base + i * R::kPass;
-            if (r < u.count) {
-                const uint8_t* s = src + (u.first + r) * src_row;
-                ra[i] = load_raw<T>(s + ea);
-                rb[i] = load_raw<T>(s + eb);
+    for (int i = 0; i < kHeld; ++i) {
+        const int r = r0 + i * pass;
+        if (r >= u.count) break;
+        float x[8], y[8];
+        widen(raw[i], x, y);
+        if (TURN && p.turned) turn(table, r, p, a.rot, a.interleaved, x, y);
+        if (dst) store_pieces<T>(dst + (u.first + r) * dst_row, p, x, y);
+        if (block0) {
+            uint8_t* c = block0 + (long long)(off + r) * row_bytes;
+            uint2 wx = make_uint2(0, 0), wy = make_uint2(0, 0);
+            if (store) {
+                wx = make_uint2(four_e4m3(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                                four_e4m3(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+                wy = make_uint2(four_e4m3(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                                four_e4m3(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
             }
-        }
-#pragma unroll
-        for (int i = 0; i < R::kDepth; ++i) {
-            const int r = base + i * R::kPass;
-            if (r >= u.count) break;
-            float x[8], y[8];
-            widen(ra[i], x);
-            widen(rb[i], y);
-            if (TURN && p.turned) turn(table, r, p, a.rot, a.interleaved, x, y);
-            if (dst) {
-                uint8_t* d = dst + (u.first + r) * dst_row;
-                store8(reinterpret_cast<T*>(d + ea), x);
-                store8(reinterpret_cast<T*>(d + eb), y);
-            }
-            if (block0) {
-                uint8_t* c = block0 + (long long)(off + r) * row_bytes;
-                uint2 wx = make_uint2(0, 0), wy = make_uint2(0, 0);
-                if (store) {
-                    wx = make_uint2(four_e4m3(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                                    four_e4m3(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
-                    wy = make_uint2(four_e4m3(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                                    four_e4m3(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
-                }
-                *reinterpret_cast<uint2*>(c + p.a) = wx;
-                *reinterpret_cast<uint2*>(c + p.b) = wy;
-            }
+            *reinterpret_cast<uint2*>(c + p.a) = wx;
+            *reinterpret_cast<uint2*>(c + p.b) = wy;
         }
     }
 }
 
-template <class T, int D, bool EIGHT>
-__global__ void __launch_bounds__(kThreads, 2)
-cache_rotary_kernel(const __grid_constant__ RotaryArgs a)
+template <class T, int D>
+__device__ __forceinline__ void units_part(const RotaryArgs& a, const int32_t* cu, const unsigned long long* turns, float2* table,
+                                           int block, int warp, int lane)
 {
-    extern __shared__ __align__(16) uint8_t dyn[];
-    float2* table = reinterpret_cast<float2*>(dyn);
-    __shared__ int32_t sh_cu[kHeldSeqs + 1];
-    __shared__ unsigned long long sh_turns[64];    // turns per position of each pair, times 2^64
     __shared__ Unit sh_unit[kMaxScaleBlock];       // of each row of the window; count 0: no unit begins there
-    __shared__ long long sh_place[kMaxScaleBlock]; // of each row of the unit, byte offset in the cache
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int32_t* cu = a.cu_seqlens;
-    if (a.N <= kHeldSeqs) {
-        for (int i = tid; i <= a.N; i += kThreads) sh_cu[i] = __ldg(a.cu_seqlens + i);
-        cu = sh_cu;
-    }
-    if (tid < a.rot / 2) {
-        // in fp64: 53 bits of a fraction that a position (31 bits) multiplies
-        double f = (double)__ldg(a.inv_freq + tid) * 0.15915494309189533577;
-        f -= floor(f);
-        sh_turns[tid] = __double2ull_rn(f * 18446744073709551616.0);
-    }
-    __syncthreads();
+    __shared__ uint32_t sh_tops[kWarps];
+    const int tid = threadIdx.x;
+    const int window = block / a.splits, split = block - window * a.splits;
     if (tid < a.window) {
         Unit u = {0, 0, 0, 0};
-        const int r = blockIdx.x * a.window + tid;
+        const long long r = (long long)window * a.window + tid;
         int n, start, end;
-        if (r < a.T && row_owner(a, cu, r, n, start, end)) {
+        if (r < a.T && row_owner(a, cu, (int)r, n, start, end)) {
             const int len = __ldg(a.lengths + n);
             if (len >= 0) {
                 u.n = n;
-                u.first = r;
-                u.pos = (long long)len + (r - start);
-                const int left = a.step - (int)(u.pos % a.step);
-                if (r == start || left == a.step) u.count = min(left, end - r);
+                u.first = (int)r;
+                u.pos = (long long)len + (u.first - start);
+                const int left = a.block - (int)(u.pos % a.block);
+                if (u.first == start || left == a.block) u.count = min(left, end - u.first);
             }
         }
         sh_unit[tid] = u;
     }
-    if (a.new_lengths && blockIdx.y == 0) {
-        for (int n = blockIdx.x * kThreads + tid; n < a.N; n += gridDim.x * kThreads)
-            a.new_lengths[n] = __ldg(a.lengths + n) + max(min(cu[n + 1], a.T) - max(cu[n], 0), 0);
-    }
     __syncthreads();
-    const int tasks = (a.q ? a.Hq : 0) + 2 * a.Hkv;
-    const int half = a.rot / 2;
+    const int half = a.rot / 2, teams = kWarps / a.team;
 #pragma unroll 1
     for (int w = 0; w < a.window; ++w) {
         const Unit u = sh_unit[w];
         if (u.count == 0) continue;                // (the same for all threads)
         for (int e = tid; e < u.count * half; e += kThreads) {
             const int r = e / half, j = e - r * half;
-            const unsigned long long t = (unsigned long long)(u.pos + r) * sh_turns[j];
-            float s, c;
-            sincospif((float)(int32_t)(t >> 32) * 4.656612873077393e-10f, &s, &c);    // 2^-31: in half turns
-            table[table_at(r, j, a.rot)] = make_float2(c, s);
+            table[table_at(r, j, a.rot)] = angle(turns[j], u.pos + r);
         }
-        if (tid < u.count) {
-            const long long pos = u.pos + tid;
-            long long place = -1;
-            if (pos < (long long)a.max_pages * a.page_size) {
-                const int at = (int)(pos / a.page_size);
-                const int page = __ldg(a.page_table + (long long)u.n * a.max_pages + at);
-                if (page >= 0 && page < a.num_pages) {
-                    const int slot = (int)(pos - (long long)at * a.page_size);
-                    // of a block of 8 bits: the page and the row in it
-                    place = EIGHT ? (long long)page << 32 | slot
-                                  : page * a.page_bytes + (long long)slot * a.Hkv * D * (int)sizeof(T);
-                }
-            }
-            sh_place[tid] = place;
-        }
+        int page, slot;
+        const bool there = place_of(a, u.n, u.pos, page, slot);    // (a block lies in one page)
         __syncthreads();
 #pragma unroll 1
-        for (int task = blockIdx.y * kWarps + warp; task < tasks; task += gridDim.y * kWarps) {
-            const int h = task - 2 * a.Hkv;        // keys and values first, they take longer
-            if (h >= 0) {
-                const long long at = (long long)h * D * (int)sizeof(T);
-                plain_head<T, D, true>(a, u, table, a.q + at, a.q_row, a.q_out + at, a.q_out_row, nullptr, sh_place, lane);
-                continue;
-            }
+        for (int task = split * teams + warp / a.team; task < 2 * a.Hkv; task += a.splits * teams) {
             const bool is_k = task < a.Hkv;
             const int hk = is_k ? task : task - a.Hkv;
             const long long at = (long long)hk * D * (int)sizeof(T);
-            uint8_t* k_out = a.k_out ? a.k_out + at : nullptr;
-            if constexpr (EIGHT) {
-                const long long place = sh_place[0];
-                uint8_t* block0 = nullptr;
-                float* scale = nullptr;
-                int off = 0;
-                if (place >= 0) {
-                    const int page = (int)(place >> 32), slot = (int)(place & 0xFFFFFFFF), b = slot / a.block;
-                    off = slot - b * a.block;
-                    block0 = (is_k ? a.k_cache : a.v_cache) + page * a.page_bytes + (long long)b * a.block * a.Hkv * D + hk * D;
-                    scale = (is_k ? a.k_scales : a.v_scales) + ((long long)page * (a.page_size / a.block) + b) * a.Hkv + hk;
-                }
-                if (is_k)
-                    e4m3_head<T, D, true>(a, u, table, a.k + at, a.k_row, k_out, a.k_out_row, block0, off, scale, lane);
-                else
-                    e4m3_head<T, D, false>(a, u, table, a.v + at, a.v_row, nullptr, 0, block0, off, scale, lane);
-            } else {
-                if (is_k)
-                    plain_head<T, D, true>(a, u, table, a.k + at, a.k_row, k_out, a.k_out_row, a.k_cache + at, sh_place, lane);
-                else
-                    plain_head<T, D, false>(a, u, table, a.v + at, a.v_row, nullptr, 0, a.v_cache + at, sh_place, lane);
+            uint8_t* block0 = nullptr;
+            float* scale = nullptr;
+            int off = 0;
+            if (there) {
+                const int b = slot / a.block;
+                off = slot - b * a.block;
+                block0 = (is_k ? a.k_cache : a.v_cache) + page * a.page_bytes + (long long)b * a.block * a.Hkv * D + hk * D;
+                scale = (is_k ? a.k_scales : a.v_scales) + ((long long)page * (a.page_size / a.block) + b) * a.Hkv + hk;
             }
+            if (is_k)
+                e4m3_head<T, D, true>(a, u, table, a.k + at, a.k_row, a.k_out ? a.k_out + at : nullptr, a.k_out_row, block0, off, scale,
+                                      sh_tops, a.team, warp, lane);
+            else if (there)
+                e4m3_head<T, D, false>(a, u, table, a.v + at, a.v_row, nullptr, 0, block0, off, scale, sh_tops, a.team, warp, lane);
         }
         __syncthreads();
     }
 }
 
+// The first unit_blocks thread blocks have the units (8 bits), the others rows.
 template <class T, int D, bool EIGHT>
-cudaError_t launch(const RotaryArgs& a, dim3 grid, cudaStream_t stream)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || !EIGHT ? 2 : 1)
+cache_rotary_kernel(const __grid_constant__ RotaryArgs a)
+{
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ int32_t sh_cu[kHeldSeqs + 1];
+    __shared__ unsigned long long sh_turns[64];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t* cu = a.cu_seqlens;
+    if (a.N <= kHeldSeqs) {
+        for (int i = tid; i <= a.N; i += kThreads) sh_cu[i] = __ldg(a.cu_seqlens + i);
+        cu = sh_cu;
+    }
+    if (tid < a.rot / 2) sh_turns[tid] = turns_of(__ldg(a.inv_freq + tid));
+    __syncthreads();
+    if (a.new_lengths) {
+        for (int n = blockIdx.x * kThreads + tid; n < a.N; n += gridDim.x * kThreads)
+            a.new_lengths[n] = __ldg(a.lengths + n) + max(min(cu[n + 1], a.T) - max(cu[n], 0), 0);
+    }
+    if (EIGHT && (int)blockIdx.x < a.unit_blocks)
+        units_part<T, D>(a, cu, sh_turns, reinterpret_cast<float2*>(dyn), blockIdx.x, warp, lane);
+    else
+        rows_part<T, D, EIGHT>(a, cu, sh_turns, blockIdx.x - a.unit_blocks, warp, lane);
+}
+
+template <class T, int D, bool EIGHT>
+cudaError_t launch(const RotaryArgs& a, unsigned blocks, cudaStream_t stream)
 {
     auto kern = cache_rotary_kernel<T, D, EIGHT>;
-    const size_t bytes = (size_t)a.step * (a.rot / 2) * sizeof(float2);
+    const size_t bytes = EIGHT ? (size_t)a.block * (a.rot / 2) * sizeof(float2) : 0;
     if (bytes > 32 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e != cudaSuccess) return e;
     }
-    kern<<<grid, kThreads, bytes, stream>>>(a);
+    kern<<<blocks, kThreads, bytes, stream>>>(a);
     return cudaGetLastError();
 }
 
 template <class T, bool EIGHT>
-cudaError_t launch_d(const RotaryArgs& a, int32_t d, dim3 grid, cudaStream_t stream)
+cudaError_t launch_d(const RotaryArgs& a, int32_t d, unsigned blocks, cudaStream_t stream)
 {
     switch (d) {
-    case 16: return launch<T, 16, EIGHT>(a, grid, stream);
-    case 32: return launch<T, 32, EIGHT>(a, grid, stream);
-    case 64: return launch<T, 64, EIGHT>(a, grid, stream);
-    default: return launch<T, 128, EIGHT>(a, grid, stream);
+    case 16: return launch<T, 16, EIGHT>(a, blocks, stream);
+    case 32: return launch<T, 32, EIGHT>(a, blocks, stream);
+    case 64: return launch<T, 64, EIGHT>(a, blocks, stream);
+    default: return launch<T, 128, EIGHT>(a, blocks, stream);
     }
 }
 
@@ -476,16 +516,32 @@ cudaError_t launch_d(const RotaryArgs& a, int32_t d, dim3 grid, cudaStream_t str
 
 cudaError_t launch_cache_append_rotary(RotaryArgs a, int32_t d, bool bf16, int sms, cudaStream_t stream)
 {
-    a.step = a.block ? a.block : 16;
-    // As many rows per thread block as a unit has, fewer when that would leave SMs idle
-    // (one per block with few tokens); then the heads are spread over more blocks too.
-    const int spread = a.T / (2 * sms);
-    a.window = spread < 1 ? 1 : spread > a.step ? a.step : spread;
-    const int blocks = a.T > 0 ? (a.T + a.window - 1) / a.window : 1;    // no rows: new_lengths alone
-    const int rounds = ((a.q ? a.Hq : 0) + 2 * a.Hkv + kWarps - 1) / kWarps;
-    int y = (4 * sms + blocks - 1) / blocks;
-    y = y > rounds ? rounds : y;
-    const dim3 grid((unsigned)blocks, (unsigned)(y > 65535 ? 65535 : y));
+    long long units = 0;
+    if (a.block) {
+        // As many rows per thread block as a unit has, fewer when that would leave SMs idle (one
+        // per block with few tokens); then the heads are spread over more blocks too.
+        const int spread = a.T / (2 * sms);
+        a.window = spread < 1 ? 1 : spread > a.block ? a.block : spread;
+        const int lanes = a.block * (d / 16);      // of a block's rows
+        a.team = 1;
+        while (a.team * 32 * kHeld < lanes) a.team *= 2;
+        const long long windows = ((long long)a.T + a.window - 1) / a.window;
+        const int rounds = (2 * a.Hkv * a.team + kWarps - 1) / kWarps;
+        const long long most = windows > 0 ? (2ll * sms + windows - 1) / windows : 1;
+        a.splits = (int)(most < 1 ? 1 : most > rounds ? rounds : most);
+        units = windows * a.splits;
+    }
+    // the rows, in groups of a warp's, and a part of their heads each, where all would
+    // leave SMs idle
+    const int per = 32 / (d / 16), heads = a.Hq + (a.block ? 0 : 2 * a.Hkv);
+    const long long groups = heads ? ((long long)a.T + per - 1) / per : 0;
+    a.chunks = 1;
+    while (a.chunks < heads / kAhead && groups * a.chunks < 2ll * kWarps * sms) a.chunks *= 2;
+    a.chunk_heads = (heads + a.chunks - 1) / a.chunks;
+    const long long blocks = units + (groups * a.chunks + kWarps - 1) / kWarps;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    a.unit_blocks = (int32_t)units;
+    const unsigned grid = blocks > 0 ? (unsigned)blocks : 1;       // no rows: new_lengths alone
     if (bf16)
         return a.block ? launch_d<__nv_bfloat16, true>(a, d, grid, stream) : launch_d<__nv_bfloat16, false>(a, d, grid, stream);
     return a.block ? launch_d<float, true>(a, d, grid, stream) : launch_d<float, false>(a, d, grid, stream);

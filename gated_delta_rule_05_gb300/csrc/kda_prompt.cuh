@@ -64,8 +64,10 @@ struct RotaryArgs {
     const float* inv_freq;            // [rot / 2]
     int32_t T, N, Hq, Hkv, rot, num_pages, page_size, max_pages;
     int32_t block;                    // rows per scale; 0: the cache is in k's type
-    int32_t step, window;             // rows of a unit at most, rows per thread block
     bool interleaved;
+    // of the launch: blocks of 8-bit units, rows of their windows, parts of a window's heads, warps
+    // of a team; parts of a row's heads and heads of a part
+    int32_t unit_blocks, window, splits, team, chunks, chunk_heads;
 };
 constexpr int kMaxScaleBlock = 128;
 cudaError_t launch_cache_append_rotary(RotaryArgs args, int32_t d, bool bf16, int sms, cudaStream_t stream);
