@@ -320,22 +320,33 @@ __device__ __forceinline__ void rows_part(const RotaryArgs& a, const int32_t* cu
 // warps: `block0` the block's first row there (null: the rows have no place), `off`
 // the rows that it already has, `scale` its scale.
 constexpr int kHeld = 4;               // rows of a lane
-template <class T, int D, bool TURN>
-__device__ __forceinline__ void e4m3_head(const RotaryArgs& a, const Unit& u, const float2* table, const uint8_t* src, long long src_row,
-                                          uint8_t* dst, long long dst_row, uint8_t* block0, int off, float* scale, uint32_t* tops, int team,
-                                          int warp, int lane)
+template <class T>
+struct Held {
+    Pieces<T> rows[kHeld];
+};
+// The rows of one head that this lane of a team holds.
+template <class T, int D>
+__device__ __forceinline__ Held<T> e4m3_load(const Unit& u, const Pair& p, const uint8_t* src, long long src_row, int team, int tl)
 {
     constexpr int L = D / 16;
-    const int tl = (warp % team) * 32 + lane;      // lane of the team
-    const Pair p = pair_of(tl % L, TURN ? a.rot : 0, a.interleaved);
-    const int r0 = tl / L, pass = team * 32 / L;
-    const int row_bytes = a.Hkv * D;
-    Pieces<T> raw[kHeld];
+    Held<T> h;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-        const int r = r0 + i * pass;
-        if (r < u.count) raw[i] = load_pieces<T>(src + (u.first + r) * src_row, p);
+        const int r = tl / L + i * (team * 32 / L);
+        if (r < u.count) h.rows[i] = load_pieces<T>(src + (u.first + r) * src_row, p);
     }
+    return h;
+}
+
+template <class T, int D, bool TURN>
+__device__ __forceinline__ void e4m3_head(const RotaryArgs& a, const Unit& u, const float2* table, const Held<T>& held, const Pair& p,
+                                          uint8_t* dst, long long dst_row, uint8_t* block0, int off, float* scale, uint32_t* tops, int team,
+                                          int warp, int lane, int tl)
+{
+    constexpr int L = D / 16;
+    const int r0 = tl / L, pass = team * 32 / L;
+    const int row_bytes = a.Hkv * D;
+    const Pieces<T>(&raw)[kHeld] = held.rows;
     uint32_t old = 0;
     if (block0 && off > 0) old = __float_as_uint(*reinterpret_cast<volatile float*>(scale)) & 0x7FFFFFFFu;
     uint32_t top = 0;
@@ -437,26 +448,30 @@ __device__ __forceinline__ void units_part(const RotaryArgs& a, const int32_t* c
         }
         int page, slot;
         const bool there = place_of(a, u.n, u.pos, page, slot);    // (a block lies in one page)
-        __syncthreads();
+        const int b = there ? slot / a.block : 0, off = there ? slot - b * a.block : 0;
+        const long long block_at = there ? page * a.page_bytes + (long long)b * a.block * a.Hkv * D : 0;
+        const long long scale_at = there ? ((long long)page * (a.page_size / a.block) + b) * a.Hkv : 0;
+        const int step = a.splits * teams, tl = (warp % a.team) * 32 + lane;
+        int task = split * teams + warp / a.team;
+        const Pair turned = pair_of(tl % (D / 16), a.rot, a.interleaved), plain = pair_of(tl % (D / 16), 0, false);
+        auto load = [&](int t) {
+            const bool is_k = t < a.Hkv;
+            const long long at = (long long)(is_k ? t : t - a.Hkv) * D * (int)sizeof(T);
+            return e4m3_load<T, D>(u, is_k ? turned : plain, (is_k ? a.k : a.v) + at, is_k ? a.k_row : a.v_row, a.team, tl);
+        };
+        __syncthreads();                           // the table is there
 #pragma unroll 1
-        for (int task = split * teams + warp / a.team; task < 2 * a.Hkv; task += a.splits * teams) {
+        for (; task < 2 * a.Hkv; task += step) {
+            const Held<T> held = load(task);
             const bool is_k = task < a.Hkv;
             const int hk = is_k ? task : task - a.Hkv;
-            const long long at = (long long)hk * D * (int)sizeof(T);
-            uint8_t* block0 = nullptr;
-            float* scale = nullptr;
-            int off = 0;
-            if (there) {
-                const int b = slot / a.block;
-                off = slot - b * a.block;
-                block0 = (is_k ? a.k_cache : a.v_cache) + page * a.page_bytes + (long long)b * a.block * a.Hkv * D + hk * D;
-                scale = (is_k ? a.k_scales : a.v_scales) + ((long long)page * (a.page_size / a.block) + b) * a.Hkv + hk;
-            }
+            uint8_t* block0 = there ? (is_k ? a.k_cache : a.v_cache) + block_at + hk * D : nullptr;
+            float* scale = (is_k ? a.k_scales : a.v_scales) + scale_at + hk;
             if (is_k)
-                e4m3_head<T, D, true>(a, u, table, a.k + at, a.k_row, a.k_out ? a.k_out + at : nullptr, a.k_out_row, block0, off, scale,
-                                      sh_tops, a.team, warp, lane);
-            else if (there)
-                e4m3_head<T, D, false>(a, u, table, a.v + at, a.v_row, nullptr, 0, block0, off, scale, sh_tops, a.team, warp, lane);
+                e4m3_head<T, D, true>(a, u, table, held, turned, a.k_out ? a.k_out + (long long)hk * D * (int)sizeof(T) : nullptr, a.k_out_row,
+                                      block0, off, scale, sh_tops, a.team, warp, lane, tl);
+            else
+                e4m3_head<T, D, false>(a, u, table, held, plain, nullptr, 0, block0, off, scale, sh_tops, a.team, warp, lane, tl);
         }
         __syncthreads();
     }
@@ -518,10 +533,10 @@ cudaError_t launch_cache_append_rotary(RotaryArgs a, int32_t d, bool bf16, int s
 {
     long long units = 0;
     if (a.block) {
-        // As many rows per thread block as a unit has, fewer when that would leave SMs idle (one
-        // per block with few tokens); then the heads are spread over more blocks too.
-        const int spread = a.T / (2 * sms);
-        a.window = spread < 1 ? 1 : spread > a.block ? a.block : spread;
+        // As many rows per thread block as a unit has on the average (every sequence may begin one
+        // in the middle of a block); with few units their heads are spread over more blocks.
+        const long long rows = a.T / ((long long)a.T / a.block + a.N);
+        a.window = rows < 1 ? 1 : rows > a.block ? a.block : (int)rows;
         const int lanes = a.block * (d / 16);      // of a block's rows
         a.team = 1;
         while (a.team * 32 * kHeld < lanes) a.team *= 2;
