@@ -523,14 +523,16 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// ------------------------------------------- whole groups of 16 rows, one scale each
-// The same where 16 rows from a multiple of 16 on lie in one page and one block of
-// scales: a warp's step is two such groups (32 keys), each of whose keys and values come
-// as one TMA box, with one scale, so that s = (c ks) S is one factor per row and
-// group and the step has half the instructions per key.  The pages' boxes come in the
+// ------------------------------------------------- whole groups of rows, one scale each
+// The same where SUB = 16 or 8 rows from a multiple of SUB on lie in one page and one
+// block of scales: a warp's step is two groups of 16 keys, whose keys and values come as
+// TMA boxes of SUB rows with one scale each, so that s = (c ks) S is one factor per row
+// and box and the step has half the instructions per key.  The pages' boxes come in the
 // swizzle of their row size, which is that of row_at above.
 constexpr int kStepGroups = 2;
 constexpr int kGroupKT = kWarps * kStepGroups * kKeys;
+// Lead of 1, 2, 4 and 8 tiles, us: 32 x 4 tokens, contexts of 100 to 16,384 rows, 127.5,
+// 116.3, 118.0 and 122.6; 64 x 1 token 385.6, 383.7, 387.2 and 395.8.
 constexpr int kGroupLead = 2;
 constexpr int kSlots = 6;                          // groups of a warp's ring
 using GroupPiece = TreePieces<kGroupKT, kGroupLead>;
@@ -553,40 +555,37 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
-// The walk of a warp's copies, a step at a time; the page numbers of a step are loaded
-// when it is entered, one before they are used.
+// The walk of a warp's copies, a step at a time; a lane's part of it is box lane %
+// kBoxes of the step, whose page number is loaded when the step is entered, one before
+// it is used.
+template <int SUB>
 struct GroupWalk {
+    static constexpr int kBoxes = kStepGroups * kKeys / SUB;
     GroupPiece w;
     bool go;
-    int t, pos, p, slot;
-    int page[kStepGroups];
+    int t, pos, p, slot, page;
 
     __device__ __forceinline__ void look_up(const E4m3Args& a)
     {
-#pragma unroll
-        for (int i = 0; i < kStepGroups; ++i) {
-            page[i] = -1;
-            const bool over = slot + i * kKeys >= a.split.page_size;
-            if (go && pos + i * kKeys < w.ctx)
-                page[i] = __ldg(a.split.page_table + (long long)w.n * a.split.max_pages + p + (over ? 1 : 0));
-        }
+        page = -1;
+        if (go && pos < w.ctx) page = __ldg(a.split.page_table + (long long)w.n * a.split.max_pages + p);
     }
-    __device__ __forceinline__ void enter(const E4m3Args& a, int warp)
+    __device__ __forceinline__ void enter(const E4m3Args& a, int warp, int lane)
     {
         if (go) {
             t = w.t0;
-            pos = t * kGroupKT + warp * (kStepGroups * kKeys);
+            pos = t * kGroupKT + warp * (kStepGroups * kKeys) + lane % kBoxes * SUB;
             p = pos / a.split.page_size;
             slot = pos - p * a.split.page_size;
         }
         look_up(a);
     }
-    __device__ __forceinline__ void step(const E4m3Args& a, int warp)
+    __device__ __forceinline__ void step(const E4m3Args& a, int warp, int lane)
     {
         if (!go) return;
         if (++t == w.t1) {
             go = w.next(a.split);
-            enter(a, warp);
+            enter(a, warp, lane);
             return;
         }
         pos += kGroupKT;
@@ -602,43 +601,49 @@ struct GroupWalk {
 
 struct GroupShared {
     uint64_t full[kWarps][kSlots];
-    int scale[kWarps][kSlots];                     // of a group: the place of its scales; -1: no rows
+    int scale[kWarps][kSlots][2];                  // of a box: the place of its scales; -1: no rows
     long long loc[kWarps + 2];
     int dead;
 };
 
-// Starts the copies of the walk's step into two slots.  What no row fills is zeros.
-template <int D>
+// Starts the copies of the walk's step into two slots, a box by a lane.  What no row fills
+// is zeros.
+template <int D, int SUB>
 __device__ __forceinline__ void start_groups(GroupShared& sh, const E4m3Args& a, const CUtensorMap* map_k,
-                                             const CUtensorMap* map_v, const GroupWalk& k, uint32_t ring, int first, int warp,
+                                             const CUtensorMap* map_v, const GroupWalk<SUB>& k, uint32_t ring, int first, int warp,
                                              int lane)
 {
+    constexpr int S = kKeys / SUB, kBoxes = GroupWalk<SUB>::kBoxes;
     if (!k.go) return;
-#pragma unroll
-    for (int i = 0; i < kStepGroups; ++i) {
-        const int at = first + i;
-        const uint32_t dst = ring + at * GroupShape<D>::kSlotBytes;
-        int row = k.slot + i * kKeys;
-        if (row >= a.split.page_size) row -= a.split.page_size;
-        if (k.page[i] >= 0 && k.page[i] < a.num_pages) {
-            if (lane == 0) {
-                const int b = a.block == 1 ? row : (int)__umulhi((uint32_t)row, a.block_magic);
-                sh.scale[warp][at] = (k.page[i] * a.blocks + b) * a.split.Hkv + k.w.hk;
-                mbar_arrive_expect_tx(&sh.full[warp][at], 2 * kKeys * D);
-                load_box(dst, map_k, k.w.hk, row, k.page[i], &sh.full[warp][at]);
-                load_box(dst + kKeys * D, map_v, k.w.hk, row, k.page[i], &sh.full[warp][at]);
-            }
-        } else {
+    const int at = first + lane % kBoxes / S, sub = lane % S;
+    const uint32_t dst = ring + at * GroupShape<D>::kSlotBytes + sub * SUB * D;
+    uint64_t* bar = &sh.full[warp][at];
+    const bool there = k.page >= 0 && k.page < a.num_pages;
+    if (lane < kBoxes) {
+        int place = -1;
+        if (there) {
+            const int b = (int)__umulhi((uint32_t)k.slot, a.block_magic);
+            place = (k.page * a.blocks + b) * a.split.Hkv + k.w.hk;
+            mbar_arrive_expect_tx(bar, 2 * SUB * D);
+            load_box(dst, map_k, k.w.hk, k.slot, k.page, bar);
+            load_box(dst + kKeys * D, map_v, k.w.hk, k.slot, k.page, bar);
+        }
+        sh.scale[warp][at][sub] = place;
+    }
+    uint32_t gone = __ballot_sync(0xffffffffu, lane < kBoxes && !there);
+    if (gone) {
 #pragma unroll 1
-            for (int e = lane; e < 2 * kKeys * D / 16; e += 32)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + e * 16), "r"(0) : "memory");
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                sh.scale[warp][at] = -1;
-                mbar_arrive(&sh.full[warp][at]);
+        for (uint32_t left = gone; left; left &= left - 1) {
+            const uint32_t to = __shfl_sync(0xffffffffu, dst, __ffs(left) - 1);
+#pragma unroll 1
+            for (int e = lane; e < SUB * D / 16; e += 32) {
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to + e * 16), "r"(0) : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to + kKeys * D + e * 16), "r"(0) : "memory");
             }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if ((gone >> lane) & 1) mbar_arrive(bar);
     }
     __syncwarp();
 }
@@ -685,7 +690,7 @@ __device__ __forceinline__ void store_run(__nv_bfloat16* p, const float (&y)[N])
     }
 }
 
-template <class T, class O, int D>
+template <class T, class O, int D, int SUB>
 __global__ void __launch_bounds__(kThreads, 1)
 cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_constant__ CUtensorMap map_k,
                              const __grid_constant__ CUtensorMap map_v)
@@ -694,6 +699,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
     constexpr bool QLO = sizeof(T) == 4, PLO = sizeof(O) == 4;
     constexpr int KS = D / 16, NT = D / 8;
     constexpr int KB = D / 4 < 16 ? D / 4 : 16;    // bytes per read of a row of K
+    constexpr int S = kKeys / SUB;                 // boxes, and scales, of a group
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ GroupShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -701,19 +707,19 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
     const int group = blockIdx.x / a.split.row_tiles, r0 = (blockIdx.x % a.split.row_tiles) * kRows;
     if (lane == 0) {
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&sh.full[warp][i], 1);
-            sh.scale[warp][i] = -1;
+            mbar_init(&sh.full[warp][i], S);
+            sh.scale[warp][i][0] = sh.scale[warp][i][1] = -1;
         }
         if (warp == 0) sh.dead = 0;
         fence_mbar_init();
     }
     const TreeSpot sp = tree_locate<kThreads, kGroupKT, kGroupLead>(a.split, group, sh.loc);   // has block barriers
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    GroupWalk ahead;
+    GroupWalk<SUB> ahead;
     ahead.go = ahead.w.start(a.split, sp, group);
     GroupPiece w = ahead.w;
     bool go = ahead.go;
-    ahead.enter(a, warp);
+    ahead.enter(a, warp, lane);
     const uint32_t base = (smem_at(dyn) + 1023u) & ~1023u;
     const uint32_t ring = base + warp * kSlots * Sh::kSlotBytes;
     float* join = reinterpret_cast<float*>(dyn + (base - smem_at(dyn)) + Sh::kRing);
@@ -721,18 +727,20 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
     uint32_t turn = 0;
 #pragma unroll 1
     for (int i = 0; i < kSlots; i += kStepGroups) {
-        start_groups<D>(sh, a, &map_k, &map_v, ahead, ring, i, warp, lane);
-        ahead.step(a, warp);
+        start_groups<D, SUB>(sh, a, &map_k, &map_v, ahead, ring, i, warp, lane);
+        ahead.step(a, warp, lane);
     }
     // the next step's scales
-    float ks[kStepGroups], vs[kStepGroups];
+    float ks[kStepGroups][S], vs[kStepGroups][S];
     auto load_scales = [&](int first) {
 #pragma unroll
-        for (int i = 0; i < kStepGroups; ++i) {
-            const int at = sh.scale[warp][first + i];
-            ks[i] = at >= 0 ? __ldg(a.k_scales + at) : -1.f;       // (-1: no rows)
-            vs[i] = at >= 0 ? __ldg(a.v_scales + at) : 0.f;
-        }
+        for (int i = 0; i < kStepGroups; ++i)
+#pragma unroll
+            for (int b = 0; b < S; ++b) {
+                const int at = sh.scale[warp][first + i][b];
+                ks[i][b] = at >= 0 ? __ldg(a.k_scales + at) : -1.f;        // (-1: no rows)
+                vs[i][b] = at >= 0 ? __ldg(a.v_scales + at) : 0.f;
+            }
     };
     if (go) load_scales(0);
     for (; go; go = w.next(a.split)) {
@@ -792,11 +800,20 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
             for (int i = 0; i < kStepGroups; ++i) wait_group(sh, &sh.full[warp][out + i], turn);
             __syncwarp();
             const uint32_t st = ring + out * Sh::kSlotBytes;
-            const float ksn[kStepGroups] = {ks[0], ks[1]}, vsn[kStepGroups] = {vs[0], vs[1]};
+            float ksn[kStepGroups][S], vsn[kStepGroups][S];
+            bool gaps = false;
+#pragma unroll
+            for (int i = 0; i < kStepGroups; ++i)
+#pragma unroll
+                for (int b = 0; b < S; ++b) {
+                    ksn[i][b] = ks[i][b];
+                    vsn[i][b] = vs[i][b];
+                    gaps |= ks[i][b] < 0.f;
+                }
             const int next = out + kStepGroups == kSlots ? 0 : out + kStepGroups;
             load_scales(next);                     // (of the last step: whatever is there)
             const int pos = t * kGroupKT + warp * (kStepGroups * kKeys);
-            const bool masked = pos + kStepGroups * kKeys > all || ksn[0] < 0.f || ksn[1] < 0.f;   // (the same for the warp)
+            const bool masked = pos + kStepGroups * kKeys > all || gaps;     // (the same for the warp)
             if (masked && pos + kStepGroups * kKeys > w.ctx) {
                 // values past the last row, whatever the page holds there
 #pragma unroll
@@ -839,12 +856,14 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                             if constexpr (QLO) mma(c[i][b], ql[s], b0, b1);
                         }
             }
-            float k1[kStepGroups][2], top[2], vtop[2];
+            float k1[kStepGroups][S][2], top[2], vtop[2];
             bool grow = false;
 #pragma unroll
             for (int i = 0; i < kStepGroups; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) k1[i][h] = ksn[i] * rs[h];
+                for (int b = 0; b < S; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) k1[i][b][h] = ksn[i][b] * rs[h];
             if (masked) {
 #pragma unroll
                 for (int i = 0; i < kStepGroups; ++i)
@@ -855,20 +874,29 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 float& x = c[i][b][2 * h + j];
-                                x *= k1[i][h];
-                                if (ksn[i] < 0.f || pos + i * kKeys + 8 * b + i4 + 4 * j >= lim[h]) x = -INFINITY;
+                                x *= k1[i][b % S][h];
+                                if (ksn[i][b % S] < 0.f || pos + i * kKeys + 8 * b + i4 + 4 * j >= lim[h]) x = -INFINITY;
                             }
-                        k1[i][h] = 1.f;
+#pragma unroll
+                        for (int b = 0; b < S; ++b) k1[i][b][h] = 1.f;
                     }
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float tops[kStepGroups];
+                top[h] = vtop[h] = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < kStepGroups; ++i)
-                    tops[i] = fmaxf(fmaxf(c[i][0][2 * h], c[i][0][2 * h + 1]), fmaxf(c[i][1][2 * h], c[i][1][2 * h + 1])) * k1[i][h];
-                top[h] = fmaxf(tops[0], tops[1]);
-                vtop[h] = fmaxf(tops[0] + lg2(vsn[0]), tops[1] + lg2(vsn[1]));
+                for (int i = 0; i < kStepGroups; ++i) {
+                    float tops[2];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) tops[b] = fmaxf(c[i][b][2 * h], c[i][b][2 * h + 1]);
+                    if (S == 1) tops[0] = fmaxf(tops[0], tops[1]);
+#pragma unroll
+                    for (int b = 0; b < S; ++b) {
+                        const float x = tops[b] * k1[i][b][h];
+                        top[h] = fmaxf(top[h], x);
+                        vtop[h] = fmaxf(vtop[h], x + lg2(vsn[i][b]));
+                    }
+                }
                 grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + kSlack;
             }
             if (__any_sync(0xffffffffu, grow)) {
@@ -895,14 +923,14 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                 const float ref = m[h] == -INFINITY ? 0.f : m[h];
 #pragma unroll
                 for (int i = 0; i < kStepGroups; ++i) {
-                    const float w1 = vsn[i] * fac[h];
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
+                        const float w1 = vsn[i][b % S] * fac[h];
                         float y[2];
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const float x = c[i][b][2 * h + j];
-                            const float p = ex2(fmaf(x, k1[i][h], -ref));
+                            const float p = ex2(fmaf(x, k1[i][b % S][h], -ref));
                             l[h] += p;
                             y[j] = p * w1;
                             if (masked && x == -INFINITY) y[j] = 0.f;
@@ -935,8 +963,8 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                 }
             }
             __syncwarp();                          // the slots have been read
-            start_groups<D>(sh, a, &map_k, &map_v, ahead, ring, out, warp, lane);
-            ahead.step(a, warp);
+            start_groups<D, SUB>(sh, a, &map_k, &map_v, ahead, ring, out, warp, lane);
+            ahead.step(a, warp, lane);
             out = next;
             turn ^= next == 0;
         }
@@ -1098,15 +1126,15 @@ cudaError_t launch_join(const E4m3Args& a, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, cache_join_kernel<O, D, KT, LEAD>, a);
 }
 
-// The pool as [num_pages][page_size][Hkv][d] bytes, boxes of 16 rows of one head.
-bool make_pool_map(CUtensorMap* m, const uint8_t* base, const E4m3Args& a, int d)
+// The pool as [num_pages][page_size][Hkv][d] bytes, boxes of `box` rows of one head.
+bool make_pool_map(CUtensorMap* m, const uint8_t* base, const E4m3Args& a, int d, int box)
 {
     const auto fn = tc_encode_fn();
     if (!fn) return false;
     const cuuint64_t row = (cuuint64_t)a.split.Hkv * d, size = a.split.page_size;
     const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)a.split.Hkv, size, (cuuint64_t)a.num_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)d, row, a.num_pages > 1 ? (cuuint64_t)a.page_stride : row * size};
-    const cuuint32_t boxes[4] = {(cuuint32_t)d, 1, kKeys, 1}, steps[4] = {1, 1, 1, 1};
+    const cuuint32_t boxes[4] = {(cuuint32_t)d, 1, (cuuint32_t)box, 1}, steps[4] = {1, 1, 1, 1};
     const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, boxes, steps,
                           CU_TENSOR_MAP_INTERLEAVE_NONE,
                           d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -1118,31 +1146,36 @@ bool make_pool_map(CUtensorMap* m, const uint8_t* base, const E4m3Args& a, int d
     return r == CUDA_SUCCESS;
 }
 
+template <class T, class O, int D, int SUB>
+cudaError_t launch_groups(E4m3Args a, const CUtensorMap& map_k, const CUtensorMap& map_v, cudaStream_t stream)
+{
+    auto kern = cache_attention_group_kernel<T, O, D, SUB>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GroupShape<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    a.tile_pages = kGroupKT / a.split.page_size;
+    a.tile_rows = kGroupKT % a.split.page_size;
+    kern<<<a.split.groups * a.split.row_tiles, kThreads, GroupShape<D>::kBytes, stream>>>(a, map_k, map_v);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join<O, D, kGroupKT, kGroupLead>(a, stream);
+}
+
 template <class T, class O, int D>
 cudaError_t launch(E4m3Args a, cudaStream_t stream)
 {
-    const int blocks = a.split.groups * a.split.row_tiles;
-    // 16 rows from a multiple of 16 on in one page and one block of scales
+    // 16 or 8 rows from a multiple of that on in one page and one block of scales
+    const int box = a.split.page_size % 16 == 0 && a.block % 16 == 0 ? 16 : 8;
     CUtensorMap map_k, map_v;
-    if (a.split.page_size % kKeys == 0 && a.block % kKeys == 0 && (long long)a.num_pages * a.blocks * a.split.Hkv <= INT32_MAX &&
-        make_pool_map(&map_k, a.k_cache, a, D) && make_pool_map(&map_v, a.v_cache, a, D)) {
-        auto kern = cache_attention_group_kernel<T, O, D>;
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GroupShape<D>::kBytes);
-        if (e != cudaSuccess) return e;
-        a.tile_pages = kGroupKT / a.split.page_size;
-        a.tile_rows = kGroupKT % a.split.page_size;
-        kern<<<blocks, kThreads, GroupShape<D>::kBytes, stream>>>(a, map_k, map_v);
-        const cudaError_t e2 = cudaGetLastError();
-        return e2 != cudaSuccess ? e2 : launch_join<O, D, kGroupKT, kGroupLead>(a, stream);
-    }
+    if (a.split.page_size % box == 0 && a.block % box == 0 && (long long)a.num_pages * a.blocks * a.split.Hkv <= INT32_MAX &&
+        make_pool_map(&map_k, a.k_cache, a, D, box) && make_pool_map(&map_v, a.v_cache, a, D, box))
+        return box == 16 ? launch_groups<T, O, D, 16>(a, map_k, map_v, stream) : launch_groups<T, O, D, 8>(a, map_k, map_v, stream);
     auto kern = cache_attention_kernel<T, O, D>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kBytes);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kBytes);
     if (e != cudaSuccess) return e;
     a.tile_pages = KT / a.split.page_size;
     a.tile_rows = KT % a.split.page_size;
-    kern<<<blocks, kThreads, Shape<D>::kBytes, stream>>>(a);
-    const cudaError_t e2 = cudaGetLastError();
-    return e2 != cudaSuccess ? e2 : launch_join<O, D, KT, kLead>(a, stream);
+    kern<<<a.split.groups * a.split.row_tiles, kThreads, Shape<D>::kBytes, stream>>>(a);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join<O, D, KT, kLead>(a, stream);
 }
 
 template <class T, class O>
