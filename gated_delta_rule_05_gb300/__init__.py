@@ -756,17 +756,33 @@ def kda_cache_append(k, v, cu_seqlens, k_cache, v_cache, page_table, lengths, *,
                         v_cache, page_table, lengths, new_lengths, (), stream)
 
 
+# Checks in the calls below are made twice: first all of them as one condition of plain
+# attribute reads (a call of theirs takes longer than most of them), then, when that does
+# not hold, one by one for the error that says what is wrong.
+def _rows_stride(t, h, d):
+    """The stride of tokens [T, h, d] that are dense within a token; -1: they are not."""
+    row, head, one = t.stride()
+    if (one != 1 and d > 1) or (head != d and h > 1):
+        if t.numel():
+            return -1
+    return row if t.shape[0] > 1 else h * d
+
+
 def _check_rows(name, t, dtype, device):
-    """Tokens [T, h, d] at any stride, dense within a token; the stride."""
+    """Tokens [T, h, d] at any stride, dense within a token."""
     if not t.is_cuda or t.device != device:
         raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    T, h, d = t.shape
-    row, head, one = t.stride()
-    if t.numel() and ((one != 1 and d > 1) or (head != d and h > 1)):
+    if _rows_stride(t, t.shape[1], t.shape[2]) < 0:
         raise ValueError("%s must be dense within a token" % name)
-    return row if T > 1 else h * d
+
+
+def _check_on(name, t, dtype, device):
+    """A contiguous tensor on ``device``."""
+    if t is not None and t.device != device:
+        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
+    _check_cuda(name, t, dtype)
 
 
 def kda_prompt_attention_workspace_bytes(num_seqs: int, Hq: int, Hkv: int, d: int,
@@ -796,27 +812,34 @@ def kda_prompt_attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=N
     _forward_only("kda_prompt_attention", q, k, v)
     T, Hq, d = q.shape
     Tk, Hkv, _ = k.shape
-    dev = q.device
+    dev, at, dtype = q.device, q.get_device(), q.dtype
     if o_dtype is None:
-        o_dtype = o.dtype if o is not None else q.dtype
+        o_dtype = dtype if o is None else o.dtype
     dt = _dtype_code(q, o_dtype)
-    strides = [_check_rows(name, t, q.dtype, dev) for name, t in (("q", q), ("k", k), ("v", v))]
-    _check_cuda("cu_seqlens", cu_seqlens, torch.int32)
-    _check_cuda("cu_seqlens_k", cu_seqlens_k, torch.int32)
-    _shape("k", k, (Tk, Hkv, d))
-    _shape("v", v, (Tk, Hkv, d))
     N = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    if cu_seqlens_k is not None:
+    strides = _rows_stride(q, Hq, d), _rows_stride(k, Hkv, d), _rows_stride(v, v.shape[1], d)
+    if not (at >= 0 and k.get_device() == at and v.get_device() == at and k.dtype is dtype
+            and v.dtype is dtype and k.shape[2] == d and v.shape == k.shape and min(strides) >= 0
+            and (Tk == T if cu_seqlens_k is None else
+                 cu_seqlens is not None and cu_seqlens_k.shape == cu_seqlens.shape)
+            and all(c is None or (c.get_device() == at and c.dtype is torch.int32
+                                  and c.is_contiguous()) for c in (cu_seqlens, cu_seqlens_k))):
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            _check_rows(name, t, dtype, dev)
+        _check_on("cu_seqlens", cu_seqlens, torch.int32, dev)
+        _check_on("cu_seqlens_k", cu_seqlens_k, torch.int32, dev)
+        _shape("k", k, (Tk, Hkv, d))
+        _shape("v", v, (Tk, Hkv, d))
+        if cu_seqlens_k is None:
+            raise ValueError("k must have q's tokens, or cu_seqlens_k be given")
         if cu_seqlens is None:
             raise ValueError("cu_seqlens_k needs cu_seqlens")
         _shape("cu_seqlens_k", cu_seqlens_k, cu_seqlens.shape)
-    elif Tk != T:
-        raise ValueError("k must have q's tokens, or cu_seqlens_k be given")
     o = _out("o", o, (T, Hq, d), o_dtype, dev, stream)
     if workspace is None:
         workspace = _new((_prompt_bytes(N, Hq, Hkv, d, dt),), torch.uint8, dev, stream)
     else:
-        _check_cuda("workspace", workspace)
+        _check_on("workspace", workspace, None, dev)
     _call("kda_prompt_attention", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
           _address(cu_seqlens), _address(cu_seqlens_k), N, T, Tk, Hq, Hkv, d, dt,
           d ** -0.5 if scale is None else scale, o.data_ptr(), workspace.data_ptr(),
@@ -825,15 +848,49 @@ def kda_prompt_attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=N
 
 
 def _check_scales(name, t, pages, page, Hkv, device):
-    """The scales of a cache of 8 bits; the rows of a block."""
+    """The scales of a cache of 8 bits."""
     torch = _torch()
-    if t is None or t.device != device:
-        raise ValueError("%s must be given, on %s" % (name, device))
-    _check_cuda(name, t, torch.float32)
+    if t is None:
+        raise ValueError("%s must be given for a cache of float8_e4m3fn" % name)
+    _check_on(name, t, torch.float32, device)
     _shape(name, t, (pages, t.shape[1], Hkv))
     if t.shape[1] < 1 or page % t.shape[1] != 0:
         raise ValueError("%s: %d blocks do not divide a page of %d rows" % (name, t.shape[1], page))
-    return page // t.shape[1]
+
+
+def _pages_ok(k_cache, v_cache, dtype, at, h, d):
+    """k_cache and v_cache are pools that the kernels take, with the same strides."""
+    shape, stride = k_cache.shape, k_cache.stride()
+    return (k_cache.dtype is dtype and v_cache.dtype is dtype and k_cache.get_device() == at
+            and v_cache.get_device() == at and len(shape) == 4 and shape[2:] == (h, d)
+            and v_cache.shape == shape and stride[1:] == (h * d, d, 1)
+            and v_cache.stride() == stride)
+
+
+def _scales_ok(k_scales, v_scales, f32, at, pages, page, h):
+    return (k_scales is not None and v_scales is not None and k_scales.dtype is f32
+            and v_scales.dtype is f32 and k_scales.get_device() == at
+            and v_scales.get_device() == at and k_scales.is_contiguous()
+            and v_scales.is_contiguous() and v_scales.shape == k_scales.shape
+            and k_scales.shape == (pages, k_scales.shape[1], h) and k_scales.shape[1] > 0
+            and page % k_scales.shape[1] == 0)
+
+
+def _explain_pages(k_cache, v_cache, k_scales, v_scales, dtype, h, d, dev):
+    """Raises what is wrong with a cache, if anything is."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check_pages(name, t, dtype, dev)
+        _shape(name, t, (k_cache.shape[0], k_cache.shape[1], h, d))
+    pages, page = k_cache.shape[:2]
+    if pages > 1 and k_cache.stride(0) != v_cache.stride(0):
+        raise ValueError("k_cache and v_cache must have the same page stride")
+    if dtype == _torch().float8_e4m3fn:
+        _check_scales("k_scales", k_scales, pages, page, h, dev)
+        _check_scales("v_scales", v_scales, pages, page, h, dev)
+        if v_scales.shape != k_scales.shape:
+            raise ValueError("k_scales and v_scales must have the same blocks")
+    elif k_scales is not None or v_scales is not None:
+        raise ValueError("k_scales and v_scales belong to a cache of float8_e4m3fn")
 
 
 def kda_cache_append_rotary(q, k, v, cu_seqlens, inv_freq, k_cache, v_cache, page_table, lengths,
@@ -853,58 +910,73 @@ def kda_cache_append_rotary(q, k, v, cu_seqlens, inv_freq, k_cache, v_cache, pag
     torch = _torch()
     _forward_only("kda_cache_append_rotary", k, v, inv_freq, *(() if q is None else (q,)))
     T, Hkv, d = k.shape
-    dev = k.device
-    if k.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError("unsupported dtype %s" % k.dtype)
-    dt = KDA_BF16 if k.dtype == torch.bfloat16 else KDA_FP32
-    k_stride, v_stride = _check_rows("k", k, k.dtype, dev), _check_rows("v", v, k.dtype, dev)
-    _shape("v", v, (T, Hkv, d))
-    for name, t in (("cu_seqlens", cu_seqlens), ("page_table", page_table), ("lengths", lengths)):
-        _check_cuda(name, t, torch.int32)
-    _check_cuda("inv_freq", inv_freq, torch.float32)
-    _shape("inv_freq", inv_freq, (inv_freq.shape[0],))
-    N = lengths.shape[0]
-    _shape("lengths", lengths, (N,))
-    _shape("cu_seqlens", cu_seqlens, (N + 1,))
-    _shape("page_table", page_table, (N, page_table.shape[1]))
-    eight = k_cache.dtype == torch.float8_e4m3fn
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check_pages(name, t, torch.float8_e4m3fn if eight else k.dtype, dev)
-        _shape(name, t, (k_cache.shape[0], k_cache.shape[1], Hkv, d))
-    pages, page = k_cache.shape[:2]
-    if pages > 1 and k_cache.stride(0) != v_cache.stride(0):
-        raise ValueError("k_cache and v_cache must have the same page stride")
-    block = 0
-    if eight:
-        block = _check_scales("k_scales", k_scales, pages, page, Hkv, dev)
-        if _check_scales("v_scales", v_scales, pages, page, Hkv, dev) != block:
-            raise ValueError("k_scales and v_scales must have the same blocks")
-    elif k_scales is not None or v_scales is not None:
-        raise ValueError("k_scales and v_scales belong to a cache of float8_e4m3fn")
+    dev, at, dtype = k.device, k.get_device(), k.dtype
+    i32, f32 = torch.int32, torch.float32
+    if dtype is torch.bfloat16:
+        dt = KDA_BF16
+    elif dtype is f32:
+        dt = KDA_FP32
+    else:
+        raise TypeError("unsupported dtype %s" % dtype)
+    N, max_pages = lengths.shape[0], page_table.shape[1]
+    eight = k_cache.dtype is torch.float8_e4m3fn
+    held = k_cache.dtype if eight else dtype
+    pages, page = k_cache.shape[0], k_cache.shape[1]
+    k_stride, v_stride = _rows_stride(k, Hkv, d), _rows_stride(v, v.shape[1], d)
+    if not (at >= 0 and v.get_device() == at and v.dtype is dtype and v.shape == k.shape
+            and k_stride >= 0 and v_stride >= 0
+            and cu_seqlens.get_device() == at and cu_seqlens.dtype is i32
+            and cu_seqlens.is_contiguous() and cu_seqlens.shape == (N + 1,)
+            and lengths.get_device() == at and lengths.dtype is i32 and lengths.is_contiguous()
+            and lengths.shape == (N,)
+            and page_table.get_device() == at and page_table.dtype is i32
+            and page_table.is_contiguous() and page_table.shape == (N, max_pages)
+            and inv_freq.get_device() == at and inv_freq.dtype is f32 and inv_freq.dim() == 1
+            and inv_freq.is_contiguous()
+            and _pages_ok(k_cache, v_cache, held, at, Hkv, d)
+            and (_scales_ok(k_scales, v_scales, f32, at, pages, page, Hkv) if eight else
+                 k_scales is None and v_scales is None)):
+        for name, t in (("k", k), ("v", v)):
+            _check_rows(name, t, dtype, dev)
+        _shape("v", v, (T, Hkv, d))
+        for name, t in (("cu_seqlens", cu_seqlens), ("page_table", page_table), ("lengths", lengths)):
+            _check_on(name, t, i32, dev)
+        _check_on("inv_freq", inv_freq, f32, dev)
+        _shape("inv_freq", inv_freq, (inv_freq.shape[0],))
+        _shape("lengths", lengths, (N,))
+        _shape("cu_seqlens", cu_seqlens, (N + 1,))
+        _shape("page_table", page_table, (N, max_pages))
+        _explain_pages(k_cache, v_cache, k_scales, v_scales, held, Hkv, d, dev)
     Hq = q_stride = q_out_stride = k_out_stride = 0
     if q is not None:
         Hq = q.shape[1]
-        q_stride = _check_rows("q", q, k.dtype, dev)
-        _shape("q", q, (T, Hq, d))
         if q_out is None:
-            q_out = _new((T, Hq, d), k.dtype, dev, stream)
-        q_out_stride = _check_rows("q_out", q_out, k.dtype, dev)
-        _shape("q_out", q_out, (T, Hq, d))
+            q_out = _new((T, Hq, d), dtype, dev, stream)
+        q_stride, q_out_stride = _rows_stride(q, Hq, d), _rows_stride(q_out, q_out.shape[1], d)
+        if not (q.get_device() == at and q.dtype is dtype and q.shape == (T, Hq, d)
+                and q_stride >= 0 and q_out.get_device() == at and q_out.dtype is dtype
+                and q_out.shape == q.shape and q_out_stride >= 0):
+            for name, t in (("q", q), ("q_out", q_out)):
+                _check_rows(name, t, dtype, dev)
+                _shape(name, t, (T, Hq, d))
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if k_out is None and want_k:
-        k_out = _new((T, Hkv, d), k.dtype, dev, stream)
+        k_out = _new((T, Hkv, d), dtype, dev, stream)
     if k_out is not None:
-        k_out_stride = _check_rows("k_out", k_out, k.dtype, dev)
-        _shape("k_out", k_out, (T, Hkv, d))
-    new_lengths = _out("new_lengths", new_lengths, (N,), torch.int32, dev, stream)
-    _call("kda_cache_append_rotary", dev, stream, _address(q), k.data_ptr(), v.data_ptr(),
-          q_stride, k_stride, v_stride, cu_seqlens.data_ptr(), T, inv_freq.data_ptr(),
-          2 * inv_freq.shape[0], int(bool(interleaved)), page_table.data_ptr(),
-          lengths.data_ptr(), N, Hq, Hkv, d, pages, page, page_table.shape[1], k_cache.stride(0),
-          block, dt, _address(q_out), q_out_stride, _address(k_out), k_out_stride,
-          k_cache.data_ptr(), v_cache.data_ptr(), _address(k_scales), _address(v_scales),
-          new_lengths.data_ptr())
+        k_out_stride = _rows_stride(k_out, k_out.shape[1], d)
+        if not (k_out.get_device() == at and k_out.dtype is dtype and k_out.shape == k.shape
+                and k_out_stride >= 0):
+            _check_rows("k_out", k_out, dtype, dev)
+            _shape("k_out", k_out, (T, Hkv, d))
+    new_lengths = _out("new_lengths", new_lengths, (N,), i32, dev, stream)
+    _call("kda_cache_append_rotary", dev, stream, None if q is None else q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), q_stride, k_stride, v_stride, cu_seqlens.data_ptr(), T,
+          inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0,
+          page_table.data_ptr(), lengths.data_ptr(), N, Hq, Hkv, d, pages, page, max_pages,
+          k_cache.stride(0), page // k_scales.shape[1] if eight else 0, dt, _address(q_out),
+          q_out_stride, _address(k_out), k_out_stride, k_cache.data_ptr(), v_cache.data_ptr(),
+          _address(k_scales), _address(v_scales), new_lengths.data_ptr())
     return q_out, k_out, new_lengths
 
 
@@ -934,33 +1006,34 @@ def kda_cache_attention_e4m3(q, k_cache, v_cache, k_scales, v_scales, page_table
     torch = _torch()
     _forward_only("kda_cache_attention_e4m3", q, k_scales, v_scales)
     N, Ts, Hq, d = q.shape
-    dev = q.device
+    dev, at = q.device, q.get_device()
+    i32, e4m3 = torch.int32, torch.float8_e4m3fn
     if o_dtype is None:
-        o_dtype = o.dtype if o is not None else q.dtype
+        o_dtype = q.dtype if o is None else o.dtype
     dt = _dtype_code(q, o_dtype)
-    _check_cuda("q", q)
-    for name, t in (("page_table", page_table), ("lengths", lengths)):
-        _check_cuda(name, t, torch.int32)
     pages, page, Hkv, _ = k_cache.shape
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check_pages(name, t, torch.float8_e4m3fn, dev)
-        _shape(name, t, (pages, page, Hkv, d))
-    if pages > 1 and k_cache.stride(0) != v_cache.stride(0):
-        raise ValueError("k_cache and v_cache must have the same page stride")
-    block = _check_scales("k_scales", k_scales, pages, page, Hkv, dev)
-    if _check_scales("v_scales", v_scales, pages, page, Hkv, dev) != block:
-        raise ValueError("k_scales and v_scales must have the same blocks")
-    _shape("page_table", page_table, (N, page_table.shape[1]))
-    _shape("lengths", lengths, (N,))
+    max_pages = page_table.shape[1]
+    if not (at >= 0 and q.is_contiguous() and page_table.get_device() == at
+            and page_table.dtype is i32 and page_table.is_contiguous()
+            and page_table.shape == (N, max_pages) and lengths.get_device() == at
+            and lengths.dtype is i32 and lengths.is_contiguous() and lengths.shape == (N,)
+            and _pages_ok(k_cache, v_cache, e4m3, at, Hkv, d)
+            and _scales_ok(k_scales, v_scales, torch.float32, at, pages, page, Hkv)):
+        _check_cuda("q", q)
+        for name, t in (("page_table", page_table), ("lengths", lengths)):
+            _check_on(name, t, i32, dev)
+        _explain_pages(k_cache, v_cache, k_scales, v_scales, e4m3, Hkv, d, dev)
+        _shape("page_table", page_table, (N, max_pages))
+        _shape("lengths", lengths, (N,))
     o = _out("o", o, (N, Ts, Hq, d), o_dtype, dev, stream)
     if workspace is None:
         workspace = _new((_e4m3_bytes(dev, N, Ts, Hq, Hkv, d, dt),), torch.uint8, dev, stream)
     else:
-        _check_cuda("workspace", workspace)
+        _check_on("workspace", workspace, None, dev)
     _call("kda_cache_attention_e4m3", dev, stream, q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), page_table.data_ptr(),
-          lengths.data_ptr(), N, Ts, Hq, Hkv, d, pages, page, page_table.shape[1],
-          k_cache.stride(0), block, dt, d ** -0.5 if scale is None else scale, o.data_ptr(),
+          lengths.data_ptr(), N, Ts, Hq, Hkv, d, pages, page, max_pages, k_cache.stride(0),
+          page // k_scales.shape[1], dt, d ** -0.5 if scale is None else scale, o.data_ptr(),
           workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return o
 
