@@ -43,10 +43,14 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs& a, int n)
     return s;
 }
 
-// The CUDA-core kernel: every type, head size and scale.
+// All three take every length and layout.  On the CUDA cores in fp32 (KDA_FORCE_SIMT in the
+// environment): every type, head size and scale.
 cudaError_t launch_prompt_attention(const PromptArgs& args, int32_t d, kda_dtype_t dtype, cudaStream_t stream);
 
-// The tensor-core kernel: bf16 in and out, d = 64 or 128, a positive scale (it finds a
+// Products of fp16 pairs: the same, to 22 bits for fp32 inputs or outputs.
+cudaError_t launch_prompt_attention_split(const PromptArgs& args, int32_t d, kda_dtype_t dtype, cudaStream_t stream);
+
+// The tcgen05 kernel: bf16 in and out, d = 64 or 128, a positive scale (it finds a
 // row's maximum before it applies the scale), at most 128 heads to a key head.
 bool prompt_tc_supported(const PromptArgs& args, int32_t d, kda_dtype_t dtype);
 cudaError_t launch_prompt_attention_tc(PromptArgs args, int32_t d, int sms, cudaStream_t stream);

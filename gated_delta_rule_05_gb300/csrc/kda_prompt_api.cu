@@ -132,9 +132,10 @@ kda_status_t kda_prompt_attention(const void* q, const void* k, const void* v, i
     a.status = static_cast<int32_t*>(workspace) + kda::kWsTimeoutWord;
     a.counter = static_cast<uint32_t*>(workspace) + kda::kWsCounterWord;
     const int sms = kda::device_sm_count();
-    const cudaError_t err = kda::prompt_tc_supported(a, d, dtype)
+    const cudaError_t err = getenv("KDA_FORCE_SIMT") != nullptr ? kda::launch_prompt_attention(a, d, dtype, stream)
+                            : kda::prompt_tc_supported(a, d, dtype)
                                 ? kda::launch_prompt_attention_tc(a, d, sms > 0 ? sms : 1, stream)
-                                : kda::launch_prompt_attention(a, d, dtype, stream);
+                                : kda::launch_prompt_attention_split(a, d, dtype, stream);
     return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -1,0 +1,522 @@
+// kda_prompt_attention_split.cu -- causal attention over packed prompts for fp32 (in or
+// out) and for d = 16 and 32: products of fp16 pairs, summed up in fp32.
+//
+// fp32 keeps its accuracy as a sum of two fp16, x = hi + lo (22 bits), in three products
+// hi hi + lo hi + hi lo; bf16 is exact in one, and a bf16 output takes P in one.  fp16's
+// range is met by powers of two, which are exact: one per query row, one per row of
+// keys and one per row of values, from its largest finite magnitude.  With the factors
+// a of the query, b of the key and c of the value
+//     s = scale log2 e a b (Q K^T),  P = 2^(s - m),  w = P c 2^(m - n),  O += w V,
+// m and n references near the running maxima of s and of s + log2 c of a row: P and w
+// stay below 2^8 whatever the values are.  O is in units of 2^n, the sum l of P in
+// units of 2^m.  They move only when a score exceeds them by more than 8.
+//
+// A thread block has 128 query rows of a (sequence, cache head), token by token (row r
+// is head r % G of token r / G), 16 to a warp, and goes through 32 keys at a time: while
+// the products of one tile run, the next is turned into fp16 pairs in shared memory and
+// the one after that is copied by cp.async.  mma.sync m16n8k16 takes 2 clocks on an SM:
+// with three products 190 TFLOP/s at most, where fp32 FMAs give 75.
+//
+// Values of keys that a row does not see must not reach it through 0 * inf: in the tiles
+// on the diagonal infinities and NaN are replaced by 0 and their keys noted; the rows that do see
+// such a key add its value at the end.
+#include <cuda_fp16.h>
+
+#include "kda_prompt.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int BM = kWarps * 16, BN = 32;
+constexpr int kNotes = 8;                          // tiles with rows that some query does not see, at most 6
+constexpr float kSlack = 8.f;
+
+template <class T, class O, int D>
+struct Shape {
+    static constexpr bool kLo = sizeof(T) == 4;    // q, k and v have a second part
+    static constexpr bool kPLo = sizeof(O) == 4;   // and the probabilities
+    static constexpr int kParts = kLo ? 2 : 1;
+    static constexpr int kQ = kParts * BM * D * 2;
+    static constexpr int kHalf = BN * D * 2;       // one part of a tile of keys or values
+    static constexpr int kTile = 2 * kParts * kHalf;
+    static constexpr int kRaw = 2 * BN * D * (int)sizeof(T);
+    static constexpr size_t kBytes = kQ + 2 * kTile + 2 * kRaw;
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
+}
+__device__ __forceinline__ void ldmatrix_t(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
+}
+__device__ __forceinline__ uint32_t two_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float quad_max(float x)
+{
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+// Byte offset of 16-byte piece c of row r of a tile of fp16 rows of D.
+template <int D>
+__device__ __forceinline__ int row_at(int r, int c)
+{
+    constexpr int S = D >= 64 ? 1 : D == 32 ? 2 : 4, M = D >= 64 ? 7 : D == 32 ? 3 : 1;
+    return r * (D * 2) + ((c ^ ((r / S) & M)) << 4);
+}
+
+// Bits of the largest finite magnitude.
+__device__ __forceinline__ uint32_t finite_top(uint32_t top, float x)
+{
+    const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+    return b < 0x7F800000u ? max(top, b) : top;
+}
+// The power of two that brings that magnitude to 2^14 or a little more.
+__device__ __forceinline__ int up_of(uint32_t top) { return top == 0 ? 0 : min(max(14 + 127 - (int)(top >> 23), -100), 100); }
+__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// One 16-byte piece of a row, widened.
+template <class T>
+struct Piece {
+    static constexpr int kN = 16 / (int)sizeof(T);
+    float x[kN];
+};
+__device__ __forceinline__ Piece<float> widen(uint4 w, float)
+{
+    return {{__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)}};
+}
+__device__ __forceinline__ Piece<__nv_bfloat16> widen(uint4 w, __nv_bfloat16)
+{
+    Piece<__nv_bfloat16> p;
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        p.x[2 * i] = __uint_as_float(u[i] << 16);
+        p.x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+    return p;
+}
+
+// The 16-byte piece c of T of row r, times up, as fp16 into the first part of a tile and
+// (LO) what that leaves into the second, `part` bytes on.  Infinities and NaN have no
+// second part.
+template <class T, int D, bool LO>
+__device__ __forceinline__ void store_parts(uint32_t tile, int part, int r, int c, const Piece<T>& p, float up)
+{
+    constexpr int N = Piece<T>::kN;
+    uint32_t h[N / 2], l[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float x = p.x[2 * i] * up, y = p.x[2 * i + 1] * up;
+        h[i] = two_f16(x, y);
+        if (LO) {
+            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+            const float dx = x - t.x, dy = y - t.y;
+            l[i] = two_f16(fabsf(dx) < INFINITY ? dx : 0.f, fabsf(dy) < INFINITY ? dy : 0.f);
+        }
+    }
+    if constexpr (N == 4) {
+        const uint32_t at = tile + row_at<D>(r, c >> 1) + (c & 1) * 8;
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(h[0]), "r"(h[1]) : "memory");
+        if (LO) asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + part), "r"(l[0]), "r"(l[1]) : "memory");
+    } else {
+        const uint32_t at = tile + row_at<D>(r, c);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+    }
+}
+
+struct Shared {
+    float q_down[BM];                              // a query row's factor, with scale log2 e
+    float k_down[2][BN], v_down[2][BN], v_log[2][BN];      // a key's and a value's, of two tiles
+    uint32_t bad[kNotes];                          // keys with an infinity or NaN in v, of the tiles from the first masked one on
+    long long sum[kWarps];
+    int seq, tile;
+};
+
+// Block b's sequence and the block's place among that sequence's; all threads call it.
+// False: there is none.
+__device__ bool locate(Shared& sh, const PromptArgs& a, long long b)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) sh.seq = -1;
+    long long base = 0;
+    for (int n0 = 0; n0 < a.N; n0 += kThreads) {
+        const int n = n0 + tid;
+        long long w = 0;
+        if (n < a.N) {
+            int first, count;
+            prompt_rows(a.cu_q, n, a.T, first, count);
+            w = ((long long)count * a.G + BM - 1) / BM;
+        }
+        long long incl = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += x;
+        }
+        if (lane == 31) sh.sum[warp] = incl;
+        __syncthreads();
+        long long before = base, all = 0;
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) before += sh.sum[i];
+            all += sh.sum[i];
+        }
+        if (b >= before + incl - w && b < before + incl) {
+            sh.seq = n;
+            sh.tile = (int)(w - 1 - (b - (before + incl - w)));    // a prompt's last rows, the longest work, first
+        }
+        base += all;
+        __syncthreads();
+        if (b < base) break;
+    }
+    __syncthreads();
+    return sh.seq >= 0;
+}
+
+__device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) { *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y); }
+
+template <class T, class O, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
+{
+    using Sh = Shape<T, O, D>;
+    constexpr int P = D * (int)sizeof(T) / 16;     // pieces of a row
+    constexpr int PT = (P + 7) / 8;                // of a thread, eight to a row
+    constexpr int NT = D / 8;
+    extern __shared__ __align__(128) uint8_t dyn[];
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hk = blockIdx.y;
+    if (tid < kNotes) sh.bad[tid] = 0;
+    if (!locate(sh, a, blockIdx.x)) return;
+    const PromptSeq s = prompt_seq(a, sh.seq);
+    const int off = s.lk - s.lq;                   // token t sees the keys up to t + off
+    const long long rows = (long long)s.lq * a.G, r0 = (long long)sh.tile * BM;
+    const int here = rows - r0 < BM ? (int)(rows - r0) : BM;
+    const int most = min(max((int)((r0 + here - 1) / a.G) + off + 1, 0), s.lk);
+    const int all = min(max((int)(r0 / a.G) + off + 1, 0), s.lk);      // keys that every row sees
+    const uint32_t q_tile = smem_at(dyn), tiles = q_tile + Sh::kQ, raw = tiles + 2 * Sh::kTile;
+    const T* kp = static_cast<const T*>(a.k) + (long long)s.k0 * a.k_stride + (long long)hk * D;
+    const T* vp = static_cast<const T*>(a.v) + (long long)s.k0 * a.v_stride + (long long)hk * D;
+    const int t8 = tid & 7, tr = tid >> 3;         // this thread's pieces and row of a tile of keys
+    const int count = (most + BN - 1) / BN;
+
+    auto copy_raw = [&](int j) {
+        if (j < count) {
+            const int key = j * BN + tr;
+            const bool there = key < most;
+            const uint32_t dst = raw + (j & 1) * Sh::kRaw + tr * (P * 16);
+#pragma unroll
+            for (int i = 0; i < PT; ++i) {
+                const int c = t8 + 8 * i;
+                if (c < P) {
+                    const long long k = there ? key : 0;
+                    copy16(dst + c * 16, reinterpret_cast<const uint4*>(kp + k * a.k_stride) + c, there);
+                    copy16(dst + BN * P * 16 + c * 16, reinterpret_cast<const uint4*>(vp + k * a.v_stride) + c, there);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // Tile j from the copies (each thread its own) to fp16 pairs.
+    auto convert = [&](int j) {
+        const uint32_t src = raw + (j & 1) * Sh::kRaw + tr * (P * 16), dst = tiles + (j & 1) * Sh::kTile;
+        const bool edge = (j + 1) * BN > all;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            Piece<T> p[PT];
+            uint32_t top = 0;
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < PT; ++i) {
+                const int c = t8 + 8 * i;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (c < P)
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                 : "r"(src + x * (BN * P * 16) + c * 16));
+                p[i] = widen(w, T());
+#pragma unroll
+                for (int e = 0; e < Piece<T>::kN; ++e) {
+                    top = finite_top(top, p[i].x[e]);
+                    if (x == 1 && edge && !(fabsf(p[i].x[e]) < INFINITY)) {
+                        p[i].x[e] = 0.f;
+                        odd = true;
+                    }
+                }
+            }
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const int e = up_of(top);
+#pragma unroll
+            for (int i = 0; i < PT; ++i)
+                if (t8 + 8 * i < P) store_parts<T, D, Sh::kLo>(dst + x * (Sh::kParts * Sh::kHalf), Sh::kHalf, tr, t8 + 8 * i, p[i], power(e));
+            if (t8 == 0) {
+                if (x == 0) {
+                    sh.k_down[j & 1][tr] = power(-e);
+                } else {
+                    sh.v_down[j & 1][tr] = power(-e);
+                    sh.v_log[j & 1][tr] = (float)-e;
+                }
+            }
+            if (odd) atomicOr(&sh.bad[j - all / BN], 1u << tr);
+        }
+    };
+
+    copy_raw(0);
+    copy_raw(1);
+    // the queries, 32 rows at a time; -1 for a negative scale, 0 for 0
+#pragma unroll 1
+    for (int b = 0; b < BM; b += 32) {
+        const int r = b + tr;
+        const T* qp = nullptr;
+        if (r < here) {
+            const int t = (int)((r0 + r) / a.G), g = (int)((r0 + r) - (long long)t * a.G);
+            qp = static_cast<const T*>(a.q) + (long long)(s.q0 + t) * a.q_stride + ((long long)hk * a.G + g) * D;
+        }
+        Piece<T> p[PT];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < PT; ++i) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (qp && t8 + 8 * i < P) w = __ldg(reinterpret_cast<const uint4*>(qp) + t8 + 8 * i);
+            p[i] = widen(w, T());
+#pragma unroll
+            for (int e = 0; e < Piece<T>::kN; ++e) top = finite_top(top, p[i].x[e]);
+        }
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const int e = up_of(top);
+        const float sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f;
+#pragma unroll
+        for (int i = 0; i < PT; ++i)
+            if (t8 + 8 * i < P) store_parts<T, D, Sh::kLo>(q_tile, BM * D * 2, r, t8 + 8 * i, p[i], power(e) * sign);
+        if (t8 == 0) sh.q_down[r] = sign == 0.f ? 1.f : fabsf(a.scale_log2) * power(-e);
+    }
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    if (count > 0) convert(0);
+    copy_raw(2);
+
+    const int g = lane >> 2, i4 = lane & 3;
+    float o[NT][4], m[2], n[2], l[2], fac[2], rs[2];
+    int lim[2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = warp * 16 + g + 8 * h;
+        lim[h] = r < here ? min(max((int)((r0 + r) / a.G) + off + 1, 0), s.lk) : 0;
+        rs[h] = sh.q_down[r];
+        m[h] = n[h] = -INFINITY;
+        l[h] = fac[h] = 0.f;
+    }
+    // the rows and pieces that this lane's ldmatrix addresses name
+    const int mr = lane & 15, mc = lane >> 4;      // q, v: 16 rows, two pieces
+    const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;  // k: two blocks of 8 rows, two pieces each
+#pragma unroll 1
+    for (int j = 0; j < count; ++j) {
+        // the next tile, while other warps are at this one's products
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if (j + 1 < count) convert(j + 1);
+        copy_raw(j + 3);
+        const uint32_t kt = tiles + (j & 1) * Sh::kTile, vt = kt + Sh::kParts * Sh::kHalf;
+        float c[4][4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[b][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            uint32_t qh[4], ql[4], kh[2][4], kl[2][4];
+            ldmatrix(qh, q_tile + row_at<D>(warp * 16 + mr, 2 * k + mc));
+            if (Sh::kLo) ldmatrix(ql, q_tile + BM * D * 2 + row_at<D>(warp * 16 + mr, 2 * k + mc));
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                ldmatrix(kh[b], kt + row_at<D>(b * 16 + kr, 2 * k + kc));
+                if (Sh::kLo) ldmatrix(kl[b], kt + Sh::kHalf + row_at<D>(b * 16 + kr, 2 * k + kc));
+            }
+#pragma unroll
+            for (int b = 0; b < 4; ++b) mma(c[b], qh, kh[b >> 1][2 * (b & 1)], kh[b >> 1][2 * (b & 1) + 1]);
+            if (Sh::kLo) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) mma(c[b], ql, kh[b >> 1][2 * (b & 1)], kh[b >> 1][2 * (b & 1) + 1]);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) mma(c[b], qh, kl[b >> 1][2 * (b & 1)], kl[b >> 1][2 * (b & 1) + 1]);
+            }
+        }
+        const bool masked = (j + 1) * BN > all;
+        float top[2], vtop[2], vd[4][2];
+        bool grow = false;
+        top[0] = top[1] = vtop[0] = vtop[1] = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const float2 kd = *reinterpret_cast<const float2*>(&sh.k_down[j & 1][8 * b + 2 * i4]);
+            const float2 v2 = *reinterpret_cast<const float2*>(&sh.v_down[j & 1][8 * b + 2 * i4]);
+            const float2 lv = *reinterpret_cast<const float2*>(&sh.v_log[j & 1][8 * b + 2 * i4]);
+            vd[b][0] = v2.x, vd[b][1] = v2.y;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float& x = c[b][2 * h + e];
+                    x = x * rs[h] * (e ? kd.y : kd.x);
+                    if (masked && j * BN + 8 * b + 2 * i4 + e >= lim[h]) x = -INFINITY;
+                    top[h] = fmaxf(top[h], x);
+                    vtop[h] = fmaxf(vtop[h], x + (e ? lv.y : lv.x));
+                }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + kSlack;
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float m2 = fmaxf(m[h], quad_max(top[h]));
+                // n is kept near m, so that 2^(m - n) is finite
+                const float n2 = fmaxf(fmaxf(n[h], quad_max(vtop[h])), m2 - 120.f);
+                const float fl = m2 == -INFINITY ? 1.f : ex2(m[h] - m2), fo = n2 == -INFINITY ? 1.f : ex2(n[h] - n2);
+                m[h] = m2;
+                n[h] = n2;
+                l[h] *= fl;
+                fac[h] = m2 == -INFINITY ? 0.f : ex2(m2 - n2);
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+                    o[x][2 * h] *= fo;
+                    o[x][2 * h + 1] *= fo;
+                }
+            }
+        }
+        uint32_t ph[2][4], pl[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float ref = m[h] == -INFINITY ? 0.f : m[h];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                float y[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float p = ex2(c[b][2 * h + e] - ref);
+                    l[h] += p;
+                    y[e] = p * (vd[b][e] * fac[h]);
+                }
+                const uint32_t z = two_f16(y[0], y[1]);
+                ph[b >> 1][2 * (b & 1) + h] = z;
+                if (Sh::kPLo) {
+                    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&z));
+                    pl[b >> 1][2 * (b & 1) + h] = two_f16(y[0] - t.x, y[1] - t.y);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int x = 0; x < NT; x += 2) {
+                uint32_t vh[4], vl[4];
+                ldmatrix_t(vh, vt + row_at<D>(k * 16 + mr, x + mc));
+                if (Sh::kLo) ldmatrix_t(vl, vt + Sh::kHalf + row_at<D>(k * 16 + mr, x + mc));
+#pragma unroll
+                for (int y = 0; y < 2; ++y) mma(o[x + y], ph[k], vh[2 * y], vh[2 * y + 1]);
+                if (Sh::kPLo) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) mma(o[x + y], pl[k], vh[2 * y], vh[2 * y + 1]);
+                }
+                if (Sh::kLo) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) mma(o[x + y], ph[k], vl[2 * y], vl[2 * y + 1]);
+                }
+            }
+        __syncthreads();                           // the next tile is there, this one has been read
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < kNotes; ++i) any |= sh.bad[i];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        const int r = warp * 16 + g + 8 * h;
+        if (r >= here) continue;
+        const int t = (int)((r0 + r) / a.G), q = (int)((r0 + r) - (long long)t * a.G);
+        const float f = lim[h] == 0 ? 0.f : ex2(n[h] - m[h]) / l[h];
+        O* op = static_cast<O*>(a.o) + ((long long)(s.q0 + t) * a.Hq + (long long)hk * a.G + q) * D;
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            float y[2] = {lim[h] == 0 ? 0.f : o[x][2 * h] * f, lim[h] == 0 ? 0.f : o[x][2 * h + 1] * f};
+            if (any) {
+#pragma unroll 1
+                for (int k = all / BN * BN; k < lim[h]; ++k) {
+                    if (!((sh.bad[(k - all / BN * BN) / BN] >> (k & 31)) & 1)) continue;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float z = (float)vp[(long long)k * a.v_stride + 8 * x + 2 * i4 + e];
+                        if (!(fabsf(z) < INFINITY)) y[e] += z;
+                    }
+                }
+            }
+            store2(op + 8 * x + 2 * i4, y[0], y[1]);
+        }
+    }
+}
+
+template <class T, class O, int D>
+cudaError_t launch(const PromptArgs& a, cudaStream_t stream)
+{
+    auto kern = prompt_attention_split_kernel<T, O, D>;
+    const size_t bytes = Shape<T, O, D>::kBytes;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    // every sequence has at most one tile that is not full
+    const long long tiles = ((long long)a.T * a.G) / BM + a.N;
+    if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    kern<<<dim3((unsigned)tiles, (unsigned)a.Hkv), kThreads, bytes, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <class T, class O>
+cudaError_t launch_d(const PromptArgs& a, int32_t d, cudaStream_t stream)
+{
+    switch (d) {
+    case 16: return launch<T, O, 16>(a, stream);
+    case 32: return launch<T, O, 32>(a, stream);
+    case 64: return launch<T, O, 64>(a, stream);
+    default: return launch<T, O, 128>(a, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attention_split(const PromptArgs& a, int32_t d, kda_dtype_t dtype, cudaStream_t stream)
+{
+    if (dtype == KDA_BF16) return launch_d<__nv_bfloat16, __nv_bfloat16>(a, d, stream);
+    if (dtype == KDA_BF16_F32OUT) return launch_d<__nv_bfloat16, float>(a, d, stream);
+    return launch_d<float, float>(a, d, stream);
+}
+
+}  // namespace kda

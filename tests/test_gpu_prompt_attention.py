@@ -4,6 +4,7 @@ Bounds, per element, with A = sum_j p_j |v_j|:
   fp32   |err| <= 1e-4 A: a score is a sum of d <= 128 products, off by at most
          d 2^-24 sum |q k| scale (about 128 * 6e-8 * 12 = 9e-5 at these inputs'
          scores), which is p's relative error; the rest is far below.
+         Products of fp16 pairs keep 22 bits of q, k, p and v (2^-22 A and less).
   bf16   |err| <= 2^-8 |o| + 2^-8 A + 1e-4 A: the rounding of o, and p rounded to
          bf16 for the second product (half a step, 2^-8, in the sum; the normaliser
          sums the unrounded).  fp32 output from bf16 inputs is held to the fp32
@@ -103,6 +104,29 @@ def test_matches_reference(kda, lens, keys, Hq, Hkv, d, dtype, out):
     o = run(kda, parts, whole, cu, cu_k, o_dtype=out)
     assert o.dtype == out
     check(o, *prompt_reference(*parts, cu, cu_k), exact_p=out == F32)
+
+
+@pytest.mark.parametrize("lens,keys,Hq,Hkv,d", CASES[3:9] + CASES[11:15], ids=lambda c: str(c).replace(" ", ""))
+@pytest.mark.parametrize("dtype,out", [(BF16, F32), (F32, F32)])
+def test_cuda_cores_match_reference(kda, monkeypatch, lens, keys, Hq, Hkv, d, dtype, out):
+    monkeypatch.setenv("KDA_FORCE_SIMT", "1")
+    cu, cu_k = starts(lens), None if keys is None else starts(keys)
+    parts, whole = inputs(cu[-1], (cu_k or cu)[-1], Hq, Hkv, d, dtype, seed=sum(lens) + d)
+    check(run(kda, parts, whole, cu, cu_k, o_dtype=out), *prompt_reference(*parts, cu, cu_k), exact_p=True)
+
+
+@pytest.mark.parametrize("spread", [1e-25, 1e25, "rows"])
+def test_magnitudes_far_apart(kda, spread):
+    # keys and values of very different magnitudes from row to row, queries of the opposite
+    (q, k, v), _ = inputs(150, 150, 4, 2, 64, F32, seed=17)
+    if spread == "rows":
+        f = 10.0 ** torch.randint(-12, 13, (150, 1, 1), generator=torch.Generator().manual_seed(1)).float()
+        v = v * f
+    else:
+        q, k, v = q / spread, k * spread, v * spread
+    o = run(kda, (q, k, v), None, None, None)
+    ref, mag = prompt_reference(q, k, v)
+    check(o, ref, mag, exact_p=True)
 
 
 @pytest.mark.parametrize("dtype,d,Hq,Hkv", [(BF16, 128, 4, 2), (BF16, 64, 3, 1), (F32, 64, 4, 4), (BF16, 32, 2, 1)])
