@@ -62,6 +62,14 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same onto nothing.
+__device__ __forceinline__ void mma0(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%10, %10, %10, %10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t at)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
@@ -90,12 +98,9 @@ __device__ __forceinline__ int row_at(int r, int c)
     return r * (D * 2) + ((c ^ ((r / S) & M)) << 4);
 }
 
-// Bits of the largest finite magnitude.
-__device__ __forceinline__ uint32_t finite_top(uint32_t top, float x)
-{
-    const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
-    return b < 0x7F800000u ? max(top, b) : top;
-}
+// Bits of the largest magnitude.
+__device__ __forceinline__ uint32_t top_of(uint32_t top, float x) { return max(top, __float_as_uint(x) & 0x7FFFFFFFu); }
+constexpr uint32_t kInfinity = 0x7F800000u;
 // The power of two that brings that magnitude to 2^14 or a little more.
 __device__ __forceinline__ int up_of(uint32_t top) { return top == 0 ? 0 : min(max(14 + 127 - (int)(top >> 23), -100), 100); }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
@@ -123,10 +128,10 @@ __device__ __forceinline__ Piece<__nv_bfloat16> widen(uint4 w, __nv_bfloat16)
 }
 
 // The 16-byte piece c of T of row r, times up, as fp16 into the first part of a tile and
-// (LO) what that leaves into the second, `part` bytes on.  Infinities and NaN have no
-// second part.
+// (LO) what that leaves into the second, `part` bytes on; odd: there may be infinities
+// or NaN.
 template <class T, int D, bool LO>
-__device__ __forceinline__ void store_parts(uint32_t tile, int part, int r, int c, const Piece<T>& p, float up)
+__device__ __forceinline__ void store_parts(uint32_t tile, int part, int r, int c, const Piece<T>& p, float up, bool odd)
 {
     constexpr int N = Piece<T>::kN;
     uint32_t h[N / 2], l[N / 2];
@@ -136,8 +141,11 @@ __device__ __forceinline__ void store_parts(uint32_t tile, int part, int r, int 
         h[i] = two_f16(x, y);
         if (LO) {
             const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-            const float dx = x - t.x, dy = y - t.y;
-            l[i] = two_f16(fabsf(dx) < INFINITY ? dx : 0.f, fabsf(dy) < INFINITY ? dy : 0.f);
+            l[i] = two_f16(x - t.x, y - t.y);
+            if (odd) {                             // (an infinity or NaN has no second part)
+                if (!(fabsf(x - t.x) < INFINITY)) l[i] &= 0xFFFF0000u;
+                if (!(fabsf(y - t.y) < INFINITY)) l[i] &= 0x0000FFFFu;
+            }
         }
     }
     if constexpr (N == 4) {
@@ -155,15 +163,58 @@ struct Shared {
     float k_down[2][BN], v_down[2][BN], v_log[2][BN];      // a key's and a value's, of two tiles
     uint32_t bad[kNotes];                          // keys with an infinity or NaN in v, of the tiles from the first masked one on
     long long sum[kWarps];
+    int tiles[kThreads];                           // of the sequences
     int seq, tile;
 };
 
-// Block b's sequence and the block's place among that sequence's; all threads call it.
-// False: there is none.
+// The block's sequence and row tile; all threads call it.  False: there is none.  Up to
+// kThreads sequences are taken in levels, the largest tile number of all first (the
+// longest work of whole prompts), so that the blocks that start last are short; more
+// sequences are taken one after the other.
 __device__ bool locate(Shared& sh, const PromptArgs& a, long long b)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) sh.seq = -1;
+    if (a.N <= kThreads) {
+        int mine = 0;
+        if (tid < a.N) {
+            int first, count;
+            prompt_rows(a.cu_q, tid, a.T, first, count);
+            mine = (int)(((long long)count * a.G + BM - 1) / BM);
+        }
+        sh.tiles[tid] = mine;
+        int top = __reduce_max_sync(0xffffffffu, mine);
+        if (lane == 0) sh.sum[warp] = top;
+        __syncthreads();
+        for (int i = 0; i < kWarps; ++i) top = max(top, (int)sh.sum[i]);
+        // the largest level v with more than b tiles of level v and above
+        auto above = [&](int v) {
+            int x = 0;
+            for (int n = lane; n < a.N; n += 32) x += max(sh.tiles[n] - v, 0);
+            return (int)__reduce_add_sync(0xffffffffu, x);
+        };
+        int lo = 0, hi = top;              // above(lo) > b >= above(hi)
+        if (b >= above(0)) return false;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (above(mid) > b) lo = mid;
+            else hi = mid;
+        }
+        int left = (int)b - above(lo + 1); // which of the sequences that have that level
+        for (int n0 = 0; n0 < a.N; n0 += 32) {
+            const uint32_t has = __ballot_sync(0xffffffffu, n0 + lane < a.N && sh.tiles[n0 + lane] > lo);
+            if (left < __popc(has)) {
+                if (warp == 0 && (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == left) {
+                    sh.seq = n0 + lane;
+                    sh.tile = lo;
+                }
+                break;
+            }
+            left -= __popc(has);
+        }
+        __syncthreads();
+        return sh.seq >= 0;                // (offsets that give rows twice may add up to anything)
+    }
     long long base = 0;
     for (int n0 = 0; n0 < a.N; n0 += kThreads) {
         const int n = n0 + tid;
@@ -202,7 +253,7 @@ __device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpre
 __device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) { *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y); }
 
 template <class T, class O, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, D <= 64 ? 2 : 1)
 prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
 {
     using Sh = Shape<T, O, D>;
@@ -211,9 +262,10 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
     constexpr int NT = D / 8;
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ Shared sh;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hk = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int hk = blockIdx.x % a.Hkv;
     if (tid < kNotes) sh.bad[tid] = 0;
-    if (!locate(sh, a, blockIdx.x)) return;
+    if (!locate(sh, a, blockIdx.x / a.Hkv)) return;
     const PromptSeq s = prompt_seq(a, sh.seq);
     const int off = s.lk - s.lq;                   // token t sees the keys up to t + off
     const long long rows = (long long)s.lq * a.G, r0 = (long long)sh.tile * BM;
@@ -251,7 +303,6 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
         for (int x = 0; x < 2; ++x) {
             Piece<T> p[PT];
             uint32_t top = 0;
-            bool odd = false;
 #pragma unroll
             for (int i = 0; i < PT; ++i) {
                 const int c = t8 + 8 * i;
@@ -261,20 +312,31 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
                                  : "r"(src + x * (BN * P * 16) + c * 16));
                 p[i] = widen(w, T());
 #pragma unroll
-                for (int e = 0; e < Piece<T>::kN; ++e) {
-                    top = finite_top(top, p[i].x[e]);
-                    if (x == 1 && edge && !(fabsf(p[i].x[e]) < INFINITY)) {
-                        p[i].x[e] = 0.f;
-                        odd = true;
-                    }
-                }
+                for (int e = 0; e < Piece<T>::kN; ++e) top = top_of(top, p[i].x[e]);
             }
 #pragma unroll
             for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const bool odd = top >= kInfinity;     // (the same for the row's threads)
+            if (__any_sync(0xffffffffu, odd)) {
+                bool mine = false;
+                if (odd) top = 0;
+#pragma unroll
+                for (int i = 0; i < PT; ++i)
+#pragma unroll
+                    for (int e = 0; e < Piece<T>::kN; ++e) {
+                        const bool fine = fabsf(p[i].x[e]) < INFINITY;
+                        if (odd && fine) top = top_of(top, p[i].x[e]);
+                        mine |= !fine;
+                        if (!fine && x == 1 && edge) p[i].x[e] = 0.f;
+                    }
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                if (mine && x == 1 && edge) atomicOr(&sh.bad[j - all / BN], 1u << tr);
+            }
             const int e = up_of(top);
 #pragma unroll
             for (int i = 0; i < PT; ++i)
-                if (t8 + 8 * i < P) store_parts<T, D, Sh::kLo>(dst + x * (Sh::kParts * Sh::kHalf), Sh::kHalf, tr, t8 + 8 * i, p[i], power(e));
+                if (t8 + 8 * i < P) store_parts<T, D, Sh::kLo>(dst + x * (Sh::kParts * Sh::kHalf), Sh::kHalf, tr, t8 + 8 * i, p[i], power(e), odd);
             if (t8 == 0) {
                 if (x == 0) {
                     sh.k_down[j & 1][tr] = power(-e);
@@ -283,7 +345,6 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
                     sh.v_log[j & 1][tr] = (float)-e;
                 }
             }
-            if (odd) atomicOr(&sh.bad[j - all / BN], 1u << tr);
         }
     };
 
@@ -306,7 +367,8 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
             if (qp && t8 + 8 * i < P) w = __ldg(reinterpret_cast<const uint4*>(qp) + t8 + 8 * i);
             p[i] = widen(w, T());
 #pragma unroll
-            for (int e = 0; e < Piece<T>::kN; ++e) top = finite_top(top, p[i].x[e]);
+            for (int e = 0; e < Piece<T>::kN; ++e)
+                if (fabsf(p[i].x[e]) < INFINITY) top = top_of(top, p[i].x[e]);
         }
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -314,8 +376,9 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
         const float sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f;
 #pragma unroll
         for (int i = 0; i < PT; ++i)
-            if (t8 + 8 * i < P) store_parts<T, D, Sh::kLo>(q_tile, BM * D * 2, r, t8 + 8 * i, p[i], power(e) * sign);
-        if (t8 == 0) sh.q_down[r] = sign == 0.f ? 1.f : fabsf(a.scale_log2) * power(-e);
+            if (t8 + 8 * i < P) store_parts<T, D, Sh::kLo>(q_tile, BM * D * 2, r, t8 + 8 * i, p[i], power(e) * sign, true);
+        // (not 0, which hidden scores of -inf are multiplied by)
+        if (t8 == 0) sh.q_down[r] = sign == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) * power(-e), 1.2e-38f);
     }
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     if (count > 0) convert(0);
@@ -347,11 +410,9 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
         if (j + 1 < count) convert(j + 1);
         copy_raw(j + 3);
         const uint32_t kt = tiles + (j & 1) * Sh::kTile, vt = kt + Sh::kParts * Sh::kHalf;
-        float c[4][4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c[b][e] = 0.f;
+        // The tensor cores cut off what does not fit as they add up: the small products have
+        // sums of their own, and so has each tile's output below.
+        float c[4][4], small[4][4];
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
             uint32_t qh[4], ql[4], kh[2][4], kl[2][4];
@@ -363,12 +424,18 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
                 if (Sh::kLo) ldmatrix(kl[b], kt + Sh::kHalf + row_at<D>(b * 16 + kr, 2 * k + kc));
             }
 #pragma unroll
-            for (int b = 0; b < 4; ++b) mma(c[b], qh, kh[b >> 1][2 * (b & 1)], kh[b >> 1][2 * (b & 1) + 1]);
+            for (int b = 0; b < 4; ++b) {
+                if (k == 0) mma0(c[b], qh, kh[b >> 1][2 * (b & 1)], kh[b >> 1][2 * (b & 1) + 1]);
+                else mma(c[b], qh, kh[b >> 1][2 * (b & 1)], kh[b >> 1][2 * (b & 1) + 1]);
+            }
             if (Sh::kLo) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b) mma(c[b], ql, kh[b >> 1][2 * (b & 1)], kh[b >> 1][2 * (b & 1) + 1]);
+                for (int b = 0; b < 4; ++b) {
+                    if (k == 0) mma0(small[b], ql, kh[b >> 1][2 * (b & 1)], kh[b >> 1][2 * (b & 1) + 1]);
+                    else mma(small[b], ql, kh[b >> 1][2 * (b & 1)], kh[b >> 1][2 * (b & 1) + 1]);
+                }
 #pragma unroll
-                for (int b = 0; b < 4; ++b) mma(c[b], qh, kl[b >> 1][2 * (b & 1)], kl[b >> 1][2 * (b & 1) + 1]);
+                for (int b = 0; b < 4; ++b) mma(small[b], qh, kl[b >> 1][2 * (b & 1)], kl[b >> 1][2 * (b & 1) + 1]);
             }
         }
         const bool masked = (j + 1) * BN > all;
@@ -386,14 +453,17 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float& x = c[b][2 * h + e];
-                    x = x * rs[h] * (e ? kd.y : kd.x);
+                    x = (Sh::kLo ? x + small[b][2 * h + e] : x) * (e ? kd.y : kd.x);      // (to be multiplied by rs)
                     if (masked && j * BN + 8 * b + 2 * i4 + e >= lim[h]) x = -INFINITY;
                     top[h] = fmaxf(top[h], x);
-                    vtop[h] = fmaxf(vtop[h], x + (e ? lv.y : lv.x));
+                    vtop[h] = fmaxf(vtop[h], fmaf(x, rs[h], e ? lv.y : lv.x));
                 }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + kSlack;
+        for (int h = 0; h < 2; ++h) {
+            top[h] *= rs[h];
+            grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + kSlack;
+        }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -421,7 +491,7 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
                 float y[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float p = ex2(c[b][2 * h + e] - ref);
+                    const float p = ex2(fmaf(c[b][2 * h + e], rs[h], -ref));
                     l[h] += p;
                     y[e] = p * (vd[b][e] * fac[h]);
                 }
@@ -434,23 +504,34 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
             }
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int x = 0; x < NT; x += 2) {
+            float z[2][4];
+            uint32_t vh[2][4], vl[2][4];
 #pragma unroll
-            for (int x = 0; x < NT; x += 2) {
-                uint32_t vh[4], vl[4];
-                ldmatrix_t(vh, vt + row_at<D>(k * 16 + mr, x + mc));
-                if (Sh::kLo) ldmatrix_t(vl, vt + Sh::kHalf + row_at<D>(k * 16 + mr, x + mc));
+            for (int k = 0; k < 2; ++k) {
+                ldmatrix_t(vh[k], vt + row_at<D>(k * 16 + mr, x + mc));
+                if (Sh::kLo) ldmatrix_t(vl[k], vt + Sh::kHalf + row_at<D>(k * 16 + mr, x + mc));
+            }
+            // the small products first, so that few sums are cut off at the large ones' size
 #pragma unroll
-                for (int y = 0; y < 2; ++y) mma(o[x + y], ph[k], vh[2 * y], vh[2 * y + 1]);
-                if (Sh::kPLo) {
+            for (int y = 0; y < 2; ++y) {
+                if constexpr (Sh::kPLo) {
+                    mma0(z[y], pl[0], vh[0][2 * y], vh[0][2 * y + 1]);
+                    mma(z[y], pl[1], vh[1][2 * y], vh[1][2 * y + 1]);
+                    if (Sh::kLo) {
+                        mma(z[y], ph[0], vl[0][2 * y], vl[0][2 * y + 1]);
+                        mma(z[y], ph[1], vl[1][2 * y], vl[1][2 * y + 1]);
+                    }
+                    mma(z[y], ph[0], vh[0][2 * y], vh[0][2 * y + 1]);
+                    mma(z[y], ph[1], vh[1][2 * y], vh[1][2 * y + 1]);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) mma(o[x + y], pl[k], vh[2 * y], vh[2 * y + 1]);
-                }
-                if (Sh::kLo) {
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) mma(o[x + y], ph[k], vl[2 * y], vl[2 * y + 1]);
+                    for (int e = 0; e < 4; ++e) o[x + y][e] += z[y][e];
+                } else {
+                    mma(o[x + y], ph[0], vh[0][2 * y], vh[0][2 * y + 1]);
+                    mma(o[x + y], ph[1], vh[1][2 * y], vh[1][2 * y + 1]);
                 }
             }
+        }
         __syncthreads();                           // the next tile is there, this one has been read
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -494,8 +575,8 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     // every sequence has at most one tile that is not full
     const long long tiles = ((long long)a.T * a.G) / BM + a.N;
-    if (tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    kern<<<dim3((unsigned)tiles, (unsigned)a.Hkv), kThreads, bytes, stream>>>(a);
+    if (tiles * a.Hkv > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    kern<<<(unsigned)(tiles * a.Hkv), kThreads, bytes, stream>>>(a);
     return cudaGetLastError();
 }
 
