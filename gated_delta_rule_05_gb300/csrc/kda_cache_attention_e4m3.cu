@@ -10,7 +10,9 @@
 // is in units of 2^n, the sum l of P in units of 2^m.  They move only when a score
 // exceeds them by more than 8, so that a step without that has no reduction over lanes.
 // q is brought into fp16's range by a power of two per row, which is exact.  With
-// fp32 queries or output, q and w are a sum of two fp16 each (22 bits).
+// fp32 queries or output, q and w are a sum of two fp16 each (22 bits), and as the tensor
+// cores cut off what does not fit as they add up (1e-5 of the result over 32,000 keys), the small
+// products and each step's output have sums of their own.
 //
 // The tensor-core instruction of one thread and TMEM is not used: with 4 to 16 rows
 // most of its 128 would be empty, and 8-bit products would need q and w in 8 bits.
@@ -87,6 +89,14 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                  "{%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same onto nothing.
+__device__ __forceinline__ void mma0(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%10, %10, %10, %10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Two e4m3 (the lower or the upper half of a word) as fp16, which holds them exactly.
 __device__ __forceinline__ uint32_t widen_lo(uint32_t w)
@@ -340,11 +350,11 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
             const uint32_t st = ring + out * Sh::kStageBytes, sc = st + 2 * kKeys * D;
             out = out + 1 == Sh::kStages ? 0 : out + 1;
 
-            float c[2][4];
+            float c[2][4], small[2][4];
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) c[b][j] = 0.f;
+                for (int j = 0; j < 4; ++j) c[b][j] = small[b][j] = 0.f;
             {
                 constexpr int KB = D / 4 < 16 ? D / 4 : 16;    // bytes per read of a row of K
                 Words<KB> kw[2][D / 4 / KB];
@@ -362,7 +372,7 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
                         const uint32_t x = kw[b][s / (KB / 4)].w[s % (KB / 4)];
                         const uint32_t b0 = widen_lo(x), b1 = widen_hi(x);
                         mma(c[b], qh[s], b0, b1);
-                        if constexpr (QLO) mma(c[b], ql[s], b0, b1);
+                        if constexpr (QLO) mma(small[b], ql[s], b0, b1);
                     }
             }
             float ks[2][2], vs[2][2];              // of keys 8 b + i4 + 4 j
@@ -391,7 +401,7 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         float& x = c[b][2 * h + j];
-                        x = x * ks[b][j] * rs[h];
+                        x = (QLO ? x + small[b][2 * h + j] : x) * ks[b][j] * rs[h];
                         const int key = 8 * b + i4 + 4 * j;
                         if (masked && (!((mask >> key) & 1) || pos + key >= lim[h])) x = -INFINITY;
                         top[h] = fmaxf(top[h], x);
@@ -452,8 +462,15 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
                     const uint32_t b1[4] = {widen_lo(lo1), widen_hi(lo1), widen_lo(hi1), widen_hi(hi1)};
 #pragma unroll
                     for (int j = 0; j < (NT < 4 ? NT : 4); ++j) {
-                        mma(o[4 * x + j], ph, b0[j], b1[j]);
-                        if constexpr (PLO) mma(o[4 * x + j], pl, b0[j], b1[j]);
+                        if constexpr (PLO) {
+                            float z[4];
+                            mma0(z, pl, b0[j], b1[j]);
+                            mma(z, ph, b0[j], b1[j]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[4 * x + j][e] += z[e];
+                        } else {
+                            mma(o[4 * x + j], ph, b0[j], b1[j]);
+                        }
                     }
                 }
             }
@@ -826,13 +843,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                 fence_proxy_async_smem();
                 __syncwarp();
             }
-            float c[kStepGroups][2][4];
-#pragma unroll
-            for (int i = 0; i < kStepGroups; ++i)
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) c[i][b][j] = 0.f;
+            float c[kStepGroups][2][4], small[kStepGroups][2][4];
             {
                 Words<KB> kw[kStepGroups][2][D / 4 / KB];
 #pragma unroll
@@ -852,9 +863,21 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                         for (int b = 0; b < 2; ++b) {
                             const uint32_t x = kw[i][b][s / (KB / 4)].w[s % (KB / 4)];
                             const uint32_t b0 = widen_lo(x), b1 = widen_hi(x);
-                            mma(c[i][b], qh[s], b0, b1);
-                            if constexpr (QLO) mma(c[i][b], ql[s], b0, b1);
+                            if (s == 0) mma0(c[i][b], qh[s], b0, b1);
+                            else mma(c[i][b], qh[s], b0, b1);
+                            if constexpr (QLO) {
+                                if (s == 0) mma0(small[i][b], ql[s], b0, b1);
+                                else mma(small[i][b], ql[s], b0, b1);
+                            }
                         }
+                if constexpr (QLO) {
+#pragma unroll
+                    for (int i = 0; i < kStepGroups; ++i)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) c[i][b][j] += small[i][b][j];
+                }
             }
             float k1[kStepGroups][S][2], top[2], vtop[2];
             bool grow = false;
@@ -940,26 +963,41 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                     }
                 }
             }
+            // this lane's D / 8 channels of keys i4, i4 + 4, 8 + i4, 12 + i4 of each group
+            Words<NT> vw[kStepGroups][4];
 #pragma unroll
-            for (int i = 0; i < kStepGroups; ++i) {
-                // this lane's D / 8 channels of keys i4, i4 + 4, 8 + i4, 12 + i4
-                Words<NT> vw[4];
+            for (int i = 0; i < kStepGroups; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int at = channel_of<D>(g);
-                    vw[j] = read_words<NT>(st + i * Sh::kSlotBytes + kKeys * D + row_at<D>(i4 + 4 * j, at >> 4) + (at & 15));
+                    vw[i][j] = read_words<NT>(st + i * Sh::kSlotBytes + kKeys * D + row_at<D>(i4 + 4 * j, at >> 4) + (at & 15));
                 }
 #pragma unroll
-                for (int x = 0; x < (NT + 3) / 4; ++x) {
-                    const uint32_t lo0 = __byte_perm(vw[0].w[x], vw[1].w[x], 0x5140), hi0 = __byte_perm(vw[0].w[x], vw[1].w[x], 0x7362);
-                    const uint32_t lo1 = __byte_perm(vw[2].w[x], vw[3].w[x], 0x5140), hi1 = __byte_perm(vw[2].w[x], vw[3].w[x], 0x7362);
+            for (int x = 0; x < (NT + 3) / 4; ++x) {
+                constexpr int J = NT < 4 ? NT : 4;
+                float z[J][4];
+#pragma unroll
+                for (int i = 0; i < kStepGroups; ++i) {
+                    const uint32_t lo0 = __byte_perm(vw[i][0].w[x], vw[i][1].w[x], 0x5140), hi0 = __byte_perm(vw[i][0].w[x], vw[i][1].w[x], 0x7362);
+                    const uint32_t lo1 = __byte_perm(vw[i][2].w[x], vw[i][3].w[x], 0x5140), hi1 = __byte_perm(vw[i][2].w[x], vw[i][3].w[x], 0x7362);
                     const uint32_t b0[4] = {widen_lo(lo0), widen_hi(lo0), widen_lo(hi0), widen_hi(hi0)};
                     const uint32_t b1[4] = {widen_lo(lo1), widen_hi(lo1), widen_lo(hi1), widen_hi(hi1)};
 #pragma unroll
-                    for (int j = 0; j < (NT < 4 ? NT : 4); ++j) {
-                        mma(o[4 * x + j], ph[i], b0[j], b1[j]);
-                        if constexpr (PLO) mma(o[4 * x + j], pl[i], b0[j], b1[j]);
+                    for (int j = 0; j < J; ++j) {
+                        if constexpr (PLO) {
+                            if (i == 0) mma0(z[j], pl[i], b0[j], b1[j]);
+                            else mma(z[j], pl[i], b0[j], b1[j]);
+                            mma(z[j], ph[i], b0[j], b1[j]);
+                        } else {
+                            mma(o[4 * x + j], ph[i], b0[j], b1[j]);
+                        }
                     }
+                }
+                if constexpr (PLO) {
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[4 * x + j][e] += z[j][e];
                 }
             }
             __syncwarp();                          // the slots have been read
