@@ -12,7 +12,7 @@
 // q is brought into fp16's range by a power of two per row, which is exact.  With
 // fp32 queries or output, q and w are a sum of two fp16 each (22 bits), and as the tensor
 // cores cut off what does not fit as they add up (1e-5 of the result over 32,000 keys), the small
-// products and each step's output have sums of their own.
+// products and each group's output have sums of their own.
 //
 // The tensor-core instruction of one thread and TMEM is not used: with 4 to 16 rows
 // most of its 128 would be empty, and 8-bit products would need q and w in 8 bits.
@@ -963,41 +963,33 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                     }
                 }
             }
-            // this lane's D / 8 channels of keys i4, i4 + 4, 8 + i4, 12 + i4 of each group
-            Words<NT> vw[kStepGroups][4];
 #pragma unroll
-            for (int i = 0; i < kStepGroups; ++i)
+            for (int i = 0; i < kStepGroups; ++i) {
+                // this lane's D / 8 channels of keys i4, i4 + 4, 8 + i4, 12 + i4
+                Words<NT> vw[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int at = channel_of<D>(g);
-                    vw[i][j] = read_words<NT>(st + i * Sh::kSlotBytes + kKeys * D + row_at<D>(i4 + 4 * j, at >> 4) + (at & 15));
+                    vw[j] = read_words<NT>(st + i * Sh::kSlotBytes + kKeys * D + row_at<D>(i4 + 4 * j, at >> 4) + (at & 15));
                 }
 #pragma unroll
-            for (int x = 0; x < (NT + 3) / 4; ++x) {
-                constexpr int J = NT < 4 ? NT : 4;
-                float z[J][4];
-#pragma unroll
-                for (int i = 0; i < kStepGroups; ++i) {
-                    const uint32_t lo0 = __byte_perm(vw[i][0].w[x], vw[i][1].w[x], 0x5140), hi0 = __byte_perm(vw[i][0].w[x], vw[i][1].w[x], 0x7362);
-                    const uint32_t lo1 = __byte_perm(vw[i][2].w[x], vw[i][3].w[x], 0x5140), hi1 = __byte_perm(vw[i][2].w[x], vw[i][3].w[x], 0x7362);
+                for (int x = 0; x < (NT + 3) / 4; ++x) {
+                    const uint32_t lo0 = __byte_perm(vw[0].w[x], vw[1].w[x], 0x5140), hi0 = __byte_perm(vw[0].w[x], vw[1].w[x], 0x7362);
+                    const uint32_t lo1 = __byte_perm(vw[2].w[x], vw[3].w[x], 0x5140), hi1 = __byte_perm(vw[2].w[x], vw[3].w[x], 0x7362);
                     const uint32_t b0[4] = {widen_lo(lo0), widen_hi(lo0), widen_lo(hi0), widen_hi(hi0)};
                     const uint32_t b1[4] = {widen_lo(lo1), widen_hi(lo1), widen_lo(hi1), widen_hi(hi1)};
 #pragma unroll
-                    for (int j = 0; j < J; ++j) {
+                    for (int j = 0; j < (NT < 4 ? NT : 4); ++j) {
                         if constexpr (PLO) {
-                            if (i == 0) mma0(z[j], pl[i], b0[j], b1[j]);
-                            else mma(z[j], pl[i], b0[j], b1[j]);
-                            mma(z[j], ph[i], b0[j], b1[j]);
+                            float z[4];
+                            mma0(z, pl[i], b0[j], b1[j]);
+                            mma(z, ph[i], b0[j], b1[j]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[4 * x + j][e] += z[e];
                         } else {
                             mma(o[4 * x + j], ph[i], b0[j], b1[j]);
                         }
                     }
-                }
-                if constexpr (PLO) {
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[4 * x + j][e] += z[j][e];
                 }
             }
             __syncwarp();                          // the slots have been read
