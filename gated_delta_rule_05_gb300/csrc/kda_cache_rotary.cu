@@ -16,8 +16,8 @@
 // 8 bits: a unit is the part of one block of rows that one sequence adds to.  The thread
 // block that owns its first row tabulates the sines and cosines of its rows; a team of as
 // many warps as hold the block in registers has a head of k or v: it reads the rows
-// once, finds the largest magnitude (as bits, so that infinities and NaN win) and stores
-// x / s.  s is a power of two: e4m3 is a floating type, so a finer scale would gain
+// once, turns them, finds the largest magnitude (so that infinities and NaN win) and
+// stores x / s.  s is a power of two: e4m3 is a floating type, so a finer scale would gain
 // nothing, and the division, a later change of the scale and the product in the attention
 // are exact but for e4m3's own rounding.  A scale of NaN marks a block with an infinity or
 // NaN; its bytes are 0, so that no product of a weight of 0 with it is NaN.
@@ -230,10 +230,12 @@ __device__ __forceinline__ void turn(const float2* table, int row, const Pair& p
     turn(w, interleaved, x, y);
 }
 
-__device__ __forceinline__ uint32_t top_bits(uint32_t top, const float (&x)[8])
+// The larger of top and eight magnitudes; NaN when one is NaN.
+__device__ __forceinline__ float top_of(float top, const float (&x)[8])
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 8; i += 2)
+        asm("{\n\t.reg .f32 a, b;\n\tabs.f32 a, %1;\n\tabs.f32 b, %2;\n\tmax.NaN.f32 %0, %0, a, b;\n\t}" : "+f"(top) : "f"(x[i]), "f"(x[i + 1]));
     return top;
 }
 
@@ -320,46 +322,39 @@ __device__ __forceinline__ void rows_part(const RotaryArgs& a, const int32_t* cu
 // warps: `block0` the block's first row there (null: the rows have no place), `off`
 // the rows that it already has, `scale` its scale.
 constexpr int kHeld = 4;               // rows of a lane
-template <class T>
 struct Held {
-    Pieces<T> rows[kHeld];
+    float x[kHeld][8], y[kHeld][8];
 };
-// The rows of one head that this lane of a team holds.
-template <class T, int D>
-__device__ __forceinline__ Held<T> e4m3_load(const Unit& u, const Pair& p, const uint8_t* src, long long src_row, int team, int tl)
-{
-    constexpr int L = D / 16;
-    Held<T> h;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int r = tl / L + i * (team * 32 / L);
-        if (r < u.count) h.rows[i] = load_pieces<T>(src + (u.first + r) * src_row, p);
-    }
-    return h;
-}
-
 template <class T, int D, bool TURN>
-__device__ __forceinline__ void e4m3_head(const RotaryArgs& a, const Unit& u, const float2* table, const Held<T>& held, const Pair& p,
+__device__ __forceinline__ void e4m3_head(const RotaryArgs& a, const Unit& u, const float2* table, const uint8_t* src, long long src_row,
                                           uint8_t* dst, long long dst_row, uint8_t* block0, int off, float* scale, uint32_t* tops, int team,
                                           int warp, int lane, int tl)
 {
     constexpr int L = D / 16;
+    const Pair p = pair_of(tl % L, TURN ? a.rot : 0, a.interleaved);
     const int r0 = tl / L, pass = team * 32 / L;
     const int row_bytes = a.Hkv * D;
-    const Pieces<T>(&raw)[kHeld] = held.rows;
-    uint32_t old = 0;
-    if (block0 && off > 0) old = __float_as_uint(*reinterpret_cast<volatile float*>(scale)) & 0x7FFFFFFFu;
-    uint32_t top = 0;
+    Held v;
+    {
+        Pieces<T> raw[kHeld];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int r = r0 + i * pass;
-        if (r < u.count) {
-            float x[8], y[8];
-            widen(raw[i], x, y);
-            if (TURN && p.turned) turn(table, r, p, a.rot, a.interleaved, x, y);
-            top = top_bits(top_bits(top, x), y);
+        for (int i = 0; i < kHeld; ++i) {
+            raw[i] = {};
+            const int r = r0 + i * pass;
+            if (r < u.count) raw[i] = load_pieces<T>(src + (u.first + r) * src_row, p);
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            widen(raw[i], v.x[i], v.y[i]);
+            if (TURN && p.turned && r0 + i * pass < u.count) turn(table, r0 + i * pass, p, a.rot, a.interleaved, v.x[i], v.y[i]);
         }
     }
+    uint32_t old = 0;
+    if (block0 && off > 0) old = __float_as_uint(*reinterpret_cast<volatile float*>(scale)) & 0x7FFFFFFFu;
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) most = top_of(top_of(most, v.x[i]), v.y[i]);
+    uint32_t top = __float_as_uint(most) & 0x7FFFFFFFu;
     top = __reduce_max_sync(0xffffffffu, top);
     if (team > 1) {
         const int first = warp / team * team;
@@ -393,9 +388,7 @@ __device__ __forceinline__ void e4m3_head(const RotaryArgs& a, const Unit& u, co
     for (int i = 0; i < kHeld; ++i) {
         const int r = r0 + i * pass;
         if (r >= u.count) break;
-        float x[8], y[8];
-        widen(raw[i], x, y);
-        if (TURN && p.turned) turn(table, r, p, a.rot, a.interleaved, x, y);
+        const float(&x)[8] = v.x[i], (&y)[8] = v.y[i];
         if (dst) store_pieces<T>(dst + (u.first + r) * dst_row, p, x, y);
         if (block0) {
             uint8_t* c = block0 + (long long)(off + r) * row_bytes;
@@ -453,25 +446,18 @@ __device__ __forceinline__ void units_part(const RotaryArgs& a, const int32_t* c
         const long long scale_at = there ? ((long long)page * (a.page_size / a.block) + b) * a.Hkv : 0;
         const int step = a.splits * teams, tl = (warp % a.team) * 32 + lane;
         int task = split * teams + warp / a.team;
-        const Pair turned = pair_of(tl % (D / 16), a.rot, a.interleaved), plain = pair_of(tl % (D / 16), 0, false);
-        auto load = [&](int t) {
-            const bool is_k = t < a.Hkv;
-            const long long at = (long long)(is_k ? t : t - a.Hkv) * D * (int)sizeof(T);
-            return e4m3_load<T, D>(u, is_k ? turned : plain, (is_k ? a.k : a.v) + at, is_k ? a.k_row : a.v_row, a.team, tl);
-        };
         __syncthreads();                           // the table is there
 #pragma unroll 1
         for (; task < 2 * a.Hkv; task += step) {
-            const Held<T> held = load(task);
             const bool is_k = task < a.Hkv;
             const int hk = is_k ? task : task - a.Hkv;
             uint8_t* block0 = there ? (is_k ? a.k_cache : a.v_cache) + block_at + hk * D : nullptr;
             float* scale = (is_k ? a.k_scales : a.v_scales) + scale_at + hk;
             if (is_k)
-                e4m3_head<T, D, true>(a, u, table, held, turned, a.k_out ? a.k_out + (long long)hk * D * (int)sizeof(T) : nullptr, a.k_out_row,
+                e4m3_head<T, D, true>(a, u, table, a.k + (long long)hk * D * (int)sizeof(T), a.k_row, a.k_out ? a.k_out + (long long)hk * D * (int)sizeof(T) : nullptr, a.k_out_row,
                                       block0, off, scale, sh_tops, a.team, warp, lane, tl);
             else
-                e4m3_head<T, D, false>(a, u, table, held, plain, nullptr, 0, block0, off, scale, sh_tops, a.team, warp, lane, tl);
+                e4m3_head<T, D, false>(a, u, table, a.v + (long long)hk * D * (int)sizeof(T), a.v_row, nullptr, 0, block0, off, scale, sh_tops, a.team, warp, lane, tl);
         }
         __syncthreads();
     }
@@ -479,7 +465,7 @@ __device__ __forceinline__ void units_part(const RotaryArgs& a, const int32_t* c
 
 // The first unit_blocks thread blocks have the units (8 bits), the others rows.
 template <class T, int D, bool EIGHT>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 || !EIGHT ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 2)
 cache_rotary_kernel(const __grid_constant__ RotaryArgs a)
 {
     extern __shared__ __align__(16) uint8_t dyn[];
