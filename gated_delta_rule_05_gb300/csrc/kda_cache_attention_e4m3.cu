@@ -638,7 +638,7 @@ __device__ __forceinline__ void start_groups(GroupShared& sh, const E4m3Args& a,
     const bool there = k.page >= 0 && k.page < a.num_pages;
     if (lane < kBoxes) {
         int place = -1;
-        if (there) {
+        if (there && !a.starve) {
             const int b = (int)__umulhi((uint32_t)k.slot, a.block_magic);
             place = (k.page * a.blocks + b) * a.split.Hkv + k.w.hk;
             mbar_arrive_expect_tx(bar, 2 * SUB * D);
@@ -666,15 +666,18 @@ __device__ __forceinline__ void start_groups(GroupShared& sh, const E4m3Args& a,
 }
 
 // Waits for a group's copies, for about two seconds at most; when a wait has given up
-// the CTA goes on with what is there and marks its rows.
-__device__ __forceinline__ void wait_group(GroupShared& sh, uint64_t* bar, uint32_t parity)
+// the CTA goes on with what is there, marks its rows and sets the workspace's timeout
+// word.
+__device__ __forceinline__ void wait_group(GroupShared& sh, uint64_t* bar, uint32_t parity, int32_t* status)
 {
     if (mbar_try_wait(bar, parity)) return;
     const long long t0 = clock64();
 #pragma unroll 1
     while (!mbar_try_wait(bar, parity)) {
-        if (clock64() - t0 > (1ll << 32) || *reinterpret_cast<volatile int*>(&sh.dead)) {
+        if (*reinterpret_cast<volatile int*>(&sh.dead)) return;
+        if (clock64() - t0 > (1ll << 32)) {
             *reinterpret_cast<volatile int*>(&sh.dead) = 1;
+            atomicOr(status, 2);
             return;
         }
     }
@@ -814,7 +817,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
 #pragma unroll 1
         for (int t = w.t0; t < w.t1; ++t) {
 #pragma unroll
-            for (int i = 0; i < kStepGroups; ++i) wait_group(sh, &sh.full[warp][out + i], turn);
+            for (int i = 0; i < kStepGroups; ++i) wait_group(sh, &sh.full[warp][out + i], turn, a.status);
             __syncwarp();
             const uint32_t st = ring + out * Sh::kSlotBytes;
             float ksn[kStepGroups][S], vsn[kStepGroups][S];
@@ -1075,6 +1078,11 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
             }
         }
     }
+    // after a wait that gave up some copies may be in flight: time for them to land
+    if (*reinterpret_cast<volatile int*>(&sh.dead)) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1ll << 22)) {}
+    }
 }
 
 // Joins the pieces of the items that were cut between groups.  Block (c, y, z): the
@@ -1231,11 +1239,12 @@ size_t e4m3_workspace_bytes(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, int 
 {
     int32_t groups, row_tiles;
     plan(Ts * (Hq / Hkv), sms > 0 ? sms : 1, groups, row_tiles);
-    return (size_t)groups * row_tiles * 2 * kRows * (d + 3) * sizeof(float);
+    return kWsHeaderBytes + (size_t)groups * row_tiles * 2 * kRows * (d + 3) * sizeof(float);
 }
 
 cudaError_t launch_cache_attention_e4m3(E4m3Args a, int32_t d, kda_dtype_t dtype, int sms, cudaStream_t stream)
 {
+    a.starve = getenv("KDA_TEST_STARVE_CONSUMERS") != nullptr;
     plan(a.R, sms > 0 ? sms : 1, a.split.groups, a.split.row_tiles);
     if (dtype == KDA_BF16) return launch_d<__nv_bfloat16, __nv_bfloat16>(a, d, stream);
     if (dtype == KDA_BF16_F32OUT) return launch_d<__nv_bfloat16, float>(a, d, stream);

@@ -93,6 +93,8 @@ struct E4m3Args {
     float scale_log2;
     void* o;
     float* part;                      // 2 slots per CTA: [16][d] o, [16] m, [16] m of the values, [16] l
+    int32_t* status;                  // the workspace's timeout word
+    bool starve;                      // test of the waits that give up
 };
 constexpr int kMaxE4m3Page = 65536;   // rows of a page (block_magic is exact up to there)
 size_t e4m3_workspace_bytes(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, int sms);

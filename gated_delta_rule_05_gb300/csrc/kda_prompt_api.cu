@@ -305,7 +305,8 @@ kda_status_t kda_cache_attention_e4m3(const void* q, const void* k_cache, const 
     a.page_stride = page_stride;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.o = o;
-    a.part = static_cast<float*>(workspace);
+    a.status = static_cast<int32_t*>(workspace) + kda::kWsTimeoutWord;
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kda::kWsHeaderBytes);
     const cudaError_t err = kda::launch_cache_attention_e4m3(a, d, dtype, sms, stream);
     return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -668,7 +668,9 @@ size_t kda_cache_attention_e4m3_workspace_bytes(int32_t N, int32_t Ts,
  *                 [0, max_pages * page_size] are clamped)
  *   workspace     kda_cache_attention_e4m3_workspace_bytes(...) bytes, 256-byte
  *                 aligned, not shared with concurrent calls; contents on entry do
- *                 not matter
+ *                 not matter.  Bit 1 of the int32 at byte 8 is set when a wait of the
+ *                 kernel has given up (after some two seconds), which no call clears;
+ *                 the rows of o that depended on it are NaN.
  * dtype is that of q and of o.  Products are of fp16 pairs (q exactly, probabilities
  * to 11 bits), with fp32 queries or output of sums of two (22 bits); sums are fp32.
  * A scale of NaN makes the tokens that see a row of its block NaN and no others;

@@ -259,3 +259,49 @@ def test_a_prompt_and_its_answer(kda, dtype, d, page, block):
         check(o, *cache_reference(turned[:, None], dequantised(kc, ks), dequantised(vc, vs), table, lengths.tolist()),
               exact_p=dtype == F32)
     assert lengths.tolist() == [x + steps for x in lens]
+
+
+@pytest.mark.parametrize("dtype,page,block", [(BF16, 32, 16), (F32, 24, 8)])
+def test_waits_that_give_up(kda, monkeypatch, dtype, page, block):
+    # no copies are made: the kernel's waits run out (about 2 s), it returns, sets the
+    # workspace's word and marks its rows (those of one CTA and joined ones), and the next call is
+    # right
+    c = Call(3, 2, 8, 2, 64, page, block, [3000, 1, 500], dtype, seed=13)
+    args = c.args()
+    code = kda.KDA_BF16 if dtype == BF16 else kda.KDA_FP32
+    ws = torch.zeros(kda.kda_cache_attention_e4m3_workspace_bytes(3, 2, 8, 2, 64, code), dtype=torch.uint8, device="cuda")
+    monkeypatch.setenv("KDA_TEST_STARVE_CONSUMERS", "1")
+    o = kda.kda_cache_attention_e4m3(**args, workspace=ws)
+    torch.cuda.synchronize()
+    monkeypatch.delenv("KDA_TEST_STARVE_CONSUMERS")
+    assert ws[8:12].view(torch.int32).item() & 2
+    assert torch.isnan(o[0]).all() and torch.isnan(o[2]).all()
+    ws[8:12].zero_()
+    check(kda.kda_cache_attention_e4m3(**args, workspace=ws), *c.reference(), exact_p=dtype == F32)
+    assert ws[8:12].view(torch.int32).item() == 0
+
+
+def test_fp32_over_many_rows(kda):
+    # the tensor cores cut off as they add up: sums over a whole context must not be theirs.
+    # some 30,000 rows in one block's walk, values with a mean of 2.  A step's own sum over 32
+    # keys is cut off by a few units of 2^-23 of it at most (4e-7 or so, not growing); the
+    # sums over 625 steps round half a unit of 2^-24 of what they have, at random: 2^-24
+    # sqrt(625 / 3) = 9e-7, in the output and in its divisor.  Cutting off instead would add
+    # up to 625 2^-24 = 3.7e-5
+    n, hi, d, page = 64, 20000, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    pages = -(-hi // page)
+    k, v = (torch.randn((pages, page, 4, d), generator=g, device="cuda") + b for b in (0.0, 2.0))
+    table = torch.stack([torch.randperm(pages, generator=torch.Generator().manual_seed(i)) for i in range(n)])
+    (k, ks), (v, vs) = ([y.cuda() if y.dtype == F32 else y.view(torch.uint8).cuda().view(E4M3) for y in eight_bits(x.cpu(), 64)]
+                        for x in (k, v))
+    q = torch.randn((n, 1, 4, d), generator=g, device="cuda")
+    lengths = torch.full((n,), hi, dtype=torch.int32, device="cuda")
+    o = kda.kda_cache_attention_e4m3(q, k, v, ks, vs, table.int().cuda(), lengths).double()
+    kd, vd = (x.view(torch.uint8).view(E4M3).double() * s.double().repeat_interleave(page, 1)[..., None] for x, s in ((k, ks), (v, vs)))
+    for i in (0, n - 1):
+        for h in range(4):
+            rows = table[i].cuda()
+            w = torch.softmax((kd[rows, :, h].flatten(0, 1)[:hi] @ q[i, 0, h].double()) * d ** -0.5, 0)
+            want = w @ vd[rows, :, h].flatten(0, 1)[:hi]
+            assert ((o[i, 0, h] - want).norm() / want.norm()).item() < 3e-6
