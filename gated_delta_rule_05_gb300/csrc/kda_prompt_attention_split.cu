@@ -373,7 +373,7 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
         const int e = up_of(top);
-        const float sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : 0.f;
+        const float sign = a.scale_log2 > 0.f ? 1.f : a.scale_log2 < 0.f ? -1.f : a.scale_log2;     // (0 or NaN stays)
 #pragma unroll
         for (int i = 0; i < PT; ++i)
             if (t8 + 8 * i < P) store_parts<T, D, Sh::kLo>(q_tile, BM * D * 2, r, t8 + 8 * i, p[i], power(e) * sign, true);

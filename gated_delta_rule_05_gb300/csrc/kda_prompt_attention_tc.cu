@@ -991,9 +991,10 @@ cudaError_t launch(PromptArgs a, int sms, cudaStream_t stream)
 
 bool prompt_tc_supported(const PromptArgs& a, int32_t d, kda_dtype_t dtype)
 {
-    // (an item takes a microsecond per 128 keys, and no wait more than two seconds)
+    // (an item takes a microsecond per 128 keys, and no wait more than two seconds; places
+    // within an item are 32-bit)
     return dtype == KDA_BF16 && (d == 64 || d == 128) && a.scale_log2 > 0.f && a.G <= 128 && a.Tk > 0 && a.Tk <= (1 << 27) &&
-           a.T <= (1 << 27);
+           a.T <= (1 << 27) && a.Hq <= (1 << 16);
 }
 
 cudaError_t launch_prompt_attention_tc(PromptArgs a, int32_t d, int sms, cudaStream_t stream)

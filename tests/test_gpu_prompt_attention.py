@@ -273,3 +273,48 @@ def test_waits_that_give_up(kda, monkeypatch):
     ref, mag = prompt_reference(*parts, cu, o=torch.full(a[0].shape, 5.0))
     check(o, ref, mag, exact_p=False)
     assert status.item() == 0
+
+
+def test_claimed_items_in_graphs_and_on_two_streams(kda):
+    # enough items that they are claimed from a counter in the workspace
+    cu = starts([2600, 900, 1, 500])
+    (q, k, v), _ = inputs(4001, 4001, 16, 8, 64, BF16, seed=18)
+    a = [x.cuda() for x in (q, k, v)]
+    b = [x.flip(0).contiguous() for x in a]
+    c = i32(cu)
+    want = [kda.kda_prompt_attention(*x, c) for x in (a, b)]
+    ref, mag = prompt_reference(q[:2600], k[:2600], v[:2600])
+    check(want[0][:2600], ref, mag, exact_p=False)
+    s = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [kda.kda_prompt_attention(*x, c, stream=t) for _ in range(4) for x, t in zip((a, b), s)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i % 2]) for i, x in enumerate(got))
+    hold, o = [x.clone() for x in a], torch.empty_like(a[0])
+    ws = torch.full((256,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[8:12] = 0
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kda.kda_prompt_attention(*hold, c, o=o, workspace=ws)
+    for x, w in zip((a, b, a), want + want[:1]):
+        for y, z in zip(hold, x):
+            y.copy_(z)
+        o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, w)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F32, 32)])
+def test_more_sequences_than_are_held(kda, dtype, d):
+    rng = np.random.default_rng(2)
+    lens = rng.integers(0, 3, 20000).tolist()
+    lens[12345] = 400
+    cu = starts(lens)
+    T = cu[-1]
+    parts, _ = inputs(T, T, 2, 1, d, dtype, seed=19)
+    o = run(kda, parts, None, cu, None)
+    check(o, *prompt_reference(*parts, cu), exact_p=dtype == F32)
+    if dtype == BF16:   # a sequence's first token sees itself alone (fp32 values are kept to 22 bits)
+        first = [a for a, n in zip(cu, lens) if n > 0]
+        assert torch.equal(o[first].cpu(), parts[2][first].expand(-1, 2, -1))
