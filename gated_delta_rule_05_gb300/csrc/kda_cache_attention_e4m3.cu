@@ -222,9 +222,9 @@ __device__ __forceinline__ void start_copies(const E4m3Args& a, const Walk& k, u
         long long row = 0;
         const float* scale = lane < 16 ? a.k_scales : a.v_scales;
         if (there) {
-            row = k.page * a.page_stride + (long long)k.slot * (a.split.Hkv * D) + k.w.hk * D;
+            row = k.page * a.page_stride + (long long)k.slot * (a.Hkv * D) + k.w.hk * D;
             const int b = a.block == 1 ? k.slot : (int)__umulhi((uint32_t)k.slot, a.block_magic);
-            scale += ((long long)k.page * a.blocks + b) * a.split.Hkv + k.w.hk;
+            scale += ((long long)k.page * a.blocks + b) * a.Hkv + k.w.hk;
         }
         copy4(stage + 2 * kKeys * D + lane * 4, scale, there);
         if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + 2 * kKeys * D + 128), "r"(mask) : "memory");
@@ -546,13 +546,27 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
 // TMA boxes of SUB rows with one scale each, so that s = (c ks) S is one factor per row
 // and box and the step has half the instructions per key.  The pages' boxes come in the
 // swizzle of their row size, which is that of row_at above.
+//
+// An item is a sequence and 1, 2, 4 or 8 of its cache heads, side by side: warp w has head w
+// % heads and every 8 / heads-th step of 32 keys.  With 8 the thread block reads whole rows
+// of the cache, and a head's sums stay in one warp: nothing to join at an item's end.  But
+// there are fewer items, and each one's pieces (below) are read by the join kernel in turn: so the
+// most heads with at most kMostCuts thread blocks to an item.  64 x 1 token on up to 32,000
+// rows, 16 x 1 on 16,000, 256 x 1 on 100 to 900, 1 x 1 on 2,047 (8 cache heads, d = 128, us):
+// one head 376, 102.8, 103.9, 12.1; this rule 344 (94 % of HBM), 95.5 (82 %), 61.5 (65 %),
+// 12.4; 8 heads always 344, 98.3, 61.6, 35.2.
+//
+// Against the kernel above, which takes any page and block, 414, 111, 107, 16.0; boxes of 8
+// rows where 16 would do 377, 103, 66, 12.7.  More warps with shorter rings (12 x 4 slots)
+// took 414 instead of 374 then, two thread blocks of 4 warps 399 instead of 377.
 constexpr int kStepGroups = 2;
-constexpr int kGroupKT = kWarps * kStepGroups * kKeys;
-// Lead of 1, 2, 4 and 8 tiles, us: 32 x 4 tokens, contexts of 100 to 16,384 rows, 127.5,
-// 116.3, 118.0 and 122.6; 64 x 1 token 385.6, 383.7, 387.2 and 395.8.
+constexpr int kStepKeys = kStepGroups * kKeys;
+// Lead of 1, 2, 4 and 8 tiles (of one head), us: 32 x 4 tokens, contexts of 100 to 16,384
+// rows, 127.5, 116.3, 118.0 and 122.6; 64 x 1 token 385.6, 383.7, 387.2 and 395.8.
 constexpr int kGroupLead = 2;
+constexpr int kMostCuts = 4;                       // 1 and 16: 32 x 4 tokens 114 and 110 us, 4: 104
 constexpr int kSlots = 6;                          // groups of a warp's ring
-using GroupPiece = TreePieces<kGroupKT, kGroupLead>;
+using GroupPiece = TreePieces<0, kGroupLead>;
 
 template <int D>
 struct GroupShape {
@@ -570,6 +584,12 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
         " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(h), "r"(row), "r"(page), "r"(smem_at(bar))
         : "memory");
+}
+
+// The cache head of a warp.
+__device__ __forceinline__ int head_of(const E4m3Args& a, const GroupPiece& w, int warp)
+{
+    return (w.hk << a.heads_log) + (warp & ((1 << a.heads_log) - 1));
 }
 
 // The walk of a warp's copies, a step at a time; a lane's part of it is box lane %
@@ -591,7 +611,7 @@ struct GroupWalk {
     {
         if (go) {
             t = w.t0;
-            pos = t * kGroupKT + warp * (kStepGroups * kKeys) + lane % kBoxes * SUB;
+            pos = (t << a.split.tile_log) + (warp >> a.heads_log) * kStepKeys + lane % kBoxes * SUB;
             p = pos / a.split.page_size;
             slot = pos - p * a.split.page_size;
         }
@@ -605,7 +625,7 @@ struct GroupWalk {
             enter(a, warp, lane);
             return;
         }
-        pos += kGroupKT;
+        pos += 1 << a.split.tile_log;
         p += a.tile_pages;
         slot += a.tile_rows;
         if (slot >= a.split.page_size) {
@@ -632,7 +652,7 @@ __device__ __forceinline__ void start_groups(GroupShared& sh, const E4m3Args& a,
 {
     constexpr int S = kKeys / SUB, kBoxes = GroupWalk<SUB>::kBoxes;
     if (!k.go) return;
-    const int at = first + lane % kBoxes / S, sub = lane % S;
+    const int at = first + lane % kBoxes / S, sub = lane % S, hk = head_of(a, k.w, warp);
     const uint32_t dst = ring + at * GroupShape<D>::kSlotBytes + sub * SUB * D;
     uint64_t* bar = &sh.full[warp][at];
     const bool there = k.page >= 0 && k.page < a.num_pages;
@@ -640,10 +660,10 @@ __device__ __forceinline__ void start_groups(GroupShared& sh, const E4m3Args& a,
         int place = -1;
         if (there && !a.starve) {
             const int b = (int)__umulhi((uint32_t)k.slot, a.block_magic);
-            place = (k.page * a.blocks + b) * a.split.Hkv + k.w.hk;
+            place = (k.page * a.blocks + b) * a.Hkv + hk;
             mbar_arrive_expect_tx(bar, 2 * SUB * D);
-            load_box(dst, map_k, k.w.hk, k.slot, k.page, bar);
-            load_box(dst + kKeys * D, map_v, k.w.hk, k.slot, k.page, bar);
+            load_box(dst, map_k, hk, k.slot, k.page, bar);
+            load_box(dst + kKeys * D, map_v, hk, k.slot, k.page, bar);
         }
         sh.scale[warp][at][sub] = place;
     }
@@ -733,7 +753,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
         if (warp == 0) sh.dead = 0;
         fence_mbar_init();
     }
-    const TreeSpot sp = tree_locate<kThreads, kGroupKT, kGroupLead>(a.split, group, sh.loc);   // has block barriers
+    const TreeSpot sp = tree_locate<kThreads, 0, kGroupLead>(a.split, group, sh.loc);   // has block barriers
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     GroupWalk<SUB> ahead;
     ahead.go = ahead.w.start(a.split, sp, group);
@@ -763,7 +783,9 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
             }
     };
     if (go) load_scales(0);
+    const int heads = 1 << a.heads_log;
     for (; go; go = w.next(a.split)) {
+        const int hk = head_of(a, w, warp);
         // the rows' queries, in fp16 times a power of two (and -1 for a negative scale; 0 for 0)
         uint32_t qh[KS][4], ql[QLO ? KS : 1][4];
         float rs[2];
@@ -774,7 +796,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
             const bool mine = r < a.R;
             lim[h] = mine ? w.ctx - a.Ts + t + 1 : 0;
             const T* qp = static_cast<const T*>(a.q) +
-                          (((long long)w.n * a.Ts + (mine ? t : 0)) * a.Hq + w.hk * a.G + (mine ? r - t * a.G : 0)) * D;
+                          (((long long)w.n * a.Ts + (mine ? t : 0)) * a.Hq + hk * a.G + (mine ? r - t * a.G : 0)) * D;
             float x[KS][4];
             uint32_t top = 0;
 #pragma unroll
@@ -832,9 +854,9 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                 }
             const int next = out + kStepGroups == kSlots ? 0 : out + kStepGroups;
             load_scales(next);                     // (of the last step: whatever is there)
-            const int pos = t * kGroupKT + warp * (kStepGroups * kKeys);
-            const bool masked = pos + kStepGroups * kKeys > all || gaps;     // (the same for the warp)
-            if (masked && pos + kStepGroups * kKeys > w.ctx) {
+            const int pos = (t << a.split.tile_log) + (warp >> a.heads_log) * kStepKeys;
+            const bool masked = pos + kStepKeys > all || gaps;     // (the same for the warp)
+            if (masked && pos + kStepKeys > w.ctx) {
                 // values past the last row, whatever the page holds there
 #pragma unroll
                 for (int i = 0; i < kStepGroups; ++i)
@@ -1001,7 +1023,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
             out = next;
             turn ^= next == 0;
         }
-        // The warps' results of the piece, halved until one warp has them all: the upper
+        // The results of a head's warps, halved until one warp has them all: the upper
         // half writes (O, m, n, l), the lower half adds them to its own.
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -1009,7 +1031,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
         }
 #pragma unroll 1
-        for (int half = kWarps / 2; half > 0; half >>= 1) {
+        for (int half = kWarps / 2; half >= heads; half >>= 1) {
             __syncthreads();                       // what was there has been read
             if (warp >= half && warp < 2 * half) {
                 float* y = join + (warp - half) * (Sh::kFrag + 3 * kRows);
@@ -1050,9 +1072,9 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                 }
             }
         }
-        if (warp == 0) {
+        if (warp < heads) {
             const bool whole = w.t0 == 0 && w.t1 == w.tiles;
-            float* part = a.part + ((size_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * kRows * (D + 3);
+            float* part = a.part + ((((size_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) << a.heads_log) + warp) * kRows * (D + 3);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = g + 8 * h, row = r0 + r;
@@ -1060,7 +1082,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                 if (row >= a.R) continue;
                 const int t = row / a.G;
                 const float f = l[h] == 0.f ? 0.f : ex2(n[h] - m[h]) / l[h];
-                O* op = static_cast<O*>(a.o) + (((long long)w.n * a.Ts + t) * a.Hq + w.hk * a.G + row - t * a.G) * D;
+                O* op = static_cast<O*>(a.o) + (((long long)w.n * a.Ts + t) * a.Hq + hk * a.G + row - t * a.G) * D;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int ch = channel_of<D>(2 * i4 + e);
@@ -1087,8 +1109,8 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
 
 // Joins the pieces of the items that were cut between groups.  Block (c, y, z): the
 // item that the boundary before group c + 1 falls into, if that is the item's first
-// boundary; rows y 8 .. y 8 + 7 of row tile z, a warp each.  The pieces are read
-// in the order of the groups, so the result does not depend on timing.
+// boundary; head y of it and then rows 8 .. of row tile z, a warp each.  The pieces are
+// read in the order of the groups, so the result does not depend on timing.
 constexpr int kJoinThreads = 256;
 
 template <class O, int D, int KT, int kLead>
@@ -1102,18 +1124,19 @@ cache_join_kernel(const __grid_constant__ E4m3Args a)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long at = tree_begin(sp, c);
     if (at >= sp.total) return;                     // an empty range at the end
-    const int tiles = tree_tiles<KT>(s, sp.n);
-    const int hk = (int)((at - sp.start) / (tiles + kLead));
+    const int tiles = tree_tiles<KT>(s, sp.n), heads = 1 << a.heads_log, h = blockIdx.y & (heads - 1);
+    int hk = (int)((at - sp.start) / (tiles + kLead));
     // where the item's tiles begin; a boundary up to there cuts nothing
     const long long first = sp.start + (long long)hk * (tiles + kLead) + kLead;
     if (at <= first || tree_begin(sp, c - 1) > first) return;
     int last = c;                                   // the last group with tiles of this item
     while (last + 1 < s.groups && tree_begin(sp, last + 1) < first + tiles) ++last;
-    const int r = blockIdx.y * (kJoinThreads / 32) + warp, row = blockIdx.z * kRows + r;
+    hk = hk * heads + h;
+    const int r = (blockIdx.y >> a.heads_log) * (kJoinThreads / 32) + warp, row = blockIdx.z * kRows + r;
     if (r >= kRows || row >= a.R) return;
     // piece p of the item: group p's first slot, but the second of group c - 1
     auto piece = [&](int p) {
-        return a.part + (((size_t)p * s.row_tiles + blockIdx.z) * 2 + (p == c - 1 ? 1 : 0)) * kRows * (D + 3);
+        return a.part + (((((size_t)p * s.row_tiles + blockIdx.z) * 2 + (p == c - 1 ? 1 : 0)) << a.heads_log) + h) * kRows * (D + 3);
     };
     constexpr int E = D / 32 > 0 ? D / 32 : 1;
     float m = -INFINITY, n = -INFINITY;
@@ -1153,7 +1176,7 @@ cudaError_t launch_join(const E4m3Args& a, cudaStream_t stream)
     if (a.split.groups < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     const int rows = a.R < kRows ? a.R : kRows;
-    cfg.gridDim = dim3(a.split.groups - 1, (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), a.split.row_tiles);
+    cfg.gridDim = dim3(a.split.groups - 1, ((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)) << a.heads_log, a.split.row_tiles);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
@@ -1169,8 +1192,8 @@ bool make_pool_map(CUtensorMap* m, const uint8_t* base, const E4m3Args& a, int d
 {
     const auto fn = tc_encode_fn();
     if (!fn) return false;
-    const cuuint64_t row = (cuuint64_t)a.split.Hkv * d, size = a.split.page_size;
-    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)a.split.Hkv, size, (cuuint64_t)a.num_pages};
+    const cuuint64_t row = (cuuint64_t)a.Hkv * d, size = a.split.page_size;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)a.Hkv, size, (cuuint64_t)a.num_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)d, row, a.num_pages > 1 ? (cuuint64_t)a.page_stride : row * size};
     const cuuint32_t boxes[4] = {(cuuint32_t)d, 1, (cuuint32_t)box, 1}, steps[4] = {1, 1, 1, 1};
     const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, boxes, steps,
@@ -1190,11 +1213,18 @@ cudaError_t launch_groups(E4m3Args a, const CUtensorMap& map_k, const CUtensorMa
     auto kern = cache_attention_group_kernel<T, O, D, SUB>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GroupShape<D>::kBytes);
     if (e != cudaSuccess) return e;
-    a.tile_pages = kGroupKT / a.split.page_size;
-    a.tile_rows = kGroupKT % a.split.page_size;
+    // (the rule at the top of this part)
+    while (a.heads_log < 3 && a.Hkv % (2 << a.heads_log) == 0 &&
+           (long long)a.split.N * (a.Hkv >> (a.heads_log + 1)) * kMostCuts >= a.split.groups)
+        ++a.heads_log;
+    a.split.Hkv = a.Hkv >> a.heads_log;
+    const int keys = kWarps * kStepKeys >> a.heads_log;
+    a.split.tile_log = __builtin_ctz(keys);
+    a.tile_pages = keys / a.split.page_size;
+    a.tile_rows = keys % a.split.page_size;
     kern<<<a.split.groups * a.split.row_tiles, kThreads, GroupShape<D>::kBytes, stream>>>(a, map_k, map_v);
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_join<O, D, kGroupKT, kGroupLead>(a, stream);
+    return e != cudaSuccess ? e : launch_join<O, D, 0, kGroupLead>(a, stream);
 }
 
 template <class T, class O, int D>
@@ -1203,9 +1233,10 @@ cudaError_t launch(E4m3Args a, cudaStream_t stream)
     // 16 or 8 rows from a multiple of that on in one page and one block of scales
     const int box = a.split.page_size % 16 == 0 && a.block % 16 == 0 ? 16 : 8;
     CUtensorMap map_k, map_v;
-    if (a.split.page_size % box == 0 && a.block % box == 0 && (long long)a.num_pages * a.blocks * a.split.Hkv <= INT32_MAX &&
+    if (a.split.page_size % box == 0 && a.block % box == 0 && (long long)a.num_pages * a.blocks * a.Hkv <= INT32_MAX &&
         make_pool_map(&map_k, a.k_cache, a, D, box) && make_pool_map(&map_v, a.v_cache, a, D, box))
         return box == 16 ? launch_groups<T, O, D, 16>(a, map_k, map_v, stream) : launch_groups<T, O, D, 8>(a, map_k, map_v, stream);
+    a.split.Hkv = a.Hkv;
     auto kern = cache_attention_kernel<T, O, D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kBytes);
     if (e != cudaSuccess) return e;
@@ -1239,7 +1270,9 @@ size_t e4m3_workspace_bytes(int32_t Ts, int32_t Hq, int32_t Hkv, int32_t d, int 
 {
     int32_t groups, row_tiles;
     plan(Ts * (Hq / Hkv), sms > 0 ? sms : 1, groups, row_tiles);
-    return kWsHeaderBytes + (size_t)groups * row_tiles * 2 * kRows * (d + 3) * sizeof(float);
+    const int heads = Hkv % 8 == 0 ? 8 : Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;   // the most of an item
+    if (groups == 1) return kWsHeaderBytes;            // (nothing is cut)
+    return kWsHeaderBytes + (size_t)groups * row_tiles * 2 * heads * kRows * (d + 3) * sizeof(float);
 }
 
 cudaError_t launch_cache_attention_e4m3(E4m3Args a, int32_t d, kda_dtype_t dtype, int sms, cudaStream_t stream)

@@ -78,21 +78,22 @@ cudaError_t launch_cache_append_rotary(RotaryArgs args, int32_t d, bool bf16, in
 
 // ------------------------------------------------ attention to a cache of 8 bits
 struct E4m3Args {
-    // N, Hkv, lengths, page_table, page_size, max_pages, groups, row_tiles of the call,
-    // and Ts = 1: the split of the work (kda_tree.cuh) over an item's rows and one more,
-    // so that an item without any has a tile
+    // N, lengths, page_table, page_size, max_pages, groups, row_tiles of the call, Hkv
+    // >> heads_log heads, and Ts = 1: the split of the work (kda_tree.cuh) over an item's
+    // rows and one more, so that an item without any has a tile
     TreeArgs split;
+    int32_t heads_log;                // log2 of the cache heads of an item
     const void* q;                    // [N, Ts, Hq, d]
     const uint8_t *k_cache, *v_cache;
     const float *k_scales, *v_scales; // [num_pages][page_size / block][Hkv]
-    int32_t Ts, Hq, G, R;             // R = Ts G rows per (sequence, cache head)
+    int32_t Ts, Hq, Hkv, G, R;        // R = Ts G rows per (sequence, cache head)
     int32_t num_pages, block, blocks; // blocks: of a page
     uint32_t block_magic;             // ceil(2^32 / block): a row's block by a multiplication
     int32_t tile_pages, tile_rows;    // a tile's keys as whole pages and rows
     long long page_stride;            // bytes
     float scale_log2;
     void* o;
-    float* part;                      // 2 slots per CTA: [16][d] o, [16] m, [16] m of the values, [16] l
+    float* part;                      // 2 slots per CTA, per head: [16][d] o, [16] m, [16] m of the values, [16] l
     int32_t* status;                  // the workspace's timeout word
     bool starve;                      // test of the waits that give up
 };

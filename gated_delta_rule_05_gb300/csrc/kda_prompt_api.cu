@@ -284,7 +284,7 @@ kda_status_t kda_cache_attention_e4m3(const void* q, const void* k_cache, const 
     kda::E4m3Args a = {};
     a.split.N = N;
     a.split.Ts = 1;
-    a.split.Hkv = Hkv;
+    a.Hkv = Hkv;
     a.split.lengths = lengths;
     a.split.page_table = page_table;
     a.split.page_size = page_size;

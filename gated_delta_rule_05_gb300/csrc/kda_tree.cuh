@@ -43,6 +43,7 @@ struct TreeArgs {
                                       // a tile's keys as whole pages and rows
     bool starve;                      // test of the waits that give up (tensor-core kernel)
     int32_t groups, row_tiles;        // CTA b: group b / row_tiles, row tile b % row_tiles
+    int32_t tile_log;                 // KT = 0 below: log2 of a tile's keys
 };
 
 __device__ __forceinline__ int tree_context(const TreeArgs& a, int n)
@@ -101,10 +102,17 @@ struct TreeSpot {
     int n;
 };
 
+// Tiles of KT keys (0: of 2^tile_log) of a context and the nodes.
+template <int KT>
+__device__ __forceinline__ int tree_tiles_of(const TreeArgs& a, int ctx)
+{
+    if constexpr (KT == 0) return (ctx + a.Ts + (1 << a.tile_log) - 1) >> a.tile_log;
+    else return (ctx + a.Ts + KT - 1) / KT;
+}
 template <int KT>
 __device__ __forceinline__ int tree_tiles(const TreeArgs& a, int n)
 {
-    return (tree_context(a, n) + a.Ts + KT - 1) / KT;
+    return tree_tiles_of<KT>(a, tree_context(a, n));
 }
 
 template <int KT, int LEAD>
@@ -194,7 +202,7 @@ struct TreePieces {
     __device__ __forceinline__ void enter(const TreeArgs& a)
     {
         ctx = tree_context(a, n);
-        tiles = (ctx + a.Ts + KT - 1) / KT;
+        tiles = tree_tiles_of<KT>(a, ctx);
     }
     // The piece of an item of which the first `skip` units lie before the range.
     __device__ __forceinline__ bool cut(long long skip)

@@ -305,3 +305,30 @@ def test_fp32_over_many_rows(kda):
             w = torch.softmax((kd[rows, :, h].flatten(0, 1)[:hi] @ q[i, 0, h].double()) * d ** -0.5, 0)
             want = w @ vd[rows, :, h].flatten(0, 1)[:hi]
             assert ((o[i, 0, h] - want).norm() / want.norm()).item() < 3e-6
+
+
+@pytest.mark.parametrize("N,Ts,Hq,Hkv,d,page,block,dtype", [
+    (64, 1, 32, 8, 128, 32, 16, BF16), (40, 3, 16, 8, 64, 32, 8, F32), (40, 2, 12, 12, 32, 16, 16, BF16),
+    (90, 1, 12, 6, 16, 24, 8, F32), (45, 5, 64, 16, 128, 64, 64, BF16), (48, 1, 8, 4, 128, 8, 8, F32)])
+def test_many_sequences(kda, N, Ts, Hq, Hkv, d, page, block, dtype):
+    # heads side by side in a thread block, their items cut between thread blocks or not
+    rng = np.random.default_rng(N)
+    lengths = rng.integers(0, 900, N)
+    lengths[:8] = [0, 1, 31, 32, 33, 256, 2000, 5]
+    c = Call(N, Ts, Hq, Hkv, d, page, block, lengths, dtype, seed=N, gap=64)
+    ref, mag = c.reference()
+    args = c.args()
+    o = kda.kda_cache_attention_e4m3(**args)
+    check(o, ref, mag, exact_p=dtype == F32)
+    # a scale of one head, and a page that is not there
+    block0 = c.table[6, 0], 0, 1
+    args["v_scales"][block0] = float("nan")
+    lost = args["page_table"].clone()
+    lost[5, :] = -1
+    args["page_table"] = lost
+    p = kda.kda_cache_attention_e4m3(**args)
+    G = Hq // Hkv
+    assert torch.isnan(p[6, :, G:2 * G]).all() and (p[5] == 0).all()
+    keep = torch.ones(o.shape[:3], dtype=torch.bool)
+    keep[6, :, G:2 * G] = keep[5] = False
+    assert torch.equal(p[keep.cuda()], o[keep.cuda()])
