@@ -520,7 +520,12 @@ cudaError_t launch_cache_append_rotary(RotaryArgs a, int32_t d, bool bf16, int s
     long long units = 0;
     if (a.block) {
         // As many rows per thread block as a unit has on the average (every sequence may begin one
-        // in the middle of a block); with few units their heads are spread over more blocks.
+        // in the middle of a block); with few units their heads are spread over more blocks, each
+        // of which tabulates the angles anew.  32 query heads on 8, d = 128, blocks of 64 rows, 1, 2,
+        // 4 and 8 parts, us: 17 windows 23.9, 17.0, 14.0, 13.8; 64 windows 31.4, 24.2, 27.6, 33.3; 164
+        // windows 53.1, 36.6, 42.5, 55.9; 254 windows 74.4, 79.2, 90.2, 117.3.  Windows of one row
+        // take 725 us instead of 320 for 12 prompts of 512 to 12,288 rows, windows of a whole block
+        // 34 instead of 5.4 for 64 sequences of a token each.
         const long long rows = a.T / ((long long)a.T / a.block + a.N);
         a.window = rows < 1 ? 1 : rows > a.block ? a.block : (int)rows;
         const int lanes = a.block * (d / 16);      // of a block's rows
@@ -528,12 +533,12 @@ cudaError_t launch_cache_append_rotary(RotaryArgs a, int32_t d, bool bf16, int s
         while (a.team * 32 * kHeld < lanes) a.team *= 2;
         const long long windows = ((long long)a.T + a.window - 1) / a.window;
         const int rounds = (2 * a.Hkv * a.team + kWarps - 1) / kWarps;
-        const long long most = windows > 0 ? (2ll * sms + windows - 1) / windows : 1;
+        const long long most = windows > 0 ? (5ll * sms / 4 + windows - 1) / windows : 1;
         a.splits = (int)(most < 1 ? 1 : most > rounds ? rounds : most);
         units = windows * a.splits;
     }
     // the rows, in groups of a warp's, and a part of their heads each, where all would
-    // leave SMs idle
+    // leave SMs idle (one prompt of 1,000 rows 9.2 us, with all heads 13.8; 64 rows 5.0 and 13.7)
     const int per = 32 / (d / 16), heads = a.Hq + (a.block ? 0 : 2 * a.Hkv);
     const long long groups = heads ? ((long long)a.T + per - 1) / per : 0;
     a.chunks = 1;

@@ -217,8 +217,8 @@ struct Plan {
 __device__ __forceinline__ int pairs_of(int lq, const Plan& p) { return (lq + 2 * p.tok - 1) / (2 * p.tok); }
 
 // The x-th item: sequence by sequence, of a sequence its last rows, the longest work,
-// first, and of those every head; but head by head where the sequence's keys and values
-// would take much of the L2.  A whole warp calls it.
+// first, and of those every head.  (Head by head takes the same time at 65,536 keys, 268 MB
+// of keys and values.)  A whole warp calls it.
 template <int D>
 __device__ __noinline__ Item item_at(const Shared& sh, const PromptArgs& a, const Plan& p, long long x)
 {
@@ -267,13 +267,8 @@ __device__ __noinline__ Item item_at(const Shared& sh, const PromptArgs& a, cons
     }
     // (offsets that give rows twice may add up to anything)
     if (x < 0 || x >= (long long)pairs * a.Hkv) return it;
-    if ((long long)s.lk * a.Hkv * D * 4 > (64 << 20)) {
-        it.hk = (int)(x / pairs);
-        y = (int)(x - (long long)it.hk * pairs);
-    } else {
-        y = (int)(x / a.Hkv);
-        it.hk = (int)(x - (long long)y * a.Hkv);
-    }
+    y = (int)(x / a.Hkv);
+    it.hk = (int)(x - (long long)y * a.Hkv);
     it.q0 = s.q0;
     it.lq = s.lq;
     it.k0 = s.k0;
