@@ -1,6 +1,7 @@
 // kda_prompt_attention.cu -- causal attention over packed prompts on the CUDA
-// cores, fp32 arithmetic: every type, head size and scale (bf16 with d = 64 or 128
-// and a positive scale has a tensor-core kernel, kda_prompt_attention_tc.cu).
+// cores, fp32 arithmetic: every type, head size and scale.  It runs when KDA_FORCE_SIMT is
+// set, as something to compare the tensor-core kernels with that shares none of their
+// products.
 //
 // One thread block per 64 query rows of a (sequence, cache head): the rows of the
 // heads that share a cache head are laid out token by token, row r being head r % G
@@ -12,6 +13,10 @@
 // A tile that some row does not see whole is masked key by key, in the second product
 // too: there a key counts only for the rows that see it, so that an infinity or
 // NaN in a value stays with them.
+//
+// Bound by fp32 FMAs and the shared memory that feeds them: 12 prompts of 512 to 12,288
+// tokens, 32 heads on 8, d = 128, bf16, 119 ms (45 TFLOP/s of 75), where tcgen05 takes 3.5 ms;
+// 7 fp32 prompts of up to 1,500, 12 heads on 4, d = 64, 353 us, fp16 pairs 125.
 #include "kda_prompt.cuh"
 
 namespace kda {

@@ -7,7 +7,7 @@
 // of its token r / G (128 / G tokens to a tile), so that a tile spans few positions.
 // Per tile of 128 keys and row tile
 //     S = Q K^T             (M = 128, N = 128, K = d; Q, K in shared memory)
-//     P = 2^(c S - m)       (registers; c = scale log2 e; bf16 back over S)
+//     P = 2^(c S - m)       (registers; c = scale log2 e; bf16 back over S, or beside it)
 //     O += P V              (M = 128, N = d, K = 128; P in TMEM, V MN-major)
 // with a reference m near the running maximum of each row that moves only when a tile
 // exceeds it by more than 8: P may reach 2^8, O and l are scaled by 2^(m - m') when m
@@ -20,7 +20,9 @@
 // shared memory); a warp that issues products, one that copies keys and values, one that
 // finds the items and copies their queries, one that looks through values (below).
 // The row tiles share K and V and alternate on the tensor core: one's softmax runs under
-// the other's products.
+// the other's products.  Tensor memory's 512 columns hold two S, two O and, with d = 64, two P: there
+// the next scores are computed while these are worked on (5 prompts of 700 to 2,048
+// tokens behind prefixes, 16 heads, 129.5 us without and 123 with).
 //
 // Values that a row of the item does not see must not reach it through 0 * inf: in the
 // tiles on the diagonal and at the end of a sequence the fourth warp replaces
@@ -33,6 +35,20 @@
 // (Taken over all sequences by their length, dealt to and fro, 1.002, but the keys of
 // all of them pass through the L2 again and again: 4.05 ms against 3.85.)  Where there are few
 // items for a CTA they are dealt to and fro, which saves the clearing of the counter.
+//
+// Bound by the softmax beside the products: 32 heads on 8, d = 128, one prompt of 65,536
+// tokens (8 heads) 5.4 ms, 1.63 PFLOP/s, of 8,192 0.36 ms (1.5), of 2,048 34 us (1.0); 12 of 512
+// to 12,288 3.5 ms (1.53).  d = 64, 16 heads on 4, 16,384 tokens 567 us (0.97): half the products for
+// as many exponentials.  Steps on the way there, 8 x 2,048 tokens: 445 us with the
+// products' loop rolled up (349 without), 291 with the output in a warpgroup of its own (250);
+// 8,192 tokens 394 us with 16-byte stores of rows, 372 with 32-byte ones, 363 with rows that go out
+// by way of shared memory; a maximum of the tile before instead of the tile's own gains
+// nothing.  Items claimed two ahead 156 us, one 129 (those 5 prompts).
+//
+// Against the kernel for everything else (fp16 products by mma.sync), 32 heads on 8, d = 128, us:
+// one prompt of 1 token 9.1 (6.4), 16 9.3 (7.8), 128 10.6 (13.8), 512 15 (33), 8,192 360 (2,815);
+// d = 64, 16 on 4, 128 tokens 9.3 (11.7), 4,096 49 (202).  The shortest are not
+// given to that one: a prompt's results would depend on how it is cut.
 //
 // Every wait has a limit; one that gives up sets the workspace's timeout word and stops
 // its CTA: the warps that start copies and products end at their next wait and wait for
@@ -73,6 +89,11 @@ struct Shape {
     static constexpr int kStageBytes = 1024;       // of a warp, for its rows on their way out
     static constexpr size_t kBytes = 1024 + kQBytes + (size_t)kSlots * kSlotBytes + 16 * kStageBytes;
     static constexpr int kO = 256;         // TMEM column of the outputs; the scores are at 0 and 128
+    // Whether P has columns of its own and a row tile's next scores may come once the last
+    // have been read.
+    static constexpr bool kOwnP = D == 64;
+    static constexpr int kP = kOwnP ? kO + 2 * D : 0;      // P of row tile 0
+    static constexpr int kPTile = kOwnP ? 64 : 128, kPHalf = kPTile / 2;
 };
 
 struct Seq {
@@ -94,13 +115,13 @@ struct alignas(16) Item {
 
 struct Shared {
     uint64_t kv_full[8], kv_land[8], kv_empty[8], q_full, q_empty, kv_started, done;
-    uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2], item_full[kItems], item_empty[kItems];
+    uint64_t s_full[2], s_read[2], p_full[2], pv_done[2], o_empty[2], item_full[kItems], item_empty[kItems];
     Item item[kItems];
     uint32_t tmem;
     int dead;
     int total;                             // row tile pairs of all sequences, for one cache head
     int per;                               // sequences of a table entry
-    float top[2][2][128];                  // of a row tile and half of a tile's keys, by row
+    float top[2][2][2][128];               // of a row tile and half of a tile's keys, by row; by turns
     float sum[2][2][128];
     int bad_tile;                          // one past the last tile with a note
     alignas(16) uint32_t bad[kRingMeta][4];    // a tile's keys with inf or NaN in v
@@ -603,7 +624,8 @@ __device__ __forceinline__ void commit_if(uint64_t* bar, bool ok)
 
 // For both row tiles in turn, the output of tile j and the scores of tile j + 1, which
 // go where tile j's scores and P were (the tensor core runs one thread's products in
-// order).  Once a wait has given up no product is issued and nothing signalled any
+// order); with P in columns of its own both row tiles' scores first, once the last have been
+// read.  Once a wait has given up no product is issued and nothing signalled any
 // more; that is a predicate, so that the loops have one way out.
 template <int D>
 __device__ void mma_role(Shared& sh, const PromptArgs& a, uint32_t q_smem, uint32_t slots, uint32_t tmem, int lane)
@@ -640,12 +662,29 @@ __device__ void mma_role(Shared& sh, const PromptArgs& a, uint32_t q_smem, uint3
             const bool more = j + 1 < cnt;
             const int ev = j >= 0 ? take() : 0;
             int ek = -1;
+            const auto scores = [&](int i, int tiles) {
+                if (j + 1 >= tiles) return;
+                if (ek < 0) ek = take();
+                const int t = (i ? done1 : done0) + j + 1;
+                if (Sh::kOwnP && t > 0) {
+                    ok &= wait_lane(sh, &sh.s_read[i], (uint32_t)(t - 1) & 1, a.status);
+                    __syncwarp();
+                    tc_fence_after();
+                }
+                const uint32_t k = slots + (uint32_t)ek * Sh::kSlotBytes;
+                issue_qk<D>(tmem + i * 128, q_desc + (uint64_t)(i * 128 * D * 2 / 16), make_sdesc(k, 16, 1024, kSwizzle128B), id_qk, ok);
+                commit_if(&sh.s_full[i], ok);
+            };
+            if (Sh::kOwnP) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) scores(i, i ? it.cnt[1] : it.cnt[0]);
+                if (more) commit_if(&sh.kv_empty[ek], ok);
+            }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int tiles = i ? it.cnt[1] : it.cnt[0];
-                const uint32_t sc = tmem + i * 128;
                 if (j >= 0 && j < tiles) {
-                    const uint32_t v = slots + (uint32_t)ev * Sh::kSlotBytes;
+                    const uint32_t v = slots + (uint32_t)ev * Sh::kSlotBytes, pt = tmem + Sh::kP + i * Sh::kPTile;
                     const uint64_t v_desc = make_sdesc(v, KT * 128, 1024, kSwizzle128B);
                     const uint32_t o = tmem + Sh::kO + i * D;
                     ok &= wait_lane(sh, &sh.p_full[i], (uint32_t)((i ? done1 : done0) + j) & 1, a.status);
@@ -653,19 +692,14 @@ __device__ void mma_role(Shared& sh, const PromptArgs& a, uint32_t q_smem, uint3
                     if (j == 0 && before > 0) ok &= wait_lane(sh, &sh.o_empty[i], (uint32_t)(before - 1) & 1, a.status);
                     __syncwarp();
                     tc_fence_after();
-                    issue_pv(o, sc, v_desc, id_pv, j > 0, ok);
-                    issue_pv(o, sc + 64, v_desc + 512, id_pv, 1, ok);
+                    issue_pv(o, pt, v_desc, id_pv, j > 0, ok);
+                    issue_pv(o, pt + Sh::kPHalf, v_desc + 512, id_pv, 1, ok);
                     commit_if(&sh.pv_done[i], ok);
                 }
-                if (j + 1 < tiles) {
-                    if (ek < 0) ek = take();
-                    const uint32_t k = slots + (uint32_t)ek * Sh::kSlotBytes;
-                    issue_qk<D>(sc, q_desc + (uint64_t)(i * 128 * D * 2 / 16), make_sdesc(k, 16, 1024, kSwizzle128B), id_qk, ok);
-                    commit_if(&sh.s_full[i], ok);
-                }
+                if (!Sh::kOwnP) scores(i, tiles);
             }
             if (j >= 0) commit_if(&sh.kv_empty[ev], ok);
-            if (more) commit_if(&sh.kv_empty[ek], ok);
+            if (!Sh::kOwnP && more) commit_if(&sh.kv_empty[ek], ok);
             if (j + 2 == cnt) commit_if(&sh.q_empty, ok);
         }
         done0 += it.cnt[0];
@@ -751,6 +785,7 @@ __device__ void softmax_role(Shared& sh, const PromptArgs& a, const Plan& p, uin
     const int r = (warp & 3) * 32 + lane;          // row of the row tile
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = lanes + i * 128 + half * 64, to = lanes + Sh::kO + i * D + half * H;
+    const uint32_t tp = lanes + Sh::kP + i * Sh::kPTile + half * Sh::kPHalf;
     const uint32_t bar = 1 + i * 4 + (warp & 3);   // named barrier of the two warps of these rows
     const int tok = r < p.rows ? r / a.G : 1 << 29, g = r < p.rows ? r - tok * a.G : 0;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
@@ -773,6 +808,11 @@ __device__ void softmax_role(Shared& sh, const PromptArgs& a, const Plan& p, uin
             tmem_ld32(ts, x[0]);
             tmem_ld32(ts + 32, x[1]);
             tmem_ld_wait();
+            if (Sh::kOwnP) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.s_read[i]);
+            }
             if ((j + 1) * KT > all) {
                 const int left = lim - j * KT - half * 64;         // this thread's keys from here on are hidden
 #pragma unroll
@@ -788,9 +828,11 @@ __device__ void softmax_role(Shared& sh, const PromptArgs& a, const Plan& p, uin
                 for (int e = 2; e < 16; e += 2) tops[c] = max3(tops[c], x[c >> 1][at + e], x[c >> 1][at + e + 1]);
             }
             float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-            sh.top[i][half][r] = top;
+            // (by turns: with scores that come early the other half may be a tile behind)
+            float(&at_top)[2][128] = sh.top[Sh::kOwnP ? j & 1 : 0][i];
+            at_top[half][r] = top;
             named_bar_sync(bar, 64);
-            top = fmaxf(top, sh.top[i][half ^ 1][r]) * a.scale_log2;   // the scale is positive on this path
+            top = fmaxf(top, at_top[half ^ 1][r]) * a.scale_log2;   // the scale is positive on this path
             const bool grow = top > m + kSlack || (m == -INFINITY && top > m);
             if (__any_sync(0xffffffffu, grow)) {
                 const float m2 = grow ? top : m;
@@ -826,7 +868,12 @@ __device__ void softmax_role(Shared& sh, const PromptArgs& a, const Plan& p, uin
                 sum[e & 1] = add2(sum[e & 1], pack2(e0, e1));
                 e2[e] = pack_bf16x2(e0, e1);
             }
-            tmem_st32(ts, e2);                     // over this half's scores, all of them in registers
+            if (Sh::kOwnP && j > 0) {              // P of the tile before is in use until its product is done
+                wait_lane(sh, &sh.pv_done[i], (uint32_t)(done + j - 1) & 1, a.status);
+                __syncwarp();
+                tc_fence_after();
+            }
+            tmem_st32(tp, e2);                     // (d = 128: over this half's scores, all of them in registers)
             float s0, s1;
             unpack2(add2(sum[0], sum[1]), s0, s1);
             l += s0 + s1;
@@ -903,6 +950,7 @@ prompt_attention_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_co
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.s_read[i], 8);
             mbar_init(&sh.p_full[i], 8);
             mbar_init(&sh.pv_done[i], 1);
             mbar_init(&sh.o_empty[i], 8);
@@ -970,7 +1018,9 @@ cudaError_t launch(PromptArgs a, int sms, cudaStream_t stream)
     const size_t bytes = Shape<D>::kBytes;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    // every sequence has at most one pair of row tiles that is not full
+    // Every sequence has at most one pair of row tiles that is not full.  Claimed or dealt to
+    // and fro, us: one prompt of 509 tokens (64 items) 18.7 and 15.1, 3 x 3,000 (564 items) 175
+    // and 214, 8,192 (1,024) 362 and 352, 65,536 (2,048) 5,385 and 6,061.
     const long long items = ((long long)a.T / (2 * p.tok) + a.N) * a.Hkv;
     if (items > 2ll * sms) {
         const cudaError_t z = cudaMemsetAsync(a.counter, 0, sizeof(uint32_t), stream);

@@ -590,15 +590,17 @@ size_t kda_prompt_attention_workspace_bytes(int32_t num_seqs, int32_t Hq,
  *                 do not exist; of sequences that claim the same row one gets it.
  *   workspace     kda_prompt_attention_workspace_bytes(...) bytes, 256-byte aligned,
  *                 not shared with concurrent calls; contents on entry do not matter.
- *                 Bit 1 of the int32 at byte 8 is set when a wait of the tensor-core
+ *                 Bit 1 of the int32 at byte 8 is set when a wait of the tcgen05
  *                 kernel has given up (after some two seconds), which no call
  *                 clears; the rows of o that depended on it are NaN.
- * dtype is that of q, k, v, and of o.  KDA_BF16 with d = 64 or 128, scale > 0 and
- * Hq / Hkv <= 128 runs on the tensor cores, with probabilities rounded to bf16 for
- * the second product; everything else, and everything when the environment variable
- * KDA_FORCE_SIMT is set, on the CUDA cores in fp32.  An infinity or NaN in a
- * row of k or v reaches the queries that see it and no others.  The result does not
- * depend on timing. */
+ * dtype is that of q, k, v, and of o.  KDA_BF16 with d = 64 or 128, scale > 0,
+ * Hq / Hkv <= 128, Hq <= 2^16 and total_tokens, total_keys <= 2^27 runs on tcgen05,
+ * with probabilities rounded to bf16 for the second product; everything else in
+ * products of fp16 pairs: bf16 inputs exactly, fp32 ones to 22 bits, probabilities to 11
+ * bits for a bf16 output and to 22 for an fp32 one; sums are fp32.  When the
+ * environment variable KDA_FORCE_SIMT is set everything runs on the CUDA cores in
+ * fp32.  An infinity or NaN in a row of k or v reaches the queries that see it and no
+ * others.  The result does not depend on timing. */
 kda_status_t kda_prompt_attention(const void *q, const void *k, const void *v,
                                   int64_t q_stride, int64_t k_stride,
                                   int64_t v_stride, const int32_t *cu_seqlens,
@@ -630,13 +632,15 @@ kda_status_t kda_prompt_attention(const void *q, const void *k, const void *v,
  *   inv_freq      device fp32 [rot_dim / 2]; rot_dim is a multiple of 16, 16 .. d
  *   block         0: the cache is in k's dtype, page_stride in elements, and
  *                 the scales are not used.  Else the cache has 8 bits, a scale for
- *                 each `block` rows (1 .. 128, more is KDA_ERR_UNSUPPORTED; it divides page_size): see above.
+ *                 each `block` rows (1 .. 128, more is KDA_ERR_UNSUPPORTED; it divides
+ *                 page_size): see above.
  *                 A block that the sequence has already begun keeps its rows: when
  *                 the new ones need a larger scale they are rounded to it.  Scales of
  *                 such blocks must be those that this call wrote (or other powers
  *                 of two).  Two sequences must not write one block.
  *   new_lengths   [N] (written) or NULL; must overlap no input
- * dtype is that of q, k, v, q_out and k_out (KDA_BF16_F32OUT is KDA_BF16 here); all arithmetic is fp32. */
+ * dtype is that of q, k, v, q_out and k_out (KDA_BF16_F32OUT is KDA_BF16 here); all
+ * arithmetic is fp32. */
 kda_status_t kda_cache_append_rotary(
     const void *q, const void *k, const void *v, int64_t q_stride,
     int64_t k_stride, int64_t v_stride, const int32_t *cu_seqlens,
@@ -663,7 +667,7 @@ size_t kda_cache_attention_e4m3_workspace_bytes(int32_t N, int32_t Ts,
  *   k_cache, v_cache, k_scales, v_scales, page_table, num_pages, page_size,
  *   max_pages, page_stride, block   see above; page_size at most 65536 (more is
  *                 KDA_ERR_UNSUPPORTED).  Positions whose table entry names no page are
- *                 hidden.  Rows past lengths[n] are never read.
+ *                 hidden.  Rows past lengths[n] do not count, whatever they hold.
  *   lengths       device int32 [N], rows with those of the Ts tokens (values outside
  *                 [0, max_pages * page_size] are clamped)
  *   workspace     kda_cache_attention_e4m3_workspace_bytes(...) bytes, 256-byte
@@ -675,8 +679,9 @@ size_t kda_cache_attention_e4m3_workspace_bytes(int32_t N, int32_t Ts,
  * to 11 bits), with fp32 queries or output of sums of two (22 bits); sums are fp32.
  * A scale of NaN makes the tokens that see a row of its block NaN and no others;
  * an e4m3 code of NaN, which kda_cache_append_rotary never writes, may reach all
- * tokens of its sequence; an infinity or NaN in q makes that head's output NaN.  No atomics: the result does not depend on
- * timing; it may differ in rounding between GPUs with different SM counts. */
+ * tokens of its sequence; an infinity or NaN in q makes that head's output NaN.  No
+ * atomics: the result does not depend on timing; it may differ in rounding between GPUs
+ * with different SM counts, and with the other sequences of the call. */
 kda_status_t kda_cache_attention_e4m3(
     const void *q, const void *k_cache, const void *v_cache,
     const float *k_scales, const float *v_scales, const int32_t *page_table,
