@@ -809,7 +809,8 @@ def kda_prompt_attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=N
     to no sequence keep what they hold.  NaN in o where the inputs have none means
     that a wait in the kernel gave up."""
     torch = _torch()
-    _forward_only("kda_prompt_attention", q, k, v)
+    if torch.is_grad_enabled():
+        _forward_only("kda_prompt_attention", q, k, v)
     T, Hq, d = q.shape
     Tk, Hkv, _ = k.shape
     dev, at, dtype = q.device, q.get_device(), q.dtype
@@ -868,12 +869,14 @@ def _pages_ok(k_cache, v_cache, dtype, at, h, d):
 
 
 def _scales_ok(k_scales, v_scales, f32, at, pages, page, h):
-    return (k_scales is not None and v_scales is not None and k_scales.dtype is f32
+    if k_scales is None or v_scales is None:
+        return False
+    shape = k_scales.shape
+    return (k_scales.dtype is f32
             and v_scales.dtype is f32 and k_scales.get_device() == at
             and v_scales.get_device() == at and k_scales.is_contiguous()
-            and v_scales.is_contiguous() and v_scales.shape == k_scales.shape
-            and k_scales.shape == (pages, k_scales.shape[1], h) and k_scales.shape[1] > 0
-            and page % k_scales.shape[1] == 0)
+            and v_scales.is_contiguous() and v_scales.shape == shape
+            and shape == (pages, shape[1], h) and shape[1] > 0 and page % shape[1] == 0)
 
 
 def _explain_pages(k_cache, v_cache, k_scales, v_scales, dtype, h, d, dev):
@@ -908,8 +911,10 @@ def kda_cache_append_rotary(q, k, v, cu_seqlens, inv_freq, k_cache, v_cache, pag
     q_out, k_out may be q and k themselves.  Returns (q_out, k_out, new_lengths);
     k_out is None when it was neither given nor wanted."""
     torch = _torch()
-    _forward_only("kda_cache_append_rotary", k, v, inv_freq, *(() if q is None else (q,)))
-    T, Hkv, d = k.shape
+    if torch.is_grad_enabled():
+        _forward_only("kda_cache_append_rotary", k, v, inv_freq, *(() if q is None else (q,)))
+    shape = k.shape
+    T, Hkv, d = shape
     dev, at, dtype = k.device, k.get_device(), k.dtype
     i32, f32 = torch.int32, torch.float32
     if dtype is torch.bfloat16:
@@ -919,11 +924,13 @@ def kda_cache_append_rotary(q, k, v, cu_seqlens, inv_freq, k_cache, v_cache, pag
     else:
         raise TypeError("unsupported dtype %s" % dtype)
     N, max_pages = lengths.shape[0], page_table.shape[1]
-    eight = k_cache.dtype is torch.float8_e4m3fn
-    held = k_cache.dtype if eight else dtype
-    pages, page = k_cache.shape[0], k_cache.shape[1]
+    held = k_cache.dtype
+    eight = held is torch.float8_e4m3fn
+    if not eight:
+        held = dtype
+    pages, page = k_cache.shape[:2]
     k_stride, v_stride = _rows_stride(k, Hkv, d), _rows_stride(v, v.shape[1], d)
-    if not (at >= 0 and v.get_device() == at and v.dtype is dtype and v.shape == k.shape
+    if not (at >= 0 and v.get_device() == at and v.dtype is dtype and v.shape == shape
             and k_stride >= 0 and v_stride >= 0
             and cu_seqlens.get_device() == at and cu_seqlens.dtype is i32
             and cu_seqlens.is_contiguous() and cu_seqlens.shape == (N + 1,)
@@ -950,25 +957,28 @@ def kda_cache_append_rotary(q, k, v, cu_seqlens, inv_freq, k_cache, v_cache, pag
     Hq = q_stride = q_out_stride = k_out_stride = 0
     if q is not None:
         Hq = q.shape[1]
+        full = T, Hq, d
+        q_stride = _rows_stride(q, Hq, d)
         if q_out is None:
-            q_out = _new((T, Hq, d), dtype, dev, stream)
-        q_stride, q_out_stride = _rows_stride(q, Hq, d), _rows_stride(q_out, q_out.shape[1], d)
-        if not (q.get_device() == at and q.dtype is dtype and q.shape == (T, Hq, d)
+            q_out, q_out_stride = _new(full, dtype, dev, stream), Hq * d
+        else:
+            q_out_stride = _rows_stride(q_out, q_out.shape[1], d)
+        if not (q.get_device() == at and q.dtype is dtype and q.shape == full
                 and q_stride >= 0 and q_out.get_device() == at and q_out.dtype is dtype
-                and q_out.shape == q.shape and q_out_stride >= 0):
+                and q_out.shape == full and q_out_stride >= 0):
             for name, t in (("q", q), ("q_out", q_out)):
                 _check_rows(name, t, dtype, dev)
-                _shape(name, t, (T, Hq, d))
+                _shape(name, t, full)
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    if k_out is None and want_k:
-        k_out = _new((T, Hkv, d), dtype, dev, stream)
     if k_out is not None:
         k_out_stride = _rows_stride(k_out, k_out.shape[1], d)
-        if not (k_out.get_device() == at and k_out.dtype is dtype and k_out.shape == k.shape
+        if not (k_out.get_device() == at and k_out.dtype is dtype and k_out.shape == shape
                 and k_out_stride >= 0):
             _check_rows("k_out", k_out, dtype, dev)
             _shape("k_out", k_out, (T, Hkv, d))
+    elif want_k:
+        k_out, k_out_stride = _new((T, Hkv, d), dtype, dev, stream), Hkv * d
     new_lengths = _out("new_lengths", new_lengths, (N,), i32, dev, stream)
     _call("kda_cache_append_rotary", dev, stream, None if q is None else q.data_ptr(), k.data_ptr(),
           v.data_ptr(), q_stride, k_stride, v_stride, cu_seqlens.data_ptr(), T,
@@ -1004,7 +1014,8 @@ def kda_cache_attention_e4m3(q, k_cache, v_cache, k_scales, v_scales, page_table
     rows 0 .. lengths[n] - Ts + t.  scale: d ** -0.5 by default.  Returns o [N, Ts,
     Hq, d]."""
     torch = _torch()
-    _forward_only("kda_cache_attention_e4m3", q, k_scales, v_scales)
+    if torch.is_grad_enabled():
+        _forward_only("kda_cache_attention_e4m3", q, k_scales, v_scales)
     N, Ts, Hq, d = q.shape
     dev, at = q.device, q.get_device()
     i32, e4m3 = torch.int32, torch.float8_e4m3fn

@@ -119,7 +119,7 @@ def test_attention_workspace(lib):
     for bad in ((0, 1, 8, 2, 64, BF16), (2, 0, 8, 2, 64, BF16), (2, 1, 7, 2, 64, BF16), (2, 1, 8, 2, 48, BF16),
                 (2, 1, 8, 2, 64, 5), (1, 1 << 20, 1 << 10, 1, 64, BF16), (1, 1, 1 << 30, 1, 64, BF16)):
         assert size(*bad) == 0
-    assert size(1, 4, 32, 8, 128, BF16) == size(1000, 4, 32, 8, 128, BF16) > 256
+    assert size(1, 4, 32, 8, 128, BF16) == size(1000, 4, 32, 8, 128, BF16) > 0
 
 
 def _calls():
