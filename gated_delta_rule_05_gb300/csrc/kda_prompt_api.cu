@@ -95,8 +95,8 @@ kda_status_t kda_prompt_attention(const void* q, const void* k, const void* v, i
         !row_stride_ok(v_stride, kw, total_keys, elem))
         return KDA_ERR_INVALID_ARG;
     if (total_tokens == 0) return KDA_OK;
-    // a row tile is a block index
-    if ((total_tokens * (Hq / Hkv)) / 64 + num_seqs > INT32_MAX) return KDA_ERR_INVALID_ARG;
+    // a row tile of a key head is a block index
+    if (((total_tokens * (Hq / Hkv)) / 64 + num_seqs) * Hkv > INT32_MAX) return KDA_ERR_INVALID_ARG;
     const size_t o_bytes = (size_t)total_tokens * qw * out_bytes(dtype);
     const size_t cu_bytes = 4 * ((size_t)num_seqs + 1);
     if (meets(row_span(q, q_stride, qw, total_tokens, elem), o, o_bytes) ||

@@ -332,3 +332,28 @@ def test_many_sequences(kda, N, Ts, Hq, Hkv, d, page, block, dtype):
     keep = torch.ones(o.shape[:3], dtype=torch.bool)
     keep[6, :, G:2 * G] = keep[5] = False
     assert torch.equal(p[keep.cuda()], o[keep.cuda()])
+
+
+@pytest.mark.parametrize("N,Ts,Hq,Hkv,lengths", [(2, 200, 16, 2, [700, 150]), (3, 60, 8, 1, [61, 333, 0])])
+def test_many_tokens(kda, N, Ts, Hq, Hkv, lengths):
+    # so many row tiles that a thread block has all items of one, or that few share them
+    c = Call(N, Ts, Hq, Hkv, 64, 32, 16, lengths, BF16, seed=Ts)
+    check(c.run(kda), *c.reference(), exact_p=False)
+
+
+def test_sequences_share_pages(kda):
+    # a common prefix: the same pages in every row of the table, and one page twice
+    c = Call(1, 1, 8, 2, 128, 32, 16, [500], BF16, seed=21)
+    args = c.args()
+    one = args["page_table"]
+    n = 50
+    args["q"] = args["q"].expand(n, 1, 8, 128).contiguous()
+    args["page_table"] = one.expand(n, one.shape[1]).contiguous()
+    args["lengths"] = args["lengths"].expand(n).contiguous()
+    ref, mag = c.reference()
+    o = kda.kda_cache_attention_e4m3(**args)
+    check(o, ref.repeat(n, 0), mag.repeat(n, 0), exact_p=False)
+    args["page_table"][:, 1] = args["page_table"][:, 0]
+    c.table[:, 1] = c.table[:, 0]
+    ref, mag = c.reference()
+    check(kda.kda_cache_attention_e4m3(**args), ref.repeat(n, 0), mag.repeat(n, 0), exact_p=False)

@@ -323,3 +323,17 @@ def test_offsets_beyond_32_bits(kda):
         assert torch.equal(tail[62:65], (x.float() / by).to(E4M3).view(torch.uint8))
         assert torch.all(tail[:62] == fill) and torch.all(tail[65:] == fill)
         assert torch.all(s[-2] == 1) and torch.all(s[:-2] == 1)
+
+
+@pytest.mark.parametrize("block", [0, 16])
+def test_more_sequences_than_are_held(kda, block):
+    rng = np.random.default_rng(4)
+    c = Call(rng.integers(0, 4, 1300).tolist(), rng.integers(0, 40, 1300).tolist(), 2, 1, 32, 16, block, BF16, seed=20)
+    c.check(*c.run(kda))
+
+
+@pytest.mark.parametrize("lens,Hkv", [([6000], 4), ([90] * 60, 8)])
+def test_heads_in_several_parts(kda, lens, Hkv):
+    # more units than SMs and fewer, so that a window's heads go to one thread block or several
+    c = Call(lens, [5] * len(lens), Hkv, Hkv, 64, 64, 32, BF16, seed=len(lens))
+    c.check(*c.run(kda))
