@@ -22,7 +22,7 @@
 // The row tiles share K and V and alternate on the tensor core: one's softmax runs under
 // the other's products.  Tensor memory's 512 columns hold two S, two O and, with d = 64, two P: there
 // the next scores are computed while these are worked on (5 prompts of 700 to 2,048
-// tokens behind prefixes, 16 heads, 129.5 us without and 123 with).
+// tokens behind prefixes, 16 heads, 129.5 us without and 121.5 with).
 //
 // Values that a row of the item does not see must not reach it through 0 * inf: in the
 // tiles on the diagonal and at the end of a sequence the fourth warp replaces
@@ -38,7 +38,7 @@
 //
 // Bound by the softmax beside the products: 32 heads on 8, d = 128, one prompt of 65,536
 // tokens (8 heads) 5.4 ms, 1.63 PFLOP/s, of 8,192 0.36 ms (1.5), of 2,048 34 us (1.0); 12 of 512
-// to 12,288 3.5 ms (1.53).  d = 64, 16 heads on 4, 16,384 tokens 567 us (0.97): half the products for
+// to 12,288 3.5 ms (1.53).  d = 64, 16 heads on 4, 16,384 tokens 545 us (1.0): half the products for
 // as many exponentials.  Steps on the way there, 8 x 2,048 tokens: 445 us with the
 // products' loop rolled up (349 without), 291 with the output in a warpgroup of its own (250);
 // 8,192 tokens 394 us with 16-byte stores of rows, 372 with 32-byte ones, 363 with rows that go out
@@ -624,8 +624,10 @@ __device__ __forceinline__ void commit_if(uint64_t* bar, bool ok)
 
 // For both row tiles in turn, the output of tile j and the scores of tile j + 1, which
 // go where tile j's scores and P were (the tensor core runs one thread's products in
-// order); with P in columns of its own both row tiles' scores first, once the last have been
-// read.  Once a wait has given up no product is issued and nothing signalled any
+// order); with P in columns of its own each row tile's scores before its output, once the last have
+// been read.  (Both row tiles' scores first and then both outputs lets them fall into step, and
+// both are at their exponentials at once: 16,384 tokens, d = 64, 567 us instead of 545.)
+// Once a wait has given up no product is issued and nothing signalled any
 // more; that is a predicate, so that the loops have one way out.
 template <int D>
 __device__ void mma_role(Shared& sh, const PromptArgs& a, uint32_t q_smem, uint32_t slots, uint32_t tmem, int lane)
@@ -675,14 +677,10 @@ __device__ void mma_role(Shared& sh, const PromptArgs& a, uint32_t q_smem, uint3
                 issue_qk<D>(tmem + i * 128, q_desc + (uint64_t)(i * 128 * D * 2 / 16), make_sdesc(k, 16, 1024, kSwizzle128B), id_qk, ok);
                 commit_if(&sh.s_full[i], ok);
             };
-            if (Sh::kOwnP) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) scores(i, i ? it.cnt[1] : it.cnt[0]);
-                if (more) commit_if(&sh.kv_empty[ek], ok);
-            }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int tiles = i ? it.cnt[1] : it.cnt[0];
+                if (Sh::kOwnP) scores(i, tiles);
                 if (j >= 0 && j < tiles) {
                     const uint32_t v = slots + (uint32_t)ev * Sh::kSlotBytes, pt = tmem + Sh::kP + i * Sh::kPTile;
                     const uint64_t v_desc = make_sdesc(v, KT * 128, 1024, kSwizzle128B);
@@ -699,7 +697,7 @@ __device__ void mma_role(Shared& sh, const PromptArgs& a, uint32_t q_smem, uint3
                 if (!Sh::kOwnP) scores(i, tiles);
             }
             if (j >= 0) commit_if(&sh.kv_empty[ev], ok);
-            if (!Sh::kOwnP && more) commit_if(&sh.kv_empty[ek], ok);
+            if (more) commit_if(&sh.kv_empty[ek], ok);
             if (j + 2 == cnt) commit_if(&sh.q_empty, ok);
         }
         done0 += it.cnt[0];
