@@ -172,14 +172,22 @@ def kda_prefill_workspace_bytes(num_seqs: int, H: int, d_k: int, d_v: int) -> in
     return int(lib().kda_prefill_workspace_bytes(num_seqs, H, d_k, d_v))
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t, out_dtype):
     """The C ABI's dtype code for inputs of t.dtype and an output of out_dtype."""
     torch = _torch()
+    if out_dtype is torch.bfloat16 and t.dtype is out_dtype:
+        return KDA_BF16
     if t.dtype == torch.bfloat16 and out_dtype == torch.bfloat16:
         return KDA_BF16
     if t.dtype == torch.bfloat16 and out_dtype == torch.float32:
@@ -533,9 +541,9 @@ def _call(name, device, stream, *args):
     """lib().<name>(*args, stream) on ``device``; raises KdaError."""
     torch = _torch()
     f = getattr(_lib if _lib is not None else lib(), name)
-    raw = stream.cuda_stream if stream is not None else \
-        torch._C._cuda_getCurrentRawStream(device.index)
-    if torch._C._cuda_getDevice() == device.index:
+    at = device.index
+    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(at)
+    if torch._C._cuda_getDevice() == at:
         rc = f(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -762,6 +770,8 @@ def kda_cache_append(k, v, cu_seqlens, k_cache, v_cache, page_table, lengths, *,
 def _rows_stride(t, h, d):
     """The stride of tokens [T, h, d] that are dense within a token; -1: they are not."""
     row, head, one = t.stride()
+    if one == 1 and head == d and row >= h * d:    # (of one token it does not count)
+        return row
     if (one != 1 and d > 1) or (head != d and h > 1):
         if t.numel():
             return -1
@@ -809,22 +819,28 @@ def kda_prompt_attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=N
     to no sequence keep what they hold.  NaN in o where the inputs have none means
     that a wait in the kernel gave up."""
     torch = _torch()
-    if torch.is_grad_enabled():
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
         _forward_only("kda_prompt_attention", q, k, v)
     T, Hq, d = q.shape
-    Tk, Hkv, _ = k.shape
+    shape = k.shape
+    Tk, Hkv, dk = shape
     dev, at, dtype = q.device, q.get_device(), q.dtype
+    i32 = torch.int32
     if o_dtype is None:
         o_dtype = dtype if o is None else o.dtype
     dt = _dtype_code(q, o_dtype)
     N = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    strides = _rows_stride(q, Hq, d), _rows_stride(k, Hkv, d), _rows_stride(v, v.shape[1], d)
+    q_stride, k_stride = _rows_stride(q, Hq, d), _rows_stride(k, Hkv, d)
+    v_stride = _rows_stride(v, v.shape[1], d)
     if not (at >= 0 and k.get_device() == at and v.get_device() == at and k.dtype is dtype
-            and v.dtype is dtype and k.shape[2] == d and v.shape == k.shape and min(strides) >= 0
+            and v.dtype is dtype and dk == d and v.shape == shape
+            and q_stride >= 0 and k_stride >= 0 and v_stride >= 0
+            and (cu_seqlens is None or (cu_seqlens.get_device() == at and cu_seqlens.dtype is i32
+                                        and cu_seqlens.is_contiguous()))
             and (Tk == T if cu_seqlens_k is None else
-                 cu_seqlens is not None and cu_seqlens_k.shape == cu_seqlens.shape)
-            and all(c is None or (c.get_device() == at and c.dtype is torch.int32
-                                  and c.is_contiguous()) for c in (cu_seqlens, cu_seqlens_k))):
+                 cu_seqlens is not None and cu_seqlens_k.shape == cu_seqlens.shape
+                 and cu_seqlens_k.get_device() == at and cu_seqlens_k.dtype is i32
+                 and cu_seqlens_k.is_contiguous())):
         for name, t in (("q", q), ("k", k), ("v", v)):
             _check_rows(name, t, dtype, dev)
         _check_on("cu_seqlens", cu_seqlens, torch.int32, dev)
@@ -836,15 +852,20 @@ def kda_prompt_attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=N
         if cu_seqlens is None:
             raise ValueError("cu_seqlens_k needs cu_seqlens")
         _shape("cu_seqlens_k", cu_seqlens_k, cu_seqlens.shape)
-    o = _out("o", o, (T, Hq, d), o_dtype, dev, stream)
+    if o is None:
+        o = _new((T, Hq, d), o_dtype, dev, stream)
+    else:
+        _out("o", o, (T, Hq, d), o_dtype, dev, stream)
     if workspace is None:
-        workspace = _new((_prompt_bytes(N, Hq, Hkv, d, dt),), torch.uint8, dev, stream)
+        size = _prompt_bytes(N, Hq, Hkv, d, dt)
+        workspace = _new((size,), torch.uint8, dev, stream)
     else:
         _check_on("workspace", workspace, None, dev)
-    _call("kda_prompt_attention", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
-          _address(cu_seqlens), _address(cu_seqlens_k), N, T, Tk, Hq, Hkv, d, dt,
-          d ** -0.5 if scale is None else scale, o.data_ptr(), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+        size = workspace.numel() * workspace.element_size()
+    _call("kda_prompt_attention", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          q_stride, k_stride, v_stride, _address(cu_seqlens), _address(cu_seqlens_k), N, T, Tk,
+          Hq, Hkv, d, dt, d ** -0.5 if scale is None else scale, o.data_ptr(),
+          workspace.data_ptr(), size)
     return o
 
 
@@ -911,7 +932,8 @@ def kda_cache_append_rotary(q, k, v, cu_seqlens, inv_freq, k_cache, v_cache, pag
     q_out, k_out may be q and k themselves.  Returns (q_out, k_out, new_lengths);
     k_out is None when it was neither given nor wanted."""
     torch = _torch()
-    if torch.is_grad_enabled():
+    if torch.is_grad_enabled() and (k.requires_grad or v.requires_grad or inv_freq.requires_grad
+                                    or (q is not None and q.requires_grad)):
         _forward_only("kda_cache_append_rotary", k, v, inv_freq, *(() if q is None else (q,)))
     shape = k.shape
     T, Hkv, d = shape
@@ -979,7 +1001,10 @@ def kda_cache_append_rotary(q, k, v, cu_seqlens, inv_freq, k_cache, v_cache, pag
             _shape("k_out", k_out, (T, Hkv, d))
     elif want_k:
         k_out, k_out_stride = _new((T, Hkv, d), dtype, dev, stream), Hkv * d
-    new_lengths = _out("new_lengths", new_lengths, (N,), i32, dev, stream)
+    if new_lengths is None:
+        new_lengths = _new((N,), i32, dev, stream)
+    else:
+        _out("new_lengths", new_lengths, (N,), i32, dev, stream)
     _call("kda_cache_append_rotary", dev, stream, None if q is None else q.data_ptr(), k.data_ptr(),
           v.data_ptr(), q_stride, k_stride, v_stride, cu_seqlens.data_ptr(), T,
           inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0,
@@ -1014,7 +1039,8 @@ def kda_cache_attention_e4m3(q, k_cache, v_cache, k_scales, v_scales, page_table
     rows 0 .. lengths[n] - Ts + t.  scale: d ** -0.5 by default.  Returns o [N, Ts,
     Hq, d]."""
     torch = _torch()
-    if torch.is_grad_enabled():
+    if torch.is_grad_enabled() and (q.requires_grad or k_scales.requires_grad
+                                    or v_scales.requires_grad):
         _forward_only("kda_cache_attention_e4m3", q, k_scales, v_scales)
     N, Ts, Hq, d = q.shape
     dev, at = q.device, q.get_device()
@@ -1036,16 +1062,21 @@ def kda_cache_attention_e4m3(q, k_cache, v_cache, k_scales, v_scales, page_table
         _explain_pages(k_cache, v_cache, k_scales, v_scales, e4m3, Hkv, d, dev)
         _shape("page_table", page_table, (N, max_pages))
         _shape("lengths", lengths, (N,))
-    o = _out("o", o, (N, Ts, Hq, d), o_dtype, dev, stream)
+    if o is None:
+        o = _new((N, Ts, Hq, d), o_dtype, dev, stream)
+    else:
+        _out("o", o, (N, Ts, Hq, d), o_dtype, dev, stream)
     if workspace is None:
-        workspace = _new((_e4m3_bytes(dev, N, Ts, Hq, Hkv, d, dt),), torch.uint8, dev, stream)
+        size = _e4m3_bytes(at, N, Ts, Hq, Hkv, d, dt)
+        workspace = _new((size,), torch.uint8, dev, stream)
     else:
         _check_on("workspace", workspace, None, dev)
+        size = workspace.numel() * workspace.element_size()
     _call("kda_cache_attention_e4m3", dev, stream, q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), page_table.data_ptr(),
           lengths.data_ptr(), N, Ts, Hq, Hkv, d, pages, page, max_pages, k_cache.stride(0),
           page // k_scales.shape[1], dt, d ** -0.5 if scale is None else scale, o.data_ptr(),
-          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+          workspace.data_ptr(), size)
     return o
 
 
