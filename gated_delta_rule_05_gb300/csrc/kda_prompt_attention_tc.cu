@@ -2,7 +2,7 @@
 // cores (bf16, d = 64 or 128): a persistent CTA per SM, tcgen05 products with TMEM
 // accumulators.
 //
-// An item is two row tiles of 128 query rows of a (sequence, cache head); the rows
+// An item is two row tiles of 128 query rows (one, in small calls) of a (sequence, cache head); the rows
 // of the G heads that share it lie token by token, row r of a tile being head r % G
 // of its token r / G (128 / G tokens to a tile), so that a tile spans few positions.
 // Per tile of 128 keys and row tile
@@ -46,8 +46,8 @@
 // nothing.  Items claimed two ahead 156 us, one 129 (those 5 prompts).
 //
 // Against the kernel for everything else (fp16 products by mma.sync), 32 heads on 8, d = 128, us:
-// one prompt of 1 token 9.1 (6.4), 16 9.3 (7.8), 128 10.6 (13.8), 512 15 (33), 8,192 360 (2,815);
-// d = 64, 16 on 4, 128 tokens 9.3 (11.7), 4,096 49 (202).  The shortest are not
+// one prompt of 1 token 8.6 (6.4), 16 9.0 (7.8), 128 9.3 (13.8), 512 13.4 (33), 8,192 360 (2,815);
+// d = 64, 16 on 4, 128 tokens 7.7 (11.7), 4,096 46 (202).  The shortest are not
 // given to that one: a prompt's results would depend on how it is cut.
 //
 // Every wait has a limit; one that gives up sets the workspace's timeout word and stops
@@ -119,7 +119,7 @@ struct Shared {
     Item item[kItems];
     uint32_t tmem;
     int dead;
-    int total;                             // row tile pairs of all sequences, for one cache head
+    int total;                             // pairs of row tiles (see Plan::span) of all sequences, for one cache head
     int per;                               // sequences of a table entry
     float top[2][2][2][128];               // of a row tile and half of a tile's keys, by row; by turns
     float sum[2][2][128];
@@ -233,9 +233,10 @@ __device__ __forceinline__ void fewer_registers()
 struct Plan {
     int tok;                               // tokens of a row tile
     int rows;                              // rows of a row tile that are used
+    int span;                              // tokens of an item: two row tiles, or one where there are few
 };
 
-__device__ __forceinline__ int pairs_of(int lq, const Plan& p) { return (lq + 2 * p.tok - 1) / (2 * p.tok); }
+__device__ __forceinline__ int pairs_of(int lq, const Plan& p) { return (lq + p.span - 1) / p.span; }
 
 // The x-th item: sequence by sequence, of a sequence its last rows, the longest work,
 // first, and of those every head.  (Head by head takes the same time at 65,536 keys, 268 MB
@@ -294,13 +295,13 @@ __device__ __noinline__ Item item_at(const Shared& sh, const PromptArgs& a, cons
     it.lq = s.lq;
     it.k0 = s.k0;
     it.lk = s.lk;
-    it.t0 = (pairs - 1 - y) * 2 * p.tok;
+    it.t0 = (pairs - 1 - y) * p.span;
     const int off = s.lk - s.lq;
     it.all = min(max(it.t0 + off + 1, 0), s.lk);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int end = min(it.t0 + (i + 1) * p.tok, s.lq);        // one past the row tile's last token
-        const int most = it.t0 + i * p.tok < s.lq ? min(max(end + off, 0), s.lk) : 0;
+        const int most = i * p.tok < p.span && it.t0 + i * p.tok < s.lq ? min(max(end + off, 0), s.lk) : 0;
         it.cnt[i] = (most + KT - 1) / KT;
     }
     return it;
@@ -793,8 +794,8 @@ __device__ void softmax_role(Shared& sh, const PromptArgs& a, const Plan& p, uin
     for (const Item* at; (at = items.next(sh, a.status)); items.release(sh, lane)) {
         const Item& it = *at;                      // (in shared memory)
         const int cnt = it.cnt[i];
-        const int first = it.t0 + i * p.tok, off = it.lk - it.lq + 1;
-        const int lim = first + tok < it.lq ? min(max(first + tok + off, 0), it.lk) : 0;   // keys that this row sees
+        const int first = it.t0 + i * p.tok, off = it.lk - it.lq + 1, past = min(it.t0 + p.span, it.lq);
+        const int lim = first + tok < past ? min(max(first + tok + off, 0), it.lk) : 0;   // keys that this row sees
         const int all = min(max(first + off, 0), it.lk);   // and those that every row of the tile sees
         float m = -INFINITY, l = 0.f;
 #pragma unroll 1
@@ -895,7 +896,7 @@ __device__ void softmax_role(Shared& sh, const PromptArgs& a, const Plan& p, uin
                 add_nonfinite<D>(sh, a, it, tile, min(lim, cnt * KT), half, to);
         }
         // this row's place, in 16-byte pieces from the item's first row; negative: none
-        const int place = first + tok < it.lq ? ((i * p.tok + tok) * a.Hq + g) * (D / 8) + half * (H / 8) : -1;
+        const int place = first + tok < past ? ((i * p.tok + tok) * a.Hq + g) * (D / 8) + half * (H / 8) : -1;
         uint4* base = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) +
                                                ((long long)(it.q0 + it.t0) * a.Hq + (long long)it.hk * a.G) * D);
         done += cnt;
@@ -1019,7 +1020,11 @@ cudaError_t launch(PromptArgs a, int sms, cudaStream_t stream)
     // Every sequence has at most one pair of row tiles that is not full.  Claimed or dealt to
     // and fro, us: one prompt of 509 tokens (64 items) 18.7 and 15.1, 3 x 3,000 (564 items) 175
     // and 214, 8,192 (1,024) 362 and 352, 65,536 (2,048) 5,385 and 6,061.
-    const long long items = ((long long)a.T / (2 * p.tok) + a.N) * a.Hkv;
+    // One row tile to an item where that leaves no CTA more than one: one prompt of 509 tokens, 32
+    // heads on 8, d = 128, 13.4 us (two 15.0), of 1,024, 16 on 4, d = 64, 13.8 us (17.3).
+    p.span = 2 * p.tok;
+    if (((long long)a.T / p.tok + a.N) * a.Hkv <= sms) p.span = p.tok;
+    const long long items = ((long long)a.T / p.span + a.N) * a.Hkv;
     if (items > 2ll * sms) {
         const cudaError_t z = cudaMemsetAsync(a.counter, 0, sizeof(uint32_t), stream);
         if (z != cudaSuccess) return z;
