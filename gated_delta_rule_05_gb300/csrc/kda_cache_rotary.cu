@@ -322,7 +322,8 @@ __device__ __forceinline__ void rows_part(const RotaryArgs& a, const int32_t* cu
 }
 
 // Rows of a lane.  Two (twice the warps to a team) took 346 us where four took 329; loads of the
-// next head before the stores of this one spill registers (408 against 342); values
+// next head before the stores of this one spill registers (408 against 342), and by cp.async
+// into shared memory, without spills, they gain nothing (319.6 against 319.9); values
 // read from the cache lines anew instead of kept turned in registers 329 against 320.
 constexpr int kHeld = 4;
 
