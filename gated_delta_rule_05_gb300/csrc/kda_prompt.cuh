@@ -33,7 +33,7 @@ __device__ __forceinline__ void prompt_rows(const int32_t* cu, int n, int rows, 
         first = max(__ldg(cu + n), 0);
         end = min(__ldg(cu + n + 1), rows);
     }
-    count = max(end - first, 0);
+    count = end > first ? end - first : 0;     // (their difference may not fit)
 }
 __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs& a, int n)
 {

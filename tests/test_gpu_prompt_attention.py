@@ -318,3 +318,18 @@ def test_more_sequences_than_are_held(kda, dtype, d):
     if dtype == BF16:   # a sequence's first token sees itself alone (fp32 values are kept to 22 bits)
         first = [a for a, n in zip(cu, lens) if n > 0]
         assert torch.equal(o[first].cpu(), parts[2][first].expand(-1, 2, -1))
+
+
+@pytest.mark.parametrize("dtype,simt", [(BF16, False), (F32, False), (F32, True)])
+def test_offsets_at_the_ends_of_their_type(kda, monkeypatch, dtype, simt):
+    # differences of offsets that do not fit 32 bits
+    if simt:
+        monkeypatch.setenv("KDA_FORCE_SIMT", "1")
+    low, high = -2 ** 31, 2 ** 31 - 1
+    for cu, cu_k in (([5, low, 30], None), ([0, 30, low], None), ([low, 20, high], None), ([high, low, high], None),
+                     ([0, 30, 50], [high, low, 64]), ([high, low, 40], [7, low, low])):
+        parts, _ = inputs(64, 64, 4, 2, 64, dtype, seed=20)
+        keep = torch.full((64, 4, 64), 3.0, dtype=dtype, device="cuda")
+        o = run(kda, parts, None, cu, cu_k, o=keep)
+        ref, mag = prompt_reference(*parts, cu, cu_k, o=torch.full((64, 4, 64), 3.0))
+        check(o, ref, mag, exact_p=dtype == F32)
