@@ -488,8 +488,10 @@ cache_rotary_kernel(const __grid_constant__ RotaryArgs a)
     if (tid < a.rot / 2) sh_turns[tid] = turns_of(__ldg(a.inv_freq + tid));
     __syncthreads();
     if (a.new_lengths) {
-        for (int n = blockIdx.x * kThreads + tid; n < a.N; n += gridDim.x * kThreads)
-            a.new_lengths[n] = __ldg(a.lengths + n) + max(min(cu[n + 1], a.T) - max(cu[n], 0), 0);
+        for (int n = blockIdx.x * kThreads + tid; n < a.N; n += gridDim.x * kThreads) {
+            const int first = max(cu[n], 0), end = min(cu[n + 1], a.T);
+            a.new_lengths[n] = __ldg(a.lengths + n) + (end > first ? end - first : 0);     // (their difference may not fit)
+        }
     }
     if (EIGHT && (int)blockIdx.x < a.unit_blocks)
         units_part<T, D>(a, cu, sh_turns, reinterpret_cast<float2*>(dyn), blockIdx.x, warp, lane);

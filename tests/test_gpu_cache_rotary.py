@@ -337,3 +337,15 @@ def test_heads_in_several_parts(kda, lens, Hkv):
     # more units than SMs and fewer, so that a window's heads go to one thread block or several
     c = Call(lens, [5] * len(lens), Hkv, Hkv, 64, 64, 32, BF16, seed=len(lens))
     c.check(*c.run(kda))
+
+
+@pytest.mark.parametrize("block", [0, 4])
+def test_offsets_at_the_ends_of_their_type(kda, block):
+    # differences of offsets that do not fit 32 bits
+    low, high = -2 ** 31, 2 ** 31 - 1
+    for cu in ([5, low, 8], [low, 3, high], [high, low, 8], [0, 8, low]):
+        c = Call([4, 4], [3, 1], 2, 1, 16, 8, block, F32, seed=21, cu=cu)
+        c.table = np.arange(6, dtype=np.int32).reshape(2, 3)
+        c.pools = [torch.cat([x] * 3)[:6] for x in c.pools]
+        c.scales = [x if x is None else torch.cat([x] * 3)[:6] for x in c.scales]
+        c.check(*c.run(kda))
