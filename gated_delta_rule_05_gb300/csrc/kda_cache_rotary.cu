@@ -488,7 +488,8 @@ cache_rotary_kernel(const __grid_constant__ RotaryArgs a)
     if (tid < a.rot / 2) sh_turns[tid] = turns_of(__ldg(a.inv_freq + tid));
     __syncthreads();
     if (a.new_lengths) {
-        for (int n = blockIdx.x * kThreads + tid; n < a.N; n += gridDim.x * kThreads) {
+        // (with millions of sequences of a token there are more threads than 2^31)
+        for (long long n = (long long)blockIdx.x * kThreads + tid; n < a.N; n += (long long)gridDim.x * kThreads) {
             const int first = max(cu[n], 0), end = min(cu[n + 1], a.T);
             a.new_lengths[n] = __ldg(a.lengths + n) + (end > first ? end - first : 0);     // (their difference may not fit)
         }

@@ -349,3 +349,19 @@ def test_offsets_at_the_ends_of_their_type(kda, block):
         c.pools = [torch.cat([x] * 3)[:6] for x in c.pools]
         c.scales = [x if x is None else torch.cat([x] * 3)[:6] for x in c.scales]
         c.check(*c.run(kda))
+
+
+def test_more_threads_than_31_bits(kda):
+    # a thread block per token of 2^23 sequences and some: 2^31 threads and more
+    N, page, d = (1 << 23) + 5, 8, 16
+    kc, vc = (torch.zeros((N, page, 1, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((N, 1, 1), device="cuda") for _ in range(2))
+    k = torch.randint(-8, 9, (N, 1, d), device="cuda").to(BF16)
+    steps = torch.arange(N + 1, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(N, dtype=torch.int32, device="cuda")
+    _, _, new = kda.kda_cache_append_rotary(None, k, -k, steps, torch.zeros(8, device="cuda"), kc.view(E4M3), vc.view(E4M3),
+                                            steps[:N, None], zero, k_scales=ks, v_scales=vs)
+    assert torch.all(new == 1)
+    # whole numbers up to 8 times a power of two are e4m3 values; frequencies of 0 turn nothing
+    for cache, s, x in ((kc, ks, k), (vc, vs, -k)):
+        assert torch.equal(cache[:, 0].view(E4M3).float() * s, x.float()) and not cache[:, 1:].any()
