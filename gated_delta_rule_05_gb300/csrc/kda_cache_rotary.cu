@@ -505,8 +505,10 @@ cudaError_t launch(const RotaryArgs& a, unsigned blocks, cudaStream_t stream)
 {
     auto kern = cache_rotary_kernel<T, D, EIGHT>;
     const size_t bytes = EIGHT ? (size_t)a.block * (a.rot / 2) * sizeof(float2) : 0;
-    if (bytes > 32 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    // (the same limit from every call, as another thread may set it between these two steps)
+    constexpr size_t most = (size_t)kMaxScaleBlock * (D / 2) * sizeof(float2);
+    if (EIGHT && most > 32 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
         if (e != cudaSuccess) return e;
     }
     kern<<<blocks, kThreads, bytes, stream>>>(a);

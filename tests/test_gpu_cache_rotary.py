@@ -365,3 +365,35 @@ def test_more_threads_than_31_bits(kda):
     # whole numbers up to 8 times a power of two are e4m3 values; frequencies of 0 turn nothing
     for cache, s, x in ((kc, ks, k), (vc, vs, -k)):
         assert torch.equal(cache[:, 0].view(E4M3).float() * s, x.float()) and not cache[:, 1:].any()
+
+
+def test_calls_from_two_threads(kda):
+    # blocks whose tables of angles differ in size, through one kernel, without the binding's time between the calls
+    import threading
+
+    lib, errors, threads, checks = kda.lib(), [], [], []
+    for block in (128, 72) * 2:
+        c = Call([block], [0], 0, 1, 128, block, block, BF16, seed=block)
+        c.run(kda)
+        want = [x.clone() for x in (c.kc.view(torch.uint8), c.vc.view(torch.uint8), c.ks, c.vs)]
+        held = [c.k.cuda(), c.v.cuda(), torch.tensor([0, block], dtype=torch.int32).cuda(), c.inv_freq.cuda(),
+                torch.from_numpy(c.table).cuda(), torch.from_numpy(c.past).cuda(), torch.cuda.Stream()]
+        k, v, cu, freq, table, past, stream = held
+        args = (None, k.data_ptr(), v.data_ptr(), 0, 128, 128, cu.data_ptr(), block, freq.data_ptr(), 128, 0, table.data_ptr(),
+                past.data_ptr(), 1, 0, 1, 128, c.kc.shape[0], block, table.shape[1], c.kc.stride(0), block, kda.KDA_BF16, None, 0,
+                None, 0, c.kc.data_ptr(), c.vc.data_ptr(), c.ks.data_ptr(), c.vs.data_ptr(), None, stream.cuda_stream)
+
+        def work(args=args, stream=stream):
+            errors.extend(filter(None, (lib.kda_cache_append_rotary(*args) for _ in range(20000))))
+            stream.synchronize()
+
+        checks.append((c, want, held))
+        threads.append(threading.Thread(target=work))
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for c, want, _ in checks:
+        assert all(torch.equal(x, y) for x, y in zip((c.kc.view(torch.uint8), c.vc.view(torch.uint8), c.ks, c.vs), want))
