@@ -77,8 +77,9 @@ constexpr int kMmaWarp = 16, kKvWarp = 17, kQWarp = 18;
 // 640 threads are launched with 96 registers: 512 x 104 + 128 x 64 = 640 x 96
 constexpr int kMore = 104, kFewer = 64;
 constexpr int kMaxTable = 256;             // sequences whose sizes are held in shared memory
-constexpr int kRingMeta = 16;              // tiles whose notes of infinities and NaN are kept
 constexpr int kItems = 4;                  // items that are known ahead
+constexpr int kEdges = 4;                  // an item's tiles on its edge: 256 rows begin within one and see up to 255
+                                           // keys more, 3 tiles
 constexpr int kItemReaders = 16 + 3;       // warps
 
 template <int D>
@@ -123,8 +124,10 @@ struct Shared {
     int per;                               // sequences of a table entry
     float top[2][2][2][128];               // of a row tile and half of a tile's keys, by row; by turns
     float sum[2][2][128];
-    int bad_tile;                          // one past the last tile with a note
-    alignas(16) uint32_t bad[kRingMeta][4];    // a tile's keys with inf or NaN in v
+    // Keys with an infinity or NaN in v, of the tiles on an item's edge; they live as long as the item
+    // (a row tile may look at them while the other is at the next items), and whether there are any.
+    alignas(16) uint32_t bad[kItems][kEdges][4];
+    int noted[kItems];
     int sums[kThreads / 32];
     int before[kMaxTable];                 // row tile pairs before a table entry
     int pairs[kMaxTable];                  // (these only where an entry is one sequence)
@@ -512,15 +515,15 @@ __device__ void scan_role(Shared& sh, const PromptArgs& a, uint32_t slots, int l
 {
     using Sh = Shape<D>;
     int entry = 0;                                 // ring entries before this item
-    int tile = 0;                                  // key tiles before this item
     uint32_t turn = 0;                             // of the landing barriers, bits by slot
     bool ok = true;
     Items items;
     for (const Item* at; (at = items.next(sh, a.status)); items.release(sh, lane)) {
         const Item it = *at;
-        const int cnt = it.tiles();
+        const int cnt = it.tiles(), from = it.all / KT, mine = items.n % kItems;
+        uint32_t some = 0;
 #pragma unroll 1
-        for (int j = it.all / KT; ok && j < cnt; ++j) {
+        for (int j = from; ok && j < cnt; ++j) {
             const int slot = (entry + 2 * j + 1) % Sh::kSlots;
             if (!(ok = wait(sh, &sh.kv_land[slot], (turn >> slot) & 1, a.status))) break;
             turn ^= 1u << slot;
@@ -554,15 +557,15 @@ __device__ void scan_role(Shared& sh, const PromptArgs& a, uint32_t slots, int l
                     }
                 }
                 const uint32_t bits = __ballot_sync(0xffffffffu, nan);
-                if (lane == 0) sh.bad[(tile + j) % kRingMeta][b] = bits;
-                if (lane == 0 && bits) sh.bad_tile = tile + j + 1;
+                some |= bits;
+                if (lane == 0) sh.bad[mine][j - from][b] = bits;
             }
+            if (lane == 0) sh.noted[mine] = some != 0;
             if (wrote) fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.kv_full[slot]);
         }
         entry = (entry + 2 * cnt) % Sh::kSlots;
-        tile += cnt;
     }
 }
 
@@ -717,17 +720,18 @@ __device__ void mma_role(Shared& sh, const PromptArgs& a, uint32_t q_smem, uint3
 // Adds to O the infinities and NaN of the keys before `lim` that the scanning warp has
 // taken out.
 template <int D>
-__device__ __forceinline__ void add_nonfinite(Shared& sh, const PromptArgs& a, const Item& it, int tile, int lim, int half, uint32_t to)
+__device__ __forceinline__ void add_nonfinite(Shared& sh, const PromptArgs& a, const Item& it, int mine, int lim, int half, uint32_t to)
 {
     constexpr int H = D / 2;
+    const int from = it.all / KT;
 #pragma unroll 1
     for (int c = 0; c < H / 16; ++c) {
         uint32_t y[16];
         tmem_ld16(to + 16 * c, y);
         tmem_ld_wait();
 #pragma unroll 1
-        for (int k = it.all / KT * KT; k < lim; ++k) {
-            if (!((sh.bad[(tile + k / KT) % kRingMeta][(k >> 5) & 3] >> (k & 31)) & 1)) continue;
+        for (int k = from * KT; k < lim; ++k) {
+            if (!((sh.bad[mine][k / KT - from][(k >> 5) & 3] >> (k & 31)) & 1)) continue;
             const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + (long long)(it.k0 + k) * a.v_stride + it.hk * D +
                                      half * H + 16 * c;
 #pragma unroll
@@ -789,7 +793,6 @@ __device__ void softmax_role(Shared& sh, const PromptArgs& a, const Plan& p, uin
     const int tok = r < p.rows ? r / a.G : 1 << 29, g = r < p.rows ? r - tok * a.G : 0;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     int done = 0;                                  // tiles before, of this row tile
-    int tile = 0;                                  // key tiles before
     Items items;
     for (const Item* at; (at = items.next(sh, a.status)); items.release(sh, lane)) {
         const Item& it = *at;                      // (in shared memory)
@@ -892,15 +895,15 @@ __device__ void softmax_role(Shared& sh, const PromptArgs& a, const Plan& p, uin
             // when some wait has given up, this item and those after it are not known
             if (*reinterpret_cast<volatile int*>(&sh.dead)) l = __int_as_float(0x7fffffff);
             scale_o = lim == 0 ? 0.f : __fdividef(1.f, l);
-            if (*reinterpret_cast<volatile int*>(&sh.bad_tile) > tile)
-                add_nonfinite<D>(sh, a, it, tile, min(lim, cnt * KT), half, to);
+            // (written before the last product began; of an item without an edge whatever was there, and no keys are looked at)
+            const int mine = items.n % kItems;
+            if (*reinterpret_cast<volatile int*>(&sh.noted[mine])) add_nonfinite<D>(sh, a, it, mine, min(lim, cnt * KT), half, to);
         }
         // this row's place, in 16-byte pieces from the item's first row; negative: none
         const int place = first + tok < past ? ((i * p.tok + tok) * a.Hq + g) * (D / 8) + half * (H / 8) : -1;
         uint4* base = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) +
                                                ((long long)(it.q0 + it.t0) * a.Hq + (long long)it.hk * a.G) * D);
         done += cnt;
-        tile += it.tiles();
         uint32_t z[H / 2];
 #pragma unroll
         for (int c = 0; c < H / 32; ++c) {
@@ -955,7 +958,7 @@ prompt_attention_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_co
             mbar_init(&sh.o_empty[i], 8);
         }
         sh.dead = 0;
-        sh.bad_tile = 0;
+        for (int i = 0; i < kItems; ++i) sh.noted[i] = 0;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {

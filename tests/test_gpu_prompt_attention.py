@@ -333,3 +333,34 @@ def test_offsets_at_the_ends_of_their_type(kda, monkeypatch, dtype, simt):
         o = run(kda, parts, None, cu, cu_k, o=keep)
         ref, mag = prompt_reference(*parts, cu, cu_k, o=torch.full((64, 4, 64), 3.0))
         check(o, ref, mag, exact_p=dtype == F32)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_noted_infinities_outlive_the_next_items(kda, d):
+    # long looks at infinities in items of two row tiles, and after those many items of a token, whose own infinities
+    # are found meanwhile
+    many, few, Lq, Lk = 60, 100, 256, 600
+    lens, keys = [Lq] * many + [1] * few, [Lk] * many + [560] * few
+    cu, cu_k = starts(lens), starts(keys)
+    g = torch.Generator().manual_seed(22)
+    f = lambda t: torch.randn((t, 4, d), generator=g).to(BF16)
+    q, k, v = f(cu[-1]), f(cu_k[-1]), f(cu_k[-1])
+    at = [Lk - 200 + 3 * i for i in range(66)]      # of the long ones' keys
+    one = d - 3                                     # and the channel
+    wild = v.clone()
+    for n in range(many):
+        wild[[cu_k[n] + x for x in at], :, one] = float("inf")
+        v[[cu_k[n] + x for x in at], :, one] = 0
+    for n in range(many, many + few):
+        wild[cu_k[n + 1] - 1, :, 0] = float("nan")
+        v[cu_k[n + 1] - 1, :, 0] = 0
+    o = run(kda, [q, k, wild], None, cu, cu_k)
+    ref, mag = prompt_reference(q, k, v, cu, cu_k)
+    long = o[:many * Lq].view(many, Lq, 4, d)
+    sees = torch.arange(Lq) + Lk - Lq >= at[0]
+    assert torch.isposinf(long[:, sees.cuda(), :, one]).all() and torch.isnan(o[many * Lq:, :, 0]).all()
+    long[:, sees.cuda(), :, one] = 0
+    o[many * Lq:, :, 0] = 0
+    ref[:many * Lq].reshape(many, Lq, 4, d)[:, sees.numpy(), :, one] = 0
+    ref[many * Lq:, :, 0] = 0
+    check(o, ref, mag, exact_p=False)
