@@ -107,6 +107,8 @@ kda_status_t kda_prompt_attention(const void* q, const void* k, const void* v, i
         return KDA_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < kda::kWsHeaderBytes || !aligned(workspace, 256)) return KDA_ERR_WORKSPACE;
     if (overlaps(workspace, kda::kWsHeaderBytes, o, o_bytes) ||
+        (cu_seqlens && overlaps(cu_seqlens, cu_bytes, workspace, kda::kWsHeaderBytes)) ||
+        (cu_seqlens_k && overlaps(cu_seqlens_k, cu_bytes, workspace, kda::kWsHeaderBytes)) ||
         meets(row_span(q, q_stride, qw, total_tokens, elem), workspace, kda::kWsHeaderBytes) ||
         meets(row_span(k, k_stride, kw, total_keys, elem), workspace, kda::kWsHeaderBytes) ||
         meets(row_span(v, v_stride, kw, total_keys, elem), workspace, kda::kWsHeaderBytes))

@@ -590,7 +590,8 @@ size_t kda_prompt_attention_workspace_bytes(int32_t num_seqs, int32_t Hq,
  *                 hold; must not overlap the inputs.  Rows before 0 or past the last
  *                 do not exist; of sequences that claim the same row one gets it.
  *   workspace     kda_prompt_attention_workspace_bytes(...) bytes, 256-byte aligned,
- *                 not shared with concurrent calls; contents on entry do not matter.
+ *                 over none of the above, not shared with concurrent calls; contents on
+ *                 entry do not matter.
  *                 Bit 1 of the int32 at byte 8 is set when a wait of the tcgen05
  *                 kernel has given up (after some two seconds), which no call
  *                 clears; the rows of o that depended on it are NaN.

@@ -41,6 +41,12 @@ def test_prompt_attention_rejects(lib, kw, code):
     assert prompt(lib, **kw) == code
 
 
+@pytest.mark.parametrize("kw", [
+    dict(cu=A * 256), dict(cu=A * 256 + 252), dict(cu=A * 256 - 8), dict(cuk=A * 256 + 64), dict(cuk=A * 256 - 4)])
+def test_prompt_attention_rejects_a_workspace_over_its_offsets(lib, kw):
+    assert prompt(lib, **kw) == BAD
+
+
 def test_prompt_attention_workspace(lib):
     size = kda.kda_prompt_attention_workspace_bytes
     for bad in ((0, 8, 2, 64, BF16), (2, 7, 2, 64, BF16), (2, 8, 2, 48, BF16), (2, 8, 2, 64, 5), (1, 1 << 17, 1 << 17, 16, BF16)):
