@@ -836,7 +836,7 @@ def kda_prompt_attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=N
             and v.dtype is dtype and dk == d and v.shape == shape
             and q_stride >= 0 and k_stride >= 0 and v_stride >= 0
             and (cu_seqlens is None or (cu_seqlens.get_device() == at and cu_seqlens.dtype is i32
-                                        and cu_seqlens.is_contiguous()))
+                                        and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous()))
             and (Tk == T if cu_seqlens_k is None else
                  cu_seqlens is not None and cu_seqlens_k.shape == cu_seqlens.shape
                  and cu_seqlens_k.get_device() == at and cu_seqlens_k.dtype is i32
@@ -845,6 +845,8 @@ def kda_prompt_attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, scale=N
             _check_rows(name, t, dtype, dev)
         _check_on("cu_seqlens", cu_seqlens, torch.int32, dev)
         _check_on("cu_seqlens_k", cu_seqlens_k, torch.int32, dev)
+        if cu_seqlens is not None:
+            _shape("cu_seqlens", cu_seqlens, (N + 1,))
         _shape("k", k, (Tk, Hkv, d))
         _shape("v", v, (Tk, Hkv, d))
         if cu_seqlens_k is None:

@@ -364,3 +364,13 @@ def test_noted_infinities_outlive_the_next_items(kda, d):
     ref[:many * Lq].reshape(many, Lq, 4, d)[:, sees.numpy(), :, one] = 0
     ref[many * Lq:, :, 0] = 0
     check(o, ref, mag, exact_p=False)
+
+
+def test_offsets_of_more_than_one_dimension_are_refused(kda):
+    (q, k, v), _ = inputs(30, 30, 4, 2, 64, BF16, seed=23)
+    a = on_gpu([q, k, v], None)
+    for cu, cu_k in ((i32([[0, 10], [20, 30]]), None), (i32([[0], [30]]), None), (i32([[0, 30]]), i32([[0, 30]]))):
+        with pytest.raises(ValueError, match="cu_seqlens"):
+            kda.kda_prompt_attention(*a, cu, cu_k)
+    with pytest.raises(ValueError, match="cu_seqlens_k"):
+        kda.kda_prompt_attention(*a, i32([0, 30]), i32([[0, 30]]))
