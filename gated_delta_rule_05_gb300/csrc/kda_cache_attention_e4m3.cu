@@ -24,9 +24,9 @@
 //
 // The work is cut into equal ranges as for the tree attention (kda_tree.cuh).
 #include <cudaTypedefs.h>
-#include <cuda_fp16.h>
 #include <stdio.h>
 
+#include "kda_f16_parts.cuh"
 #include "kda_prompt.cuh"
 #include "kda_sm100.cuh"
 
@@ -43,6 +43,7 @@ using sm100::mbar_arrive;
 using sm100::mbar_arrive_expect_tx;
 using sm100::mbar_init;
 using sm100::mbar_try_wait;
+using namespace f16_parts;
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kKeys = 16;                          // of a warp's step
@@ -62,41 +63,15 @@ struct Shape {
     static constexpr size_t kBytes = kRing + kJoin;
 };
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float lg2(float x)
 {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// The same onto nothing.
-__device__ __forceinline__ void mma0(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%10, %10, %10, %10};"
-                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Two e4m3 (the lower or the upper half of a word) as fp16, which holds them exactly.
 __device__ __forceinline__ uint32_t widen_lo(uint32_t w)
@@ -111,24 +86,6 @@ __device__ __forceinline__ uint32_t widen_hi(uint32_t w)
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
     return r;
 }
-__device__ __forceinline__ uint32_t two_f16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// What two_f16 leaves of the pair, as fp16.
-__device__ __forceinline__ uint32_t two_f16_rest(float lo, float hi, uint32_t taken)
-{
-    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&taken));
-    return two_f16(lo - t.x, hi - t.y);
-}
-__device__ __forceinline__ float quad_max(float x)
-{
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-}
-
 template <int BYTES>
 struct Words {
     uint32_t w[(BYTES + 3) / 4];
@@ -313,13 +270,12 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
+                for (int j = 0; j < 4; ++j) top = top_of(top, x[s][j]);
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            int e = 14 + 127 - (int)(top >> 23);   // the largest magnitude becomes 2^14 or a little more
-            e = top == 0 ? 0 : min(max(e, -100), 100);
-            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-            rs[h] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+            const int e = up_of(top);
+            const float up = power(e);
+            rs[h] = a.scale_log2 * power(-e);
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -807,13 +763,12 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
+                for (int j = 0; j < 4; ++j) top = top_of(top, x[s][j]);
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            int e = 14 + 127 - (int)(top >> 23);   // the largest magnitude becomes 2^14 or a little more
-            e = top == 0 ? 0 : min(max(e, -100), 100);
-            float up = __uint_as_float((uint32_t)(127 + e) << 23);
-            rs[h] = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - e) << 23);
+            const int e = up_of(top);
+            float up = power(e);
+            rs[h] = fabsf(a.scale_log2) * power(-e);
             if (a.scale_log2 < 0.f) up = -up;
             if (a.scale_log2 == 0.f) up = 0.f, rs[h] = 1.f;
 #pragma unroll

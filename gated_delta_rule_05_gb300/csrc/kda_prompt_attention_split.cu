@@ -33,12 +33,13 @@
 // is 65 TFLOP/s where the three products would allow 190.  7 prompts of up to 1,500, 12 heads on
 // 4, d = 64: 125 us (353).  bf16, d = 128, one prompt of 8,192 tokens, 32 heads on 8: 2.8 ms, 195
 // TFLOP/s (tcgen05 0.36, CUDA cores 12.4).
-#include <cuda_fp16.h>
-
+#include "kda_f16_parts.cuh"
 #include "kda_prompt.cuh"
 
 namespace kda {
 namespace {
+
+using namespace f16_parts;
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int BM = kWarps * 16, BN = 32;
@@ -57,32 +58,6 @@ struct Shape {
     static constexpr size_t kBytes = kQ + 2 * kTile + 2 * kRaw;
 };
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// The same onto nothing.
-__device__ __forceinline__ void mma0(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%10, %10, %10, %10};"
-                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
 __device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t at)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
@@ -91,18 +66,6 @@ __device__ __forceinline__ void ldmatrix_t(uint32_t (&r)[4], uint32_t at)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
 }
-__device__ __forceinline__ uint32_t two_f16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float quad_max(float x)
-{
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-}
-
 // Byte offset of 16-byte piece c of row r of a tile of fp16 rows of D.
 template <int D>
 __device__ __forceinline__ int row_at(int r, int c)
@@ -111,12 +74,7 @@ __device__ __forceinline__ int row_at(int r, int c)
     return r * (D * 2) + ((c ^ ((r / S) & M)) << 4);
 }
 
-// Bits of the largest magnitude.
-__device__ __forceinline__ uint32_t top_of(uint32_t top, float x) { return max(top, __float_as_uint(x) & 0x7FFFFFFFu); }
 constexpr uint32_t kInfinity = 0x7F800000u;
-// The power of two that brings that magnitude to 2^14 or a little more.
-__device__ __forceinline__ int up_of(uint32_t top) { return top == 0 ? 0 : min(max(14 + 127 - (int)(top >> 23), -100), 100); }
-__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // One 16-byte piece of a row, widened.
 template <class T>
