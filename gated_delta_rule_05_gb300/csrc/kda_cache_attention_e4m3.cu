@@ -395,7 +395,7 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
                         const float x = c[b][2 * h + j];
                         const float p = ex2(x - ref);
                         l[h] += p;
-                        y[j] = p * (vs[b][j] * fac[h]);
+                        y[j] = p * weight_factor(vs[b][j], fac[h]);
                         if (masked && x == -INFINITY) y[j] = 0.f;
                     }
                     ph[2 * b + h] = two_f16(y[0], y[1]);
@@ -928,7 +928,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                 for (int i = 0; i < kStepGroups; ++i) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const float w1 = vsn[i][b % S] * fac[h];
+                        const float w1 = weight_factor(vsn[i][b % S], fac[h]);
                         float y[2];
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {

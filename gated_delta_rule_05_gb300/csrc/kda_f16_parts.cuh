@@ -58,5 +58,15 @@ __device__ __forceinline__ uint32_t top_of(uint32_t top, float x) { return max(t
 __device__ __forceinline__ int up_of(uint32_t top) { return top == 0 ? 0 : min(max(14 + 127 - (int)(top >> 23), -100), 100); }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
+// What a value's probability is multiplied by to become its weight: the value's factor times 2^(m - n),
+// but finite, so that a probability of 0 (of a hidden key, or of one far below the maximum) gives a
+// weight of 0.  Where this cuts off, the probability is 2^-112 at most.  NaN stays NaN.
+__device__ __forceinline__ float weight_factor(float down, float fac)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(down * fac), "f"(1.7014118e38f));
+    return r;
+}
+
 }  // namespace f16_parts
 }  // namespace kda

@@ -464,7 +464,7 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
                 for (int e = 0; e < 2; ++e) {
                     const float p = ex2(fmaf(c[b][2 * h + e], rs[h], -ref));
                     l[h] += p;
-                    y[e] = p * (vd[b][e] * fac[h]);
+                    y[e] = p * weight_factor(vd[b][e], fac[h]);
                 }
                 const uint32_t z = two_f16(y[0], y[1]);
                 ph[b >> 1][2 * (b & 1) + h] = z;

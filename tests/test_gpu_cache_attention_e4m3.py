@@ -357,3 +357,22 @@ def test_sequences_share_pages(kda):
     c.table[:, 1] = c.table[:, 0]
     ref, mag = c.reference()
     check(kda.kda_cache_attention_e4m3(**args), ref.repeat(n, 0), mag.repeat(n, 0), exact_p=False)
+
+
+@pytest.mark.parametrize("page,block", [(32, 16), (8, 8), (7, 7)])
+@pytest.mark.parametrize("dtype,out", [(F32, F32), (BF16, F32), (BF16, BF16)])
+def test_values_far_above_those_of_the_keys_that_count(kda, page, block, dtype, out):
+    # rows of probability 0 with values of 2^75 beside ones of 2^-75 that have all of it
+    n = 3 * 32 * 7
+    c = Call(1, 1, 4, 2, 64, page, block, [n], dtype, seed=31)
+    last = c.table[0, -1]
+    c.q[:] = 8.0
+    c.k.view(torch.uint8)[:] = 0
+    c.ks[:] = 1.0
+    c.k[last, :] = 2.0                              # scores of 64 * 8 * 2 / 8 = 128
+    low = c.vs[last] * 2.0 ** -75
+    c.vs *= 2.0 ** 75
+    c.vs[last] = low
+    ref, mag = c.reference()
+    assert 0 < np.abs(ref).max() < 2.0 ** -70
+    check(c.run(kda, o_dtype=out), ref, mag, exact_p=out == F32)

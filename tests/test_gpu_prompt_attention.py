@@ -374,3 +374,22 @@ def test_offsets_of_more_than_one_dimension_are_refused(kda):
             kda.kda_prompt_attention(*a, cu, cu_k)
     with pytest.raises(ValueError, match="cu_seqlens_k"):
         kda.kda_prompt_attention(*a, i32([0, 30]), i32([[0, 30]]))
+
+
+@pytest.mark.parametrize("dtype,out,d", [(F32, F32, 64), (BF16, F32, 128), (BF16, BF16, 32)])
+def test_values_far_above_those_of_the_keys_that_count(kda, dtype, out, d):
+    # keys that a row does not see, or sees with a probability of 0, have values of 2^60 and more beside ones of 2^-60
+    T = 100
+    q, k, v = inputs(T, T, 2, 1, d, dtype, seed=26)[0]
+    q, k = torch.full_like(q, d ** 0.5), 0.25 * k
+    k[80:] += 128 / d                               # scores some 128 above the others'
+    big = torch.zeros(T, 1, 1, dtype=torch.bool)
+    big[1:80:2] = True                              # hidden from the rows before, and of probability 0 for the last ones
+    v = torch.where(big, v * 2.0 ** 75, v * 2.0 ** -75)
+    o = run(kda, (q, k, v), None, None, None, o_dtype=out)
+    ref, mag = prompt_reference(q, k, v)
+    assert np.abs(ref[80:]).max() < 2.0 ** -70 and np.abs(ref[2:80]).min() > 2.0 ** 50
+    check(o[:80], ref[:80], mag[:80], exact_p=out == F32)
+    # scores of 128 from d products: 22 bits of each and 8 sums cut off at 2^-23, 128 (2^-22 + 8 2^-23) = 1.5e-4, for
+    # two keys that are compared
+    check(o[80:], ref[80:], 3 * mag[80:], exact_p=out == F32)
