@@ -5,12 +5,13 @@
 //     S = Q K^T, s = c ks S (c = scale log2 e, ks the key's scale)
 //     P = 2^(s - m), w = P vs 2^(m - n) (vs the value's scale), O += w V
 // on mma.sync m16n8k16 with K and V widened to fp16 in registers, which holds e4m3
-// exactly.  m and n are references near the running maxima of s and of s + log2 vs
-// of each row: P and w stay below 2^8, in fp16's range whatever the scales are; O
+// exactly.  m is a reference near the running maximum of s of each row, n one 2^7 below that of s + log2
+// vs: P stays below 2^8 and w below 2^15, in fp16's range whatever the scales are, and w's largest is 2^7
+// at least, so that the weights of many keys far below one keep their bits (kda_f16_parts.cuh); O
 // is in units of 2^n, the sum l of P in units of 2^m.  They move only when a score
 // exceeds them by more than 8, so that a step without that has no reduction over lanes.
 // q is brought into fp16's range by a power of two per row, which is exact.  With
-// fp32 queries or output, q and w are a sum of two fp16 each (22 bits), and as the tensor
+// fp32 queries or output, q and w are a sum of two fp16 each (22 bits, hi + 2^-11 lo), and as the tensor
 // cores cut off what does not fit as they add up (1e-5 of the result over 32,000 keys), the small
 // products and each group's output have sums of their own.
 //
@@ -50,7 +51,6 @@ constexpr int kKeys = 16;                          // of a warp's step
 constexpr int KT = kWarps * kKeys;                 // of a tile
 constexpr int kLead = 4;
 constexpr int kRows = 16;
-constexpr float kSlack = 8.f;
 using Piece = TreePieces<KT, kLead>;
 
 template <int D>
@@ -357,20 +357,20 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         float& x = c[b][2 * h + j];
-                        x = (QLO ? x + small[b][2 * h + j] : x) * ks[b][j] * rs[h];
+                        x = (QLO ? fmaf(small[b][2 * h + j], kRest, x) : x) * ks[b][j] * rs[h];
                         const int key = 8 * b + i4 + 4 * j;
                         if (masked && (!((mask >> key) & 1) || pos + key >= lim[h])) x = -INFINITY;
                         top[h] = fmaxf(top[h], x);
                         vtop[h] = fmaxf(vtop[h], x + lv[b][j]);
                     }
-                grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + kSlack;
+                grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + (kSlack + kHead);
             }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float m2 = fmaxf(m[h], quad_max(top[h]));
                     // n is kept near m, so that 2^(m - n) is finite
-                    const float n2 = fmaxf(fmaxf(n[h], quad_max(vtop[h])), m2 - 120.f);
+                    const float n2 = fmaxf(fmaxf(n[h], quad_max(vtop[h]) - kHead), m2 - 120.f);
                     const float fl = m2 == -INFINITY ? 1.f : ex2(m[h] - m2), fo = n2 == -INFINITY ? 1.f : ex2(n[h] - n2);
                     m[h] = m2;
                     n[h] = n2;
@@ -387,6 +387,7 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float ref = m[h] == -INFINITY ? 0.f : m[h];
+                float sum = 0.f;                   // (few additions to l, which small probabilities would be lost in)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     float y[2];
@@ -394,13 +395,14 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
                     for (int j = 0; j < 2; ++j) {
                         const float x = c[b][2 * h + j];
                         const float p = ex2(x - ref);
-                        l[h] += p;
+                        sum += p;
                         y[j] = p * weight_factor(vs[b][j], fac[h]);
                         if (masked && x == -INFINITY) y[j] = 0.f;
                     }
                     ph[2 * b + h] = two_f16(y[0], y[1]);
                     if constexpr (PLO) pl[2 * b + h] = two_f16_rest(y[0], y[1], ph[2 * b + h]);
                 }
+                l[h] += sum;
             }
             {
                 // this lane's D / 8 channels of keys i4, i4 + 4, 8 + i4, 12 + i4
@@ -419,11 +421,11 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
 #pragma unroll
                     for (int j = 0; j < (NT < 4 ? NT : 4); ++j) {
                         if constexpr (PLO) {
-                            float z[4];
-                            mma0(z, pl, b0[j], b1[j]);
-                            mma(z, ph, b0[j], b1[j]);
+                            float z[4], rest[4];
+                            mma0(rest, pl, b0[j], b1[j]);
+                            mma0(z, ph, b0[j], b1[j]);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) o[4 * x + j][e] += z[e];
+                            for (int e = 0; e < 4; ++e) o[4 * x + j][e] = fmaf(rest[e], kRest, o[4 * x + j][e] + z[e]);
                         } else {
                             mma(o[4 * x + j], ph, b0[j], b1[j]);
                         }
@@ -856,7 +858,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
 #pragma unroll
                         for (int b = 0; b < 2; ++b)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) c[i][b][j] += small[i][b][j];
+                            for (int j = 0; j < 4; ++j) c[i][b][j] = fmaf(small[i][b][j], kRest, c[i][b][j]);
                 }
             }
             float k1[kStepGroups][S][2], top[2], vtop[2];
@@ -900,14 +902,14 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                         vtop[h] = fmaxf(vtop[h], x + lg2(vsn[i][b]));
                     }
                 }
-                grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + kSlack;
+                grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + (kSlack + kHead);
             }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float m2 = fmaxf(m[h], quad_max(top[h]));
                     // n is kept near m, so that 2^(m - n) is finite
-                    const float n2 = fmaxf(fmaxf(n[h], quad_max(vtop[h])), m2 - 120.f);
+                    const float n2 = fmaxf(fmaxf(n[h], quad_max(vtop[h]) - kHead), m2 - 120.f);
                     const float fl = m2 == -INFINITY ? 1.f : ex2(m[h] - m2), fo = n2 == -INFINITY ? 1.f : ex2(n[h] - n2);
                     m[h] = m2;
                     n[h] = n2;
@@ -924,6 +926,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float ref = m[h] == -INFINITY ? 0.f : m[h];
+                float sum = 0.f;                   // (few additions to l, which small probabilities would be lost in)
 #pragma unroll
                 for (int i = 0; i < kStepGroups; ++i) {
 #pragma unroll
@@ -934,7 +937,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                         for (int j = 0; j < 2; ++j) {
                             const float x = c[i][b][2 * h + j];
                             const float p = ex2(fmaf(x, k1[i][b % S][h], -ref));
-                            l[h] += p;
+                            sum += p;
                             y[j] = p * w1;
                             if (masked && x == -INFINITY) y[j] = 0.f;
                         }
@@ -942,6 +945,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                         if constexpr (PLO) pl[i][2 * b + h] = two_f16_rest(y[0], y[1], ph[i][2 * b + h]);
                     }
                 }
+                l[h] += sum;
             }
 #pragma unroll
             for (int i = 0; i < kStepGroups; ++i) {
@@ -961,11 +965,11 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
 #pragma unroll
                     for (int j = 0; j < (NT < 4 ? NT : 4); ++j) {
                         if constexpr (PLO) {
-                            float z[4];
-                            mma0(z, pl[i], b0[j], b1[j]);
-                            mma(z, ph[i], b0[j], b1[j]);
+                            float z[4], rest[4];
+                            mma0(rest, pl[i], b0[j], b1[j]);
+                            mma0(z, ph[i], b0[j], b1[j]);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) o[4 * x + j][e] += z[e];
+                            for (int e = 0; e < 4; ++e) o[4 * x + j][e] = fmaf(rest[e], kRest, o[4 * x + j][e] + z[e]);
                         } else {
                             mma(o[4 * x + j], ph[i], b0[j], b1[j]);
                         }

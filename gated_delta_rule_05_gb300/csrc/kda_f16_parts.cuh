@@ -40,12 +40,21 @@ __device__ __forceinline__ uint32_t two_f16(float lo, float hi)
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// What two_f16 leaves of the pair, as fp16.
+// What two_f16 leaves of the pair, times 2^11, as fp16: next to its first part, the second has all
+// of its bits then wherever the first is a normal number, and reaches down to 2^-36 below that.
+// Products with it have sums of their own, which count 2^-11 (kRest).
+constexpr float kRest = 1.f / 2048.f;
 __device__ __forceinline__ uint32_t two_f16_rest(float lo, float hi, uint32_t taken)
 {
     const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&taken));
-    return two_f16(lo - t.x, hi - t.y);
+    return two_f16((lo - t.x) * 2048.f, (hi - t.y) * 2048.f);
 }
+// The references of a softmax: m near the maximum of a row's scores moves when one exceeds it by more
+// than kSlack; n lies kHead below the one of the scores with their values' factors, so that a row's
+// largest weight is 2^7 to 2^15 in fp16, whose normal numbers reach down to 2^-14: a weight has its 11
+// bits down to 2^-21 of the largest, and is off by 2^-32 of that at most below.
+constexpr float kSlack = 8.f, kHead = 7.f;
+
 __device__ __forceinline__ float quad_max(float x)
 {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));

@@ -2,15 +2,16 @@
 // tcgen05 kernel does not take (fp32 in or out, d = 16 and 32, scales that are not positive, more
 // than 128 heads to a key head): products of fp16 pairs, summed up in fp32.
 //
-// fp32 keeps its accuracy as a sum of two fp16, x = hi + lo (22 bits), in three products
-// hi hi + lo hi + hi lo; bf16 is exact in one, and a bf16 output takes P in one.  fp16's
+// fp32 keeps its accuracy as a sum of two fp16, x = hi + 2^-11 lo (22 bits), in three products
+// hi hi + 2^-11 (lo hi + hi lo); bf16 is exact in one, and a bf16 output takes P in one.  fp16's
 // range is met by powers of two, which are exact: one per query row, one per row of
 // keys and one per row of values, from its largest finite magnitude.  With the factors
 // a of the query, b of the key and c of the value
 //     s = scale log2 e a b (Q K^T),  P = 2^(s - m),  w = P c 2^(m - n),  O += w V,
-// m and n references near the running maxima of s and of s + log2 c of a row: P and w
-// stay below 2^8 whatever the values are.  O is in units of 2^n, the sum l of P in
-// units of 2^m.  They move only when a score exceeds them by more than 8.
+// m a reference near the running maximum of s of a row, n one 2^7 below that of s + log2 c: P stays
+// below 2^8 and w below 2^15 whatever the values are, and w's largest is 2^7 at least, so that
+// the weights of many keys far below one keep their bits (kda_f16_parts.cuh).  O is in units of 2^n, the
+// sum l of P in units of 2^m.  They move only when a score exceeds them by more than 8.
 //
 // A thread block has 128 query rows of a (sequence, cache head), token by token (row r
 // is head r % G of token r / G), 16 to a warp, and goes through 32 keys at a time: while
@@ -44,7 +45,6 @@ using namespace f16_parts;
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int BM = kWarps * 16, BN = 32;
 constexpr int kNotes = 8;                          // tiles with rows that some query does not see, at most 6
-constexpr float kSlack = 8.f;
 
 template <class T, class O, int D>
 struct Shape {
@@ -111,11 +111,10 @@ __device__ __forceinline__ void store_parts(uint32_t tile, int part, int r, int 
         const float x = p.x[2 * i] * up, y = p.x[2 * i + 1] * up;
         h[i] = two_f16(x, y);
         if (LO) {
-            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-            l[i] = two_f16(x - t.x, y - t.y);
+            l[i] = two_f16_rest(x, y, h[i]);
             if (odd) {                             // (an infinity or NaN has no second part)
-                if (!(fabsf(x - t.x) < INFINITY)) l[i] &= 0xFFFF0000u;
-                if (!(fabsf(y - t.y) < INFINITY)) l[i] &= 0x0000FFFFu;
+                if (!(fabsf(x) < INFINITY)) l[i] &= 0xFFFF0000u;
+                if (!(fabsf(y) < INFINITY)) l[i] &= 0x0000FFFFu;
             }
         }
     }
@@ -312,8 +311,10 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
                 if (x == 0) {
                     sh.k_down[j & 1][tr] = power(-e);
                 } else {
-                    sh.v_down[j & 1][tr] = power(-e);
-                    sh.v_log[j & 1][tr] = (float)-e;
+                    // (a row of zeros has no weight and does not move the reference of the others')
+                    const bool none = top == 0 && !odd;
+                    sh.v_down[j & 1][tr] = none ? 0.f : power(-e);
+                    sh.v_log[j & 1][tr] = none ? -INFINITY : (float)-e;
                 }
             }
         }
@@ -424,7 +425,7 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float& x = c[b][2 * h + e];
-                    x = (Sh::kLo ? x + small[b][2 * h + e] : x) * (e ? kd.y : kd.x);      // (to be multiplied by rs)
+                    x = (Sh::kLo ? fmaf(small[b][2 * h + e], kRest, x) : x) * (e ? kd.y : kd.x);      // (to be multiplied by rs)
                     if (masked && j * BN + 8 * b + 2 * i4 + e >= lim[h]) x = -INFINITY;
                     top[h] = fmaxf(top[h], x);
                     vtop[h] = fmaxf(vtop[h], fmaf(x, rs[h], e ? lv.y : lv.x));
@@ -433,14 +434,14 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             top[h] *= rs[h];
-            grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + kSlack;
+            grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + (kSlack + kHead);
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float m2 = fmaxf(m[h], quad_max(top[h]));
                 // n is kept near m, so that 2^(m - n) is finite
-                const float n2 = fmaxf(fmaxf(n[h], quad_max(vtop[h])), m2 - 120.f);
+                const float n2 = fmaxf(fmaxf(n[h], quad_max(vtop[h]) - kHead), m2 - 120.f);
                 const float fl = m2 == -INFINITY ? 1.f : ex2(m[h] - m2), fo = n2 == -INFINITY ? 1.f : ex2(n[h] - n2);
                 m[h] = m2;
                 n[h] = n2;
@@ -457,46 +458,44 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const float ref = m[h] == -INFINITY ? 0.f : m[h];
+            float sum = 0.f;                       // (few additions to l, which small probabilities would be lost in)
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 float y[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float p = ex2(fmaf(c[b][2 * h + e], rs[h], -ref));
-                    l[h] += p;
+                    sum += p;
                     y[e] = p * weight_factor(vd[b][e], fac[h]);
                 }
                 const uint32_t z = two_f16(y[0], y[1]);
                 ph[b >> 1][2 * (b & 1) + h] = z;
-                if (Sh::kPLo) {
-                    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&z));
-                    pl[b >> 1][2 * (b & 1) + h] = two_f16(y[0] - t.x, y[1] - t.y);
-                }
+                if (Sh::kPLo) pl[b >> 1][2 * (b & 1) + h] = two_f16_rest(y[0], y[1], z);
             }
+            l[h] += sum;
         }
 #pragma unroll
         for (int x = 0; x < NT; x += 2) {
-            float z[2][4];
             uint32_t vh[2][4], vl[2][4];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 ldmatrix_t(vh[k], vt + row_at<D>(k * 16 + mr, x + mc));
                 if (Sh::kLo) ldmatrix_t(vl[k], vt + Sh::kHalf + row_at<D>(k * 16 + mr, x + mc));
             }
-            // the small products first, so that few sums are cut off at the large ones' size
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 if constexpr (Sh::kPLo) {
-                    mma0(z[y], pl[0], vh[0][2 * y], vh[0][2 * y + 1]);
-                    mma(z[y], pl[1], vh[1][2 * y], vh[1][2 * y + 1]);
+                    float z[4], rest[4];
+                    mma0(rest, pl[0], vh[0][2 * y], vh[0][2 * y + 1]);
+                    mma(rest, pl[1], vh[1][2 * y], vh[1][2 * y + 1]);
                     if (Sh::kLo) {
-                        mma(z[y], ph[0], vl[0][2 * y], vl[0][2 * y + 1]);
-                        mma(z[y], ph[1], vl[1][2 * y], vl[1][2 * y + 1]);
+                        mma(rest, ph[0], vl[0][2 * y], vl[0][2 * y + 1]);
+                        mma(rest, ph[1], vl[1][2 * y], vl[1][2 * y + 1]);
                     }
-                    mma(z[y], ph[0], vh[0][2 * y], vh[0][2 * y + 1]);
-                    mma(z[y], ph[1], vh[1][2 * y], vh[1][2 * y + 1]);
+                    mma0(z, ph[0], vh[0][2 * y], vh[0][2 * y + 1]);
+                    mma(z, ph[1], vh[1][2 * y], vh[1][2 * y + 1]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[x + y][e] += z[y][e];
+                    for (int e = 0; e < 4; ++e) o[x + y][e] = fmaf(rest[e], kRest, o[x + y][e] + z[e]);
                 } else {
                     mma(o[x + y], ph[0], vh[0][2 * y], vh[0][2 * y + 1]);
                     mma(o[x + y], ph[1], vh[1][2 * y], vh[1][2 * y + 1]);

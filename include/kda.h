@@ -598,11 +598,14 @@ size_t kda_prompt_attention_workspace_bytes(int32_t num_seqs, int32_t Hq,
  * dtype is that of q, k, v, and of o.  KDA_BF16 with d = 64 or 128, scale > 0,
  * Hq / Hkv <= 128, Hq <= 2^16 and total_tokens, total_keys <= 2^27 runs on tcgen05,
  * with probabilities rounded to bf16 for the second product; everything else in
- * products of fp16 pairs: bf16 inputs exactly, fp32 ones to 22 bits, probabilities to 11
- * bits for a bf16 output and to 22 for an fp32 one; sums are fp32.  When the
- * environment variable KDA_FORCE_SIMT is set everything runs on the CUDA cores in
- * fp32.  An infinity or NaN in a row of k or v reaches the queries that see it and no
- * others.  The result does not depend on timing. */
+ * products of fp16 pairs.  Of a row of q, k or v these hold bf16 values exactly down to
+ * 2^-31 of the row's largest, and 22 bits of fp32 ones down to 2^-28; of the
+ * probabilities (each times its value row's magnitude) 11 bits for a bf16 output and 22
+ * for an fp32 one, down to 2^-20 of a query's largest, and smaller ones to 2^-32 and
+ * 2^-43 of that.  Sums are fp32.  When the environment variable KDA_FORCE_SIMT is set
+ * everything runs on the CUDA cores in fp32.  An infinity or NaN in a row of k or v
+ * reaches the queries that see it and no others.  The result does not depend on
+ * timing. */
 kda_status_t kda_prompt_attention(const void *q, const void *k, const void *v,
                                   int64_t q_stride, int64_t k_stride,
                                   int64_t v_stride, const int32_t *cu_seqlens,
@@ -677,8 +680,11 @@ size_t kda_cache_attention_e4m3_workspace_bytes(int32_t N, int32_t Ts,
  *                 not matter.  Bit 1 of the int32 at byte 8 is set when a wait of the
  *                 kernel has given up (after some two seconds), which no call clears;
  *                 the rows of o that depended on it are NaN.
- * dtype is that of q and of o.  Products are of fp16 pairs (q exactly, probabilities
- * to 11 bits), with fp32 queries or output of sums of two (22 bits); sums are fp32.
+ * dtype is that of q and of o.  Products are of fp16 pairs: of q's head they hold bf16
+ * values exactly down to 2^-31 of its largest, and 22 bits of fp32 ones down to 2^-28; of
+ * the probabilities (each times its value's scale) 11 bits for a bf16 output and 22 for
+ * an fp32 one, down to 2^-20 of a token's largest, and smaller ones to 2^-32 and 2^-43 of
+ * that.  Sums are fp32.
  * A scale of NaN makes the tokens that see a row of its block NaN and no others;
  * an e4m3 code of NaN, which kda_cache_append_rotary never writes, may reach all
  * tokens of its sequence; an infinity or NaN in q makes that head's output NaN.  No

@@ -376,3 +376,39 @@ def test_values_far_above_those_of_the_keys_that_count(kda, page, block, dtype, 
     ref, mag = c.reference()
     assert 0 < np.abs(ref).max() < 2.0 ** -70
     check(c.run(kda, o_dtype=out), ref, mag, exact_p=out == F32)
+
+
+@pytest.mark.parametrize("page,block", [(64, 16), (56, 8), (56, 7)])
+@pytest.mark.parametrize("dtype,out", [(F32, F32), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("gap", [10, 12, 14, 16, 18])
+@pytest.mark.parametrize("first", [True, False])
+def test_one_row_far_above_many_others(kda, page, block, dtype, out, gap, first):
+    # an attention sink: one row's score lies `gap` above those of 2^15 others, which are all the same, so that
+    # errors of their weights add up.  Values of 1 throughout, which the output has to be; then a sink
+    # without a value, where the others are all of the output.  64 sequences, so that one walk has many rows.
+    n, N, d = 1 << 15, 64, 32
+    pages = -(-n // page)
+    at = (0, 0) if first else ((n - 1) // page, (n - 1) % page)
+    one = torch.ones((pages, page, 1, d)).to(E4M3)
+    k = torch.zeros((pages, page, 1, d)).to(E4M3)
+    k[at] = one[at]
+    ks, vs = (torch.ones((pages, page // block, 1)) for _ in range(2))
+    ks[at[0], at[1] // block] = gap / d ** 0.5
+    table = torch.arange(pages, dtype=torch.int32).expand(N, pages).contiguous()
+    lengths = torch.full((N,), n, dtype=torch.int32)
+    q = torch.ones((N, 1, 2, d), dtype=dtype)
+    # Added up in n / 32 steps at most, each off by half a unit of 2^-23 of a sum between 1 and 2, in the output and in its
+    # divisor: 2 * 2^10 * 2^-24, always the same way.  The exponentials: 2^-22 each, and 18 log2 e 2^-24 of their
+    # argument's rounding; the scale of that block 2^-24 of a score of 18.
+    bound = 2.0 ** -13 + 2.0 ** -19
+    if out == BF16:
+        bound += 2.0 ** -11 + 2.0 ** -8
+    for sink in (1.0, 0.0):
+        v = one.clone()
+        v[at] = torch.full((1, d), sink).to(E4M3)
+        held = [x.view(torch.uint8).cuda().view(E4M3) for x in (k, v)]
+        o = kda.kda_cache_attention_e4m3(q.cuda(), *held, ks.cuda(), vs.cuda(), table.cuda(), lengths.cuda(), o_dtype=out)
+        ref, mag = cache_reference(q[:1], dequantised(k, ks), dequantised(v, vs), table[:1].numpy(), [n])
+        # (with 11 bits and no more, weights below 2^-21 of the largest have fewer: e^-14.6)
+        if sink or out == F32 or gap < 14.5:
+            assert (np.abs(o.double().cpu().numpy() - ref) <= bound * mag).all()

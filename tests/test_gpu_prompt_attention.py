@@ -393,3 +393,32 @@ def test_values_far_above_those_of_the_keys_that_count(kda, dtype, out, d):
     # scores of 128 from d products: 22 bits of each and 8 sums cut off at 2^-23, 128 (2^-22 + 8 2^-23) = 1.5e-4, for
     # two keys that are compared
     check(o[80:], ref[80:], 3 * mag[80:], exact_p=out == F32)
+
+
+@pytest.mark.parametrize("dtype,out,d", [(F32, F32, 64), (BF16, F32, 64), (F32, F32, 16), (BF16, BF16, 32)])
+@pytest.mark.parametrize("gap", [10, 12, 14, 16, 18])
+@pytest.mark.parametrize("first", [True, False])
+def test_one_key_far_above_many_others(kda, dtype, out, d, gap, first):
+    # an attention sink: one key's score lies `gap` above those of 2^15 others, which are all the same, so that
+    # errors of their weights add up.  Values of 1 throughout, which the output has to be; then a sink
+    # without a value, where the others are all of the output.
+    n = 1 << 15
+    q = torch.ones((2, 1, d), dtype=dtype)
+    k = torch.zeros((n + 2, 1, d), dtype=dtype)
+    at = 0 if first else n
+    k[at] = gap / d ** 0.5
+    v = torch.ones_like(k)
+    # The output and, in the thread that has the sink, its divisor are added up in n / 32 steps, each off by half a unit
+    # of 2^-23 of a sum between 1 and 2: 2 * 2^10 * 2^-24, always the same way.  The exponentials: 2^-22 each, and
+    # 18 log2 e 2^-24 of their argument's rounding.  Scores are exact.
+    bound = 2.0 ** -13 + 2.0 ** -20
+    # a bf16 output: weights to 11 bits, and the output's rounding
+    if out == BF16:
+        bound += 2.0 ** -11 + 2.0 ** -8
+    for sink in (1.0, 0.0):
+        v[at] = sink
+        o = run(kda, (q, k, v), None, [0, 2], [0, n + 2], o_dtype=out)
+        ref, mag = prompt_reference(q, k, v, [0, 2], [0, n + 2])
+        # (with 11 bits and no more, weights below 2^-21 of the largest have fewer: e^-14.6)
+        if sink or out == F32 or gap < 14.5:
+            assert (np.abs(o.double().cpu().numpy() - ref) <= bound * mag).all()
