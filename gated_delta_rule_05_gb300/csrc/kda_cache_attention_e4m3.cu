@@ -248,6 +248,7 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
         ahead.step(a, warp, lane);
         in = in + 1 == Sh::kStages ? 0 : in + 1;
     }
+    const ScaleParts scale = scale_parts(a.scale_log2);
     for (; go; go = w.next(a.split)) {
         // the rows' queries, in fp16 times a power of two
         uint32_t qh[KS][4], ql[QLO ? KS : 1][4];
@@ -270,12 +271,15 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) top = top_of(top, x[s][j]);
+                for (int j = 0; j < 4; ++j) {
+                    x[s][j] *= scale.pre;
+                    top = top_of(top, x[s][j]);
+                }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int e = up_of(top);
             const float up = power(e);
-            rs[h] = a.scale_log2 * power(-e);
+            rs[h] = copysignf(scale.rest * power(-e), a.scale_log2);
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -357,7 +361,8 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         float& x = c[b][2 * h + j];
-                        x = (QLO ? fmaf(small[b][2 * h + j], kRest, x) : x) * ks[b][j] * rs[h];
+                        // (by both factors at once: with one of them alone it may not fit)
+                        x = (QLO ? fmaf(small[b][2 * h + j], kRest, x) : x) * (ks[b][j] * rs[h]);
                         const int key = 8 * b + i4 + 4 * j;
                         if (masked && (!((mask >> key) & 1) || pos + key >= lim[h])) x = -INFINITY;
                         top[h] = fmaxf(top[h], x);
@@ -742,6 +747,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
     };
     if (go) load_scales(0);
     const int heads = 1 << a.heads_log;
+    const ScaleParts scale = scale_parts(a.scale_log2);
     for (; go; go = w.next(a.split)) {
         const int hk = head_of(a, w, warp);
         // the rows' queries, in fp16 times a power of two (and -1 for a negative scale; 0 for 0)
@@ -765,12 +771,15 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) top = top_of(top, x[s][j]);
+                for (int j = 0; j < 4; ++j) {
+                    x[s][j] *= scale.pre;
+                    top = top_of(top, x[s][j]);
+                }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int e = up_of(top);
             float up = power(e);
-            rs[h] = fabsf(a.scale_log2) * power(-e);
+            rs[h] = scale.rest * power(-e);
             if (a.scale_log2 < 0.f) up = -up;
             if (a.scale_log2 == 0.f) up = 0.f, rs[h] = 1.f;
 #pragma unroll

@@ -63,8 +63,9 @@ __device__ __forceinline__ float quad_max(float x)
 
 // Bits of the largest magnitude.
 __device__ __forceinline__ uint32_t top_of(uint32_t top, float x) { return max(top, __float_as_uint(x) & 0x7FFFFFFFu); }
-// The power of two that brings that magnitude to 2^14 or a little more.
-__device__ __forceinline__ int up_of(uint32_t top) { return top == 0 ? 0 : min(max(14 + 127 - (int)(top >> 23), -100), 100); }
+// The power of two that brings that magnitude to 2^14 or a little more; for the smallest, some of them
+// subnormal, the one whose inverse is still a normal number.
+__device__ __forceinline__ int up_of(uint32_t top) { return top == 0 ? 0 : min(14 + 127 - (int)(top >> 23), 126); }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // What a value's probability is multiplied by to become its weight: the value's factor times 2^(m - n),
@@ -75,6 +76,18 @@ __device__ __forceinline__ float weight_factor(float down, float fac)
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(down * fac), "f"(1.7014118e38f));
     return r;
+}
+
+// A scale's magnitude as pre * rest: pre, a power of two up to 1, goes to the queries before their rows'
+// factors are found, so that rest times the inverse of such a factor is a normal number however small
+// the scale is.
+struct ScaleParts {
+    float pre, rest;
+};
+__device__ __forceinline__ ScaleParts scale_parts(float scale)
+{
+    const int e = max(min((int)((__float_as_uint(scale) >> 23) & 255) - 127, 0), -126);
+    return {power(e), fabsf(scale) * power(-e)};
 }
 
 }  // namespace f16_parts

@@ -323,6 +323,7 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
     copy_raw(0);
     copy_raw(1);
     // the queries, 32 rows at a time; -1 for a negative scale, 0 for 0
+    const ScaleParts scale = scale_parts(a.scale_log2);
 #pragma unroll 1
     for (int b = 0; b < BM; b += 32) {
         const int r = b + tr;
@@ -339,8 +340,10 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
             if (qp && t8 + 8 * i < P) w = __ldg(reinterpret_cast<const uint4*>(qp) + t8 + 8 * i);
             p[i] = widen(w, T());
 #pragma unroll
-            for (int e = 0; e < Piece<T>::kN; ++e)
+            for (int e = 0; e < Piece<T>::kN; ++e) {
+                p[i].x[e] *= scale.pre;
                 if (fabsf(p[i].x[e]) < INFINITY) top = top_of(top, p[i].x[e]);
+            }
         }
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -349,8 +352,7 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
 #pragma unroll
         for (int i = 0; i < PT; ++i)
             if (t8 + 8 * i < P) store_parts<T, D, Sh::kLo>(q_tile, BM * D * 2, r, t8 + 8 * i, p[i], power(e) * sign, true);
-        // (not 0, which hidden scores of -inf are multiplied by)
-        if (t8 == 0) sh.q_down[r] = sign == 0.f ? 1.f : fmaxf(fabsf(a.scale_log2) * power(-e), 1.2e-38f);
+        if (t8 == 0) sh.q_down[r] = sign == 0.f ? 1.f : scale.rest * power(-e);
     }
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     if (count > 0) convert(0);
@@ -425,17 +427,15 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float& x = c[b][2 * h + e];
-                    x = (Sh::kLo ? fmaf(small[b][2 * h + e], kRest, x) : x) * (e ? kd.y : kd.x);      // (to be multiplied by rs)
+                    // (by both factors at once: with one of them alone it may not fit)
+                    x = (Sh::kLo ? fmaf(small[b][2 * h + e], kRest, x) : x) * ((e ? kd.y : kd.x) * rs[h]);
                     if (masked && j * BN + 8 * b + 2 * i4 + e >= lim[h]) x = -INFINITY;
                     top[h] = fmaxf(top[h], x);
-                    vtop[h] = fmaxf(vtop[h], fmaf(x, rs[h], e ? lv.y : lv.x));
+                    vtop[h] = fmaxf(vtop[h], x + (e ? lv.y : lv.x));
                 }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            top[h] *= rs[h];
-            grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + (kSlack + kHead);
-        }
+        for (int h = 0; h < 2; ++h) grow |= top[h] > m[h] + kSlack || vtop[h] > n[h] + (kSlack + kHead);
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -464,7 +464,7 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
                 float y[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float p = ex2(fmaf(c[b][2 * h + e], rs[h], -ref));
+                    const float p = ex2(c[b][2 * h + e] - ref);
                     sum += p;
                     y[e] = p * weight_factor(vd[b][e], fac[h]);
                 }

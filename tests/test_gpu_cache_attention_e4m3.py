@@ -412,3 +412,20 @@ def test_one_row_far_above_many_others(kda, page, block, dtype, out, gap, first)
         # (with 11 bits and no more, weights below 2^-21 of the largest have fewer: e^-14.6)
         if sink or out == F32 or gap < 14.5:
             assert (np.abs(o.double().cpu().numpy() - ref) <= bound * mag).all()
+
+
+@pytest.mark.parametrize("page,block", [(32, 16), (24, 8), (7, 7)])
+@pytest.mark.parametrize("dtype,out", [(F32, F32), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("which,power", [("q", 118), ("q", -118), ("q", -124), ("k", 100), ("k", -100), ("v", 100), ("v", -100)])
+def test_magnitudes_near_the_ends_of_fp32(kda, page, block, dtype, out, which, power):
+    c = Call(3, 2, 8, 2, 64, page, block, [100, 333, 1], dtype, seed=30)
+    f, scale = 2.0 ** power, 64 ** -0.5
+    if which == "q":
+        c.q = c.q * f
+    elif which == "k":
+        c.ks = c.ks * f
+    else:
+        c.vs = c.vs * f
+    if which != "v":
+        scale /= f
+    check(c.run(kda, scale=scale, o_dtype=out), *c.reference(scale=scale), exact_p=out == F32)

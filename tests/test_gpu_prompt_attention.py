@@ -422,3 +422,36 @@ def test_one_key_far_above_many_others(kda, dtype, out, d, gap, first):
         # (with 11 bits and no more, weights below 2^-21 of the largest have fewer: e^-14.6)
         if sink or out == F32 or gap < 14.5:
             assert (np.abs(o.double().cpu().numpy() - ref) <= bound * mag).all()
+
+
+@pytest.mark.parametrize("dtype,out,d", [(F32, F32, 64), (F32, F32, 128), (BF16, F32, 64), (BF16, F32, 32), (BF16, BF16, 32)])
+@pytest.mark.parametrize("which", ["q", "k", "v"])
+@pytest.mark.parametrize("power", [118, -118, -124])
+def test_magnitudes_near_the_ends_of_fp32(kda, dtype, out, d, which, power):
+    # (at 2^-124 a part of the values is subnormal; they are compared as they are)
+    q, k, v = inputs(150, 150, 4, 2, d, dtype, seed=24)[0]
+    f = 2.0 ** power
+    scale = d ** -0.5
+    if which != "v":
+        scale /= f
+    parts = [x * f if y == which else x for x, y in ((q, "q"), (k, "k"), (v, "v"))]
+    o = run(kda, parts, None, None, None, scale=scale, o_dtype=out)
+    ref, mag = prompt_reference(*parts, scale=scale)
+    # what p's rounding to 11 bits adds for a bf16 output is below what that check allows; one around 2^-126 has steps of
+    # 2^-133, as it is subnormal: half of that, 2^-134, is 2^-8 of 2^-126
+    check(o, ref, mag + (2.0 ** -126 if out == BF16 else 0), exact_p=out == F32)
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_rows_of_all_magnitudes(kda, which):
+    # row by row, over most of fp32's range; the queries match where the keys have it
+    q, k, v = inputs(200, 200, 2, 2, 64, F32, seed=25)[0]
+    f = 2.0 ** torch.linspace(-120, 120, 200)[torch.randperm(200, generator=torch.Generator().manual_seed(1))][:, None, None]
+    scale = 64 ** -0.5
+    if which == "v":
+        v = v * f
+    else:
+        k, q, scale = k * f, q * 2.0 ** -118, scale
+    o = run(kda, (q, k, v), None, None, None, scale=scale)
+    ref, mag = prompt_reference(q, k, v, scale=scale)
+    check(o, ref, mag, exact_p=True)
