@@ -51,6 +51,8 @@ constexpr int kKeys = 16;                          // of a warp's step
 constexpr int KT = kWarps * kKeys;                 // of a tile
 constexpr int kLead = 4;
 constexpr int kRows = 16;
+constexpr uint32_t kInfinity = 0x7F800000u;
+constexpr float kNaN = __builtin_nanf("");
 using Piece = TreePieces<KT, kLead>;
 
 template <int D>
@@ -280,6 +282,7 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
             const int e = up_of(top);
             const float up = power(e);
             rs[h] = copysignf(scale.rest * power(-e), a.scale_log2);
+            if (top >= kInfinity) rs[h] = kNaN;    // (scores of -inf alone would count as no rows)
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -782,6 +785,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
             rs[h] = scale.rest * power(-e);
             if (a.scale_log2 < 0.f) up = -up;
             if (a.scale_log2 == 0.f) up = 0.f, rs[h] = 1.f;
+            if (top >= kInfinity) rs[h] = kNaN;    // (scores of -inf alone would count as no rows)
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll

@@ -429,3 +429,23 @@ def test_magnitudes_near_the_ends_of_fp32(kda, page, block, dtype, out, which, p
     if which != "v":
         scale /= f
     check(c.run(kda, scale=scale, o_dtype=out), *c.reference(scale=scale), exact_p=out == F32)
+
+
+@pytest.mark.parametrize("page,block", [(16, 16), (7, 7)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_infinite_queries(kda, page, block, dtype, value):
+    # scores of -inf alone are not the same as no rows; a token that sees no row gives 0 all the same
+    c = Call(4, 2, 4, 2, 32, page, block, [1, 2, 300, 0], dtype, seed=32)
+    bits = c.k.view(torch.uint8)
+    live = (bits & 0x7F) != 0x7F
+    bits[live] = (bits[live] & 0x7F) | (0x80 if value > 0 else 0)       # one sign, so that inf * k = -inf in all rows
+    for scale in (0.2, -0.2):
+        want = c.run(kda, scale=scale).clone()
+        q = c.q.clone()
+        q[:, 1, 1, 5] = value
+        o = c.run(kda, q=q.cuda(), scale=scale)
+        hit = torch.zeros(o.shape[:3], dtype=torch.bool, device="cuda")
+        hit[:3, 1, 1] = True
+        assert torch.isnan(o[hit]).all() and torch.equal(o[~hit], want[~hit])
+        assert torch.all(o[3] == 0) and torch.all(o[0, 0] == 0)
