@@ -3,9 +3,10 @@
 //
 // A pair (x, y) of a row at position p is turned by p f, f the pair's frequency:
 // (x cos - y sin, x sin + y cos).  The angle is taken in turns, in fixed point:
-// p * round(2^64 frac(f / 2 pi)) mod 2^64 is the fraction of a turn exactly, whatever
-// p is, where fp32 would lose what matters (at position 10^6 an angle is off by
-// 0.03).  Its upper 32 bits go to sincospif.
+// p * round(2^64 frac(f / 2 pi)) mod 2^64 is the fraction of a turn, whatever p is, but for
+// the 53 bits that f / 2 pi is worked out in (p f 2^-54 of a turn), where fp32 would lose what
+// matters (at position 10^6 an angle is off by 0.03).  Its upper 32 bits go to sincospif as
+// fp32, which rounds them to 2^-26 of a turn.
 //
 // Rows that are only turned and copied (queries; in a cache of the model's type keys and
 // values too): a lane holds 16 channels of a row, two vectors of eight that belong

@@ -621,8 +621,9 @@ kda_status_t kda_prompt_attention(const void *q, const void *k, const void *v,
  * Each pair (x, y) of the first rot_dim channels of q and k becomes
  *     (x cos a - y sin a, x sin a + y cos a),  a = p * inv_freq[j],
  * the j-th pair being channels j and j + rot_dim / 2, or 2 j and 2 j + 1
- * (interleaved != 0); the other channels, and v, stay.  The angle is exact to 2^-32
- * of a turn at every position.
+ * (interleaved != 0); the other channels, and v, stay.  The angle is off by 2^-26 of a
+ * turn and p |inv_freq[j]| 2^-54 more at most (as much again for a frequency of 1 at position
+ * 2^28).
  *
  *   q, q_out      [total_tokens, Hq, d]; Hq = 0 and NULL: k and v only
  *   k, v          [total_tokens, Hkv, d]
@@ -634,7 +635,7 @@ kda_status_t kda_prompt_attention(const void *q, const void *k, const void *v,
  *                 Hkv, d]).  Rows without a place in the cache are dropped there,
  *                 but turned; those of no sequence, or of one with a negative
  *                 length, are left as they were.
- *   inv_freq      device fp32 [rot_dim / 2]; rot_dim is a multiple of 16, 16 .. d
+ *   inv_freq      device fp32 [rot_dim / 2], finite; rot_dim is a multiple of 16, 16 .. d
  *   block         0: the cache is in k's dtype, page_stride in elements, and
  *                 the scales are not used.  Else the cache has 8 bits, a scale for
  *                 each `block` rows (1 .. 128, more is KDA_ERR_UNSUPPORTED; it divides

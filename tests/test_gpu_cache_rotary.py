@@ -397,3 +397,23 @@ def test_calls_from_two_threads(kda):
     assert not errors
     for c, want, _ in checks:
         assert all(torch.equal(x, y) for x, y in zip((c.kc.view(torch.uint8), c.vc.view(torch.uint8), c.ks, c.vs), want))
+
+
+@pytest.mark.parametrize("base", [1e4, 5e5])
+def test_angles_at_all_positions(kda, base):
+    # pairs of (1, 0) become (cos, sin).  Off by 2 pi times 2^-26 + p f 2^-54 + 2^-32 of a turn (the fraction's rounding
+    # to fp32, the frequency's 53 bits, the part below 32 bits), and by sincospif: 2 units of 2^-24 of 1
+    d = 128
+    pos = [0, 1, 1000, 10 ** 6, 2 ** 24 + 1, 2 ** 28 - 1, 2 ** 30 + 12345, 2 ** 31 - 2]
+    n = len(pos)
+    f = frequencies(d, base)
+    q = torch.zeros((n, 1, d))
+    q[..., 0::2] = 1
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    kv = torch.zeros((n, 1, d), device="cuda")
+    pool = [torch.zeros((1, 8, 1, d), device="cuda") for _ in range(2)]
+    got, _, _ = kda.kda_cache_append_rotary(q.cuda(), kv, kv, i32(range(n + 1)), f.cuda(), *pool, i32([[-1]] * n), i32(pos),
+                                            interleaved=True)
+    want = np.concatenate([rotate(q[i:i + 1], [p], f, True)[0] for i, p in enumerate(pos)])
+    bound = 2 * np.pi * (2.0 ** -26 + 2.0 ** -32 + np.outer(pos, f.double().numpy()) * 2.0 ** -54) + 2.0 ** -23
+    assert (np.abs(got.double().cpu().numpy() - want) <= np.repeat(bound, 2, 1)[:, None]).all()
