@@ -433,7 +433,7 @@ cache_attention_kernel(const __grid_constant__ E4m3Args a)
                             mma0(rest, pl, b0[j], b1[j]);
                             mma0(z, ph, b0[j], b1[j]);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) o[4 * x + j][e] = fmaf(rest[e], kRest, o[4 * x + j][e] + z[e]);
+                            for (int e = 0; e < 4; ++e) o[4 * x + j][e] += fmaf(rest[e], kRest, z[e]);
                         } else {
                             mma(o[4 * x + j], ph, b0[j], b1[j]);
                         }
@@ -982,7 +982,7 @@ cache_attention_group_kernel(const __grid_constant__ E4m3Args a, const __grid_co
                             mma0(rest, pl[i], b0[j], b1[j]);
                             mma0(z, ph[i], b0[j], b1[j]);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) o[4 * x + j][e] = fmaf(rest[e], kRest, o[4 * x + j][e] + z[e]);
+                            for (int e = 0; e < 4; ++e) o[4 * x + j][e] += fmaf(rest[e], kRest, z[e]);
                         } else {
                             mma(o[4 * x + j], ph[i], b0[j], b1[j]);
                         }
