@@ -482,20 +482,24 @@ prompt_attention_split_kernel(const __grid_constant__ PromptArgs a)
                 ldmatrix_t(vh[k], vt + row_at<D>(k * 16 + mr, x + mc));
                 if (Sh::kLo) ldmatrix_t(vl[k], vt + Sh::kHalf + row_at<D>(k * 16 + mr, x + mc));
             }
+            // the small products first, times 2^-11 (which is exact), and the large ones onto them; two sums instead of one
+            // take 410 us for 4 prompts of 2,000 tokens, d = 128, this 395
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 if constexpr (Sh::kPLo) {
-                    float z[4], rest[4];
-                    mma0(rest, pl[0], vh[0][2 * y], vh[0][2 * y + 1]);
-                    mma(rest, pl[1], vh[1][2 * y], vh[1][2 * y + 1]);
+                    float z[4];
+                    mma0(z, pl[0], vh[0][2 * y], vh[0][2 * y + 1]);
+                    mma(z, pl[1], vh[1][2 * y], vh[1][2 * y + 1]);
                     if (Sh::kLo) {
-                        mma(rest, ph[0], vl[0][2 * y], vl[0][2 * y + 1]);
-                        mma(rest, ph[1], vl[1][2 * y], vl[1][2 * y + 1]);
+                        mma(z, ph[0], vl[0][2 * y], vl[0][2 * y + 1]);
+                        mma(z, ph[1], vl[1][2 * y], vl[1][2 * y + 1]);
                     }
-                    mma0(z, ph[0], vh[0][2 * y], vh[0][2 * y + 1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[e] *= kRest;
+                    mma(z, ph[0], vh[0][2 * y], vh[0][2 * y + 1]);
                     mma(z, ph[1], vh[1][2 * y], vh[1][2 * y + 1]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[x + y][e] = fmaf(rest[e], kRest, o[x + y][e] + z[e]);
+                    for (int e = 0; e < 4; ++e) o[x + y][e] += z[e];
                 } else {
                     mma(o[x + y], ph[0], vh[0][2 * y], vh[0][2 * y + 1]);
                     mma(o[x + y], ph[1], vh[1][2 * y], vh[1][2 * y + 1]);
