@@ -15,8 +15,8 @@
 // NaN in a value stays with them.
 //
 // Bound by fp32 FMAs and the shared memory that feeds them: 12 prompts of 512 to 12,288
-// tokens, 32 heads on 8, d = 128, bf16, 119 ms (45 TFLOP/s of 75), where tcgen05 takes 3.5 ms;
-// 7 fp32 prompts of up to 1,500, 12 heads on 4, d = 64, 353 us, fp16 pairs 125.
+// tokens, 32 heads on 8, d = 128, bf16, 119 ms (45 TFLOP/s of 75), where tcgen05 takes 3.6 ms;
+// 7 fp32 prompts of up to 1,500, 12 heads on 4, d = 64, 353 us, fp16 pairs 130.
 #include "kda_prompt.cuh"
 
 namespace kda {

@@ -25,15 +25,15 @@
 //
 // The tensor cores cut off what does not fit as they add up, so the products with the small
 // parts and each tile's output have sums of their own (1.2e-6 of the result otherwise,
-// 2.1e-7 with them; the sums in fp32 FMAs, 3.1e-7).
+// 2.0e-7 with them; the sums in fp32 FMAs, 3.1e-7).
 //
 // Thread blocks take the row tiles of all sequences and heads with most keys first.
 //
 // Bound by mma.sync and the conversions between the products: fp32, 4 prompts of 2,000
-// tokens, 8 heads on 2, d = 128, 64, 16: 380, 198 and 101 us (CUDA cores 980, 558, 223); the first
-// is 65 TFLOP/s where the three products would allow 190.  7 prompts of up to 1,500, 12 heads on
-// 4, d = 64: 125 us (353).  bf16, d = 128, one prompt of 8,192 tokens, 32 heads on 8: 2.8 ms, 195
-// TFLOP/s (tcgen05 0.36, CUDA cores 12.4).
+// tokens, 8 heads on 2, d = 128, 64, 16: 395, 196 and 105 us (CUDA cores 983, 552, 223); the first
+// is 83 TFLOP/s where the three products would allow 190.  7 prompts of up to 1,500, 12 heads on
+// 4, d = 64: 130 us (353).  bf16, d = 128, one prompt of 8,192 tokens, 32 heads on 8: 2.9 ms, 192
+// TFLOP/s, with an fp32 output 3.5 ms (tcgen05 0.35, CUDA cores 12.4).
 #include "kda_f16_parts.cuh"
 #include "kda_prompt.cuh"
 

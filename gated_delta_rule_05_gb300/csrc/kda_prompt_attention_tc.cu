@@ -37,8 +37,8 @@
 // items for a CTA they are dealt to and fro, which saves the clearing of the counter.
 //
 // Bound by the softmax beside the products: 32 heads on 8, d = 128, one prompt of 65,536
-// tokens (8 heads) 5.4 ms, 1.63 PFLOP/s, of 8,192 0.36 ms (1.5), of 2,048 34 us (1.0); 12 of 512
-// to 12,288 3.5 ms (1.53).  d = 64, 16 heads on 4, 16,384 tokens 545 us (1.0): half the products for
+// tokens (8 heads) 5.4 ms, 1.63 PFLOP/s, of 8,192 0.35 ms (1.57), of 2,048 34 us (1.0); 12 of 512
+// to 12,288 3.6 ms (1.49).  d = 64, 16 heads on 4, 16,384 tokens 545 us (1.0): half the products for
 // as many exponentials.  Steps on the way there, 8 x 2,048 tokens: 445 us with the
 // products' loop rolled up (349 without), 291 with the output in a warpgroup of its own (250);
 // 8,192 tokens 394 us with 16-byte stores of rows, 372 with 32-byte ones, 363 with rows that go out
@@ -46,8 +46,8 @@
 // nothing.  Items claimed two ahead 156 us, one 129 (those 5 prompts).
 //
 // Against the kernel for everything else (fp16 products by mma.sync), 32 heads on 8, d = 128, us:
-// one prompt of 1 token 8.6 (6.4), 16 9.0 (7.8), 128 9.3 (13.8), 512 13.4 (33), 8,192 360 (2,815);
-// d = 64, 16 on 4, 128 tokens 7.7 (11.7), 4,096 46 (202).  The shortest are not
+// one prompt of 1 token 8.3 (6.1), 16 8.8 (7.4), 128 8.9 (13.8), 512 13.2 (33.5), 8,192 353 (2,863);
+// d = 64, 16 on 4, 128 tokens 7.5 (11.2), 4,096 47 (204).  The shortest are not
 // given to that one: a prompt's results would depend on how it is cut.
 //
 // Every wait has a limit; one that gives up sets the workspace's timeout word and stops
