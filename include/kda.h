@@ -588,7 +588,9 @@ size_t kda_prompt_attention_workspace_bytes(int32_t num_seqs, int32_t Hq,
  *                 total_keys is total_tokens
  *   o             (written) rows that cu_seqlens gives to no sequence keep what they
  *                 hold; must not overlap the inputs.  Rows before 0 or past the last
- *                 do not exist; of sequences that claim the same row one gets it.
+ *                 do not exist; where offsets fall, so that sequences claim the same
+ *                 rows, it is not defined which rows of theirs are written, and from
+ *                 which of them.
  *   workspace     kda_prompt_attention_workspace_bytes(...) bytes, 256-byte aligned,
  *                 over none of the above, not shared with concurrent calls; contents on
  *                 entry do not matter.
