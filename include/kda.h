@@ -567,8 +567,9 @@ kda_status_t kda_cache_append(const void *k, const void *v,
  * e4m3.  A block of `block` rows (of one page, position i of a sequence being row i
  * % page_size) and head has the scale 2^e with the smallest e >= -126 for which 448
  * * 2^e reaches its largest magnitude, 0 when it has only zeros, NaN (and bytes 0 for
- * the rows that are written then and later) when it has an infinity or NaN.  (kda_cache_attention_e4m3 takes any scales that are not
- * negative.)  page_stride counts bytes here. */
+ * the rows that are written then and later) when it has an infinity or NaN.
+ * (kda_cache_attention_e4m3 takes any scales that are not negative.)  page_stride
+ * counts bytes here. */
 
 /* Bytes of device workspace kda_prompt_attention needs; 0 for arguments that it
  * refuses. */
