@@ -455,3 +455,23 @@ def test_rows_of_all_magnitudes(kda, which):
     o = run(kda, (q, k, v), None, None, None, scale=scale)
     ref, mag = prompt_reference(q, k, v, scale=scale)
     check(o, ref, mag, exact_p=True)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_rows_beyond_32_bits(kda, out):
+    # more than 2^32 elements of q and o: the last sequences come out as by themselves
+    Hq, Hkv, d, n, L = 128, 4, 64, 4200, 128
+    T = n * L
+    assert T * Hq * d > 1 << 32
+    g = torch.Generator(device="cuda").manual_seed(27)
+    f = lambda h: torch.empty((T, h, d), dtype=BF16, device="cuda").normal_(generator=g)
+    q, k, v = f(Hq), f(Hkv), f(Hkv)
+    cu = torch.arange(0, T + 1, L, dtype=torch.int32, device="cuda")
+    o = kda.kda_prompt_attention(q, k, v, cu, o_dtype=out)
+    for at in (0, T // 2 // L * L, T - 2 * L):
+        part = [x[at:at + 2 * L].clone() for x in (q, k, v)]
+        assert torch.equal(o[at:at + 2 * L], kda.kda_prompt_attention(*part, i32([0, L, 2 * L]), o_dtype=out))
+    # a sequence's first token sees itself alone; an fp32 output has a weight of 22 bits (2^-23), 2^(m - n) and 2^(n - m),
+    # 2^-22 each by ex2 (their arguments' rounding is the same and cancels), and three products of 2^-24: below 2^-20
+    first = v[::L].repeat_interleave(Hq // Hkv, 1).float()
+    assert ((o[::L].float() - first).abs() <= (2.0 ** -20 if out == F32 else 0) * first.abs()).all()
